@@ -47,10 +47,12 @@ typedef enum sv_status {
     SV_ERR_CUDA = -4,         /* a CUDA runtime call failed (launch, attribute query) */
     SV_ERR_DEVICE_INPUT = -5, /* (status word) invalid device-resident data was seen */
     SV_ERR_TIMEOUT = -6,      /* (status word) a bounded device wait gave up */
-    SV_ERR_WORKSPACE = -7     /* workspace missing, too small or misaligned */
+    SV_ERR_WORKSPACE = -7,    /* workspace missing, too small or misaligned */
+    SV_ERR_NO_PAGES = -8      /* (status word) a cache ran out of free pages */
 } sv_status;
 
-typedef enum sv_dtype { SV_F32 = 0, SV_BF16 = 1 } sv_dtype;
+/* SV_F16 only where a call says so (the cache calls). */
+typedef enum sv_dtype { SV_F32 = 0, SV_BF16 = 1, SV_F16 = 2 } sv_dtype;
 
 /* Supported sizes. */
 #define SV_MAX_B 4096         /* requests per verify call */
@@ -362,9 +364,157 @@ sv_status sv_verify_tree(const void *target_d, const void *draft_d, sv_dtype dty
                          size_t ws_bytes, void *stream);
 
 /*
+ * ---------------------------------------------------------------------------------
+ * The target's key/value cache between verification rounds: paged, 8 bits a value, one
+ * scale for each page and head. A round reserves pages for the drafted block
+ * (sv_kv_reserve), writes every layer's new keys and values (sv_kv_append) and attends
+ * over them (sv_kv_attend); sv_verify or sv_verify_tree decides on the logits; and
+ * sv_kv_commit keeps the accepted tokens and gives the rest back. sv_kv_fork copies,
+ * reorders and frees whole rows (beams, samples, finished requests).
+ *
+ * A value is q * scale with q in e4m3 (1-4-3 bits, largest 448). Keys and values have
+ * their own scales. Rows of the table are requests ("rows" below); they may share pages
+ * (refs counts the rows that hold a page). All arrays are device arrays of the caller:
+ *  k_d, v_d              [layers, pages, heads, page, dim] e4m3, 16-byte aligned
+ *  k_scale_d, v_scale_d  [layers, pages, heads] float32, in [2^-64, 2^64]
+ *  table_d               [batch, max_pages] int32: page ids, -1 from n_pages_d on
+ *  n_pages_d, len_d      [batch] int32: pages held, tokens cached
+ *  refs_d                [pages] int32: rows that hold the page, 0 = free
+ * An empty cache has refs, len and n_pages 0 and the table -1; the pools need no
+ * initial value. Token i of a row is in slot i % page of its page table[i / page].
+ * Calls work on the whole batch; rows with nothing to do are skipped.
+ *  Limits: layers, pages, max_pages >= 1; page 16, 32, 64 or 128; heads 1..SV_KV_MAX_HEADS;
+ *  dim a multiple of 16 up to SV_KV_MAX_DIM; batch 1..SV_MAX_B;
+ *  pages * heads * page and max_pages * page below 2^31 (pools themselves may be larger).
+ * Device data that is wrong (a page id outside the pool, a length past the pages held, a
+ * count outside its range, a page that must be written while another row holds it) marks
+ * its row as each call says and sets SV_ERR_DEVICE_INPUT; nothing is read or written out
+ * of range. The workspace (sv_kv_workspace_bytes, sv_workspace_init) serves one call at a
+ * time, and a cache's calls are ordered on one stream.
+ */
+#define SV_KV_MAX_DIM 256
+#define SV_KV_MAX_HEADS 1024
+#define SV_KV_MAX_T 65535     /* new tokens of a row per call */
+#define SV_KV_MIN_EXP (-64)   /* scales written by append: 2^SV_KV_MIN_EXP .. 2^64 */
+
+typedef struct sv_kv_cache {
+    void *k_d, *v_d;
+    float *k_scale_d, *v_scale_d;
+    int32_t *table_d, *n_pages_d, *len_d, *refs_d;
+    int layers, pages, page, heads, dim, batch, max_pages;
+} sv_kv_cache;
+
+/* Bytes of the device workspace of a cache's calls (0: unsupported sizes). */
+size_t sv_kv_workspace_bytes(const sv_kv_cache *cache);
+
+/*
+ * sv_kv_reserve: give every row the pages for n_new_d[b] more tokens.
+ *  n_new_d [batch] int32 >= 0.   ok_d [batch] int32 out or NULL: 1, or 0 for a row that
+ *  got nothing.
+ * Row b needs max(0, ceil((len + n_new) / page) - n_pages) pages. Rows are served in
+ * order with the free pages in ascending order. The first row whose need the free pages
+ * no longer cover and every later one that needs pages get none (ok 0,
+ * SV_ERR_NO_PAGES); so does a row whose table is too narrow or whose n_new is negative
+ * (ok 0, SV_ERR_DEVICE_INPUT), which takes none away from the others.
+ */
+sv_status sv_kv_reserve(const sv_kv_cache *cache, const int32_t *n_new_d, int32_t *ok_d,
+                        void *ws_d, size_t ws_bytes, void *stream);
+
+/*
+ * sv_kv_append: write the keys and values of up to T new tokens per row at positions
+ * len .. len + n_new - 1 of one layer. len is not changed (every layer of a round writes
+ * the same positions; sv_kv_commit moves len).
+ *  k_src_d, v_src_d  [batch, T, heads, dim], dtype SV_BF16, SV_F16 or SV_F32; heads and dim
+ *             dense, rows and tokens k_row / k_tok (v_row / v_tok) elements apart, so a
+ *             slice of a fused projection can be passed. Multiples of 16 bytes.
+ *  n_new_d    [batch] int32 in [0, T], or NULL for T everywhere.
+ * For each page and head written, with a the largest |x| among its new tokens, the scale
+ * becomes max(old scale if the page holds older tokens of the row, 2^e), e the smallest
+ * exponent >= SV_KV_MIN_EXP with a <= 448 * 2^e. Older tokens of a page whose scale grows
+ * are rounded to the new one. Values round to the nearest e4m3, ties to even. A value
+ * that is not finite or above 448 * 2^64 does not count towards a; it is stored as NaN
+ * or saturated, and sets SV_ERR_DEVICE_INPUT. A row with a bad count, missing pages or a
+ * page to write that refs does not give to it alone is left as it was.
+ */
+sv_status sv_kv_append(const sv_kv_cache *cache, int layer, const void *k_src_d,
+                       const void *v_src_d, sv_dtype dtype, int64_t k_row, int64_t k_tok,
+                       int64_t v_row, int64_t v_tok, int T, const int32_t *n_new_d, void *ws_d,
+                       size_t ws_bytes, void *stream);
+
+/*
+ * sv_kv_read: the values of positions start_d[b] .. start_d[b] + count_d[b] - 1 of
+ * n_layers layers from `layer` on, as numbers: k_out_d, v_out_d [n_layers, batch, T, heads,
+ * dim] in SV_BF16 (exact when the scales are powers of two inside its range) or SV_F32.
+ * Rows t >= count_d[b] (NULL: T), and positions outside the row's pages, are 0.
+ */
+sv_status sv_kv_read(const sv_kv_cache *cache, int layer, int n_layers, const int32_t *start_d,
+                     const int32_t *count_d, int T, void *k_out_d, void *v_out_d,
+                     sv_dtype dtype, void *ws_d, size_t ws_bytes, void *stream);
+
+/*
+ * sv_kv_attend: attention of T new tokens per row over the row's cache in one layer, the
+ * new tokens (appended before) included.
+ *  q_d        [batch, T, q_heads, dim] SV_BF16 or SV_F16, heads and dim dense, rows and
+ *             tokens q_row / q_tok elements apart (multiples of 16 bytes). q_heads is a
+ *             multiple of heads, at most 128 times as many: query head h reads key/value
+ *             head h / (q_heads / heads).
+ *  n_new_d    [batch] int32 in [0, T], or NULL for T everywhere.
+ *  parent_d   [batch, T] int32 or NULL. NULL: the new tokens are a chain. Otherwise a
+ *             draft tree as in sv_verify_tree: parent of node i >= 1 in [0, i), entry 0
+ *             ignored; T <= SV_MAX_TREE.
+ *  scale      factor of the scores (finite).
+ *  window     0: every cached token is visible. W >= 1: a query at position P sees keys
+ *             at positions above P - W, and the first `sinks` tokens of the row. The
+ *             position of node i is len + its depth.
+ *  out_d      [batch, T, q_heads, dim] dense, dtype of q.
+ *  lse_d      [batch, T, q_heads] float32 or NULL: log of the sum of exp(scale * q.k).
+ * Query t of a row sees the cached tokens and, of the new ones, its ancestors and itself
+ * (a chain: those up to t), as far as window and sinks allow. Scores, maximum, sum and
+ * output are accumulated in float32. Queries t >= n_new get 0 (lse -inf). A row with a
+ * bad count, tree or pages gets NaN in out and lse and sets SV_ERR_DEVICE_INPUT.
+ */
+sv_status sv_kv_attend(const sv_kv_cache *cache, int layer, const void *q_d, sv_dtype dtype,
+                       int64_t q_row, int64_t q_tok, int T, int q_heads,
+                       const int32_t *n_new_d, const int32_t *parent_d, float scale, int window,
+                       int sinks, void *out_d, float *lse_d, void *ws_d, size_t ws_bytes,
+                       void *stream);
+
+/*
+ * sv_kv_commit: keep the accepted part of the last block in every layer, and release the
+ * pages past it.
+ *  accepted_d [batch] int32 in [-1, N-1]: out_accepted of sv_verify (block position 0 is
+ *             the last emitted token, 1.. the drafted ones) or sv_verify_tree. The root
+ *             and the accepted tokens stay: n = accepted + 1 tokens (-1: none).
+ *  path_d     [batch, N] int32 or NULL: out_path of sv_verify_tree. NULL: a chain, whose
+ *             tokens are in place. 1 <= N <= SV_MAX_TREE with a path.
+ * Token len + path[i-1] moves to len + i (i = 1 .. accepted; the path is increasing). The
+ * scale of a page that receives tokens becomes the largest source scale among the tokens
+ * it then holds, and each token whose scale changes is rounded to the new one. Then len
+ * += n, and pages from ceil(len / page) on are released. A row with a bad count or path,
+ * missing pages, or a page to write that another row holds is left as it was.
+ */
+sv_status sv_kv_commit(const sv_kv_cache *cache, const int32_t *accepted_d, const int32_t *path_d,
+                       int N, void *ws_d, size_t ws_bytes, void *stream);
+
+/*
+ * sv_kv_fork: row b becomes what row src_d[b] was (src_d [batch] int32; -1 frees the row).
+ * Rows that keep a full page share it. A partly filled last page stays, with any pages
+ * reserved past it, with one taker of its row (the row itself if src says so, else the
+ * lowest); every other taker gets a copy of its tokens in a fresh page (all layers). Pages
+ * nobody holds any more become free first; copies then take the lowest free pages in row
+ * order.
+ *  ok_d       [batch] int32 out or NULL: 1, or 0 for a taker the free pages do not cover:
+ *             it holds the full pages only (its len is cut to them), SV_ERR_NO_PAGES. A
+ *             src outside [-1, batch) keeps the row (ok 0, SV_ERR_DEVICE_INPUT).
+ */
+sv_status sv_kv_fork(const sv_kv_cache *cache, const int32_t *src_d, int32_t *ok_d, void *ws_d,
+                     size_t ws_bytes, void *stream);
+
+/*
  * sv_get_status: wait for `stream`, then read the sticky status word of the
- * workspace into *status_out (SV_OK, SV_ERR_DEVICE_INPUT or SV_ERR_TIMEOUT; the most
- * severe seen since the last clear). clear != 0 resets it to SV_OK.
+ * workspace into *status_out (SV_OK, SV_ERR_NO_PAGES, SV_ERR_DEVICE_INPUT or
+ * SV_ERR_TIMEOUT; the most severe, in this order, seen since the last clear).
+ * clear != 0 resets it to SV_OK.
  * Returns SV_OK or the error of the copy.
  */
 sv_status sv_get_status(void *ws_d, void *stream, int clear, int32_t *status_out);

@@ -18,8 +18,18 @@ _lib = None
 
 SV_OK, SV_ERR_ARG, SV_ERR_SHAPE, SV_ERR_DTYPE = 0, -1, -2, -3
 SV_ERR_CUDA, SV_ERR_DEVICE_INPUT, SV_ERR_TIMEOUT, SV_ERR_WORKSPACE = -4, -5, -6, -7
-SV_F32, SV_BF16 = 0, 1
+SV_ERR_NO_PAGES = -8
+SV_F32, SV_BF16, SV_F16 = 0, 1, 2
 SV_MAX_B, SV_MAX_K = 4096, 32
+
+
+class _CacheStruct(ctypes.Structure):
+    """sv_kv_cache of specverify.h."""
+
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "table",
+                                               "n_pages", "len", "refs")] + \
+               [(n, ctypes.c_int) for n in ("layers", "pages", "page", "heads", "dim", "batch",
+                                            "max_pages")]
 
 
 class SpecVerifyError(RuntimeError):
@@ -75,6 +85,22 @@ def load(build_if_missing: bool = True):
     lib.sv_verify_tree.argtypes = [vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, f32, vp, vp, vp,
                                    vp, sz, vp]
     lib.sv_verify_tree.restype = i32
+    i64, cp = ctypes.c_int64, ctypes.POINTER(_CacheStruct)
+    lib.sv_kv_workspace_bytes.argtypes = [cp]
+    lib.sv_kv_workspace_bytes.restype = sz
+    lib.sv_kv_reserve.argtypes = [cp, vp, vp, vp, sz, vp]
+    lib.sv_kv_reserve.restype = i32
+    lib.sv_kv_append.argtypes = [cp, i32, vp, vp, i32, i64, i64, i64, i64, i32, vp, vp, sz, vp]
+    lib.sv_kv_append.restype = i32
+    lib.sv_kv_read.argtypes = [cp, i32, i32, vp, vp, i32, vp, vp, i32, vp, sz, vp]
+    lib.sv_kv_read.restype = i32
+    lib.sv_kv_attend.argtypes = [cp, i32, vp, i32, i64, i64, i32, i32, vp, vp, f32, i32, i32, vp,
+                                 vp, vp, sz, vp]
+    lib.sv_kv_attend.restype = i32
+    lib.sv_kv_commit.argtypes = [cp, vp, vp, i32, vp, sz, vp]
+    lib.sv_kv_commit.restype = i32
+    lib.sv_kv_fork.argtypes = [cp, vp, vp, vp, sz, vp]
+    lib.sv_kv_fork.restype = i32
     lib.sv_get_status.argtypes = [vp, vp, i32, ctypes.POINTER(ctypes.c_int32)]
     lib.sv_get_status.restype = i32
     lib.sv_status_string.argtypes = [i32]
@@ -357,3 +383,176 @@ def sv_verify_tree(target, draft, parent, draft_tok, n_nodes, uniforms, temperat
                                _ptr(out_path), _ptr(ws.t), ws.nbytes, _stream(stream))
     _check("sv_verify_tree", rc)
     return out_tok, out_accepted, out_path
+
+
+class KVCache:
+    """A paged 8-bit key/value cache (see specverify.h): k, v [layers, pages, heads, page,
+    dim] float8_e4m3fn with k_scale, v_scale [layers, pages, heads] float32; table [batch,
+    max_pages], n_pages, len [batch] and refs [pages] int32. Starts empty; the pools are
+    not initialised. Holds the workspace of its calls."""
+
+    def __init__(self, layers, pages, page, heads, dim, batch, max_pages, device=None,
+                 stream=None):
+        sizes = dict(layers=int(layers), pages=int(pages), page=int(page), heads=int(heads),
+                     dim=int(dim), batch=int(batch), max_pages=int(max_pages))
+        c = _CacheStruct(**sizes)
+        self.nbytes = int(load().sv_kv_workspace_bytes(ctypes.byref(c)))
+        if self.nbytes == 0:
+            raise ValueError("unsupported cache sizes " + ", ".join(
+                f"{k}={v}" for k, v in sizes.items()))
+        dev = torch.device(device or "cuda")
+        i32 = dict(dtype=torch.int32, device=dev)
+        pool = (c.layers, c.pages, c.heads, c.page, c.dim)
+        self.k = torch.empty(pool, dtype=torch.float8_e4m3fn, device=dev)
+        self.v = torch.empty(pool, dtype=torch.float8_e4m3fn, device=dev)
+        self.k_scale = torch.ones(pool[:3], dtype=torch.float32, device=dev)
+        self.v_scale = torch.ones(pool[:3], dtype=torch.float32, device=dev)
+        self.table = torch.full((c.batch, c.max_pages), -1, **i32)
+        self.n_pages = torch.zeros(c.batch, **i32)
+        self.len = torch.zeros(c.batch, **i32)
+        self.refs = torch.zeros(c.pages, **i32)
+        for n in ("k", "v", "k_scale", "v_scale", "table", "n_pages", "len", "refs"):
+            setattr(c, n, getattr(self, n).data_ptr())
+        self.c = c
+        self.buf = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=dev)
+        off = (-self.buf.data_ptr()) % 256
+        self.t = self.buf[off: off + self.nbytes]
+        _check("sv_workspace_init",
+               load().sv_workspace_init(_ptr(self.t), self.nbytes, _stream(stream)))
+        # Everything above must be complete before a call on any other stream uses it.
+        torch.cuda.synchronize(self.t.device)
+
+    status = Workspace.status
+
+
+def _kv_src(t, name, cache, heads):
+    """A [batch, T, heads, dim] tensor whose last two dimensions are dense: (T, element
+    strides of rows and tokens)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    c = cache.c
+    if t.dim() != 4 or t.shape[0] != c.batch or t.shape[3] != c.dim or \
+            (heads is not None and t.shape[2] != heads):
+        raise ValueError(f"{name} must be [{c.batch}, T, {heads or 'q_heads'}, {c.dim}], got "
+                         f"{list(t.shape)}")
+    if t.stride(3) != 1 or (t.shape[2] > 1 and t.stride(2) != c.dim):
+        raise ValueError(f"{name}: heads and dim must be contiguous")
+    # Strides of dimensions of one element are free in torch: use the dense ones.
+    tok = t.stride(1) if t.shape[1] > 1 else t.shape[2] * c.dim
+    row = t.stride(0) if t.shape[0] > 1 else t.shape[1] * tok
+    return t.shape[1], row, tok
+
+
+def _kv_counts(t, name, cache):
+    if t is not None:
+        _dev(t, name, torch.int32)
+        if tuple(t.shape) != (cache.c.batch,):
+            raise ValueError(f"{name} must be [{cache.c.batch}]")
+    return t
+
+
+def _kv_dtype(t, name):
+    try:
+        return {torch.float32: SV_F32, torch.bfloat16: SV_BF16, torch.float16: SV_F16}[t.dtype]
+    except KeyError:
+        raise ValueError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}") from None
+
+
+def sv_kv_reserve(cache: KVCache, n_new, ok=None, stream=None):
+    """Pages for n_new [batch] int32 more tokens per row (see specverify.h). ok [batch]
+    int32, when given, receives 1 per row served. Returns ok."""
+    _kv_counts(n_new, "n_new", cache)
+    _kv_counts(ok, "ok", cache)
+    _check("sv_kv_reserve", load().sv_kv_reserve(ctypes.byref(cache.c), _ptr(n_new), _ptr(ok),
+                                                 _ptr(cache.t), cache.nbytes, _stream(stream)))
+    return ok
+
+
+def sv_kv_append(cache: KVCache, layer, k, v, n_new=None, stream=None):
+    """Write the new tokens' keys and values [batch, T, heads, dim] (bf16, fp16 or fp32;
+    slices of a fused projection are fine) into one layer (see specverify.h)."""
+    T, k_row, k_tok = _kv_src(k, "k", cache, cache.c.heads)
+    Tv, v_row, v_tok = _kv_src(v, "v", cache, cache.c.heads)
+    if T != Tv or k.dtype != v.dtype:
+        raise ValueError("k and v must have one shape and dtype")
+    _kv_counts(n_new, "n_new", cache)
+    _check("sv_kv_append", load().sv_kv_append(
+        ctypes.byref(cache.c), int(layer), _ptr(k), _ptr(v), _kv_dtype(k, "k"), k_row, k_tok,
+        v_row, v_tok, T, _ptr(n_new), _ptr(cache.t), cache.nbytes, _stream(stream)))
+
+
+def sv_kv_read(cache: KVCache, start, T, count=None, layer=0, n_layers=None,
+               dtype=torch.bfloat16, k_out=None, v_out=None, stream=None):
+    """The cached values at positions start .. start + count - 1 of each row as numbers (see
+    specverify.h). Returns (k, v) [n_layers, batch, T, heads, dim]."""
+    c = cache.c
+    _kv_counts(start, "start", cache)
+    _kv_counts(count, "count", cache)
+    if n_layers is None:
+        n_layers = c.layers - int(layer)
+    shape = (int(n_layers), c.batch, int(T), c.heads, c.dim)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=start.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dtype, device=start.device)
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        _dev(t, name, dtype)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be {list(shape)}")
+    _check("sv_kv_read", load().sv_kv_read(
+        ctypes.byref(c), int(layer), int(n_layers), _ptr(start), _ptr(count), int(T), _ptr(k_out),
+        _ptr(v_out), _kv_dtype(k_out, "k_out"), _ptr(cache.t), cache.nbytes, _stream(stream)))
+    return k_out, v_out
+
+
+def sv_kv_attend(cache: KVCache, layer, q, n_new=None, parent=None, scale=None, window=0,
+                 sinks=0, out=None, lse=None, want_lse=False, stream=None):
+    """Attention of the new tokens' queries [batch, T, q_heads, dim] (bf16 or fp16) over one
+    layer of the cache (see specverify.h); scale defaults to dim ** -0.5. Returns out, or
+    (out, lse) when lse is given or wanted."""
+    c = cache.c
+    T, row, tok = _kv_src(q, "q", cache, None)
+    Hq = q.shape[2]
+    _kv_counts(n_new, "n_new", cache)
+    if parent is not None:
+        _dev(parent, "parent", torch.int32)
+        if tuple(parent.shape) != (c.batch, T):
+            raise ValueError(f"parent must be [{c.batch}, {T}]")
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    _dev(out, "out", q.dtype)
+    if lse is None and want_lse:
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    _dev(lse, "lse", torch.float32)
+    if out.shape != q.shape or (lse is not None and lse.shape != q.shape[:3]):
+        raise ValueError("out must have q's shape, lse its first three dimensions")
+    _check("sv_kv_attend", load().sv_kv_attend(
+        ctypes.byref(c), int(layer), _ptr(q), _kv_dtype(q, "q"), row, tok, T, Hq, _ptr(n_new),
+        _ptr(parent), float(c.dim ** -0.5 if scale is None else scale), int(window), int(sinks),
+        _ptr(out), _ptr(lse), _ptr(cache.t), cache.nbytes, _stream(stream)))
+    return out if lse is None else (out, lse)
+
+
+def sv_kv_commit(cache: KVCache, accepted, N, path=None, stream=None):
+    """Keep the accepted part of the last block of N positions and release the pages past
+    it (see specverify.h): accepted [batch] int32 and path [batch, N] int32 are what
+    sv_verify and sv_verify_tree return."""
+    _kv_counts(accepted, "accepted", cache)
+    if path is not None:
+        _dev(path, "path", torch.int32)
+        if tuple(path.shape) != (cache.c.batch, int(N)):
+            raise ValueError(f"path must be [{cache.c.batch}, {int(N)}]")
+    _check("sv_kv_commit", load().sv_kv_commit(
+        ctypes.byref(cache.c), _ptr(accepted), _ptr(path), int(N), _ptr(cache.t), cache.nbytes,
+        _stream(stream)))
+
+
+def sv_kv_fork(cache: KVCache, src, ok=None, stream=None):
+    """Row b becomes what row src[b] was, -1 frees it (see specverify.h): beams, samples,
+    finished requests. ok [batch] int32, when given, receives 1 per row served. Returns
+    ok."""
+    _kv_counts(src, "src", cache)
+    _kv_counts(ok, "ok", cache)
+    _check("sv_kv_fork", load().sv_kv_fork(ctypes.byref(cache.c), _ptr(src), _ptr(ok),
+                                           _ptr(cache.t), cache.nbytes, _stream(stream)))
+    return ok

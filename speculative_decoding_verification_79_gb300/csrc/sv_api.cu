@@ -343,6 +343,7 @@ sv_status sv_get_status(void* ws_d, void* stream, int clear, int32_t* status_out
   if (cudaStreamSynchronize(st) != cudaSuccess) return SV_ERR_CUDA;
   *status_out = (bits & ST_TIMEOUT) ? SV_ERR_TIMEOUT
                 : (bits & ST_DEVICE_INPUT) ? SV_ERR_DEVICE_INPUT
+                : (bits & ST_NO_PAGES)     ? SV_ERR_NO_PAGES
                                            : SV_OK;
   if (clear) {
     if (cudaMemsetAsync(ws_d, 0, sizeof(bits), st) != cudaSuccess) return SV_ERR_CUDA;
@@ -361,6 +362,7 @@ const char* sv_status_string(sv_status s) {
     case SV_ERR_DEVICE_INPUT: return "invalid device-resident input";
     case SV_ERR_TIMEOUT: return "device wait timed out";
     case SV_ERR_WORKSPACE: return "workspace missing, too small or misaligned";
+    case SV_ERR_NO_PAGES: return "not enough free cache pages";
   }
   return "unknown status";
 }

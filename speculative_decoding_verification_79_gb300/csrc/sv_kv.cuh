@@ -1,0 +1,160 @@
+// sv_kv.cuh -- the paged 8-bit key/value cache: kernel arguments, workspace layout, row
+// checks and e4m3 helpers shared by its kernels (sv_kv_*.cu).
+#pragma once
+#include <cuda_fp8.h>
+
+#include "sv_common.cuh"
+
+namespace sv {
+
+// The cache as kernels see it (see sv_kv_cache in specverify.h).
+struct KvCache {
+  uint8_t *k, *v;    // [layers, pages, heads, page, dim] e4m3
+  float *ks, *vs;    // [layers, pages, heads]
+  int32_t *table;    // [batch, max_pages]
+  int32_t *np, *len; // [batch]
+  int32_t* refs;     // [pages]
+  int layers, pages, page, heads, dim, batch, max_pages;
+  int lgp;           // log2(page)
+};
+
+// Workspace: header, then the snapshot that sv_kv_fork reads while it rewrites rows, the
+// list of fresh pages, a flag per row, and the attention's partial results.
+constexpr int KV_MAX_CTAS = 160;  // persistent CTAs of the attention kernel
+constexpr int KV_ROWS = 128;      // most query rows of its tile
+
+struct KvWs {
+  size_t ticket;  // uint32 [KV_MAX_CTAS]: partial results that have arrived
+  size_t table;   // int32 [batch * max_pages]
+  size_t np, len, keeper, fresh, flag;  // int32 [batch] each
+  size_t list;    // int32 [min(pages, batch * max_pages)]
+  size_t part;    // float [2 * KV_MAX_CTAS][KV_ROWS * dim]
+  size_t stat;    // float2 [2 * KV_MAX_CTAS][KV_ROWS]
+  size_t total;
+};
+
+inline KvWs kv_ws(const KvCache& C) {
+  KvWs W;
+  size_t off = sizeof(WsHeader);
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align_up(off + bytes, 256);
+    return at;
+  };
+  const size_t B = (size_t)C.batch, P = B * (size_t)C.max_pages;
+  W.ticket = take(4 * KV_MAX_CTAS);
+  W.table = take(4 * P);
+  W.np = take(4 * B);
+  W.len = take(4 * B);
+  W.keeper = take(4 * B);
+  W.fresh = take(4 * B);
+  W.flag = take(4 * B);
+  W.list = take(4 * (P < (size_t)C.pages ? P : (size_t)C.pages));
+  W.part = take(4 * (size_t)2 * KV_MAX_CTAS * KV_ROWS * C.dim);
+  W.stat = take(8 * (size_t)2 * KV_MAX_CTAS * KV_ROWS);
+  W.total = off;
+  return W;
+}
+
+struct KvScratch {  // the same, as pointers
+  WsHeader* hdr;
+  uint32_t* ticket;
+  int32_t *table, *np, *len, *keeper, *fresh, *flag, *list;
+  float* part;
+  float2* stat;
+};
+
+// Largest |x| that the scales 2^-64 .. 2^64 cover, and the bounds of a scale.
+constexpr float KV_XMAX = 448.f * 18446744073709551616.f;
+
+// Smallest power of two s = 2^e, e >= SV_KV_MIN_EXP, with a <= 448 s, for 0 <= a <=
+// KV_XMAX: 448 = 1.75 * 2^8, so with a = f * 2^x, 1 <= f < 2, e = x - 8, plus one when
+// f > 1.75. Exact, from the bits.
+__device__ __forceinline__ float kv_scale(float a) {
+  const uint32_t u = __float_as_uint(a);
+  int e = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  e = e < SV_KV_MIN_EXP ? SV_KV_MIN_EXP : e;
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+// Four floats to e4m3, nearest, ties to even, saturating (NaN stays NaN).
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+
+// Two e4m3 (the low 16 bits) as floats, exactly.
+__device__ __forceinline__ float2 e4m3_to_f2(uint16_t w) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(w));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// The page that holds position pos of row b, or -1 when the row does not hold one in
+// range (0 <= pos < 2^31).
+__device__ __forceinline__ int kv_page(const KvCache& C, int b, int pos) {
+  const int j = pos >> C.lgp;
+  if (pos < 0 || j >= C.max_pages || j >= __ldg(C.np + b)) return -1;
+  const int p = __ldg(C.table + (size_t)b * C.max_pages + j);
+  return p >= 0 && p < C.pages ? p : -1;
+}
+
+// Does row b hold pages, in range, for the positions [lo, hi)? With `alone`, pages that
+// no other row holds. Called by one thread; the ranges it is used for are short.
+__device__ __forceinline__ bool kv_holds(const KvCache& C, int b, int lo, int hi, bool alone) {
+  if (lo < 0 || hi < lo) return false;
+  for (int j = lo >> C.lgp; (long long)j << C.lgp < hi; ++j) {
+    const int p = kv_page(C, b, j << C.lgp);
+    if (p < 0 || (alone && __ldg(C.refs + p) != 1)) return false;
+  }
+  return true;
+}
+
+__device__ __forceinline__ void kv_report(WsHeader* hdr, uint32_t bits) {
+  atomicOr(&hdr->status, bits);
+}
+
+// Byte offset of (layer, page, head)'s block of page x dim values, and its scale's index.
+__device__ __forceinline__ size_t kv_block(const KvCache& C, int layer, int p, int h) {
+  return (((size_t)layer * C.pages + p) * C.heads + h) * ((size_t)C.page * C.dim);
+}
+__device__ __forceinline__ size_t kv_sidx(const KvCache& C, int layer, int p, int h) {
+  return ((size_t)layer * C.pages + p) * C.heads + h;
+}
+
+// Source of a call's new keys or values: elements between rows and between tokens.
+struct KvSrc {
+  const void* p;
+  long long row, tok;
+};
+
+struct AttendArgs {
+  KvCache C;
+  KvScratch S;
+  int layer;
+  const void* q;
+  long long q_row, q_tok;
+  int T, q_heads, group;
+  const int32_t *n_new, *parent;
+  float scale;  // scale * log2(e)
+  int window, sinks;
+  void* out;
+  float* lse;
+};
+
+cudaError_t launch_kv_reserve(const KvCache& C, const KvScratch& S, const int32_t* n_new,
+                              int32_t* ok, cudaStream_t st);
+cudaError_t launch_kv_fork(const KvCache& C, const KvScratch& S, const int32_t* src, int32_t* ok,
+                           cudaStream_t st);
+cudaError_t launch_kv_commit(const KvCache& C, const KvScratch& S, const int32_t* acc,
+                             const int32_t* path, int N, cudaStream_t st);
+cudaError_t launch_kv_append(const KvCache& C, const KvScratch& S, int layer, KvSrc k, KvSrc v,
+                             sv_dtype dt, int T, const int32_t* n_new, cudaStream_t st);
+cudaError_t launch_kv_read(const KvCache& C, const KvScratch& S, int layer, int n_layers,
+                           const int32_t* start, const int32_t* count, int T, void* ko, void* vo,
+                           sv_dtype dt, cudaStream_t st);
+cudaError_t launch_kv_attend(const AttendArgs& A, sv_dtype dt, cudaStream_t st);
+
+}  // namespace sv

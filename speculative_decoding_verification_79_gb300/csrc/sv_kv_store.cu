@@ -1,0 +1,280 @@
+// sv_kv_store.cu -- writing and reading the key/value cache (sm_103a).
+//
+// Append: a CTA takes one page and head of one row; half of its threads the keys, half the
+// values. Two steps: the largest |x| of the page's new tokens gives the scale, then each
+// value is rounded to e4m3 at that scale, sixteen to a 16-byte store.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "sv_kv.cuh"
+
+namespace sv {
+
+constexpr int AP_THREADS = 256;
+constexpr int AP_HALF = AP_THREADS / 2;
+constexpr int AP_CACHE = 4;  // vectors of 16 values that a thread keeps between the steps
+
+template <typename E>
+struct Vec16;  // sixteen consecutive elements
+template <>
+struct Vec16<float> {
+  float4 x[4];
+  __device__ __forceinline__ void load(const float* p) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = __ldg(reinterpret_cast<const float4*>(p) + i);
+  }
+  __device__ __forceinline__ void get(float* f) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[4 * i] = x[i].x;
+      f[4 * i + 1] = x[i].y;
+      f[4 * i + 2] = x[i].z;
+      f[4 * i + 3] = x[i].w;
+    }
+  }
+};
+template <>
+struct Vec16<__nv_bfloat16> {
+  uint4 x[2];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    x[0] = __ldg(reinterpret_cast<const uint4*>(p));
+    x[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+  }
+  __device__ __forceinline__ void get(float* f) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f[8 * i + 2 * j] = bf_lo(w[j]);
+        f[8 * i + 2 * j + 1] = bf_hi(w[j]);
+      }
+    }
+  }
+};
+template <>
+struct Vec16<__half> {
+  uint4 x[2];
+  __device__ __forceinline__ void load(const __half* p) {
+    x[0] = __ldg(reinterpret_cast<const uint4*>(p));
+    x[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+  }
+  __device__ __forceinline__ void get(float* f) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+        f[8 * i + 2 * j] = t.x;
+        f[8 * i + 2 * j + 1] = t.y;
+      }
+    }
+  }
+};
+
+// Sixteen values at scale s (inv = 1 / s, exact for a power of two).
+__device__ __forceinline__ uint4 quantise16(const float* f, float inv) {
+  uint4 o;
+  o.x = e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+  o.y = e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
+  o.z = e4m3x4(f[8] * inv, f[9] * inv, f[10] * inv, f[11] * inv);
+  o.w = e4m3x4(f[12] * inv, f[13] * inv, f[14] * inv, f[15] * inv);
+  return o;
+}
+
+// grid (x: pages the new tokens can touch, y: heads, z: rows)
+template <typename E>
+__global__ void __launch_bounds__(AP_THREADS)
+    kv_append_kernel(const KvCache C, const KvScratch S, int layer, const KvSrc ksrc,
+                     const KvSrc vsrc, int T, const int32_t* __restrict__ n_new) {
+  __shared__ float s_max[AP_THREADS / 32];
+  const int b = blockIdx.z, h = blockIdx.y, tid = threadIdx.x;
+  const int n = n_new ? __ldg(n_new + b) : T;
+  if (n == 0) return;
+  const int len = __ldg(C.len + b);
+  const bool sane = n > 0 && n <= T && len >= 0 && ((long long)len + n - 1) >> C.lgp < C.max_pages;
+  bool fine = sane;
+  const int j0 = len >> C.lgp;
+  if (sane) {  // every page that the row writes is its own
+    const int j1 = (len + n - 1) >> C.lgp;
+    for (int j = j0 + tid; j <= j1; j += AP_THREADS) {
+      const int p = kv_page(C, b, j << C.lgp);
+      fine = fine && p >= 0 && __ldg(C.refs + p) == 1;
+    }
+  }
+  if (!__syncthreads_and(fine ? 1 : 0)) {
+    if (tid == 0 && h == 0 && blockIdx.x == 0) kv_report(S.hdr, ST_DEVICE_INPUT);
+    return;
+  }
+  const int j = j0 + blockIdx.x;
+  const int lo = max(len, j << C.lgp), hi = min(len + n, (j + 1) << C.lgp);
+  if (hi <= lo) return;
+  const int p = kv_page(C, b, j << C.lgp);
+  const int half = tid / AP_HALF, t0 = tid - half * AP_HALF;
+  const KvSrc src = half ? vsrc : ksrc;
+  const int vpt = C.dim / 16, nv = (hi - lo) * vpt, off = lo - (j << C.lgp);
+  const E* base = static_cast<const E*>(src.p) + b * src.row + (lo - len) * src.tok +
+                  (size_t)h * C.dim;
+  uint8_t* dst = (half ? C.v : C.k) + kv_block(C, layer, p, h);
+  float* scale = (half ? C.vs : C.ks) + kv_sidx(C, layer, p, h);
+  Vec16<E> keep[AP_CACHE];
+  float a = 0.f;
+  bool odd = false;  // a value outside the scales' range
+  auto see = [&](const Vec16<E>& x) {
+    float f[16];
+    x.get(f);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float y = fabsf(f[e]);
+      if (y <= KV_XMAX)
+        a = fmaxf(a, y);
+      else
+        odd = true;
+    }
+  };
+  auto at = [&](int i) {
+    const int t = i / vpt, c = i - t * vpt;
+    return base + t * src.tok + c * 16;
+  };
+#pragma unroll
+  for (int r = 0; r < AP_CACHE; ++r) {
+    const int i = t0 + r * AP_HALF;
+    if (i < nv) keep[r].load(at(i));
+  }
+#pragma unroll
+  for (int r = 0; r < AP_CACHE; ++r)
+    if (t0 + r * AP_HALF < nv) see(keep[r]);
+  for (int i = t0 + AP_CACHE * AP_HALF; i < nv; i += AP_HALF) {
+    Vec16<E> x;
+    x.load(at(i));
+    see(x);
+  }
+  if (odd) kv_report(S.hdr, ST_DEVICE_INPUT);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
+  if ((tid & 31) == 0) s_max[tid >> 5] = a;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < AP_HALF / 32; ++w) a = fmaxf(a, s_max[half * (AP_HALF / 32) + w]);
+  float s = kv_scale(a);
+  if (off) {
+    const float old = *scale;
+    s = fmaxf(s, old);
+    if (s != old) {  // older tokens of the page, at its new scale
+      const float f = old / s;
+      for (int i = t0; i < off * vpt; i += AP_HALF) {
+        uint4 x = reinterpret_cast<uint4*>(dst)[i];
+        uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float2 u = e4m3_to_f2(w[q] & 0xffffu), v = e4m3_to_f2(w[q] >> 16);
+          w[q] = e4m3x4(u.x * f, u.y * f, v.x * f, v.y * f);
+        }
+        reinterpret_cast<uint4*>(dst)[i] = x;
+      }
+    }
+  }
+  const float inv = 1.f / s;
+  uint4* out = reinterpret_cast<uint4*>(dst + (size_t)off * C.dim);
+#pragma unroll
+  for (int r = 0; r < AP_CACHE; ++r) {
+    const int i = t0 + r * AP_HALF;
+    if (i < nv) {
+      float f[16];
+      keep[r].get(f);
+      out[i] = quantise16(f, inv);
+    }
+  }
+  for (int i = t0 + AP_CACHE * AP_HALF; i < nv; i += AP_HALF) {
+    Vec16<E> x;
+    x.load(at(i));
+    float f[16];
+    x.get(f);
+    out[i] = quantise16(f, inv);
+  }
+  __syncthreads();  // every thread has read the old scale
+  if (t0 == 0) *scale = s;
+}
+
+// One thread per 16 values; grid (x: vectors of one row and layer, y: rows, z: layers).
+template <bool BF16>
+__global__ void __launch_bounds__(256)
+    kv_read_kernel(const KvCache C, int layer0, const int32_t* __restrict__ start,
+                   const int32_t* __restrict__ count, int T, void* ko, void* vo) {
+  const int b = blockIdx.y, layer = layer0 + blockIdx.z;
+  const int vpt = C.dim / 16;
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  const int t = i / (C.heads * vpt);
+  if (t >= T) return;
+  const int r = i - t * (C.heads * vpt), h = r / vpt, c = r - h * vpt;
+  const int n = count ? __ldg(count + b) : T;
+  const long long pos = (long long)__ldg(start + b) + t;
+  const int p = t < n && pos >= 0 && pos < 0x7fffffffLL ? kv_page(C, b, (int)pos) : -1;
+  uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+  float s[2] = {0.f, 0.f};
+  if (p >= 0) {
+    const size_t o = kv_block(C, layer, p, h) + (size_t)(pos & (C.page - 1)) * C.dim + c * 16;
+    x[0] = *reinterpret_cast<const uint4*>(C.k + o);
+    x[1] = *reinterpret_cast<const uint4*>(C.v + o);
+    s[0] = C.ks[kv_sidx(C, layer, p, h)];
+    s[1] = C.vs[kv_sidx(C, layer, p, h)];
+  }
+  const size_t to = (((size_t)blockIdx.z * C.batch + b) * T * C.heads * vpt + i) * 16;
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+    const uint32_t w[4] = {x[kv].x, x[kv].y, x[kv].z, x[kv].w};
+    float f[16];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float2 lo = e4m3_to_f2(w[q] & 0xffffu), hi = e4m3_to_f2(w[q] >> 16);
+      f[4 * q] = lo.x * s[kv];
+      f[4 * q + 1] = lo.y * s[kv];
+      f[4 * q + 2] = hi.x * s[kv];
+      f[4 * q + 3] = hi.y * s[kv];
+    }
+    if (BF16) {
+      uint32_t o[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const __nv_bfloat162 y = __floats2bfloat162_rn(f[2 * q], f[2 * q + 1]);
+        o[q] = *reinterpret_cast<const uint32_t*>(&y);
+      }
+      uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(kv ? vo : ko) + to);
+      __stcs(d, make_uint4(o[0], o[1], o[2], o[3]));
+      __stcs(d + 1, make_uint4(o[4], o[5], o[6], o[7]));
+    } else {
+      float4* d = reinterpret_cast<float4*>(static_cast<float*>(kv ? vo : ko) + to);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        __stcs(d + q, make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]));
+    }
+  }
+}
+
+cudaError_t launch_kv_append(const KvCache& C, const KvScratch& S, int layer, KvSrc k, KvSrc v,
+                             sv_dtype dt, int T, const int32_t* n_new, cudaStream_t st) {
+  // A row's tokens start anywhere in a page, so T of them touch at most this many.
+  const dim3 grid((T + C.page - 2) / C.page + 1, C.heads, C.batch);
+  if (dt == SV_F32)
+    kv_append_kernel<float><<<grid, AP_THREADS, 0, st>>>(C, S, layer, k, v, T, n_new);
+  else if (dt == SV_BF16)
+    kv_append_kernel<__nv_bfloat16><<<grid, AP_THREADS, 0, st>>>(C, S, layer, k, v, T, n_new);
+  else
+    kv_append_kernel<__half><<<grid, AP_THREADS, 0, st>>>(C, S, layer, k, v, T, n_new);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_read(const KvCache& C, const KvScratch&, int layer, int n_layers,
+                           const int32_t* start, const int32_t* count, int T, void* ko, void* vo,
+                           sv_dtype dt, cudaStream_t st) {
+  const long long vecs = (long long)T * C.heads * (C.dim / 16);
+  const dim3 grid(static_cast<unsigned>((vecs + 255) / 256), C.batch, n_layers);
+  if (dt == SV_BF16)
+    kv_read_kernel<true><<<grid, 256, 0, st>>>(C, layer, start, count, T, ko, vo);
+  else
+    kv_read_kernel<false><<<grid, 256, 0, st>>>(C, layer, start, count, T, ko, vo);
+  return cudaGetLastError();
+}
+
+}  // namespace sv
