@@ -1,127 +1,1123 @@
 // sv_kv_attend.cu -- attention of a round's new tokens over the key/value cache (sm_103a).
 //
-// A CTA takes one query (row, token, head): its warps take keys in turn, a lane holds
-// dim / 32 of the vector, and each warp keeps the running maximum and sum of the softmax
-// and its output; the warps' results are joined at the end.
+// For one row, key/value head and tile of R <= 128 query rows (tokens x query heads of the
+// group, flattened) the scores are a product over the cached keys, in tiles of 128 tokens:
+//     S^T = K Q^T  [128 tokens x R],   P^T = 2^(S^T - m),   O^T += V^T P^T  [dim x R].
+// Both products run on the fifth-generation tensor cores with the cache's own e4m3 bytes as
+// the first operand, straight from TMA: nothing of the cache is converted. The other
+// operand is carried as a sum of 8-bit terms, multiplied one after the other into the same
+// float32 accumulator: a query row, scaled by a power of two to the e4m3 range, is exactly
+// the sum of two (bf16) or three (fp16) e4m3 terms down to 2^-18 of its largest component;
+// a weight is rounded to fp16 and split into three e5m2 terms of at least 9 bits in all
+// (e5m2 is fp16's upper byte, so a split is integer arithmetic).
+// Tokens lie on the accumulator's lanes, so that a thread owns one token: the page's
+// scales are a factor of the thread, and a small R costs little (N is R, M stays 128).
+//
+// The key scale multiplies the scores, the value scale is folded into the weights (its
+// logarithm added to the score, so that no weight exceeds the reference); the sum of the
+// softmax takes it out again. The reference m of a query row only moves when a score
+// passes it by 2^4 (the accumulators are then rescaled), or with the first keys a row sees:
+// most tiles need no exchange between threads but one vote.
+//
+// A persistent CTA per SM takes an equal share of all (row, head, query tile, key tile)
+// units in order; a query tile that crosses from one CTA to the next leaves partial
+// results (output, m, sum) in the workspace, and the last of its CTAs to arrive joins them.
+// Ten warps, coupled by mbarriers: one copies K and V tiles page by page by tensor-map TMA
+// (128-byte swizzle) into a ring; one issues the products; eight form the weights, four on
+// each half of the query rows.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cudaTypedefs.h>
 
 #include <cmath>
+#include <mutex>
 
 #include "sv_kv.cuh"
 
 namespace sv {
 
-constexpr int AT_WARPS = 4;
-constexpr int AT_E = SV_KV_MAX_DIM / 32;
+constexpr int AT_KEYS = 128;     // tokens per key tile
+constexpr int AT_SM_WARPS = 8;   // warps that form the weights
+constexpr int AT_THREADS = 32 * (2 + AT_SM_WARPS);
+constexpr int AT_SM0 = 64;       // first of their threads
+constexpr int AT_SM_THREADS = 32 * AT_SM_WARPS;
+constexpr int AT_BLK = AT_KEYS * 128;  // 128 tokens x 128 bytes
+constexpr int AT_MAX_STAGES = 6;
+constexpr int AT_PTERMS = 3;
+// Weights are kept as 2^(x - m + 11): up to 2^15 before the reference must move (below
+// e5m2's 57344). Their terms end at 2^-16, e5m2's smallest, so a weight has its 9 bits down
+// to 2^-19 of the reference and counts down to 2^-28. A larger shift would leave less room
+// for later maxima and move references in more tiles.
+constexpr float AT_SHIFT = 11.f, AT_LIMIT = 15.f;
 
-// grid (x: query heads, y: tokens, z: rows)
-template <typename Q>
-__global__ void __launch_bounds__(32 * AT_WARPS) kv_attend_kernel(const AttendArgs A) {
+// Instruction descriptors of kind::f8f6f4 (float32 accumulator, M = 128), without N.
+// Scores: A and B e4m3, K-major. Output: A e4m3 and B e5m2, both MN-major.
+constexpr uint32_t AT_IDESC_S = (1u << 4) | (8u << 24);
+constexpr uint32_t AT_IDESC_O = (1u << 4) | (1u << 10) | (1u << 15) | (1u << 16) | (8u << 24);
+
+__device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                   smem_addr(bar))
+               : "memory");
+}
+__device__ __forceinline__ void tm_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tm_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+// Eight consecutive float32 columns of this thread's lane; complete after tm_wait_ld.
+__device__ __forceinline__ void tm_ld8(uint32_t addr, float* v) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+                 "=f"(v[6]), "=f"(v[7])
+               : "r"(addr));
+}
+__device__ __forceinline__ void tm_st8(uint32_t addr, const float* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
+                   addr),
+               "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]),
+               "f"(v[7])
+               : "memory");
+}
+// The loaded registers are operands of the wait, so that no use of them moves above it.
+template <int C>
+__device__ __forceinline__ void tm_wait_ld(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < C; ++i) asm volatile("" : "+f"(v[i]));
+}
+__device__ __forceinline__ void tm_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Shared-memory matrix descriptor of a swizzled operand whose 8-row groups (K-major: rows;
+// MN-major: steps of K) are `group` bytes apart; rows of 128, 64 or 32 bytes (mode 2, 4, 6).
+// One swizzle atom covers the other dimension, so the leading offset is not used.
+__device__ __forceinline__ uint64_t at_desc(uint32_t addr, uint32_t group, uint32_t mode) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3fffu) | (1ull << 16) |
+         (static_cast<uint64_t>(group >> 4) << 32) | (1ull << 46) |
+         (static_cast<uint64_t>(mode) << 61);
+}
+
+__device__ __forceinline__ void at_tma(void* dst, const CUtensorMap* map, int x, int y,
+                                       uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ bool at_try(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity), "r"(2000u)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void fence_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void at_bar(int id, int n) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+// Barrier `id` of n threads; true everywhere when x is true anywhere.
+__device__ __forceinline__ bool at_vote(int id, int n, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(x ? 1u : 0u), "r"(id), "r"(n)
+      : "memory");
+  return r != 0;
+}
+
+// ---------------------------------------------------------------------------
+// Units of work.
+// ---------------------------------------------------------------------------
+
+// What a launch needs beside AttendArgs.
+struct AttendPlan {
+  int rt;      // most query rows of a tile
+  int width;   // columns of an accumulator: 32, 64 or 128
+  int stages;  // K + V tiles in the ring
+  int ndb;     // 128-byte blocks of a token's vector
+  int qterms;  // e4m3 terms of a query
+  int bf16;
+};
+
+// Row b of the batch.
+struct AtRow {
+  int len, n;    // cached and new tokens; n = 0 when the row's data is wrong
+  int rows;      // query rows of a head
+  int nrt, rr;   // query tiles, rows of each (the last may have fewer)
+  bool bad;
+};
+
+__device__ __forceinline__ AtRow at_row(const AttendArgs& A, const AttendPlan& P, int b) {
+  AtRow r;
+  r.len = __ldg(A.C.len + b);
+  r.n = A.n_new ? __ldg(A.n_new + b) : A.T;
+  r.bad = r.n < 0 || r.n > A.T || r.len < 0 ||
+          (long long)r.len + r.n > (long long)A.C.max_pages << A.C.lgp;
+  if (r.bad) r.n = 0;
+  r.rows = r.n * A.group;
+  r.nrt = (r.rows + P.rt - 1) / P.rt;
+  r.rr = r.nrt ? (r.rows + r.nrt - 1) / r.nrt : 0;
+  return r;
+}
+
+// Query tile rt of a row: rows r0 .. r1 - 1, and the key tiles that any of them sees:
+// `ns` at the row's start (sinks), then `lo` to `hi` - 1.
+struct AtTile {
+  int r0, r1;
+  int end;            // keys below end are visible to some query
+  int pos_lo, pos_hi; // bounds of the queries' positions
+  int ns, lo, hi;
+  __device__ __forceinline__ int tiles() const { return ns + hi - lo; }
+  __device__ __forceinline__ int key_tile(int i) const { return i < ns ? i : lo + i - ns; }
+};
+
+__device__ __forceinline__ AtTile at_tile(const AttendArgs& A, const AtRow& r, int rt) {
+  AtTile t;
+  t.r0 = rt * r.rr;
+  t.r1 = min(t.r0 + r.rr, r.rows);
+  const int t0 = t.r0 / A.group, t1 = (t.r1 - 1) / A.group;
+  t.pos_lo = A.parent ? r.len : r.len + t0;
+  t.pos_hi = A.parent ? r.len + r.n - 1 : r.len + t1;
+  t.end = t.pos_hi + 1;
+  t.hi = (t.end + AT_KEYS - 1) / AT_KEYS;
+  t.lo = 0;
+  t.ns = 0;
+  if (A.window) {
+    t.lo = max(0, t.pos_lo - A.window + 1) / AT_KEYS;
+    t.ns = min((min(A.sinks, t.end) + AT_KEYS - 1) / AT_KEYS, t.lo);
+  }
+  return t;
+}
+
+__device__ __forceinline__ long long at_head_units(const AttendArgs& A, const AtRow& r) {
+  long long c = 0;
+  for (int rt = 0; rt < r.nrt; ++rt) c += at_tile(A, r, rt).tiles();
+  return c;
+}
+
+// The units of this CTA, one query tile after the other: units i0 .. i1 - 1 of the current
+// one. Every role walks the same sequence.
+struct AtWalk {
+  int b, h, rt;
+  AtRow row;
+  AtTile tile;
+  int i0, i1;
+  long long at, end;  // unit index of i0, end of the CTA's share
+
+  __device__ __forceinline__ void settle() {
+    const long long left = end - at;
+    i1 = static_cast<int>(min((long long)tile.tiles(), i0 + left));
+  }
+  // From row b0, unit `rem` of it.
+  __device__ void start(const AttendArgs& A, const AttendPlan& P, int b0, long long rem,
+                        long long from, long long to) {
+    b = b0;
+    at = from;
+    end = to;
+    if (at >= end) return;
+    row = at_row(A, P, b);
+    const long long per = at_head_units(A, row);
+    h = static_cast<int>(rem / per);
+    rem -= h * per;
+    rt = 0;
+    tile = at_tile(A, row, 0);
+    while (rem >= tile.tiles()) {
+      rem -= tile.tiles();
+      tile = at_tile(A, row, ++rt);
+    }
+    i0 = static_cast<int>(rem);
+    settle();
+  }
+  __device__ __forceinline__ bool live() const { return at < end; }
+  __device__ void next(const AttendArgs& A, const AttendPlan& P) {
+    at += i1 - i0;
+    if (at >= end) return;
+    i0 = 0;
+    if (++rt == row.nrt) {
+      rt = 0;
+      if (++h == A.C.heads) {
+        h = 0;
+        do {  // (a row with queries exists: units are left)
+          row = at_row(A, P, ++b);
+        } while (row.rows == 0);
+      }
+    }
+    tile = at_tile(A, row, rt);
+    settle();
+  }
+};
+
+// Column of query row r of a tile of R: the first half of the rows from column 0, the
+// others from column nh; and back (-1: a column without a row).
+__device__ __forceinline__ int at_row_of(int col, int R, int nh) {
+  const int rh = (R + 1) >> 1;
+  if (col < nh) return col < rh ? col : -1;
+  return col - nh < R - rh ? rh + col - nh : -1;
+}
+
+// Sums of C values over the 32 lanes (C a power of two up to 32): lane c (mod C) gets
+// column c's, by halving the columns a lane is responsible for at each exchange.
+template <int C>
+__device__ __forceinline__ float at_lane_sums(float* v, int lane) {
+#pragma unroll
+  for (int s = C / 2; s >= 1; s >>= 1) {
+    const bool up = (lane & s) != 0;
+#pragma unroll
+    for (int i = 0; i < s; ++i) {
+      const float keep = up ? v[i + s] : v[i], give = up ? v[i] : v[i + s];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, s);
+    }
+  }
+  float x = v[0];
+#pragma unroll
+  for (int s = C; s < 32; s <<= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
+  return x;
+}
+
+__device__ __forceinline__ void at_store(void* out, long long at, float y, int bf16) {
+  if (bf16)
+    static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(y);
+  else
+    static_cast<__half*>(out)[at] = __float2half_rn(y);
+}
+
+// A float as an integer of the same order, and back.
+__device__ __forceinline__ int at_order(float x) {
+  const int i = __float_as_int(x);
+  return i ^ ((i >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float at_unorder(int i) {
+  return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
+}
+
+// MAXC: most columns of a thread (half of the plan's width).
+template <int MAXC>
+__global__ void __launch_bounds__(AT_THREADS, 1)
+    kv_attend_kernel(const AttendArgs A, const AttendPlan P,
+                     const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV) {
+  constexpr int W = 2 * MAXC;  // columns of an accumulator, bytes of a token's weights
+  constexpr uint32_t PMODE = W == 128 ? 2 : (W == 64 ? 4 : 6);
+  constexpr int PBLK = AT_KEYS * W;
+  extern __shared__ unsigned char dsm_raw[];
+  __shared__ uint64_t kfull[AT_MAX_STAGES], kempty[AT_MAX_STAGES];
+  __shared__ uint64_t vfull[AT_MAX_STAGES], vempty[AT_MAX_STAGES];
+  __shared__ uint64_t sfull[2], sempty[2], pfull, pvdone, qfull, drain;
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_abort;
+  __shared__ int s_b0, s_last;
+  __shared__ long long s_rem, s_sum[AT_THREADS / 32];
+  // Per stage and page of the tile: key scale, log2 and inverse of the value scale.
+  __shared__ float s_ks[AT_MAX_STAGES][8], s_lv[AT_MAX_STAGES][8], s_iv[AT_MAX_STAGES][8];
+  __shared__ __align__(16) float2 s_cm[W];  // per column: factor of the score, reference - 11
+  __shared__ __align__(16) float2 s_mv[W];  // a reference's move and the factor it brings
+  __shared__ float s_inv[W];                // inverse sum
+  __shared__ int s_mx[4][W];
+  __shared__ float s_l[4][W];
+  __shared__ int s_pos[W];                  // position of the column's query
+  __shared__ unsigned long long s_see[W];   // block nodes it sees (trees)
+  __shared__ long long s_out[W];            // its row of the output, -1: none
+  __shared__ int s_par[SV_MAX_TREE];
+
+  unsigned char* dsm = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const KvCache& C = A.C;
-  const int hq = blockIdx.x, t = blockIdx.y, b = blockIdx.z, h = hq / A.group;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  __shared__ unsigned long long s_see;
-  __shared__ int s_pos, s_bad;
-  __shared__ float s_m[AT_WARPS], s_l[AT_WARPS], s_o[AT_WARPS][SV_KV_MAX_DIM];
-  const int n = A.n_new ? __ldg(A.n_new + b) : A.T, len = __ldg(C.len + b);
-  if (tid == 0) {
-    bool bad = n < 0 || n > A.T || len < 0 || ((long long)len + n) > (long long)C.max_pages << C.lgp;
-    unsigned long long see = 0;
-    int depth = t;
-    if (!bad && A.parent) {
-      const int32_t* par = A.parent + (size_t)b * A.T;
-      for (int i = 1; i < n; ++i) bad = bad || __ldg(par + i) < 0 || __ldg(par + i) >= i;
-      depth = 0;
-      if (!bad && t < n)
-        for (int i = t;; i = __ldg(par + i)) {
-          // `depth` steps above t: visible inside the window, or as a sink.
-          if (!A.window || depth < A.window || len + i < A.sinks) see |= 1ull << i;
-          if (i == 0) break;
-          ++depth;
-        }
+  const int ndb = P.ndb, NT = P.stages;
+  unsigned char* Qs = dsm;                                       // [terms][ndb][W][128]
+  unsigned char* Ps = Qs + (size_t)P.qterms * ndb * W * 128;     // [terms][128 tokens][W]
+  unsigned char* ring = Ps + AT_PTERMS * PBLK;                   // [stages][K, V][ndb][128][128]
+  const int slot = ndb * AT_BLK;
+  auto kbuf = [&](int q) { return ring + (size_t)q * 2 * slot; };
+  auto vbuf = [&](int q) { return ring + (size_t)q * 2 * slot + slot; };
+
+  // Bounded wait: false (and a report) when it runs out or another one has.
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (mbar_test(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!at_try(bar, parity)) {
+      if (s_abort) return false;
+      if (clock64() - t0 > WAIT_CYCLES) {
+        s_abort = 1;
+        kv_report(A.S.hdr, ST_TIMEOUT);
+        return false;
+      }
     }
-    s_see = see;
-    s_pos = bad ? 0 : len + depth;
-    s_bad = bad;
+    return true;
+  };
+
+  if (tid == 0) {
+    for (int q = 0; q < NT; ++q) {
+      mbar_init(&kfull[q], 1);
+      mbar_init(&kempty[q], 1);
+      mbar_init(&vfull[q], 1);
+      mbar_init(&vempty[q], 1);
+    }
+    for (int q = 0; q < 2; ++q) {
+      mbar_init(&sfull[q], 1);
+      mbar_init(&sempty[q], AT_SM_WARPS);
+    }
+    mbar_init(&pfull, AT_SM_WARPS);
+    mbar_init(&qfull, AT_SM_WARPS);
+    mbar_init(&pvdone, 1);
+    mbar_init(&drain, 1);
+    s_abort = 0;
+    fence_mbar_init();
   }
+  if (w == 1) {
+    const uint32_t need = (2 + ndb) * W, cols = need <= 128 ? 128 : (need <= 256 ? 256 : 512);
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(&s_tmem)),
+                 "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  // This CTA's share: the units of all rows, cut into equal parts. Rows are counted by the
+  // threads in turn; the second pass finds the row where the share begins.
+  long long total = 0, mine0 = 0;
+  for (int b = tid; b < C.batch; b += AT_THREADS) {
+    const AtRow r = at_row(A, P, b);
+    const long long c = at_head_units(A, r) * C.heads;
+    if (b == tid) mine0 = c;
+    total += c;
+  }
+  auto block_sum = [&](long long x, long long* before) {  // sum; *before: of lower threads
+    long long v = x;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, v, d);
+      if (lane >= d) v += t;
+    }
+    if (lane == 31) s_sum[w] = v;
+    __syncthreads();
+    long long sum = 0, pre = 0;
+    for (int i = 0; i < AT_THREADS / 32; ++i) {
+      if (i < w) pre += s_sum[i];
+      sum += s_sum[i];
+    }
+    __syncthreads();
+    *before = pre + v - x;
+    return sum;
+  };
+  long long before;
+  total = block_sum(total, &before);
+  const long long ctas = min((long long)gridDim.x, total);
+  const long long cta = blockIdx.x;
+  const long long from = cta < ctas ? cta * total / ctas : 0;
+  const long long to = cta < ctas ? (cta + 1) * total / ctas : 0;
+  if (from < to) {
+    long long base = 0;
+    for (int b0 = 0; b0 < C.batch; b0 += AT_THREADS) {
+      const int b = b0 + tid;
+      const long long c =
+          b >= C.batch ? 0 : (b0 == 0 ? mine0 : at_head_units(A, at_row(A, P, b)) * C.heads);
+      const long long sum = block_sum(c, &before);
+      if (from >= base + before && from < base + before + c) {
+        s_b0 = b;
+        s_rem = from - base - before;
+      }
+      base += sum;
+      if (base > from) break;
+    }
+  }
+  tm_fence_before();
   __syncthreads();
-  const size_t row = ((size_t)b * A.T + t) * A.q_heads + hq;
-  Q* out = static_cast<Q*>(A.out) + row * C.dim;
-  bool bad = s_bad;
-  float m = -INFINITY, l = 0.f, o[AT_E], q[AT_E];
-#pragma unroll
-  for (int e = 0; e < AT_E; ++e) o[e] = 0.f;
-  if (!bad && t < n) {
-    const Q* src = static_cast<const Q*>(A.q) + b * A.q_row + t * A.q_tok + (size_t)hq * C.dim;
-#pragma unroll
-    for (int e = 0; e < AT_E; ++e)
-      q[e] = lane + 32 * e < C.dim ? static_cast<float>(src[lane + 32 * e]) : 0.f;
-    for (int j = w; j < len + n; j += AT_WARPS) {
-      if (j < len ? (A.window && s_pos - j >= A.window && j >= A.sinks)
-                  : (A.parent ? !((s_see >> (j - len)) & 1)
-                              : (j - len > t || (A.window && s_pos - j >= A.window && j >= A.sinks))))
-        continue;
-      const int p = kv_page(C, b, j);
-      if (p < 0) {
-        bad = true;
-        break;
+  tm_fence_after();
+  const uint32_t tmem = s_tmem;
+  AtWalk walk;
+  walk.start(A, P, s_b0, s_rem, from, to);
+
+  if (w == 0) {
+    // ---- Copies: pages of one or more tiles are looked up at a time, a page per lane and
+    // a step ahead of their use.
+    const int ppt = AT_KEYS >> C.lgp;  // pages per tile
+    const int tpc = 32 / ppt;          // tiles per step
+    const size_t layer0 = (size_t)A.layer * C.pages;
+    int b = 0, h = 0, n = 0, page = -1;  // the step in hand: row, head, tiles; its page
+    bool used = false;
+    float ks = 1.f, vs = 1.f;
+    int nb = 0, nh = 0, nn = 0, npage = -1;  // the step ahead
+    bool nused = false;
+    int i = walk.live() ? walk.i0 : 0;
+    auto look = [&]() {  // the next step's pages
+      nn = 0;
+      if (!walk.live()) return;
+      nb = walk.b;
+      nh = walk.h;
+      nn = min(tpc, walk.i1 - i);
+      const int mt = lane / ppt;
+      const int key = (mt < nn ? walk.tile.key_tile(i + mt) : 0) * AT_KEYS +
+                      ((lane - mt * ppt) << C.lgp);
+      nused = mt < nn && key < walk.tile.end;
+      npage = nused ? kv_page(C, nb, key) : -1;
+      i += nn;
+      if (i == walk.i1) {
+        walk.next(A, P);
+        i = walk.live() ? walk.i0 : 0;
       }
-      const size_t at = kv_block(C, A.layer, p, h) + (size_t)(j & (C.page - 1)) * C.dim;
-      float s = 0.f, v[AT_E];
-#pragma unroll
-      for (int e = 0; e < AT_E; ++e) {
-        const int d = lane + 32 * e;
-        v[e] = 0.f;
-        if (d < C.dim) {
-          s += q[e] * e4m3_to_f2(C.k[at + d]).x;
-          v[e] = e4m3_to_f2(C.v[at + d]).x;
+    };
+    auto scales = [&](int pg, bool use, int head, float* k, float* v) {
+      *k = *v = 1.f;
+      if (!use) return;
+      if (pg >= 0) {
+        *k = __ldg(C.ks + (layer0 + pg) * C.heads + head);
+        *v = __ldg(C.vs + (layer0 + pg) * C.heads + head);
+      }
+      // A page out of range, or scales outside theirs: the scores become NaN.
+      constexpr float LO = 5.421010862427522e-20f, HI = 18446744073709551616.f;  // 2^-64, 2^64
+      if (pg < 0 || !(*k >= LO && *k <= HI && *v >= LO && *v <= HI)) {
+        *k = NAN;
+        *v = 1.f;
+        kv_report(A.S.hdr, ST_DEVICE_INPUT);
+      }
+    };
+    look();
+    bool ok = true;
+    int g = 0, q = 0, ph = 0;  // tile, its stage, the stage's pass
+    float nks, nvs;
+    scales(npage, nused, nh, &nks, &nvs);
+    while (ok && nn) {
+      b = nb; h = nh; n = nn; page = npage; used = nused; ks = nks; vs = nvs;
+      look();
+      for (int t = 0; t < n; ++t, ++g) {
+        const bool mine = lane >= t * ppt && lane < (t + 1) * ppt;
+        const int sub = lane - t * ppt;
+        const uint32_t count = __popc(__ballot_sync(0xffffffffu, mine && page >= 0));
+        const uint32_t bytes = (count << C.lgp) * 128u * ndb;
+        for (int kv = 0; kv < 2; ++kv) {
+          uint64_t* full = kv ? &vfull[q] : &kfull[q];
+          uint64_t* empty = kv ? &vempty[q] : &kempty[q];
+          bool go = true;
+          if (ph > 0) go = wait(empty, (ph - 1) & 1);
+          if (!__all_sync(0xffffffffu, go)) {
+            ok = false;
+            break;
+          }
+          if (kv == 1 && mine) {
+            s_ks[q][sub] = ks;
+            s_lv[q][sub] = log2f(vs);
+            s_iv[q][sub] = 1.f / vs;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+          __syncwarp();
+          if (mine && page >= 0) {
+            unsigned char* dst = (kv ? vbuf(q) : kbuf(q)) + ((size_t)sub << C.lgp) * 128;
+            const int y = (page * C.heads + h) << C.lgp;
+            for (int db = 0; db < ndb; ++db)
+              at_tma(dst + db * AT_BLK, kv ? &tmV : &tmK, db * 128, y, full);
+          }
+        }
+        if (!ok) break;
+        if (t == 0) scales(npage, nused, nh, &nks, &nvs);
+        if (++q == NT) {
+          q = 0;
+          ++ph;
         }
       }
+    }
+    if (!ok) {
+      // After a wait gave up: let the copies already issued land before the CTA exits. (A
+      // stage's barrier whose last pass was consumed answers at once.)
+      for (int j = max(0, g - NT); j <= g; ++j) {
+        const long long t0 = clock64();
+        const uint32_t par = static_cast<uint32_t>((j / NT) & 1);
+        while (!(mbar_test(&kfull[j % NT], par) && (j == g || mbar_test(&vfull[j % NT], par))))
+          if (clock64() - t0 > WAIT_CYCLES / 8) break;
+      }
+    }
+  } else if (w == 1) {
+    // ---- Products. Scores of tile i, then the output of tile i - 1, so that a tile's
+    // weights form while the next tile's scores multiply.
+    if (lane == 0) {
+      const int ksteps = (C.dim + 31) / 32;
+      const uint64_t pd = at_desc(smem_addr(Ps), 8 * W, PMODE);
+      bool ok = true;
+      int g = 0, q = 0, ph = 0, item = 0;
+      int pq = 0, pph = 0;  // stage of the tile whose output is next
+      for (; ok && walk.live(); walk.next(A, P), ++item) {
+        const int R = walk.tile.r1 - walk.tile.r0;
+        const int N = 2 * ((((R + 1) >> 1) + 7) & ~7);
+        const uint32_t ids = AT_IDESC_S | (static_cast<uint32_t>(N >> 3) << 17);
+        const uint32_t ido = AT_IDESC_O | (static_cast<uint32_t>(N >> 3) << 17);
+        const int m = walk.i1 - walk.i0;
+        if (!wait(&qfull, item & 1)) break;
+        for (int i = 0; i <= m; ++i) {
+          if (i < m) {
+            if (!wait(&kfull[q], ph & 1) || (g >= 2 && !wait(&sempty[g & 1], ((g >> 1) - 1) & 1))) {
+              ok = false;
+              break;
+            }
+            tm_fence_after();
+            const uint32_t d = tmem + (g & 1) * W;
+            bool acc = false;
+            for (int t = 0; t < P.qterms; ++t)
+              for (int k = 0; k < ksteps; ++k) {
+                const uint32_t db = k >> 2, sub = (k & 3) * 32;
+                umma_f8(d, at_desc(smem_addr(kbuf(q)) + db * AT_BLK + sub, 1024, 2),
+                        at_desc(smem_addr(Qs) + (t * ndb + db) * (W * 128) + sub, 1024, 2), ids,
+                        acc);
+                acc = true;
+              }
+            umma_commit(&kempty[q]);
+            umma_commit(&sfull[g & 1]);
+            ++g;
+            if (++q == NT) {
+              q = 0;
+              ++ph;
+            }
+          }
+          if (i > 0) {
+            const int pg = i < m ? g - 2 : g - 1;  // the tile before the one just issued
+            if (!wait(&vfull[pq], pph & 1) || !wait(&pfull, pg & 1)) {
+              ok = false;
+              break;
+            }
+            tm_fence_after();
+            for (int db = 0; db < ndb; ++db) {
+              const uint32_t d = tmem + 2 * W + db * W;
+              bool acc = i > 1;
+              for (int t = 0; t < AT_PTERMS; ++t)
+                for (int k = 0; k < AT_KEYS / 32; ++k) {
+                  umma_f8(d, at_desc(smem_addr(vbuf(pq)) + db * AT_BLK + k * 4096, 1024, 2),
+                          pd + ((t * PBLK + k * 32 * W) >> 4), ido, acc);
+                  acc = true;
+                }
+            }
+            umma_commit(&vempty[pq]);
+            umma_commit(&pvdone);
+            if (++pq == NT) {
+              pq = 0;
+              ++pph;
+            }
+          }
+        }
+      }
+      if (s_abort) {  // no product may be in flight when the accumulators are freed
+        umma_commit(&drain);
+        const long long t0 = clock64();
+        while (!mbar_test(&drain, 0))
+          if (clock64() - t0 > WAIT_CYCLES / 8) break;
+      }
+    }
+  } else {
+    // ---- Weights and results.
+    const int sw = w - 2, quad = w & 3, grp = sw >> 2;  // lanes 32 quad ..; half of the columns
+    const int st = tid - AT_SM0;
+    const int tok = quad * 32 + lane;  // token of a tile; component of the output
+    const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    // Queries without a token and rows with wrong data: zeros or NaN.
+    for (long long u0 = (long long)blockIdx.x * AT_SM_WARPS + sw; u0 * 32 < (long long)C.batch * A.T;
+         u0 += (long long)gridDim.x * AT_SM_WARPS) {
+      const long long u = u0 * 32 + lane;
+      int fill = 0;
+      if (u < (long long)C.batch * A.T) {
+        const int b = static_cast<int>(u / A.T), t = static_cast<int>(u - (long long)b * A.T);
+        const AtRow r = at_row(A, P, b);
+        fill = r.bad ? 2 : (t >= r.n ? 1 : 0);
+        if (r.bad && t == 0) kv_report(A.S.hdr, ST_DEVICE_INPUT);
+      }
+      unsigned todo = __ballot_sync(0xffffffffu, fill != 0);
+      while (todo) {
+        const int j = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const bool nan = __shfl_sync(0xffffffffu, fill, j) == 2;
+        const long long row = (u0 * 32 + j) * A.q_heads;
+        const uint32_t x = nan ? 0x7fff7fffu : 0u;  // NaN in bf16 and fp16
+        uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.out) + row * C.dim);
+        for (int e = lane; e < A.q_heads * C.dim / 8; e += 32) o[e] = make_uint4(x, x, x, x);
+        if (A.lse)
+          for (int e = lane; e < A.q_heads; e += 32) A.lse[row + e] = nan ? NAN : -INFINITY;
+      }
+    }
+    bool dead = false;  // a wait gave up: skip the work, keep meeting the other warps
+    int g = 0, q = 0, ph = 0;
+    for (; walk.live(); walk.next(A, P)) {
+      const AtTile& tile = walk.tile;
+      const int R = tile.r1 - tile.r0, rh = (R + 1) >> 1, nh = (rh + 7) & ~7;
+      const int m = walk.i1 - walk.i0, len = walk.row.len, n = walk.row.n;
+      const int c0 = grp * nh;  // first column of this group
+      // -- The queries, and what the columns stand for. Every warp is done with the last
+      // query tile first.
+      at_bar(3, AT_SM_THREADS);
+      bool badtree = false;
+      if (A.parent && st < n) {
+        const int p = __ldg(A.parent + (size_t)walk.b * A.T + st);
+        badtree = st > 0 && (p < 0 || p >= st);
+        s_par[st] = p;
+      }
+      badtree = A.parent && at_vote(3, AT_SM_THREADS, badtree);
+      if (badtree && st == 0) kv_report(A.S.hdr, ST_DEVICE_INPUT);
+      if (st < 2 * nh) {
+        const int r = at_row_of(st, R, nh);
+        int pos = -1;
+        unsigned long long see = badtree ? ~0ull : 0ull;  // (a bad tree's scores are NaN)
+        long long out = -1;
+        if (r >= 0) {
+          const int t = (tile.r0 + r) / A.group, gh = tile.r0 + r - t * A.group;
+          pos = len + t;
+          out = ((long long)walk.b * A.T + t) * A.q_heads + walk.h * A.group + gh;
+          if (A.parent && !badtree) {
+            int up = 0;
+            for (int i = t;; i = s_par[i]) {
+              if (!A.window || up < A.window || len + i < A.sinks) see |= 1ull << i;
+              if (i == 0) break;
+              ++up;
+            }
+            pos = len + up;
+          }
+        }
+        s_pos[st] = pos;
+        s_see[st] = see;
+        s_out[st] = out;
+      }
+      for (int col = sw * 2 + (lane >> 4); col < 2 * nh; col += 2 * AT_SM_WARPS) {
+        const int r = at_row_of(col, R, nh), l16 = lane & 15;
+        float f[2][8];
+        float a = 0.f;
+        const uint16_t* src = nullptr;
+        if (r >= 0) {
+          const int t = (tile.r0 + r) / A.group, gh = tile.r0 + r - t * A.group;
+          src = static_cast<const uint16_t*>(A.q) + walk.b * A.q_row + t * A.q_tok +
+                (size_t)(walk.h * A.group + gh) * C.dim;
+        }
 #pragma unroll
-      for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-      s *= C.ks[kv_sidx(C, A.layer, p, h)] * A.scale;
-      const float mn = fmaxf(m, s), f = exp2f(m - mn), x = exp2f(s - mn);
-      const float xv = x * C.vs[kv_sidx(C, A.layer, p, h)];
-      l = l * f + x;
-      m = mn;
+        for (int db = 0; db < 2; ++db) {
+          const int d = db * 128 + l16 * 8;
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (src && d < C.dim) x = __ldg(reinterpret_cast<const uint4*>(src + d));
+          const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-      for (int e = 0; e < AT_E; ++e) o[e] = o[e] * f + xv * v[e];
+          for (int e = 0; e < 4; ++e) {
+            if (P.bf16) {
+              f[db][2 * e] = bf_lo(xw[e]);
+              f[db][2 * e + 1] = bf_hi(xw[e]);
+            } else {
+              const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&xw[e]));
+              f[db][2 * e] = y.x;
+              f[db][2 * e + 1] = y.y;
+            }
+            a = fmaxf(a, fmaxf(fabsf(f[db][2 * e]), fabsf(f[db][2 * e + 1])));
+          }
+        }
+#pragma unroll
+        for (int s = 8; s; s >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, s));
+        const float sc = kv_scale(a), inv = 1.f / sc;
+        if (l16 == 0) {
+          // (An infinite component makes the scores NaN, as the saturating terms would
+          // not; a column without a row keeps weight 0 under any reference.)
+          const bool nan = badtree || a == INFINITY;
+          s_cm[col] = r >= 0 ? make_float2(nan ? NAN : sc * A.scale, 0.f)
+                             : make_float2(0.f, 3.0e38f);
+        }
+#pragma unroll
+        for (int db = 0; db < 2; ++db) {
+          if (db >= ndb) break;
+          float y[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = f[db][e] * inv;
+          unsigned char* dst = Qs + (size_t)db * W * 128 + col * 128 +
+                               (((l16 >> 1) ^ (col & 7)) << 4) + (l16 & 1) * 8;
+          for (int t = 0; t < P.qterms; ++t) {
+            uint2 o;
+            o.x = e4m3x4(y[0], y[1], y[2], y[3]);
+            o.y = e4m3x4(y[4], y[5], y[6], y[7]);
+            *reinterpret_cast<uint2*>(dst + (size_t)t * ndb * W * 128) = o;
+            const uint32_t ow[2] = {o.x, o.y};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float2 lo = e4m3_to_f2(ow[e] & 0xffffu), hi = e4m3_to_f2(ow[e] >> 16);
+              y[4 * e] -= lo.x;
+              y[4 * e + 1] -= lo.y;
+              y[4 * e + 2] -= hi.x;
+              y[4 * e + 3] -= hi.y;
+            }
+          }
+        }
+      }
+      fence_async();
+      at_bar(3, AT_SM_THREADS);
+      if (lane == 0) mbar_arrive(&qfull);
+      float l[MAXC];
+#pragma unroll
+      for (int c = 0; c < MAXC; ++c) l[c] = 0.f;
+
+      // Thread j of a group keeps column c0 + j's state: has its query seen a key?
+      const int j = st - grp * 128, real = grp ? R - rh : rh;
+      bool unseen = j < real, any_unseen = true;
+
+      // -- Key tiles.
+      for (int i = 0; i < m; ++i, ++g) {
+        const int key0 = tile.key_tile(walk.i0 + i) * AT_KEYS, key = key0 + tok;
+        // (The page scales are written before V's barrier is armed.)
+        if (!dead && !(wait(&vfull[q], ph & 1) && wait(&sfull[g & 1], (g >> 1) & 1))) dead = true;
+        tm_fence_after();
+        const int sub = tok >> C.lgp;
+        const float ks = s_ks[q][sub], lv = s_lv[q][sub], iv = s_iv[q][sub];
+        float x[MAXC];
+        const uint32_t sa = tl + (g & 1) * W + c0;
+#pragma unroll
+        for (int c = 0; c < MAXC; c += 8)
+          if (c < nh) tm_ld8(sa + c, x + c);
+        // Is there a key of the tile that some query does not see? Then also look after the
+        // values that weight 0 would not hide: tokens past the end (whatever the page
+        // holds) are zeroed, and a NaN is zeroed where it stands and made the weight of the
+        // queries that do see it.
+        const bool cut = key0 + AT_KEYS > len ||
+                         (A.window && key0 < tile.pos_hi - A.window + 1 && key0 + AT_KEYS > A.sinks);
+        bool vnan = false;
+        if (cut) {
+          for (int db = 0; db < ndb; ++db) {
+            const uint4* p = reinterpret_cast<const uint4*>(vbuf(q) + db * AT_BLK + tok * 128);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const uint4 y = p[e];
+              vnan = vnan || ((__vcmpeq4(y.x & 0x7f7f7f7fu, 0x7f7f7f7fu) |
+                               __vcmpeq4(y.y & 0x7f7f7f7fu, 0x7f7f7f7fu) |
+                               __vcmpeq4(y.z & 0x7f7f7f7fu, 0x7f7f7f7fu) |
+                               __vcmpeq4(y.w & 0x7f7f7f7fu, 0x7f7f7f7fu)) != 0);
+            }
+          }
+          at_bar(3, AT_SM_THREADS);  // both groups have looked
+          if (!dead && (vnan || key >= tile.end)) {
+            for (int db = 0; db < ndb; ++db) {
+              uint32_t* p = reinterpret_cast<uint32_t*>(vbuf(q) + db * AT_BLK + tok * 128);
+              for (int e = 0; e < 32; ++e) {
+                const uint32_t y = p[e];
+                p[e] = key >= tile.end ? 0u : y & ~__vcmpeq4(y & 0x7f7f7f7fu, 0x7f7f7f7fu);
+              }
+            }
+          }
+        }
+        tm_wait_ld<MAXC>(x);
+        tm_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sempty[g & 1]);
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < MAXC; c += 8) {
+          if (c >= nh) continue;
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            const float4 cm = *reinterpret_cast<const float4*>(&s_cm[c0 + c + e]);
+            x[c + e] = fmaf(x[c + e] * ks, cm.x, lv) - cm.y;
+            x[c + e + 1] = fmaf(x[c + e + 1] * ks, cm.z, lv) - cm.w;
+          }
+          if (cut) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int pos = s_pos[c0 + c + e];
+              bool see = !A.window || pos - key < A.window || key < A.sinks;
+              if (key >= len) {
+                const int o = key - len;
+                see = A.parent ? o < n && ((s_see[c0 + c + e] >> (o & 63)) & 1) != 0
+                               : see && key <= pos;
+              }
+              x[c + e] = !see ? -INFINITY : (vnan ? NAN : x[c + e]);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) top = fmaxf(top, x[c + e]);
+        }
+        if (at_vote(1 + grp, 128, any_unseen || top > AT_LIMIT)) {
+          // Move references to the tile's largest scores: maximum over the lanes, then over
+          // the four warps; the outputs and sums so far shrink by the difference.
+#pragma unroll
+          for (int c = 0; c < MAXC; ++c) {
+            if ((c & ~7) >= nh) continue;
+            const int o = __reduce_max_sync(0xffffffffu, at_order(x[c]));
+            if (lane == (c & 31)) s_mx[quad][c0 + c] = o;
+          }
+          at_bar(1 + grp, 128);
+          if (j < nh) {
+            int o = max(s_mx[0][c0 + j], s_mx[1][c0 + j]);
+            o = max(o, max(s_mx[2][c0 + j], s_mx[3][c0 + j]));
+            const float d = at_unorder(o);  // over the reference - 11
+            float move = 0.f, fac = 1.f;
+            if (unseen) {  // nothing to shrink: the reference goes wherever the scores are
+              if (d > -INFINITY) move = d - AT_SHIFT;
+              unseen = d == -INFINITY;
+            } else if (d > AT_SHIFT) {
+              move = d - AT_SHIFT;
+              fac = exp2f(-move);
+            }
+            s_mv[c0 + j] = make_float2(move, fac);
+            s_cm[c0 + j].y += move;
+          }
+          any_unseen = at_vote(1 + grp, 128, unseen);
+          if (i > 0 && !dead && !wait(&pvdone, (g - 1) & 1)) dead = true;
+          tm_fence_after();
+#pragma unroll
+          for (int c = 0; c < MAXC; c += 8) {
+            if (c >= nh) continue;
+            float fac[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float2 mv = s_mv[c0 + c + e];
+              x[c + e] -= mv.x;
+              fac[e] = mv.y;
+              l[c + e] *= mv.y;
+            }
+            if (i == 0) continue;
+            for (int db = 0; db < ndb; ++db) {
+              const uint32_t oa = tl + (2 + db) * W + c0 + c;
+              float o[8];
+              tm_ld8(oa, o);
+              tm_wait_ld<8>(o);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o[e] *= fac[e];
+              tm_st8(oa, o);
+            }
+          }
+          tm_wait_st();
+          tm_fence_before();
+        }
+        // Weights: 2^x, summed with the value scale taken out, rounded to fp16 and split.
+        // A term is the upper byte of the remainder rounded to it (halves away from zero);
+        // what is left of an fp16 number after that is exact.
+        if (i > 0 && !dead && !wait(&pvdone, (g - 1) & 1)) dead = true;
+        unsigned char* prow = Ps + tok * W;
+        const int swz = W == 128 ? (tok & 7) : (W == 64 ? (tok >> 1) & 3 : (tok >> 2) & 1);
+#pragma unroll
+        for (int c = 0; c < MAXC; c += 8) {
+          if (c >= nh) continue;
+          uint32_t t[AT_PTERMS][4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float p0 = ex2(x[c + 2 * e]), p1 = ex2(x[c + 2 * e + 1]);
+            l[c + 2 * e] = fmaf(p0, iv, l[c + 2 * e]);
+            l[c + 2 * e + 1] = fmaf(p1, iv, l[c + 2 * e + 1]);
+            __half2 r = __floats2half2_rn(p0, p1);
+#pragma unroll
+            for (int k = 0; k < AT_PTERMS; ++k) {
+              t[k][e] = *reinterpret_cast<const uint32_t*>(&r) + 0x00800080u;
+              const uint32_t hi = t[k][e] & 0xff00ff00u;
+              r = __hsub2(r, *reinterpret_cast<const __half2*>(&hi));
+            }
+          }
+          const int col = c0 + c;
+          unsigned char* dst = prow + (((col >> 4) ^ swz) << 4) + (col & 8);
+#pragma unroll
+          for (int k = 0; k < AT_PTERMS; ++k)
+            *reinterpret_cast<uint2*>(dst + k * PBLK) =
+                make_uint2(__byte_perm(t[k][0], t[k][1], 0x7531),
+                           __byte_perm(t[k][2], t[k][3], 0x7531));
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull);
+        if (++q == NT) {
+          q = 0;
+          ++ph;
+        }
+      }
+
+      // -- The query tile's sums and outputs: the result when this CTA saw all its keys,
+      // else partial results.
+      if (!dead && !wait(&pvdone, (g - 1) & 1)) dead = true;
+      tm_fence_after();
+      const bool whole = walk.i0 == 0 && walk.i1 == tile.tiles();
+      const int slot_id = 2 * static_cast<int>(cta) + (walk.i0 == 0 ? 1 : 0);
+      constexpr int LC = MAXC < 32 ? MAXC : 32;
+#pragma unroll
+      for (int c = 0; c < MAXC; c += LC) {
+        const float sum = at_lane_sums<LC>(l + c, lane);
+        if (lane < LC && c + lane < nh) s_l[quad][c0 + c + lane] = sum;
+      }
+      at_bar(1 + grp, 128);
+      if (j < real) {
+        const float sum = s_l[0][c0 + j] + s_l[1][c0 + j] + s_l[2][c0 + j] + s_l[3][c0 + j];
+        const float ref = s_cm[c0 + j].y;
+        s_inv[c0 + j] = sum == 0.f ? 0.f : 1.f / sum;
+        if (!whole)
+          A.S.stat[(size_t)slot_id * KV_ROWS + (grp ? rh : 0) + j] = make_float2(ref, sum);
+        else if (A.lse)
+          A.lse[s_out[c0 + j]] =
+              sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+      }
+      at_bar(1 + grp, 128);
+      for (int db = 0; db < ndb; ++db) {
+        const int d = db * 128 + tok;
+#pragma unroll
+        for (int c = 0; c < MAXC; c += 8) {
+          if (c >= nh) continue;
+          float o[8];
+          tm_ld8(tl + (2 + db) * W + c0 + c, o);
+          tm_wait_ld<8>(o);
+          if (d >= C.dim) continue;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (c + e >= real) continue;
+            if (whole) {
+              const float y = s_inv[c0 + c + e] == 0.f ? 0.f : o[e] * s_inv[c0 + c + e];
+              at_store(A.out, s_out[c0 + c + e] * C.dim + d, y, P.bf16);
+            } else {
+              A.S.part[((size_t)slot_id * KV_ROWS + (grp ? rh : 0) + c + e) * C.dim + d] = o[e];
+            }
+          }
+        }
+      }
+      tm_fence_before();
+      if (!whole) {
+        // The CTAs that hold this query tile: the first of them keeps the ticket.
+        const long long u0 = walk.at - walk.i0;
+        const int first = static_cast<int>(((u0 + 1) * ctas - 1) / total);
+        const int last = static_cast<int>(((u0 + tile.tiles()) * ctas - 1) / total);
+        __threadfence();
+        at_bar(3, AT_SM_THREADS);
+        if (st == 0) {
+          const bool end = atomicAdd(A.S.ticket + first, 1u) == static_cast<uint32_t>(last - first);
+          if (end) A.S.ticket[first] = 0;
+          s_last = end;
+        }
+        at_bar(3, AT_SM_THREADS);
+        if (s_last) {
+          __threadfence();
+          const int vec = C.dim / 4;
+          for (int e = st; e < R * vec; e += AT_SM_THREADS) {
+            const int r = e / vec, dv = e - r * vec;
+            auto slot_of = [&](int k) { return (size_t)(2 * k + (k == first ? 1 : 0)) * KV_ROWS + r; };
+            float top = -INFINITY;
+            for (int k = first; k <= last; ++k) {
+              const float2 s2 = __ldcg(A.S.stat + slot_of(k));
+              if (s2.y != 0.f) top = fmaxf(top, s2.x);
+            }
+            float sum = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = first; k <= last; ++k) {
+              const float2 s2 = __ldcg(A.S.stat + slot_of(k));
+              if (s2.y == 0.f) continue;
+              const float f = exp2f(s2.x - top);
+              const float4 y =
+                  __ldcg(reinterpret_cast<const float4*>(A.S.part + slot_of(k) * C.dim) + dv);
+              sum = fmaf(s2.y, f, sum);
+              o.x = fmaf(y.x, f, o.x);
+              o.y = fmaf(y.y, f, o.y);
+              o.z = fmaf(y.z, f, o.z);
+              o.w = fmaf(y.w, f, o.w);
+            }
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const int col = r < rh ? r : nh + r - rh;
+            const long long at = s_out[col] * C.dim + dv * 4;
+            at_store(A.out, at, o.x * inv, P.bf16);
+            at_store(A.out, at + 1, o.y * inv, P.bf16);
+            at_store(A.out, at + 2, o.z * inv, P.bf16);
+            at_store(A.out, at + 3, o.w * inv, P.bf16);
+            if (dv == 0 && A.lse)
+              A.lse[s_out[col]] =
+                  sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+          }
+        }
+      }
     }
   }
-  if (lane == 0) {
-    s_m[w] = m;
-    s_l[w] = l;
-  }
-#pragma unroll
-  for (int e = 0; e < AT_E; ++e)
-    if (lane + 32 * e < C.dim) s_o[w][lane + 32 * e] = o[e];
-  bad = __syncthreads_or(bad ? 1 : 0);
-  float mx = -INFINITY, sum = 0.f;
-  for (int i = 0; i < AT_WARPS; ++i) mx = fmaxf(mx, s_m[i]);
-  for (int i = 0; i < AT_WARPS; ++i)
-    if (s_m[i] != -INFINITY) sum += s_l[i] * exp2f(s_m[i] - mx);
-  for (int d = tid; d < C.dim; d += 32 * AT_WARPS) {
-    float y = 0.f;
-    for (int i = 0; i < AT_WARPS; ++i)
-      if (s_m[i] != -INFINITY) y += s_o[i][d] * exp2f(s_m[i] - mx);
-    y = bad ? NAN : (mx == -INFINITY ? 0.f : y / sum);
-    out[d] = static_cast<Q>(y);
-  }
-  if (tid == 0) {
-    if (bad) kv_report(A.S.hdr, ST_DEVICE_INPUT);
-    if (A.lse)
-      A.lse[row] = bad ? NAN : (mx == -INFINITY ? -INFINITY
-                                                : (mx + log2f(sum)) * 0.6931471805599453f);
+
+  tm_fence_before();
+  __syncthreads();
+  if (w == 1) {
+    __syncwarp();
+    tm_fence_after();
+    const uint32_t need = (2 + ndb) * W, cols = need <= 128 ? 128 : (need <= 256 ? 256 : 512);
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols)
+                 : "memory");
   }
 }
 
+// The driver's tensor-map encoder, looked up once through the runtime.
+static PFN_cuTensorMapEncodeTiled_v12000 at_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    (void)cudaGetLastError();
+  });
+  return fn;
+}
+
+// Shared memory that a kernel may use beside its static arrays (227 KB a CTA).
+constexpr size_t AT_SMEM = 232448 - 12288;
+
 cudaError_t launch_kv_attend(const AttendArgs& A, sv_dtype dt, cudaStream_t st) {
-  const dim3 grid(A.q_heads, A.T, A.C.batch);
-  if (dt == SV_BF16)
-    kv_attend_kernel<__nv_bfloat16><<<grid, 32 * AT_WARPS, 0, st>>>(A);
+  static std::once_flag once;
+  static cudaError_t attr = cudaSuccess;
+  std::call_once(once, [] {
+    const void* ks[3] = {reinterpret_cast<const void*>(kv_attend_kernel<16>),
+                         reinterpret_cast<const void*>(kv_attend_kernel<32>),
+                         reinterpret_cast<const void*>(kv_attend_kernel<64>)};
+    for (int i = 0; i < 3 && attr == cudaSuccess; ++i)
+      attr = cudaFuncSetAttribute(ks[i], cudaFuncAttributeMaxDynamicSharedMemorySize, (int)AT_SMEM);
+  });
+  if (attr != cudaSuccess) return attr;
+  const KvCache& C = A.C;
+  AttendPlan P;
+  P.bf16 = dt == SV_BF16;
+  P.qterms = P.bf16 ? 2 : 3;
+  P.ndb = C.dim > 128 ? 2 : 1;
+  // Above dim 128 the ring's tiles take 64 KB, which leaves room for the queries and weights
+  // of 64 rows.
+  P.rt = P.ndb == 2 ? 64 : KV_ROWS;
+  const long long rows = (long long)A.T * A.group;
+  P.width = rows <= 32 ? 32 : (rows <= 64 || P.rt == 64 ? 64 : 128);
+  const size_t fixed = 1024 + (size_t)P.qterms * P.ndb * P.width * 128 +
+                       (size_t)AT_PTERMS * AT_KEYS * P.width;
+  const size_t stage = (size_t)2 * P.ndb * AT_BLK;
+  P.stages = (int)((AT_SMEM - fixed) / stage);
+  if (P.stages > AT_MAX_STAGES) P.stages = AT_MAX_STAGES;
+  const size_t smem = fixed + P.stages * stage;
+  // The pools of one layer as matrices [pages * heads * page tokens][dim bytes], in boxes of
+  // one page x 128 bytes (128-byte swizzle, zeros past dim).
+  PFN_cuTensorMapEncodeTiled_v12000 enc = at_encoder();
+  if (!enc) return cudaErrorNotSupported;
+  CUtensorMap tm[2];
+  const size_t layer = (size_t)C.pages * C.heads * C.page * C.dim;
+  for (int kv = 0; kv < 2; ++kv) {
+    const cuuint64_t gdim[2] = {(cuuint64_t)C.dim, (cuuint64_t)C.pages * C.heads * C.page};
+    const cuuint64_t gstride[1] = {(cuuint64_t)C.dim};
+    const cuuint32_t box[2] = {128, (cuuint32_t)C.page};
+    const cuuint32_t estr[2] = {1, 1};
+    if (enc(&tm[kv], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, (kv ? C.v : C.k) + A.layer * layer, gdim,
+            gstride, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  int dev = 0, sms = 0;
+  cudaError_t e;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+    return e;
+  const int grid = sms < KV_MAX_CTAS ? sms : KV_MAX_CTAS;
+  if (P.width == 32)
+    kv_attend_kernel<16><<<grid, AT_THREADS, smem, st>>>(A, P, tm[0], tm[1]);
+  else if (P.width == 64)
+    kv_attend_kernel<32><<<grid, AT_THREADS, smem, st>>>(A, P, tm[0], tm[1]);
   else
-    kv_attend_kernel<__half><<<grid, 32 * AT_WARPS, 0, st>>>(A);
+    kv_attend_kernel<64><<<grid, AT_THREADS, smem, st>>>(A, P, tm[0], tm[1]);
   return cudaGetLastError();
 }
 
