@@ -22,9 +22,9 @@
 // A persistent CTA per SM takes an equal share of all (row, head, query tile, key tile)
 // units in order; a query tile that crosses from one CTA to the next leaves partial
 // results (output, m, sum) in the workspace, and the last of its CTAs to arrive joins them.
-// Ten warps, coupled by mbarriers: one copies K and V tiles page by page by tensor-map TMA
-// (128-byte swizzle) into a ring; one issues the products; eight form the weights, four on
-// each half of the query rows.
+// Warps coupled by mbarriers: one copies K and V tiles page by page by tensor-map TMA
+// (128-byte swizzle) into a ring; one issues the products; sixteen form the weights, four
+// to a group, the groups taking eight query rows each in turn.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -38,9 +38,10 @@
 namespace sv {
 
 constexpr int AT_KEYS = 128;     // tokens per key tile
-constexpr int AT_SM_WARPS = 8;   // warps that form the weights
-constexpr int AT_THREADS = 32 * (2 + AT_SM_WARPS);
-constexpr int AT_SM0 = 64;       // first of their threads
+constexpr int AT_GROUPS = 4;     // groups of four warps that form the weights
+constexpr int AT_SM_WARPS = 4 * AT_GROUPS;
+constexpr int AT_THREADS = 32 * (4 + AT_SM_WARPS);  // and a copy, a product, a planning, an idle one
+constexpr int AT_SM0 = 128;      // first of their threads
 constexpr int AT_SM_THREADS = 32 * AT_SM_WARPS;
 constexpr int AT_BLK = AT_KEYS * 128;  // 128 tokens x 128 bytes
 constexpr int AT_MAX_STAGES = 6;
@@ -56,12 +57,15 @@ constexpr float AT_SHIFT = 11.f, AT_LIMIT = 15.f;
 constexpr uint32_t AT_IDESC_S = (1u << 4) | (8u << 24);
 constexpr uint32_t AT_IDESC_O = (1u << 4) | (1u << 10) | (1u << 15) | (1u << 16) | (8u << 24);
 
-__device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                        bool accumulate) {
+// Descriptors are given as their low words (address and the unused leading offset) with the
+// constant high words of the operand's layout.
+__device__ __forceinline__ void umma_f8(uint32_t d, uint32_t alo, uint32_t ahi, uint32_t blo,
+                                        uint32_t bhi, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %2};\n\t"
+      "mov.b64 b, {%3, %4};\n\tsetp.ne.u32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+      "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 __device__ __forceinline__ void umma_commit(uint64_t* bar) {
@@ -103,10 +107,20 @@ __device__ __forceinline__ void tm_wait_st() {
 // Shared-memory matrix descriptor of a swizzled operand whose 8-row groups (K-major: rows;
 // MN-major: steps of K) are `group` bytes apart; rows of 128, 64 or 32 bytes (mode 2, 4, 6).
 // One swizzle atom covers the other dimension, so the leading offset is not used.
-__device__ __forceinline__ uint64_t at_desc(uint32_t addr, uint32_t group, uint32_t mode) {
-  return static_cast<uint64_t>((addr >> 4) & 0x3fffu) | (1ull << 16) |
-         (static_cast<uint64_t>(group >> 4) << 32) | (1ull << 46) |
-         (static_cast<uint64_t>(mode) << 61);
+__device__ __forceinline__ uint32_t at_desc_lo(uint32_t addr) {
+  return ((addr >> 4) & 0x3fffu) | (1u << 16);
+}
+__host__ __device__ constexpr uint32_t at_desc_hi(uint32_t group, uint32_t mode) {
+  return (group >> 4) | (1u << 14) | (mode << 29);
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool at_elect() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
 }
 
 __device__ __forceinline__ void at_tma(void* dst, const CUtensorMap* map, int x, int y,
@@ -210,24 +224,31 @@ __device__ __forceinline__ AtTile at_tile(const AttendArgs& A, const AtRow& r, i
   return t;
 }
 
+// Work is counted in key tiles, with AT_EXTRA more for each query tile: what its queries'
+// conversion and its results cost.
+constexpr int AT_EXTRA = 2;
+
 __device__ __forceinline__ long long at_head_units(const AttendArgs& A, const AtRow& r) {
   long long c = 0;
-  for (int rt = 0; rt < r.nrt; ++rt) c += at_tile(A, r, rt).tiles();
+  for (int rt = 0; rt < r.nrt; ++rt) c += AT_EXTRA + at_tile(A, r, rt).tiles();
   return c;
 }
 
-// The units of this CTA, one query tile after the other: units i0 .. i1 - 1 of the current
-// one. Every role walks the same sequence.
+// The units of this CTA, one query tile after the other: key tiles i0 .. i1 - 1 of the
+// current one. Every role walks the same sequence.
 struct AtWalk {
   int b, h, rt;
   AtRow row;
   AtTile tile;
   int i0, i1;
-  long long at, end;  // unit index of i0, end of the CTA's share
+  long long base, at, end;  // first unit of the query tile, of the share in it, share's end
 
-  __device__ __forceinline__ void settle() {
-    const long long left = end - at;
-    i1 = static_cast<int>(min((long long)tile.tiles(), i0 + left));
+  // The share of the current query tile; false when it has no key tile.
+  __device__ __forceinline__ bool settle() {
+    const long long stop = min(end, base + AT_EXTRA + tile.tiles());
+    i0 = max(0, static_cast<int>(at - base) - AT_EXTRA);
+    i1 = max(0, static_cast<int>(stop - base) - AT_EXTRA);
+    return i1 > i0;
   }
   // From row b0, unit `rem` of it.
   __device__ void start(const AttendArgs& A, const AttendPlan& P, int b0, long long rem,
@@ -242,39 +263,44 @@ struct AtWalk {
     rem -= h * per;
     rt = 0;
     tile = at_tile(A, row, 0);
-    while (rem >= tile.tiles()) {
-      rem -= tile.tiles();
+    while (rem >= AT_EXTRA + tile.tiles()) {
+      rem -= AT_EXTRA + tile.tiles();
       tile = at_tile(A, row, ++rt);
     }
-    i0 = static_cast<int>(rem);
-    settle();
+    base = from - rem;
+    if (!settle()) next(A, P);
   }
   __device__ __forceinline__ bool live() const { return at < end; }
   __device__ void next(const AttendArgs& A, const AttendPlan& P) {
-    at += i1 - i0;
-    if (at >= end) return;
-    i0 = 0;
-    if (++rt == row.nrt) {
-      rt = 0;
-      if (++h == A.C.heads) {
-        h = 0;
-        do {  // (a row with queries exists: units are left)
-          row = at_row(A, P, ++b);
-        } while (row.rows == 0);
+    do {
+      base += AT_EXTRA + tile.tiles();
+      at = base;
+      if (at >= end) return;
+      if (++rt == row.nrt) {
+        rt = 0;
+        if (++h == A.C.heads) {
+          h = 0;
+          do {  // (a row with queries exists: units are left)
+            row = at_row(A, P, ++b);
+          } while (row.rows == 0);
+        }
       }
-    }
-    tile = at_tile(A, row, rt);
-    settle();
+      tile = at_tile(A, row, rt);
+    } while (!settle());
   }
 };
 
-// Column of query row r of a tile of R: the first half of the rows from column 0, the
-// others from column nh; and back (-1: a column without a row).
-__device__ __forceinline__ int at_row_of(int col, int R, int nh) {
-  const int rh = (R + 1) >> 1;
-  if (col < nh) return col < rh ? col : -1;
-  return col - nh < R - rh ? rh + col - nh : -1;
-}
+// A query tile's share as the product and weight warps read it from shared memory.
+struct AtItem {
+  int b, h, len, n;
+  int r0, R;        // query rows r0 .. r0 + R - 1 of the head
+  int i0, m;        // key tiles i0 .. i0 + m - 1 (m = 0: no more work)
+  int tiles;        // of the query tile
+  int end, pos_hi;  // as AtTile
+  int ns, lo;
+  long long u0;     // unit of its first key tile
+  __device__ __forceinline__ int key_tile(int i) const { return i < ns ? i : lo + i - ns; }
+};
 
 // Sums of C values over the 32 lanes (C a power of two up to 32): lane c (mod C) gets
 // column c's, by halving the columns a lane is responsible for at each exchange.
@@ -311,13 +337,13 @@ __device__ __forceinline__ float at_unorder(int i) {
   return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
 }
 
-// MAXC: most columns of a thread (half of the plan's width).
-template <int MAXC>
+// W: columns of an accumulator (query rows), bytes of a token's weights.
+template <int W>
 __global__ void __launch_bounds__(AT_THREADS, 1)
     kv_attend_kernel(const AttendArgs A, const AttendPlan P,
                      const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV) {
-  constexpr int W = 2 * MAXC;  // columns of an accumulator, bytes of a token's weights
+  constexpr int SLOTS = W / 8 / AT_GROUPS;  // eights of columns of a thread, at most
   constexpr uint32_t PMODE = W == 128 ? 2 : (W == 64 ? 4 : 6);
   constexpr int PBLK = AT_KEYS * W;
   extern __shared__ unsigned char dsm_raw[];
@@ -327,6 +353,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
   __shared__ int s_b0, s_last;
+  __shared__ int s_vnan[2][AT_KEYS];
+  __shared__ AtItem s_item[2];  // of item k at k & 1
   __shared__ long long s_rem, s_sum[AT_THREADS / 32];
   // Per stage and page of the tile: key scale, log2 and inverse of the value scale.
   __shared__ float s_ks[AT_MAX_STAGES][8], s_lv[AT_MAX_STAGES][8], s_iv[AT_MAX_STAGES][8];
@@ -445,10 +473,16 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   __syncthreads();
   tm_fence_after();
   const uint32_t tmem = s_tmem;
-  AtWalk walk;
-  walk.start(A, P, s_b0, s_rem, from, to);
+  // Registers move from the first four warps to those that form the weights: 128 x 64 +
+  // 512 x 104 is what the launch gave (640 x 96).
+  if (w < 4)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+  else
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
 
   if (w == 0) {
+    AtWalk walk;
+    walk.start(A, P, s_b0, s_rem, from, to);
     // ---- Copies: pages of one or more tiles are looked up at a time, a page per lane and
     // a step ahead of their use.
     const int ppt = AT_KEYS >> C.lgp;  // pages per tile
@@ -550,19 +584,20 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   } else if (w == 1) {
     // ---- Products. Scores of tile i, then the output of tile i - 1, so that a tile's
     // weights form while the next tile's scores multiply.
-    if (lane == 0) {
+    if (at_elect()) {
       const int ksteps = (C.dim + 31) / 32;
-      const uint64_t pd = at_desc(smem_addr(Ps), 8 * W, PMODE);
+      constexpr uint32_t HI128 = at_desc_hi(1024, 2), HIP = at_desc_hi(8 * W, PMODE);
+      const uint32_t qd = at_desc_lo(smem_addr(Qs)), pd = at_desc_lo(smem_addr(Ps));
+      const uint32_t ring0 = at_desc_lo(smem_addr(ring)), rstep = static_cast<uint32_t>(slot) >> 4;
       bool ok = true;
       int g = 0, q = 0, ph = 0, item = 0;
       int pq = 0, pph = 0;  // stage of the tile whose output is next
-      for (; ok && walk.live(); walk.next(A, P), ++item) {
-        const int R = walk.tile.r1 - walk.tile.r0;
-        const int N = 2 * ((((R + 1) >> 1) + 7) & ~7);
-        const uint32_t ids = AT_IDESC_S | (static_cast<uint32_t>(N >> 3) << 17);
-        const uint32_t ido = AT_IDESC_O | (static_cast<uint32_t>(N >> 3) << 17);
-        const int m = walk.i1 - walk.i0;
+      for (; ok; ++item) {
         if (!wait(&qfull, item & 1)) break;
+        const int R = s_item[item & 1].R, m = s_item[item & 1].m;
+        if (m == 0) break;
+        const uint32_t N8 = static_cast<uint32_t>((R + 15) >> 4) * 2;  // N / 8
+        const uint32_t ids = AT_IDESC_S | (N8 << 17), ido = AT_IDESC_O | (N8 << 17);
         for (int i = 0; i <= m; ++i) {
           if (i < m) {
             if (!wait(&kfull[q], ph & 1) || (g >= 2 && !wait(&sempty[g & 1], ((g >> 1) - 1) & 1))) {
@@ -570,15 +605,14 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
               break;
             }
             tm_fence_after();
-            const uint32_t d = tmem + (g & 1) * W;
-            bool acc = false;
+            const uint32_t d = tmem + (g & 1) * W, ka = ring0 + 2 * q * rstep;
             for (int t = 0; t < P.qterms; ++t)
-              for (int k = 0; k < ksteps; ++k) {
-                const uint32_t db = k >> 2, sub = (k & 3) * 32;
-                umma_f8(d, at_desc(smem_addr(kbuf(q)) + db * AT_BLK + sub, 1024, 2),
-                        at_desc(smem_addr(Qs) + (t * ndb + db) * (W * 128) + sub, 1024, 2), ids,
-                        acc);
-                acc = true;
+              for (int db = 0; db < ndb; ++db) {
+                const uint32_t al = ka + db * (AT_BLK >> 4), bl = qd + (t * ndb + db) * (W * 8);
+                const int kn = ksteps - 4 * db;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  if (k < kn) umma_f8(d, al + 2 * k, HI128, bl + 2 * k, HI128, ids, t + db + k);
               }
             umma_commit(&kempty[q]);
             umma_commit(&sfull[g & 1]);
@@ -596,14 +630,14 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             }
             tm_fence_after();
             for (int db = 0; db < ndb; ++db) {
-              const uint32_t d = tmem + 2 * W + db * W;
-              bool acc = i > 1;
+              const uint32_t d = tmem + (2 + db) * W;
+              const uint32_t va = ring0 + (2 * pq + 1) * rstep + db * (AT_BLK >> 4);
+#pragma unroll
               for (int t = 0; t < AT_PTERMS; ++t)
-                for (int k = 0; k < AT_KEYS / 32; ++k) {
-                  umma_f8(d, at_desc(smem_addr(vbuf(pq)) + db * AT_BLK + k * 4096, 1024, 2),
-                          pd + ((t * PBLK + k * 32 * W) >> 4), ido, acc);
-                  acc = true;
-                }
+#pragma unroll
+                for (int k = 0; k < AT_KEYS / 32; ++k)
+                  umma_f8(d, va + k * (4096 >> 4), HI128, pd + ((t * PBLK + k * 32 * W) >> 4), HIP,
+                          ido, t + k > 0 ? 1u : (i > 1 ? 1u : 0u));
             }
             umma_commit(&vempty[pq]);
             umma_commit(&pvdone);
@@ -621,9 +655,39 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           if (clock64() - t0 > WAIT_CYCLES / 8) break;
       }
     }
+  } else if (w == 2) {
+    // ---- Planning: item k + 1 while item k is in work.
+    AtWalk walk;
+    walk.start(A, P, s_b0, s_rem, from, to);
+    for (int k = 0;; ++k) {
+      const bool live = walk.live();
+      if (lane == 0) {
+        AtItem& o = s_item[k & 1];
+        o.m = live ? walk.i1 - walk.i0 : 0;
+        o.b = walk.b;
+        o.h = walk.h;
+        o.len = walk.row.len;
+        o.n = walk.row.n;
+        o.r0 = walk.tile.r0;
+        o.R = walk.tile.r1 - walk.tile.r0;
+        o.i0 = walk.i0;
+        o.tiles = walk.tile.tiles();
+        o.end = walk.tile.end;
+        o.pos_hi = walk.tile.pos_hi;
+        o.ns = walk.tile.ns;
+        o.lo = walk.tile.lo;
+        o.u0 = walk.base + AT_EXTRA;
+      }
+      __syncwarp();
+      at_bar(6, AT_SM_THREADS + 32);  // item k is there, item k - 1 done with
+      if (!live) break;
+      walk.next(A, P);
+    }
+  } else if (w == 3) {
+    // (idle: it fills the first four warps)
   } else {
     // ---- Weights and results.
-    const int sw = w - 2, quad = w & 3, grp = sw >> 2;  // lanes 32 quad ..; half of the columns
+    const int sw = w - 4, quad = w & 3, grp = sw >> 2;  // lanes 32 quad ..; eights of columns
     const int st = tid - AT_SM0;
     const int tok = quad * 32 + lane;  // token of a tile; component of the output
     const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
@@ -653,31 +717,37 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     }
     bool dead = false;  // a wait gave up: skip the work, keep meeting the other warps
     int g = 0, q = 0, ph = 0;
-    for (; walk.live(); walk.next(A, P)) {
-      const AtTile& tile = walk.tile;
-      const int R = tile.r1 - tile.r0, rh = (R + 1) >> 1, nh = (rh + 7) & ~7;
-      const int m = walk.i1 - walk.i0, len = walk.row.len, n = walk.row.n;
-      const int c0 = grp * nh;  // first column of this group
-      // -- The queries, and what the columns stand for. Every warp is done with the last
-      // query tile first.
-      at_bar(3, AT_SM_THREADS);
-      bool badtree = false;
-      if (A.parent && st < n) {
-        const int p = __ldg(A.parent + (size_t)walk.b * A.T + st);
-        badtree = st > 0 && (p < 0 || p >= st);
-        s_par[st] = p;
+    for (int item = 0;; ++item) {
+      // Every warp is done with the last query tile.
+      at_bar(6, AT_SM_THREADS + 32);
+      const AtItem& it = s_item[item & 1];
+      const int R = it.R, m = it.m, len = it.len, N = (R + 15) & ~15;
+      if (m == 0) {
+        if (lane == 0) mbar_arrive(&qfull);  // the product warp sees it too
+        break;
       }
-      badtree = A.parent && at_vote(3, AT_SM_THREADS, badtree);
-      if (badtree && st == 0) kv_report(A.S.hdr, ST_DEVICE_INPUT);
-      if (st < 2 * nh) {
-        const int r = at_row_of(st, R, nh);
+      // Columns of this thread: eights grp, grp + 4, ...; `mine` of them have a row.
+      const int mine = max(0, (((R + 7) >> 3) - grp + AT_GROUPS - 1) / AT_GROUPS);
+      auto col0 = [&](int slot) { return (grp + AT_GROUPS * slot) * 8; };
+      // -- The queries, and what the columns stand for.
+      bool badtree = false;
+      if (A.parent) {
+        if (st < it.n) {
+          const int p = __ldg(A.parent + (size_t)it.b * A.T + st);
+          badtree = st > 0 && (p < 0 || p >= st);
+          s_par[st] = p;
+        }
+        badtree = at_vote(5, AT_SM_THREADS, badtree);
+        if (badtree && st == 0) kv_report(A.S.hdr, ST_DEVICE_INPUT);
+      }
+      if (st < N) {
         int pos = -1;
         unsigned long long see = badtree ? ~0ull : 0ull;  // (a bad tree's scores are NaN)
         long long out = -1;
-        if (r >= 0) {
-          const int t = (tile.r0 + r) / A.group, gh = tile.r0 + r - t * A.group;
+        if (st < R) {
+          const int t = (it.r0 + st) / A.group, gh = it.r0 + st - t * A.group;
           pos = len + t;
-          out = ((long long)walk.b * A.T + t) * A.q_heads + walk.h * A.group + gh;
+          out = ((long long)it.b * A.T + t) * A.q_heads + it.h * A.group + gh;
           if (A.parent && !badtree) {
             int up = 0;
             for (int i = t;; i = s_par[i]) {
@@ -692,15 +762,15 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         s_see[st] = see;
         s_out[st] = out;
       }
-      for (int col = sw * 2 + (lane >> 4); col < 2 * nh; col += 2 * AT_SM_WARPS) {
-        const int r = at_row_of(col, R, nh), l16 = lane & 15;
+      for (int col = sw * 2 + (lane >> 4); col < N; col += 2 * AT_SM_WARPS) {
+        const int l16 = lane & 15;
         float f[2][8];
         float a = 0.f;
         const uint16_t* src = nullptr;
-        if (r >= 0) {
-          const int t = (tile.r0 + r) / A.group, gh = tile.r0 + r - t * A.group;
-          src = static_cast<const uint16_t*>(A.q) + walk.b * A.q_row + t * A.q_tok +
-                (size_t)(walk.h * A.group + gh) * C.dim;
+        if (col < R) {
+          const int t = (it.r0 + col) / A.group, gh = it.r0 + col - t * A.group;
+          src = static_cast<const uint16_t*>(A.q) + it.b * A.q_row + t * A.q_tok +
+                (size_t)(it.h * A.group + gh) * C.dim;
         }
 #pragma unroll
         for (int db = 0; db < 2; ++db) {
@@ -728,8 +798,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           // (An infinite component makes the scores NaN, as the saturating terms would
           // not; a column without a row keeps weight 0 under any reference.)
           const bool nan = badtree || a == INFINITY;
-          s_cm[col] = r >= 0 ? make_float2(nan ? NAN : sc * A.scale, 0.f)
-                             : make_float2(0.f, 3.0e38f);
+          s_cm[col] = col < R ? make_float2(nan ? NAN : sc * A.scale, 0.f)
+                              : make_float2(0.f, 3.0e38f);
         }
 #pragma unroll
         for (int db = 0; db < 2; ++db) {
@@ -757,102 +827,110 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         }
       }
       fence_async();
-      at_bar(3, AT_SM_THREADS);
+      at_bar(5, AT_SM_THREADS);
       if (lane == 0) mbar_arrive(&qfull);
-      float l[MAXC];
+      float l[8 * SLOTS];
 #pragma unroll
-      for (int c = 0; c < MAXC; ++c) l[c] = 0.f;
-
-      // Thread j of a group keeps column c0 + j's state: has its query seen a key?
-      const int j = st - grp * 128, real = grp ? R - rh : rh;
-      bool unseen = j < real, any_unseen = true;
+      for (int c = 0; c < 8 * SLOTS; ++c) l[c] = 0.f;
+      // Thread j of a group keeps the state of its column j: has its query seen a key?
+      const int j = st & 127, jcol = col0(j >> 3) + (j & 7);
+      const bool jreal = j < 8 * SLOTS && jcol < R;
+      bool unseen = jreal, any_unseen = mine > 0;
 
       // -- Key tiles.
       for (int i = 0; i < m; ++i, ++g) {
-        const int key0 = tile.key_tile(walk.i0 + i) * AT_KEYS, key = key0 + tok;
+        const int key0 = it.key_tile(it.i0 + i) * AT_KEYS, key = key0 + tok;
         // (The page scales are written before V's barrier is armed.)
         if (!dead && !(wait(&vfull[q], ph & 1) && wait(&sfull[g & 1], (g >> 1) & 1))) dead = true;
         tm_fence_after();
         const int sub = tok >> C.lgp;
         const float ks = s_ks[q][sub], lv = s_lv[q][sub], iv = s_iv[q][sub];
-        float x[MAXC];
-        const uint32_t sa = tl + (g & 1) * W + c0;
+        float x[8 * SLOTS];
+        const uint32_t sa = tl + (g & 1) * W;
 #pragma unroll
-        for (int c = 0; c < MAXC; c += 8)
-          if (c < nh) tm_ld8(sa + c, x + c);
+        for (int s = 0; s < SLOTS; ++s)
+          if (s < mine) tm_ld8(sa + col0(s), x + 8 * s);
         // Is there a key of the tile that some query does not see? Then also look after the
         // values that weight 0 would not hide: tokens past the end (whatever the page
         // holds) are zeroed, and a NaN is zeroed where it stands and made the weight of the
         // queries that do see it.
         const bool cut = key0 + AT_KEYS > len ||
-                         (A.window && key0 < tile.pos_hi - A.window + 1 && key0 + AT_KEYS > A.sinks);
+                         (A.window && key0 < it.pos_hi - A.window + 1 && key0 + AT_KEYS > A.sinks);
         bool vnan = false;
         if (cut) {
-          for (int db = 0; db < ndb; ++db) {
-            const uint4* p = reinterpret_cast<const uint4*>(vbuf(q) + db * AT_BLK + tok * 128);
+          // A group looks at two of a token's eight 16-byte chunks, turned so that the lanes
+          // of a warp spread over the banks.
+          if (grp == 0) s_vnan[g & 1][tok] = 0;
+          at_bar(5, AT_SM_THREADS);
+          for (int db = 0; db < ndb && !dead; ++db) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const uint4 y = p[e];
-              vnan = vnan || ((__vcmpeq4(y.x & 0x7f7f7f7fu, 0x7f7f7f7fu) |
-                               __vcmpeq4(y.y & 0x7f7f7f7fu, 0x7f7f7f7fu) |
-                               __vcmpeq4(y.z & 0x7f7f7f7fu, 0x7f7f7f7fu) |
-                               __vcmpeq4(y.w & 0x7f7f7f7fu, 0x7f7f7f7fu)) != 0);
-            }
-          }
-          at_bar(3, AT_SM_THREADS);  // both groups have looked
-          if (!dead && (vnan || key >= tile.end)) {
-            for (int db = 0; db < ndb; ++db) {
-              uint32_t* p = reinterpret_cast<uint32_t*>(vbuf(q) + db * AT_BLK + tok * 128);
-              for (int e = 0; e < 32; ++e) {
-                const uint32_t y = p[e];
-                p[e] = key >= tile.end ? 0u : y & ~__vcmpeq4(y & 0x7f7f7f7fu, 0x7f7f7f7fu);
+            for (int e = 0; e < 2; ++e) {
+              uint4* p = reinterpret_cast<uint4*>(vbuf(q) + db * AT_BLK + tok * 128) +
+                         ((2 * grp + e + tok) & 7);
+              if (key >= it.end) {
+                *p = make_uint4(0, 0, 0, 0);
+                continue;
+              }
+              uint4 y = *p;
+              const uint4 z = make_uint4(
+                  __vcmpeq4(y.x & 0x7f7f7f7fu, 0x7f7f7f7fu), __vcmpeq4(y.y & 0x7f7f7f7fu, 0x7f7f7f7fu),
+                  __vcmpeq4(y.z & 0x7f7f7f7fu, 0x7f7f7f7fu), __vcmpeq4(y.w & 0x7f7f7f7fu, 0x7f7f7f7fu));
+              if (z.x | z.y | z.z | z.w) {
+                s_vnan[g & 1][tok] = 1;
+                *p = make_uint4(y.x & ~z.x, y.y & ~z.y, y.z & ~z.z, y.w & ~z.w);
               }
             }
           }
+          at_bar(5, AT_SM_THREADS);
+          vnan = s_vnan[g & 1][tok] != 0;
         }
-        tm_wait_ld<MAXC>(x);
+        tm_wait_ld<8 * SLOTS>(x);
         tm_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sempty[g & 1]);
         float top = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < MAXC; c += 8) {
-          if (c >= nh) continue;
+        for (int s = 0; s < SLOTS; ++s) {
+          if (s >= mine) continue;
+          const int c0 = col0(s);
 #pragma unroll
           for (int e = 0; e < 8; e += 2) {
-            const float4 cm = *reinterpret_cast<const float4*>(&s_cm[c0 + c + e]);
-            x[c + e] = fmaf(x[c + e] * ks, cm.x, lv) - cm.y;
-            x[c + e + 1] = fmaf(x[c + e + 1] * ks, cm.z, lv) - cm.w;
+            const float4 cm = *reinterpret_cast<const float4*>(&s_cm[c0 + e]);
+            x[8 * s + e] = fmaf(x[8 * s + e], ks * cm.x, lv - cm.y);
+            x[8 * s + e + 1] = fmaf(x[8 * s + e + 1], ks * cm.z, lv - cm.w);
           }
           if (cut) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const int pos = s_pos[c0 + c + e];
+              const int pos = s_pos[c0 + e];
               bool see = !A.window || pos - key < A.window || key < A.sinks;
               if (key >= len) {
                 const int o = key - len;
-                see = A.parent ? o < n && ((s_see[c0 + c + e] >> (o & 63)) & 1) != 0
+                see = A.parent ? o < it.n && ((s_see[c0 + e] >> (o & 63)) & 1) != 0
                                : see && key <= pos;
               }
-              x[c + e] = !see ? -INFINITY : (vnan ? NAN : x[c + e]);
+              x[8 * s + e] = !see ? -INFINITY : (vnan ? NAN : x[8 * s + e]);
             }
           }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) top = fmaxf(top, x[c + e]);
+          for (int e = 0; e < 8; ++e) top = fmaxf(top, x[8 * s + e]);
         }
-        if (at_vote(1 + grp, 128, any_unseen || top > AT_LIMIT)) {
+        if (mine && at_vote(1 + grp, 128, any_unseen || top > AT_LIMIT)) {
           // Move references to the tile's largest scores: maximum over the lanes, then over
           // the four warps; the outputs and sums so far shrink by the difference.
 #pragma unroll
-          for (int c = 0; c < MAXC; ++c) {
-            if ((c & ~7) >= nh) continue;
-            const int o = __reduce_max_sync(0xffffffffu, at_order(x[c]));
-            if (lane == (c & 31)) s_mx[quad][c0 + c] = o;
+          for (int s = 0; s < SLOTS; ++s) {
+            if (s >= mine) continue;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int o = __reduce_max_sync(0xffffffffu, at_order(x[8 * s + e]));
+              if (lane == e) s_mx[quad][col0(s) + e] = o;
+            }
           }
           at_bar(1 + grp, 128);
-          if (j < nh) {
-            int o = max(s_mx[0][c0 + j], s_mx[1][c0 + j]);
-            o = max(o, max(s_mx[2][c0 + j], s_mx[3][c0 + j]));
+          if (jreal) {
+            int o = max(s_mx[0][jcol], s_mx[1][jcol]);
+            o = max(o, max(s_mx[2][jcol], s_mx[3][jcol]));
             const float d = at_unorder(o);  // over the reference - 11
             float move = 0.f, fac = 1.f;
             if (unseen) {  // nothing to shrink: the reference goes wherever the scores are
@@ -862,26 +940,28 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
               move = d - AT_SHIFT;
               fac = exp2f(-move);
             }
-            s_mv[c0 + j] = make_float2(move, fac);
-            s_cm[c0 + j].y += move;
+            s_mv[jcol] = make_float2(move, fac);
+            s_cm[jcol].y += move;
+          } else if (j < 8 * SLOTS) {
+            s_mv[jcol] = make_float2(0.f, 1.f);
           }
           any_unseen = at_vote(1 + grp, 128, unseen);
           if (i > 0 && !dead && !wait(&pvdone, (g - 1) & 1)) dead = true;
           tm_fence_after();
 #pragma unroll
-          for (int c = 0; c < MAXC; c += 8) {
-            if (c >= nh) continue;
+          for (int s = 0; s < SLOTS; ++s) {
+            if (s >= mine) continue;
             float fac[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float2 mv = s_mv[c0 + c + e];
-              x[c + e] -= mv.x;
+              const float2 mv = s_mv[col0(s) + e];
+              x[8 * s + e] -= mv.x;
               fac[e] = mv.y;
-              l[c + e] *= mv.y;
+              l[8 * s + e] *= mv.y;
             }
             if (i == 0) continue;
             for (int db = 0; db < ndb; ++db) {
-              const uint32_t oa = tl + (2 + db) * W + c0 + c;
+              const uint32_t oa = tl + (2 + db) * W + col0(s);
               float o[8];
               tm_ld8(oa, o);
               tm_wait_ld<8>(o);
@@ -900,14 +980,15 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         unsigned char* prow = Ps + tok * W;
         const int swz = W == 128 ? (tok & 7) : (W == 64 ? (tok >> 1) & 3 : (tok >> 2) & 1);
 #pragma unroll
-        for (int c = 0; c < MAXC; c += 8) {
-          if (c >= nh) continue;
+        for (int s = 0; s < SLOTS; ++s) {
+          if (s >= mine) continue;
           uint32_t t[AT_PTERMS][4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float p0 = ex2(x[c + 2 * e]), p1 = ex2(x[c + 2 * e + 1]);
-            l[c + 2 * e] = fmaf(p0, iv, l[c + 2 * e]);
-            l[c + 2 * e + 1] = fmaf(p1, iv, l[c + 2 * e + 1]);
+            const int c = 8 * s + 2 * e;
+            const float p0 = ex2(x[c]), p1 = ex2(x[c + 1]);
+            l[c] = fmaf(p0, iv, l[c]);
+            l[c + 1] = fmaf(p1, iv, l[c + 1]);
             __half2 r = __floats2half2_rn(p0, p1);
 #pragma unroll
             for (int k = 0; k < AT_PTERMS; ++k) {
@@ -916,8 +997,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
               r = __hsub2(r, *reinterpret_cast<const __half2*>(&hi));
             }
           }
-          const int col = c0 + c;
-          unsigned char* dst = prow + (((col >> 4) ^ swz) << 4) + (col & 8);
+          unsigned char* dst = prow + (((col0(s) >> 4) ^ swz) << 4) + (col0(s) & 8);
 #pragma unroll
           for (int k = 0; k < AT_PTERMS; ++k)
             *reinterpret_cast<uint2*>(dst + k * PBLK) =
@@ -937,43 +1017,43 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       // else partial results.
       if (!dead && !wait(&pvdone, (g - 1) & 1)) dead = true;
       tm_fence_after();
-      const bool whole = walk.i0 == 0 && walk.i1 == tile.tiles();
-      const int slot_id = 2 * static_cast<int>(cta) + (walk.i0 == 0 ? 1 : 0);
-      constexpr int LC = MAXC < 32 ? MAXC : 32;
+      const bool whole = m == it.tiles;
+      const int slot_id = 2 * static_cast<int>(cta) + (it.i0 == 0 ? 1 : 0);
+      if (mine) {
+        constexpr int LC = 8 * SLOTS;
+        const float lsum = at_lane_sums<LC>(l, lane);
+        if (lane < LC) s_l[quad][col0(lane >> 3) + (lane & 7)] = lsum;
+        at_bar(1 + grp, 128);
+        if (jreal) {
+          const float sum = s_l[0][jcol] + s_l[1][jcol] + s_l[2][jcol] + s_l[3][jcol];
+          const float ref = s_cm[jcol].y;
+          s_inv[jcol] = sum == 0.f ? 0.f : 1.f / sum;
+          if (!whole)
+            A.S.stat[(size_t)slot_id * KV_ROWS + jcol] = make_float2(ref, sum);
+          else if (A.lse)
+            A.lse[s_out[jcol]] =
+                sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+        }
+        at_bar(1 + grp, 128);
+        for (int db = 0; db < ndb; ++db) {
+          const int d = db * 128 + tok;
 #pragma unroll
-      for (int c = 0; c < MAXC; c += LC) {
-        const float sum = at_lane_sums<LC>(l + c, lane);
-        if (lane < LC && c + lane < nh) s_l[quad][c0 + c + lane] = sum;
-      }
-      at_bar(1 + grp, 128);
-      if (j < real) {
-        const float sum = s_l[0][c0 + j] + s_l[1][c0 + j] + s_l[2][c0 + j] + s_l[3][c0 + j];
-        const float ref = s_cm[c0 + j].y;
-        s_inv[c0 + j] = sum == 0.f ? 0.f : 1.f / sum;
-        if (!whole)
-          A.S.stat[(size_t)slot_id * KV_ROWS + (grp ? rh : 0) + j] = make_float2(ref, sum);
-        else if (A.lse)
-          A.lse[s_out[c0 + j]] =
-              sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
-      }
-      at_bar(1 + grp, 128);
-      for (int db = 0; db < ndb; ++db) {
-        const int d = db * 128 + tok;
+          for (int s = 0; s < SLOTS; ++s) {
+            if (s >= mine) continue;
+            const int c0 = col0(s);
+            float o[8];
+            tm_ld8(tl + (2 + db) * W + c0, o);
+            tm_wait_ld<8>(o);
+            if (d >= C.dim) continue;
 #pragma unroll
-        for (int c = 0; c < MAXC; c += 8) {
-          if (c >= nh) continue;
-          float o[8];
-          tm_ld8(tl + (2 + db) * W + c0 + c, o);
-          tm_wait_ld<8>(o);
-          if (d >= C.dim) continue;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (c + e >= real) continue;
-            if (whole) {
-              const float y = s_inv[c0 + c + e] == 0.f ? 0.f : o[e] * s_inv[c0 + c + e];
-              at_store(A.out, s_out[c0 + c + e] * C.dim + d, y, P.bf16);
-            } else {
-              A.S.part[((size_t)slot_id * KV_ROWS + (grp ? rh : 0) + c + e) * C.dim + d] = o[e];
+            for (int e = 0; e < 8; ++e) {
+              if (c0 + e >= R) continue;
+              if (whole) {
+                const float inv = s_inv[c0 + e];
+                at_store(A.out, s_out[c0 + e] * C.dim + d, inv == 0.f ? 0.f : o[e] * inv, P.bf16);
+              } else {
+                A.S.part[((size_t)slot_id * KV_ROWS + c0 + e) * C.dim + d] = o[e];
+              }
             }
           }
         }
@@ -981,17 +1061,16 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       tm_fence_before();
       if (!whole) {
         // The CTAs that hold this query tile: the first of them keeps the ticket.
-        const long long u0 = walk.at - walk.i0;
-        const int first = static_cast<int>(((u0 + 1) * ctas - 1) / total);
-        const int last = static_cast<int>(((u0 + tile.tiles()) * ctas - 1) / total);
+        const int first = static_cast<int>(((it.u0 + 1) * ctas - 1) / total);
+        const int last = static_cast<int>(((it.u0 + it.tiles) * ctas - 1) / total);
         __threadfence();
-        at_bar(3, AT_SM_THREADS);
+        at_bar(5, AT_SM_THREADS);
         if (st == 0) {
           const bool end = atomicAdd(A.S.ticket + first, 1u) == static_cast<uint32_t>(last - first);
           if (end) A.S.ticket[first] = 0;
           s_last = end;
         }
-        at_bar(3, AT_SM_THREADS);
+        at_bar(5, AT_SM_THREADS);
         if (s_last) {
           __threadfence();
           const int vec = C.dim / 4;
@@ -1018,14 +1097,13 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
               o.w = fmaf(y.w, f, o.w);
             }
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            const int col = r < rh ? r : nh + r - rh;
-            const long long at = s_out[col] * C.dim + dv * 4;
+            const long long at = s_out[r] * C.dim + dv * 4;
             at_store(A.out, at, o.x * inv, P.bf16);
             at_store(A.out, at + 1, o.y * inv, P.bf16);
             at_store(A.out, at + 2, o.z * inv, P.bf16);
             at_store(A.out, at + 3, o.w * inv, P.bf16);
             if (dv == 0 && A.lse)
-              A.lse[s_out[col]] =
+              A.lse[s_out[r]] =
                   sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
           }
         }
@@ -1067,9 +1145,9 @@ cudaError_t launch_kv_attend(const AttendArgs& A, sv_dtype dt, cudaStream_t st) 
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
   std::call_once(once, [] {
-    const void* ks[3] = {reinterpret_cast<const void*>(kv_attend_kernel<16>),
-                         reinterpret_cast<const void*>(kv_attend_kernel<32>),
-                         reinterpret_cast<const void*>(kv_attend_kernel<64>)};
+    const void* ks[3] = {reinterpret_cast<const void*>(kv_attend_kernel<32>),
+                         reinterpret_cast<const void*>(kv_attend_kernel<64>),
+                         reinterpret_cast<const void*>(kv_attend_kernel<128>)};
     for (int i = 0; i < 3 && attr == cudaSuccess; ++i)
       attr = cudaFuncSetAttribute(ks[i], cudaFuncAttributeMaxDynamicSharedMemorySize, (int)AT_SMEM);
   });
@@ -1113,11 +1191,11 @@ cudaError_t launch_kv_attend(const AttendArgs& A, sv_dtype dt, cudaStream_t st) 
     return e;
   const int grid = sms < KV_MAX_CTAS ? sms : KV_MAX_CTAS;
   if (P.width == 32)
-    kv_attend_kernel<16><<<grid, AT_THREADS, smem, st>>>(A, P, tm[0], tm[1]);
-  else if (P.width == 64)
     kv_attend_kernel<32><<<grid, AT_THREADS, smem, st>>>(A, P, tm[0], tm[1]);
-  else
+  else if (P.width == 64)
     kv_attend_kernel<64><<<grid, AT_THREADS, smem, st>>>(A, P, tm[0], tm[1]);
+  else
+    kv_attend_kernel<128><<<grid, AT_THREADS, smem, st>>>(A, P, tm[0], tm[1]);
   return cudaGetLastError();
 }
 
