@@ -79,6 +79,32 @@ __device__ __forceinline__ void tm_fence_before() {
 __device__ __forceinline__ void tm_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
+// Two float32 operations in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
 // Eight consecutive float32 columns of this thread's lane; complete after tm_wait_ld.
 __device__ __forceinline__ void tm_ld8(uint32_t addr, float* v) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -358,7 +384,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   __shared__ long long s_rem, s_sum[AT_THREADS / 32];
   // Per stage and page of the tile: key scale, log2 and inverse of the value scale.
   __shared__ float s_ks[AT_MAX_STAGES][8], s_lv[AT_MAX_STAGES][8], s_iv[AT_MAX_STAGES][8];
-  __shared__ __align__(16) float2 s_cm[W];  // per column: factor of the score, reference - 11
+  __shared__ __align__(16) float s_c[W];    // per column: factor of the score
+  __shared__ __align__(16) float s_nm[W];   // and 11 - reference
   __shared__ __align__(16) float2 s_mv[W];  // a reference's move and the factor it brings
   __shared__ float s_inv[W];                // inverse sum
   __shared__ int s_mx[4][W];
@@ -473,13 +500,6 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   __syncthreads();
   tm_fence_after();
   const uint32_t tmem = s_tmem;
-  // Registers move from the first four warps to those that form the weights: 128 x 64 +
-  // 512 x 104 is what the launch gave (640 x 96).
-  if (w < 4)
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-  else
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-
   if (w == 0) {
     AtWalk walk;
     walk.start(A, P, s_b0, s_rem, from, to);
@@ -798,8 +818,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           // (An infinite component makes the scores NaN, as the saturating terms would
           // not; a column without a row keeps weight 0 under any reference.)
           const bool nan = badtree || a == INFINITY;
-          s_cm[col] = col < R ? make_float2(nan ? NAN : sc * A.scale, 0.f)
-                              : make_float2(0.f, 3.0e38f);
+          s_c[col] = col >= R ? 0.f : (nan ? NAN : sc * A.scale);
+          s_nm[col] = col >= R ? -3.0e38f : 0.f;
         }
 #pragma unroll
         for (int db = 0; db < 2; ++db) {
@@ -845,11 +865,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         tm_fence_after();
         const int sub = tok >> C.lgp;
         const float ks = s_ks[q][sub], lv = s_lv[q][sub], iv = s_iv[q][sub];
-        float x[8 * SLOTS];
         const uint32_t sa = tl + (g & 1) * W;
-#pragma unroll
-        for (int s = 0; s < SLOTS; ++s)
-          if (s < mine) tm_ld8(sa + col0(s), x + 8 * s);
         // Is there a key of the tile that some query does not see? Then also look after the
         // values that weight 0 would not hide: tokens past the end (whatever the page
         // holds) are zeroed, and a NaN is zeroed where it stands and made the weight of the
@@ -884,47 +900,72 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           at_bar(5, AT_SM_THREADS);
           vnan = s_vnan[g & 1][tok] != 0;
         }
-        tm_wait_ld<8 * SLOTS>(x);
-        tm_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sempty[g & 1]);
-        float top = -INFINITY;
+        // Columns of slots s0 .. s0 + XS - 1, as the accumulator has them, and as logarithms of
+        // their weights. All of a thread's columns stay in registers when they are few; else
+        // (W = 128) each use takes them from the accumulator again, which costs less than
+        // registers that spill.
+        constexpr int XS = SLOTS < 2 ? SLOTS : 2;
+        float x[8 * XS];
+        auto fetch = [&](int s0) {
 #pragma unroll
-        for (int s = 0; s < SLOTS; ++s) {
-          if (s >= mine) continue;
-          const int c0 = col0(s);
+          for (int s = 0; s < XS; ++s)
+            if (s0 + s < mine) tm_ld8(sa + col0(s0 + s), x + 8 * s);
+          tm_wait_ld<8 * XS>(x);
 #pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const float4 cm = *reinterpret_cast<const float4*>(&s_cm[c0 + e]);
-            x[8 * s + e] = fmaf(x[8 * s + e], ks * cm.x, lv - cm.y);
-            x[8 * s + e + 1] = fmaf(x[8 * s + e + 1], ks * cm.z, lv - cm.w);
-          }
-          if (cut) {
+          for (int s = 0; s < XS; ++s) {
+            if (s0 + s >= mine) continue;
+            const int c0 = col0(s0 + s);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int pos = s_pos[c0 + e];
-              bool see = !A.window || pos - key < A.window || key < A.sinks;
-              if (key >= len) {
-                const int o = key - len;
-                see = A.parent ? o < it.n && ((s_see[c0 + e] >> (o & 63)) & 1) != 0
-                               : see && key <= pos;
+            for (int e = 0; e < 8; e += 4) {
+              const float4 cf = *reinterpret_cast<const float4*>(&s_c[c0 + e]);
+              const float4 nm = *reinterpret_cast<const float4*>(&s_nm[c0 + e]);
+              float* y = x + 8 * s + e;
+              const float2 ks2 = make_float2(ks, ks), lv2 = make_float2(lv, lv);
+              const float2 u = fma2(make_float2(y[0], y[1]), mul2(make_float2(cf.x, cf.y), ks2),
+                                    add2(make_float2(nm.x, nm.y), lv2));
+              const float2 v = fma2(make_float2(y[2], y[3]), mul2(make_float2(cf.z, cf.w), ks2),
+                                    add2(make_float2(nm.z, nm.w), lv2));
+              y[0] = u.x;
+              y[1] = u.y;
+              y[2] = v.x;
+              y[3] = v.y;
+            }
+            if (cut) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int pos = s_pos[c0 + e];
+                bool see = !A.window || pos - key < A.window || key < A.sinks;
+                if (key >= len) {
+                  const int o = key - len;
+                  see = A.parent ? o < it.n && ((s_see[c0 + e] >> (o & 63)) & 1) != 0
+                                 : see && key <= pos;
+                }
+                x[8 * s + e] = !see ? -INFINITY : (vnan ? NAN : x[8 * s + e]);
               }
-              x[8 * s + e] = !see ? -INFINITY : (vnan ? NAN : x[8 * s + e]);
             }
           }
+        };
+        float top = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) top = fmaxf(top, x[8 * s + e]);
+        for (int s0 = 0; s0 < SLOTS; s0 += XS) {
+          if (s0 >= mine) continue;
+          fetch(s0);
+#pragma unroll
+          for (int e = 0; e < 8 * XS; ++e)
+            if (s0 + e / 8 < mine) top = fmaxf(top, x[e]);
         }
         if (mine && at_vote(1 + grp, 128, any_unseen || top > AT_LIMIT)) {
           // Move references to the tile's largest scores: maximum over the lanes, then over
           // the four warps; the outputs and sums so far shrink by the difference.
 #pragma unroll
-          for (int s = 0; s < SLOTS; ++s) {
-            if (s >= mine) continue;
+          for (int s0 = 0; s0 < SLOTS; s0 += XS) {
+            if (s0 >= mine) continue;
+            if (SLOTS > XS) fetch(s0);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int o = __reduce_max_sync(0xffffffffu, at_order(x[8 * s + e]));
-              if (lane == e) s_mx[quad][col0(s) + e] = o;
+            for (int e = 0; e < 8 * XS; ++e) {
+              if (s0 + e / 8 >= mine) continue;
+              const int o = __reduce_max_sync(0xffffffffu, at_order(x[e]));
+              if (lane == (e & 7)) s_mx[quad][col0(s0 + e / 8) + (e & 7)] = o;
             }
           }
           at_bar(1 + grp, 128);
@@ -941,7 +982,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
               fac = exp2f(-move);
             }
             s_mv[jcol] = make_float2(move, fac);
-            s_cm[jcol].y += move;
+            s_nm[jcol] -= move;
           } else if (j < 8 * SLOTS) {
             s_mv[jcol] = make_float2(0.f, 1.f);
           }
@@ -955,7 +996,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const float2 mv = s_mv[col0(s) + e];
-              x[8 * s + e] -= mv.x;
+              if (SLOTS == XS) x[8 * (s % XS) + e] -= mv.x;
               fac[e] = mv.y;
               l[8 * s + e] *= mv.y;
             }
@@ -980,33 +1021,44 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         unsigned char* prow = Ps + tok * W;
         const int swz = W == 128 ? (tok & 7) : (W == 64 ? (tok >> 1) & 3 : (tok >> 2) & 1);
 #pragma unroll
-        for (int s = 0; s < SLOTS; ++s) {
-          if (s >= mine) continue;
-          uint32_t t[AT_PTERMS][4];
+        for (int s0 = 0; s0 < SLOTS; s0 += XS) {
+          if (s0 >= mine) continue;
+          if (SLOTS > XS) fetch(s0);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int c = 8 * s + 2 * e;
-            const float p0 = ex2(x[c]), p1 = ex2(x[c + 1]);
-            l[c] = fmaf(p0, iv, l[c]);
-            l[c + 1] = fmaf(p1, iv, l[c + 1]);
-            __half2 r = __floats2half2_rn(p0, p1);
+          for (int s = 0; s < XS; ++s) {
+            if (s0 + s >= mine) continue;
+            uint32_t t[AT_PTERMS][4];
 #pragma unroll
-            for (int k = 0; k < AT_PTERMS; ++k) {
-              t[k][e] = *reinterpret_cast<const uint32_t*>(&r) + 0x00800080u;
-              const uint32_t hi = t[k][e] & 0xff00ff00u;
-              r = __hsub2(r, *reinterpret_cast<const __half2*>(&hi));
+            for (int e = 0; e < 4; ++e) {
+              const int c = 8 * s + 2 * e, k2 = 8 * (s0 + s) + 2 * e;
+              const float2 p = make_float2(ex2(x[c]), ex2(x[c + 1]));
+              const float2 sum = fma2(p, make_float2(iv, iv), make_float2(l[k2], l[k2 + 1]));
+              l[k2] = sum.x;
+              l[k2 + 1] = sum.y;
+              __half2 r = __floats2half2_rn(p.x, p.y);
+#pragma unroll
+              for (int k = 0; k < AT_PTERMS; ++k) {
+                t[k][e] = *reinterpret_cast<const uint32_t*>(&r) + 0x00800080u;
+                const uint32_t hi = t[k][e] & 0xff00ff00u;
+                r = __hsub2(r, *reinterpret_cast<const __half2*>(&hi));
+              }
             }
-          }
-          unsigned char* dst = prow + (((col0(s) >> 4) ^ swz) << 4) + (col0(s) & 8);
+            const int c0 = col0(s0 + s);
+            unsigned char* dst = prow + (((c0 >> 4) ^ swz) << 4) + (c0 & 8);
 #pragma unroll
-          for (int k = 0; k < AT_PTERMS; ++k)
-            *reinterpret_cast<uint2*>(dst + k * PBLK) =
-                make_uint2(__byte_perm(t[k][0], t[k][1], 0x7531),
-                           __byte_perm(t[k][2], t[k][3], 0x7531));
+            for (int k = 0; k < AT_PTERMS; ++k)
+              *reinterpret_cast<uint2*>(dst + k * PBLK) =
+                  make_uint2(__byte_perm(t[k][0], t[k][1], 0x7531),
+                             __byte_perm(t[k][2], t[k][3], 0x7531));
+          }
         }
+        tm_fence_before();
         fence_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&pfull);
+        if (lane == 0) {
+          mbar_arrive(&sempty[g & 1]);
+          mbar_arrive(&pfull);
+        }
         if (++q == NT) {
           q = 0;
           ++ph;
@@ -1026,7 +1078,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         at_bar(1 + grp, 128);
         if (jreal) {
           const float sum = s_l[0][jcol] + s_l[1][jcol] + s_l[2][jcol] + s_l[3][jcol];
-          const float ref = s_cm[jcol].y;
+          const float ref = -s_nm[jcol];
           s_inv[jcol] = sum == 0.f ? 0.f : 1.f / sum;
           if (!whole)
             A.S.stat[(size_t)slot_id * KV_ROWS + jcol] = make_float2(ref, sum);
