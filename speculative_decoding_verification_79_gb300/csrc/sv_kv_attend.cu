@@ -23,8 +23,9 @@
 // units in order; a query tile that crosses from one CTA to the next leaves partial
 // results (output, m, sum) in the workspace, and the last of its CTAs to arrive joins them.
 // Warps coupled by mbarriers: one copies K and V tiles page by page by tensor-map TMA
-// (128-byte swizzle) into a ring; one issues the products; sixteen form the weights, four
-// to a group, the groups taking eight query rows each in turn.
+// (128-byte swizzle) into a ring; one issues the scores' products and one the output's; one
+// plans the next query tile; sixteen form the weights, four to a group, the groups taking
+// eight query rows each in turn.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -40,7 +41,7 @@ namespace sv {
 constexpr int AT_KEYS = 128;     // tokens per key tile
 constexpr int AT_GROUPS = 4;     // groups of four warps that form the weights
 constexpr int AT_SM_WARPS = 4 * AT_GROUPS;
-constexpr int AT_THREADS = 32 * (4 + AT_SM_WARPS);  // and a copy, a product, a planning, an idle one
+constexpr int AT_THREADS = 32 * (4 + AT_SM_WARPS);  // and copies, scores, planning, outputs
 constexpr int AT_SM0 = 128;      // first of their threads
 constexpr int AT_SM_THREADS = 32 * AT_SM_WARPS;
 constexpr int AT_BLK = AT_KEYS * 128;  // 128 tokens x 128 bytes
@@ -363,6 +364,15 @@ __device__ __forceinline__ float at_unorder(int i) {
   return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
 }
 
+// After a wait gave up, products already issued must end before the accumulators are freed.
+__device__ __forceinline__ void at_drain(uint64_t* bar, bool abort) {
+  if (!abort) return;
+  umma_commit(bar);
+  const long long t0 = clock64();
+  while (!mbar_test(bar, 0))
+    if (clock64() - t0 > WAIT_CYCLES / 8) break;
+}
+
 // W: columns of an accumulator (query rows), bytes of a token's weights.
 template <int W>
 __global__ void __launch_bounds__(AT_THREADS, 1)
@@ -372,10 +382,11 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   constexpr int SLOTS = W / 8 / AT_GROUPS;  // eights of columns of a thread, at most
   constexpr uint32_t PMODE = W == 128 ? 2 : (W == 64 ? 4 : 6);
   constexpr int PBLK = AT_KEYS * W;
+  constexpr uint32_t HI128 = at_desc_hi(1024, 2), HIP = at_desc_hi(8 * W, PMODE);
   extern __shared__ unsigned char dsm_raw[];
   __shared__ uint64_t kfull[AT_MAX_STAGES], kempty[AT_MAX_STAGES];
   __shared__ uint64_t vfull[AT_MAX_STAGES], vempty[AT_MAX_STAGES];
-  __shared__ uint64_t sfull[2], sempty[2], pfull, pvdone, qfull, drain;
+  __shared__ uint64_t sfull[2], sempty[2], pfull, pvdone, qfull, drain[2];
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
   __shared__ int s_b0, s_last;
@@ -436,7 +447,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     mbar_init(&pfull, AT_SM_WARPS);
     mbar_init(&qfull, AT_SM_WARPS);
     mbar_init(&pvdone, 1);
-    mbar_init(&drain, 1);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     s_abort = 0;
     fence_mbar_init();
   }
@@ -602,78 +614,88 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       }
     }
   } else if (w == 1) {
-    // ---- Products. Scores of tile i, then the output of tile i - 1, so that a tile's
-    // weights form while the next tile's scores multiply.
+    // ---- Scores: S^T of a tile into one of two accumulators.
     if (at_elect()) {
       const int ksteps = (C.dim + 31) / 32;
-      constexpr uint32_t HI128 = at_desc_hi(1024, 2), HIP = at_desc_hi(8 * W, PMODE);
-      const uint32_t qd = at_desc_lo(smem_addr(Qs)), pd = at_desc_lo(smem_addr(Ps));
-      const uint32_t ring0 = at_desc_lo(smem_addr(ring)), rstep = static_cast<uint32_t>(slot) >> 4;
+      const uint32_t qd = at_desc_lo(smem_addr(Qs)), ring0 = at_desc_lo(smem_addr(ring));
+      const uint32_t rstep = static_cast<uint32_t>(2 * slot) >> 4;
       bool ok = true;
-      int g = 0, q = 0, ph = 0, item = 0;
-      int pq = 0, pph = 0;  // stage of the tile whose output is next
-      for (; ok; ++item) {
+      int g = 0, q = 0, ph = 0;
+      for (int item = 0; ok; ++item) {
         if (!wait(&qfull, item & 1)) break;
         const int R = s_item[item & 1].R, m = s_item[item & 1].m;
         if (m == 0) break;
-        const uint32_t N8 = static_cast<uint32_t>((R + 15) >> 4) * 2;  // N / 8
-        const uint32_t ids = AT_IDESC_S | (N8 << 17), ido = AT_IDESC_O | (N8 << 17);
-        for (int i = 0; i <= m; ++i) {
-          if (i < m) {
-            if (!wait(&kfull[q], ph & 1) || (g >= 2 && !wait(&sempty[g & 1], ((g >> 1) - 1) & 1))) {
-              ok = false;
-              break;
-            }
-            tm_fence_after();
-            const uint32_t d = tmem + (g & 1) * W, ka = ring0 + 2 * q * rstep;
-            for (int t = 0; t < P.qterms; ++t)
-              for (int db = 0; db < ndb; ++db) {
-                const uint32_t al = ka + db * (AT_BLK >> 4), bl = qd + (t * ndb + db) * (W * 8);
-                const int kn = ksteps - 4 * db;
+        const uint32_t ids = AT_IDESC_S | (static_cast<uint32_t>((R + 15) >> 4) << 18);
+        for (int i = 0; i < m; ++i, ++g) {
+          if (!wait(&kfull[q], ph & 1) || (g >= 2 && !wait(&sempty[g & 1], ((g >> 1) - 1) & 1))) {
+            ok = false;
+            break;
+          }
+          tm_fence_after();
+          const uint32_t d = tmem + (g & 1) * W, ka = ring0 + q * rstep;
+          uint32_t acc = 0;
+          for (int t = 0; t < P.qterms; ++t)
+            for (int db = 0; db < ndb; ++db) {
+              const uint32_t al = ka + db * (AT_BLK >> 4), bl = qd + (t * ndb + db) * (W * 8);
+              const int kn = ksteps - 4 * db;
+              if (kn >= 4) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                  if (k < kn) umma_f8(d, al + 2 * k, HI128, bl + 2 * k, HI128, ids, t + db + k);
+                  umma_f8(d, al + 2 * k, HI128, bl + 2 * k, HI128, ids, k ? 1u : acc);
+              } else {
+                for (int k = 0; k < kn; ++k)
+                  umma_f8(d, al + 2 * k, HI128, bl + 2 * k, HI128, ids, k ? 1u : acc);
               }
-            umma_commit(&kempty[q]);
-            umma_commit(&sfull[g & 1]);
-            ++g;
-            if (++q == NT) {
-              q = 0;
-              ++ph;
+              acc = 1;
             }
-          }
-          if (i > 0) {
-            const int pg = i < m ? g - 2 : g - 1;  // the tile before the one just issued
-            if (!wait(&vfull[pq], pph & 1) || !wait(&pfull, pg & 1)) {
-              ok = false;
-              break;
-            }
-            tm_fence_after();
-            for (int db = 0; db < ndb; ++db) {
-              const uint32_t d = tmem + (2 + db) * W;
-              const uint32_t va = ring0 + (2 * pq + 1) * rstep + db * (AT_BLK >> 4);
-#pragma unroll
-              for (int t = 0; t < AT_PTERMS; ++t)
-#pragma unroll
-                for (int k = 0; k < AT_KEYS / 32; ++k)
-                  umma_f8(d, va + k * (4096 >> 4), HI128, pd + ((t * PBLK + k * 32 * W) >> 4), HIP,
-                          ido, t + k > 0 ? 1u : (i > 1 ? 1u : 0u));
-            }
-            umma_commit(&vempty[pq]);
-            umma_commit(&pvdone);
-            if (++pq == NT) {
-              pq = 0;
-              ++pph;
-            }
+          umma_commit(&sfull[g & 1]);
+          umma_commit(&kempty[q]);
+          if (++q == NT) {
+            q = 0;
+            ++ph;
           }
         }
       }
-      if (s_abort) {  // no product may be in flight when the accumulators are freed
-        umma_commit(&drain);
-        const long long t0 = clock64();
-        while (!mbar_test(&drain, 0))
-          if (clock64() - t0 > WAIT_CYCLES / 8) break;
+      at_drain(&drain[0], s_abort);
+    }
+  } else if (w == 3) {
+    // ---- Outputs: O^T += V^T P^T of a tile, while the next tile's scores multiply and its
+    // weights form.
+    if (at_elect()) {
+      const uint32_t pd = at_desc_lo(smem_addr(Ps)), ring0 = at_desc_lo(smem_addr(ring)) + (slot >> 4);
+      const uint32_t rstep = static_cast<uint32_t>(2 * slot) >> 4;
+      bool ok = true;
+      int g = 0, q = 0, ph = 0;
+      for (int item = 0; ok; ++item) {
+        if (!wait(&qfull, item & 1)) break;
+        const int R = s_item[item & 1].R, m = s_item[item & 1].m;
+        if (m == 0) break;
+        const uint32_t ido = AT_IDESC_O | (static_cast<uint32_t>((R + 15) >> 4) << 18);
+        for (int i = 0; i < m; ++i, ++g) {
+          if (!wait(&vfull[q], ph & 1) || !wait(&pfull, g & 1)) {
+            ok = false;
+            break;
+          }
+          tm_fence_after();
+          for (int db = 0; db < ndb; ++db) {
+            const uint32_t d = tmem + (2 + db) * W, va = ring0 + q * rstep + db * (AT_BLK >> 4);
+            const uint32_t acc = i > 0;
+#pragma unroll
+            for (int t = 0; t < AT_PTERMS; ++t)
+#pragma unroll
+              for (int k = 0; k < AT_KEYS / 32; ++k)
+                umma_f8(d, va + k * (4096 >> 4), HI128, pd + ((t * PBLK + k * 32 * W) >> 4), HIP, ido,
+                        t + k ? 1u : acc);
+          }
+          umma_commit(&pvdone);
+          umma_commit(&vempty[q]);
+          if (++q == NT) {
+            q = 0;
+            ++ph;
+          }
+        }
       }
+      at_drain(&drain[1], s_abort);
     }
   } else if (w == 2) {
     // ---- Planning: item k + 1 while item k is in work.
@@ -703,8 +725,6 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       if (!live) break;
       walk.next(A, P);
     }
-  } else if (w == 3) {
-    // (idle: it fills the first four warps)
   } else {
     // ---- Weights and results.
     const int sw = w - 4, quad = w & 3, grp = sw >> 2;  // lanes 32 quad ..; eights of columns
