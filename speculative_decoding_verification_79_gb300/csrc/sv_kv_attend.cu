@@ -1,31 +1,38 @@
 // sv_kv_attend.cu -- attention of a round's new tokens over the key/value cache (sm_103a).
 //
 // For one row, key/value head and tile of R <= 128 query rows (tokens x query heads of the
-// group, flattened) the scores are a product over the cached keys, in tiles of 128 tokens:
-//     S^T = K Q^T  [128 tokens x R],   P^T = 2^(S^T - m),   O^T += V^T P^T  [dim x R].
+// group, flattened) and key tiles of 128 tokens:
+//     S = Q K^T  [R x 128],   P = 2^(S - m),   O += P V  [R x dim].
 // Both products run on the fifth-generation tensor cores with the cache's own e4m3 bytes as
-// the first operand, straight from TMA: nothing of the cache is converted. The other
+// the second operand, straight from TMA: nothing of the cache is converted. The first
 // operand is carried as a sum of 8-bit terms, multiplied one after the other into the same
 // float32 accumulator: a query row, scaled by a power of two to the e4m3 range, is exactly
 // the sum of two (bf16) or three (fp16) e4m3 terms down to 2^-18 of its largest component;
 // a weight is rounded to fp16 and split into three e5m2 terms of at least 9 bits in all
-// (e5m2 is fp16's upper byte, so a split is integer arithmetic).
-// Tokens lie on the accumulator's lanes, so that a thread owns one token: the page's
-// scales are a factor of the thread, and a small R costs little (N is R, M stays 128).
+// (e5m2 is fp16's upper byte, so a split is integer arithmetic). Weights go from registers
+// to tensor memory and are multiplied from there.
 //
-// The key scale multiplies the scores, the value scale is folded into the weights (its
-// logarithm added to the score, so that no weight exceeds the reference); the sum of the
-// softmax takes it out again. The reference m of a query row only moves when a score
-// passes it by 2^4 (the accumulators are then rescaled), or with the first keys a row sees:
-// most tiles need no exchange between threads but one vote.
+// A thread owns a query row (a lane of the accumulator) and some of the tile's tokens, so
+// that the softmax needs no exchange but one vote between the two threads of a row. Sixteen
+// tokens share a page: its key scale is a factor of their scores; its value scale is
+// folded into their weights (its logarithm added to the scores, so that no weight exceeds
+// the reference) and taken out of their sum again. The reference m of a row only moves when
+// a score passes it by 2^4 (the accumulators are then rescaled), or with the first keys the
+// row sees.
+//
+// The product has 128 rows whatever R is. Few rows are therefore repeated, 128 / W times
+// for W = 32 or 64 >= R: each copy of a row takes its own W tokens of a tile (the weights
+// of the others stay zero), so that all lanes have work and a tile's softmax costs R / 128
+// of a full one; the copies' outputs are added at the end.
 //
 // A persistent CTA per SM takes an equal share of all (row, head, query tile, key tile)
 // units in order; a query tile that crosses from one CTA to the next leaves partial
 // results (output, m, sum) in the workspace, and the last of its CTAs to arrive joins them.
-// Warps coupled by mbarriers: one copies K and V tiles page by page by tensor-map TMA
-// (128-byte swizzle) into a ring; one issues the scores' products and one the output's; one
-// plans the next query tile; sixteen form the weights, four to a group, the groups taking
-// eight query rows each in turn.
+//
+// Warps, coupled by mbarriers: one copies K tiles page by page by tensor-map TMA (128-byte
+// swizzle) into a ring, another V tiles into a second (and plans the next query tile while
+// this one is in work); one issues the scores' products and one the output's; eight form
+// the weights, four on each half of a row copy's tokens.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -39,14 +46,15 @@
 namespace sv {
 
 constexpr int AT_KEYS = 128;     // tokens per key tile
-constexpr int AT_GROUPS = 4;     // groups of four warps that form the weights
-constexpr int AT_SM_WARPS = 4 * AT_GROUPS;
-constexpr int AT_THREADS = 32 * (4 + AT_SM_WARPS);  // and copies, scores, planning, outputs
-constexpr int AT_SM0 = 128;      // first of their threads
+constexpr int AT_SM_WARPS = 8;   // warps that form the weights
+constexpr int AT_SM0 = 128;      // first of their threads, after copies, scores and outputs
 constexpr int AT_SM_THREADS = 32 * AT_SM_WARPS;
+constexpr int AT_THREADS = AT_SM0 + AT_SM_THREADS;
 constexpr int AT_BLK = AT_KEYS * 128;  // 128 tokens x 128 bytes
-constexpr int AT_MAX_STAGES = 6;
+constexpr int AT_MAX_RING = 8;   // most K tiles, and V tiles, in shared memory
+constexpr int AT_INFO = 32;      // key tiles whose page data are kept
 constexpr int AT_PTERMS = 3;
+constexpr int AT_JOIN = 33;      // floats of a row in the buffer that adds copies
 // Weights are kept as 2^(x - m + 11): up to 2^15 before the reference must move (below
 // e5m2's 57344). Their terms end at 2^-16, e5m2's smallest, so a weight has its 9 bits down
 // to 2^-19 of the reference and counts down to 2^-28. A larger shift would leave less room
@@ -54,19 +62,27 @@ constexpr int AT_PTERMS = 3;
 constexpr float AT_SHIFT = 11.f, AT_LIMIT = 15.f;
 
 // Instruction descriptors of kind::f8f6f4 (float32 accumulator, M = 128), without N.
-// Scores: A and B e4m3, K-major. Output: A e4m3 and B e5m2, both MN-major.
+// Scores: A and B e4m3, K-major. Output: A e5m2 (tensor memory), B e4m3, MN-major.
 constexpr uint32_t AT_IDESC_S = (1u << 4) | (8u << 24);
-constexpr uint32_t AT_IDESC_O = (1u << 4) | (1u << 10) | (1u << 15) | (1u << 16) | (8u << 24);
+constexpr uint32_t AT_IDESC_O = (1u << 4) | (1u << 7) | (1u << 16) | (8u << 24);
 
 // Descriptors are given as their low words (address and the unused leading offset) with the
-// constant high words of the operand's layout.
-__device__ __forceinline__ void umma_f8(uint32_t d, uint32_t alo, uint32_t ahi, uint32_t blo,
-                                        uint32_t bhi, uint32_t idesc, uint32_t accumulate) {
+// constant high word of the operands' layout. A from shared memory, or from tensor memory.
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t alo, uint32_t blo, uint32_t hi,
+                                        uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %2};\n\t"
-      "mov.b64 b, {%3, %4};\n\tsetp.ne.u32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n\t}" ::"r"(d),
-      "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %3};\n\t"
+      "mov.b64 b, {%2, %3};\n\tsetp.ne.u32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+      "r"(alo), "r"(blo), "r"(hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t blo, uint32_t hi,
+                                        uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %3};\n\tsetp.ne.u32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(blo), "r"(hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 __device__ __forceinline__ void umma_commit(uint64_t* bar) {
@@ -80,44 +96,35 @@ __device__ __forceinline__ void tm_fence_before() {
 __device__ __forceinline__ void tm_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-// Two float32 operations in one instruction.
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 
-// Eight consecutive float32 columns of this thread's lane; complete after tm_wait_ld.
-__device__ __forceinline__ void tm_ld8(uint32_t addr, float* v) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
-                 "=f"(v[6]), "=f"(v[7])
-               : "r"(addr));
+// Sixteen consecutive float32 columns of this thread's lane; complete after tm_wait_ld.
+__device__ __forceinline__ void tm_ld16(uint32_t addr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+        "=f"(v[14]), "=f"(v[15])
+      : "r"(addr));
 }
-__device__ __forceinline__ void tm_st8(uint32_t addr, const float* v) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
-                   addr),
-               "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]),
-               "f"(v[7])
+__device__ __forceinline__ void tm_st16(uint32_t addr, const float* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16};" ::"r"(addr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
+      "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]),
+      "f"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tm_st4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                       uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(a), "r"(b), "r"(c), "r"(d)
                : "memory");
 }
 // The loaded registers are operands of the wait, so that no use of them moves above it.
@@ -131,15 +138,13 @@ __device__ __forceinline__ void tm_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// Shared-memory matrix descriptor of a swizzled operand whose 8-row groups (K-major: rows;
-// MN-major: steps of K) are `group` bytes apart; rows of 128, 64 or 32 bytes (mode 2, 4, 6).
-// One swizzle atom covers the other dimension, so the leading offset is not used.
+// Shared-memory matrix descriptor of an operand in 128-byte swizzled rows whose groups of
+// eight (K-major: rows; MN-major: steps of K) follow each other. One swizzle atom covers the
+// other dimension, so the leading offset is not used.
 __device__ __forceinline__ uint32_t at_desc_lo(uint32_t addr) {
   return ((addr >> 4) & 0x3fffu) | (1u << 16);
 }
-__host__ __device__ constexpr uint32_t at_desc_hi(uint32_t group, uint32_t mode) {
-  return (group >> 4) | (1u << 14) | (mode << 29);
-}
+constexpr uint32_t AT_HI = (1024 >> 4) | (1u << 14) | (2u << 29);
 
 // One lane of a converged warp.
 __device__ __forceinline__ bool at_elect() {
@@ -157,17 +162,6 @@ __device__ __forceinline__ void at_tma(void* dst, const CUtensorMap* map, int x,
       "[%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar))
       : "memory");
-}
-__device__ __forceinline__ bool at_try(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity), "r"(2000u)
-      : "memory");
-  return ok != 0;
 }
 __device__ __forceinline__ void fence_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -193,9 +187,7 @@ __device__ __forceinline__ bool at_vote(int id, int n, bool x) {
 
 // What a launch needs beside AttendArgs.
 struct AttendPlan {
-  int rt;      // most query rows of a tile
-  int width;   // columns of an accumulator: 32, 64 or 128
-  int stages;  // K + V tiles in the ring
+  int nk, nv;  // tiles of the rings
   int ndb;     // 128-byte blocks of a token's vector
   int qterms;  // e4m3 terms of a query
   int bf16;
@@ -209,7 +201,7 @@ struct AtRow {
   bool bad;
 };
 
-__device__ __forceinline__ AtRow at_row(const AttendArgs& A, const AttendPlan& P, int b) {
+__device__ __forceinline__ AtRow at_row(const AttendArgs& A, int b) {
   AtRow r;
   r.len = __ldg(A.C.len + b);
   r.n = A.n_new ? __ldg(A.n_new + b) : A.T;
@@ -217,7 +209,7 @@ __device__ __forceinline__ AtRow at_row(const AttendArgs& A, const AttendPlan& P
           (long long)r.len + r.n > (long long)A.C.max_pages << A.C.lgp;
   if (r.bad) r.n = 0;
   r.rows = r.n * A.group;
-  r.nrt = (r.rows + P.rt - 1) / P.rt;
+  r.nrt = (r.rows + KV_ROWS - 1) / KV_ROWS;
   r.rr = r.nrt ? (r.rows + r.nrt - 1) / r.nrt : 0;
   return r;
 }
@@ -278,13 +270,12 @@ struct AtWalk {
     return i1 > i0;
   }
   // From row b0, unit `rem` of it.
-  __device__ void start(const AttendArgs& A, const AttendPlan& P, int b0, long long rem,
-                        long long from, long long to) {
+  __device__ __noinline__ void start(const AttendArgs& A, int b0, long long rem, long long from, long long to) {
     b = b0;
     at = from;
     end = to;
     if (at >= end) return;
-    row = at_row(A, P, b);
+    row = at_row(A, b);
     const long long per = at_head_units(A, row);
     h = static_cast<int>(rem / per);
     rem -= h * per;
@@ -295,10 +286,10 @@ struct AtWalk {
       tile = at_tile(A, row, ++rt);
     }
     base = from - rem;
-    if (!settle()) next(A, P);
+    if (!settle()) next(A);
   }
   __device__ __forceinline__ bool live() const { return at < end; }
-  __device__ void next(const AttendArgs& A, const AttendPlan& P) {
+  __device__ __noinline__ void next(const AttendArgs& A) {
     do {
       base += AT_EXTRA + tile.tiles();
       at = base;
@@ -308,7 +299,7 @@ struct AtWalk {
         if (++h == A.C.heads) {
           h = 0;
           do {  // (a row with queries exists: units are left)
-            row = at_row(A, P, ++b);
+            row = at_row(A, ++b);
           } while (row.rows == 0);
         }
       }
@@ -325,28 +316,10 @@ struct AtItem {
   int tiles;        // of the query tile
   int end, pos_hi;  // as AtTile
   int ns, lo;
+  int bad;          // the row's tree is wrong
   long long u0;     // unit of its first key tile
   __device__ __forceinline__ int key_tile(int i) const { return i < ns ? i : lo + i - ns; }
 };
-
-// Sums of C values over the 32 lanes (C a power of two up to 32): lane c (mod C) gets
-// column c's, by halving the columns a lane is responsible for at each exchange.
-template <int C>
-__device__ __forceinline__ float at_lane_sums(float* v, int lane) {
-#pragma unroll
-  for (int s = C / 2; s >= 1; s >>= 1) {
-    const bool up = (lane & s) != 0;
-#pragma unroll
-    for (int i = 0; i < s; ++i) {
-      const float keep = up ? v[i + s] : v[i], give = up ? v[i] : v[i + s];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, s);
-    }
-  }
-  float x = v[0];
-#pragma unroll
-  for (int s = C; s < 32; s <<= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
-  return x;
-}
 
 __device__ __forceinline__ void at_store(void* out, long long at, float y, int bf16) {
   if (bf16)
@@ -355,13 +328,52 @@ __device__ __forceinline__ void at_store(void* out, long long at, float y, int b
     static_cast<__half*>(out)[at] = __float2half_rn(y);
 }
 
-// A float as an integer of the same order, and back.
-__device__ __forceinline__ int at_order(float x) {
-  const int i = __float_as_int(x);
-  return i ^ ((i >> 31) & 0x7fffffff);
+// Sixteen consecutive values, rounded to the output's type, or as they are.
+__device__ __forceinline__ void at_store16(void* out, long long at, const float* y, int bf16) {
+  uint32_t o[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if (bf16) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * e], y[2 * e + 1]);
+      o[e] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      const __half2 h = __floats2half2_rn(y[2 * e], y[2 * e + 1]);
+      o[e] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at);
+  p[0] = make_uint4(o[0], o[1], o[2], o[3]);
+  p[1] = make_uint4(o[4], o[5], o[6], o[7]);
 }
-__device__ __forceinline__ float at_unorder(int i) {
-  return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
+__device__ __forceinline__ void at_store16(float* out, const float* y) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    reinterpret_cast<float4*>(out)[e] =
+        make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+}
+
+// Has it been WAIT_CYCLES since the first call with *t0 == 0?
+__device__ __forceinline__ bool at_expired(long long* t0) {
+  const long long t = clock64();
+  if (*t0 == 0) *t0 = t;
+  return t - *t0 > WAIT_CYCLES;
+}
+
+// The rest of a wait whose first probe (which suspends the thread for some microseconds at
+// most) was in vain. Bounded: false (and a report) when it runs out or another one has. Not
+// expanded at every wait: the kernel's loops share the instruction cache.
+__device__ __noinline__ bool at_wait_on(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                        WsHeader* hdr) {
+  long long t0 = 0;
+  while (!mbar_try(bar, parity)) {
+    if (*abort) return false;
+    if (at_expired(&t0)) {
+      *abort = 1;
+      kv_report(hdr, ST_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
 }
 
 // After a wait gave up, products already issued must end before the accumulators are freed.
@@ -373,90 +385,208 @@ __device__ __forceinline__ void at_drain(uint64_t* bar, bool abort) {
     if (clock64() - t0 > WAIT_CYCLES / 8) break;
 }
 
-// W: columns of an accumulator (query rows), bytes of a token's weights.
+// Query row `row` of an item, by half a warp (lane l16): e4m3 terms into shared memory in the
+// layout of a K-major operand, in each of the row's copies (W rows apart); returns the power
+// of two that the terms were divided by, or NaN when a component is infinite (which the
+// saturating terms would not show).
+template <int W>
+__device__ float at_query(const AttendArgs& A, const AttendPlan& P, const uint16_t* src, int row,
+                          int l16, unsigned char* Q) {
+  float f[2][8];
+  float a = 0.f;
+#pragma unroll
+  for (int db = 0; db < 2; ++db) {
+    const int d = db * 128 + l16 * 8;
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (d < A.C.dim) x = __ldg(reinterpret_cast<const uint4*>(src + d));
+    const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (P.bf16) {
+        f[db][2 * e] = bf_lo(xw[e]);
+        f[db][2 * e + 1] = bf_hi(xw[e]);
+      } else {
+        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&xw[e]));
+        f[db][2 * e] = y.x;
+        f[db][2 * e + 1] = y.y;
+      }
+      a = fmaxf(a, fmaxf(fabsf(f[db][2 * e]), fabsf(f[db][2 * e + 1])));
+    }
+  }
+  const uint32_t half = 0xffffu << (threadIdx.x & 16);  // (the other half may have no row)
+#pragma unroll
+  for (int s = 8; s; s >>= 1) a = fmaxf(a, __shfl_xor_sync(half, a, s));
+  const float sc = kv_scale(a), inv = 1.f / sc;
+#pragma unroll
+  for (int db = 0; db < 2; ++db) {
+    if (db >= P.ndb) break;
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = f[db][e] * inv;
+    unsigned char* dst =
+        Q + (size_t)db * AT_BLK + row * 128 + (((l16 >> 1) ^ (row & 7)) << 4) + (l16 & 1) * 8;
+    for (int t = 0; t < P.qterms; ++t) {
+      uint2 o;
+      o.x = e4m3x4(y[0], y[1], y[2], y[3]);
+      o.y = e4m3x4(y[4], y[5], y[6], y[7]);
+#pragma unroll
+      for (int c = 0; c < 128 / W; ++c)
+        *reinterpret_cast<uint2*>(dst + (size_t)t * P.ndb * AT_BLK + c * W * 128) = o;
+      const uint32_t ow[2] = {o.x, o.y};
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float2 lo = e4m3_to_f2(ow[e] & 0xffffu), hi = e4m3_to_f2(ow[e] >> 16);
+        y[4 * e] -= lo.x;
+        y[4 * e + 1] -= lo.y;
+        y[4 * e + 2] -= hi.x;
+        y[4 * e + 3] -= hi.y;
+      }
+    }
+  }
+  return a == INFINITY ? NAN : sc;
+}
+
+// Waits for the copies of the last tiles 0 .. g - 1 of a ring of n.
+__device__ __noinline__ void at_land(uint64_t* full, int n, int g) {
+  const long long t0 = clock64();
+  for (int j = max(0, g - n); j < g; ++j)
+    while (!mbar_test(&full[j % n], (j / n) & 1) && clock64() - t0 < WAIT_CYCLES / 4) {
+    }
+}
+
+// The queries of an item and their scores' factors, two to a warp of those that form the
+// weights. (Rows past the item's keep what they held: each row's results are its own.) Not
+// expanded in place: once per query tile, and the kernel's loops have to fit the
+// instruction cache together.
+template <int W>
+__device__ __noinline__ void at_queries(const AttendArgs& A, const AttendPlan& P, const AtItem* it,
+                                        unsigned char* Q, float* cs) {
+  const int sw = (threadIdx.x - AT_SM0) >> 5, lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int row = sw * 2 + (lane >> 4); row < it->R; row += 2 * AT_SM_WARPS) {
+    const int t = (it->r0 + row) / A.group, gh = it->r0 + row - t * A.group;
+    const uint16_t* src = static_cast<const uint16_t*>(A.q) + it->b * A.q_row + t * A.q_tok +
+                          (size_t)(it->h * A.group + gh) * A.C.dim;
+    const float sc = at_query<W>(A, P, src, row, lane & 15, Q);
+    if ((lane & 15) == 0) cs[row] = it->bad ? NAN : sc * A.scale;
+  }
+  __syncwarp();
+  fence_async();
+}
+
+// Joins the partial results of a query tile's CTAs first .. last (outputs, sums and
+// references) into its output. All threads of the weights; `out` has the rows' places.
+__device__ __noinline__ void at_join(const AttendArgs& A, int bf16, int R, int first, int last,
+                                     const long long* out) {
+  const int vec = A.C.dim / 4;
+  for (int e = threadIdx.x - AT_SM0; e < R * vec; e += AT_SM_THREADS) {
+    const int r = e / vec, dv = e - r * vec;
+    auto slot_of = [&](int k) { return (size_t)(2 * k + (k == first ? 1 : 0)) * KV_ROWS + r; };
+    float top = -INFINITY;
+    for (int k = first; k <= last; ++k) {
+      const float2 s2 = __ldcg(A.S.stat + slot_of(k));
+      if (s2.y != 0.f) top = fmaxf(top, s2.x);
+    }
+    float sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = first; k <= last; ++k) {
+      const float2 s2 = __ldcg(A.S.stat + slot_of(k));
+      if (s2.y == 0.f) continue;
+      const float f = exp2f(s2.x - top);
+      const float4 y = __ldcg(reinterpret_cast<const float4*>(A.S.part + slot_of(k) * A.C.dim) + dv);
+      sum = fmaf(s2.y, f, sum);
+      o.x = fmaf(y.x, f, o.x);
+      o.y = fmaf(y.y, f, o.y);
+      o.z = fmaf(y.z, f, o.z);
+      o.w = fmaf(y.w, f, o.w);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const long long at = out[r] * A.C.dim + dv * 4;
+    at_store(A.out, at, o.x * inv, bf16);
+    at_store(A.out, at + 1, o.y * inv, bf16);
+    at_store(A.out, at + 2, o.z * inv, bf16);
+    at_store(A.out, at + 3, o.w * inv, bf16);
+    if (dv == 0 && A.lse)
+      A.lse[out[r]] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+  }
+}
+
+// W: rows of a copy (32, 64 or 128 >= the query rows of a tile).
 template <int W>
 __global__ void __launch_bounds__(AT_THREADS, 1)
-    kv_attend_kernel(const AttendArgs A, const AttendPlan P,
+    kv_attend_kernel(const __grid_constant__ AttendArgs A, const __grid_constant__ AttendPlan P,
                      const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV) {
-  constexpr int SLOTS = W / 8 / AT_GROUPS;  // eights of columns of a thread, at most
-  constexpr uint32_t PMODE = W == 128 ? 2 : (W == 64 ? 4 : 6);
-  constexpr int PBLK = AT_KEYS * W;
-  constexpr uint32_t HI128 = at_desc_hi(1024, 2), HIP = at_desc_hi(8 * W, PMODE);
+  constexpr int COPIES = 128 / W;
+  constexpr int NC = W / 2;  // tokens of a thread
+  // Tensor memory: the output's accumulator, then three of scores (two above dim 128). A
+  // tile's weights (32 columns a term) replace its scores.
+  const int nsb = P.ndb == 1 ? 3 : 2;
+  const uint32_t scol = 128 * P.ndb;
   extern __shared__ unsigned char dsm_raw[];
-  __shared__ uint64_t kfull[AT_MAX_STAGES], kempty[AT_MAX_STAGES];
-  __shared__ uint64_t vfull[AT_MAX_STAGES], vempty[AT_MAX_STAGES];
-  __shared__ uint64_t sfull[2], sempty[2], pfull, pvdone, qfull, drain[2];
+  __shared__ uint64_t kfull[AT_MAX_RING], kempty[AT_MAX_RING];
+  __shared__ uint64_t vfull[AT_MAX_RING], vempty[AT_MAX_RING], tinfo[AT_INFO];
+  __shared__ uint64_t sfull[3], pfull[3], pvdone[3], qfull, dfull[2], dempty[2], drain[2];
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
   __shared__ int s_b0, s_last;
-  __shared__ int s_vnan[2][AT_KEYS];
-  __shared__ AtItem s_item[2];  // of item k at k & 1
-  __shared__ long long s_rem, s_sum[AT_THREADS / 32];
-  // Per stage and page of the tile: key scale, log2 and inverse of the value scale.
-  __shared__ float s_ks[AT_MAX_STAGES][8], s_lv[AT_MAX_STAGES][8], s_iv[AT_MAX_STAGES][8];
-  __shared__ __align__(16) float s_c[W];    // per column: factor of the score
-  __shared__ __align__(16) float s_nm[W];   // and 11 - reference
-  __shared__ __align__(16) float2 s_mv[W];  // a reference's move and the factor it brings
-  __shared__ float s_inv[W];                // inverse sum
-  __shared__ int s_mx[4][W];
-  __shared__ float s_l[4][W];
-  __shared__ int s_pos[W];                  // position of the column's query
-  __shared__ unsigned long long s_see[W];   // block nodes it sees (trees)
-  __shared__ long long s_out[W];            // its row of the output, -1: none
+  __shared__ long long s_rem, s_total, s_sum[AT_THREADS / 32];
+  // Per key tile and page of it: row of the pool (-1: none); key scale, log2 and inverse of
+  // the value scale.
+  __shared__ int s_y[AT_INFO][8];
+  __shared__ float4 s_sc[AT_INFO][8];
+  // Item k's description and rows, at k & 1: factor of the score, position of the query,
+  // block nodes it sees (trees), its row of the output.
+  __shared__ AtItem s_item[2];
+  __shared__ float s_c[2][W];
+  __shared__ int s_pos[2][W];
+  __shared__ unsigned long long s_see[2][W];
+  __shared__ long long s_out[2][W];
   __shared__ int s_par[SV_MAX_TREE];
+  __shared__ float s_top[2][128], s_l[2][128];  // per half and row: largest scores, sums
+  __shared__ float2 s_stat[128];     // reference and sum of a row copy
+  __shared__ int s_vnan[AT_KEYS];
 
   unsigned char* dsm = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const KvCache& C = A.C;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int ndb = P.ndb, NT = P.stages;
-  unsigned char* Qs = dsm;                                       // [terms][ndb][W][128]
-  unsigned char* Ps = Qs + (size_t)P.qterms * ndb * W * 128;     // [terms][128 tokens][W]
-  unsigned char* ring = Ps + AT_PTERMS * PBLK;                   // [stages][K, V][ndb][128][128]
-  const int slot = ndb * AT_BLK;
-  auto kbuf = [&](int q) { return ring + (size_t)q * 2 * slot; };
-  auto vbuf = [&](int q) { return ring + (size_t)q * 2 * slot + slot; };
+  const int ndb = P.ndb, slot = ndb * AT_BLK;
+  unsigned char* Qs = dsm;                                  // [terms][ndb][128][128]
+  unsigned char* Ks = Qs + P.qterms * slot;                 // [nk][ndb][128][128]
+  unsigned char* Vs = Ks + (size_t)P.nk * slot;             // [nv][ndb][128][128]
+  float* joinb = reinterpret_cast<float*>(Vs + (size_t)P.nv * slot);  // [128][AT_JOIN], copies only
 
-  // Bounded wait: false (and a report) when it runs out or another one has.
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    if (mbar_test(bar, parity)) return true;
-    const long long t0 = clock64();
-    while (!at_try(bar, parity)) {
-      if (s_abort) return false;
-      if (clock64() - t0 > WAIT_CYCLES) {
-        s_abort = 1;
-        kv_report(A.S.hdr, ST_TIMEOUT);
-        return false;
-      }
-    }
-    return true;
+    return mbar_try(bar, parity) || at_wait_on(bar, parity, &s_abort, A.S.hdr);
   };
 
   if (tid == 0) {
-    for (int q = 0; q < NT; ++q) {
+    for (int q = 0; q < AT_MAX_RING; ++q) {
       mbar_init(&kfull[q], 1);
       mbar_init(&kempty[q], 1);
       mbar_init(&vfull[q], 1);
       mbar_init(&vempty[q], 1);
     }
-    for (int q = 0; q < 2; ++q) {
-      mbar_init(&sfull[q], 1);
-      mbar_init(&sempty[q], AT_SM_WARPS);
+    for (int q = 0; q < AT_INFO; ++q) mbar_init(&tinfo[q], 1);
+    for (int q = 0; q < 3; ++q) {
+      mbar_init(&sfull[q], 2);
+      mbar_init(&pfull[q], AT_SM_WARPS);
+      mbar_init(&pvdone[q], 1);
     }
-    mbar_init(&pfull, AT_SM_WARPS);
+    for (int q = 0; q < 2; ++q) {
+      mbar_init(&dfull[q], 1);
+      mbar_init(&dempty[q], AT_SM_WARPS);
+      mbar_init(&drain[q], 1);
+    }
     mbar_init(&qfull, AT_SM_WARPS);
-    mbar_init(&pvdone, 1);
-    mbar_init(&drain[0], 1);
-    mbar_init(&drain[1], 1);
     s_abort = 0;
     fence_mbar_init();
   }
   if (w == 1) {
-    const uint32_t need = (2 + ndb) * W, cols = need <= 128 ? 128 : (need <= 256 ? 256 : 512);
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr(&s_tmem)),
-                 "r"(cols)
+                 "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -464,7 +594,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   // threads in turn; the second pass finds the row where the share begins.
   long long total = 0, mine0 = 0;
   for (int b = tid; b < C.batch; b += AT_THREADS) {
-    const AtRow r = at_row(A, P, b);
+    const AtRow r = at_row(A, b);
     const long long c = at_head_units(A, r) * C.heads;
     if (b == tid) mine0 = c;
     total += c;
@@ -493,12 +623,13 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   const long long cta = blockIdx.x;
   const long long from = cta < ctas ? cta * total / ctas : 0;
   const long long to = cta < ctas ? (cta + 1) * total / ctas : 0;
+  if (tid == 0) s_total = total;
   if (from < to) {
     long long base = 0;
     for (int b0 = 0; b0 < C.batch; b0 += AT_THREADS) {
       const int b = b0 + tid;
       const long long c =
-          b >= C.batch ? 0 : (b0 == 0 ? mine0 : at_head_units(A, at_row(A, P, b)) * C.heads);
+          b >= C.batch ? 0 : (b0 == 0 ? mine0 : at_head_units(A, at_row(A, b)) * C.heads);
       const long long sum = block_sum(c, &before);
       if (from >= base + before && from < base + before + c) {
         s_b0 = b;
@@ -512,145 +643,132 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   __syncthreads();
   tm_fence_after();
   const uint32_t tmem = s_tmem;
+
   if (w == 0) {
+    // ---- K copies. Pages are looked up for several tiles at a time, a page per lane and a
+    // chunk ahead of their use; their data go to the other warps through a ring of entries,
+    // one per tile, written before the tile's barrier is armed. (An entry is used again 32
+    // tiles later, and K is never more than its ring and three steps ahead of the rest.)
     AtWalk walk;
-    walk.start(A, P, s_b0, s_rem, from, to);
-    // ---- Copies: pages of one or more tiles are looked up at a time, a page per lane and
-    // a step ahead of their use.
-    const int ppt = AT_KEYS >> C.lgp;  // pages per tile
-    const int tpc = 32 / ppt;          // tiles per step
+    walk.start(A, s_b0, s_rem, from, to);
+    const int ppt = AT_KEYS >> C.lgp;             // pages per tile
+    const int tpc = min(32 / ppt, AT_INFO / 4);   // tiles per chunk
+    const int mt = lane / ppt, sub = lane - mt * ppt;
     const size_t layer0 = (size_t)A.layer * C.pages;
-    int b = 0, h = 0, n = 0, page = -1;  // the step in hand: row, head, tiles; its page
+    int n = 0, h = 0, page = -1;  // the chunk ahead: tiles, head, this lane's page
     bool used = false;
-    float ks = 1.f, vs = 1.f;
-    int nb = 0, nh = 0, nn = 0, npage = -1;  // the step ahead
-    bool nused = false;
     int i = walk.live() ? walk.i0 : 0;
-    auto look = [&]() {  // the next step's pages
-      nn = 0;
+    auto look = [&]() {
+      n = 0;
       if (!walk.live()) return;
-      nb = walk.b;
-      nh = walk.h;
-      nn = min(tpc, walk.i1 - i);
-      const int mt = lane / ppt;
-      const int key = (mt < nn ? walk.tile.key_tile(i + mt) : 0) * AT_KEYS +
-                      ((lane - mt * ppt) << C.lgp);
-      nused = mt < nn && key < walk.tile.end;
-      npage = nused ? kv_page(C, nb, key) : -1;
-      i += nn;
+      h = walk.h;
+      n = min(tpc, walk.i1 - i);
+      const int key = (mt < n ? walk.tile.key_tile(i + mt) : 0) * AT_KEYS + (sub << C.lgp);
+      used = mt < n && key < walk.tile.end;
+      page = used ? kv_page(C, walk.b, key) : -1;
+      i += n;
       if (i == walk.i1) {
-        walk.next(A, P);
+        walk.next(A);
         i = walk.live() ? walk.i0 : 0;
       }
     };
-    auto scales = [&](int pg, bool use, int head, float* k, float* v) {
-      *k = *v = 1.f;
-      if (!use) return;
-      if (pg >= 0) {
-        *k = __ldg(C.ks + (layer0 + pg) * C.heads + head);
-        *v = __ldg(C.vs + (layer0 + pg) * C.heads + head);
-      }
-      // A page out of range, or scales outside theirs: the scores become NaN.
-      constexpr float LO = 5.421010862427522e-20f, HI = 18446744073709551616.f;  // 2^-64, 2^64
-      if (pg < 0 || !(*k >= LO && *k <= HI && *v >= LO && *v <= HI)) {
-        *k = NAN;
-        *v = 1.f;
-        kv_report(A.S.hdr, ST_DEVICE_INPUT);
-      }
-    };
-    look();
+    int g = 0, q = 0, ph = 0;
     bool ok = true;
-    int g = 0, q = 0, ph = 0;  // tile, its stage, the stage's pass
-    float nks, nvs;
-    scales(npage, nused, nh, &nks, &nvs);
-    while (ok && nn) {
-      b = nb; h = nh; n = nn; page = npage; used = nused; ks = nks; vs = nvs;
-      look();
-      for (int t = 0; t < n; ++t, ++g) {
-        const bool mine = lane >= t * ppt && lane < (t + 1) * ppt;
-        const int sub = lane - t * ppt;
-        const uint32_t count = __popc(__ballot_sync(0xffffffffu, mine && page >= 0));
-        const uint32_t bytes = (count << C.lgp) * 128u * ndb;
-        for (int kv = 0; kv < 2; ++kv) {
-          uint64_t* full = kv ? &vfull[q] : &kfull[q];
-          uint64_t* empty = kv ? &vempty[q] : &kempty[q];
-          bool go = true;
-          if (ph > 0) go = wait(empty, (ph - 1) & 1);
-          if (!__all_sync(0xffffffffu, go)) {
-            ok = false;
-            break;
-          }
-          if (kv == 1 && mine) {
-            s_ks[q][sub] = ks;
-            s_lv[q][sub] = log2f(vs);
-            s_iv[q][sub] = 1.f / vs;
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive_expect_tx(full, bytes);
-          __syncwarp();
-          if (mine && page >= 0) {
-            unsigned char* dst = (kv ? vbuf(q) : kbuf(q)) + ((size_t)sub << C.lgp) * 128;
-            const int y = (page * C.heads + h) << C.lgp;
-            for (int db = 0; db < ndb; ++db)
-              at_tma(dst + db * AT_BLK, kv ? &tmV : &tmK, db * 128, y, full);
-          }
+    look();
+    while (ok && n) {
+      const int count = n;
+      const int y = page >= 0 ? (page * C.heads + h) << C.lgp : -1;
+      float ks = 1.f, vs = 1.f;
+      if (used) {
+        if (page >= 0) {
+          ks = __ldg(C.ks + (layer0 + page) * C.heads + h);
+          vs = __ldg(C.vs + (layer0 + page) * C.heads + h);
         }
-        if (!ok) break;
-        if (t == 0) scales(npage, nused, nh, &nks, &nvs);
-        if (++q == NT) {
+        // A page out of range, or scales outside theirs: the scores become NaN.
+        constexpr float LO = 5.421010862427522e-20f, HI = 18446744073709551616.f;  // 2^-64, 2^64
+        if (page < 0 || !(ks >= LO && ks <= HI && vs >= LO && vs <= HI)) {
+          ks = NAN;
+          vs = 1.f;
+          kv_report(A.S.hdr, ST_DEVICE_INPUT);
+        }
+      }
+      if (mt < count) {
+        const int e = (g + mt) & (AT_INFO - 1);
+        s_y[e][sub] = y;
+        s_sc[e][sub] = make_float4(ks, log2f(vs), 1.f / vs, 0.f);
+      }
+      __syncwarp();
+      look();
+      const uint32_t held = __ballot_sync(0xffffffffu, y >= 0);
+      for (int t = 0; t < count; ++t, ++g) {
+        if (ph > 0 && !__all_sync(0xffffffffu, wait(&kempty[q], (ph - 1) & 1))) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          const uint32_t pages = __popc((held >> (t * ppt)) & ((1u << ppt) - 1u));
+          mbar_arrive_expect_tx(&kfull[q], (pages << C.lgp) * 128u * ndb);
+          mbar_arrive(&tinfo[g & (AT_INFO - 1)]);
+        }
+        __syncwarp();
+        if (mt == t && y >= 0) {
+          unsigned char* dst = Ks + (size_t)q * slot + ((size_t)sub << C.lgp) * 128;
+          for (int db = 0; db < ndb; ++db) at_tma(dst + db * AT_BLK, &tmK, db * 128, y, &kfull[q]);
+        }
+        if (++q == P.nk) {
           q = 0;
           ++ph;
         }
       }
     }
-    if (!ok) {
-      // After a wait gave up: let the copies already issued land before the CTA exits. (A
-      // stage's barrier whose last pass was consumed answers at once.)
-      for (int j = max(0, g - NT); j <= g; ++j) {
-        const long long t0 = clock64();
-        const uint32_t par = static_cast<uint32_t>((j / NT) & 1);
-        while (!(mbar_test(&kfull[j % NT], par) && (j == g || mbar_test(&vfull[j % NT], par))))
-          if (clock64() - t0 > WAIT_CYCLES / 8) break;
-      }
-    }
+    // After a wait gave up, let the copies already issued land before the CTA exits. (A
+    // stage's barrier whose last pass was consumed answers at once.)
+    if (s_abort) at_land(kfull, P.nk, g);
   } else if (w == 1) {
-    // ---- Scores: S^T of a tile into one of two accumulators.
+    // ---- Scores of a tile.
     if (at_elect()) {
       const int ksteps = (C.dim + 31) / 32;
-      const uint32_t qd = at_desc_lo(smem_addr(Qs)), ring0 = at_desc_lo(smem_addr(ring));
-      const uint32_t rstep = static_cast<uint32_t>(2 * slot) >> 4;
+      const uint32_t qd = at_desc_lo(smem_addr(Qs)), ring0 = at_desc_lo(smem_addr(Ks));
+      const uint32_t rstep = static_cast<uint32_t>(slot) >> 4;
+      constexpr uint32_t ids = AT_IDESC_S | ((AT_KEYS / 8) << 17);
       bool ok = true;
-      int g = 0, q = 0, ph = 0;
+      int q = 0, ph = 0, sb = 0, sph = 0;
       for (int item = 0; ok; ++item) {
         if (!wait(&qfull, item & 1)) break;
-        const int R = s_item[item & 1].R, m = s_item[item & 1].m;
+        const int m = s_item[item & 1].m;
         if (m == 0) break;
-        const uint32_t ids = AT_IDESC_S | (static_cast<uint32_t>((R + 15) >> 4) << 18);
-        for (int i = 0; i < m; ++i, ++g) {
-          if (!wait(&kfull[q], ph & 1) || (g >= 2 && !wait(&sempty[g & 1], ((g >> 1) - 1) & 1))) {
+        for (int i = 0; i < m; ++i) {
+          // An accumulator is free once the weights that replaced its scores are multiplied.
+          if ((sph > 0 && !wait(&pvdone[sb], (sph - 1) & 1)) || !wait(&kfull[q], ph & 1)) {
             ok = false;
             break;
           }
           tm_fence_after();
-          const uint32_t d = tmem + (g & 1) * W, ka = ring0 + q * rstep;
+          const uint32_t d = tmem + scol + sb * 128, kd = ring0 + q * rstep;
           uint32_t acc = 0;
           for (int t = 0; t < P.qterms; ++t)
             for (int db = 0; db < ndb; ++db) {
-              const uint32_t al = ka + db * (AT_BLK >> 4), bl = qd + (t * ndb + db) * (W * 8);
+              const uint32_t al = qd + (t * ndb + db) * (AT_BLK >> 4), bl = kd + db * (AT_BLK >> 4);
               const int kn = ksteps - 4 * db;
               if (kn >= 4) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                  umma_f8(d, al + 2 * k, HI128, bl + 2 * k, HI128, ids, k ? 1u : acc);
+                  umma_ss(d, al + 2 * k, bl + 2 * k, AT_HI, ids, k ? 1u : acc);
               } else {
                 for (int k = 0; k < kn; ++k)
-                  umma_f8(d, al + 2 * k, HI128, bl + 2 * k, HI128, ids, k ? 1u : acc);
+                  umma_ss(d, al + 2 * k, bl + 2 * k, AT_HI, ids, k ? 1u : acc);
               }
               acc = 1;
             }
-          umma_commit(&sfull[g & 1]);
+          // (Two arrivals: the products' end, and what this thread has seen of the tile's data.)
+          umma_commit(&sfull[sb]);
+          mbar_arrive(&sfull[sb]);
           umma_commit(&kempty[q]);
-          if (++q == NT) {
+          if (++sb == nsb) {
+            sb = 0;
+            ++sph;
+          }
+          if (++q == P.nk) {
             q = 0;
             ++ph;
           }
@@ -658,136 +776,86 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       }
       at_drain(&drain[0], s_abort);
     }
-  } else if (w == 3) {
-    // ---- Outputs: O^T += V^T P^T of a tile, while the next tile's scores multiply and its
-    // weights form.
-    if (at_elect()) {
-      const uint32_t pd = at_desc_lo(smem_addr(Ps)), ring0 = at_desc_lo(smem_addr(ring)) + (slot >> 4);
-      const uint32_t rstep = static_cast<uint32_t>(2 * slot) >> 4;
-      bool ok = true;
-      int g = 0, q = 0, ph = 0;
-      for (int item = 0; ok; ++item) {
-        if (!wait(&qfull, item & 1)) break;
-        const int R = s_item[item & 1].R, m = s_item[item & 1].m;
-        if (m == 0) break;
-        const uint32_t ido = AT_IDESC_O | (static_cast<uint32_t>((R + 15) >> 4) << 18);
-        for (int i = 0; i < m; ++i, ++g) {
-          if (!wait(&vfull[q], ph & 1) || !wait(&pfull, g & 1)) {
-            ok = false;
-            break;
-          }
-          tm_fence_after();
-          for (int db = 0; db < ndb; ++db) {
-            const uint32_t d = tmem + (2 + db) * W, va = ring0 + q * rstep + db * (AT_BLK >> 4);
-            const uint32_t acc = i > 0;
-#pragma unroll
-            for (int t = 0; t < AT_PTERMS; ++t)
-#pragma unroll
-              for (int k = 0; k < AT_KEYS / 32; ++k)
-                umma_f8(d, va + k * (4096 >> 4), HI128, pd + ((t * PBLK + k * 32 * W) >> 4), HIP, ido,
-                        t + k ? 1u : acc);
-          }
-          umma_commit(&pvdone);
-          umma_commit(&vempty[q]);
-          if (++q == NT) {
-            q = 0;
-            ++ph;
-          }
-        }
-      }
-      at_drain(&drain[1], s_abort);
-    }
   } else if (w == 2) {
-    // ---- Planning: item k + 1 while item k is in work.
+    // ---- V copies, and in their pauses planning: the next item's description and columns.
     AtWalk walk;
-    walk.start(A, P, s_b0, s_rem, from, to);
-    for (int k = 0;; ++k) {
-      const bool live = walk.live();
-      if (lane == 0) {
-        AtItem& o = s_item[k & 1];
-        o.m = live ? walk.i1 - walk.i0 : 0;
-        o.b = walk.b;
-        o.h = walk.h;
-        o.len = walk.row.len;
-        o.n = walk.row.n;
-        o.r0 = walk.tile.r0;
-        o.R = walk.tile.r1 - walk.tile.r0;
-        o.i0 = walk.i0;
-        o.tiles = walk.tile.tiles();
-        o.end = walk.tile.end;
-        o.pos_hi = walk.tile.pos_hi;
-        o.ns = walk.tile.ns;
-        o.lo = walk.tile.lo;
-        o.u0 = walk.base + AT_EXTRA;
-      }
-      __syncwarp();
-      at_bar(6, AT_SM_THREADS + 32);  // item k is there, item k - 1 done with
-      if (!live) break;
-      walk.next(A, P);
-    }
-  } else {
-    // ---- Weights and results.
-    const int sw = w - 4, quad = w & 3, grp = sw >> 2;  // lanes 32 quad ..; eights of columns
-    const int st = tid - AT_SM0;
-    const int tok = quad * 32 + lane;  // token of a tile; component of the output
-    const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    // Queries without a token and rows with wrong data: zeros or NaN.
-    for (long long u0 = (long long)blockIdx.x * AT_SM_WARPS + sw; u0 * 32 < (long long)C.batch * A.T;
-         u0 += (long long)gridDim.x * AT_SM_WARPS) {
-      const long long u = u0 * 32 + lane;
-      int fill = 0;
-      if (u < (long long)C.batch * A.T) {
-        const int b = static_cast<int>(u / A.T), t = static_cast<int>(u - (long long)b * A.T);
-        const AtRow r = at_row(A, P, b);
-        fill = r.bad ? 2 : (t >= r.n ? 1 : 0);
-        if (r.bad && t == 0) kv_report(A.S.hdr, ST_DEVICE_INPUT);
-      }
-      unsigned todo = __ballot_sync(0xffffffffu, fill != 0);
-      while (todo) {
-        const int j = __ffs(todo) - 1;
-        todo &= todo - 1;
-        const bool nan = __shfl_sync(0xffffffffu, fill, j) == 2;
-        const long long row = (u0 * 32 + j) * A.q_heads;
-        const uint32_t x = nan ? 0x7fff7fffu : 0u;  // NaN in bf16 and fp16
-        uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.out) + row * C.dim);
-        for (int e = lane; e < A.q_heads * C.dim / 8; e += 32) o[e] = make_uint4(x, x, x, x);
-        if (A.lse)
-          for (int e = lane; e < A.q_heads; e += 32) A.lse[row + e] = nan ? NAN : -INFINITY;
-      }
-    }
-    bool dead = false;  // a wait gave up: skip the work, keep meeting the other warps
+    walk.start(A, s_b0, s_rem, from, to);
+    const int ppt = AT_KEYS >> C.lgp;
+    int k = 0, planned = 0;       // items planned, and their tiles
+    bool more = true;
     int g = 0, q = 0, ph = 0;
-    for (int item = 0;; ++item) {
-      // Every warp is done with the last query tile.
-      at_bar(6, AT_SM_THREADS + 32);
-      const AtItem& it = s_item[item & 1];
-      const int R = it.R, m = it.m, len = it.len, N = (R + 15) & ~15;
-      if (m == 0) {
-        if (lane == 0) mbar_arrive(&qfull);  // the product warp sees it too
-        break;
-      }
-      // Columns of this thread: eights grp, grp + 4, ...; `mine` of them have a row.
-      const int mine = max(0, (((R + 7) >> 3) - grp + AT_GROUPS - 1) / AT_GROUPS);
-      auto col0 = [&](int slot) { return (grp + AT_GROUPS * slot) * 8; };
-      // -- The queries, and what the columns stand for.
-      bool badtree = false;
-      if (A.parent) {
-        if (st < it.n) {
-          const int p = __ldg(A.parent + (size_t)it.b * A.T + st);
-          badtree = st > 0 && (p < 0 || p >= st);
-          s_par[st] = p;
+    long long idle = 0;
+    auto ready = [&](uint64_t* bar, int parity) {
+      return __any_sync(0xffffffffu, mbar_test(bar, parity & 1)) != 0;
+    };
+    while (more || g < planned) {
+      if (g < planned && ready(&tinfo[g & (AT_INFO - 1)], g / AT_INFO) &&
+          (ph == 0 || ready(&vempty[q], ph - 1))) {
+        const int y = lane < ppt ? s_y[g & (AT_INFO - 1)][lane] : -1;
+        const uint32_t pages = __popc(__ballot_sync(0xffffffffu, y >= 0));
+        if (lane == 0) mbar_arrive_expect_tx(&vfull[q], (pages << C.lgp) * 128u * ndb);
+        __syncwarp();
+        if (y >= 0) {
+          unsigned char* dst = Vs + (size_t)q * slot + ((size_t)lane << C.lgp) * 128;
+          for (int db = 0; db < ndb; ++db) at_tma(dst + db * AT_BLK, &tmV, db * 128, y, &vfull[q]);
         }
-        badtree = at_vote(5, AT_SM_THREADS, badtree);
-        if (badtree && st == 0) kv_report(A.S.hdr, ST_DEVICE_INPUT);
+        ++g;
+        if (++q == P.nv) {
+          q = 0;
+          ++ph;
+        }
+        idle = 0;
+        continue;
       }
-      if (st < N) {
-        int pos = -1;
-        unsigned long long see = badtree ? ~0ull : 0ull;  // (a bad tree's scores are NaN)
-        long long out = -1;
-        if (st < R) {
-          const int t = (it.r0 + st) / A.group, gh = it.r0 + st - t * A.group;
-          pos = len + t;
-          out = ((long long)it.b * A.T + t) * A.q_heads + it.h * A.group + gh;
+      const int kb = k & 1;
+      // (Item k's place is free once item k - 2 is done with.)
+      if (!more || (k >= 2 && !ready(&dempty[kb], (k >> 1) - 1))) {
+        if (__any_sync(0xffffffffu, s_abort || at_expired(&idle))) {
+          if (!s_abort) kv_report(A.S.hdr, ST_TIMEOUT);
+          s_abort = 1;
+          break;
+        }
+        __nanosleep(20);
+        continue;
+      }
+      more = walk.live();
+      const bool live = more;
+      AtItem& it = s_item[kb];
+      if (lane == 0) it.m = live ? walk.i1 - walk.i0 : 0;
+      if (live) {
+        const int R = walk.tile.r1 - walk.tile.r0;
+        const int len = walk.row.len, nnew = walk.row.n;
+        if (lane == 0) {
+          it.b = walk.b;
+          it.h = walk.h;
+          it.len = len;
+          it.n = nnew;
+          it.r0 = walk.tile.r0;
+          it.R = R;
+          it.i0 = walk.i0;
+          it.tiles = walk.tile.tiles();
+          it.end = walk.tile.end;
+          it.pos_hi = walk.tile.pos_hi;
+          it.ns = walk.tile.ns;
+          it.lo = walk.tile.lo;
+          it.u0 = walk.base + AT_EXTRA;
+        }
+        bool badtree = false;
+        if (A.parent) {
+          __syncwarp();
+          for (int t = lane; t < nnew; t += 32) {
+            const int p = __ldg(A.parent + (size_t)walk.b * A.T + t);
+            badtree = badtree || (t > 0 && (p < 0 || p >= t));
+            s_par[t] = p;
+          }
+          badtree = __any_sync(0xffffffffu, badtree);
+          __syncwarp();
+          if (badtree && lane == 0) kv_report(A.S.hdr, ST_DEVICE_INPUT);
+        }
+        for (int r = lane; r < R; r += 32) {
+          unsigned long long see = badtree ? ~0ull : 0ull;  // (a bad tree's scores are NaN)
+          const int t = (walk.tile.r0 + r) / A.group, gh = walk.tile.r0 + r - t * A.group;
+          int pos = len + t;
           if (A.parent && !badtree) {
             int up = 0;
             for (int i = t;; i = s_par[i]) {
@@ -797,95 +865,132 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             }
             pos = len + up;
           }
+          s_pos[kb][r] = pos;
+          s_see[kb][r] = see;
+          s_out[kb][r] = ((long long)walk.b * A.T + t) * A.q_heads + walk.h * A.group + gh;
         }
-        s_pos[st] = pos;
-        s_see[st] = see;
-        s_out[st] = out;
+        if (lane == 0) it.bad = badtree;
       }
-      for (int col = sw * 2 + (lane >> 4); col < N; col += 2 * AT_SM_WARPS) {
-        const int l16 = lane & 15;
-        float f[2][8];
-        float a = 0.f;
-        const uint16_t* src = nullptr;
-        if (col < R) {
-          const int t = (it.r0 + col) / A.group, gh = it.r0 + col - t * A.group;
-          src = static_cast<const uint16_t*>(A.q) + it.b * A.q_row + t * A.q_tok +
-                (size_t)(it.h * A.group + gh) * C.dim;
-        }
-#pragma unroll
-        for (int db = 0; db < 2; ++db) {
-          const int d = db * 128 + l16 * 8;
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (src && d < C.dim) x = __ldg(reinterpret_cast<const uint4*>(src + d));
-          const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (P.bf16) {
-              f[db][2 * e] = bf_lo(xw[e]);
-              f[db][2 * e + 1] = bf_hi(xw[e]);
-            } else {
-              const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&xw[e]));
-              f[db][2 * e] = y.x;
-              f[db][2 * e + 1] = y.y;
-            }
-            a = fmaxf(a, fmaxf(fabsf(f[db][2 * e]), fabsf(f[db][2 * e + 1])));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&dfull[kb]);
+      if (live) planned += walk.i1 - walk.i0;
+      if (live) walk.next(A);
+      ++k;
+      idle = 0;
+    }
+    if (s_abort) at_land(vfull, P.nv, g);
+  } else if (w == 3) {
+    // ---- Outputs: O += P V of a tile, while the next tile's scores multiply and its weights
+    // form.
+    if (at_elect()) {
+      const uint32_t ring0 = at_desc_lo(smem_addr(Vs)), rstep = static_cast<uint32_t>(slot) >> 4;
+      bool ok = true;
+      int q = 0, ph = 0, sb = 0, sph = 0;
+      for (int item = 0; ok; ++item) {
+        if (!wait(&qfull, item & 1)) break;
+        const int m = s_item[item & 1].m;
+        if (m == 0) break;
+        for (int i = 0; i < m; ++i) {
+          if (!wait(&vfull[q], ph & 1) || !wait(&pfull[sb], sph & 1)) {
+            ok = false;
+            break;
           }
-        }
+          tm_fence_after();
+          const uint32_t pa = tmem + scol + sb * 128;
+          for (int db = 0; db < ndb; ++db) {
+            const uint32_t d = tmem + db * 128, vd = ring0 + q * rstep + db * (AT_BLK >> 4);
+            const uint32_t ido = AT_IDESC_O | (static_cast<uint32_t>(min(128, C.dim - db * 128)) >> 3 << 17);
+            const uint32_t acc = i > 0;
 #pragma unroll
-        for (int s = 8; s; s >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, s));
-        const float sc = kv_scale(a), inv = 1.f / sc;
-        if (l16 == 0) {
-          // (An infinite component makes the scores NaN, as the saturating terms would
-          // not; a column without a row keeps weight 0 under any reference.)
-          const bool nan = badtree || a == INFINITY;
-          s_c[col] = col >= R ? 0.f : (nan ? NAN : sc * A.scale);
-          s_nm[col] = col >= R ? -3.0e38f : 0.f;
-        }
+            for (int t = 0; t < AT_PTERMS; ++t)
 #pragma unroll
-        for (int db = 0; db < 2; ++db) {
-          if (db >= ndb) break;
-          float y[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = f[db][e] * inv;
-          unsigned char* dst = Qs + (size_t)db * W * 128 + col * 128 +
-                               (((l16 >> 1) ^ (col & 7)) << 4) + (l16 & 1) * 8;
-          for (int t = 0; t < P.qterms; ++t) {
-            uint2 o;
-            o.x = e4m3x4(y[0], y[1], y[2], y[3]);
-            o.y = e4m3x4(y[4], y[5], y[6], y[7]);
-            *reinterpret_cast<uint2*>(dst + (size_t)t * ndb * W * 128) = o;
-            const uint32_t ow[2] = {o.x, o.y};
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float2 lo = e4m3_to_f2(ow[e] & 0xffffu), hi = e4m3_to_f2(ow[e] >> 16);
-              y[4 * e] -= lo.x;
-              y[4 * e + 1] -= lo.y;
-              y[4 * e + 2] -= hi.x;
-              y[4 * e + 3] -= hi.y;
-            }
+              for (int k = 0; k < AT_KEYS / 32; ++k)
+                umma_ts(d, pa + t * 32 + k * 8, vd + k * (4096 >> 4), AT_HI, ido, t + k ? 1u : acc);
+          }
+          umma_commit(&pvdone[sb]);
+          umma_commit(&vempty[q]);
+          if (++sb == nsb) {
+            sb = 0;
+            ++sph;
+          }
+          if (++q == P.nv) {
+            q = 0;
+            ++ph;
           }
         }
       }
-      fence_async();
-      at_bar(5, AT_SM_THREADS);
+      at_drain(&drain[1], s_abort);
+    }
+  } else {
+    // ---- Weights and results.
+    const int st = tid - AT_SM0, quad = w & 3, half = (w - 4) >> 2;
+    const int row = quad * 32 + lane;             // lane of the accumulators
+    const int copy = row / W, r = row % W;        // copy of query row r
+    const int c0 = copy * W + half * NC;          // first of this thread's tokens
+    const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    // Queries without a token and rows with wrong data: zeros or NaN.
+    for (long long u0 = (long long)blockIdx.x * AT_SM_WARPS + (w - 4);
+         u0 * 32 < (long long)C.batch * A.T; u0 += (long long)gridDim.x * AT_SM_WARPS) {
+      const long long u = u0 * 32 + lane;
+      int fill = 0;
+      if (u < (long long)C.batch * A.T) {
+        const int b = static_cast<int>(u / A.T), t = static_cast<int>(u - (long long)b * A.T);
+        const AtRow rw = at_row(A, b);
+        fill = rw.bad ? 2 : (t >= rw.n ? 1 : 0);
+        if (rw.bad && t == 0) kv_report(A.S.hdr, ST_DEVICE_INPUT);
+      }
+      unsigned todo = __ballot_sync(0xffffffffu, fill != 0);
+      while (todo) {
+        const int j = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const bool nan = __shfl_sync(0xffffffffu, fill, j) == 2;
+        const long long at = (u0 * 32 + j) * A.q_heads;
+        const uint32_t x = nan ? 0x7fff7fffu : 0u;  // NaN in bf16 and fp16
+        uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.out) + at * C.dim);
+        for (int e = lane; e < A.q_heads * C.dim / 8; e += 32) o[e] = make_uint4(x, x, x, x);
+        if (A.lse)
+          for (int e = lane; e < A.q_heads; e += 32) A.lse[at + e] = nan ? NAN : -INFINITY;
+      }
+    }
+    bool dead = false;  // a wait gave up: skip the work, keep meeting the other warps
+    // The queries of item k into shared memory; then the scores may begin.
+    auto queries = [&](int k) {
+      if (!dead && !wait(&dfull[k & 1], (k >> 1) & 1)) dead = true;
+      if (!dead && s_item[k & 1].m > 0) at_queries<W>(A, P, &s_item[k & 1], Qs, s_c[k & 1]);
+      __syncwarp();
       if (lane == 0) mbar_arrive(&qfull);
-      float l[8 * SLOTS];
-#pragma unroll
-      for (int c = 0; c < 8 * SLOTS; ++c) l[c] = 0.f;
-      // Thread j of a group keeps the state of its column j: has its query seen a key?
-      const int j = st & 127, jcol = col0(j >> 3) + (j & 7);
-      const bool jreal = j < 8 * SLOTS && jcol < R;
-      bool unseen = jreal, any_unseen = mine > 0;
+    };
+    // Is the output of the tile before done?
+    int sb = 0, sph = 0;  // accumulator of the tile's scores, and its pass
+    auto done = [&]() {
+      const int b = sb ? sb - 1 : nsb - 1;
+      return wait(&pvdone[b], (sb ? sph : sph - 1) & 1);
+    };
+    queries(0);
+    int g = 0, q = 0, ph = 0;
+    for (int item = 0;; ++item) {
+      const int kb = item & 1;
+      if (!dead && !wait(&qfull, item & 1)) dead = true;
+      // (The waits of a CTA give up together: see s_abort. Warps that saw the item must not
+      // meet others that did not, so all of them agree first.)
+      if (at_vote(5, AT_SM_THREADS, dead)) break;
+      const AtItem& it = s_item[kb];
+      const int m = it.m, len = it.len;
+      if (m == 0) break;
+      const bool live = quad * 32 % W < it.R;  // does the warp have a query row?
+      const bool real = r < it.R;
+      const float cs = real ? s_c[kb][r] : 0.f;
+      const int pos = real ? s_pos[kb][r] : -1;
+      const unsigned long long see = real ? s_see[kb][r] : 0;
+      float l = 0.f, nm = 0.f;  // sum of the weights; 11 - reference
+      bool unseen = real;       // has the row copy seen no key yet?
 
       // -- Key tiles.
+#pragma unroll 1
       for (int i = 0; i < m; ++i, ++g) {
-        const int key0 = it.key_tile(it.i0 + i) * AT_KEYS, key = key0 + tok;
-        // (The page scales are written before V's barrier is armed.)
-        if (!dead && !(wait(&vfull[q], ph & 1) && wait(&sfull[g & 1], (g >> 1) & 1))) dead = true;
+        const int key0 = it.key_tile(it.i0 + i) * AT_KEYS;
+        if (!dead && !wait(&sfull[sb], sph & 1)) dead = true;
         tm_fence_after();
-        const int sub = tok >> C.lgp;
-        const float ks = s_ks[q][sub], lv = s_lv[q][sub], iv = s_iv[q][sub];
-        const uint32_t sa = tl + (g & 1) * W;
         // Is there a key of the tile that some query does not see? Then also look after the
         // values that weight 0 would not hide: tokens past the end (whatever the page
         // holds) are zeroed, and a NaN is zeroed where it stands and made the weight of the
@@ -893,248 +998,241 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         const bool cut = key0 + AT_KEYS > len ||
                          (A.window && key0 < it.pos_hi - A.window + 1 && key0 + AT_KEYS > A.sinks);
         bool vnan = false;
-        if (cut) {
-          // A group looks at two of a token's eight 16-byte chunks, turned so that the lanes
-          // of a warp spread over the banks.
-          if (grp == 0) s_vnan[g & 1][tok] = 0;
-          at_bar(5, AT_SM_THREADS);
+        if (__builtin_expect(cut, 0)) {
+          // (Once the last tile's output is done, V's barriers cannot be a pass behind.)
+          if (!dead && ((i > 0 && !done()) || !wait(&vfull[q], ph & 1)))
+            dead = true;
+          const int tok = st & 127;
+          bool nan = false;
           for (int db = 0; db < ndb && !dead; ++db) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              uint4* p = reinterpret_cast<uint4*>(vbuf(q) + db * AT_BLK + tok * 128) +
-                         ((2 * grp + e + tok) & 7);
-              if (key >= it.end) {
+            // Half of a token's eight 16-byte chunks, turned so that the lanes of a warp
+            // spread over the banks.
+#pragma unroll 1
+            for (int e = 0; e < 4; ++e) {
+              uint4* p = reinterpret_cast<uint4*>(Vs + (size_t)q * slot + db * AT_BLK + tok * 128) +
+                         ((4 * half + e + tok) & 7);
+              if (key0 + tok >= it.end) {
                 *p = make_uint4(0, 0, 0, 0);
                 continue;
               }
-              uint4 y = *p;
+              const uint4 y = *p;
               const uint4 z = make_uint4(
                   __vcmpeq4(y.x & 0x7f7f7f7fu, 0x7f7f7f7fu), __vcmpeq4(y.y & 0x7f7f7f7fu, 0x7f7f7f7fu),
                   __vcmpeq4(y.z & 0x7f7f7f7fu, 0x7f7f7f7fu), __vcmpeq4(y.w & 0x7f7f7f7fu, 0x7f7f7f7fu));
               if (z.x | z.y | z.z | z.w) {
-                s_vnan[g & 1][tok] = 1;
+                nan = true;
                 *p = make_uint4(y.x & ~z.x, y.y & ~z.y, y.z & ~z.z, y.w & ~z.w);
               }
             }
           }
-          at_bar(5, AT_SM_THREADS);
-          vnan = s_vnan[g & 1][tok] != 0;
+          fence_async();
+          vnan = at_vote(5, AT_SM_THREADS, nan);
+          if (vnan) {
+            if (half == 0) s_vnan[tok] = nan;
+            at_bar(5, AT_SM_THREADS);
+            if (half == 1 && nan) s_vnan[tok] = 1;
+            at_bar(5, AT_SM_THREADS);
+          }
         }
-        // Columns of slots s0 .. s0 + XS - 1, as the accumulator has them, and as logarithms of
-        // their weights. All of a thread's columns stay in registers when they are few; else
-        // (W = 128) each use takes them from the accumulator again, which costs less than
-        // registers that spill.
-        constexpr int XS = SLOTS < 2 ? SLOTS : 2;
-        float x[8 * XS];
-        auto fetch = [&](int s0) {
+        const uint32_t sa = tl + scol + sb * 128;
+        if (live) {
+          // This thread's scores as logarithms of their weights, sixteen tokens at a time.
+          float x[NC];
 #pragma unroll
-          for (int s = 0; s < XS; ++s)
-            if (s0 + s < mine) tm_ld8(sa + col0(s0 + s), x + 8 * s);
-          tm_wait_ld<8 * XS>(x);
+          for (int c = 0; c < NC; c += 16) tm_ld16(sa + c0 + c, x + c);
+          tm_wait_ld<NC>(x);
+          const float4* sc = s_sc[g & (AT_INFO - 1)];
+          float top = -INFINITY;
 #pragma unroll
-          for (int s = 0; s < XS; ++s) {
-            if (s0 + s >= mine) continue;
-            const int c0 = col0(s0 + s);
+          for (int c = 0; c < NC; c += 16) {
+            const float4 f = sc[(c0 + c) >> C.lgp];
+            const float2 a = make_float2(f.x * cs, f.x * cs), b = make_float2(f.y + nm, f.y + nm);
 #pragma unroll
-            for (int e = 0; e < 8; e += 4) {
-              const float4 cf = *reinterpret_cast<const float4*>(&s_c[c0 + e]);
-              const float4 nm = *reinterpret_cast<const float4*>(&s_nm[c0 + e]);
-              float* y = x + 8 * s + e;
-              const float2 ks2 = make_float2(ks, ks), lv2 = make_float2(lv, lv);
-              const float2 u = fma2(make_float2(y[0], y[1]), mul2(make_float2(cf.x, cf.y), ks2),
-                                    add2(make_float2(nm.x, nm.y), lv2));
-              const float2 v = fma2(make_float2(y[2], y[3]), mul2(make_float2(cf.z, cf.w), ks2),
-                                    add2(make_float2(nm.z, nm.w), lv2));
-              y[0] = u.x;
-              y[1] = u.y;
-              y[2] = v.x;
-              y[3] = v.y;
+            for (int e = c; e < c + 16; e += 2) {
+              const float2 y = __ffma2_rn(make_float2(x[e], x[e + 1]), a, b);
+              x[e] = y.x;
+              x[e + 1] = y.y;
             }
-            if (cut) {
+          }
+          if (__builtin_expect(cut, 0)) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const int pos = s_pos[c0 + e];
-                bool see = !A.window || pos - key < A.window || key < A.sinks;
-                if (key >= len) {
-                  const int o = key - len;
-                  see = A.parent ? o < it.n && ((s_see[c0 + e] >> (o & 63)) & 1) != 0
-                                 : see && key <= pos;
-                }
-                x[8 * s + e] = !see ? -INFINITY : (vnan ? NAN : x[8 * s + e]);
+            for (int c = 0; c < NC; ++c) {
+              const int key = key0 + c0 + c, o = key - len;
+              bool sees = !A.window || pos - key < A.window || key < A.sinks;
+              if (A.parent) {
+                if (o >= 0) sees = o < it.n && ((see >> (o & 63)) & 1) != 0;
+              } else {
+                sees = sees && key <= pos;
               }
+              if (vnan && s_vnan[c0 + c]) x[c] = NAN;
+              x[c] = sees ? x[c] : -INFINITY;
             }
           }
-        };
-        float top = -INFINITY;
 #pragma unroll
-        for (int s0 = 0; s0 < SLOTS; s0 += XS) {
-          if (s0 >= mine) continue;
-          fetch(s0);
-#pragma unroll
-          for (int e = 0; e < 8 * XS; ++e)
-            if (s0 + e / 8 < mine) top = fmaxf(top, x[e]);
-        }
-        if (mine && at_vote(1 + grp, 128, any_unseen || top > AT_LIMIT)) {
-          // Move references to the tile's largest scores: maximum over the lanes, then over
-          // the four warps; the outputs and sums so far shrink by the difference.
-#pragma unroll
-          for (int s0 = 0; s0 < SLOTS; s0 += XS) {
-            if (s0 >= mine) continue;
-            if (SLOTS > XS) fetch(s0);
-#pragma unroll
-            for (int e = 0; e < 8 * XS; ++e) {
-              if (s0 + e / 8 >= mine) continue;
-              const int o = __reduce_max_sync(0xffffffffu, at_order(x[e]));
-              if (lane == (e & 7)) s_mx[quad][col0(s0 + e / 8) + (e & 7)] = o;
-            }
-          }
-          at_bar(1 + grp, 128);
-          if (jreal) {
-            int o = max(s_mx[0][jcol], s_mx[1][jcol]);
-            o = max(o, max(s_mx[2][jcol], s_mx[3][jcol]));
-            const float d = at_unorder(o);  // over the reference - 11
+          for (int c = 0; c < NC; c += 2) top = max3(top, x[c], x[c + 1]);
+          if (at_vote(1 + quad, 64, unseen || (real && top > AT_LIMIT))) {
+            // Move references to the tile's largest scores; the outputs and sums so far shrink
+            // by the difference.
+            s_top[half][row] = top;
+            at_bar(1 + quad, 64);
+            const float d = fmaxf(s_top[0][row], s_top[1][row]);  // over the reference - 11
             float move = 0.f, fac = 1.f;
             if (unseen) {  // nothing to shrink: the reference goes wherever the scores are
-              if (d > -INFINITY) move = d - AT_SHIFT;
-              unseen = d == -INFINITY;
-            } else if (d > AT_SHIFT) {
+              if (d > -INFINITY) {
+                move = d - AT_SHIFT;
+                unseen = false;
+              }
+            } else if (real && d > AT_SHIFT) {
               move = d - AT_SHIFT;
               fac = exp2f(-move);
             }
-            s_mv[jcol] = make_float2(move, fac);
-            s_nm[jcol] -= move;
-          } else if (j < 8 * SLOTS) {
-            s_mv[jcol] = make_float2(0.f, 1.f);
-          }
-          any_unseen = at_vote(1 + grp, 128, unseen);
-          if (i > 0 && !dead && !wait(&pvdone, (g - 1) & 1)) dead = true;
-          tm_fence_after();
+            nm -= move;
+            l *= fac;
 #pragma unroll
-          for (int s = 0; s < SLOTS; ++s) {
-            if (s >= mine) continue;
-            float fac[8];
+            for (int c = 0; c < NC; ++c) x[c] -= move;
+            if (i > 0) {
+              if (!dead && !done()) dead = true;
+              tm_fence_after();
+#pragma unroll 1
+              for (int c = half * 16; c < C.dim; c += 32) {
+                float o[16];
+                tm_ld16(tl + c, o);
+                tm_wait_ld<16>(o);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float2 mv = s_mv[col0(s) + e];
-              if (SLOTS == XS) x[8 * (s % XS) + e] -= mv.x;
-              fac[e] = mv.y;
-              l[8 * s + e] *= mv.y;
-            }
-            if (i == 0) continue;
-            for (int db = 0; db < ndb; ++db) {
-              const uint32_t oa = tl + (2 + db) * W + col0(s);
-              float o[8];
-              tm_ld8(oa, o);
-              tm_wait_ld<8>(o);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) o[e] *= fac[e];
-              tm_st8(oa, o);
-            }
-          }
-          tm_wait_st();
-          tm_fence_before();
-        }
-        // Weights: 2^x, summed with the value scale taken out, rounded to fp16 and split.
-        // A term is the upper byte of the remainder rounded to it (halves away from zero);
-        // what is left of an fp16 number after that is exact.
-        if (i > 0 && !dead && !wait(&pvdone, (g - 1) & 1)) dead = true;
-        unsigned char* prow = Ps + tok * W;
-        const int swz = W == 128 ? (tok & 7) : (W == 64 ? (tok >> 1) & 3 : (tok >> 2) & 1);
-#pragma unroll
-        for (int s0 = 0; s0 < SLOTS; s0 += XS) {
-          if (s0 >= mine) continue;
-          if (SLOTS > XS) fetch(s0);
-#pragma unroll
-          for (int s = 0; s < XS; ++s) {
-            if (s0 + s >= mine) continue;
-            uint32_t t[AT_PTERMS][4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int c = 8 * s + 2 * e, k2 = 8 * (s0 + s) + 2 * e;
-              const float2 p = make_float2(ex2(x[c]), ex2(x[c + 1]));
-              const float2 sum = fma2(p, make_float2(iv, iv), make_float2(l[k2], l[k2 + 1]));
-              l[k2] = sum.x;
-              l[k2 + 1] = sum.y;
-              __half2 r = __floats2half2_rn(p.x, p.y);
-#pragma unroll
-              for (int k = 0; k < AT_PTERMS; ++k) {
-                t[k][e] = *reinterpret_cast<const uint32_t*>(&r) + 0x00800080u;
-                const uint32_t hi = t[k][e] & 0xff00ff00u;
-                r = __hsub2(r, *reinterpret_cast<const __half2*>(&hi));
+                for (int e = 0; e < 16; ++e) o[e] *= fac;
+                tm_st16(tl + c, o);
               }
             }
-            const int c0 = col0(s0 + s);
-            unsigned char* dst = prow + (((c0 >> 4) ^ swz) << 4) + (c0 & 8);
+          }
+          // Weights: 2^x, summed with the value scale taken out, rounded to fp16 and split. A
+          // term is the upper byte of the remainder rounded to it (halves away from zero);
+          // what is left of an fp16 number after that is exact.
+#pragma unroll
+          for (int c = 0; c < NC; c += 16) {
+            uint32_t t[AT_PTERMS][8];
+            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float2 p = make_float2(ex2(x[c + 2 * e]), ex2(x[c + 2 * e + 1]));
+              sum = __fadd2_rn(sum, p);
+              __half2 y = __floats2half2_rn(p.x, p.y);
+#pragma unroll
+              for (int k = 0; k < AT_PTERMS; ++k) {
+                t[k][e] = *reinterpret_cast<const uint32_t*>(&y) + 0x00800080u;
+                const uint32_t hi = t[k][e] & 0xff00ff00u;
+                y = __hsub2(y, *reinterpret_cast<const __half2*>(&hi));
+              }
+            }
+            l = fmaf(sum.x + sum.y, sc[(c0 + c) >> C.lgp].z, l);
 #pragma unroll
             for (int k = 0; k < AT_PTERMS; ++k)
-              *reinterpret_cast<uint2*>(dst + k * PBLK) =
-                  make_uint2(__byte_perm(t[k][0], t[k][1], 0x7531),
-                             __byte_perm(t[k][2], t[k][3], 0x7531));
+              tm_st4(sa + k * 32 + (c0 + c) / 4, __byte_perm(t[k][0], t[k][1], 0x7531),
+                     __byte_perm(t[k][2], t[k][3], 0x7531), __byte_perm(t[k][4], t[k][5], 0x7531),
+                     __byte_perm(t[k][6], t[k][7], 0x7531));
           }
+          // Tokens that belong to the row's other copies.
+#pragma unroll
+          for (int c = 0; c < AT_KEYS / 16; c += 2) {
+            if ((c + half) * 16 / W == copy) continue;
+#pragma unroll
+            for (int k = 0; k < AT_PTERMS; ++k) tm_st4(sa + k * 32 + (c + half) * 4, 0, 0, 0, 0);
+          }
+          tm_wait_st();
         }
         tm_fence_before();
-        fence_async();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sempty[g & 1]);
-          mbar_arrive(&pfull);
-        }
-        if (++q == NT) {
+        if (lane == 0) mbar_arrive(&pfull[sb]);
+        if (++q == P.nv) {
           q = 0;
           ++ph;
+        }
+        if (++sb == nsb) {
+          sb = 0;
+          ++sph;
         }
       }
 
       // -- The query tile's sums and outputs: the result when this CTA saw all its keys,
-      // else partial results.
-      if (!dead && !wait(&pvdone, (g - 1) & 1)) dead = true;
+      // else partial results. The last scores are done, so the next queries go in first.
+      s_l[half][row] = l;
+      if (half == 0) s_stat[row].x = -nm;
+      queries(item + 1);
+      at_bar(5, AT_SM_THREADS);
+      if (st < 128) s_stat[st].y = st % W < it.R ? s_l[0][st] + s_l[1][st] : 0.f;
+      if (!dead && !done()) dead = true;
       tm_fence_after();
+      at_bar(5, AT_SM_THREADS);
       const bool whole = m == it.tiles;
-      const int slot_id = 2 * static_cast<int>(cta) + (it.i0 == 0 ? 1 : 0);
-      if (mine) {
-        constexpr int LC = 8 * SLOTS;
-        const float lsum = at_lane_sums<LC>(l, lane);
-        if (lane < LC) s_l[quad][col0(lane >> 3) + (lane & 7)] = lsum;
-        at_bar(1 + grp, 128);
-        if (jreal) {
-          const float sum = s_l[0][jcol] + s_l[1][jcol] + s_l[2][jcol] + s_l[3][jcol];
-          const float ref = -s_nm[jcol];
-          s_inv[jcol] = sum == 0.f ? 0.f : 1.f / sum;
-          if (!whole)
-            A.S.stat[(size_t)slot_id * KV_ROWS + jcol] = make_float2(ref, sum);
-          else if (A.lse)
-            A.lse[s_out[jcol]] =
-                sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
-        }
-        at_bar(1 + grp, 128);
-        for (int db = 0; db < ndb; ++db) {
-          const int d = db * 128 + tok;
+      const int slot_id = 2 * blockIdx.x + (it.i0 == 0 ? 1 : 0);
+      // Reference and sum over the row's copies, and this copy's factor.
+      float ref = -INFINITY, sum = 0.f;
 #pragma unroll
-          for (int s = 0; s < SLOTS; ++s) {
-            if (s >= mine) continue;
-            const int c0 = col0(s);
-            float o[8];
-            tm_ld8(tl + (2 + db) * W + c0, o);
-            tm_wait_ld<8>(o);
-            if (d >= C.dim) continue;
+      for (int c = 0; c < COPIES; ++c)
+        if (s_stat[c * W + r].y != 0.f) ref = fmaxf(ref, s_stat[c * W + r].x);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              if (c0 + e >= R) continue;
-              if (whole) {
-                const float inv = s_inv[c0 + e];
-                at_store(A.out, s_out[c0 + e] * C.dim + d, inv == 0.f ? 0.f : o[e] * inv, P.bf16);
-              } else {
-                A.S.part[((size_t)slot_id * KV_ROWS + c0 + e) * C.dim + d] = o[e];
-              }
-            }
+      for (int c = 0; c < COPIES; ++c) {
+        const float2 s2 = s_stat[c * W + r];
+        if (s2.y != 0.f) sum = fmaf(s2.y, exp2f(s2.x - ref), sum);
+      }
+      const float2 own = s_stat[row];
+      float f = own.y == 0.f ? 0.f : exp2f(own.x - ref);
+      if (whole) f = sum == 0.f ? 0.f : f / sum;
+      if (copy == 0 && half == 0 && real) {
+        if (!whole)
+          A.S.stat[(size_t)slot_id * KV_ROWS + r] = make_float2(ref, sum);
+        else if (A.lse)
+          A.lse[s_out[kb][r]] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+      }
+      if (COPIES == 1) {
+        if (live) {
+#pragma unroll 1
+          for (int c = half * 16; c < C.dim; c += 32) {
+            float o[16];
+            tm_ld16(tl + c, o);
+            tm_wait_ld<16>(o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = f == 0.f ? 0.f : o[e] * f;
+            if (!real) continue;
+            if (whole)
+              at_store16(A.out, s_out[kb][r] * C.dim + c, o, P.bf16);
+            else
+              at_store16(A.S.part + ((size_t)slot_id * KV_ROWS + r) * C.dim + c, o);
           }
+        }
+      } else {
+        // Copies are added through shared memory, 32 components at a time.
+#pragma unroll 1
+        for (int c = 0; c < C.dim; c += 32) {
+          const int n = min(32, C.dim - c);
+          if (live && half * 16 < n) {
+            float o[16];
+            tm_ld16(tl + c + half * 16, o);
+            tm_wait_ld<16>(o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              joinb[row * AT_JOIN + half * 16 + e] = f == 0.f ? 0.f : o[e] * f;
+          }
+          at_bar(5, AT_SM_THREADS);
+          for (int e = st; e < it.R * 32; e += AT_SM_THREADS) {
+            const int rr = e >> 5, d = e & 31;
+            if (d >= n) continue;
+            float y = 0.f;
+#pragma unroll
+            for (int k = 0; k < COPIES; ++k) y += joinb[(k * W + rr) * AT_JOIN + d];
+            if (whole)
+              at_store(A.out, s_out[kb][rr] * C.dim + c + d, y, P.bf16);
+            else
+              A.S.part[((size_t)slot_id * KV_ROWS + rr) * C.dim + c + d] = y;
+          }
+          at_bar(5, AT_SM_THREADS);
         }
       }
       tm_fence_before();
       if (!whole) {
         // The CTAs that hold this query tile: the first of them keeps the ticket.
-        const int first = static_cast<int>(((it.u0 + 1) * ctas - 1) / total);
-        const int last = static_cast<int>(((it.u0 + it.tiles) * ctas - 1) / total);
+        const long long all = s_total, n = min((long long)gridDim.x, all);
+        const int first = static_cast<int>(((it.u0 + 1) * n - 1) / all);
+        const int last = static_cast<int>(((it.u0 + it.tiles) * n - 1) / all);
         __threadfence();
         at_bar(5, AT_SM_THREADS);
         if (st == 0) {
@@ -1145,41 +1243,11 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         at_bar(5, AT_SM_THREADS);
         if (s_last) {
           __threadfence();
-          const int vec = C.dim / 4;
-          for (int e = st; e < R * vec; e += AT_SM_THREADS) {
-            const int r = e / vec, dv = e - r * vec;
-            auto slot_of = [&](int k) { return (size_t)(2 * k + (k == first ? 1 : 0)) * KV_ROWS + r; };
-            float top = -INFINITY;
-            for (int k = first; k <= last; ++k) {
-              const float2 s2 = __ldcg(A.S.stat + slot_of(k));
-              if (s2.y != 0.f) top = fmaxf(top, s2.x);
-            }
-            float sum = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int k = first; k <= last; ++k) {
-              const float2 s2 = __ldcg(A.S.stat + slot_of(k));
-              if (s2.y == 0.f) continue;
-              const float f = exp2f(s2.x - top);
-              const float4 y =
-                  __ldcg(reinterpret_cast<const float4*>(A.S.part + slot_of(k) * C.dim) + dv);
-              sum = fmaf(s2.y, f, sum);
-              o.x = fmaf(y.x, f, o.x);
-              o.y = fmaf(y.y, f, o.y);
-              o.z = fmaf(y.z, f, o.z);
-              o.w = fmaf(y.w, f, o.w);
-            }
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            const long long at = s_out[r] * C.dim + dv * 4;
-            at_store(A.out, at, o.x * inv, P.bf16);
-            at_store(A.out, at + 1, o.y * inv, P.bf16);
-            at_store(A.out, at + 2, o.z * inv, P.bf16);
-            at_store(A.out, at + 3, o.w * inv, P.bf16);
-            if (dv == 0 && A.lse)
-              A.lse[s_out[r]] =
-                  sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
-          }
+          at_join(A, P.bf16, it.R, first, last, s_out[kb]);
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&dempty[kb]);
     }
   }
 
@@ -1188,8 +1256,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   if (w == 1) {
     __syncwarp();
     tm_fence_after();
-    const uint32_t need = (2 + ndb) * W, cols = need <= 128 ? 128 : (need <= 256 ? 256 : 512);
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
                  : "memory");
   }
 }
@@ -1210,8 +1277,8 @@ static PFN_cuTensorMapEncodeTiled_v12000 at_encoder() {
   return fn;
 }
 
-// Shared memory that a kernel may use beside its static arrays (227 KB a CTA).
-constexpr size_t AT_SMEM = 232448 - 12288;
+// Shared memory of a CTA, and what the kernels' static arrays take of it (at most).
+constexpr size_t AT_SMEM = 232448, AT_STATIC = 16384;
 
 cudaError_t launch_kv_attend(const AttendArgs& A, sv_dtype dt, cudaStream_t st) {
   static std::once_flag once;
@@ -1221,7 +1288,8 @@ cudaError_t launch_kv_attend(const AttendArgs& A, sv_dtype dt, cudaStream_t st) 
                          reinterpret_cast<const void*>(kv_attend_kernel<64>),
                          reinterpret_cast<const void*>(kv_attend_kernel<128>)};
     for (int i = 0; i < 3 && attr == cudaSuccess; ++i)
-      attr = cudaFuncSetAttribute(ks[i], cudaFuncAttributeMaxDynamicSharedMemorySize, (int)AT_SMEM);
+      attr = cudaFuncSetAttribute(ks[i], cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  (int)(AT_SMEM - AT_STATIC));
   });
   if (attr != cudaSuccess) return attr;
   const KvCache& C = A.C;
@@ -1229,17 +1297,14 @@ cudaError_t launch_kv_attend(const AttendArgs& A, sv_dtype dt, cudaStream_t st) 
   P.bf16 = dt == SV_BF16;
   P.qterms = P.bf16 ? 2 : 3;
   P.ndb = C.dim > 128 ? 2 : 1;
-  // Above dim 128 the ring's tiles take 64 KB, which leaves room for the queries and weights
-  // of 64 rows.
-  P.rt = P.ndb == 2 ? 64 : KV_ROWS;
   const long long rows = (long long)A.T * A.group;
-  P.width = rows <= 32 ? 32 : (rows <= 64 || P.rt == 64 ? 64 : 128);
-  const size_t fixed = 1024 + (size_t)P.qterms * P.ndb * P.width * 128 +
-                       (size_t)AT_PTERMS * AT_KEYS * P.width;
-  const size_t stage = (size_t)2 * P.ndb * AT_BLK;
-  P.stages = (int)((AT_SMEM - fixed) / stage);
-  if (P.stages > AT_MAX_STAGES) P.stages = AT_MAX_STAGES;
-  const size_t smem = fixed + P.stages * stage;
+  const int width = rows <= 32 ? 32 : (rows <= 64 ? 64 : 128);
+  const size_t tile = (size_t)P.ndb * AT_BLK;
+  const size_t fixed = 1024 + P.qterms * tile + (width < 128 ? 4 * 128 * AT_JOIN : 0);
+  const int ring = (int)((AT_SMEM - AT_STATIC - fixed) / tile);
+  P.nk = ring / 2 < AT_MAX_RING ? ring / 2 : AT_MAX_RING;
+  P.nv = ring - ring / 2 < AT_MAX_RING ? ring - ring / 2 : AT_MAX_RING;
+  const size_t smem = fixed + (P.nk + P.nv) * tile;
   // The pools of one layer as matrices [pages * heads * page tokens][dim bytes], in boxes of
   // one page x 128 bytes (128-byte swizzle, zeros past dim).
   PFN_cuTensorMapEncodeTiled_v12000 enc = at_encoder();
@@ -1262,9 +1327,9 @@ cudaError_t launch_kv_attend(const AttendArgs& A, sv_dtype dt, cudaStream_t st) 
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
     return e;
   const int grid = sms < KV_MAX_CTAS ? sms : KV_MAX_CTAS;
-  if (P.width == 32)
+  if (width == 32)
     kv_attend_kernel<32><<<grid, AT_THREADS, smem, st>>>(A, P, tm[0], tm[1]);
-  else if (P.width == 64)
+  else if (width == 64)
     kv_attend_kernel<64><<<grid, AT_THREADS, smem, st>>>(A, P, tm[0], tm[1]);
   else
     kv_attend_kernel<128><<<grid, AT_THREADS, smem, st>>>(A, P, tm[0], tm[1]);
