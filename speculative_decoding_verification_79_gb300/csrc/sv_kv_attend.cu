@@ -13,7 +13,7 @@
 // to tensor memory and are multiplied from there.
 //
 // A thread owns a query row (a lane of the accumulator) and some of the tile's tokens, so
-// that the softmax needs no exchange but one vote between the two threads of a row. Sixteen
+// that the softmax needs no exchange but one vote between the four threads of a row. Sixteen
 // tokens share a page: its key scale is a factor of their scores; its value scale is
 // folded into their weights (its logarithm added to the scores, so that no weight exceeds
 // the reference) and taken out of their sum again. The reference m of a row only moves when
@@ -31,8 +31,8 @@
 //
 // Warps, coupled by mbarriers: one copies K tiles page by page by tensor-map TMA (128-byte
 // swizzle) into a ring, another V tiles into a second (and plans the next query tile while
-// this one is in work); one issues the scores' products and one the output's; eight form
-// the weights, four on each half of a row copy's tokens.
+// this one is in work); one issues the scores' products and one the output's; sixteen form
+// the weights, four on each quarter of a row copy's tokens.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -46,7 +46,8 @@
 namespace sv {
 
 constexpr int AT_KEYS = 128;     // tokens per key tile
-constexpr int AT_SM_WARPS = 8;   // warps that form the weights
+constexpr int AT_PARTS = 4;      // threads of a query row copy
+constexpr int AT_SM_WARPS = 4 * AT_PARTS;  // warps that form the weights
 constexpr int AT_SM0 = 128;      // first of their threads, after copies, scores and outputs
 constexpr int AT_SM_THREADS = 32 * AT_SM_WARPS;
 constexpr int AT_THREADS = AT_SM0 + AT_SM_THREADS;
@@ -54,7 +55,7 @@ constexpr int AT_BLK = AT_KEYS * 128;  // 128 tokens x 128 bytes
 constexpr int AT_MAX_RING = 8;   // most K tiles, and V tiles, in shared memory
 constexpr int AT_INFO = 32;      // key tiles whose page data are kept
 constexpr int AT_PTERMS = 3;
-constexpr int AT_JOIN = 33;      // floats of a row in the buffer that adds copies
+constexpr int AT_JOIN = 33;      // floats of a row in the buffer that outputs go through
 // Weights are kept as 2^(x - m + 11): up to 2^15 before the reference must move (below
 // e5m2's 57344). Their terms end at 2^-16, e5m2's smallest, so a weight has its 9 bits down
 // to 2^-19 of the reference and counts down to 2^-28. A larger shift would leave less room
@@ -120,6 +121,16 @@ __device__ __forceinline__ void tm_st16(uint32_t addr, const float* v) {
       "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]),
       "f"(v[15])
       : "memory");
+}
+__device__ __forceinline__ void tm_ld8(uint32_t addr, float* v) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+                 "=f"(v[6]), "=f"(v[7])
+               : "r"(addr));
+}
+__device__ __forceinline__ void tm_st2(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b)
+               : "memory");
 }
 __device__ __forceinline__ void tm_st4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
                                        uint32_t d) {
@@ -244,13 +255,13 @@ __device__ __forceinline__ AtTile at_tile(const AttendArgs& A, const AtRow& r, i
 }
 
 // Work is counted in key tiles, with AT_EXTRA more for each query tile: what its queries'
-// conversion and its results cost.
-constexpr int AT_EXTRA = 2;
+// conversion and its results cost. Its order is rows, query tiles, heads.
+constexpr int AT_EXTRA = 3;
 
-__device__ __forceinline__ long long at_head_units(const AttendArgs& A, const AtRow& r) {
-  long long c = 0;
-  for (int rt = 0; rt < r.nrt; ++rt) c += AT_EXTRA + at_tile(A, r, rt).tiles();
-  return c;
+// Units of row b's query tile rt for one head (0: none).
+__device__ __forceinline__ int at_units(const AttendArgs& A, int b, int rt) {
+  const AtRow r = at_row(A, b);
+  return rt < r.nrt ? AT_EXTRA + at_tile(A, r, rt).tiles() : 0;
 }
 
 // The units of this CTA, one query tile after the other: key tiles i0 .. i1 - 1 of the
@@ -269,23 +280,19 @@ struct AtWalk {
     i1 = max(0, static_cast<int>(stop - base) - AT_EXTRA);
     return i1 > i0;
   }
-  // From row b0, unit `rem` of it.
-  __device__ __noinline__ void start(const AttendArgs& A, int b0, long long rem, long long from, long long to) {
-    b = b0;
+  // From unit `rem` of query tile rt0 of row b0 (all heads).
+  __device__ __noinline__ void start(const AttendArgs& A, int b0, int rt0, long long rem,
+                                     long long from, long long to) {
     at = from;
     end = to;
     if (at >= end) return;
+    b = b0;
+    rt = rt0;
     row = at_row(A, b);
-    const long long per = at_head_units(A, row);
-    h = static_cast<int>(rem / per);
-    rem -= h * per;
-    rt = 0;
-    tile = at_tile(A, row, 0);
-    while (rem >= AT_EXTRA + tile.tiles()) {
-      rem -= AT_EXTRA + tile.tiles();
-      tile = at_tile(A, row, ++rt);
-    }
-    base = from - rem;
+    tile = at_tile(A, row, rt);
+    const int per = AT_EXTRA + tile.tiles();
+    h = static_cast<int>(static_cast<unsigned long long>(rem) / static_cast<unsigned>(per));
+    base = from - (rem - static_cast<long long>(h) * per);
     if (!settle()) next(A);
   }
   __device__ __forceinline__ bool live() const { return at < end; }
@@ -294,16 +301,16 @@ struct AtWalk {
       base += AT_EXTRA + tile.tiles();
       at = base;
       if (at >= end) return;
-      if (++rt == row.nrt) {
-        rt = 0;
-        if (++h == A.C.heads) {
-          h = 0;
+      if (++h == A.C.heads) {
+        h = 0;
+        if (++rt == row.nrt) {
+          rt = 0;
           do {  // (a row with queries exists: units are left)
             row = at_row(A, ++b);
           } while (row.rows == 0);
         }
+        tile = at_tile(A, row, rt);
       }
-      tile = at_tile(A, row, rt);
     } while (!settle());
   }
 };
@@ -321,35 +328,15 @@ struct AtItem {
   __device__ __forceinline__ int key_tile(int i) const { return i < ns ? i : lo + i - ns; }
 };
 
-__device__ __forceinline__ void at_store(void* out, long long at, float y, int bf16) {
-  if (bf16)
-    static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(y);
-  else
-    static_cast<__half*>(out)[at] = __float2half_rn(y);
+// Two and four consecutive values, rounded to the output's type.
+__device__ __forceinline__ uint32_t at_pack(float a, float b, int bf16) {
+  const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
+  const __half2 y = __floats2half2_rn(a, b);
+  return bf16 ? *reinterpret_cast<const uint32_t*>(&x) : *reinterpret_cast<const uint32_t*>(&y);
 }
-
-// Sixteen consecutive values, rounded to the output's type, or as they are.
-__device__ __forceinline__ void at_store16(void* out, long long at, const float* y, int bf16) {
-  uint32_t o[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    if (bf16) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * e], y[2 * e + 1]);
-      o[e] = *reinterpret_cast<const uint32_t*>(&h);
-    } else {
-      const __half2 h = __floats2half2_rn(y[2 * e], y[2 * e + 1]);
-      o[e] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-  }
-  uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at);
-  p[0] = make_uint4(o[0], o[1], o[2], o[3]);
-  p[1] = make_uint4(o[4], o[5], o[6], o[7]);
-}
-__device__ __forceinline__ void at_store16(float* out, const float* y) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    reinterpret_cast<float4*>(out)[e] =
-        make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+__device__ __forceinline__ void at_store4(void* out, long long at, float4 y, int bf16) {
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) =
+      make_uint2(at_pack(y.x, y.y, bf16), at_pack(y.z, y.w, bf16));
 }
 
 // Has it been WAIT_CYCLES since the first call with *t0 == 0?
@@ -385,65 +372,97 @@ __device__ __forceinline__ void at_drain(uint64_t* bar, bool abort) {
     if (clock64() - t0 > WAIT_CYCLES / 8) break;
 }
 
-// Query row `row` of an item, by half a warp (lane l16): e4m3 terms into shared memory in the
-// layout of a K-major operand, in each of the row's copies (W rows apart); returns the power
-// of two that the terms were divided by, or NaN when a component is infinite (which the
-// saturating terms would not show).
+// The queries of an item: half a warp takes a row, a lane eight components (sixteen above
+// dim 128). at_fetch copies them, as they are, to where the lane's own terms will be, so
+// that all rows are on their way at once; at_convert makes the terms: e4m3 in the layout of
+// a K-major operand, in each of the row's copies (W rows apart). The factor of a row's
+// scores is the power of two that its terms were divided by, times the call's scale; NaN
+// when a component is infinite, which the saturating terms would not show. (Rows past the
+// item's keep what they held: each row's results are its own.) Not expanded in place: once
+// per query tile, and the kernel's loops share the instruction cache.
+__device__ __forceinline__ uint32_t at_raw(int db, int terms, int ndb, int row, int l16) {
+  // The 16 bytes go to chunk l16 & 7 of the row in block 0 (l16 < 8) or 1 of the terms'
+  // blocks; above dim 128 the second half of the row to blocks 2 and 3.
+  return (2 * db + (l16 >> 3)) * AT_BLK + row * 128 + (l16 & 7) * 16;
+}
+__device__ __noinline__ void at_fetch(const AttendArgs& A, int terms, int ndb, const AtItem* it,
+                                      unsigned char* Q) {
+  const int hw = (threadIdx.x - AT_SM0) >> 4, l16 = threadIdx.x & 15;
+#pragma unroll 1
+  for (int row = hw; row < it->R; row += 2 * AT_SM_WARPS) {
+    const int t = (it->r0 + row) / A.group, gh = it->r0 + row - t * A.group;
+    const uint16_t* src = static_cast<const uint16_t*>(A.q) + it->b * A.q_row + t * A.q_tok +
+                          (size_t)(it->h * A.group + gh) * A.C.dim;
+    for (int db = 0; db < ndb; ++db) {
+      const int d = db * 128 + l16 * 8;
+      if (d < A.C.dim)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                         smem_addr(Q + at_raw(db, terms, ndb, row, l16))),
+                     "l"(src + d)
+                     : "memory");
+    }
+  }
+}
 template <int W>
-__device__ float at_query(const AttendArgs& A, const AttendPlan& P, const uint16_t* src, int row,
-                          int l16, unsigned char* Q) {
-  float f[2][8];
-  float a = 0.f;
-#pragma unroll
-  for (int db = 0; db < 2; ++db) {
-    const int d = db * 128 + l16 * 8;
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (d < A.C.dim) x = __ldg(reinterpret_cast<const uint4*>(src + d));
-    const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (P.bf16) {
-        f[db][2 * e] = bf_lo(xw[e]);
-        f[db][2 * e + 1] = bf_hi(xw[e]);
-      } else {
-        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&xw[e]));
-        f[db][2 * e] = y.x;
-        f[db][2 * e + 1] = y.y;
-      }
-      a = fmaxf(a, fmaxf(fabsf(f[db][2 * e]), fabsf(f[db][2 * e + 1])));
-    }
-  }
+__device__ __noinline__ void at_convert(const AttendArgs& A, int terms, int ndb, int bf16,
+                                        const AtItem* it, unsigned char* Q, float* cs) {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
+  const int hw = (threadIdx.x - AT_SM0) >> 4, l16 = threadIdx.x & 15;
   const uint32_t half = 0xffffu << (threadIdx.x & 16);  // (the other half may have no row)
+#pragma unroll 1
+  for (int row = hw; row < it->R; row += 2 * AT_SM_WARPS) {
+    float f[2][8];
+    float a = 0.f;
 #pragma unroll
-  for (int s = 8; s; s >>= 1) a = fmaxf(a, __shfl_xor_sync(half, a, s));
-  const float sc = kv_scale(a), inv = 1.f / sc;
+    for (int db = 0; db < 2; ++db) {
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (db * 128 + l16 * 8 < A.C.dim)
+        x = *reinterpret_cast<const uint4*>(Q + at_raw(db, terms, ndb, row, l16));
+      const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-  for (int db = 0; db < 2; ++db) {
-    if (db >= P.ndb) break;
-    float y[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = f[db][e] * inv;
-    unsigned char* dst =
-        Q + (size_t)db * AT_BLK + row * 128 + (((l16 >> 1) ^ (row & 7)) << 4) + (l16 & 1) * 8;
-    for (int t = 0; t < P.qterms; ++t) {
-      uint2 o;
-      o.x = e4m3x4(y[0], y[1], y[2], y[3]);
-      o.y = e4m3x4(y[4], y[5], y[6], y[7]);
-#pragma unroll
-      for (int c = 0; c < 128 / W; ++c)
-        *reinterpret_cast<uint2*>(dst + (size_t)t * P.ndb * AT_BLK + c * W * 128) = o;
-      const uint32_t ow[2] = {o.x, o.y};
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float2 lo = e4m3_to_f2(ow[e] & 0xffffu), hi = e4m3_to_f2(ow[e] >> 16);
-        y[4 * e] -= lo.x;
-        y[4 * e + 1] -= lo.y;
-        y[4 * e + 2] -= hi.x;
-        y[4 * e + 3] -= hi.y;
+      for (int e = 0; e < 4; ++e) {
+        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&xw[e]));
+        f[db][2 * e] = bf16 ? bf_lo(xw[e]) : y.x;
+        f[db][2 * e + 1] = bf16 ? bf_hi(xw[e]) : y.y;
+        a = fmaxf(a, fmaxf(fabsf(f[db][2 * e]), fabsf(f[db][2 * e + 1])));
       }
     }
+    __syncwarp(half);  // the row is in registers: its place is free
+#pragma unroll
+    for (int s = 8; s; s >>= 1) a = fmaxf(a, __shfl_xor_sync(half, a, s));
+    const float sc = kv_scale(a), inv = 1.f / sc;
+#pragma unroll
+    for (int db = 0; db < 2; ++db) {
+      if (db >= ndb) break;
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = f[db][e] * inv;
+      unsigned char* dst =
+          Q + (size_t)db * AT_BLK + row * 128 + (((l16 >> 1) ^ (row & 7)) << 4) + (l16 & 1) * 8;
+#pragma unroll 1
+      for (int t = 0; t < terms; ++t) {
+        uint2 o;
+        o.x = e4m3x4(y[0], y[1], y[2], y[3]);
+        o.y = e4m3x4(y[4], y[5], y[6], y[7]);
+#pragma unroll
+        for (int c = 0; c < 128 / W; ++c)
+          *reinterpret_cast<uint2*>(dst + (size_t)t * ndb * AT_BLK + c * W * 128) = o;
+        const uint32_t ow[2] = {o.x, o.y};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float2 lo = e4m3_to_f2(ow[e] & 0xffffu), hi = e4m3_to_f2(ow[e] >> 16);
+          y[4 * e] -= lo.x;
+          y[4 * e + 1] -= lo.y;
+          y[4 * e + 2] -= hi.x;
+          y[4 * e + 3] -= hi.y;
+        }
+      }
+    }
+    if (l16 == 0) cs[row] = it->bad || a == INFINITY ? NAN : sc * A.scale;
   }
-  return a == INFINITY ? NAN : sc;
+  __syncwarp();
+  fence_async();
 }
 
 // Waits for the copies of the last tiles 0 .. g - 1 of a ring of n.
@@ -454,61 +473,80 @@ __device__ __noinline__ void at_land(uint64_t* full, int n, int g) {
     }
 }
 
-// The queries of an item and their scores' factors, two to a warp of those that form the
-// weights. (Rows past the item's keep what they held: each row's results are its own.) Not
-// expanded in place: once per query tile, and the kernel's loops have to fit the
-// instruction cache together.
-template <int W>
-__device__ __noinline__ void at_queries(const AttendArgs& A, const AttendPlan& P, const AtItem* it,
-                                        unsigned char* Q, float* cs) {
-  const int sw = (threadIdx.x - AT_SM0) >> 5, lane = threadIdx.x & 31;
-#pragma unroll 1
-  for (int row = sw * 2 + (lane >> 4); row < it->R; row += 2 * AT_SM_WARPS) {
-    const int t = (it->r0 + row) / A.group, gh = it->r0 + row - t * A.group;
-    const uint16_t* src = static_cast<const uint16_t*>(A.q) + it->b * A.q_row + t * A.q_tok +
-                          (size_t)(it->h * A.group + gh) * A.C.dim;
-    const float sc = at_query<W>(A, P, src, row, lane & 15, Q);
-    if ((lane & 15) == 0) cs[row] = it->bad ? NAN : sc * A.scale;
-  }
-  __syncwarp();
-  fence_async();
-}
-
 // Joins the partial results of a query tile's CTAs first .. last (outputs, sums and
-// references) into its output. All threads of the weights; `out` has the rows' places.
+// references) into its output. All threads of the weights; `out` has the rows' places. A
+// warp a row finds the common reference and the sum; then a thread adds four components of a
+// row over the CTAs, several loads in flight.
 __device__ __noinline__ void at_join(const AttendArgs& A, int bf16, int R, int first, int last,
-                                     const long long* out) {
-  const int vec = A.C.dim / 4;
-  for (int e = threadIdx.x - AT_SM0; e < R * vec; e += AT_SM_THREADS) {
-    const int r = e / vec, dv = e - r * vec;
-    auto slot_of = [&](int k) { return (size_t)(2 * k + (k == first ? 1 : 0)) * KV_ROWS + r; };
-    float top = -INFINITY;
-    for (int k = first; k <= last; ++k) {
-      const float2 s2 = __ldcg(A.S.stat + slot_of(k));
-      if (s2.y != 0.f) top = fmaxf(top, s2.x);
-    }
-    float sum = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = first; k <= last; ++k) {
-      const float2 s2 = __ldcg(A.S.stat + slot_of(k));
+                                     const long long* out, float2* rows) {
+  const int st = threadIdx.x - AT_SM0, lane = st & 31;
+  auto slot_of = [&](int k, int r) {
+    return (size_t)(2 * k + (k == first ? 1 : 0)) * KV_ROWS + r;
+  };
+  for (int r = st >> 5; r < R; r += AT_SM_WARPS) {
+    float ref = -INFINITY, sum = 0.f;
+    for (int k = first + lane; k <= last; k += 32) {
+      const float2 s2 = __ldcg(A.S.stat + slot_of(k, r));
       if (s2.y == 0.f) continue;
-      const float f = exp2f(s2.x - top);
-      const float4 y = __ldcg(reinterpret_cast<const float4*>(A.S.part + slot_of(k) * A.C.dim) + dv);
-      sum = fmaf(s2.y, f, sum);
-      o.x = fmaf(y.x, f, o.x);
-      o.y = fmaf(y.y, f, o.y);
-      o.z = fmaf(y.z, f, o.z);
-      o.w = fmaf(y.w, f, o.w);
+      const float top = fmaxf(ref, s2.x);
+      sum = (sum == 0.f ? 0.f : sum * exp2f(ref - top)) + s2.y * exp2f(s2.x - top);
+      ref = top;
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const long long at = out[r] * A.C.dim + dv * 4;
-    at_store(A.out, at, o.x * inv, bf16);
-    at_store(A.out, at + 1, o.y * inv, bf16);
-    at_store(A.out, at + 2, o.z * inv, bf16);
-    at_store(A.out, at + 3, o.w * inv, bf16);
-    if (dv == 0 && A.lse)
-      A.lse[out[r]] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+      const float r2 = __shfl_xor_sync(0xffffffffu, ref, d), s2 = __shfl_xor_sync(0xffffffffu, sum, d);
+      const float top = fmaxf(ref, r2);
+      sum = (sum == 0.f ? 0.f : sum * exp2f(ref - top)) + (s2 == 0.f ? 0.f : s2 * exp2f(r2 - top));
+      ref = top;
+    }
+    if (lane == 0) {
+      rows[r] = make_float2(ref, sum == 0.f ? 0.f : 1.f / sum);
+      if (A.lse)
+        A.lse[out[r]] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+    }
   }
+  at_bar(5, AT_SM_THREADS);
+  const int vec = A.C.dim / 4, n = R * vec;
+  constexpr int J = 4;
+#pragma unroll 1
+  for (int e0 = st; e0 < n; e0 += J * AT_SM_THREADS) {
+    float4 o[J];
+    int r[J], dv[J];
+    float ref[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int e = min(e0 + j * AT_SM_THREADS, n - 1);  // (the last is done again)
+      r[j] = e / vec;
+      dv[j] = e - r[j] * vec;
+      ref[j] = rows[r[j]].x;
+      o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll 1
+    for (int k = first; k <= last; ++k) {
+      float2 s2[J];
+      float4 y[J];
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        s2[j] = __ldcg(A.S.stat + slot_of(k, r[j]));
+        y[j] = __ldcg(reinterpret_cast<const float4*>(A.S.part + slot_of(k, r[j]) * A.C.dim) + dv[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const float f = s2[j].y == 0.f ? 0.f : exp2f(s2[j].x - ref[j]);
+        o[j].x = fmaf(y[j].x, f, o[j].x);
+        o[j].y = fmaf(y[j].y, f, o[j].y);
+        o[j].z = fmaf(y[j].z, f, o[j].z);
+        o[j].w = fmaf(y[j].w, f, o[j].w);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const float inv = rows[r[j]].y;
+      at_store4(A.out, out[r[j]] * A.C.dim + dv[j] * 4,
+                make_float4(o[j].x * inv, o[j].y * inv, o[j].z * inv, o[j].w * inv), bf16);
+    }
+  }
+  at_bar(5, AT_SM_THREADS);  // the rows' data are used again
 }
 
 // W: rows of a copy (32, 64 or 128 >= the query rows of a tile).
@@ -518,7 +556,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
                      const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV) {
   constexpr int COPIES = 128 / W;
-  constexpr int NC = W / 2;  // tokens of a thread
+  constexpr int NC = W / AT_PARTS;     // tokens of a thread
+  constexpr int GC = NC < 16 ? NC : 16;  // taken at a time
   // Tensor memory: the output's accumulator, then three of scores (two above dim 128). A
   // tile's weights (32 columns a term) replace its scores.
   const int nsb = P.ndb == 1 ? 3 : 2;
@@ -529,7 +568,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   __shared__ uint64_t sfull[3], pfull[3], pvdone[3], qfull, dfull[2], dempty[2], drain[2];
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
-  __shared__ int s_b0, s_last;
+  __shared__ int s_b0, s_rt0, s_last;
   __shared__ long long s_rem, s_total, s_sum[AT_THREADS / 32];
   // Per key tile and page of it: row of the pool (-1: none); key scale, log2 and inverse of
   // the value scale.
@@ -542,8 +581,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   __shared__ int s_pos[2][W];
   __shared__ unsigned long long s_see[2][W];
   __shared__ long long s_out[2][W];
-  __shared__ int s_par[SV_MAX_TREE];
-  __shared__ float s_top[2][128], s_l[2][128];  // per half and row: largest scores, sums
+  __shared__ int s_par[SV_MAX_TREE], s_tpos[SV_MAX_TREE];  // a tree: parents, positions
+  __shared__ unsigned long long s_tsee[SV_MAX_TREE];       // and what a node sees
+  __shared__ float s_top[AT_PARTS][128], s_l[AT_PARTS][128];  // largest scores, sums
   __shared__ float2 s_stat[128];     // reference and sum of a row copy
   __shared__ int s_vnan[AT_KEYS];
 
@@ -555,7 +595,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   unsigned char* Qs = dsm;                                  // [terms][ndb][128][128]
   unsigned char* Ks = Qs + P.qterms * slot;                 // [nk][ndb][128][128]
   unsigned char* Vs = Ks + (size_t)P.nk * slot;             // [nv][ndb][128][128]
-  float* joinb = reinterpret_cast<float*>(Vs + (size_t)P.nv * slot);  // [128][AT_JOIN], copies only
+  float* joinb = reinterpret_cast<float*>(Vs + (size_t)P.nv * slot);  // [128][AT_JOIN]
 
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return mbar_try(bar, parity) || at_wait_on(bar, parity, &s_abort, A.S.hdr);
@@ -590,13 +630,20 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  // This CTA's share: the units of all rows, cut into equal parts. Rows are counted by the
-  // threads in turn; the second pass finds the row where the share begins.
+  // This CTA's share: the units of all rows' query tiles, cut into equal parts. Query tiles
+  // are counted by the threads in turn; the second pass finds the one where the share begins.
+  const int nrt = static_cast<int>(((long long)A.T * A.group + KV_ROWS - 1) / KV_ROWS);
+  const long long pairs = (long long)C.batch * nrt;
+  auto units_of = [&](long long p) -> long long {
+    if (p >= pairs) return 0;
+    const int b = nrt == 1 ? static_cast<int>(p) : static_cast<int>(p / nrt);
+    return (long long)at_units(A, b, static_cast<int>(p - (long long)b * nrt)) * C.heads;
+  };
   long long total = 0, mine0 = 0;
-  for (int b = tid; b < C.batch; b += AT_THREADS) {
-    const AtRow r = at_row(A, b);
-    const long long c = at_head_units(A, r) * C.heads;
-    if (b == tid) mine0 = c;
+#pragma unroll 1
+  for (long long p = tid; p < pairs; p += AT_THREADS) {
+    const long long c = units_of(p);
+    if (p == tid) mine0 = c;
     total += c;
   }
   auto block_sum = [&](long long x, long long* before) {  // sum; *before: of lower threads
@@ -626,13 +673,13 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   if (tid == 0) s_total = total;
   if (from < to) {
     long long base = 0;
-    for (int b0 = 0; b0 < C.batch; b0 += AT_THREADS) {
-      const int b = b0 + tid;
-      const long long c =
-          b >= C.batch ? 0 : (b0 == 0 ? mine0 : at_head_units(A, at_row(A, b)) * C.heads);
+#pragma unroll 1
+    for (long long p0 = 0; p0 < pairs; p0 += AT_THREADS) {
+      const long long c = p0 == 0 ? mine0 : units_of(p0 + tid);
       const long long sum = block_sum(c, &before);
       if (from >= base + before && from < base + before + c) {
-        s_b0 = b;
+        s_b0 = static_cast<int>((p0 + tid) / nrt);
+        s_rt0 = static_cast<int>((p0 + tid) % nrt);
         s_rem = from - base - before;
       }
       base += sum;
@@ -650,7 +697,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     // one per tile, written before the tile's barrier is armed. (An entry is used again 32
     // tiles later, and K is never more than its ring and three steps ahead of the rest.)
     AtWalk walk;
-    walk.start(A, s_b0, s_rem, from, to);
+    walk.start(A, s_b0, s_rt0, s_rem, from, to);
     const int ppt = AT_KEYS >> C.lgp;             // pages per tile
     const int tpc = min(32 / ppt, AT_INFO / 4);   // tiles per chunk
     const int mt = lane / ppt, sub = lane - mt * ppt;
@@ -779,7 +826,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   } else if (w == 2) {
     // ---- V copies, and in their pauses planning: the next item's description and columns.
     AtWalk walk;
-    walk.start(A, s_b0, s_rem, from, to);
+    walk.start(A, s_b0, s_rt0, s_rem, from, to);
     const int ppt = AT_KEYS >> C.lgp;
     int k = 0, planned = 0;       // items planned, and their tiles
     bool more = true;
@@ -852,21 +899,26 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           __syncwarp();
           if (badtree && lane == 0) kv_report(A.S.hdr, ST_DEVICE_INPUT);
         }
-        for (int r = lane; r < R; r += 32) {
-          unsigned long long see = badtree ? ~0ull : 0ull;  // (a bad tree's scores are NaN)
-          const int t = (walk.tile.r0 + r) / A.group, gh = walk.tile.r0 + r - t * A.group;
-          int pos = len + t;
-          if (A.parent && !badtree) {
+        if (A.parent && !badtree) {  // what a node of the tree sees, and its position
+          for (int t = lane; t < nnew; t += 32) {
+            unsigned long long see = 0;
             int up = 0;
             for (int i = t;; i = s_par[i]) {
               if (!A.window || up < A.window || len + i < A.sinks) see |= 1ull << i;
               if (i == 0) break;
               ++up;
             }
-            pos = len + up;
+            s_tsee[t] = see;
+            s_tpos[t] = len + up;
           }
-          s_pos[kb][r] = pos;
-          s_see[kb][r] = see;
+          __syncwarp();
+        }
+#pragma unroll 1
+        for (int r = lane; r < R; r += 32) {
+          const int t = (walk.tile.r0 + r) / A.group, gh = walk.tile.r0 + r - t * A.group;
+          const bool tree = A.parent && !badtree;
+          s_pos[kb][r] = tree ? s_tpos[t] : len + t;
+          s_see[kb][r] = tree ? s_tsee[t] : ~0ull;  // (a bad tree's scores are NaN)
           s_out[kb][r] = ((long long)walk.b * A.T + t) * A.q_heads + walk.h * A.group + gh;
         }
         if (lane == 0) it.bad = badtree;
@@ -923,10 +975,10 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     }
   } else {
     // ---- Weights and results.
-    const int st = tid - AT_SM0, quad = w & 3, half = (w - 4) >> 2;
+    const int st = tid - AT_SM0, quad = w & 3, part = (w - 4) >> 2;
     const int row = quad * 32 + lane;             // lane of the accumulators
     const int copy = row / W, r = row % W;        // copy of query row r
-    const int c0 = copy * W + half * NC;          // first of this thread's tokens
+    const int c0 = copy * W + part * NC;          // first of this thread's tokens
     const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     // Queries without a token and rows with wrong data: zeros or NaN.
     for (long long u0 = (long long)blockIdx.x * AT_SM_WARPS + (w - 4);
@@ -953,10 +1005,14 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       }
     }
     bool dead = false;  // a wait gave up: skip the work, keep meeting the other warps
-    // The queries of item k into shared memory; then the scores may begin.
-    auto queries = [&](int k) {
+    // The queries of item k: on their way, and into shared memory; then the scores may begin.
+    auto fetch = [&](int k) {
       if (!dead && !wait(&dfull[k & 1], (k >> 1) & 1)) dead = true;
-      if (!dead && s_item[k & 1].m > 0) at_queries<W>(A, P, &s_item[k & 1], Qs, s_c[k & 1]);
+      if (!dead && s_item[k & 1].m > 0) at_fetch(A, P.qterms, ndb, &s_item[k & 1], Qs);
+    };
+    auto convert = [&](int k) {
+      if (!dead && s_item[k & 1].m > 0)
+        at_convert<W>(A, P.qterms, ndb, P.bf16, &s_item[k & 1], Qs, s_c[k & 1]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&qfull);
     };
@@ -966,7 +1022,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       const int b = sb ? sb - 1 : nsb - 1;
       return wait(&pvdone[b], (sb ? sph : sph - 1) & 1);
     };
-    queries(0);
+    fetch(0);
+    convert(0);
     int g = 0, q = 0, ph = 0;
     for (int item = 0;; ++item) {
       const int kb = item & 1;
@@ -991,6 +1048,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         const int key0 = it.key_tile(it.i0 + i) * AT_KEYS;
         if (!dead && !wait(&sfull[sb], sph & 1)) dead = true;
         tm_fence_after();
+        if (i == m - 1) fetch(item + 1);  // (the last scores are done: the queries' place is free)
         // Is there a key of the tile that some query does not see? Then also look after the
         // values that weight 0 would not hide: tokens past the end (whatever the page
         // holds) are zeroed, and a NaN is zeroed where it stands and made the weight of the
@@ -1005,12 +1063,12 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           const int tok = st & 127;
           bool nan = false;
           for (int db = 0; db < ndb && !dead; ++db) {
-            // Half of a token's eight 16-byte chunks, turned so that the lanes of a warp
+            // Two of a token's eight 16-byte chunks, turned so that the lanes of a warp
             // spread over the banks.
 #pragma unroll 1
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 2; ++e) {
               uint4* p = reinterpret_cast<uint4*>(Vs + (size_t)q * slot + db * AT_BLK + tok * 128) +
-                         ((4 * half + e + tok) & 7);
+                         ((2 * part + e + tok) & 7);
               if (key0 + tok >= it.end) {
                 *p = make_uint4(0, 0, 0, 0);
                 continue;
@@ -1028,9 +1086,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           fence_async();
           vnan = at_vote(5, AT_SM_THREADS, nan);
           if (vnan) {
-            if (half == 0) s_vnan[tok] = nan;
+            if (part == 0) s_vnan[tok] = 0;
             at_bar(5, AT_SM_THREADS);
-            if (half == 1 && nan) s_vnan[tok] = 1;
+            if (nan) s_vnan[tok] = 1;
             at_bar(5, AT_SM_THREADS);
           }
         }
@@ -1039,16 +1097,21 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           // This thread's scores as logarithms of their weights, sixteen tokens at a time.
           float x[NC];
 #pragma unroll
-          for (int c = 0; c < NC; c += 16) tm_ld16(sa + c0 + c, x + c);
+          for (int c = 0; c < NC; c += GC) {
+            if (GC == 16)
+              tm_ld16(sa + c0 + c, x + c);
+            else
+              tm_ld8(sa + c0 + c, x + c);
+          }
           tm_wait_ld<NC>(x);
           const float4* sc = s_sc[g & (AT_INFO - 1)];
           float top = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < NC; c += 16) {
+          for (int c = 0; c < NC; c += GC) {
             const float4 f = sc[(c0 + c) >> C.lgp];
             const float2 a = make_float2(f.x * cs, f.x * cs), b = make_float2(f.y + nm, f.y + nm);
 #pragma unroll
-            for (int e = c; e < c + 16; e += 2) {
+            for (int e = c; e < c + GC; e += 2) {
               const float2 y = __ffma2_rn(make_float2(x[e], x[e + 1]), a, b);
               x[e] = y.x;
               x[e + 1] = y.y;
@@ -1070,12 +1133,13 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           }
 #pragma unroll
           for (int c = 0; c < NC; c += 2) top = max3(top, x[c], x[c + 1]);
-          if (at_vote(1 + quad, 64, unseen || (real && top > AT_LIMIT))) {
+          if (at_vote(1 + quad, 128, unseen || (real && top > AT_LIMIT))) {
             // Move references to the tile's largest scores; the outputs and sums so far shrink
             // by the difference.
-            s_top[half][row] = top;
-            at_bar(1 + quad, 64);
-            const float d = fmaxf(s_top[0][row], s_top[1][row]);  // over the reference - 11
+            s_top[part][row] = top;
+            at_bar(1 + quad, 128);
+            const float d = fmaxf(fmaxf(s_top[0][row], s_top[1][row]),
+                                  fmaxf(s_top[2][row], s_top[3][row]));  // over the reference - 11
             float move = 0.f, fac = 1.f;
             if (unseen) {  // nothing to shrink: the reference goes wherever the scores are
               if (d > -INFINITY) {
@@ -1094,7 +1158,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
               if (!dead && !done()) dead = true;
               tm_fence_after();
 #pragma unroll 1
-              for (int c = half * 16; c < C.dim; c += 32) {
+              for (int c = part * 16; c < C.dim; c += 64) {
                 float o[16];
                 tm_ld16(tl + c, o);
                 tm_wait_ld<16>(o);
@@ -1108,11 +1172,11 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           // term is the upper byte of the remainder rounded to it (halves away from zero);
           // what is left of an fp16 number after that is exact.
 #pragma unroll
-          for (int c = 0; c < NC; c += 16) {
-            uint32_t t[AT_PTERMS][8];
+          for (int c = 0; c < NC; c += GC) {
+            uint32_t t[AT_PTERMS][GC / 2];
             float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < GC / 2; ++e) {
               const float2 p = make_float2(ex2(x[c + 2 * e]), ex2(x[c + 2 * e + 1]));
               sum = __fadd2_rn(sum, p);
               __half2 y = __floats2half2_rn(p.x, p.y);
@@ -1125,17 +1189,24 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             }
             l = fmaf(sum.x + sum.y, sc[(c0 + c) >> C.lgp].z, l);
 #pragma unroll
-            for (int k = 0; k < AT_PTERMS; ++k)
-              tm_st4(sa + k * 32 + (c0 + c) / 4, __byte_perm(t[k][0], t[k][1], 0x7531),
-                     __byte_perm(t[k][2], t[k][3], 0x7531), __byte_perm(t[k][4], t[k][5], 0x7531),
-                     __byte_perm(t[k][6], t[k][7], 0x7531));
+            for (int k = 0; k < AT_PTERMS; ++k) {
+              uint32_t v[GC / 4];
+#pragma unroll
+              for (int e = 0; e < GC / 4; ++e) v[e] = __byte_perm(t[k][2 * e], t[k][2 * e + 1], 0x7531);
+              if constexpr (GC == 16)
+                tm_st4(sa + k * 32 + (c0 + c) / 4, v[0], v[1], v[2], v[3]);
+              else
+                tm_st2(sa + k * 32 + (c0 + c) / 4, v[0], v[1]);
+            }
           }
           // Tokens that belong to the row's other copies.
+          if (COPIES > 1) {
 #pragma unroll
-          for (int c = 0; c < AT_KEYS / 16; c += 2) {
-            if ((c + half) * 16 / W == copy) continue;
+            for (int c = 0; c < AT_KEYS / 16; c += AT_PARTS) {
+              if ((c + part) * 16 / W == copy) continue;
 #pragma unroll
-            for (int k = 0; k < AT_PTERMS; ++k) tm_st4(sa + k * 32 + (c + half) * 4, 0, 0, 0, 0);
+              for (int k = 0; k < AT_PTERMS; ++k) tm_st4(sa + k * 32 + (c + part) * 4, 0, 0, 0, 0);
+            }
           }
           tm_wait_st();
         }
@@ -1154,11 +1225,12 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
 
       // -- The query tile's sums and outputs: the result when this CTA saw all its keys,
       // else partial results. The last scores are done, so the next queries go in first.
-      s_l[half][row] = l;
-      if (half == 0) s_stat[row].x = -nm;
-      queries(item + 1);
+      s_l[part][row] = l;
+      if (part == 0) s_stat[row].x = -nm;
+      convert(item + 1);
       at_bar(5, AT_SM_THREADS);
-      if (st < 128) s_stat[st].y = st % W < it.R ? s_l[0][st] + s_l[1][st] : 0.f;
+      if (st < 128)
+        s_stat[st].y = st % W < it.R ? s_l[0][st] + s_l[1][st] + (s_l[2][st] + s_l[3][st]) : 0.f;
       if (!dead && !done()) dead = true;
       tm_fence_after();
       at_bar(5, AT_SM_THREADS);
@@ -1177,55 +1249,44 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       const float2 own = s_stat[row];
       float f = own.y == 0.f ? 0.f : exp2f(own.x - ref);
       if (whole) f = sum == 0.f ? 0.f : f / sum;
-      if (copy == 0 && half == 0 && real) {
+      if (copy == 0 && part == 0 && real) {
         if (!whole)
           A.S.stat[(size_t)slot_id * KV_ROWS + r] = make_float2(ref, sum);
         else if (A.lse)
           A.lse[s_out[kb][r]] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
       }
-      if (COPIES == 1) {
-        if (live) {
+      // Through shared memory, 32 components at a time: copies are added there, and rows
+      // leave in whole sectors.
 #pragma unroll 1
-          for (int c = half * 16; c < C.dim; c += 32) {
-            float o[16];
-            tm_ld16(tl + c, o);
-            tm_wait_ld<16>(o);
+      for (int c = 0; c < C.dim; c += 32) {
+        const int n = min(32, C.dim - c);
+        if (live && part * 8 < n) {
+          float o[8];
+          tm_ld8(tl + c + part * 8, o);
+          tm_wait_ld<8>(o);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = f == 0.f ? 0.f : o[e] * f;
-            if (!real) continue;
-            if (whole)
-              at_store16(A.out, s_out[kb][r] * C.dim + c, o, P.bf16);
-            else
-              at_store16(A.S.part + ((size_t)slot_id * KV_ROWS + r) * C.dim + c, o);
-          }
+          for (int e = 0; e < 8; ++e)
+            joinb[row * AT_JOIN + part * 8 + e] = f == 0.f ? 0.f : o[e] * f;
         }
-      } else {
-        // Copies are added through shared memory, 32 components at a time.
+        at_bar(5, AT_SM_THREADS);
 #pragma unroll 1
-        for (int c = 0; c < C.dim; c += 32) {
-          const int n = min(32, C.dim - c);
-          if (live && half * 16 < n) {
-            float o[16];
-            tm_ld16(tl + c + half * 16, o);
-            tm_wait_ld<16>(o);
+        for (int e = st; e < it.R * 16; e += AT_SM_THREADS) {
+          const int rr = e >> 4, d = (e & 15) * 2;
+          if (d >= n) continue;
+          float y0 = 0.f, y1 = 0.f;
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              joinb[row * AT_JOIN + half * 16 + e] = f == 0.f ? 0.f : o[e] * f;
+          for (int k = 0; k < COPIES; ++k) {
+            y0 += joinb[(k * W + rr) * AT_JOIN + d];
+            y1 += joinb[(k * W + rr) * AT_JOIN + d + 1];
           }
-          at_bar(5, AT_SM_THREADS);
-          for (int e = st; e < it.R * 32; e += AT_SM_THREADS) {
-            const int rr = e >> 5, d = e & 31;
-            if (d >= n) continue;
-            float y = 0.f;
-#pragma unroll
-            for (int k = 0; k < COPIES; ++k) y += joinb[(k * W + rr) * AT_JOIN + d];
-            if (whole)
-              at_store(A.out, s_out[kb][rr] * C.dim + c + d, y, P.bf16);
-            else
-              A.S.part[((size_t)slot_id * KV_ROWS + rr) * C.dim + c + d] = y;
-          }
-          at_bar(5, AT_SM_THREADS);
+          if (whole)
+            *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(A.out) + s_out[kb][rr] * C.dim + c + d) =
+                at_pack(y0, y1, P.bf16);
+          else
+            *reinterpret_cast<float2*>(A.S.part + ((size_t)slot_id * KV_ROWS + rr) * C.dim + c + d) =
+                make_float2(y0, y1);
         }
+        at_bar(5, AT_SM_THREADS);
       }
       tm_fence_before();
       if (!whole) {
@@ -1243,7 +1304,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         at_bar(5, AT_SM_THREADS);
         if (s_last) {
           __threadfence();
-          at_join(A, P.bf16, it.R, first, last, s_out[kb]);
+          at_join(A, P.bf16, it.R, first, last, s_out[kb], s_stat);
         }
       }
       __syncwarp();
@@ -1278,7 +1339,7 @@ static PFN_cuTensorMapEncodeTiled_v12000 at_encoder() {
 }
 
 // Shared memory of a CTA, and what the kernels' static arrays take of it (at most).
-constexpr size_t AT_SMEM = 232448, AT_STATIC = 16384;
+constexpr size_t AT_SMEM = 232448, AT_STATIC = 20480;
 
 cudaError_t launch_kv_attend(const AttendArgs& A, sv_dtype dt, cudaStream_t st) {
   static std::once_flag once;
@@ -1300,7 +1361,7 @@ cudaError_t launch_kv_attend(const AttendArgs& A, sv_dtype dt, cudaStream_t st) 
   const long long rows = (long long)A.T * A.group;
   const int width = rows <= 32 ? 32 : (rows <= 64 ? 64 : 128);
   const size_t tile = (size_t)P.ndb * AT_BLK;
-  const size_t fixed = 1024 + P.qterms * tile + (width < 128 ? 4 * 128 * AT_JOIN : 0);
+  const size_t fixed = 1024 + P.qterms * tile + 4 * 128 * AT_JOIN;
   const int ring = (int)((AT_SMEM - AT_STATIC - fixed) / tile);
   P.nk = ring / 2 < AT_MAX_RING ? ring / 2 : AT_MAX_RING;
   P.nv = ring - ring / 2 < AT_MAX_RING ? ring - ring / 2 : AT_MAX_RING;
