@@ -457,7 +457,8 @@ sv_status sv_kv_read(const sv_kv_cache *cache, int layer, int n_layers, const in
  *  q_d        [batch, T, q_heads, dim] SV_BF16 or SV_F16, heads and dim dense, rows and
  *             tokens q_row / q_tok elements apart (multiples of 16 bytes). q_heads is a
  *             multiple of heads, at most 128 times as many: query head h reads key/value
- *             head h / (q_heads / heads).
+ *             head h / (q_heads / heads). batch * heads * ceil(T * q_heads / heads / 128) *
+ *             (max_pages * page / 128 + 8) stays below 2^31.
  *  n_new_d    [batch] int32 in [0, T], or NULL for T everywhere.
  *  parent_d   [batch, T] int32 or NULL. NULL: the new tokens are a chain. Otherwise a
  *             draft tree as in sv_verify_tree: parent of node i >= 1 in [0, i), entry 0

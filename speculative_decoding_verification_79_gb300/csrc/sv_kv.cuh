@@ -22,6 +22,7 @@ struct KvCache {
 // list of fresh pages, a flag per row, and the attention's partial results.
 constexpr int KV_MAX_CTAS = 160;  // persistent CTAs of the attention kernel
 constexpr int KV_ROWS = 128;      // most query rows of its tile
+constexpr int KV_EXTRA = 7;       // its work per query tile beside the key tiles, in key tiles
 
 struct KvWs {
   size_t ticket;  // uint32 [KV_MAX_CTAS]: partial results that have arrived

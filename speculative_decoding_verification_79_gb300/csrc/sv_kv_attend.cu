@@ -240,7 +240,8 @@ __device__ __forceinline__ AtTile at_tile(const AttendArgs& A, const AtRow& r, i
   AtTile t;
   t.r0 = rt * r.rr;
   t.r1 = min(t.r0 + r.rr, r.rows);
-  const int t0 = t.r0 / A.group, t1 = (t.r1 - 1) / A.group;
+  // (One query tile holds all tokens: no division.)
+  const int t0 = rt ? t.r0 / A.group : 0, t1 = r.nrt == 1 ? r.n - 1 : (t.r1 - 1) / A.group;
   t.pos_lo = A.parent ? r.len : r.len + t0;
   t.pos_hi = A.parent ? r.len + r.n - 1 : r.len + t1;
   t.end = t.pos_hi + 1;
@@ -256,7 +257,7 @@ __device__ __forceinline__ AtTile at_tile(const AttendArgs& A, const AtRow& r, i
 
 // Work is counted in key tiles, with AT_EXTRA more for each query tile: what its queries'
 // conversion and its results cost. Its order is rows, query tiles, heads.
-constexpr int AT_EXTRA = 3;
+constexpr int AT_EXTRA = KV_EXTRA;
 
 // Units of row b's query tile rt for one head (0: none).
 __device__ __forceinline__ int at_units(const AttendArgs& A, int b, int rt) {
@@ -271,18 +272,18 @@ struct AtWalk {
   AtRow row;
   AtTile tile;
   int i0, i1;
-  long long base, at, end;  // first unit of the query tile, of the share in it, share's end
+  int base, at, end;  // first unit of the query tile, of the share in it, share's end
 
   // The share of the current query tile; false when it has no key tile.
   __device__ __forceinline__ bool settle() {
-    const long long stop = min(end, base + AT_EXTRA + tile.tiles());
-    i0 = max(0, static_cast<int>(at - base) - AT_EXTRA);
-    i1 = max(0, static_cast<int>(stop - base) - AT_EXTRA);
+    const int stop = min(end, base + AT_EXTRA + tile.tiles());
+    i0 = max(0, at - base - AT_EXTRA);
+    i1 = max(0, stop - base - AT_EXTRA);
     return i1 > i0;
   }
   // From unit `rem` of query tile rt0 of row b0 (all heads).
-  __device__ __noinline__ void start(const AttendArgs& A, int b0, int rt0, long long rem,
-                                     long long from, long long to) {
+  __device__ __noinline__ void start(const AttendArgs& A, int b0, int rt0, int rem, int from,
+                                     int to) {
     at = from;
     end = to;
     if (at >= end) return;
@@ -291,8 +292,8 @@ struct AtWalk {
     row = at_row(A, b);
     tile = at_tile(A, row, rt);
     const int per = AT_EXTRA + tile.tiles();
-    h = static_cast<int>(static_cast<unsigned long long>(rem) / static_cast<unsigned>(per));
-    base = from - (rem - static_cast<long long>(h) * per);
+    h = rem / per;
+    base = from - (rem - h * per);
     if (!settle()) next(A);
   }
   __device__ __forceinline__ bool live() const { return at < end; }
@@ -315,6 +316,17 @@ struct AtWalk {
   }
 };
 
+// Share c of n equal parts of `total` units begins at at_share(c); at_owner is the share that
+// holds unit u.
+__device__ __forceinline__ int at_share(int c, int total, int n) {
+  const int per = total / n;
+  return c * per + min(c, total - per * n);
+}
+__device__ __forceinline__ int at_owner(int u, int total, int n) {
+  const int per = total / n, big = total - per * n;  // the first `big` shares have one more
+  return u < big * (per + 1) ? u / (per + 1) : big + (u - big * (per + 1)) / per;
+}
+
 // A query tile's share as the product and weight warps read it from shared memory.
 struct AtItem {
   int b, h, len, n;
@@ -324,7 +336,7 @@ struct AtItem {
   int end, pos_hi;  // as AtTile
   int ns, lo;
   int bad;          // the row's tree is wrong
-  long long u0;     // unit of its first key tile
+  int u0;           // unit of its first key tile
   __device__ __forceinline__ int key_tile(int i) const { return i < ns ? i : lo + i - ns; }
 };
 
@@ -507,41 +519,47 @@ __device__ __noinline__ void at_join(const AttendArgs& A, int bf16, int R, int f
   }
   at_bar(5, AT_SM_THREADS);
   const int vec = A.C.dim / 4, n = R * vec;
-  constexpr int J = 4;
+  constexpr int J = 2, K = 4;  // components and CTAs whose loads are in flight together
 #pragma unroll 1
   for (int e0 = st; e0 < n; e0 += J * AT_SM_THREADS) {
     float4 o[J];
     int r[J], dv[J];
-    float ref[J];
+    float2 row[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int e = min(e0 + j * AT_SM_THREADS, n - 1);  // (the last is done again)
       r[j] = e / vec;
       dv[j] = e - r[j] * vec;
-      ref[j] = rows[r[j]].x;
+      row[j] = rows[r[j]];
       o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
 #pragma unroll 1
-    for (int k = first; k <= last; ++k) {
-      float2 s2[J];
-      float4 y[J];
+    for (int k0 = first; k0 <= last; k0 += K) {
+      float2 s2[J][K];
+      float4 y[J][K];
 #pragma unroll
-      for (int j = 0; j < J; ++j) {
-        s2[j] = __ldcg(A.S.stat + slot_of(k, r[j]));
-        y[j] = __ldcg(reinterpret_cast<const float4*>(A.S.part + slot_of(k, r[j]) * A.C.dim) + dv[j]);
-      }
+      for (int k = 0; k < K; ++k)
 #pragma unroll
-      for (int j = 0; j < J; ++j) {
-        const float f = s2[j].y == 0.f ? 0.f : exp2f(s2[j].x - ref[j]);
-        o[j].x = fmaf(y[j].x, f, o[j].x);
-        o[j].y = fmaf(y[j].y, f, o[j].y);
-        o[j].z = fmaf(y[j].z, f, o[j].z);
-        o[j].w = fmaf(y[j].w, f, o[j].w);
-      }
+        for (int j = 0; j < J; ++j) {
+          const size_t sl = slot_of(min(k0 + k, last), r[j]);
+          s2[j][k] = __ldcg(A.S.stat + sl);
+          y[j][k] = __ldcg(reinterpret_cast<const float4*>(A.S.part + sl * A.C.dim) + dv[j]);
+        }
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const float f =
+              s2[j][k].y == 0.f || k0 + k > last ? 0.f : exp2f(s2[j][k].x - row[j].x);
+          o[j].x = fmaf(y[j][k].x, f, o[j].x);
+          o[j].y = fmaf(y[j][k].y, f, o[j].y);
+          o[j].z = fmaf(y[j][k].z, f, o[j].z);
+          o[j].w = fmaf(y[j][k].w, f, o[j].w);
+        }
     }
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const float inv = rows[r[j]].y;
+      const float inv = row[j].y;
       at_store4(A.out, out[r[j]] * A.C.dim + dv[j] * 4,
                 make_float4(o[j].x * inv, o[j].y * inv, o[j].z * inv, o[j].w * inv), bf16);
     }
@@ -568,8 +586,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   __shared__ uint64_t sfull[3], pfull[3], pvdone[3], qfull, dfull[2], dempty[2], drain[2];
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
-  __shared__ int s_b0, s_rt0, s_last;
-  __shared__ long long s_rem, s_total, s_sum[AT_THREADS / 32];
+  __shared__ int s_b0, s_rt0, s_rem, s_total, s_last, s_sum[AT_THREADS / 32];
   // Per key tile and page of it: row of the pool (-1: none); key scale, log2 and inverse of
   // the value scale.
   __shared__ int s_y[AT_INFO][8];
@@ -603,7 +620,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
 
   if (tid == 0) {
     for (int q = 0; q < AT_MAX_RING; ++q) {
-      mbar_init(&kfull[q], 1);
+      mbar_init(&kfull[q], 2);
       mbar_init(&kempty[q], 1);
       mbar_init(&vfull[q], 1);
       mbar_init(&vempty[q], 1);
@@ -632,57 +649,58 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   }
   // This CTA's share: the units of all rows' query tiles, cut into equal parts. Query tiles
   // are counted by the threads in turn; the second pass finds the one where the share begins.
-  const int nrt = static_cast<int>(((long long)A.T * A.group + KV_ROWS - 1) / KV_ROWS);
-  const long long pairs = (long long)C.batch * nrt;
-  auto units_of = [&](long long p) -> long long {
+  const int nrt = (A.T * A.group + KV_ROWS - 1) / KV_ROWS, pairs = C.batch * nrt;
+  auto units_of = [&](int p) -> int {
     if (p >= pairs) return 0;
-    const int b = nrt == 1 ? static_cast<int>(p) : static_cast<int>(p / nrt);
-    return (long long)at_units(A, b, static_cast<int>(p - (long long)b * nrt)) * C.heads;
+    const int b = nrt == 1 ? p : p / nrt;
+    return at_units(A, b, p - b * nrt) * C.heads;
   };
-  long long total = 0, mine0 = 0;
+  int mine = 0, sum = 0;
 #pragma unroll 1
-  for (long long p = tid; p < pairs; p += AT_THREADS) {
-    const long long c = units_of(p);
-    if (p == tid) mine0 = c;
-    total += c;
+  for (int p = tid; p < pairs; p += AT_THREADS) {
+    const int c = units_of(p);
+    if (p == tid) mine = c;
+    sum += c;
   }
-  auto block_sum = [&](long long x, long long* before) {  // sum; *before: of lower threads
-    long long v = x;
+  auto block_sum = [&](int x, int* before) {  // sum; *before: of lower threads
+    int v = x;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const long long t = __shfl_up_sync(0xffffffffu, v, d);
+      const int t = __shfl_up_sync(0xffffffffu, v, d);
       if (lane >= d) v += t;
     }
     if (lane == 31) s_sum[w] = v;
     __syncthreads();
-    long long sum = 0, pre = 0;
+    int all = 0, pre = 0;
     for (int i = 0; i < AT_THREADS / 32; ++i) {
       if (i < w) pre += s_sum[i];
-      sum += s_sum[i];
+      all += s_sum[i];
     }
-    __syncthreads();
     *before = pre + v - x;
-    return sum;
+    return all;
   };
-  long long before;
-  total = block_sum(total, &before);
-  const long long ctas = min((long long)gridDim.x, total);
-  const long long cta = blockIdx.x;
-  const long long from = cta < ctas ? cta * total / ctas : 0;
-  const long long to = cta < ctas ? (cta + 1) * total / ctas : 0;
+  int before;
+  const int total = block_sum(sum, &before);
+  const int ctas = min(static_cast<int>(gridDim.x), total), cta = blockIdx.x;
+  const int from = cta < ctas ? at_share(cta, total, ctas) : 0;
+  const int to = cta < ctas ? at_share(cta + 1, total, ctas) : 0;
   if (tid == 0) s_total = total;
   if (from < to) {
-    long long base = 0;
+    int base = 0;
 #pragma unroll 1
-    for (long long p0 = 0; p0 < pairs; p0 += AT_THREADS) {
-      const long long c = p0 == 0 ? mine0 : units_of(p0 + tid);
-      const long long sum = block_sum(c, &before);
+    for (int p0 = 0;; p0 += AT_THREADS) {
+      const int c = p0 == 0 ? mine : units_of(p0 + tid);
+      int all = total;
+      if (pairs > AT_THREADS) {  // (otherwise `before` is right already)
+        __syncthreads();
+        all = block_sum(c, &before);
+      }
       if (from >= base + before && from < base + before + c) {
-        s_b0 = static_cast<int>((p0 + tid) / nrt);
-        s_rt0 = static_cast<int>((p0 + tid) % nrt);
+        s_b0 = (p0 + tid) / nrt;
+        s_rt0 = (p0 + tid) % nrt;
         s_rem = from - base - before;
       }
-      base += sum;
+      base += all;
       if (base > from) break;
     }
   }
@@ -723,31 +741,11 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     bool ok = true;
     look();
     while (ok && n) {
-      const int count = n;
-      const int y = page >= 0 ? (page * C.heads + h) << C.lgp : -1;
-      float ks = 1.f, vs = 1.f;
-      if (used) {
-        if (page >= 0) {
-          ks = __ldg(C.ks + (layer0 + page) * C.heads + h);
-          vs = __ldg(C.vs + (layer0 + page) * C.heads + h);
-        }
-        // A page out of range, or scales outside theirs: the scores become NaN.
-        constexpr float LO = 5.421010862427522e-20f, HI = 18446744073709551616.f;  // 2^-64, 2^64
-        if (page < 0 || !(ks >= LO && ks <= HI && vs >= LO && vs <= HI)) {
-          ks = NAN;
-          vs = 1.f;
-          kv_report(A.S.hdr, ST_DEVICE_INPUT);
-        }
-      }
-      if (mt < count) {
-        const int e = (g + mt) & (AT_INFO - 1);
-        s_y[e][sub] = y;
-        s_sc[e][sub] = make_float4(ks, log2f(vs), 1.f / vs, 0.f);
-      }
-      __syncwarp();
-      look();
+      const int count = n, head = h;
+      const bool use = used;
+      const int pg = page, y = pg >= 0 ? (pg * C.heads + head) << C.lgp : -1;
       const uint32_t held = __ballot_sync(0xffffffffu, y >= 0);
-      for (int t = 0; t < count; ++t, ++g) {
+      for (int t = 0; t < count; ++t) {
         if (ph > 0 && !__all_sync(0xffffffffu, wait(&kempty[q], (ph - 1) & 1))) {
           ok = false;
           break;
@@ -755,17 +753,44 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         if (lane == 0) {
           const uint32_t pages = __popc((held >> (t * ppt)) & ((1u << ppt) - 1u));
           mbar_arrive_expect_tx(&kfull[q], (pages << C.lgp) * 128u * ndb);
-          mbar_arrive(&tinfo[g & (AT_INFO - 1)]);
         }
         __syncwarp();
         if (mt == t && y >= 0) {
           unsigned char* dst = Ks + (size_t)q * slot + ((size_t)sub << C.lgp) * 128;
           for (int db = 0; db < ndb; ++db) at_tma(dst + db * AT_BLK, &tmK, db * 128, y, &kfull[q]);
         }
+        if (t == 0) {  // the chunk's data, while its first tile is on its way
+          float ks = 1.f, vs = 1.f;
+          if (use) {
+            if (pg >= 0) {
+              ks = __ldg(C.ks + (layer0 + pg) * C.heads + head);
+              vs = __ldg(C.vs + (layer0 + pg) * C.heads + head);
+            }
+            // A page out of range, or scales outside theirs: the scores become NaN.
+            constexpr float LO = 5.421010862427522e-20f, HI = 18446744073709551616.f;  // 2^-64, 2^64
+            if (pg < 0 || !(ks >= LO && ks <= HI && vs >= LO && vs <= HI)) {
+              ks = NAN;
+              vs = 1.f;
+              kv_report(A.S.hdr, ST_DEVICE_INPUT);
+            }
+          }
+          if (mt < count) {
+            const int e = (g + mt) & (AT_INFO - 1);
+            s_y[e][sub] = y;
+            s_sc[e][sub] = make_float4(ks, log2f(vs), 1.f / vs, 0.f);
+          }
+          __syncwarp();
+        }
+        if (lane == 0) {  // (the second of kfull's arrivals: the tile's data are there)
+          mbar_arrive(&kfull[q]);
+          mbar_arrive(&tinfo[g & (AT_INFO - 1)]);
+        }
+        ++g;
         if (++q == P.nk) {
           q = 0;
           ++ph;
         }
+        if (t == 0) look();
       }
     }
     // After a wait gave up, let the copies already issued land before the CTA exits. (A
@@ -1034,6 +1059,11 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       const AtItem& it = s_item[kb];
       const int m = it.m, len = it.len;
       if (m == 0) break;
+      // Key tiles i < turn follow the row's start, the others the window; a tile is cut (some
+      // query does not see all of it) from key `cut_hi` on, and from `sinks` to `cut_lo`.
+      int kt = it.key_tile(it.i0);
+      const int turn = it.ns - it.i0, resume = it.lo;
+      const int cut_hi = len - AT_KEYS, cut_lo = A.window ? it.pos_hi - A.window + 1 : 0;
       const bool live = quad * 32 % W < it.R;  // does the warp have a query row?
       const bool real = r < it.R;
       const float cs = real ? s_c[kb][r] : 0.f;
@@ -1045,7 +1075,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       // -- Key tiles.
 #pragma unroll 1
       for (int i = 0; i < m; ++i, ++g) {
-        const int key0 = it.key_tile(it.i0 + i) * AT_KEYS;
+        if (i == turn) kt = resume;
+        const int key0 = kt * AT_KEYS;
+        ++kt;
         if (!dead && !wait(&sfull[sb], sph & 1)) dead = true;
         tm_fence_after();
         if (i == m - 1) fetch(item + 1);  // (the last scores are done: the queries' place is free)
@@ -1053,8 +1085,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         // values that weight 0 would not hide: tokens past the end (whatever the page
         // holds) are zeroed, and a NaN is zeroed where it stands and made the weight of the
         // queries that do see it.
-        const bool cut = key0 + AT_KEYS > len ||
-                         (A.window && key0 < it.pos_hi - A.window + 1 && key0 + AT_KEYS > A.sinks);
+        const bool cut = key0 > cut_hi || (key0 < cut_lo && key0 + AT_KEYS > A.sinks);
         bool vnan = false;
         if (__builtin_expect(cut, 0)) {
           // (Once the last tile's output is done, V's barriers cannot be a pass behind.)
@@ -1291,9 +1322,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       tm_fence_before();
       if (!whole) {
         // The CTAs that hold this query tile: the first of them keeps the ticket.
-        const long long all = s_total, n = min((long long)gridDim.x, all);
-        const int first = static_cast<int>(((it.u0 + 1) * n - 1) / all);
-        const int last = static_cast<int>(((it.u0 + it.tiles) * n - 1) / all);
+        const int all = s_total, n = min(static_cast<int>(gridDim.x), all);
+        const int first = at_owner(it.u0, all, n), last = at_owner(it.u0 + it.tiles - 1, all, n);
         __threadfence();
         at_bar(5, AT_SM_THREADS);
         if (st == 0) {
