@@ -618,26 +618,28 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     return mbar_try(bar, parity) || at_wait_on(bar, parity, &s_abort, A.S.hdr);
   };
 
-  if (tid == 0) {
-    for (int q = 0; q < AT_MAX_RING; ++q) {
-      mbar_init(&kfull[q], 2);
-      mbar_init(&kempty[q], 1);
-      mbar_init(&vfull[q], 1);
-      mbar_init(&vempty[q], 1);
+  if (tid < AT_INFO) {
+    mbar_init(&tinfo[tid], 1);
+    if (tid < AT_MAX_RING) {
+      mbar_init(&kfull[tid], 2);
+      mbar_init(&kempty[tid], 1);
+      mbar_init(&vfull[tid], 1);
+      mbar_init(&vempty[tid], 1);
     }
-    for (int q = 0; q < AT_INFO; ++q) mbar_init(&tinfo[q], 1);
-    for (int q = 0; q < 3; ++q) {
-      mbar_init(&sfull[q], 2);
-      mbar_init(&pfull[q], AT_SM_WARPS);
-      mbar_init(&pvdone[q], 1);
+    if (tid < 3) {
+      mbar_init(&sfull[tid], 2);
+      mbar_init(&pfull[tid], AT_SM_WARPS);
+      mbar_init(&pvdone[tid], 1);
     }
-    for (int q = 0; q < 2; ++q) {
-      mbar_init(&dfull[q], 1);
-      mbar_init(&dempty[q], AT_SM_WARPS);
-      mbar_init(&drain[q], 1);
+    if (tid < 2) {
+      mbar_init(&dfull[tid], 1);
+      mbar_init(&dempty[tid], AT_SM_WARPS);
+      mbar_init(&drain[tid], 1);
     }
-    mbar_init(&qfull, AT_SM_WARPS);
-    s_abort = 0;
+    if (tid == 0) {
+      mbar_init(&qfull, AT_SM_WARPS);
+      s_abort = 0;
+    }
     fence_mbar_init();
   }
   if (w == 1) {
