@@ -24,8 +24,14 @@ constexpr int KV_MAX_CTAS = 160;  // persistent CTAs of the attention kernel
 constexpr int KV_ROWS = 128;      // most query rows of its tile
 constexpr int KV_EXTRA = 7;       // its work per query tile beside the key tiles, in key tiles
 
+// A query tile of the attention that begins in one CTA and goes on in others, up to `last`:
+// rows r0 .. r0 + R - 1 of (row b, head h). R = 0: the CTA has none.
+struct KvOpen {
+  int b, h, r0, R, last;
+};
+
 struct KvWs {
-  size_t ticket;  // uint32 [KV_MAX_CTAS]: partial results that have arrived
+  size_t open;    // KvOpen [KV_MAX_CTAS]
   size_t table;   // int32 [batch * max_pages]
   size_t np, len, keeper, fresh, flag;  // int32 [batch] each
   size_t list;    // int32 [min(pages, batch * max_pages)]
@@ -43,7 +49,7 @@ inline KvWs kv_ws(const KvCache& C) {
     return at;
   };
   const size_t B = (size_t)C.batch, P = B * (size_t)C.max_pages;
-  W.ticket = take(4 * KV_MAX_CTAS);
+  W.open = take(sizeof(KvOpen) * KV_MAX_CTAS);
   W.table = take(4 * P);
   W.np = take(4 * B);
   W.len = take(4 * B);
@@ -59,7 +65,7 @@ inline KvWs kv_ws(const KvCache& C) {
 
 struct KvScratch {  // the same, as pointers
   WsHeader* hdr;
-  uint32_t* ticket;
+  KvOpen* open;
   int32_t *table, *np, *len, *keeper, *fresh, *flag, *list;
   float* part;
   float2* stat;

@@ -58,7 +58,7 @@ sv_status kv_open(const sv_kv_cache* c, void* ws_d, size_t ws_bytes, KvCache* C,
   C->refs = c->refs_d;
   unsigned char* ws = static_cast<unsigned char*>(ws_d);
   S->hdr = reinterpret_cast<WsHeader*>(ws);
-  S->ticket = reinterpret_cast<uint32_t*>(ws + W.ticket);
+  S->open = reinterpret_cast<KvOpen*>(ws + W.open);
   S->table = reinterpret_cast<int32_t*>(ws + W.table);
   S->np = reinterpret_cast<int32_t*>(ws + W.np);
   S->len = reinterpret_cast<int32_t*>(ws + W.len);

@@ -27,7 +27,7 @@
 //
 // A persistent CTA per SM takes an equal share of all (row, head, query tile, key tile)
 // units in order; a query tile that crosses from one CTA to the next leaves partial
-// results (output, m, sum) in the workspace, and the last of its CTAs to arrive joins them.
+// results (output, m, sum) in the workspace, which a second kernel joins on all SMs.
 //
 // Warps, coupled by mbarriers: one copies K tiles page by page by tensor-map TMA (128-byte
 // swizzle) into a ring, another V tiles into a second (and plans the next query tile while
@@ -485,88 +485,6 @@ __device__ __noinline__ void at_land(uint64_t* full, int n, int g) {
     }
 }
 
-// Joins the partial results of a query tile's CTAs first .. last (outputs, sums and
-// references) into its output. All threads of the weights; `out` has the rows' places. A
-// warp a row finds the common reference and the sum; then a thread adds four components of a
-// row over the CTAs, several loads in flight.
-__device__ __noinline__ void at_join(const AttendArgs& A, int bf16, int R, int first, int last,
-                                     const long long* out, float2* rows) {
-  const int st = threadIdx.x - AT_SM0, lane = st & 31;
-  auto slot_of = [&](int k, int r) {
-    return (size_t)(2 * k + (k == first ? 1 : 0)) * KV_ROWS + r;
-  };
-  for (int r = st >> 5; r < R; r += AT_SM_WARPS) {
-    float ref = -INFINITY, sum = 0.f;
-    for (int k = first + lane; k <= last; k += 32) {
-      const float2 s2 = __ldcg(A.S.stat + slot_of(k, r));
-      if (s2.y == 0.f) continue;
-      const float top = fmaxf(ref, s2.x);
-      sum = (sum == 0.f ? 0.f : sum * exp2f(ref - top)) + s2.y * exp2f(s2.x - top);
-      ref = top;
-    }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) {
-      const float r2 = __shfl_xor_sync(0xffffffffu, ref, d), s2 = __shfl_xor_sync(0xffffffffu, sum, d);
-      const float top = fmaxf(ref, r2);
-      sum = (sum == 0.f ? 0.f : sum * exp2f(ref - top)) + (s2 == 0.f ? 0.f : s2 * exp2f(r2 - top));
-      ref = top;
-    }
-    if (lane == 0) {
-      rows[r] = make_float2(ref, sum == 0.f ? 0.f : 1.f / sum);
-      if (A.lse)
-        A.lse[out[r]] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
-    }
-  }
-  at_bar(5, AT_SM_THREADS);
-  const int vec = A.C.dim / 4, n = R * vec;
-  constexpr int J = 2, K = 4;  // components and CTAs whose loads are in flight together
-#pragma unroll 1
-  for (int e0 = st; e0 < n; e0 += J * AT_SM_THREADS) {
-    float4 o[J];
-    int r[J], dv[J];
-    float2 row[J];
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int e = min(e0 + j * AT_SM_THREADS, n - 1);  // (the last is done again)
-      r[j] = e / vec;
-      dv[j] = e - r[j] * vec;
-      row[j] = rows[r[j]];
-      o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-#pragma unroll 1
-    for (int k0 = first; k0 <= last; k0 += K) {
-      float2 s2[J][K];
-      float4 y[J][K];
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-          const size_t sl = slot_of(min(k0 + k, last), r[j]);
-          s2[j][k] = __ldcg(A.S.stat + sl);
-          y[j][k] = __ldcg(reinterpret_cast<const float4*>(A.S.part + sl * A.C.dim) + dv[j]);
-        }
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-          const float f =
-              s2[j][k].y == 0.f || k0 + k > last ? 0.f : exp2f(s2[j][k].x - row[j].x);
-          o[j].x = fmaf(y[j][k].x, f, o[j].x);
-          o[j].y = fmaf(y[j][k].y, f, o[j].y);
-          o[j].z = fmaf(y[j][k].z, f, o[j].z);
-          o[j].w = fmaf(y[j][k].w, f, o[j].w);
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const float inv = row[j].y;
-      at_store4(A.out, out[r[j]] * A.C.dim + dv[j] * 4,
-                make_float4(o[j].x * inv, o[j].y * inv, o[j].z * inv, o[j].w * inv), bf16);
-    }
-  }
-  at_bar(5, AT_SM_THREADS);  // the rows' data are used again
-}
-
 // W: rows of a copy (32, 64 or 128 >= the query rows of a tile).
 template <int W>
 __global__ void __launch_bounds__(AT_THREADS, 1)
@@ -586,7 +504,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   __shared__ uint64_t sfull[3], pfull[3], pvdone[3], qfull, dfull[2], dempty[2], drain[2];
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
-  __shared__ int s_b0, s_rt0, s_rem, s_total, s_last, s_sum[AT_THREADS / 32];
+  __shared__ int s_b0, s_rt0, s_rem, s_total, s_sum[AT_THREADS / 32];
   // Per key tile and page of it: row of the pool (-1: none); key scale, log2 and inverse of
   // the value scale.
   __shared__ int s_y[AT_INFO][8];
@@ -1052,6 +970,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     fetch(0);
     convert(0);
     int g = 0, q = 0, ph = 0;
+    bool opened = false;  // does a query tile that begins here go on in the next CTA?
     for (int item = 0;; ++item) {
       const int kb = item & 1;
       if (!dead && !wait(&qfull, item & 1)) dead = true;
@@ -1322,26 +1241,18 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         at_bar(5, AT_SM_THREADS);
       }
       tm_fence_before();
-      if (!whole) {
-        // The CTAs that hold this query tile: the first of them keeps the ticket.
-        const int all = s_total, n = min(static_cast<int>(gridDim.x), all);
-        const int first = at_owner(it.u0, all, n), last = at_owner(it.u0 + it.tiles - 1, all, n);
-        __threadfence();
-        at_bar(5, AT_SM_THREADS);
+      if (!whole && it.i0 == 0) {  // the first of the CTAs that hold this query tile
+        opened = true;
         if (st == 0) {
-          const bool end = atomicAdd(A.S.ticket + first, 1u) == static_cast<uint32_t>(last - first);
-          if (end) A.S.ticket[first] = 0;
-          s_last = end;
-        }
-        at_bar(5, AT_SM_THREADS);
-        if (s_last) {
-          __threadfence();
-          at_join(A, P.bf16, it.R, first, last, s_out[kb], s_stat);
+          const int all = s_total, n = min(static_cast<int>(gridDim.x), all);
+          A.S.open[blockIdx.x] =
+              KvOpen{it.b, it.h, it.r0, it.R, at_owner(it.u0 + it.tiles - 1, all, n)};
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&dempty[kb]);
     }
+    if (!opened && st == 0) A.S.open[blockIdx.x].R = 0;
   }
 
   tm_fence_before();
@@ -1351,6 +1262,64 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     tm_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
                  : "memory");
+  }
+}
+
+// Joins the partial results of the query tile that begins in CTA blockIdx.x and goes on in
+// others: a thread takes four components of a row over its CTAs, with the loads of four of
+// them in flight and a running reference. (A join by the last of the CTAs themselves held
+// up its SM for up to 27 us: 128 rows of 256 components are 128 KB a CTA.)
+constexpr int JOIN_THREADS = 256, JOIN_BLOCKS = 8;  // and blocks of a query tile
+__global__ void __launch_bounds__(JOIN_THREADS)
+    kv_attend_join_kernel(const __grid_constant__ AttendArgs A, int bf16) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int first = blockIdx.x;
+  const KvOpen it = A.S.open[first];
+  const int vec = A.C.dim / 4, n = it.R * vec;
+  constexpr int K = 4;
+  for (int e = blockIdx.y * JOIN_THREADS + threadIdx.x; e < n; e += JOIN_BLOCKS * JOIN_THREADS) {
+    const int r = e / vec, dv = e - r * vec;
+    float ref = -INFINITY, sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = first; k0 <= it.last; k0 += K) {
+      float2 s2[K];
+      float4 y[K];
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int kk = min(k0 + k, it.last);
+        const size_t sl = (size_t)(2 * kk + (kk == first ? 1 : 0)) * KV_ROWS + r;
+        s2[k] = __ldcg(A.S.stat + sl);
+        y[k] = __ldcg(reinterpret_cast<const float4*>(A.S.part + sl * A.C.dim) + dv);
+      }
+      float top = ref;
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (s2[k].y != 0.f) top = fmaxf(top, s2[k].x);
+      const float f0 = sum == 0.f ? 0.f : exp2f(ref - top);
+      ref = top;
+      sum *= f0;
+      o.x *= f0;
+      o.y *= f0;
+      o.z *= f0;
+      o.w *= f0;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (s2[k].y == 0.f || k0 + k > it.last) continue;
+        const float f = exp2f(s2[k].x - top);
+        sum = fmaf(s2[k].y, f, sum);
+        o.x = fmaf(y[k].x, f, o.x);
+        o.y = fmaf(y[k].y, f, o.y);
+        o.z = fmaf(y[k].z, f, o.z);
+        o.w = fmaf(y[k].w, f, o.w);
+      }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int t = (it.r0 + r) / A.group, gh = it.r0 + r - t * A.group;
+    const long long row = ((long long)it.b * A.T + t) * A.q_heads + it.h * A.group + gh;
+    at_store4(A.out, row * A.C.dim + dv * 4,
+              make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv), bf16);
+    if (dv == 0 && A.lse)
+      A.lse[row] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
   }
 }
 
@@ -1426,7 +1395,18 @@ cudaError_t launch_kv_attend(const AttendArgs& A, sv_dtype dt, cudaStream_t st) 
     kv_attend_kernel<64><<<grid, AT_THREADS, smem, st>>>(A, P, tm[0], tm[1]);
   else
     kv_attend_kernel<128><<<grid, AT_THREADS, smem, st>>>(A, P, tm[0], tm[1]);
-  return cudaGetLastError();
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  // The join's blocks are brought up while the first kernel ends, and wait for it.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, JOIN_BLOCKS);
+  cfg.blockDim = dim3(JOIN_THREADS);
+  cfg.stream = st;
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_attend_join_kernel, A, P.bf16);
 }
 
 }  // namespace sv
