@@ -413,7 +413,7 @@ class KVCache:
         self.refs = torch.zeros(c.pages, **i32)
         for n in ("k", "v", "k_scale", "v_scale", "table", "n_pages", "len", "refs"):
             setattr(c, n, getattr(self, n).data_ptr())
-        self.c = c
+        self.c, self.ref = c, ctypes.byref(c)
         self.buf = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=dev)
         off = (-self.buf.data_ptr()) % 256
         self.t = self.buf[off: off + self.nbytes]
@@ -422,7 +422,21 @@ class KVCache:
         # Everything above must be complete before a call on any other stream uses it.
         torch.cuda.synchronize(self.t.device)
 
+        self.ws = self.t.data_ptr()
+
     status = Workspace.status
+
+
+# The cache's calls are made for every layer of every step, so their marshalling is kept
+# short: plain integers for pointers, the current stream without a Python object for it.
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _kv_stream(stream, device):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index or 0)
 
 
 def _kv_src(t, name, cache, heads):
@@ -463,8 +477,8 @@ def sv_kv_reserve(cache: KVCache, n_new, ok=None, stream=None):
     int32, when given, receives 1 per row served. Returns ok."""
     _kv_counts(n_new, "n_new", cache)
     _kv_counts(ok, "ok", cache)
-    _check("sv_kv_reserve", load().sv_kv_reserve(ctypes.byref(cache.c), _ptr(n_new), _ptr(ok),
-                                                 _ptr(cache.t), cache.nbytes, _stream(stream)))
+    _check("sv_kv_reserve", load().sv_kv_reserve(cache.ref, _addr(n_new), _addr(ok),
+                                                 cache.ws, cache.nbytes, _kv_stream(stream, cache.t.device)))
     return ok
 
 
@@ -477,8 +491,8 @@ def sv_kv_append(cache: KVCache, layer, k, v, n_new=None, stream=None):
         raise ValueError("k and v must have one shape and dtype")
     _kv_counts(n_new, "n_new", cache)
     _check("sv_kv_append", load().sv_kv_append(
-        ctypes.byref(cache.c), int(layer), _ptr(k), _ptr(v), _kv_dtype(k, "k"), k_row, k_tok,
-        v_row, v_tok, T, _ptr(n_new), _ptr(cache.t), cache.nbytes, _stream(stream)))
+        cache.ref, int(layer), _addr(k), _addr(v), _kv_dtype(k, "k"), k_row, k_tok,
+        v_row, v_tok, T, _addr(n_new), cache.ws, cache.nbytes, _kv_stream(stream, cache.t.device)))
 
 
 def sv_kv_read(cache: KVCache, start, T, count=None, layer=0, n_layers=None,
@@ -500,8 +514,8 @@ def sv_kv_read(cache: KVCache, start, T, count=None, layer=0, n_layers=None,
         if tuple(t.shape) != shape:
             raise ValueError(f"{name} must be {list(shape)}")
     _check("sv_kv_read", load().sv_kv_read(
-        ctypes.byref(c), int(layer), int(n_layers), _ptr(start), _ptr(count), int(T), _ptr(k_out),
-        _ptr(v_out), _kv_dtype(k_out, "k_out"), _ptr(cache.t), cache.nbytes, _stream(stream)))
+        cache.ref, int(layer), int(n_layers), _addr(start), _addr(count), int(T), _addr(k_out),
+        _addr(v_out), _kv_dtype(k_out, "k_out"), cache.ws, cache.nbytes, _kv_stream(stream, cache.t.device)))
     return k_out, v_out
 
 
@@ -527,9 +541,9 @@ def sv_kv_attend(cache: KVCache, layer, q, n_new=None, parent=None, scale=None, 
     if out.shape != q.shape or (lse is not None and lse.shape != q.shape[:3]):
         raise ValueError("out must have q's shape, lse its first three dimensions")
     _check("sv_kv_attend", load().sv_kv_attend(
-        ctypes.byref(c), int(layer), _ptr(q), _kv_dtype(q, "q"), row, tok, T, Hq, _ptr(n_new),
-        _ptr(parent), float(c.dim ** -0.5 if scale is None else scale), int(window), int(sinks),
-        _ptr(out), _ptr(lse), _ptr(cache.t), cache.nbytes, _stream(stream)))
+        cache.ref, int(layer), _addr(q), _kv_dtype(q, "q"), row, tok, T, Hq, _addr(n_new),
+        _addr(parent), float(c.dim ** -0.5 if scale is None else scale), int(window), int(sinks),
+        _addr(out), _addr(lse), cache.ws, cache.nbytes, _kv_stream(stream, cache.t.device)))
     return out if lse is None else (out, lse)
 
 
@@ -543,8 +557,8 @@ def sv_kv_commit(cache: KVCache, accepted, N, path=None, stream=None):
         if tuple(path.shape) != (cache.c.batch, int(N)):
             raise ValueError(f"path must be [{cache.c.batch}, {int(N)}]")
     _check("sv_kv_commit", load().sv_kv_commit(
-        ctypes.byref(cache.c), _ptr(accepted), _ptr(path), int(N), _ptr(cache.t), cache.nbytes,
-        _stream(stream)))
+        cache.ref, _addr(accepted), _addr(path), int(N), cache.ws, cache.nbytes,
+        _kv_stream(stream, cache.t.device)))
 
 
 def sv_kv_fork(cache: KVCache, src, ok=None, stream=None):
@@ -553,6 +567,6 @@ def sv_kv_fork(cache: KVCache, src, ok=None, stream=None):
     ok."""
     _kv_counts(src, "src", cache)
     _kv_counts(ok, "ok", cache)
-    _check("sv_kv_fork", load().sv_kv_fork(ctypes.byref(cache.c), _ptr(src), _ptr(ok),
-                                           _ptr(cache.t), cache.nbytes, _stream(stream)))
+    _check("sv_kv_fork", load().sv_kv_fork(cache.ref, _addr(src), _addr(ok),
+                                           cache.ws, cache.nbytes, _kv_stream(stream, cache.t.device)))
     return ok

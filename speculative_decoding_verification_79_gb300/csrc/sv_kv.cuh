@@ -151,6 +151,30 @@ struct AttendArgs {
   float* lse;
 };
 
+// Every kernel of the cache is launched with programmatic stream serialization: it may be
+// brought up while the kernel before it in the stream ends, and first waits for that one's
+// completion (kv_enter), so that its results and all earlier ones are there. It lets the
+// next one be brought up at once.
+__device__ __forceinline__ void kv_enter() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <typename... P>
+cudaError_t kv_launch(void (*kernel)(P...), dim3 grid, int block, size_t smem, cudaStream_t st,
+                      P... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 cudaError_t launch_kv_reserve(const KvCache& C, const KvScratch& S, const int32_t* n_new,
                               int32_t* ok, cudaStream_t st);
 cudaError_t launch_kv_fork(const KvCache& C, const KvScratch& S, const int32_t* src, int32_t* ok,

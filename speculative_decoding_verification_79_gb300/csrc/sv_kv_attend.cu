@@ -567,6 +567,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  kv_enter();
   // This CTA's share: the units of all rows' query tiles, cut into equal parts. Query tiles
   // are counted by the threads in turn; the second pass finds the one where the share begins.
   const int nrt = (A.T * A.group + KV_ROWS - 1) / KV_ROWS, pairs = C.batch * nrt;
@@ -1272,7 +1273,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
 constexpr int JOIN_THREADS = 256, JOIN_BLOCKS = 8;  // and blocks of a query tile
 __global__ void __launch_bounds__(JOIN_THREADS)
     kv_attend_join_kernel(const __grid_constant__ AttendArgs A, int bf16) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  kv_enter();
   const int first = blockIdx.x;
   const KvOpen it = A.S.open[first];
   const int vec = A.C.dim / 4, n = it.R * vec;
@@ -1389,24 +1390,11 @@ cudaError_t launch_kv_attend(const AttendArgs& A, sv_dtype dt, cudaStream_t st) 
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
     return e;
   const int grid = sms < KV_MAX_CTAS ? sms : KV_MAX_CTAS;
-  if (width == 32)
-    kv_attend_kernel<32><<<grid, AT_THREADS, smem, st>>>(A, P, tm[0], tm[1]);
-  else if (width == 64)
-    kv_attend_kernel<64><<<grid, AT_THREADS, smem, st>>>(A, P, tm[0], tm[1]);
-  else
-    kv_attend_kernel<128><<<grid, AT_THREADS, smem, st>>>(A, P, tm[0], tm[1]);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  // The join's blocks are brought up while the first kernel ends, and wait for it.
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, JOIN_BLOCKS);
-  cfg.blockDim = dim3(JOIN_THREADS);
-  cfg.stream = st;
-  cudaLaunchAttribute pdl[1];
-  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  pdl[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = pdl;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_attend_join_kernel, A, P.bf16);
+  const auto kernel = width == 32 ? kv_attend_kernel<32>
+                                  : (width == 64 ? kv_attend_kernel<64> : kv_attend_kernel<128>);
+  if ((e = kv_launch(kernel, dim3(grid), AT_THREADS, smem, st, A, P, tm[0], tm[1])) != cudaSuccess)
+    return e;
+  return kv_launch(kv_attend_join_kernel, dim3(grid, JOIN_BLOCKS), JOIN_THREADS, 0, st, A, P.bf16);
 }
 
 }  // namespace sv

@@ -61,8 +61,9 @@ __device__ int find_free(const KvCache& C, int want, int32_t* list, int* sh) {
 }
 
 __global__ void __launch_bounds__(PG_THREADS, 1)
-    kv_reserve_kernel(const KvCache C, const KvScratch S, const int32_t* __restrict__ n_new,
+    kv_reserve_kernel(const KvCache C, const KvScratch S, const int32_t* n_new,
                       int32_t* ok) {
+  kv_enter();
   __shared__ int sh[64];
   __shared__ long long shl[64];
   extern __shared__ int end[];  // [batch] pages needed by rows 0 .. b, cut at pages + 1
@@ -130,7 +131,8 @@ __device__ __forceinline__ int fork_src(const KvCache& C, const int32_t* src, in
 }
 
 __global__ void __launch_bounds__(128)
-    kv_fork_count_kernel(const KvCache C, const KvScratch S, const int32_t* __restrict__ src) {
+    kv_fork_count_kernel(const KvCache C, const KvScratch S, const int32_t* src) {
+  kv_enter();
   __shared__ int s_m, s_first;
   const int i = blockIdx.x, tid = threadIdx.x;
   if (tid == 0) {
@@ -175,8 +177,9 @@ __global__ void __launch_bounds__(128)
 }
 
 __global__ void __launch_bounds__(PG_THREADS, 1)
-    kv_fork_alloc_kernel(const KvCache C, const KvScratch S, const int32_t* __restrict__ src,
+    kv_fork_alloc_kernel(const KvCache C, const KvScratch S, const int32_t* src,
                          int32_t* ok) {
+  kv_enter();
   __shared__ int sh[64];
   const int tid = threadIdx.x;
   int all = 0;
@@ -216,7 +219,8 @@ __global__ void __launch_bounds__(PG_THREADS, 1)
 
 // grid (x: shares of the (layer, head) pairs, y: new rows)
 __global__ void __launch_bounds__(128)
-    kv_fork_write_kernel(const KvCache C, const KvScratch S, const int32_t* __restrict__ src) {
+    kv_fork_write_kernel(const KvCache C, const KvScratch S, const int32_t* src) {
+  kv_enter();
   const int b = blockIdx.y, tid = threadIdx.x;
   const int s = fork_src(C, src, b);
   if (s == b) return;  // the row itself: nothing of it changes (it keeps its partial page)
@@ -297,8 +301,9 @@ __device__ bool commit_ok(const KvCache& C, int b, int acc, const int32_t* path,
 
 // grid (x: shares of the (layer, head) pairs, y: rows)
 __global__ void __launch_bounds__(CM_THREADS)
-    kv_commit_move_kernel(const KvCache C, const KvScratch S, const int32_t* __restrict__ accepted,
-                          const int32_t* __restrict__ path, int N) {
+    kv_commit_move_kernel(const KvCache C, const KvScratch S, const int32_t* accepted,
+                          const int32_t* path, int N) {
+  kv_enter();
   const int b = blockIdx.y, tid = threadIdx.x;
   __shared__ int s_moves;
   __shared__ int s_src[SV_MAX_TREE], s_dst[SV_MAX_TREE];      // page of each kept token
@@ -390,7 +395,8 @@ __global__ void __launch_bounds__(CM_THREADS)
 
 __global__ void __launch_bounds__(CM_THREADS)
     kv_commit_release_kernel(const KvCache C, const KvScratch S,
-                             const int32_t* __restrict__ accepted) {
+                             const int32_t* accepted) {
+  kv_enter();
   const int b = blockIdx.x, tid = threadIdx.x;
   __shared__ int s_len, s_np;
   if (tid == 0) {
@@ -419,8 +425,7 @@ __global__ void __launch_bounds__(CM_THREADS)
 
 cudaError_t launch_kv_reserve(const KvCache& C, const KvScratch& S, const int32_t* n_new,
                               int32_t* ok, cudaStream_t st) {
-  kv_reserve_kernel<<<1, PG_THREADS, 4 * (size_t)C.batch, st>>>(C, S, n_new, ok);
-  return cudaGetLastError();
+  return kv_launch(kv_reserve_kernel, dim3(1), PG_THREADS, 4 * (size_t)C.batch, st, C, S, n_new, ok);
 }
 
 // Shares of the (layer, head) pairs per row: enough CTAs to fill the GPU a few times over.
@@ -431,11 +436,12 @@ static int shares(const KvCache& C, int pairs) {
 
 cudaError_t launch_kv_fork(const KvCache& C, const KvScratch& S, const int32_t* src, int32_t* ok,
                            cudaStream_t st) {
-  kv_fork_count_kernel<<<C.batch, 128, 0, st>>>(C, S, src);
-  kv_fork_alloc_kernel<<<1, PG_THREADS, 0, st>>>(C, S, src, ok);
+  cudaError_t e = kv_launch(kv_fork_count_kernel, dim3(C.batch), 128, 0, st, C, S, src);
+  if (e != cudaSuccess) return e;
+  e = kv_launch(kv_fork_alloc_kernel, dim3(1), PG_THREADS, 0, st, C, S, src, ok);
+  if (e != cudaSuccess) return e;
   const dim3 grid(shares(C, C.layers * C.heads), C.batch);
-  kv_fork_write_kernel<<<grid, 128, 0, st>>>(C, S, src);
-  return cudaGetLastError();
+  return kv_launch(kv_fork_write_kernel, grid, 128, 0, st, C, S, src);
 }
 
 cudaError_t launch_kv_commit(const KvCache& C, const KvScratch& S, const int32_t* acc,
@@ -443,9 +449,9 @@ cudaError_t launch_kv_commit(const KvCache& C, const KvScratch& S, const int32_t
   // A chain moves nothing: one CTA per row checks it.
   const dim3 grid(path ? shares(C, 2 * C.layers * C.heads) : 1, C.batch);
   const size_t smem = path ? (size_t)N * C.dim : 0;
-  kv_commit_move_kernel<<<grid, CM_THREADS, smem, st>>>(C, S, acc, path, N);
-  kv_commit_release_kernel<<<C.batch, CM_THREADS, 0, st>>>(C, S, acc);
-  return cudaGetLastError();
+  const cudaError_t e = kv_launch(kv_commit_move_kernel, grid, CM_THREADS, smem, st, C, S, acc, path, N);
+  if (e != cudaSuccess) return e;
+  return kv_launch(kv_commit_release_kernel, dim3(C.batch), CM_THREADS, 0, st, C, S, acc);
 }
 
 }  // namespace sv

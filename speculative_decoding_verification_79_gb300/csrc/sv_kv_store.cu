@@ -87,19 +87,37 @@ __device__ __forceinline__ uint4 quantise16(const float* f, float inv) {
 template <typename E>
 __global__ void __launch_bounds__(AP_THREADS)
     kv_append_kernel(const KvCache C, const KvScratch S, int layer, const KvSrc ksrc,
-                     const KvSrc vsrc, int T, const int32_t* __restrict__ n_new) {
+                     const KvSrc vsrc, int T, const int32_t* n_new) {
+  kv_enter();
   __shared__ float s_max[AP_THREADS / 32];
   const int b = blockIdx.z, h = blockIdx.y, tid = threadIdx.x;
   const int n = n_new ? __ldg(n_new + b) : T;
   if (n == 0) return;
   const int len = __ldg(C.len + b);
   const bool sane = n > 0 && n <= T && len >= 0 && ((long long)len + n - 1) >> C.lgp < C.max_pages;
+  const int half = tid / AP_HALF, t0 = tid - half * AP_HALF;
+  const KvSrc src = half ? vsrc : ksrc;
+  const int j0 = sane ? len >> C.lgp : 0, j = j0 + blockIdx.x;
+  const int lo = max(len, j << C.lgp), hi = sane ? min(len + n, (j + 1) << C.lgp) : 0;
+  const int vpt = C.dim / 16, nv = max(0, hi - lo) * vpt, off = lo - (j << C.lgp);
+  const E* base = static_cast<const E*>(src.p) + b * src.row + (lo - len) * src.tok +
+                  (size_t)h * C.dim;
+  auto at = [&](int i) {
+    const int t = i / vpt, c = i - t * vpt;
+    return base + t * src.tok + c * 16;
+  };
+  // The values are on their way while the row's pages are looked up.
+  Vec16<E> keep[AP_CACHE];
+#pragma unroll
+  for (int r = 0; r < AP_CACHE; ++r) {
+    const int i = t0 + r * AP_HALF;
+    if (i < nv) keep[r].load(at(i));
+  }
   bool fine = sane;
-  const int j0 = len >> C.lgp;
   if (sane) {  // every page that the row writes is its own
     const int j1 = (len + n - 1) >> C.lgp;
-    for (int j = j0 + tid; j <= j1; j += AP_THREADS) {
-      const int p = kv_page(C, b, j << C.lgp);
+    for (int jj = j0 + tid; jj <= j1; jj += AP_THREADS) {
+      const int p = kv_page(C, b, jj << C.lgp);
       fine = fine && p >= 0 && __ldg(C.refs + p) == 1;
     }
   }
@@ -107,18 +125,10 @@ __global__ void __launch_bounds__(AP_THREADS)
     if (tid == 0 && h == 0 && blockIdx.x == 0) kv_report(S.hdr, ST_DEVICE_INPUT);
     return;
   }
-  const int j = j0 + blockIdx.x;
-  const int lo = max(len, j << C.lgp), hi = min(len + n, (j + 1) << C.lgp);
   if (hi <= lo) return;
   const int p = kv_page(C, b, j << C.lgp);
-  const int half = tid / AP_HALF, t0 = tid - half * AP_HALF;
-  const KvSrc src = half ? vsrc : ksrc;
-  const int vpt = C.dim / 16, nv = (hi - lo) * vpt, off = lo - (j << C.lgp);
-  const E* base = static_cast<const E*>(src.p) + b * src.row + (lo - len) * src.tok +
-                  (size_t)h * C.dim;
   uint8_t* dst = (half ? C.v : C.k) + kv_block(C, layer, p, h);
   float* scale = (half ? C.vs : C.ks) + kv_sidx(C, layer, p, h);
-  Vec16<E> keep[AP_CACHE];
   float a = 0.f;
   bool odd = false;  // a value outside the scales' range
   auto see = [&](const Vec16<E>& x) {
@@ -133,15 +143,6 @@ __global__ void __launch_bounds__(AP_THREADS)
         odd = true;
     }
   };
-  auto at = [&](int i) {
-    const int t = i / vpt, c = i - t * vpt;
-    return base + t * src.tok + c * 16;
-  };
-#pragma unroll
-  for (int r = 0; r < AP_CACHE; ++r) {
-    const int i = t0 + r * AP_HALF;
-    if (i < nv) keep[r].load(at(i));
-  }
 #pragma unroll
   for (int r = 0; r < AP_CACHE; ++r)
     if (t0 + r * AP_HALF < nv) see(keep[r]);
@@ -200,8 +201,9 @@ __global__ void __launch_bounds__(AP_THREADS)
 // One thread per 16 values; grid (x: vectors of one row and layer, y: rows, z: layers).
 template <bool BF16>
 __global__ void __launch_bounds__(256)
-    kv_read_kernel(const KvCache C, int layer0, const int32_t* __restrict__ start,
-                   const int32_t* __restrict__ count, int T, void* ko, void* vo) {
+    kv_read_kernel(const KvCache C, int layer0, const int32_t* start,
+                   const int32_t* count, int T, void* ko, void* vo) {
+  kv_enter();
   const int b = blockIdx.y, layer = layer0 + blockIdx.z;
   const int vpt = C.dim / 16;
   const int i = blockIdx.x * blockDim.x + threadIdx.x;
@@ -256,13 +258,10 @@ cudaError_t launch_kv_append(const KvCache& C, const KvScratch& S, int layer, Kv
                              sv_dtype dt, int T, const int32_t* n_new, cudaStream_t st) {
   // A row's tokens start anywhere in a page, so T of them touch at most this many.
   const dim3 grid((T + C.page - 2) / C.page + 1, C.heads, C.batch);
-  if (dt == SV_F32)
-    kv_append_kernel<float><<<grid, AP_THREADS, 0, st>>>(C, S, layer, k, v, T, n_new);
-  else if (dt == SV_BF16)
-    kv_append_kernel<__nv_bfloat16><<<grid, AP_THREADS, 0, st>>>(C, S, layer, k, v, T, n_new);
-  else
-    kv_append_kernel<__half><<<grid, AP_THREADS, 0, st>>>(C, S, layer, k, v, T, n_new);
-  return cudaGetLastError();
+  const auto kernel = dt == SV_F32    ? kv_append_kernel<float>
+                      : dt == SV_BF16 ? kv_append_kernel<__nv_bfloat16>
+                                      : kv_append_kernel<__half>;
+  return kv_launch(kernel, grid, AP_THREADS, 0, st, C, S, layer, k, v, T, n_new);
 }
 
 cudaError_t launch_kv_read(const KvCache& C, const KvScratch&, int layer, int n_layers,
@@ -270,11 +269,8 @@ cudaError_t launch_kv_read(const KvCache& C, const KvScratch&, int layer, int n_
                            sv_dtype dt, cudaStream_t st) {
   const long long vecs = (long long)T * C.heads * (C.dim / 16);
   const dim3 grid(static_cast<unsigned>((vecs + 255) / 256), C.batch, n_layers);
-  if (dt == SV_BF16)
-    kv_read_kernel<true><<<grid, 256, 0, st>>>(C, layer, start, count, T, ko, vo);
-  else
-    kv_read_kernel<false><<<grid, 256, 0, st>>>(C, layer, start, count, T, ko, vo);
-  return cudaGetLastError();
+  const auto kernel = dt == SV_BF16 ? kv_read_kernel<true> : kv_read_kernel<false>;
+  return kv_launch(kernel, grid, 256, 0, st, C, layer, start, count, T, ko, vo);
 }
 
 }  // namespace sv
