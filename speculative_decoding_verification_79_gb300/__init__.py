@@ -423,6 +423,8 @@ class KVCache:
         torch.cuda.synchronize(self.t.device)
 
         self.ws = self.t.data_ptr()
+        self.__dict__.update(sizes)  # layers, pages, page, heads, dim, batch, max_pages
+        self.rows = (c.batch,)
 
     status = Workspace.status
 
@@ -440,36 +442,39 @@ def _kv_stream(stream, device):
 
 
 def _kv_src(t, name, cache, heads):
-    """A [batch, T, heads, dim] tensor whose last two dimensions are dense: (T, element
-    strides of rows and tokens)."""
+    """A [batch, T, heads, dim] tensor whose last two dimensions are dense: its shape, and
+    the element strides of rows and tokens."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    c = cache.c
-    if t.dim() != 4 or t.shape[0] != c.batch or t.shape[3] != c.dim or \
-            (heads is not None and t.shape[2] != heads):
-        raise ValueError(f"{name} must be [{c.batch}, T, {heads or 'q_heads'}, {c.dim}], got "
-                         f"{list(t.shape)}")
-    if t.stride(3) != 1 or (t.shape[2] > 1 and t.stride(2) != c.dim):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 4 or shape[0] != cache.batch or shape[3] != cache.dim or \
+            (heads is not None and shape[2] != heads):
+        raise ValueError(f"{name} must be [{cache.batch}, T, {heads or 'q_heads'}, {cache.dim}], "
+                         f"got {list(shape)}")
+    if stride[3] != 1 or (shape[2] > 1 and stride[2] != shape[3]):
         raise ValueError(f"{name}: heads and dim must be contiguous")
     # Strides of dimensions of one element are free in torch: use the dense ones.
-    tok = t.stride(1) if t.shape[1] > 1 else t.shape[2] * c.dim
-    row = t.stride(0) if t.shape[0] > 1 else t.shape[1] * tok
-    return t.shape[1], row, tok
+    tok = stride[1] if shape[1] > 1 else shape[2] * shape[3]
+    row = stride[0] if shape[0] > 1 else shape[1] * tok
+    return shape, row, tok
 
 
 def _kv_counts(t, name, cache):
     if t is not None:
         _dev(t, name, torch.int32)
-        if tuple(t.shape) != (cache.c.batch,):
-            raise ValueError(f"{name} must be [{cache.c.batch}]")
+        if t.shape != cache.rows:
+            raise ValueError(f"{name} must be [{cache.batch}]")
     return t
 
 
+_KV_DTYPES = {torch.float32: SV_F32, torch.bfloat16: SV_BF16, torch.float16: SV_F16}
+
+
 def _kv_dtype(t, name):
-    try:
-        return {torch.float32: SV_F32, torch.bfloat16: SV_BF16, torch.float16: SV_F16}[t.dtype]
-    except KeyError:
-        raise ValueError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}") from None
+    code = _KV_DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+    return code
 
 
 def sv_kv_reserve(cache: KVCache, n_new, ok=None, stream=None):
@@ -485,14 +490,14 @@ def sv_kv_reserve(cache: KVCache, n_new, ok=None, stream=None):
 def sv_kv_append(cache: KVCache, layer, k, v, n_new=None, stream=None):
     """Write the new tokens' keys and values [batch, T, heads, dim] (bf16, fp16 or fp32;
     slices of a fused projection are fine) into one layer (see specverify.h)."""
-    T, k_row, k_tok = _kv_src(k, "k", cache, cache.c.heads)
-    Tv, v_row, v_tok = _kv_src(v, "v", cache, cache.c.heads)
-    if T != Tv or k.dtype != v.dtype:
+    shape, k_row, k_tok = _kv_src(k, "k", cache, cache.heads)
+    v_shape, v_row, v_tok = _kv_src(v, "v", cache, cache.heads)
+    if shape != v_shape or k.dtype != v.dtype:
         raise ValueError("k and v must have one shape and dtype")
     _kv_counts(n_new, "n_new", cache)
     _check("sv_kv_append", load().sv_kv_append(
         cache.ref, int(layer), _addr(k), _addr(v), _kv_dtype(k, "k"), k_row, k_tok,
-        v_row, v_tok, T, _addr(n_new), cache.ws, cache.nbytes, _kv_stream(stream, cache.t.device)))
+        v_row, v_tok, shape[1], _addr(n_new), cache.ws, cache.nbytes, _kv_stream(stream, cache.t.device)))
 
 
 def sv_kv_read(cache: KVCache, start, T, count=None, layer=0, n_layers=None,
@@ -524,25 +529,25 @@ def sv_kv_attend(cache: KVCache, layer, q, n_new=None, parent=None, scale=None, 
     """Attention of the new tokens' queries [batch, T, q_heads, dim] (bf16 or fp16) over one
     layer of the cache (see specverify.h); scale defaults to dim ** -0.5. Returns out, or
     (out, lse) when lse is given or wanted."""
-    c = cache.c
-    T, row, tok = _kv_src(q, "q", cache, None)
-    Hq = q.shape[2]
+    shape, row, tok = _kv_src(q, "q", cache, None)
+    T, heads = shape[1], shape[2]
     _kv_counts(n_new, "n_new", cache)
     if parent is not None:
         _dev(parent, "parent", torch.int32)
-        if tuple(parent.shape) != (c.batch, T):
-            raise ValueError(f"parent must be [{c.batch}, {T}]")
+        if parent.shape != shape[:2]:
+            raise ValueError(f"parent must be [{cache.batch}, {T}]")
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    _dev(out, "out", q.dtype)
-    if lse is None and want_lse:
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
-    _dev(lse, "lse", torch.float32)
-    if out.shape != q.shape or (lse is not None and lse.shape != q.shape[:3]):
-        raise ValueError("out must have q's shape, lse its first three dimensions")
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+    elif _dev(out, "out", q.dtype).shape != shape:
+        raise ValueError("out must have q's shape")
+    if lse is not None:
+        if _dev(lse, "lse", torch.float32).shape != shape[:3]:
+            raise ValueError("lse must have q's first three dimensions")
+    elif want_lse:
+        lse = torch.empty(shape[:3], dtype=torch.float32, device=q.device)
     _check("sv_kv_attend", load().sv_kv_attend(
-        cache.ref, int(layer), _addr(q), _kv_dtype(q, "q"), row, tok, T, Hq, _addr(n_new),
-        _addr(parent), float(c.dim ** -0.5 if scale is None else scale), int(window), int(sinks),
+        cache.ref, int(layer), _addr(q), _kv_dtype(q, "q"), row, tok, T, heads, _addr(n_new),
+        _addr(parent), float(cache.dim ** -0.5 if scale is None else scale), int(window), int(sinks),
         _addr(out), _addr(lse), cache.ws, cache.nbytes, _kv_stream(stream, cache.t.device)))
     return out if lse is None else (out, lse)
 
@@ -554,8 +559,8 @@ def sv_kv_commit(cache: KVCache, accepted, N, path=None, stream=None):
     _kv_counts(accepted, "accepted", cache)
     if path is not None:
         _dev(path, "path", torch.int32)
-        if tuple(path.shape) != (cache.c.batch, int(N)):
-            raise ValueError(f"path must be [{cache.c.batch}, {int(N)}]")
+        if path.shape != (cache.batch, int(N)):
+            raise ValueError(f"path must be [{cache.batch}, {int(N)}]")
     _check("sv_kv_commit", load().sv_kv_commit(
         cache.ref, _addr(accepted), _addr(path), int(N), cache.ws, cache.nbytes,
         _kv_stream(stream, cache.t.device)))
