@@ -458,7 +458,8 @@ sv_status sv_kv_read(const sv_kv_cache *cache, int layer, int n_layers, const in
  *             tokens q_row / q_tok elements apart (multiples of 16 bytes). q_heads is a
  *             multiple of heads, at most 128 times as many: query head h reads key/value
  *             head h / (q_heads / heads). batch * heads * ceil(T * q_heads / heads / 128) *
- *             (max_pages * page / 128 + 8) stays below 2^31.
+ *             (max_pages * page / 128 + 8) stays below 2^31, max_pages * page at most
+ *             2^31 - 256.
  *  n_new_d    [batch] int32 in [0, T], or NULL for T everywhere.
  *  parent_d   [batch, T] int32 or NULL. NULL: the new tokens are a chain. Otherwise a
  *             draft tree as in sv_verify_tree: parent of node i >= 1 in [0, i), entry 0
@@ -472,7 +473,10 @@ sv_status sv_kv_read(const sv_kv_cache *cache, int layer, int n_layers, const in
  * Query t of a row sees the cached tokens and, of the new ones, its ancestors and itself
  * (a chain: those up to t), as far as window and sinks allow. Scores, maximum, sum and
  * output are accumulated in float32. Queries t >= n_new get 0 (lse -inf). A row with a
- * bad count, tree or pages gets NaN in out and lse and sets SV_ERR_DEVICE_INPUT.
+ * bad count or tree gets NaN in out and lse and sets SV_ERR_DEVICE_INPUT; a page that is
+ * missing, out of range or has a scale outside [2^-64, 2^64] sets it too and gives NaN to
+ * the queries that see a token of it. A NaN stored in the cache gives NaN to the queries
+ * that see it and to no other.
  */
 sv_status sv_kv_attend(const sv_kv_cache *cache, int layer, const void *q_d, sv_dtype dtype,
                        int64_t q_row, int64_t q_tok, int T, int q_heads,

@@ -99,12 +99,20 @@ __device__ __forceinline__ float2 e4m3_to_f2(uint16_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// A load of data that an earlier kernel of the stream may have written. Not a read-only load:
+// those may be moved above the wait of kv_enter, and the data still changes while a kernel
+// that was brought up early is resident.
+template <typename V>
+__device__ __forceinline__ V kv_ld(const V* p) {
+  return *p;
+}
+
 // The page that holds position pos of row b, or -1 when the row does not hold one in
 // range (0 <= pos < 2^31).
 __device__ __forceinline__ int kv_page(const KvCache& C, int b, int pos) {
   const int j = pos >> C.lgp;
-  if (pos < 0 || j >= C.max_pages || j >= __ldg(C.np + b)) return -1;
-  const int p = __ldg(C.table + (size_t)b * C.max_pages + j);
+  if (pos < 0 || j >= C.max_pages || j >= kv_ld(C.np + b)) return -1;
+  const int p = kv_ld(C.table + (size_t)b * C.max_pages + j);
   return p >= 0 && p < C.pages ? p : -1;
 }
 
@@ -114,7 +122,7 @@ __device__ __forceinline__ bool kv_holds(const KvCache& C, int b, int lo, int hi
   if (lo < 0 || hi < lo) return false;
   for (int j = lo >> C.lgp; (long long)j << C.lgp < hi; ++j) {
     const int p = kv_page(C, b, j << C.lgp);
-    if (p < 0 || (alone && __ldg(C.refs + p) != 1)) return false;
+    if (p < 0 || (alone && kv_ld(C.refs + p) != 1)) return false;
   }
   return true;
 }

@@ -158,6 +158,7 @@ sv_status sv_kv_attend(const sv_kv_cache* cache, int layer, const void* q_d, sv_
   const long long qtiles = ((long long)T * (q_heads / C.heads) + KV_ROWS - 1) / KV_ROWS;
   const long long ktiles = ((long long)C.max_pages * C.page + 127) / 128 + KV_EXTRA;
   if (qtiles * C.batch * C.heads >= (1LL << 31) / ktiles) return SV_ERR_SHAPE;
+  if ((long long)C.max_pages * C.page > (1LL << 31) - 256) return SV_ERR_SHAPE;
   const float scale2 = static_cast<float>((double)scale * 1.4426950408889634);
   if (layer < 0 || layer >= C.layers || !std::isfinite(scale2) || window < 0 || sinks < 0)
     return SV_ERR_ARG;

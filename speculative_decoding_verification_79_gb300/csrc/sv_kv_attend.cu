@@ -45,6 +45,8 @@
 
 namespace sv {
 
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // sv_markov.cu
+
 constexpr int AT_KEYS = 128;     // tokens per key tile
 constexpr int AT_PARTS = 4;      // threads of a query row copy
 constexpr int AT_SM_WARPS = 4 * AT_PARTS;  // warps that form the weights
@@ -177,6 +179,9 @@ __device__ __forceinline__ void at_tma(void* dst, const CUtensorMap* map, int x,
 __device__ __forceinline__ void fence_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
+__device__ __forceinline__ void fence_async_global() {
+  asm volatile("fence.proxy.async.global;" ::: "memory");
+}
 __device__ __forceinline__ void at_bar(int id, int n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
@@ -214,8 +219,8 @@ struct AtRow {
 
 __device__ __forceinline__ AtRow at_row(const AttendArgs& A, int b) {
   AtRow r;
-  r.len = __ldg(A.C.len + b);
-  r.n = A.n_new ? __ldg(A.n_new + b) : A.T;
+  r.len = kv_ld(A.C.len + b);
+  r.n = A.n_new ? kv_ld(A.n_new + b) : A.T;
   r.bad = r.n < 0 || r.n > A.T || r.len < 0 ||
           (long long)r.len + r.n > (long long)A.C.max_pages << A.C.lgp;
   if (r.bad) r.n = 0;
@@ -245,7 +250,7 @@ __device__ __forceinline__ AtTile at_tile(const AttendArgs& A, const AtRow& r, i
   t.pos_lo = A.parent ? r.len : r.len + t0;
   t.pos_hi = A.parent ? r.len + r.n - 1 : r.len + t1;
   t.end = t.pos_hi + 1;
-  t.hi = (t.end + AT_KEYS - 1) / AT_KEYS;
+  t.hi = (t.end + AT_KEYS - 1) / AT_KEYS;  // (positions end 256 below 2^31)
   t.lo = 0;
   t.ns = 0;
   if (A.window) {
@@ -392,12 +397,12 @@ __device__ __forceinline__ void at_drain(uint64_t* bar, bool abort) {
 // when a component is infinite, which the saturating terms would not show. (Rows past the
 // item's keep what they held: each row's results are its own.) Not expanded in place: once
 // per query tile, and the kernel's loops share the instruction cache.
-__device__ __forceinline__ uint32_t at_raw(int db, int terms, int ndb, int row, int l16) {
+__device__ __forceinline__ uint32_t at_raw(int db, int row, int l16) {
   // The 16 bytes go to chunk l16 & 7 of the row in block 0 (l16 < 8) or 1 of the terms'
   // blocks; above dim 128 the second half of the row to blocks 2 and 3.
   return (2 * db + (l16 >> 3)) * AT_BLK + row * 128 + (l16 & 7) * 16;
 }
-__device__ __noinline__ void at_fetch(const AttendArgs& A, int terms, int ndb, const AtItem* it,
+__device__ __noinline__ void at_fetch(const AttendArgs& A, int ndb, const AtItem* it,
                                       unsigned char* Q) {
   const int hw = (threadIdx.x - AT_SM0) >> 4, l16 = threadIdx.x & 15;
 #pragma unroll 1
@@ -409,7 +414,7 @@ __device__ __noinline__ void at_fetch(const AttendArgs& A, int terms, int ndb, c
       const int d = db * 128 + l16 * 8;
       if (d < A.C.dim)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                         smem_addr(Q + at_raw(db, terms, ndb, row, l16))),
+                         smem_addr(Q + at_raw(db, row, l16))),
                      "l"(src + d)
                      : "memory");
     }
@@ -430,7 +435,7 @@ __device__ __noinline__ void at_convert(const AttendArgs& A, int terms, int ndb,
     for (int db = 0; db < 2; ++db) {
       uint4 x = make_uint4(0, 0, 0, 0);
       if (db * 128 + l16 * 8 < A.C.dim)
-        x = *reinterpret_cast<const uint4*>(Q + at_raw(db, terms, ndb, row, l16));
+        x = *reinterpret_cast<const uint4*>(Q + at_raw(db, row, l16));
       const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -635,6 +640,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     // chunk ahead of their use; their data go to the other warps through a ring of entries,
     // one per tile, written before the tile's barrier is armed. (An entry is used again 32
     // tiles later, and K is never more than its ring and three steps ahead of the rest.)
+    fence_async_global();  // (what earlier kernels stored, before copies read it)
     AtWalk walk;
     walk.start(A, s_b0, s_rt0, s_rem, from, to);
     const int ppt = AT_KEYS >> C.lgp;             // pages per tile
@@ -684,8 +690,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           float ks = 1.f, vs = 1.f;
           if (use) {
             if (pg >= 0) {
-              ks = __ldg(C.ks + (layer0 + pg) * C.heads + head);
-              vs = __ldg(C.vs + (layer0 + pg) * C.heads + head);
+              ks = kv_ld(C.ks + (layer0 + pg) * C.heads + head);
+              vs = kv_ld(C.vs + (layer0 + pg) * C.heads + head);
             }
             // A page out of range, or scales outside theirs: the scores become NaN.
             constexpr float LO = 5.421010862427522e-20f, HI = 18446744073709551616.f;  // 2^-64, 2^64
@@ -771,6 +777,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     }
   } else if (w == 2) {
     // ---- V copies, and in their pauses planning: the next item's description and columns.
+    fence_async_global();
     AtWalk walk;
     walk.start(A, s_b0, s_rt0, s_rem, from, to);
     const int ppt = AT_KEYS >> C.lgp;
@@ -837,7 +844,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         if (A.parent) {
           __syncwarp();
           for (int t = lane; t < nnew; t += 32) {
-            const int p = __ldg(A.parent + (size_t)walk.b * A.T + t);
+            const int p = kv_ld(A.parent + (size_t)walk.b * A.T + t);
             badtree = badtree || (t > 0 && (p < 0 || p >= t));
             s_par[t] = p;
           }
@@ -954,7 +961,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     // The queries of item k: on their way, and into shared memory; then the scores may begin.
     auto fetch = [&](int k) {
       if (!dead && !wait(&dfull[k & 1], (k >> 1) & 1)) dead = true;
-      if (!dead && s_item[k & 1].m > 0) at_fetch(A, P.qterms, ndb, &s_item[k & 1], Qs);
+      if (!dead && s_item[k & 1].m > 0) at_fetch(A, ndb, &s_item[k & 1], Qs);
     };
     auto convert = [&](int k) {
       if (!dead && s_item[k & 1].m > 0)
@@ -1324,22 +1331,6 @@ __global__ void __launch_bounds__(JOIN_THREADS)
   }
 }
 
-// The driver's tensor-map encoder, looked up once through the runtime.
-static PFN_cuTensorMapEncodeTiled_v12000 at_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    (void)cudaGetLastError();
-  });
-  return fn;
-}
-
 // Shared memory of a CTA, and what the kernels' static arrays take of it (at most).
 constexpr size_t AT_SMEM = 232448, AT_STATIC = 20480;
 
@@ -1370,7 +1361,7 @@ cudaError_t launch_kv_attend(const AttendArgs& A, sv_dtype dt, cudaStream_t st) 
   const size_t smem = fixed + (P.nk + P.nv) * tile;
   // The pools of one layer as matrices [pages * heads * page tokens][dim bytes], in boxes of
   // one page x 128 bytes (128-byte swizzle, zeros past dim).
-  PFN_cuTensorMapEncodeTiled_v12000 enc = at_encoder();
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc) return cudaErrorNotSupported;
   CUtensorMap tm[2];
   const size_t layer = (size_t)C.pages * C.heads * C.page * C.dim;

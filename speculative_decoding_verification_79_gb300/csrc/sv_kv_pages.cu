@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(PG_THREADS, 1)
   const int tid = threadIdx.x;
   // Pages that row b needs in all, or -1 when its data is wrong.
   auto holds = [&](int b) -> long long {
-    const int n = __ldg(n_new + b), len = C.len[b], np = S.np[b];
+    const int n = kv_ld(n_new + b), len = C.len[b], np = S.np[b];
     const long long h = ((long long)len + n + C.page - 1) >> C.lgp;
     return n < 0 || len < 0 || np < 0 || np > C.max_pages || h > C.max_pages ? -1 : h;
   };
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(PG_THREADS, 1)
 
 // src of row b, with one outside [-1, batch) read as b.
 __device__ __forceinline__ int fork_src(const KvCache& C, const int32_t* src, int b) {
-  const int s = __ldg(src + b);
+  const int s = kv_ld(src + b);
   return s >= -1 && s < C.batch ? s : b;
 }
 
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(128)
   const int len = max(0, static_cast<int>(min((long long)C.len[i], (long long)np << C.lgp)));
   const int full = len >> C.lgp;
   if (tid == 0) {
-    const int raw = __ldg(src + i);
+    const int raw = kv_ld(src + i);
     if (raw < -1 || raw >= C.batch || np != C.np[i] || len != C.len[i])
       kv_report(S.hdr, ST_DEVICE_INPUT);
     S.keeper[i] = m == 0 ? -1 : (fork_src(C, src, i) == i ? i : s_first);
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(PG_THREADS, 1)
   const int cap = C.batch < C.pages ? C.batch : C.pages;
   const int got = find_free(C, all < cap ? all : cap, S.list, sh);
   for (int b = tid; b < C.batch; b += PG_THREADS) {
-    const int raw = __ldg(src + b);
+    const int raw = kv_ld(src + b);
     bool good = raw >= -1 && raw < C.batch;
     const int r = S.fresh[b];
     if (r >= 0) {
@@ -280,8 +280,8 @@ __device__ bool commit_ok(const KvCache& C, int b, int acc, const int32_t* path,
   if (good && path) {
     bool bad = false;
     for (int i = lane; i < acc; i += 32) {
-      const int x = __ldg(path + (size_t)b * N + i);
-      const int prev = i ? __ldg(path + (size_t)b * N + i - 1) : 0;
+      const int x = kv_ld(path + (size_t)b * N + i);
+      const int prev = i ? kv_ld(path + (size_t)b * N + i - 1) : 0;
       bad = bad || x <= prev || x >= N;
       mv = mv || x != i + 1;
     }
@@ -289,7 +289,7 @@ __device__ bool commit_ok(const KvCache& C, int b, int acc, const int32_t* path,
     mv = __any_sync(0xffffffffu, mv);
   }
   if (good && acc >= 0) {
-    const int last = path && acc > 0 ? __ldg(path + (size_t)b * N + acc - 1) : acc;
+    const int last = path && acc > 0 ? kv_ld(path + (size_t)b * N + acc - 1) : acc;
     if (lane == 0)
       good = (long long)len + last < (1LL << 31) - 1 && kv_holds(C, b, len, len + last + 1, false) &&
              (!mv || kv_holds(C, b, len, len + acc + 1, true));
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(CM_THREADS)
   __shared__ int s_slot[SV_MAX_TREE], s_dslot[SV_MAX_TREE];   // and its slot there
   __shared__ float s_ss[SV_MAX_TREE], s_ds[SV_MAX_TREE];      // source and new scale
   extern __shared__ __align__(16) uint4 buf[];                // kept tokens of one block
-  const int acc = __ldg(accepted + b);
+  const int acc = kv_ld(accepted + b);
   if (tid < 32) {
     bool moves;
     const bool good = commit_ok(C, b, acc, path, N, &moves);
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(CM_THREADS)
   if (!s_moves) return;
   const int len = C.len[b], n = acc + 1;
   if (tid < n) {
-    const int from = len + (tid ? __ldg(path + (size_t)b * N + tid - 1) : 0), to = len + tid;
+    const int from = len + (tid ? kv_ld(path + (size_t)b * N + tid - 1) : 0), to = len + tid;
     s_src[tid] = kv_page(C, b, from);
     s_slot[tid] = from & (C.page - 1);
     s_dst[tid] = kv_page(C, b, to);
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(CM_THREADS)
   const int b = blockIdx.x, tid = threadIdx.x;
   __shared__ int s_len, s_np;
   if (tid == 0) {
-    s_len = C.len[b] + __ldg(accepted + b) + 1;
+    s_len = C.len[b] + kv_ld(accepted + b) + 1;
     s_np = min(max(C.np[b], 0), C.max_pages);
   }
   __syncthreads();

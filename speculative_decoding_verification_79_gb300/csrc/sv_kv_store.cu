@@ -21,7 +21,7 @@ struct Vec16<float> {
   float4 x[4];
   __device__ __forceinline__ void load(const float* p) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = __ldg(reinterpret_cast<const float4*>(p) + i);
+    for (int i = 0; i < 4; ++i) x[i] = kv_ld(reinterpret_cast<const float4*>(p) + i);
   }
   __device__ __forceinline__ void get(float* f) const {
 #pragma unroll
@@ -37,8 +37,8 @@ template <>
 struct Vec16<__nv_bfloat16> {
   uint4 x[2];
   __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    x[0] = __ldg(reinterpret_cast<const uint4*>(p));
-    x[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    x[0] = kv_ld(reinterpret_cast<const uint4*>(p));
+    x[1] = kv_ld(reinterpret_cast<const uint4*>(p) + 1);
   }
   __device__ __forceinline__ void get(float* f) const {
 #pragma unroll
@@ -56,8 +56,8 @@ template <>
 struct Vec16<__half> {
   uint4 x[2];
   __device__ __forceinline__ void load(const __half* p) {
-    x[0] = __ldg(reinterpret_cast<const uint4*>(p));
-    x[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    x[0] = kv_ld(reinterpret_cast<const uint4*>(p));
+    x[1] = kv_ld(reinterpret_cast<const uint4*>(p) + 1);
   }
   __device__ __forceinline__ void get(float* f) const {
 #pragma unroll
@@ -91,14 +91,15 @@ __global__ void __launch_bounds__(AP_THREADS)
   kv_enter();
   __shared__ float s_max[AP_THREADS / 32];
   const int b = blockIdx.z, h = blockIdx.y, tid = threadIdx.x;
-  const int n = n_new ? __ldg(n_new + b) : T;
+  const int n = n_new ? kv_ld(n_new + b) : T;
   if (n == 0) return;
-  const int len = __ldg(C.len + b);
+  const int len = kv_ld(C.len + b);
   const bool sane = n > 0 && n <= T && len >= 0 && ((long long)len + n - 1) >> C.lgp < C.max_pages;
   const int half = tid / AP_HALF, t0 = tid - half * AP_HALF;
   const KvSrc src = half ? vsrc : ksrc;
   const int j0 = sane ? len >> C.lgp : 0, j = j0 + blockIdx.x;
-  const int lo = max(len, j << C.lgp), hi = sane ? min(len + n, (j + 1) << C.lgp) : 0;
+  const bool in = sane && j < C.max_pages;
+  const int lo = in ? max(len, j << C.lgp) : 0, hi = in ? min(len + n, (j + 1) << C.lgp) : 0;
   const int vpt = C.dim / 16, nv = max(0, hi - lo) * vpt, off = lo - (j << C.lgp);
   const E* base = static_cast<const E*>(src.p) + b * src.row + (lo - len) * src.tok +
                   (size_t)h * C.dim;
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(AP_THREADS)
     const int j1 = (len + n - 1) >> C.lgp;
     for (int jj = j0 + tid; jj <= j1; jj += AP_THREADS) {
       const int p = kv_page(C, b, jj << C.lgp);
-      fine = fine && p >= 0 && __ldg(C.refs + p) == 1;
+      fine = fine && p >= 0 && kv_ld(C.refs + p) == 1;
     }
   }
   if (!__syncthreads_and(fine ? 1 : 0)) {
@@ -210,8 +211,8 @@ __global__ void __launch_bounds__(256)
   const int t = i / (C.heads * vpt);
   if (t >= T) return;
   const int r = i - t * (C.heads * vpt), h = r / vpt, c = r - h * vpt;
-  const int n = count ? __ldg(count + b) : T;
-  const long long pos = (long long)__ldg(start + b) + t;
+  const int n = count ? kv_ld(count + b) : T;
+  const long long pos = (long long)kv_ld(start + b) + t;
   const int p = t < n && pos >= 0 && pos < 0x7fffffffLL ? kv_page(C, b, (int)pos) : -1;
   uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
   float s[2] = {0.f, 0.f};

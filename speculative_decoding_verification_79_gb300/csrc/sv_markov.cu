@@ -633,7 +633,7 @@ __global__ void sv_markov_finish_kernel(const MarkovArgs A) {
 }
 
 // The driver's tensor-map encoder, looked up once through the runtime.
-static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {

@@ -673,3 +673,82 @@ def test_binding_refusals(sv):
             sv.sv_kv_fork(c, n)
     with pytest.raises(ValueError):
         sv.sv_kv_commit(c, good, 3, path=torch.zeros(2, 4, dtype=torch.int32, device="cuda"))
+
+
+@needs_cuda
+@pytest.mark.parametrize("what", ["k", "v"])
+@pytest.mark.parametrize("trees,window,sinks,dim,T,lens,at", [
+    (False, 0, 0, 64, 9, [130, 300], 134),    # among the new tokens: later queries see it
+    (True, 0, 0, 128, 16, [120, 300], 125),   # a node: its descendants
+    (False, 40, 0, 128, 20, [250, 300], 222),  # leaves the window during the block
+    (False, 40, 3, 192, 20, [250, 300], 4),   # between the sinks and the window
+    (False, 40, 3, 64, 20, [250, 300], 2),    # a sink
+    (False, 0, 0, 64, 40, [140, 10], 60),     # a tile that every query sees
+])
+def test_attend_stored_nan(sv, what, trees, window, sinks, dim, T, lens, at):
+    """A NaN in the cache reaches the queries that see it and no other."""
+    both, q, n, par = attend_case(sv, lens, T, 2, 2, dim, 32, torch.bfloat16, trees, window, sinks,
+                                  seed=at, n_new=[T, T])
+    g, r = both.g, both.r
+    pool = g.k if what == "k" else g.v
+    pool.view(torch.uint8)[0, int(g.table[0, at // 32]), 1, at % 32, 5] = 0x7F
+    got = sv.sv_kv_attend(g, 0, q, n_new=i32(n), parent=None if par is None else i32(par),
+                          window=window, sinks=sinks, want_lse=True)
+    out, lse = f64(got[0]), f64(got[1])
+    L = r.len[0]
+    o, ls, av, ab, qk = kv_ref.attend(f64(q[0]), r.values(0, 0, 0, 0, L + T),
+                                      r.values(1, 0, 0, 0, L + T), L, T, dim ** -0.5,
+                                      None if par is None else par[0], window, sinks)
+    bo, bl = bounds(o, ls, av, ab, qk, dim ** -0.5, q.dtype)
+    for t in range(T):
+        sees = kv_ref.visible(L, T, t, None if par is None else par[0], window, sinks)[at]
+        clean = slice(0, 2) if sees else slice(0, 4)
+        if sees:
+            assert np.isnan(out[0, t, 2:, 5]).all(), t
+            assert what == "v" or np.isnan(lse[0, t, 2:]).all(), t
+        assert (np.abs(out[0, t, clean] - o[t, clean]) <= bo[t, clean]).all(), t
+        assert (np.abs(lse[0, t, clean] - ls[t, clean]) <= bl[t, clean]).all(), t
+    check_attend(both, 0, q, n, par, window=window, sinks=sinks, rows=[1], got=got)
+
+
+@needs_cuda
+def test_attend_without_lse(sv):
+    """The log sum left out, output the same bits; whole query tiles and joined ones."""
+    for lens in ([50, 7], [30000, 5]):
+        both, q, n, _ = attend_case(sv, lens, 3, 2, 4, 64, 64, torch.float16, seed=8, n_new=[3, 2])
+        a = sv.sv_kv_attend(both.g, 0, q, n_new=i32(n))
+        b, _ = sv.sv_kv_attend(both.g, 0, q, n_new=i32(n), want_lse=True)
+        a = a[0] if isinstance(a, tuple) else a
+        assert torch.equal(a, b)
+
+
+@needs_cuda
+def test_calls_back_to_back(sv):
+    """Rounds on one stream without a pause, each call reading what the one before it wrote:
+    the same as with a synchronisation after every call."""
+    states = []
+    for paused in (False, True):
+        both = Both(sv, 1, 80, 16, 2, 64, 4, 18)
+        both.fill([40, 0, 33, 100], 21)
+        g = both.g
+        xs = [rand_kv(both.r, 6, 300 + i) for i in range(12)]
+        n, acc = i32([6, 5, 6, 2]), i32([2, 1, 3, 0])
+        path = i32([[2, 4] + [-1] * 4, [3] + [-1] * 5, [1, 3, 5] + [-1] * 3, [-1] * 6])
+        src = i32([0, 2, 2, 3])
+        outs = []
+        gap = torch.cuda.synchronize if paused else (lambda: None)
+        torch.cuda.synchronize()
+        for i, (k, v) in enumerate(xs):
+            for call in (lambda: sv.sv_kv_reserve(g, n), lambda: sv.sv_kv_append(g, 0, k, v, n_new=n),
+                         lambda: outs.append(sv.sv_kv_attend(g, 0, k, n_new=n, want_lse=True)),
+                         lambda: sv.sv_kv_commit(g, acc, 6, path=path),
+                         lambda: sv.sv_kv_fork(g, src) if i % 4 == 3 else None,
+                         lambda: outs.append(sv.sv_kv_read(g, i32([0] * 4), 120, count=g.len))):
+                gap()
+                call()
+        torch.cuda.synchronize()
+        assert g.status() == 0
+        states.append([t.clone() for t in (g.table, g.n_pages, g.len, g.refs)] +
+                      [t for o in outs for t in o])
+    for a, b in zip(*states):
+        assert torch.equal(a, b)

@@ -153,3 +153,12 @@ def test_model_invariants():
             for p in r:
                 count[p] += 1
         assert (count == c.refs).all()
+
+
+def test_attend_limits(sv):
+    """Work units and positions that pass 31 bits are refused, by attend only."""
+    c = cache(sv, max_pages=1 << 24)
+    assert calls(sv, c, T=65535, tok=1024)["attend"]() == sv.SV_ERR_SHAPE
+    c = cache(sv, page=16, max_pages=(1 << 27) - 1, batch=1)
+    assert calls(sv, c)["attend"]() == sv.SV_ERR_SHAPE
+    assert calls(sv, c, T=0)["append"]() == sv.SV_OK
