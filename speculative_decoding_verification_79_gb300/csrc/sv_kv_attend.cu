@@ -57,7 +57,6 @@ constexpr int AT_BLK = AT_KEYS * 128;  // 128 tokens x 128 bytes
 constexpr int AT_MAX_RING = 8;   // most K tiles, and V tiles, in shared memory
 constexpr int AT_INFO = 32;      // key tiles whose page data are kept
 constexpr int AT_PTERMS = 3;
-constexpr int AT_JOIN = 33;      // floats of a row in the buffer that outputs go through
 // Weights are kept as 2^(x - m + 11): up to 2^15 before the reference must move (below
 // e5m2's 57344). Their terms end at 2^-16, e5m2's smallest, so a weight has its 9 bits down
 // to 2^-19 of the reference and counts down to 2^-28. A larger shift would leave less room
@@ -207,6 +206,7 @@ struct AttendPlan {
   int ndb;     // 128-byte blocks of a token's vector
   int qterms;  // e4m3 terms of a query
   int bf16;
+  int chunk;   // components at a time in which row copies are added
 };
 
 // Row b of the batch.
@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   unsigned char* Qs = dsm;                                  // [terms][ndb][128][128]
   unsigned char* Ks = Qs + P.qterms * slot;                 // [nk][ndb][128][128]
   unsigned char* Vs = Ks + (size_t)P.nk * slot;             // [nv][ndb][128][128]
-  float* joinb = reinterpret_cast<float*>(Vs + (size_t)P.nv * slot);  // [128][AT_JOIN]
+  float* joinb = reinterpret_cast<float*>(Vs + (size_t)P.nv * slot);  // [128][chunk + 1]
 
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return mbar_try(bar, parity) || at_wait_on(bar, parity, &s_abort, A.S.hdr);
@@ -815,7 +815,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           s_abort = 1;
           break;
         }
-        __nanosleep(20);
+        __nanosleep(200);
         continue;
       }
       more = walk.live();
@@ -1129,8 +1129,12 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             }
           }
           // Weights: 2^x, summed with the value scale taken out, rounded to fp16 and split. A
-          // term is the upper byte of the remainder rounded to it (halves away from zero);
-          // what is left of an fp16 number after that is exact.
+          // term is the upper byte of what is left of the fp16 number; the rest after it is
+          // exact. The second and third are rounded (halves away from zero). The first is
+          // cut off: of an 11-bit number that leaves 8 bits, of those the second at most 4
+          // (and a sign) and the third none but an error of 2^-10. (Rounding it as well would
+          // not make that smaller, and an addition a pair is 3 % of the time: the kernel is
+          // bound by such integer instructions with 128 rows.)
 #pragma unroll
           for (int c = 0; c < NC; c += GC) {
             uint32_t t[AT_PTERMS][GC / 2];
@@ -1142,7 +1146,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
               __half2 y = __floats2half2_rn(p.x, p.y);
 #pragma unroll
               for (int k = 0; k < AT_PTERMS; ++k) {
-                t[k][e] = *reinterpret_cast<const uint32_t*>(&y) + 0x00800080u;
+                t[k][e] = *reinterpret_cast<const uint32_t*>(&y) + (k ? 0x00800080u : 0u);
                 const uint32_t hi = t[k][e] & 0xff00ff00u;
                 y = __hsub2(y, *reinterpret_cast<const __half2*>(&hi));
               }
@@ -1215,38 +1219,65 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         else if (A.lse)
           A.lse[s_out[kb][r]] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
       }
-      // Through shared memory, 32 components at a time: copies are added there, and rows
-      // leave in whole sectors.
+      if constexpr (COPIES == 1) {
+        // A row's 16 components are whole sectors: straight from the accumulator.
 #pragma unroll 1
-      for (int c = 0; c < C.dim; c += 32) {
-        const int n = min(32, C.dim - c);
-        if (live && part * 8 < n) {
-          float o[8];
-          tm_ld8(tl + c + part * 8, o);
-          tm_wait_ld<8>(o);
+        for (int c = part * 16; live && c < C.dim; c += 16 * AT_PARTS) {
+          float o[16];
+          tm_ld16(tl + c, o);
+          tm_wait_ld<16>(o);
+          if (!real) continue;
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            joinb[row * AT_JOIN + part * 8 + e] = f == 0.f ? 0.f : o[e] * f;
-        }
-        at_bar(5, AT_SM_THREADS);
-#pragma unroll 1
-        for (int e = st; e < it.R * 16; e += AT_SM_THREADS) {
-          const int rr = e >> 4, d = (e & 15) * 2;
-          if (d >= n) continue;
-          float y0 = 0.f, y1 = 0.f;
+          for (int e = 0; e < 16; ++e) o[e] = f == 0.f ? 0.f : o[e] * f;
+          if (whole) {
+            uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.out) +
+                                                 s_out[kb][r] * C.dim + c);
 #pragma unroll
-          for (int k = 0; k < COPIES; ++k) {
-            y0 += joinb[(k * W + rr) * AT_JOIN + d];
-            y1 += joinb[(k * W + rr) * AT_JOIN + d + 1];
+            for (int e = 0; e < 16; e += 8)
+              to[e / 8] = make_uint4(
+                  at_pack(o[e], o[e + 1], P.bf16), at_pack(o[e + 2], o[e + 3], P.bf16),
+                  at_pack(o[e + 4], o[e + 5], P.bf16), at_pack(o[e + 6], o[e + 7], P.bf16));
+          } else {
+            float4* to = reinterpret_cast<float4*>(A.S.part +
+                                                   ((size_t)slot_id * KV_ROWS + r) * C.dim + c);
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              to[e / 4] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           }
-          if (whole)
-            *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(A.out) + s_out[kb][rr] * C.dim + c + d) =
-                at_pack(y0, y1, P.bf16);
-          else
-            *reinterpret_cast<float2*>(A.S.part + ((size_t)slot_id * KV_ROWS + rr) * C.dim + c + d) =
-                make_float2(y0, y1);
         }
-        at_bar(5, AT_SM_THREADS);
+      } else {
+        // Copies are added in shared memory, `chunk` components at a time.
+#pragma unroll 1
+        for (int c = 0; c < C.dim; c += P.chunk) {
+          const int n = min(P.chunk, C.dim - c);
+          if (live && part * 8 < n) {
+            float o[8];
+            tm_ld8(tl + c + part * 8, o);
+            tm_wait_ld<8>(o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              joinb[row * (P.chunk + 1) + part * 8 + e] = f == 0.f ? 0.f : o[e] * f;
+          }
+          at_bar(5, AT_SM_THREADS);
+#pragma unroll 1
+          for (int e = st; e < it.R * 16; e += AT_SM_THREADS) {
+            const int rr = e >> 4, d = (e & 15) * 2;
+            if (d >= n) continue;
+            float y0 = 0.f, y1 = 0.f;
+#pragma unroll
+            for (int k = 0; k < COPIES; ++k) {
+              y0 += joinb[(k * W + rr) * (P.chunk + 1) + d];
+              y1 += joinb[(k * W + rr) * (P.chunk + 1) + d + 1];
+            }
+            if (whole)
+              *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(A.out) +
+                                           s_out[kb][rr] * C.dim + c + d) = at_pack(y0, y1, P.bf16);
+            else
+              *reinterpret_cast<float2*>(A.S.part + ((size_t)slot_id * KV_ROWS + rr) * C.dim + c +
+                                         d) = make_float2(y0, y1);
+          }
+          at_bar(5, AT_SM_THREADS);
+        }
       }
       tm_fence_before();
       if (!whole && it.i0 == 0) {  // the first of the CTAs that hold this query tile
@@ -1354,7 +1385,8 @@ cudaError_t launch_kv_attend(const AttendArgs& A, sv_dtype dt, cudaStream_t st) 
   const long long rows = (long long)A.T * A.group;
   const int width = rows <= 32 ? 32 : (rows <= 64 ? 64 : 128);
   const size_t tile = (size_t)P.ndb * AT_BLK;
-  const size_t fixed = 1024 + P.qterms * tile + 4 * 128 * AT_JOIN;
+  P.chunk = P.ndb == 1 ? 32 : 16;  // (16: room for one more tile of 256 bytes a token)
+  const size_t fixed = 1024 + P.qterms * tile + (width < 128 ? 4 * 128 * (P.chunk + 1) : 0);
   const int ring = (int)((AT_SMEM - AT_STATIC - fixed) / tile);
   P.nk = ring / 2 < AT_MAX_RING ? ring / 2 : AT_MAX_RING;
   P.nv = ring - ring / 2 < AT_MAX_RING ? ring - ring / 2 : AT_MAX_RING;
