@@ -338,12 +338,21 @@ struct AtItem {
   int r0, R;        // query rows r0 .. r0 + R - 1 of the head
   int i0, m;        // key tiles i0 .. i0 + m - 1 (m = 0: no more work)
   int tiles;        // of the query tile
-  int end, pos_hi;  // as AtTile
+  int end, pos_lo, pos_hi;  // as AtTile
   int ns, lo;
   int bad;          // the row's tree is wrong
   int u0;           // unit of its first key tile
   __device__ __forceinline__ int key_tile(int i) const { return i < ns ? i : lo + i - ns; }
+  // A tile is cut (some query does not see all of it) when its first key is cut_hi or above,
+  // and when it has a key below cut_lo that is not a sink.
+  __device__ __forceinline__ int cut_hi() const { return pos_lo - AT_KEYS + 2; }
+  __device__ __forceinline__ int cut_lo(int window) const { return window ? pos_hi - window + 1 : 0; }
 };
+
+// The lowest n bits (none below 1, all from 32 on).
+__device__ __forceinline__ uint32_t at_below(int n) {
+  return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u);
+}
 
 // Two and four consecutive values, rounded to the output's type.
 __device__ __forceinline__ uint32_t at_pack(float a, float b, int bf16) {
@@ -482,6 +491,61 @@ __device__ __noinline__ void at_convert(const AttendArgs& A, int terms, int ndb,
   fence_async();
 }
 
+// Bytes of x that are NaN (e4m3), as their upper bits.
+__device__ __forceinline__ uint32_t at_nan4(uint32_t x) {
+  return ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+
+// The values of a cut tile, before they are multiplied: what weight 0 would not hide. Tokens
+// from `end` on (whatever the page holds) are zeroed; a NaN is zeroed where it stands, and
+// its token's bit set in `nans`: it becomes the weight of the queries that see it. One warp,
+// eight lanes a token, 32 tokens at a time. (All weight warps stopping for it held up a cut
+// tile by 4,000 cycles.)
+__device__ __noinline__ void at_check(unsigned char* v, int ndb, int end, uint32_t* nans) {
+  const int lane = threadIdx.x & 31;
+  if (lane < AT_KEYS / 32) nans[lane] = 0;
+  __syncwarp();
+#pragma unroll 1
+  for (int blk = 0; blk < ndb * (AT_KEYS / 32); ++blk) {
+    const int t0 = blk % (AT_KEYS / 32) * 32;
+    uint4* p = reinterpret_cast<uint4*>(v + blk * 32 * 128) + lane;  // (tokens t0 + 4 u + lane / 8)
+    if (t0 < end) {
+      uint4 y[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) y[u] = p[32 * u];
+      uint32_t nan = 0;
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        nan |= at_nan4(y[u].x) | at_nan4(y[u].y) | at_nan4(y[u].z) | at_nan4(y[u].w);
+      if (__any_sync(0xffffffffu, nan != 0)) {
+#pragma unroll 1
+        for (int u = 0; u < 8; ++u) {
+          uint4 x = p[32 * u];
+          uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+          uint32_t has = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t m = at_nan4(w[i]);
+            has |= m;
+            w[i] &= ~((m >> 7) * 0xffu);
+          }
+          const int tok = t0 + 4 * u + (lane >> 3);
+          if (!has || tok >= end) continue;
+          p[32 * u] = x;
+          atomicOr(&nans[tok / 32], 1u << (tok % 32));
+        }
+      }
+    }
+    if (t0 + 32 > end) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (t0 + 4 * u + (lane >> 3) >= end) p[32 * u] = make_uint4(0, 0, 0, 0);
+    }
+  }
+  fence_async();
+  __syncwarp();
+}
+
 // Waits for the copies of the last tiles 0 .. g - 1 of a ring of n.
 __device__ __noinline__ void at_land(uint64_t* full, int n, int g) {
   const long long t0 = clock64();
@@ -506,7 +570,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   extern __shared__ unsigned char dsm_raw[];
   __shared__ uint64_t kfull[AT_MAX_RING], kempty[AT_MAX_RING];
   __shared__ uint64_t vfull[AT_MAX_RING], vempty[AT_MAX_RING], tinfo[AT_INFO];
-  __shared__ uint64_t sfull[3], pfull[3], pvdone[3], qfull, dfull[2], dempty[2], drain[2];
+  __shared__ uint64_t sfull[3], pfull[3], pvdone[3], vchk[AT_MAX_RING], qfull, dfull[2], dempty[2], drain[2];
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
   __shared__ int s_b0, s_rt0, s_rem, s_total, s_sum[AT_THREADS / 32];
@@ -525,7 +589,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   __shared__ unsigned long long s_tsee[SV_MAX_TREE];       // and what a node sees
   __shared__ float s_top[AT_PARTS][128], s_l[AT_PARTS][128];  // largest scores, sums
   __shared__ float2 s_stat[128];     // reference and sum of a row copy
-  __shared__ int s_vnan[AT_KEYS];
+  // Tokens of a cut tile with a NaN value, an entry per cut tile (no more of them than tiles
+  // in V's ring are checked and not yet multiplied).
+  __shared__ uint32_t s_vnan[AT_MAX_RING][AT_KEYS / 32];
 
   unsigned char* dsm = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -548,6 +614,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       mbar_init(&kempty[tid], 1);
       mbar_init(&vfull[tid], 1);
       mbar_init(&vempty[tid], 1);
+      mbar_init(&vchk[tid], 1);
     }
     if (tid < 3) {
       mbar_init(&sfull[tid], 2);
@@ -776,7 +843,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       at_drain(&drain[0], s_abort);
     }
   } else if (w == 2) {
-    // ---- V copies, and in their pauses planning: the next item's description and columns.
+    // ---- V copies, the values of cut tiles, and in the pauses planning: the next item's
+    // description and rows.
     fence_async_global();
     AtWalk walk;
     walk.start(A, s_b0, s_rt0, s_rem, from, to);
@@ -788,8 +856,31 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     auto ready = [&](uint64_t* bar, int parity) {
       return __any_sync(0xffffffffu, mbar_test(bar, parity & 1)) != 0;
     };
-    while (more || g < planned) {
-      if (g < planned && ready(&tinfo[g & (AT_INFO - 1)], g / AT_INFO) &&
+    // Checked tiles, their place in the ring, and in their item ck. (No copy or plan passes
+    // what is not checked.)
+    int c = 0, cq = 0, cph = 0, ck = 0, ci = 0, cuts = 0;
+    while (more || c < planned) {
+      if (c < g && ready(&vfull[cq], cph)) {
+        const AtItem& it = s_item[ck & 1];
+        const int key0 = it.key_tile(it.i0 + ci) * AT_KEYS;
+        if (key0 >= it.cut_hi() || (key0 < it.cut_lo(A.window) && key0 + AT_KEYS > A.sinks)) {
+          at_check(Vs + (size_t)cq * slot, ndb, it.end - key0, s_vnan[cuts % AT_MAX_RING]);
+          if (lane == 0) mbar_arrive(&vchk[cuts % AT_MAX_RING]);
+          ++cuts;
+        }
+        if (++ci == it.m) {
+          ci = 0;
+          ++ck;
+        }
+        ++c;
+        if (++cq == P.nv) {
+          cq = 0;
+          ++cph;
+        }
+        idle = 0;
+        continue;
+      }
+      if (g < planned && g - c < P.nv && ready(&tinfo[g & (AT_INFO - 1)], g / AT_INFO) &&
           (ph == 0 || ready(&vempty[q], ph - 1))) {
         const int y = lane < ppt ? s_y[g & (AT_INFO - 1)][lane] : -1;
         const uint32_t pages = __popc(__ballot_sync(0xffffffffu, y >= 0));
@@ -809,13 +900,13 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       }
       const int kb = k & 1;
       // (Item k's place is free once item k - 2 is done with.)
-      if (!more || (k >= 2 && !ready(&dempty[kb], (k >> 1) - 1))) {
+      if (!more || (k >= 2 && (ck < k - 1 || !ready(&dempty[kb], (k >> 1) - 1)))) {
         if (__any_sync(0xffffffffu, s_abort || at_expired(&idle))) {
           if (!s_abort) kv_report(A.S.hdr, ST_TIMEOUT);
           s_abort = 1;
           break;
         }
-        __nanosleep(200);
+        __nanosleep(50);
         continue;
       }
       more = walk.live();
@@ -835,6 +926,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           it.i0 = walk.i0;
           it.tiles = walk.tile.tiles();
           it.end = walk.tile.end;
+          it.pos_lo = walk.tile.pos_lo;
           it.pos_hi = walk.tile.pos_hi;
           it.ns = walk.tile.ns;
           it.lo = walk.tile.lo;
@@ -977,7 +1069,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     };
     fetch(0);
     convert(0);
-    int g = 0, q = 0, ph = 0;
+    int g = 0, cuts = 0;  // key tiles, and cut ones
     bool opened = false;  // does a query tile that begins here go on in the next CTA?
     for (int item = 0;; ++item) {
       const int kb = item & 1;
@@ -989,10 +1081,10 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       const int m = it.m, len = it.len;
       if (m == 0) break;
       // Key tiles i < turn follow the row's start, the others the window; a tile is cut (some
-      // query does not see all of it) from key `cut_hi` on, and from `sinks` to `cut_lo`.
+      // query does not see all of it) from first key `cut_hi` on, and from `sinks` to `cut_lo`.
       int kt = it.key_tile(it.i0);
       const int turn = it.ns - it.i0, resume = it.lo;
-      const int cut_hi = len - AT_KEYS, cut_lo = A.window ? it.pos_hi - A.window + 1 : 0;
+      const int cut_hi = it.cut_hi(), cut_lo = it.cut_lo(A.window);
       const bool live = quad * 32 % W < it.R;  // does the warp have a query row?
       const bool real = r < it.R;
       const float cs = real ? s_c[kb][r] : 0.f;
@@ -1010,48 +1102,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         if (!dead && !wait(&sfull[sb], sph & 1)) dead = true;
         tm_fence_after();
         if (i == m - 1) fetch(item + 1);  // (the last scores are done: the queries' place is free)
-        // Is there a key of the tile that some query does not see? Then also look after the
-        // values that weight 0 would not hide: tokens past the end (whatever the page
-        // holds) are zeroed, and a NaN is zeroed where it stands and made the weight of the
-        // queries that do see it.
-        const bool cut = key0 > cut_hi || (key0 < cut_lo && key0 + AT_KEYS > A.sinks);
-        bool vnan = false;
-        if (__builtin_expect(cut, 0)) {
-          // (Once the last tile's output is done, V's barriers cannot be a pass behind.)
-          if (!dead && ((i > 0 && !done()) || !wait(&vfull[q], ph & 1)))
-            dead = true;
-          const int tok = st & 127;
-          bool nan = false;
-          for (int db = 0; db < ndb && !dead; ++db) {
-            // Two of a token's eight 16-byte chunks, turned so that the lanes of a warp
-            // spread over the banks.
-#pragma unroll 1
-            for (int e = 0; e < 2; ++e) {
-              uint4* p = reinterpret_cast<uint4*>(Vs + (size_t)q * slot + db * AT_BLK + tok * 128) +
-                         ((2 * part + e + tok) & 7);
-              if (key0 + tok >= it.end) {
-                *p = make_uint4(0, 0, 0, 0);
-                continue;
-              }
-              const uint4 y = *p;
-              const uint4 z = make_uint4(
-                  __vcmpeq4(y.x & 0x7f7f7f7fu, 0x7f7f7f7fu), __vcmpeq4(y.y & 0x7f7f7f7fu, 0x7f7f7f7fu),
-                  __vcmpeq4(y.z & 0x7f7f7f7fu, 0x7f7f7f7fu), __vcmpeq4(y.w & 0x7f7f7f7fu, 0x7f7f7f7fu));
-              if (z.x | z.y | z.z | z.w) {
-                nan = true;
-                *p = make_uint4(y.x & ~z.x, y.y & ~z.y, y.z & ~z.z, y.w & ~z.w);
-              }
-            }
-          }
-          fence_async();
-          vnan = at_vote(5, AT_SM_THREADS, nan);
-          if (vnan) {
-            if (part == 0) s_vnan[tok] = 0;
-            at_bar(5, AT_SM_THREADS);
-            if (nan) s_vnan[tok] = 1;
-            at_bar(5, AT_SM_THREADS);
-          }
-        }
+        // Is there a key of the tile that some query does not see?
+        const bool cut = key0 >= cut_hi || (key0 < cut_lo && key0 + AT_KEYS > A.sinks);
         const uint32_t sa = tl + scol + sb * 128;
         if (live) {
           // This thread's scores as logarithms of their weights, sixteen tokens at a time.
@@ -1078,17 +1130,22 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             }
           }
           if (__builtin_expect(cut, 0)) {
+            // Which of this thread's NC tokens the query sees, as bits. A chain sees those up
+            // to its position; a tree the cached ones and its own of the block.
+            const int k0 = key0 + c0;
+            uint32_t sees = at_below(A.parent ? len - k0 : pos - k0 + 1);
+            if (A.window) sees &= ~at_below(max(pos - k0 + 1, 0) - A.window) | at_below(A.sinks - k0);
+            if (A.parent) {
+              const int o = k0 - len;
+              if (o > -32 && o < 64)
+                sees |= static_cast<uint32_t>(o >= 0 ? see >> o : see << -o) & at_below(len + it.n - k0);
+            }
+            if (!dead && !wait(&vchk[cuts % AT_MAX_RING], (cuts / AT_MAX_RING) & 1)) dead = true;
+            const uint32_t bad = s_vnan[cuts % AT_MAX_RING][c0 / 32] >> (c0 % 32);
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
-              const int key = key0 + c0 + c, o = key - len;
-              bool sees = !A.window || pos - key < A.window || key < A.sinks;
-              if (A.parent) {
-                if (o >= 0) sees = o < it.n && ((see >> (o & 63)) & 1) != 0;
-              } else {
-                sees = sees && key <= pos;
-              }
-              if (vnan && s_vnan[c0 + c]) x[c] = NAN;
-              x[c] = sees ? x[c] : -INFINITY;
+              if ((bad >> c) & 1) x[c] = NAN;
+              if (!((sees >> c) & 1)) x[c] = -INFINITY;
             }
           }
 #pragma unroll
@@ -1174,13 +1231,10 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           }
           tm_wait_st();
         }
+        cuts += cut;
         tm_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&pfull[sb]);
-        if (++q == P.nv) {
-          q = 0;
-          ++ph;
-        }
         if (++sb == nsb) {
           sb = 0;
           ++sph;
