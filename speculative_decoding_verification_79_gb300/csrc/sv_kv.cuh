@@ -22,7 +22,7 @@ struct KvCache {
 // list of fresh pages, a flag per row, and the attention's partial results.
 constexpr int KV_MAX_CTAS = 160;  // persistent CTAs of the attention kernel
 constexpr int KV_ROWS = 128;      // most query rows of its tile
-constexpr int KV_EXTRA = 7;       // its work per query tile beside the key tiles, in key tiles
+constexpr int KV_EXTRA = 6;       // its work per query tile beside the key tiles, in key tiles
 
 // A query tile of the attention that begins in one CTA and goes on in others, up to `last`:
 // rows r0 .. r0 + R - 1 of (row b, head h). R = 0: the CTA has none.

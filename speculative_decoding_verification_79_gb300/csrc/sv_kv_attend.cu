@@ -206,7 +206,7 @@ struct AttendPlan {
   int ndb;     // 128-byte blocks of a token's vector
   int qterms;  // e4m3 terms of a query
   int bf16;
-  int chunk;   // components at a time in which row copies are added
+  int join;    // floats of the buffer in which row copies are added
 };
 
 // Row b of the batch.
@@ -363,6 +363,13 @@ __device__ __forceinline__ uint32_t at_pack(float a, float b, int bf16) {
 __device__ __forceinline__ void at_store4(void* out, long long at, float4 y, int bf16) {
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) =
       make_uint2(at_pack(y.x, y.y, bf16), at_pack(y.z, y.w, bf16));
+}
+
+// Partial results: where (in vectors of four floats) components c .. c + 3 of row r are in
+// slot `id`. Rows are next to each other: their threads store, and the join reads, whole
+// sectors. (Rows one after the other made the stores of 128 x 256 floats 9,000 cycles.)
+__device__ __forceinline__ size_t at_part(int id, int r, int c, int dim) {
+  return ((size_t)id * (dim / 4) + c / 4) * KV_ROWS + r;
 }
 
 // Has it been WAIT_CYCLES since the first call with *t0 == 0?
@@ -601,7 +608,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   unsigned char* Qs = dsm;                                  // [terms][ndb][128][128]
   unsigned char* Ks = Qs + P.qterms * slot;                 // [nk][ndb][128][128]
   unsigned char* Vs = Ks + (size_t)P.nk * slot;             // [nv][ndb][128][128]
-  float* joinb = reinterpret_cast<float*>(Vs + (size_t)P.nv * slot);  // [128][chunk + 1]
+  float* joinb = reinterpret_cast<float*>(Vs + (size_t)P.nv * slot);  // row copies being added
 
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return mbar_try(bar, parity) || at_wait_on(bar, parity, &s_abort, A.S.hdr);
@@ -1292,43 +1299,50 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
                   at_pack(o[e], o[e + 1], P.bf16), at_pack(o[e + 2], o[e + 3], P.bf16),
                   at_pack(o[e + 4], o[e + 5], P.bf16), at_pack(o[e + 6], o[e + 7], P.bf16));
           } else {
-            float4* to = reinterpret_cast<float4*>(A.S.part +
-                                                   ((size_t)slot_id * KV_ROWS + r) * C.dim + c);
+            float4* to = reinterpret_cast<float4*>(A.S.part) + at_part(slot_id, r, c, C.dim);
 #pragma unroll
             for (int e = 0; e < 16; e += 4)
-              to[e / 4] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              to[e / 4 * KV_ROWS] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           }
         }
       } else {
-        // Copies are added in shared memory, `chunk` components at a time.
+        // Copies are added in shared memory, as many components at a time (a multiple of 8)
+        // as fit there for the item's rows.
+        const int R = it.R, fit = (P.join / (COPIES * R) - 1) & ~7, line = min(fit, C.dim) + 1;
 #pragma unroll 1
-        for (int c = 0; c < C.dim; c += P.chunk) {
-          const int n = min(P.chunk, C.dim - c);
-          if (live && part * 8 < n) {
+        for (int c = 0; c < C.dim; c += fit) {
+          const int n = min(fit, C.dim - c);
+#pragma unroll 1
+          for (int d = part * 8; live && d < n; d += 8 * AT_PARTS) {
             float o[8];
-            tm_ld8(tl + c + part * 8, o);
+            tm_ld8(tl + c + d, o);
             tm_wait_ld<8>(o);
+            if (!real) continue;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              joinb[row * (P.chunk + 1) + part * 8 + e] = f == 0.f ? 0.f : o[e] * f;
+              joinb[(copy * R + r) * line + d + e] = f == 0.f ? 0.f : o[e] * f;
           }
           at_bar(5, AT_SM_THREADS);
+          // Four components each: neighbours take a row's in the result, a column's in partial
+          // results.
+          const int inner = whole ? n / 4 : R;
 #pragma unroll 1
-          for (int e = st; e < it.R * 16; e += AT_SM_THREADS) {
-            const int rr = e >> 4, d = (e & 15) * 2;
-            if (d >= n) continue;
-            float y0 = 0.f, y1 = 0.f;
+          for (int e = st; e < R * (n / 4); e += AT_SM_THREADS) {
+            const int hi = e / inner, lo = e - hi * inner;
+            const int rr = whole ? hi : lo, d = 4 * (whole ? lo : hi);
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int k = 0; k < COPIES; ++k) {
-              y0 += joinb[(k * W + rr) * (P.chunk + 1) + d];
-              y1 += joinb[(k * W + rr) * (P.chunk + 1) + d + 1];
+              const float* j = joinb + (k * R + rr) * line + d;
+              y.x += j[0];
+              y.y += j[1];
+              y.z += j[2];
+              y.w += j[3];
             }
             if (whole)
-              *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(A.out) +
-                                           s_out[kb][rr] * C.dim + c + d) = at_pack(y0, y1, P.bf16);
+              at_store4(A.out, s_out[kb][rr] * C.dim + c + d, y, P.bf16);
             else
-              *reinterpret_cast<float2*>(A.S.part + ((size_t)slot_id * KV_ROWS + rr) * C.dim + c +
-                                         d) = make_float2(y0, y1);
+              reinterpret_cast<float4*>(A.S.part)[at_part(slot_id, rr, c + d, C.dim)] = y;
           }
           at_bar(5, AT_SM_THREADS);
         }
@@ -1368,10 +1382,12 @@ __global__ void __launch_bounds__(JOIN_THREADS)
   kv_enter();
   const int first = blockIdx.x;
   const KvOpen it = A.S.open[first];
-  const int vec = A.C.dim / 4, n = it.R * vec;
+  // (Eight rows and four of their vectors to a warp: whole sectors on both sides.)
+  const int vec = A.C.dim / 4, n = (it.R + 7) / 8 * 8 * vec;
   constexpr int K = 4;
   for (int e = blockIdx.y * JOIN_THREADS + threadIdx.x; e < n; e += JOIN_BLOCKS * JOIN_THREADS) {
-    const int r = e / vec, dv = e - r * vec;
+    const int r = e / (8 * vec) * 8 + e % 8, dv = e / 8 % vec;
+    if (r >= it.R) continue;
     float ref = -INFINITY, sum = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k0 = first; k0 <= it.last; k0 += K) {
@@ -1380,9 +1396,9 @@ __global__ void __launch_bounds__(JOIN_THREADS)
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const int kk = min(k0 + k, it.last);
-        const size_t sl = (size_t)(2 * kk + (kk == first ? 1 : 0)) * KV_ROWS + r;
-        s2[k] = __ldcg(A.S.stat + sl);
-        y[k] = __ldcg(reinterpret_cast<const float4*>(A.S.part + sl * A.C.dim) + dv);
+        const int id = 2 * kk + (kk == first ? 1 : 0);
+        s2[k] = __ldcg(A.S.stat + (size_t)id * KV_ROWS + r);
+        y[k] = __ldcg(reinterpret_cast<const float4*>(A.S.part) + at_part(id, r, 4 * dv, A.C.dim));
       }
       float top = ref;
 #pragma unroll
@@ -1439,8 +1455,10 @@ cudaError_t launch_kv_attend(const AttendArgs& A, sv_dtype dt, cudaStream_t st) 
   const long long rows = (long long)A.T * A.group;
   const int width = rows <= 32 ? 32 : (rows <= 64 ? 64 : 128);
   const size_t tile = (size_t)P.ndb * AT_BLK;
-  P.chunk = P.ndb == 1 ? 32 : 16;  // (16: room for one more tile of 256 bytes a token)
-  const size_t fixed = 1024 + P.qterms * tile + (width < 128 ? 4 * 128 * (P.chunk + 1) : 0);
+  // At least 39 components of 128 row copies, or 16 of them, which leaves room for one more
+  // tile of 256 bytes a token.
+  P.join = width == 128 ? 0 : 128 * (P.ndb == 1 ? 40 : 17);
+  const size_t fixed = 1024 + P.qterms * tile + 4 * P.join;
   const int ring = (int)((AT_SMEM - AT_STATIC - fixed) / tile);
   P.nk = ring / 2 < AT_MAX_RING ? ring / 2 : AT_MAX_RING;
   P.nv = ring - ring / 2 < AT_MAX_RING ? ring - ring / 2 : AT_MAX_RING;
