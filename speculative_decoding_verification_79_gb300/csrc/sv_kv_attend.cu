@@ -1261,19 +1261,20 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       at_bar(5, AT_SM_THREADS);
       const bool whole = m == it.tiles;
       const int slot_id = 2 * blockIdx.x + (it.i0 == 0 ? 1 : 0);
-      // Reference and sum over the row's copies, and this copy's factor.
+      // Reference and sum over the row's copies, and this copy's factor. (The approximate
+      // power and quotient are off by 2^-22; short code, since it comes from memory each time.)
       float ref = -INFINITY, sum = 0.f;
-#pragma unroll
-      for (int c = 0; c < COPIES; ++c)
-        if (s_stat[c * W + r].y != 0.f) ref = fmaxf(ref, s_stat[c * W + r].x);
-#pragma unroll
-      for (int c = 0; c < COPIES; ++c) {
-        const float2 s2 = s_stat[c * W + r];
-        if (s2.y != 0.f) sum = fmaf(s2.y, exp2f(s2.x - ref), sum);
+#pragma unroll 1
+      for (int c = r; c < 128; c += W) {
+        const float2 s2 = s_stat[c];
+        if (s2.y == 0.f) continue;
+        const float top = fmaxf(ref, s2.x);
+        sum = fmaf(s2.y, ex2(s2.x - top), sum * ex2(ref - top));
+        ref = top;
       }
       const float2 own = s_stat[row];
-      float f = own.y == 0.f ? 0.f : exp2f(own.x - ref);
-      if (whole) f = sum == 0.f ? 0.f : f / sum;
+      float f = own.y == 0.f ? 0.f : ex2(own.x - ref);
+      if (whole) f = sum == 0.f ? 0.f : __fdividef(f, sum);
       if (copy == 0 && part == 0 && real) {
         if (!whole)
           A.S.stat[(size_t)slot_id * KV_ROWS + r] = make_float2(ref, sum);
