@@ -727,6 +727,130 @@ def run_tree(args):
                                     "each call"}), flush=True)
 
 
+class KvRounds:
+    """Rounds of tree decoding through the key/value cache: 64 requests of 1,000 to 5,000
+    cached tokens, trees of 16 nodes, 4 layers of 8 key/value and 32 query heads of 128, pages
+    of 64 tokens; the verification is the bench's tree workload (V=151,936 bf16, T=1), and its
+    path is what the cache keeps."""
+
+    LAYERS, PAGE, HEADS, Q_HEADS, DIM = 4, 64, 8, 32, 128
+
+    def __init__(self, dev, rounds):
+        import numpy as np
+        import speculative_decoding_verification_79_gb300 as sv
+        import synth
+
+        self.sv = sv
+        self.inp = synth.tree_qwen3(1.0, seed=1, device=dev)
+        B, N, _ = self.inp["target"].shape
+        rng = np.random.default_rng(1)
+        lens = [int(x) for x in rng.integers(1000, 5001, B)]
+        width = max(-(-(n + (rounds + 1) * N) // self.PAGE) for n in lens)
+        self.cache = sv.KVCache(self.LAYERS, B * width, self.PAGE, self.HEADS, self.DIM, B, width,
+                                device=dev)
+        gen = torch.Generator(device=dev).manual_seed(2)
+        # The prompts, 512 tokens at a time, then one fused projection per layer and round.
+        most = max(lens)
+        for t in range(0, most, 512):
+            n = torch.tensor([min(512, max(0, x - t)) for x in lens], dtype=torch.int32, device=dev)
+            kv = torch.randn(2, B, 512, self.HEADS, self.DIM, generator=gen, device=dev).bfloat16()
+            sv.sv_kv_reserve(self.cache, n)
+            for layer in range(self.LAYERS):
+                sv.sv_kv_append(self.cache, layer, kv[0], kv[1], n_new=n)
+            sv.sv_kv_commit(self.cache, n - 1, 512)
+        H, K = self.Q_HEADS, self.HEADS
+        self.qkv = torch.randn(self.LAYERS, B, N, H + 2 * K, self.DIM, generator=gen,
+                               device=dev).bfloat16()
+        self.n = torch.full((B,), N, dtype=torch.int32, device=dev)
+        self.outs = [torch.empty((B, N), dtype=torch.int32, device=dev),
+                     torch.empty(B, dtype=torch.int32, device=dev),
+                     torch.empty((B, N), dtype=torch.int32, device=dev)]
+        self.att = torch.empty((B, N, H, self.DIM), dtype=torch.bfloat16, device=dev)
+        self.ws = sv.Workspace(1, 1, 1, device=dev)
+        self.N = N
+
+    def calls(self, st):
+        """The calls of a round in order, by name."""
+        sv, c, i = self.sv, self.cache, self.inp
+        H, K = self.Q_HEADS, self.HEADS
+        yield "reserve", lambda: sv.sv_kv_reserve(c, self.n, stream=st)
+        for layer in range(self.LAYERS):
+            x = self.qkv[layer]
+            yield "append", lambda: sv.sv_kv_append(c, layer, x[:, :, H:H + K], x[:, :, H + K:],
+                                                    stream=st)
+            yield "attend", lambda: sv.sv_kv_attend(c, layer, x[:, :, :H], parent=i["parent"],
+                                                    out=self.att, stream=st)
+        yield "verify_tree", lambda: sv.sv_verify_tree(
+            i["target"], i["draft"], i["parent"], i["draft_tok"], i["n_nodes"], i["uniforms"], 1.0,
+            self.ws, *self.outs, stream=st)
+        yield "commit", lambda: sv.sv_kv_commit(c, self.outs[1], self.N, path=self.outs[2],
+                                                stream=st)
+
+    def check(self, st):
+        if self.cache.status(stream=st) != self.sv.SV_OK or self.ws.status(stream=st) != self.sv.SV_OK:
+            raise RuntimeError("device status not OK in the cache rounds")
+
+
+def run_kv(args):
+    """One JSON line: tree decoding rounds through the key/value cache (see KvRounds). Ten
+    rounds with events around every call in a CUDA graph, and ten without events as one span."""
+    dev = torch.device("cuda", 0)
+    st = torch.cuda.Stream(device=dev)
+    n = 10
+    kv = KvRounds(dev, 2 * n + 3)
+    st.wait_stream(torch.cuda.current_stream(dev))
+    with torch.cuda.stream(st):
+        for _ in range(3):
+            for _, call in kv.calls(st):
+                call()
+    st.synchronize()
+    ev = lambda: torch.cuda.Event(enable_timing=True, external=True)  # noqa: E731
+    spans, marks = [ev(), ev()], []
+    graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    with torch.cuda.graph(graphs[0], stream=st):
+        spans[0].record(st)
+        for _ in range(n):
+            for _, call in kv.calls(st):
+                call()
+        spans[1].record(st)
+    with torch.cuda.graph(graphs[1], stream=st):
+        for _ in range(n):
+            for name, call in kv.calls(st):
+                a, b = ev(), ev()
+                a.record(st)
+                call()
+                b.record(st)
+                marks.append((name, a, b))
+    with torch.cuda.stream(st):
+        for g in graphs:
+            g.replay()
+    kv.check(st)
+    us = {}
+    for name, a, b in marks:
+        us.setdefault(name, []).append(a.elapsed_time(b) * 1e3)
+    emitted = float((kv.outs[1] + 1).sum())
+    span = spans[0].elapsed_time(spans[1]) * 1e3 / n
+    print(json.dumps({"kv": True, "B": len(kv.n), "N": kv.N, "layers": kv.LAYERS,
+                      "kv_heads": kv.HEADS, "q_heads": kv.Q_HEADS, "dim": kv.DIM, "page": kv.PAGE,
+                      "cache": "e4m3", "dtype": "bf16", "round_us": span,
+                      "tokens_per_s": emitted / (span / 1e6),
+                      "us_per_call": {k: sorted(x)[len(x) // 2] for k, x in us.items()},
+                      "timing": f"{n} rounds as one span in a CUDA graph; calls: medians of "
+                                "in-graph events"}), flush=True)
+
+
+def run_kv_once(args):
+    """N untimed rounds through the key/value cache (for ncu captures)."""
+    dev = torch.device("cuda", 0)
+    kv = KvRounds(dev, args.once)
+    for _ in range(args.once):
+        for _, call in kv.calls(torch.cuda.current_stream(dev)):
+            call()
+    torch.cuda.synchronize()
+    kv.check(torch.cuda.current_stream(dev))
+    print(json.dumps({"kv_once": args.once, "status": 0}))
+
+
 def run_tree_once(args):
     """N untimed tree verification calls on the bench's tree workload (for ncu)."""
     import speculative_decoding_verification_79_gb300 as sv
@@ -822,6 +946,8 @@ def main():
                     help="time the Markov logit-bias drafting loop")
     ap.add_argument("--tree", action="store_true",
                     help="time tree (multi-candidate) verification")
+    ap.add_argument("--kv", action="store_true",
+                    help="time tree decoding rounds through the key/value cache")
     ap.add_argument("--tree-B", type=lambda x: [int(v) for v in x.split(",")], default=[64],
                     help="batch sizes of --tree, comma-separated")
     ap.add_argument("--sweep-B", type=lambda x: [int(v) for v in x.split(",")], default=None)
@@ -834,6 +960,8 @@ def main():
         run_reference(args)
     elif args.once > 0 and args.tree:
         run_tree_once(args)
+    elif args.once > 0 and args.kv:
+        run_kv_once(args)
     elif args.once > 0 and args.markov:
         run_markov_once(args)
     elif args.once > 0 and args.calib:
@@ -848,6 +976,8 @@ def main():
         run_markov(args)
     elif args.tree:
         run_tree(args)
+    elif args.kv:
+        run_kv(args)
     else:
         run_gpu(args)
 
