@@ -260,14 +260,13 @@ __device__ __forceinline__ AtTile at_tile(const AttendArgs& A, const AtRow& r, i
   return t;
 }
 
-// Work is counted in key tiles, with AT_EXTRA more for each query tile: what its queries'
+// Work is counted in key tiles, with KV_EXTRA more for each query tile: what its queries'
 // conversion and its results cost. Its order is rows, query tiles, heads.
-constexpr int AT_EXTRA = KV_EXTRA;
 
 // Units of row b's query tile rt for one head (0: none).
 __device__ __forceinline__ int at_units(const AttendArgs& A, int b, int rt) {
   const AtRow r = at_row(A, b);
-  return rt < r.nrt ? AT_EXTRA + at_tile(A, r, rt).tiles() : 0;
+  return rt < r.nrt ? KV_EXTRA + at_tile(A, r, rt).tiles() : 0;
 }
 
 // The units of this CTA, one query tile after the other: key tiles i0 .. i1 - 1 of the
@@ -281,22 +280,21 @@ struct AtWalk {
 
   // The share of the current query tile; false when it has no key tile.
   __device__ __forceinline__ bool settle() {
-    const int stop = min(end, base + AT_EXTRA + tile.tiles());
-    i0 = max(0, at - base - AT_EXTRA);
-    i1 = max(0, stop - base - AT_EXTRA);
+    const int stop = min(end, base + KV_EXTRA + tile.tiles());
+    i0 = max(0, at - base - KV_EXTRA);
+    i1 = max(0, stop - base - KV_EXTRA);
     return i1 > i0;
   }
   // From unit `rem` of query tile rt0 of row b0 (all heads).
-  __device__ __noinline__ void start(const AttendArgs& A, int b0, int rt0, int rem, int from,
-                                     int to) {
+  __device__ __forceinline__ void start(const AttendArgs& A, int b0, int rt0, int rem, int from,
+                                        int to) {
     at = from;
     end = to;
-    if (at >= end) return;
     b = b0;
     rt = rt0;
     row = at_row(A, b);
     tile = at_tile(A, row, rt);
-    const int per = AT_EXTRA + tile.tiles();
+    const int per = KV_EXTRA + tile.tiles();
     h = rem / per;
     base = from - (rem - h * per);
     if (!settle()) next(A);
@@ -304,7 +302,7 @@ struct AtWalk {
   __device__ __forceinline__ bool live() const { return at < end; }
   __device__ __noinline__ void next(const AttendArgs& A) {
     do {
-      base += AT_EXTRA + tile.tiles();
+      base += KV_EXTRA + tile.tiles();
       at = base;
       if (at >= end) return;
       if (++h == A.C.heads) {
@@ -580,7 +578,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   __shared__ uint64_t sfull[3], pfull[3], pvdone[3], vchk[AT_MAX_RING], qfull, dfull[2], dempty[2], drain[2];
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
-  __shared__ int s_b0, s_rt0, s_rem, s_total, s_sum[AT_THREADS / 32];
+  __shared__ AtWalk s_walk;
+  __shared__ int s_total, s_sum[AT_THREADS / 32];
   // Per key tile and page of it: row of the pool (-1: none); key scale, log2 and inverse of
   // the value scale.
   __shared__ int s_y[AT_INFO][8];
@@ -684,7 +683,10 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   const int ctas = min(static_cast<int>(gridDim.x), total), cta = blockIdx.x;
   const int from = cta < ctas ? at_share(cta, total, ctas) : 0;
   const int to = cta < ctas ? at_share(cta + 1, total, ctas) : 0;
-  if (tid == 0) s_total = total;
+  if (tid == 0) {
+    s_total = total;
+    if (from >= to) s_walk.at = s_walk.end = 0;
+  }
   if (from < to) {
     int base = 0;
 #pragma unroll 1
@@ -696,9 +698,12 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         all = block_sum(c, &before);
       }
       if (from >= base + before && from < base + before + c) {
-        s_b0 = (p0 + tid) / nrt;
-        s_rt0 = (p0 + tid) % nrt;
-        s_rem = from - base - before;
+        // (One thread for all: its row's data and this code are at hand, which saves the
+        // copies 3,000 cycles before their first page.)
+        const int b = (p0 + tid) / nrt;
+        AtWalk walk;
+        walk.start(A, b, p0 + tid - b * nrt, from - base - before, from, to);
+        s_walk = walk;
       }
       base += all;
       if (base > from) break;
@@ -715,8 +720,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     // one per tile, written before the tile's barrier is armed. (An entry is used again 32
     // tiles later, and K is never more than its ring and three steps ahead of the rest.)
     fence_async_global();  // (what earlier kernels stored, before copies read it)
-    AtWalk walk;
-    walk.start(A, s_b0, s_rt0, s_rem, from, to);
+    AtWalk walk = s_walk;
     const int ppt = AT_KEYS >> C.lgp;             // pages per tile
     const int tpc = min(32 / ppt, AT_INFO / 4);   // tiles per chunk
     const int mt = lane / ppt, sub = lane - mt * ppt;
@@ -853,8 +857,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     // ---- V copies, the values of cut tiles, and in the pauses planning: the next item's
     // description and rows.
     fence_async_global();
-    AtWalk walk;
-    walk.start(A, s_b0, s_rt0, s_rem, from, to);
+    AtWalk walk = s_walk;
     const int ppt = AT_KEYS >> C.lgp;
     int k = 0, planned = 0;       // items planned, and their tiles
     bool more = true;
@@ -937,7 +940,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           it.pos_hi = walk.tile.pos_hi;
           it.ns = walk.tile.ns;
           it.lo = walk.tile.lo;
-          it.u0 = walk.base + AT_EXTRA;
+          it.u0 = walk.base + KV_EXTRA;
         }
         bool badtree = false;
         if (A.parent) {
