@@ -85,7 +85,7 @@ __device__ __forceinline__ uint4 quantise16(const float* f, float inv) {
 
 // grid (x: pages the new tokens can touch, y: heads, z: rows)
 template <typename E>
-__global__ void __launch_bounds__(AP_THREADS)
+__global__ void __launch_bounds__(AP_THREADS, sizeof(E) == 2 ? 4 : 2)
     kv_append_kernel(const KvCache C, const KvScratch S, int layer, const KvSrc ksrc,
                      const KvSrc vsrc, int T, const int32_t* n_new) {
   kv_enter();
@@ -114,12 +114,16 @@ __global__ void __launch_bounds__(AP_THREADS)
     const int i = t0 + r * AP_HALF;
     if (i < nv) keep[r].load(at(i));
   }
+  // So are this page's scales, when it holds older tokens.
+  const int p = hi > lo ? kv_page(C, b, j << C.lgp) : -1;
+  float* scale = (half ? C.vs : C.ks) + kv_sidx(C, layer, max(p, 0), h);
+  const float old = off && p >= 0 ? kv_ld(scale) : 0.f;
   bool fine = sane;
   if (sane) {  // every page that the row writes is its own
     const int j1 = (len + n - 1) >> C.lgp;
     for (int jj = j0 + tid; jj <= j1; jj += AP_THREADS) {
-      const int p = kv_page(C, b, jj << C.lgp);
-      fine = fine && p >= 0 && kv_ld(C.refs + p) == 1;
+      const int pj = kv_page(C, b, jj << C.lgp);
+      fine = fine && pj >= 0 && kv_ld(C.refs + pj) == 1;
     }
   }
   if (!__syncthreads_and(fine ? 1 : 0)) {
@@ -127,9 +131,7 @@ __global__ void __launch_bounds__(AP_THREADS)
     return;
   }
   if (hi <= lo) return;
-  const int p = kv_page(C, b, j << C.lgp);
   uint8_t* dst = (half ? C.v : C.k) + kv_block(C, layer, p, h);
-  float* scale = (half ? C.vs : C.ks) + kv_sidx(C, layer, p, h);
   float a = 0.f;
   bool odd = false;  // a value outside the scales' range
   auto see = [&](const Vec16<E>& x) {
@@ -161,7 +163,6 @@ __global__ void __launch_bounds__(AP_THREADS)
   for (int w = 0; w < AP_HALF / 32; ++w) a = fmaxf(a, s_max[half * (AP_HALF / 32) + w]);
   float s = kv_scale(a);
   if (off) {
-    const float old = *scale;
     s = fmaxf(s, old);
     if (s != old) {  // older tokens of the page, at its new scale
       const float f = old / s;
@@ -195,7 +196,6 @@ __global__ void __launch_bounds__(AP_THREADS)
     x.get(f);
     out[i] = quantise16(f, inv);
   }
-  __syncthreads();  // every thread has read the old scale
   if (t0 == 0) *scale = s;
 }
 
