@@ -13,7 +13,9 @@
 // to tensor memory and are multiplied from there.
 //
 // A thread owns a query row (a lane of the accumulator) and some of the tile's tokens, so
-// that the softmax needs no exchange but one vote between the four threads of a row. Sixteen
+// that the softmax needs no exchange but one vote between the four threads of a row. (With
+// tokens on the lanes instead, weights went through shared memory and sums across lanes: 472
+// instead of 292 us for trees of 16 nodes at the time.) Sixteen
 // tokens share a page: its key scale is a factor of their scores; its value scale is
 // folded into their weights (its logarithm added to the scores, so that no weight exceeds
 // the reference) and taken out of their sum again. The reference m of a row only moves when
@@ -30,9 +32,21 @@
 // results (output, m, sum) in the workspace, which a second kernel joins on all SMs.
 //
 // Warps, coupled by mbarriers: one copies K tiles page by page by tensor-map TMA (128-byte
-// swizzle) into a ring, another V tiles into a second (and plans the next query tile while
-// this one is in work); one issues the scores' products and one the output's; sixteen form
-// the weights, four on each quarter of a row copy's tokens.
+// swizzle) into a ring, another V tiles into a second (and looks through those whose weights
+// are cut, and plans the next query tile while this one is in work); one issues the scores'
+// products and one the output's; sixteen form the weights, four on each quarter of a row
+// copy's tokens.
+//
+// What bounds it. Up to dim 128 a key tile is 32 KB, 1,400 cycles of an SM's share of the
+// memory rate, and 20 products of 64 cycles; its softmax is a chain of waits, loads,
+// a vote, powers, splits and stores of about 1,500 cycles for 32 rows, 1,900 for 64 and 2,700
+// for 128, where the integer instructions of the split alone fill half of it. Measured on
+// 64 rows with 8 key/value heads of 128: single tokens of 8 queries a head, 4,100 tokens
+// cached in the mean, 127 us (4.2 TB/s, 62 % of a copy); blocks of 9 tokens of 4 queries,
+// 143 us; trees of 16 nodes of 8 queries, 173 us (480 TFLOP/s of the formula's, 2.5 times as
+// many of 8-bit products). A query tile costs about 9,000 cycles beside its key tiles, and a
+// launch 12,000 to 18,000 before the first (counting, page table, queries, each a trip to
+// memory), which is most of the 13 us of one row's single token.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -1378,8 +1392,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
 
 // Joins the partial results of the query tile that begins in CTA blockIdx.x and goes on in
 // others: a thread takes four components of a row over its CTAs, with the loads of four of
-// them in flight and a running reference. (A join by the last of the CTAs themselves held
-// up its SM for up to 27 us: 128 rows of 256 components are 128 KB a CTA.)
+// them in flight and a running reference. It reads what the CTAs left in L2: 2 to 3 us for
+// 30 MB. (A join by the last of the CTAs themselves held up its SM for up to 27 us: 128 rows
+// of 256 components are 128 KB a CTA.)
 constexpr int JOIN_THREADS = 256, JOIN_BLOCKS = 8;  // and blocks of a query tile
 __global__ void __launch_bounds__(JOIN_THREADS)
     kv_attend_join_kernel(const __grid_constant__ AttendArgs A, int bf16) {
@@ -1457,6 +1472,8 @@ cudaError_t launch_kv_attend(const AttendArgs& A, sv_dtype dt, cudaStream_t st) 
   P.qterms = P.bf16 ? 2 : 3;
   P.ndb = C.dim > 128 ? 2 : 1;
   const long long rows = (long long)A.T * A.group;
+  // The narrowest copy that holds the rows: 8 rows of 64 took 127 us with copies of 32, 141
+  // with 64 and 182 with 128; 36 rows 143 with 64 and 189 with 128.
   const int width = rows <= 32 ? 32 : (rows <= 64 ? 64 : 128);
   const size_t tile = (size_t)P.ndb * AT_BLK;
   // At least 39 components of 128 row copies, or 16 of them, which leaves room for one more
