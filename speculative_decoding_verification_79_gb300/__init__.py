@@ -511,9 +511,9 @@ def sv_kv_read(cache: KVCache, start, T, count=None, layer=0, n_layers=None,
         n_layers = c.layers - int(layer)
     shape = (int(n_layers), c.batch, int(T), c.heads, c.dim)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=dtype, device=start.device)
+        k_out = start.new_empty(shape, dtype=dtype)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=dtype, device=start.device)
+        v_out = start.new_empty(shape, dtype=dtype)
     for name, t in (("k_out", k_out), ("v_out", v_out)):
         _dev(t, name, dtype)
         if tuple(t.shape) != shape:
@@ -537,14 +537,14 @@ def sv_kv_attend(cache: KVCache, layer, q, n_new=None, parent=None, scale=None, 
         if parent.shape != shape[:2]:
             raise ValueError(f"parent must be [{cache.batch}, {T}]")
     if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        out = q.new_empty(shape)
     elif _dev(out, "out", q.dtype).shape != shape:
         raise ValueError("out must have q's shape")
     if lse is not None:
         if _dev(lse, "lse", torch.float32).shape != shape[:3]:
             raise ValueError("lse must have q's first three dimensions")
     elif want_lse:
-        lse = torch.empty(shape[:3], dtype=torch.float32, device=q.device)
+        lse = q.new_empty(shape[:3], dtype=torch.float32)
     _check("sv_kv_attend", load().sv_kv_attend(
         cache.ref, int(layer), _addr(q), _kv_dtype(q, "q"), row, tok, T, heads, _addr(n_new),
         _addr(parent), float(cache.dim ** -0.5 if scale is None else scale), int(window), int(sinks),
