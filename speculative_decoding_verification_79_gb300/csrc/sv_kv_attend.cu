@@ -8,8 +8,8 @@
 // operand is carried as a sum of 8-bit terms, multiplied one after the other into the same
 // float32 accumulator: a query row, scaled by a power of two to the e4m3 range, is exactly
 // the sum of two (bf16) or three (fp16) e4m3 terms down to 2^-18 of its largest component;
-// a weight is rounded to fp16 and split into three e5m2 terms of at least 9 bits in all
-// (e5m2 is fp16's upper byte, so a split is integer arithmetic). Weights go from registers
+// a weight is rounded to fp16 and split into three e5m2 terms (e5m2 is fp16's upper byte, so
+// a split is integer arithmetic). Weights go from registers
 // to tensor memory and are multiplied from there.
 //
 // A thread owns a query row (a lane of the accumulator) and some of the tile's tokens, so
@@ -70,7 +70,9 @@ constexpr int AT_THREADS = AT_SM0 + AT_SM_THREADS;
 constexpr int AT_BLK = AT_KEYS * 128;  // 128 tokens x 128 bytes
 constexpr int AT_MAX_RING = 8;   // most K tiles, and V tiles, in shared memory
 constexpr int AT_INFO = 32;      // key tiles whose page data are kept
-constexpr int AT_PTERMS = 3;
+constexpr int AT_PTERMS = 3;     // e5m2 terms of a weight
+template <bool BF16>
+constexpr int AT_QTERMS = BF16 ? 2 : 3;  // e4m3 terms of a query
 // Weights are kept as 2^(x - m + 11): up to 2^15 before the reference must move (below
 // e5m2's 57344). Their terms end at 2^-16, e5m2's smallest, so a weight has its 9 bits down
 // to 2^-19 of the reference and counts down to 2^-28. A larger shift would leave less room
@@ -218,8 +220,6 @@ __device__ __forceinline__ bool at_vote(int id, int n, bool x) {
 struct AttendPlan {
   int nk, nv;  // tiles of the rings
   int ndb;     // 128-byte blocks of a token's vector
-  int qterms;  // e4m3 terms of a query
-  int bf16;
   int join;    // floats of the buffer in which row copies are added
 };
 
@@ -448,9 +448,9 @@ __device__ __noinline__ void at_fetch(const AttendArgs& A, int ndb, const AtItem
     }
   }
 }
-template <int W>
-__device__ __noinline__ void at_convert(const AttendArgs& A, int terms, int ndb, int bf16,
-                                        const AtItem* it, unsigned char* Q, float* cs) {
+template <int W, bool BF16>
+__device__ __noinline__ void at_convert(const AttendArgs& A, int ndb, const AtItem* it,
+                                        unsigned char* Q, float* cs) {
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncwarp();
   const int hw = (threadIdx.x - AT_SM0) >> 4, l16 = threadIdx.x & 15;
@@ -468,8 +468,8 @@ __device__ __noinline__ void at_convert(const AttendArgs& A, int terms, int ndb,
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&xw[e]));
-        f[db][2 * e] = bf16 ? bf_lo(xw[e]) : y.x;
-        f[db][2 * e + 1] = bf16 ? bf_hi(xw[e]) : y.y;
+        f[db][2 * e] = BF16 ? bf_lo(xw[e]) : y.x;
+        f[db][2 * e + 1] = BF16 ? bf_hi(xw[e]) : y.y;
         a = fmaxf(a, fmaxf(fabsf(f[db][2 * e]), fabsf(f[db][2 * e + 1])));
       }
     }
@@ -486,7 +486,7 @@ __device__ __noinline__ void at_convert(const AttendArgs& A, int terms, int ndb,
       unsigned char* dst =
           Q + (size_t)db * AT_BLK + row * 128 + (((l16 >> 1) ^ (row & 7)) << 4) + (l16 & 1) * 8;
 #pragma unroll 1
-      for (int t = 0; t < terms; ++t) {
+      for (int t = 0; t < AT_QTERMS<BF16>; ++t) {
         uint2 o;
         o.x = e4m3x4(y[0], y[1], y[2], y[3]);
         o.y = e4m3x4(y[4], y[5], y[6], y[7]);
@@ -573,8 +573,9 @@ __device__ __noinline__ void at_land(uint64_t* full, int n, int g) {
     }
 }
 
-// W: rows of a copy (32, 64 or 128 >= the query rows of a tile).
-template <int W>
+// W: rows of a copy (32, 64 or 128 >= the query rows of a tile). BF16: type of the queries and
+// outputs (else fp16).
+template <int W, bool BF16>
 __global__ void __launch_bounds__(AT_THREADS, 1)
     kv_attend_kernel(const __grid_constant__ AttendArgs A, const __grid_constant__ AttendPlan P,
                      const __grid_constant__ CUtensorMap tmK,
@@ -619,7 +620,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int ndb = P.ndb, slot = ndb * AT_BLK;
   unsigned char* Qs = dsm;                                  // [terms][ndb][128][128]
-  unsigned char* Ks = Qs + P.qterms * slot;                 // [nk][ndb][128][128]
+  unsigned char* Ks = Qs + AT_QTERMS<BF16> * slot;                 // [nk][ndb][128][128]
   unsigned char* Vs = Ks + (size_t)P.nk * slot;             // [nv][ndb][128][128]
   float* joinb = reinterpret_cast<float*>(Vs + (size_t)P.nv * slot);  // row copies being added
 
@@ -837,7 +838,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           tm_fence_after();
           const uint32_t d = tmem + scol + sb * 128, kd = ring0 + q * rstep;
           uint32_t acc = 0;
-          for (int t = 0; t < P.qterms; ++t)
+          for (int t = 0; t < AT_QTERMS<BF16>; ++t)
             for (int db = 0; db < ndb; ++db) {
               const uint32_t al = qd + (t * ndb + db) * (AT_BLK >> 4), bl = kd + db * (AT_BLK >> 4);
               const int kn = ksteps - 4 * db;
@@ -1081,7 +1082,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     };
     auto convert = [&](int k) {
       if (!dead && s_item[k & 1].m > 0)
-        at_convert<W>(A, P.qterms, ndb, P.bf16, &s_item[k & 1], Qs, s_c[k & 1]);
+        at_convert<W, BF16>(A, ndb, &s_item[k & 1], Qs, s_c[k & 1]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&qfull);
     };
@@ -1211,11 +1212,10 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           }
           // Weights: 2^x, summed with the value scale taken out, rounded to fp16 and split. A
           // term is the upper byte of what is left of the fp16 number; the rest after it is
-          // exact. The second and third are rounded (halves away from zero). The first is
-          // cut off: of an 11-bit number that leaves 8 bits, of those the second at most 4
-          // (and a sign) and the third none but an error of 2^-10. (Rounding it as well would
-          // not make that smaller, and an addition a pair is 3 % of the time: the kernel is
-          // bound by such integer instructions with 128 rows.)
+          // exact. Rounding each term (halves away from zero) splits all of its 11 bits. For
+          // bf16 outputs, which keep 8, the first term is cut off instead: the three are then
+          // off by up to 2^-10 (2^-12 in the mean square, to both sides), and an addition a
+          // pair is saved, 3 % of the time with 128 rows, which such instructions bound.
 #pragma unroll
           for (int c = 0; c < NC; c += GC) {
             uint32_t t[AT_PTERMS][GC / 2];
@@ -1227,7 +1227,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
               __half2 y = __floats2half2_rn(p.x, p.y);
 #pragma unroll
               for (int k = 0; k < AT_PTERMS; ++k) {
-                t[k][e] = *reinterpret_cast<const uint32_t*>(&y) + (k ? 0x00800080u : 0u);
+                t[k][e] = *reinterpret_cast<const uint32_t*>(&y) + (BF16 && k == 0 ? 0u : 0x00800080u);
                 const uint32_t hi = t[k][e] & 0xff00ff00u;
                 y = __hsub2(y, *reinterpret_cast<const __half2*>(&hi));
               }
@@ -1314,8 +1314,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
 #pragma unroll
             for (int e = 0; e < 16; e += 8)
               to[e / 8] = make_uint4(
-                  at_pack(o[e], o[e + 1], P.bf16), at_pack(o[e + 2], o[e + 3], P.bf16),
-                  at_pack(o[e + 4], o[e + 5], P.bf16), at_pack(o[e + 6], o[e + 7], P.bf16));
+                  at_pack(o[e], o[e + 1], BF16), at_pack(o[e + 2], o[e + 3], BF16),
+                  at_pack(o[e + 4], o[e + 5], BF16), at_pack(o[e + 6], o[e + 7], BF16));
           } else {
             float4* to = reinterpret_cast<float4*>(A.S.part) + at_part(slot_id, r, c, C.dim);
 #pragma unroll
@@ -1358,7 +1358,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
               y.w += j[3];
             }
             if (whole)
-              at_store4(A.out, s_out[kb][rr] * C.dim + c + d, y, P.bf16);
+              at_store4(A.out, s_out[kb][rr] * C.dim + c + d, y, BF16);
             else
               reinterpret_cast<float4*>(A.S.part)[at_part(slot_id, rr, c + d, C.dim)] = y;
           }
@@ -1455,21 +1455,22 @@ __global__ void __launch_bounds__(JOIN_THREADS)
 constexpr size_t AT_SMEM = 232448, AT_STATIC = 20480;
 
 cudaError_t launch_kv_attend(const AttendArgs& A, sv_dtype dt, cudaStream_t st) {
+  typedef void (*Kernel)(const AttendArgs, const AttendPlan, const CUtensorMap, const CUtensorMap);
+  static const Kernel kernels[2][3] = {
+      {kv_attend_kernel<32, false>, kv_attend_kernel<64, false>, kv_attend_kernel<128, false>},
+      {kv_attend_kernel<32, true>, kv_attend_kernel<64, true>, kv_attend_kernel<128, true>}};
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
   std::call_once(once, [] {
-    const void* ks[3] = {reinterpret_cast<const void*>(kv_attend_kernel<32>),
-                         reinterpret_cast<const void*>(kv_attend_kernel<64>),
-                         reinterpret_cast<const void*>(kv_attend_kernel<128>)};
-    for (int i = 0; i < 3 && attr == cudaSuccess; ++i)
-      attr = cudaFuncSetAttribute(ks[i], cudaFuncAttributeMaxDynamicSharedMemorySize,
+    for (int i = 0; i < 6 && attr == cudaSuccess; ++i)
+      attr = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernels[i / 3][i % 3]),
+                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   (int)(AT_SMEM - AT_STATIC));
   });
   if (attr != cudaSuccess) return attr;
   const KvCache& C = A.C;
   AttendPlan P;
-  P.bf16 = dt == SV_BF16;
-  P.qterms = P.bf16 ? 2 : 3;
+  const bool bf16 = dt == SV_BF16;
   P.ndb = C.dim > 128 ? 2 : 1;
   const long long rows = (long long)A.T * A.group;
   // The narrowest copy that holds the rows: 8 rows of 64 took 127 us with copies of 32, 141
@@ -1479,7 +1480,7 @@ cudaError_t launch_kv_attend(const AttendArgs& A, sv_dtype dt, cudaStream_t st) 
   // At least 39 components of 128 row copies, or 16 of them, which leaves room for one more
   // tile of 256 bytes a token.
   P.join = width == 128 ? 0 : 128 * (P.ndb == 1 ? 40 : 17);
-  const size_t fixed = 1024 + P.qterms * tile + 4 * P.join;
+  const size_t fixed = 1024 + (bf16 ? AT_QTERMS<true> : AT_QTERMS<false>) * tile + 4 * P.join;
   const int ring = (int)((AT_SMEM - AT_STATIC - fixed) / tile);
   P.nk = ring / 2 < AT_MAX_RING ? ring / 2 : AT_MAX_RING;
   P.nv = ring - ring / 2 < AT_MAX_RING ? ring - ring / 2 : AT_MAX_RING;
@@ -1506,11 +1507,10 @@ cudaError_t launch_kv_attend(const AttendArgs& A, sv_dtype dt, cudaStream_t st) 
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
     return e;
   const int grid = sms < KV_MAX_CTAS ? sms : KV_MAX_CTAS;
-  const auto kernel = width == 32 ? kv_attend_kernel<32>
-                                  : (width == 64 ? kv_attend_kernel<64> : kv_attend_kernel<128>);
+  const Kernel kernel = kernels[bf16][width == 32 ? 0 : (width == 64 ? 1 : 2)];
   if ((e = kv_launch(kernel, dim3(grid), AT_THREADS, smem, st, A, P, tm[0], tm[1])) != cudaSuccess)
     return e;
-  return kv_launch(kv_attend_join_kernel, dim3(grid, JOIN_BLOCKS), JOIN_THREADS, 0, st, A, P.bf16);
+  return kv_launch(kv_attend_join_kernel, dim3(grid, JOIN_BLOCKS), JOIN_THREADS, 0, st, A, bf16 ? 1 : 0);
 }
 
 }  // namespace sv
