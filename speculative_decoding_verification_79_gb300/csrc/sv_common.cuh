@@ -39,7 +39,6 @@ constexpr long long WAIT_CYCLES = 4000000000LL;  // ~2 s at 2 GHz: bound on any 
 // caller).
 constexpr uint32_t ST_DEVICE_INPUT = 1u;
 constexpr uint32_t ST_TIMEOUT = 2u;
-constexpr uint32_t ST_NO_PAGES = 4u;
 
 // ---------------------------------------------------------------------------
 // Workspace layout (computed identically on host and device from B, K, V).

@@ -18,6 +18,9 @@ struct KvCache {
   int lgp;           // log2(page)
 };
 
+// Status bit of the cache calls, beside those of every workspace header.
+constexpr uint32_t ST_NO_PAGES = 4u;
+
 // Workspace: header, then the snapshot that sv_kv_fork reads while it rewrites rows, the
 // list of fresh pages, a flag per row, and the attention's partial results.
 constexpr int KV_MAX_CTAS = 160;  // persistent CTAs of the attention kernel
