@@ -384,6 +384,15 @@ __device__ __forceinline__ size_t at_part(int id, int r, int c, int dim) {
   return ((size_t)id * (dim / 4) + c / 4) * KV_ROWS + r;
 }
 
+// log2 of a positive normal number (or NaN): its exponent, and the hardware's logarithm of the
+// rest, which is good to 2^-22 there.
+__device__ __forceinline__ float at_log2(float x) {
+  const uint32_t u = __float_as_uint(x);
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(__uint_as_float((u & 0x7fffffu) | 0x3f800000u)));
+  return x == x ? static_cast<float>(static_cast<int>(u >> 23) - 127) + y : x;
+}
+
 // Has it been WAIT_CYCLES since the first call with *t0 == 0?
 __device__ __forceinline__ bool at_expired(long long* t0) {
   const long long t = clock64();
@@ -1296,7 +1305,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         if (!whole)
           A.S.stat[(size_t)slot_id * KV_ROWS + r] = make_float2(ref, sum);
         else if (A.lse)
-          A.lse[s_out[kb][r]] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+          A.lse[s_out[kb][r]] = sum == 0.f ? -INFINITY : (ref + at_log2(sum)) * 0.6931471805599453f;
       }
       if constexpr (COPIES == 1) {
         // A row's 16 components are whole sectors: straight from the accumulator.
@@ -1325,43 +1334,53 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         }
       } else {
         // Copies are added in shared memory, as many components at a time (a multiple of 8)
-        // as fit there for the item's rows.
-        const int R = it.R, fit = (P.join / (COPIES * R) - 1) & ~7, line = min(fit, C.dim) + 1;
+        // as fit there for the item's rows. (A row's stride is four floats more, so that
+        // neither rows nor columns meet in a bank, 16 bytes at a time.)
+        const int R = it.R, fit = (P.join / (COPIES * R) - 4) & ~7, line = min(fit, C.dim) + 4;
 #pragma unroll 1
         for (int c = 0; c < C.dim; c += fit) {
           const int n = min(fit, C.dim - c);
 #pragma unroll 1
-          for (int d = part * 8; live && d < n; d += 8 * AT_PARTS) {
-            float o[8];
-            tm_ld8(tl + c + d, o);
-            tm_wait_ld<8>(o);
+          for (int d0 = part * 8; live && d0 < n; d0 += 16 * AT_PARTS) {
+            float o[2][8];
+            tm_ld8(tl + c + d0, o[0]);
+            const int d1 = d0 + 8 * AT_PARTS;
+            if (d1 < n) tm_ld8(tl + c + d1, o[1]);
+            tm_wait_ld<16>(o[0]);
             if (!real) continue;
+            float* to = joinb + (copy * R + r) * line;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              joinb[(copy * R + r) * line + d + e] = f == 0.f ? 0.f : o[e] * f;
+            for (int u = 0; u < 2; ++u) {
+              if (u && d1 >= n) break;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o[u][e] = f == 0.f ? 0.f : o[u][e] * f;
+              float4* at = reinterpret_cast<float4*>(to + (u ? d1 : d0));
+              at[0] = make_float4(o[u][0], o[u][1], o[u][2], o[u][3]);
+              at[1] = make_float4(o[u][4], o[u][5], o[u][6], o[u][7]);
+            }
           }
           at_bar(5, AT_SM_THREADS);
-          // Four components each: neighbours take a row's in the result, a column's in partial
-          // results.
-          const int inner = whole ? n / 4 : R;
+          // Four components to a thread: of a row in the result, of a column in partial results.
+          const int wi = w - 4, inner = whole ? n / 4 : R, outer = whole ? R : n / 4;
 #pragma unroll 1
-          for (int e = st; e < R * (n / 4); e += AT_SM_THREADS) {
-            const int hi = e / inner, lo = e - hi * inner;
-            const int rr = whole ? hi : lo, d = 4 * (whole ? lo : hi);
-            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int a = wi; a < outer; a += AT_SM_WARPS)
+#pragma unroll 1
+            for (int b = lane; b < inner; b += 32) {
+              const int rr = whole ? a : b, d = 4 * (whole ? b : a);
+              float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int k = 0; k < COPIES; ++k) {
-              const float* j = joinb + (k * R + rr) * line + d;
-              y.x += j[0];
-              y.y += j[1];
-              y.z += j[2];
-              y.w += j[3];
+              for (int k = 0; k < COPIES; ++k) {
+                const float4 x = *reinterpret_cast<const float4*>(joinb + (k * R + rr) * line + d);
+                y.x += x.x;
+                y.y += x.y;
+                y.z += x.z;
+                y.w += x.w;
+              }
+              if (whole)
+                at_store4(A.out, s_out[kb][rr] * C.dim + c + d, y, BF16);
+              else
+                reinterpret_cast<float4*>(A.S.part)[at_part(slot_id, rr, c + d, C.dim)] = y;
             }
-            if (whole)
-              at_store4(A.out, s_out[kb][rr] * C.dim + c + d, y, BF16);
-            else
-              reinterpret_cast<float4*>(A.S.part)[at_part(slot_id, rr, c + d, C.dim)] = y;
-          }
           at_bar(5, AT_SM_THREADS);
         }
       }
@@ -1477,9 +1496,9 @@ cudaError_t launch_kv_attend(const AttendArgs& A, sv_dtype dt, cudaStream_t st) 
   // with 64 and 182 with 128; 36 rows 143 with 64 and 189 with 128.
   const int width = rows <= 32 ? 32 : (rows <= 64 ? 64 : 128);
   const size_t tile = (size_t)P.ndb * AT_BLK;
-  // At least 39 components of 128 row copies, or 16 of them, which leaves room for one more
+  // At least 32 components of 128 row copies, or 16 of them, which leaves room for one more
   // tile of 256 bytes a token.
-  P.join = width == 128 ? 0 : 128 * (P.ndb == 1 ? 40 : 17);
+  P.join = width == 128 ? 0 : 128 * (P.ndb == 1 ? 40 : 20);
   const size_t fixed = 1024 + (bf16 ? AT_QTERMS<true> : AT_QTERMS<false>) * tile + 4 * P.join;
   const int ring = (int)((AT_SMEM - AT_STATIC - fixed) / tile);
   P.nk = ring / 2 < AT_MAX_RING ? ring / 2 : AT_MAX_RING;
