@@ -752,3 +752,23 @@ def test_calls_back_to_back(sv):
                       [t for o in outs for t in o])
     for a, b in zip(*states):
         assert torch.equal(a, b)
+
+
+@needs_cuda
+@pytest.mark.parametrize("B,T,heads,group,window", [(700, 2, 1, 2, 0), (1500, 1, 2, 1, 5),
+                                                    (1, 2600, 1, 40, 0), (2, 900, 1, 128, 300)])
+def test_attend_many_query_tiles(sv, B, T, heads, group, window):
+    """More query tiles than a CTA has threads, one or many to a row, rows without any among
+    them."""
+    rng = np.random.default_rng(B + T)
+    lens = [int(x) for x in rng.integers(0, 40, B)]
+    n = [int(x) for x in rng.integers(0, T + 1, B)] if B > 2 else [T] * B
+    both = Both(sv, 1, B * (-(-(40 + T) // 16) + 1), 16, heads, 16, B, -(-(40 + T) // 16) + 1)
+    both.fill(lens, 3)
+    assert all(both.reserve(n))
+    k, v = rand_kv(both.r, T, 9)
+    both.append(0, k, v, n)
+    q = torch.randn(B, T, heads * group, 16, device="cuda").to(torch.bfloat16)
+    check_attend(both, 0, q, n, window=window,
+                 rows=sorted({0, B - 1, *(int(x) for x in rng.integers(0, B, 60))}))
+    both.same()
