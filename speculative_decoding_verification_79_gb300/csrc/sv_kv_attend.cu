@@ -219,7 +219,6 @@ __device__ __forceinline__ bool at_vote(int id, int n, bool x) {
 // What a launch needs beside AttendArgs.
 struct AttendPlan {
   int nk, nv;  // tiles of the rings
-  int ndb;     // 128-byte blocks of a token's vector
   int join;    // floats of the buffer in which row copies are added
 };
 
@@ -457,8 +456,8 @@ __device__ __noinline__ void at_fetch(const AttendArgs& A, int ndb, const AtItem
     }
   }
 }
-template <int W, bool BF16>
-__device__ __noinline__ void at_convert(const AttendArgs& A, int ndb, const AtItem* it,
+template <int W, bool BF16, int NDB>
+__device__ __noinline__ void at_convert(const AttendArgs& A, const AtItem* it,
                                         unsigned char* Q, float* cs) {
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncwarp();
@@ -466,10 +465,10 @@ __device__ __noinline__ void at_convert(const AttendArgs& A, int ndb, const AtIt
   const uint32_t half = 0xffffu << (threadIdx.x & 16);  // (the other half may have no row)
 #pragma unroll 1
   for (int row = hw; row < it->R; row += 2 * AT_SM_WARPS) {
-    float f[2][8];
+    float f[NDB][8];
     float a = 0.f;
 #pragma unroll
-    for (int db = 0; db < 2; ++db) {
+    for (int db = 0; db < NDB; ++db) {
       uint4 x = make_uint4(0, 0, 0, 0);
       if (db * 128 + l16 * 8 < A.C.dim)
         x = *reinterpret_cast<const uint4*>(Q + at_raw(db, row, l16));
@@ -485,23 +484,23 @@ __device__ __noinline__ void at_convert(const AttendArgs& A, int ndb, const AtIt
     __syncwarp(half);  // the row is in registers: its place is free
 #pragma unroll
     for (int s = 8; s; s >>= 1) a = fmaxf(a, __shfl_xor_sync(half, a, s));
-    const float sc = kv_scale(a), inv = 1.f / sc;
+    const float sc = kv_scale(a);
+    const float inv = __uint_as_float((254u << 23) - __float_as_uint(sc));
 #pragma unroll
-    for (int db = 0; db < 2; ++db) {
-      if (db >= ndb) break;
+    for (int db = 0; db < NDB; ++db) {
       float y[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] = f[db][e] * inv;
       unsigned char* dst =
           Q + (size_t)db * AT_BLK + row * 128 + (((l16 >> 1) ^ (row & 7)) << 4) + (l16 & 1) * 8;
-#pragma unroll 1
+#pragma unroll
       for (int t = 0; t < AT_QTERMS<BF16>; ++t) {
         uint2 o;
         o.x = e4m3x4(y[0], y[1], y[2], y[3]);
         o.y = e4m3x4(y[4], y[5], y[6], y[7]);
 #pragma unroll
         for (int c = 0; c < 128 / W; ++c)
-          *reinterpret_cast<uint2*>(dst + (size_t)t * ndb * AT_BLK + c * W * 128) = o;
+          *reinterpret_cast<uint2*>(dst + (size_t)t * NDB * AT_BLK + c * W * 128) = o;
         const uint32_t ow[2] = {o.x, o.y};
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -583,8 +582,8 @@ __device__ __noinline__ void at_land(uint64_t* full, int n, int g) {
 }
 
 // W: rows of a copy (32, 64 or 128 >= the query rows of a tile). BF16: type of the queries and
-// outputs (else fp16).
-template <int W, bool BF16>
+// outputs (else fp16). NDB: 128-byte blocks of a token's vector.
+template <int W, bool BF16, int NDB>
 __global__ void __launch_bounds__(AT_THREADS, 1)
     kv_attend_kernel(const __grid_constant__ AttendArgs A, const __grid_constant__ AttendPlan P,
                      const __grid_constant__ CUtensorMap tmK,
@@ -594,8 +593,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   constexpr int GC = NC < 16 ? NC : 16;  // taken at a time
   // Tensor memory: the output's accumulator, then three of scores (two above dim 128). A
   // tile's weights (32 columns a term) replace its scores.
-  const int nsb = P.ndb == 1 ? 3 : 2;
-  const uint32_t scol = 128 * P.ndb;
+  constexpr int ndb = NDB, nsb = ndb == 1 ? 3 : 2;
+  constexpr uint32_t scol = 128 * ndb;
   extern __shared__ unsigned char dsm_raw[];
   __shared__ uint64_t kfull[AT_MAX_RING], kempty[AT_MAX_RING];
   __shared__ uint64_t vfull[AT_MAX_RING], vempty[AT_MAX_RING], tinfo[AT_INFO];
@@ -627,9 +626,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       (reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const KvCache& C = A.C;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int ndb = P.ndb, slot = ndb * AT_BLK;
+  constexpr int slot = ndb * AT_BLK;
   unsigned char* Qs = dsm;                                  // [terms][ndb][128][128]
-  unsigned char* Ks = Qs + AT_QTERMS<BF16> * slot;                 // [nk][ndb][128][128]
+  unsigned char* Ks = Qs + AT_QTERMS<BF16> * slot;          // [nk][ndb][128][128]
   unsigned char* Vs = Ks + (size_t)P.nk * slot;             // [nv][ndb][128][128]
   float* joinb = reinterpret_cast<float*>(Vs + (size_t)P.nv * slot);  // row copies being added
 
@@ -1091,7 +1090,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     };
     auto convert = [&](int k) {
       if (!dead && s_item[k & 1].m > 0)
-        at_convert<W, BF16>(A, ndb, &s_item[k & 1], Qs, s_c[k & 1]);
+        at_convert<W, BF16, NDB>(A, &s_item[k & 1], Qs, s_c[k & 1]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&qfull);
     };
@@ -1475,14 +1474,16 @@ constexpr size_t AT_SMEM = 232448, AT_STATIC = 20480;
 
 cudaError_t launch_kv_attend(const AttendArgs& A, sv_dtype dt, cudaStream_t st) {
   typedef void (*Kernel)(const AttendArgs, const AttendPlan, const CUtensorMap, const CUtensorMap);
-  static const Kernel kernels[2][3] = {
-      {kv_attend_kernel<32, false>, kv_attend_kernel<64, false>, kv_attend_kernel<128, false>},
-      {kv_attend_kernel<32, true>, kv_attend_kernel<64, true>, kv_attend_kernel<128, true>}};
+#define SV_ROW(bf16, ndb) \
+  { kv_attend_kernel<32, bf16, ndb>, kv_attend_kernel<64, bf16, ndb>, kv_attend_kernel<128, bf16, ndb> }
+  static const Kernel kernels[2][2][3] = {{SV_ROW(false, 1), SV_ROW(false, 2)},
+                                          {SV_ROW(true, 1), SV_ROW(true, 2)}};
+#undef SV_ROW
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
   std::call_once(once, [] {
-    for (int i = 0; i < 6 && attr == cudaSuccess; ++i)
-      attr = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernels[i / 3][i % 3]),
+    for (int i = 0; i < 12 && attr == cudaSuccess; ++i)
+      attr = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernels[i / 6][i / 3 % 2][i % 3]),
                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   (int)(AT_SMEM - AT_STATIC));
   });
@@ -1490,15 +1491,15 @@ cudaError_t launch_kv_attend(const AttendArgs& A, sv_dtype dt, cudaStream_t st) 
   const KvCache& C = A.C;
   AttendPlan P;
   const bool bf16 = dt == SV_BF16;
-  P.ndb = C.dim > 128 ? 2 : 1;
+  const int ndb = C.dim > 128 ? 2 : 1;
   const long long rows = (long long)A.T * A.group;
   // The narrowest copy that holds the rows: 8 rows of 64 took 127 us with copies of 32, 141
   // with 64 and 182 with 128; 36 rows 143 with 64 and 189 with 128.
   const int width = rows <= 32 ? 32 : (rows <= 64 ? 64 : 128);
-  const size_t tile = (size_t)P.ndb * AT_BLK;
+  const size_t tile = (size_t)ndb * AT_BLK;
   // At least 32 components of 128 row copies, or 16 of them, which leaves room for one more
   // tile of 256 bytes a token.
-  P.join = width == 128 ? 0 : 128 * (P.ndb == 1 ? 40 : 20);
+  P.join = width == 128 ? 0 : 128 * (ndb == 1 ? 40 : 20);
   const size_t fixed = 1024 + (bf16 ? AT_QTERMS<true> : AT_QTERMS<false>) * tile + 4 * P.join;
   const int ring = (int)((AT_SMEM - AT_STATIC - fixed) / tile);
   P.nk = ring / 2 < AT_MAX_RING ? ring / 2 : AT_MAX_RING;
@@ -1526,7 +1527,7 @@ cudaError_t launch_kv_attend(const AttendArgs& A, sv_dtype dt, cudaStream_t st) 
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
     return e;
   const int grid = sms < KV_MAX_CTAS ? sms : KV_MAX_CTAS;
-  const Kernel kernel = kernels[bf16][width == 32 ? 0 : (width == 64 ? 1 : 2)];
+  const Kernel kernel = kernels[bf16][ndb - 1][width == 32 ? 0 : (width == 64 ? 1 : 2)];
   if ((e = kv_launch(kernel, dim3(grid), AT_THREADS, smem, st, A, P, tm[0], tm[1])) != cudaSuccess)
     return e;
   return kv_launch(kv_attend_join_kernel, dim3(grid, JOIN_BLOCKS), JOIN_THREADS, 0, st, A, bf16 ? 1 : 0);
