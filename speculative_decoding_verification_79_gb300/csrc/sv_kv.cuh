@@ -25,10 +25,10 @@ constexpr uint32_t ST_NO_PAGES = 4u;
 // list of fresh pages, a flag per row, and the attention's partial results.
 constexpr int KV_MAX_CTAS = 160;  // persistent CTAs of the attention kernel
 constexpr int KV_ROWS = 128;      // most query rows of its tile
-// Work of a query tile beside its key tiles, in key tiles: 3, 4, 5, 6, 7 and 9 took 145, 131,
-// 128, 128, 130 and 131 us for single tokens of 64 rows, and 168, 169, 170, 173, 175 and 177
-// for trees of 16 nodes.
-constexpr int KV_EXTRA = 6;
+// Work of a query tile beside its key tiles, in key tiles: 5, 6, 7 and 8 took 119, 119, 121 and
+// 121 us for single tokens of 64 rows (3: 20 us more when it was swept), and 164, 166, 168 and
+// 168 for trees of 16 nodes.
+constexpr int KV_EXTRA = 5;
 
 // A query tile of the attention that begins in one CTA and goes on in others, up to `last`:
 // rows r0 .. r0 + R - 1 of (row b, head h). R = 0: the CTA has none.
@@ -120,17 +120,6 @@ __device__ __forceinline__ int kv_page(const KvCache& C, int b, int pos) {
   if (pos < 0 || j >= C.max_pages || j >= kv_ld(C.np + b)) return -1;
   const int p = kv_ld(C.table + (size_t)b * C.max_pages + j);
   return p >= 0 && p < C.pages ? p : -1;
-}
-
-// Does row b hold pages, in range, for the positions [lo, hi)? With `alone`, pages that
-// no other row holds. Called by one thread; the ranges it is used for are short.
-__device__ __forceinline__ bool kv_holds(const KvCache& C, int b, int lo, int hi, bool alone) {
-  if (lo < 0 || hi < lo) return false;
-  for (int j = lo >> C.lgp; (long long)j << C.lgp < hi; ++j) {
-    const int p = kv_page(C, b, j << C.lgp);
-    if (p < 0 || (alone && kv_ld(C.refs + p) != 1)) return false;
-  }
-  return true;
 }
 
 __device__ __forceinline__ void kv_report(WsHeader* hdr, uint32_t bits) {

@@ -297,10 +297,15 @@ __device__ bool commit_ok(const KvCache& C, int b, int acc, const int32_t* path,
   }
   if (good && acc >= 0) {
     const int last = path && acc > 0 ? kv_ld(path + (size_t)b * N + acc - 1) : acc;
-    if (lane == 0)
-      good = (long long)len + last < (1LL << 31) - 1 && kv_holds(C, b, len, len + last + 1, false) &&
-             (!mv || kv_holds(C, b, len, len + acc + 1, true));
-    good = __shfl_sync(0xffffffffu, good ? 1 : 0, 0);
+    good = (long long)len + last < (1LL << 31) - 1;
+    // The row holds the block's pages, and alone those that tokens move to. A lane a page.
+    bool bad = false;
+    if (good)
+      for (int j = (len >> C.lgp) + lane; j <= (len + last) >> C.lgp; j += 32) {
+        const int p = kv_page(C, b, j << C.lgp);
+        bad = bad || p < 0 || (mv && j <= (len + acc) >> C.lgp && kv_ld(C.refs + p) != 1);
+      }
+    good = good && !__any_sync(0xffffffffu, bad);
   }
   *moves = mv && good;
   return good;
