@@ -1058,13 +1058,15 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     const int copy = row / W, r = row % W;        // copy of query row r
     const int c0 = copy * W + part * NC;          // first of this thread's tokens
     const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    // Queries without a token and rows with wrong data: zeros or NaN.
-    for (long long u0 = (long long)blockIdx.x * AT_SM_WARPS + (w - 4);
-         u0 * 32 < (long long)C.batch * A.T; u0 += (long long)gridDim.x * AT_SM_WARPS) {
-      const long long u = u0 * 32 + lane;
+    // Queries without a token and rows with wrong data: zeros or NaN. Neighbouring queries go
+    // to different CTAs (the results of 32 may be half a megabyte), looked at by a lane each.
+    const int queries = C.batch * A.T, spread = static_cast<int>(gridDim.x) * AT_SM_WARPS;
+    const int first = static_cast<int>(gridDim.x) * (w - 4) + static_cast<int>(blockIdx.x);
+    for (int u0 = first; u0 < queries; u0 += 32 * spread) {
+      const long long u = u0 + (long long)lane * spread;
       int fill = 0;
-      if (u < (long long)C.batch * A.T) {
-        const int b = static_cast<int>(u / A.T), t = static_cast<int>(u - (long long)b * A.T);
+      if (u < queries) {
+        const int b = static_cast<int>(u) / A.T, t = static_cast<int>(u) - b * A.T;
         const AtRow rw = at_row(A, b);
         fill = rw.bad ? 2 : (t >= rw.n ? 1 : 0);
         if (rw.bad && t == 0) kv_report(A.S.hdr, ST_DEVICE_INPUT);
@@ -1074,7 +1076,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         const int j = __ffs(todo) - 1;
         todo &= todo - 1;
         const bool nan = __shfl_sync(0xffffffffu, fill, j) == 2;
-        const long long at = (u0 * 32 + j) * A.q_heads;
+        const long long at = (u0 + (long long)j * spread) * A.q_heads;
         const uint32_t x = nan ? 0x7fff7fffu : 0u;  // NaN in bf16 and fp16
         uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.out) + at * C.dim);
         for (int e = lane; e < A.q_heads * C.dim / 8; e += 32) o[e] = make_uint4(x, x, x, x);
