@@ -25,10 +25,10 @@ constexpr uint32_t ST_NO_PAGES = 4u;
 // list of fresh pages, a flag per row, and the attention's partial results.
 constexpr int KV_MAX_CTAS = 160;  // persistent CTAs of the attention kernel
 constexpr int KV_ROWS = 128;      // most query rows of its tile
-// Work of a query tile beside its key tiles, in key tiles: 5, 6, 7 and 8 took 119, 119, 121 and
-// 121 us for single tokens of 64 rows (3: 20 us more when it was swept), and 164, 166, 168 and
-// 168 for trees of 16 nodes.
-constexpr int KV_EXTRA = 5;
+// Work of a query tile beside its key tiles, in key tiles: 3, 4, 5, 6 and 7 took 130, 122, 122,
+// 122 and 123 us for single tokens of 64 rows, and 156, 148, 145, 143 and 145 for trees of 16
+// nodes.
+constexpr int KV_EXTRA = 6;
 
 // A query tile of the attention that begins in one CTA and goes on in others, up to `last`:
 // rows r0 .. r0 + R - 1 of (row b, head h). R = 0: the CTA has none.
