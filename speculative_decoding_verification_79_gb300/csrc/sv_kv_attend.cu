@@ -9,16 +9,16 @@
 // float32 accumulator: a query row, scaled by a power of two to the e4m3 range, is exactly
 // the sum of two (bf16) or three (fp16) e4m3 terms down to 2^-18 of its largest component;
 // a weight is rounded to fp16 and split into three e5m2 terms (e5m2 is fp16's upper byte, so
-// a split is integer arithmetic). Weights go from registers
-// to tensor memory and are multiplied from there.
+// a split is integer arithmetic). Weights go from registers to tensor memory and are
+// multiplied from there.
 //
 // A thread owns a query row (a lane of the accumulator) and some of the tile's tokens, so
 // that the softmax needs no exchange but one vote between the four threads of a row. (With
 // tokens on the lanes instead, weights went through shared memory and sums across lanes: 472
-// instead of 292 us for trees of 16 nodes at the time.) Sixteen
-// tokens share a page: its key scale is a factor of their scores; its value scale is
-// folded into their weights (its logarithm added to the scores, so that no weight exceeds
-// the reference) and taken out of their sum again. The reference m of a row only moves when
+// instead of 292 us for trees of 16 nodes, both as first built.) Sixteen tokens share a page:
+// its key scale is a factor of their scores; its value scale is folded into their weights
+// (its logarithm added to the scores, so that no weight exceeds the reference) and taken out
+// of their sum again. The reference m of a row only moves when
 // a score passes it by 2^4 (the accumulators are then rescaled), or with the first keys the
 // row sees.
 //
@@ -39,14 +39,14 @@
 //
 // What bounds it. Up to dim 128 a key tile is 32 KB, 1,400 cycles of an SM's share of the
 // memory rate, and 20 products of 64 cycles; its softmax is a chain of waits, loads,
-// a vote, powers, splits and stores of about 1,500 cycles for 32 rows, 1,900 for 64 and 2,700
+// a vote, powers, splits and stores of about 1,600 cycles for 32 rows, 1,800 for 64 and 2,500
 // for 128, where the integer instructions of the split alone fill half of it. Measured on
 // 64 rows with 8 key/value heads of 128: single tokens of 8 queries a head, 4,100 tokens
-// cached in the mean, 127 us (4.2 TB/s, 62 % of a copy); blocks of 9 tokens of 4 queries,
-// 143 us; trees of 16 nodes of 8 queries, 173 us (480 TFLOP/s of the formula's, 2.5 times as
-// many of 8-bit products). A query tile costs about 9,000 cycles beside its key tiles, and a
-// launch 12,000 to 18,000 before the first (counting, page table, queries, each a trip to
-// memory), which is most of the 13 us of one row's single token.
+// cached in the mean, 120 us (4.5 TB/s, 66 % of a copy); blocks of 9 tokens of 4 queries,
+// 134 us; trees of up to 16 nodes of 8 queries, 143 us (585 TFLOP/s of the formula's, 2.5
+// times as many of 8-bit products). A query tile costs 3,000 to 8,000 cycles beside its key
+// tiles, and a launch 11,000 to 18,000 before the first (counting, page table, queries, each
+// a trip to memory), which is most of the 13 us of one row's single token.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -581,7 +581,9 @@ __device__ __noinline__ void at_land(uint64_t* full, int n, int g) {
     }
 }
 
-// W: rows of a copy (32, 64 or 128 >= the query rows of a tile). BF16: type of the queries and
+// (The three are template parameters because the loops' registers and instruction fetches
+// matter: with the vector's width a variable, single tokens took 127 us instead of 120 and
+// trees 173 instead of 166.) W: rows of a copy (32, 64 or 128 >= the query rows of a tile). BF16: type of the queries and
 // outputs (else fp16). NDB: 128-byte blocks of a token's vector.
 template <int W, bool BF16, int NDB>
 __global__ void __launch_bounds__(AT_THREADS, 1)
@@ -1495,8 +1497,8 @@ cudaError_t launch_kv_attend(const AttendArgs& A, sv_dtype dt, cudaStream_t st) 
   const bool bf16 = dt == SV_BF16;
   const int ndb = C.dim > 128 ? 2 : 1;
   const long long rows = (long long)A.T * A.group;
-  // The narrowest copy that holds the rows: 8 rows of 64 took 127 us with copies of 32, 141
-  // with 64 and 182 with 128; 36 rows 143 with 64 and 189 with 128.
+  // The narrowest copy that holds the rows: 8 rows a head took 119 us with copies of 32, 123
+  // with 64 and 150 with 128 (64 rows of single tokens); 36 rows 134 with 64 and 158 with 128.
   const int width = rows <= 32 ? 32 : (rows <= 64 ? 64 : 128);
   const size_t tile = (size_t)ndb * AT_BLK;
   // At least 32 components of 128 row copies, or 16 of them, which leaves room for one more
