@@ -337,7 +337,7 @@ def test_rows_with_wrong_data_are_left_alone(sv):
 #    of dim products: scale * 2^-23 * sqrt(dim) * sum|q||k| at most for the orders used,
 #    taken as 2^-19; the exponential's argument and function: 2^-20 + 2^-22 |score|;
 #  - weights are carried in at least 9 bits with their own exponent: 2^-10 mean|v|, and
-#    one that small underflows only below 2^-30 of the largest;
+#    one that small underflows only below 2^-28 of the largest;
 #  - the sum of float32 weights and products: 2^-20.
 def bounds(o, lse, av, ab, qk, scale, dtype):
     d = scale * (2.0 ** -18 * qk + 2.0 ** -19 * ab) + 2.0 ** -20 + 2.0 ** -22 * scale * ab
