@@ -70,7 +70,8 @@ __global__ void __launch_bounds__(PG_THREADS, 1)
   __shared__ long long shl[64];
   extern __shared__ int end[];  // [batch] pages needed by rows 0 .. b, cut at pages + 1
   const int tid = threadIdx.x;
-  // Pages that row b needs in all, or -1 when its data is wrong.
+  // Pages that row b needs in all, or -1 when its data is wrong. (A negative n_pages is below
+  // that -1: compare the two only for h >= 0.)
   auto holds = [&](int b) -> long long {
     const int n = kv_ld(n_new + b), len = C.len[b], np = S.np[b];
     const long long h = ((long long)len + n + C.page - 1) >> C.lgp;
@@ -84,7 +85,7 @@ __global__ void __launch_bounds__(PG_THREADS, 1)
       S.np[b] = C.np[b];  // as it was: the row's own entry changes below
       const long long h = holds(b);
       if (h < 0) kv_report(S.hdr, ST_DEVICE_INPUT);
-      need = h > S.np[b] ? h - S.np[b] : 0;
+      need = h >= 0 && h > S.np[b] ? h - S.np[b] : 0;
     }
     long long total;
     const long long e = all + block_scan(need, shl, &total) + need;
@@ -113,7 +114,7 @@ __global__ void __launch_bounds__(PG_THREADS, 1)
   }
   for (int b = tid; b < C.batch; b += PG_THREADS) {
     const long long h = holds(b);
-    const bool needs = h > S.np[b], served = h >= 0 && (!needs || end[b] <= got);
+    const bool needs = h >= 0 && h > S.np[b], served = h >= 0 && (!needs || end[b] <= got);
     if (needs && served) C.np[b] = static_cast<int>(h);
     if (needs && !served) kv_report(S.hdr, ST_NO_PAGES);
     if (ok) ok[b] = served ? 1 : 0;

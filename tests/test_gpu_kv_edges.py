@@ -1,0 +1,50 @@
+"""The key/value cache calls on wrong device data, at the ends of their ranges and on streams
+and devices other than their own."""
+import pytest
+import torch
+
+from test_gpu_kv import Both, i32, needs_cuda
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def sv():
+    import speculative_decoding_verification_79_gb300 as m
+
+    m.load()
+    return m
+
+
+@needs_cuda
+@pytest.mark.parametrize("row", [0, 1, 3])
+@pytest.mark.parametrize("held", [-1, -2, -7, -2 ** 31, 5, 2 ** 31 - 1])
+def test_reserve_with_wrong_page_counts(sv, row, held):
+    """A row whose n_pages is outside [0, max_pages] gets nothing, takes no page from the
+    others, and nothing outside the other rows' entries is written."""
+    both = Both(sv, 1, 12, 16, 1, 16, 4, 4)
+    both.reserve([20, 5, 33, 1])
+    both.same()
+    g = both.g
+    before = g.table.clone()
+    guard = torch.full((64 + g.table.numel(),), -7, dtype=torch.int32, device="cuda")
+    guard[32: 32 + g.table.numel()] = g.table.flatten()
+    g.c.table = guard[32:].data_ptr()  # the same table with entries of nobody around it
+    good = int(g.n_pages[row])
+    g.n_pages[row] = held
+    n = [40, 40, 40, 40]
+    ok = torch.full((4,), 9, dtype=torch.int32, device="cuda")
+    sv.sv_kv_reserve(g, i32(n), ok)
+    torch.cuda.synchronize()
+    assert g.status(clear=True) == sv.SV_ERR_DEVICE_INPUT
+    n[row] = 0
+    want = both.r.reserve(n)
+    want[row] = 0
+    assert ok.tolist() == want
+    assert int(g.n_pages[row]) == held
+    g.n_pages[row] = good
+    table = guard[32: 32 + g.table.numel()].view_as(before)
+    assert (table.cpu().numpy() == both.r.table()).all()
+    assert (guard[:32] == -7).all() and (guard[32 + g.table.numel():] == -7).all()
+    assert g.n_pages.tolist() == [len(x) for x in both.r.rows]
+    assert (g.refs.cpu().numpy() == both.r.refs).all()
