@@ -1087,9 +1087,15 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       }
     }
     bool dead = false;  // a wait gave up: skip the work, keep meeting the other warps
+    // A wait of these warps. Its lanes take up the answer together: loads and stores of the
+    // accumulators, and the warps' barriers, are for converged warps, and `dead` has to be the
+    // same in all of them.
+    auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, wait(bar, parity)) != 0;
+    };
     // The queries of item k: on their way, and into shared memory; then the scores may begin.
     auto fetch = [&](int k) {
-      if (!dead && !wait(&dfull[k & 1], (k >> 1) & 1)) dead = true;
+      if (!dead && !warp_wait(&dfull[k & 1], (k >> 1) & 1)) dead = true;
       if (!dead && s_item[k & 1].m > 0) at_fetch(A, ndb, &s_item[k & 1], Qs);
     };
     auto convert = [&](int k) {
@@ -1102,7 +1108,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     int sb = 0, sph = 0;  // accumulator of the tile's scores, and its pass
     auto done = [&]() {
       const int b = sb ? sb - 1 : nsb - 1;
-      return wait(&pvdone[b], (sb ? sph : sph - 1) & 1);
+      return warp_wait(&pvdone[b], (sb ? sph : sph - 1) & 1);
     };
     fetch(0);
     convert(0);
@@ -1110,7 +1116,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     bool opened = false;  // does a query tile that begins here go on in the next CTA?
     for (int item = 0;; ++item) {
       const int kb = item & 1;
-      if (!dead && !wait(&qfull, item & 1)) dead = true;
+      if (!dead && !warp_wait(&qfull, item & 1)) dead = true;
       // (The waits of a CTA give up together: see s_abort. Warps that saw the item must not
       // meet others that did not, so all of them agree first.)
       if (at_vote(5, AT_SM_THREADS, dead)) break;
@@ -1136,7 +1142,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         if (i == turn) kt = resume;
         const int key0 = kt * AT_KEYS;
         ++kt;
-        if (!dead && !wait(&sfull[sb], sph & 1)) dead = true;
+        if (!dead && !warp_wait(&sfull[sb], sph & 1)) dead = true;
         tm_fence_after();
         if (i == m - 1) fetch(item + 1);  // (the last scores are done: the queries' place is free)
         // Is there a key of the tile that some query does not see?
@@ -1177,7 +1183,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
               if (o > -32 && o < 64)
                 sees |= static_cast<uint32_t>(o >= 0 ? see >> o : see << -o) & at_below(len + it.n - k0);
             }
-            if (!dead && !wait(&vchk[cuts % AT_MAX_RING], (cuts / AT_MAX_RING) & 1)) dead = true;
+            if (!dead && !warp_wait(&vchk[cuts % AT_MAX_RING], (cuts / AT_MAX_RING) & 1)) dead = true;
             const uint32_t bad = s_vnan[cuts % AT_MAX_RING][c0 / 32] >> (c0 % 32);
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
@@ -1208,6 +1214,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             l *= fac;
 #pragma unroll
             for (int c = 0; c < NC; ++c) x[c] -= move;
+            __syncwarp();
             if (i > 0) {
               if (!dead && !done()) dead = true;
               tm_fence_after();
@@ -1310,6 +1317,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         else if (A.lse)
           A.lse[s_out[kb][r]] = sum == 0.f ? -INFINITY : (ref + at_log2(sum)) * 0.6931471805599453f;
       }
+      // (Lanes without a query row skip what follows a load; all are together again at the next.)
+      __syncwarp();
       if constexpr (COPIES == 1) {
         // A row's 16 components are whole sectors: straight from the accumulator.
 #pragma unroll 1
@@ -1317,23 +1326,25 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           float o[16];
           tm_ld16(tl + c, o);
           tm_wait_ld<16>(o);
-          if (!real) continue;
+          if (real) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = f == 0.f ? 0.f : o[e] * f;
-          if (whole) {
-            uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.out) +
-                                                 s_out[kb][r] * C.dim + c);
+            for (int e = 0; e < 16; ++e) o[e] = f == 0.f ? 0.f : o[e] * f;
+            if (whole) {
+              uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.out) +
+                                                   s_out[kb][r] * C.dim + c);
 #pragma unroll
-            for (int e = 0; e < 16; e += 8)
-              to[e / 8] = make_uint4(
-                  at_pack(o[e], o[e + 1], BF16), at_pack(o[e + 2], o[e + 3], BF16),
-                  at_pack(o[e + 4], o[e + 5], BF16), at_pack(o[e + 6], o[e + 7], BF16));
-          } else {
-            float4* to = reinterpret_cast<float4*>(A.S.part) + at_part(slot_id, r, c, C.dim);
+              for (int e = 0; e < 16; e += 8)
+                to[e / 8] = make_uint4(
+                    at_pack(o[e], o[e + 1], BF16), at_pack(o[e + 2], o[e + 3], BF16),
+                    at_pack(o[e + 4], o[e + 5], BF16), at_pack(o[e + 6], o[e + 7], BF16));
+            } else {
+              float4* to = reinterpret_cast<float4*>(A.S.part) + at_part(slot_id, r, c, C.dim);
 #pragma unroll
-            for (int e = 0; e < 16; e += 4)
-              to[e / 4 * KV_ROWS] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              for (int e = 0; e < 16; e += 4)
+                to[e / 4 * KV_ROWS] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            }
           }
+          __syncwarp();
         }
       } else {
         // Copies are added in shared memory, as many components at a time (a multiple of 8)
@@ -1350,17 +1361,19 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             const int d1 = d0 + 8 * AT_PARTS;
             if (d1 < n) tm_ld8(tl + c + d1, o[1]);
             tm_wait_ld<16>(o[0]);
-            if (!real) continue;
-            float* to = joinb + (copy * R + r) * line;
+            if (real) {
+              float* to = joinb + (copy * R + r) * line;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              if (u && d1 >= n) break;
+              for (int u = 0; u < 2; ++u) {
+                if (u && d1 >= n) break;
 #pragma unroll
-              for (int e = 0; e < 8; ++e) o[u][e] = f == 0.f ? 0.f : o[u][e] * f;
-              float4* at = reinterpret_cast<float4*>(to + (u ? d1 : d0));
-              at[0] = make_float4(o[u][0], o[u][1], o[u][2], o[u][3]);
-              at[1] = make_float4(o[u][4], o[u][5], o[u][6], o[u][7]);
+                for (int e = 0; e < 8; ++e) o[u][e] = f == 0.f ? 0.f : o[u][e] * f;
+                float4* at = reinterpret_cast<float4*>(to + (u ? d1 : d0));
+                at[0] = make_float4(o[u][0], o[u][1], o[u][2], o[u][3]);
+                at[1] = make_float4(o[u][4], o[u][5], o[u][6], o[u][7]);
+              }
             }
+            __syncwarp();
           }
           at_bar(5, AT_SM_THREADS);
           // Four components to a thread: of a row in the result, of a column in partial results.
@@ -1384,6 +1397,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
               else
                 reinterpret_cast<float4*>(A.S.part)[at_part(slot_id, rr, c + d, C.dim)] = y;
             }
+          __syncwarp();
           at_bar(5, AT_SM_THREADS);
         }
       }

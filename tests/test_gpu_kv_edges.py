@@ -3,7 +3,7 @@ and devices other than their own."""
 import pytest
 import torch
 
-from test_gpu_kv import Both, i32, needs_cuda
+from test_gpu_kv import Both, attend_case, i32, needs_cuda
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +48,16 @@ def test_reserve_with_wrong_page_counts(sv, row, held):
     assert (guard[:32] == -7).all() and (guard[32 + g.table.numel():] == -7).all()
     assert g.n_pages.tolist() == [len(x) for x in both.r.rows]
     assert (g.refs.cpu().numpy() == both.r.refs).all()
+
+
+@needs_cuda
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("dim", [128, 256])
+@pytest.mark.parametrize("T,group", [(1, 1), (1, 31), (3, 11), (9, 4), (1, 63), (5, 13), (9, 8),
+                                     (1, 97), (1, 127), (3, 43)])
+def test_attend_part_filled_warps(sv, T, group, dim, dtype):
+    """Query rows that fill a warp's lanes in part, in results that one CTA writes whole and in
+    such that are joined: every row's result is its own, and the lanes without a row write
+    nothing (the queries past a row's count are zeros)."""
+    attend_case(sv, [40, 9000], T, 1, group, dim, 64, dtype, seed=T + group, n_new=[T, T])
+    attend_case(sv, [9000, 40], T, 1, group, dim, 64, dtype, seed=T + group, n_new=[T, T - 1])
