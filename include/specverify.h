@@ -307,7 +307,8 @@ sv_status sv_verify_diag(const void *target_d, const void *draft_d, sv_dtype dty
 /*
  * sv_set_wait_limit: bound, in GPU clock cycles, on how long a verify call's warps
  * wait for results published by other warps (a row's partial sums, a request's
- * decision, a queued terminal job) before the call gives up: SV_ERR_TIMEOUT in the
+ * decision, a queued terminal job), and a cache attention's for one another (a tile's
+ * copies, products, weights), before the call gives up: SV_ERR_TIMEOUT in the
  * status word, outputs unspecified, the workspace left ready for the next call.
  * cycles <= 0 restores the default (about 2 s). Applies to calls made afterwards in
  * this process; returns the previous bound. A testing aid: the default is far above

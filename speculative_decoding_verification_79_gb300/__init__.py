@@ -348,7 +348,7 @@ def sv_verify(target, draft, draft_tok, verify_len, uniforms, temperature, ws: W
 
 
 def set_wait_limit(cycles: int) -> int:
-    """Bound (GPU clock cycles) on a verify call's waits for other warps' results;
+    """Bound (GPU clock cycles) on a verify or cache attention call's waits for other warps;
     cycles <= 0 restores the default. Returns the previous bound (a testing aid)."""
     return int(load().sv_set_wait_limit(int(cycles)))
 

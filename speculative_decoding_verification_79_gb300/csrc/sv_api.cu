@@ -159,9 +159,10 @@ sv_status sv_calib_update(double* stats_d, float* temps_d, int K, float lr, floa
 
 namespace sv {
 
-// Bound on a verify call's waits for other warps' results (clock cycles); a testing
-// aid can shorten it (sv_set_wait_limit).
+// Bound on a call's waits for other warps' results (clock cycles); a testing aid can
+// shorten it (sv_set_wait_limit).
 static std::atomic<long long> g_wait_limit{WAIT_CYCLES};
+long long wait_limit() { return g_wait_limit.load(std::memory_order_relaxed); }
 
 // Every host-side check of a verify call, then the kernel arguments (nothing is
 // enqueued here).
@@ -218,7 +219,7 @@ sv_status verify_prepare(const void* target_d, const void* draft_d, sv_dtype dty
   A.E2 = SLOT_BYTES / 2 / (int)eb;
   A.RS = L.RS;
   A.Rmax = L.Rmax;
-  A.wait_limit = g_wait_limit.load(std::memory_order_relaxed);
+  A.wait_limit = wait_limit();
   A.out_tok = out_tok_d;
   A.out_acc = out_accepted_d;
   A.out_p = out_p_d;

@@ -150,6 +150,7 @@ struct AttendArgs {
   const int32_t *n_new, *parent;
   float scale;  // scale * log2(e)
   int window, sinks;
+  long long wait_limit;  // bound, in clock cycles, on waits inside a CTA
   void* out;
   float* lse;
 };

@@ -182,6 +182,7 @@ sv_status sv_kv_attend(const sv_kv_cache* cache, int layer, const void* q_d, sv_
   A.scale = scale2;
   A.window = window;
   A.sinks = sinks;
+  A.wait_limit = wait_limit();
   A.out = out_d;
   A.lse = lse_d;
   return done(launch_kv_attend(A, dtype, static_cast<cudaStream_t>(stream)));

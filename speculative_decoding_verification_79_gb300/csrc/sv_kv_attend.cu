@@ -392,24 +392,24 @@ __device__ __forceinline__ float at_log2(float x) {
   return x == x ? static_cast<float>(static_cast<int>(u >> 23) - 127) + y : x;
 }
 
-// Has it been WAIT_CYCLES since the first call with *t0 == 0?
-__device__ __forceinline__ bool at_expired(long long* t0) {
+// Have `limit` cycles passed since the first call with *t0 == 0?
+__device__ __forceinline__ bool at_expired(long long* t0, long long limit) {
   const long long t = clock64();
   if (*t0 == 0) *t0 = t;
-  return t - *t0 > WAIT_CYCLES;
+  return t - *t0 > limit;
 }
 
 // The rest of a wait whose first probe (which suspends the thread for some microseconds at
 // most) was in vain. Bounded: false (and a report) when it runs out or another one has. Not
 // expanded at every wait: the kernel's loops share the instruction cache.
 __device__ __noinline__ bool at_wait_on(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                        WsHeader* hdr) {
+                                        const AttendArgs& A) {
   long long t0 = 0;
   while (!mbar_try(bar, parity)) {
     if (*abort) return false;
-    if (at_expired(&t0)) {
+    if (at_expired(&t0, A.wait_limit)) {
       *abort = 1;
-      kv_report(hdr, ST_TIMEOUT);
+      kv_report(A.S.hdr, ST_TIMEOUT);
       return false;
     }
   }
@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   float* joinb = reinterpret_cast<float*>(Vs + (size_t)P.nv * slot);  // row copies being added
 
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return mbar_try(bar, parity) || at_wait_on(bar, parity, &s_abort, A.S.hdr);
+    return mbar_try(bar, parity) || at_wait_on(bar, parity, &s_abort, A);
   };
 
   if (tid < AT_INFO) {
@@ -739,6 +739,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   tm_fence_after();
   const uint32_t tmem = s_tmem;
 
+  int copied = 0;  // tiles whose copies this warp has issued
   if (w == 0) {
     // ---- K copies. Pages are looked up for several tiles at a time, a page per lane and a
     // chunk ahead of their use; their data go to the other warps through a ring of entries,
@@ -823,9 +824,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         if (t == 0) look();
       }
     }
-    // After a wait gave up, let the copies already issued land before the CTA exits. (A
-    // stage's barrier whose last pass was consumed answers at once.)
-    if (s_abort) at_land(kfull, P.nk, g);
+    copied = g;
   } else if (w == 1) {
     // ---- Scores of a tile.
     if (at_elect()) {
@@ -936,7 +935,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       const int kb = k & 1;
       // (Item k's place is free once item k - 2 is done with.)
       if (!more || (k >= 2 && (ck < k - 1 || !ready(&dempty[kb], (k >> 1) - 1)))) {
-        if (__any_sync(0xffffffffu, s_abort || at_expired(&idle))) {
+        if (__any_sync(0xffffffffu, s_abort || at_expired(&idle, A.wait_limit))) {
           if (!s_abort) kv_report(A.S.hdr, ST_TIMEOUT);
           s_abort = 1;
           break;
@@ -1010,7 +1009,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       ++k;
       idle = 0;
     }
-    if (s_abort) at_land(vfull, P.nv, g);
+    copied = g;
   } else if (w == 3) {
     // ---- Outputs: O += P V of a tile, while the next tile's scores multiply and its weights
     // form.
@@ -1418,6 +1417,14 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
 
   tm_fence_before();
   __syncthreads();
+  // After a wait gave up, what is on its way to shared memory lands before the CTA exits, also
+  // the copies of a warp that was through before. (A stage's barrier whose last pass was
+  // consumed answers at once.)
+  if (s_abort) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (w == 0) at_land(kfull, P.nk, copied);
+    if (w == 2) at_land(vfull, P.nv, copied);
+  }
   if (w == 1) {
     __syncwarp();
     tm_fence_after();

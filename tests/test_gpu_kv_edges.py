@@ -61,3 +61,28 @@ def test_attend_part_filled_warps(sv, T, group, dim, dtype):
     nothing (the queries past a row's count are zeros)."""
     attend_case(sv, [40, 9000], T, 1, group, dim, 64, dtype, seed=T + group, n_new=[T, T])
     attend_case(sv, [9000, 40], T, 1, group, dim, 64, dtype, seed=T + group, n_new=[T, T - 1])
+
+
+@needs_cuda
+@pytest.mark.parametrize("dim,T,group,lens", [(128, 1, 8, [9000, 300]), (64, 9, 4, [20000, 17]),
+                                              (128, 16, 8, [3000, 9000]), (256, 40, 4, [700, 5000])])
+def test_attend_gives_up(sv, dim, T, group, lens):
+    """Waits with a bound that they pass, at the first of them or later: the call ends, says
+    SV_ERR_TIMEOUT, and the next call on the same workspace has the bits it had before."""
+    both, q, n, _ = attend_case(sv, lens, T, 2, group, dim, 64, torch.bfloat16, seed=T,
+                                n_new=[T, T])
+    g = both.g
+    want = [t.clone() for t in sv.sv_kv_attend(g, 0, q, n_new=i32(n), want_lse=True)]
+    torch.cuda.synchronize()
+    for limit in (1, 300, 1000, 3000, 10000, 30000, 1):
+        prev = sv.set_wait_limit(limit)
+        try:
+            sv.sv_kv_attend(g, 0, q, n_new=i32(n))
+            torch.cuda.synchronize()
+        finally:
+            sv.set_wait_limit(prev)
+        assert g.status() in ((sv.SV_ERR_TIMEOUT,) if limit == 1 else (sv.SV_OK, sv.SV_ERR_TIMEOUT))
+        got = sv.sv_kv_attend(g, 0, q, n_new=i32(n), want_lse=True)
+        torch.cuda.synchronize()
+        g.status(clear=True)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), limit
