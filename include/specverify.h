@@ -473,8 +473,9 @@ sv_status sv_kv_read(const sv_kv_cache *cache, int layer, int n_layers, const in
  *  lse_d      [batch, T, q_heads] float32 or NULL: log of the sum of exp(scale * q.k).
  * Query t of a row sees the cached tokens and, of the new ones, its ancestors and itself
  * (a chain: those up to t), as far as window and sinks allow. Scores, maximum, sum and
- * output are accumulated in float32; a weight (times its value's scale) below 2^-28 of the
- * row's largest may count as 0 in the output. Queries t >= n_new get 0 (lse -inf). A row with a
+ * output are accumulated in float32. In the output a weight is carried to 11 bits (off by up to
+ * 2^-11 of itself, rounded to nearest) and, times its value's scale, to 2^-28 of the row's
+ * largest such product: the smallest may count as 0. lse has the unrounded weights. Queries t >= n_new get 0 (lse -inf). A row with a
  * bad count or tree gets NaN in out and lse and sets SV_ERR_DEVICE_INPUT; a page that is
  * missing, out of range or has a scale outside [2^-64, 2^64] sets it too and gives NaN to
  * the queries that see a token of it. A NaN stored in the cache gives NaN to the queries

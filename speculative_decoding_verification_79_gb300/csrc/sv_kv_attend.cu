@@ -74,9 +74,9 @@ constexpr int AT_PTERMS = 3;     // e5m2 terms of a weight
 template <bool BF16>
 constexpr int AT_QTERMS = BF16 ? 2 : 3;  // e4m3 terms of a query
 // Weights are kept as 2^(x - m + 11): up to 2^15 before the reference must move (below
-// e5m2's 57344). Their terms end at 2^-16, e5m2's smallest, so a weight has its 9 bits down
-// to 2^-19 of the reference and counts down to 2^-28. A larger shift would leave less room
-// for later maxima and move references in more tiles.
+// e5m2's 57344). Their terms end at 2^-16, e5m2's smallest: a weight has its 11 bits down to
+// 2^-17 of the reference's, below that a resolution of 2^-27 of it. A larger shift would leave
+// less room for later maxima and move references in more tiles.
 constexpr float AT_SHIFT = 11.f, AT_LIMIT = 15.f;
 
 // Instruction descriptors of kind::f8f6f4 (float32 accumulator, M = 128), without N.
@@ -1228,12 +1228,13 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
               }
             }
           }
-          // Weights: 2^x, summed with the value scale taken out, rounded to fp16 and split. A
-          // term is the upper byte of what is left of the fp16 number; the rest after it is
-          // exact. Rounding each term (halves away from zero) splits all of its 11 bits. For
-          // bf16 outputs, which keep 8, the first term is cut off instead: the three are then
-          // off by up to 2^-10 (2^-12 in the mean square, to both sides), and an addition a
-          // pair is saved, 3 % of the time with 128 rows, which such instructions bound.
+          // Weights: 2^x, summed with the value scale taken out, rounded to fp16 (off by up to
+          // 2^-11) and split. A term is the upper byte of what is left of the fp16 number,
+          // rounded (halves away from zero); the rest after it is exact. Three terms hold all
+          // of its 11 bits down to a weight of 2^-6; below, they end at e5m2's smallest, 2^-16,
+          // so that a weight is off by up to 2^-17 (2^-28 of one at the reference). Cutting the
+          // first term off instead saves an addition a pair (trees of 16 nodes 145.5 us instead
+          // of 148.7), but the three are then off by up to 0.88 * 2^-10 on top.
 #pragma unroll
           for (int c = 0; c < NC; c += GC) {
             uint32_t t[AT_PTERMS][GC / 2];
@@ -1245,7 +1246,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
               __half2 y = __floats2half2_rn(p.x, p.y);
 #pragma unroll
               for (int k = 0; k < AT_PTERMS; ++k) {
-                t[k][e] = *reinterpret_cast<const uint32_t*>(&y) + (BF16 && k == 0 ? 0u : 0x00800080u);
+                t[k][e] = *reinterpret_cast<const uint32_t*>(&y) + 0x00800080u;
                 const uint32_t hi = t[k][e] & 0xff00ff00u;
                 y = __hsub2(y, *reinterpret_cast<const __half2*>(&hi));
               }
