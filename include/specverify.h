@@ -473,7 +473,9 @@ sv_status sv_kv_read(const sv_kv_cache *cache, int layer, int n_layers, const in
  *  lse_d      [batch, T, q_heads] float32 or NULL: log of the sum of exp(scale * q.k).
  * Query t of a row sees the cached tokens and, of the new ones, its ancestors and itself
  * (a chain: those up to t), as far as window and sinks allow. Scores, maximum, sum and
- * output are accumulated in float32. In the output a weight is carried to 11 bits (off by up to
+ * output are accumulated in float32. A query's component is exact, or off by up to 2^-21 (SV_BF16)
+ * or 2^-24 (SV_F16) of the largest of its token and head (or by 2^-78, when that is more), so
+ * that a score may be off by |scale| * 2^-21 (2^-24) * max|q| * sum|k|. In the output a weight is carried to 11 bits (off by up to
  * 2^-11 of itself, rounded to nearest) and, times its value's scale, to 2^-28 of the row's
  * largest such product: the smallest may count as 0. lse has the unrounded weights. Queries t >= n_new get 0 (lse -inf). A row with a
  * bad count or tree gets NaN in out and lse and sets SV_ERR_DEVICE_INPUT; a page that is

@@ -98,10 +98,24 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
+// The same for e5m2.
+__device__ __forceinline__ uint32_t e5m2x4(float a, float b, float c, float d) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+
 // Two e4m3 (the low 16 bits) as floats, exactly.
 __device__ __forceinline__ float2 e4m3_to_f2(uint16_t w) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(w));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// The same for e5m2, which is the upper byte of fp16.
+__device__ __forceinline__ float2 e5m2_to_f2(uint16_t w) {
+  const uint32_t h = __byte_perm(w, 0, 0x1404);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 

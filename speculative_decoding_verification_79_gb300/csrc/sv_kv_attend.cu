@@ -6,10 +6,13 @@
 // Both products run on the fifth-generation tensor cores with the cache's own e4m3 bytes as
 // the second operand, straight from TMA: nothing of the cache is converted. The first
 // operand is carried as a sum of 8-bit terms, multiplied one after the other into the same
-// float32 accumulator: a query row, scaled by a power of two to the e4m3 range, is exactly
-// the sum of two (bf16) or three (fp16) e4m3 terms down to 2^-18 of its largest component;
-// a weight is rounded to fp16 and split into three e5m2 terms (e5m2 is fp16's upper byte, so
-// a split is integer arithmetic). Weights go from registers to tensor memory and are
+// float32 accumulator. A query row, scaled by a power of two to the e4m3 range, is the sum of
+// an e4m3 term (4 bits) and one (bf16) or two (fp16) e5m2 terms for the rest: after rounding to
+// 4 bits the rest of bf16's 8 has 3, which e5m2 holds, and its exponents reach 2^-10 further
+// down. (With e4m3 for all terms they end at 2^-10, 2^-18 of the largest component.) That is
+// exact down to 2^-15 of the largest component, and off by up to 2^-21 (bf16) or 2^-24 (fp16)
+// of that one below. A weight is rounded to fp16 and split into three e5m2 terms (e5m2 is
+// fp16's upper byte, so a split is integer arithmetic). Weights go from registers to tensor memory and are
 // multiplied from there.
 //
 // A thread owns a query row (a lane of the accumulator) and some of the tile's tokens, so
@@ -72,7 +75,7 @@ constexpr int AT_MAX_RING = 8;   // most K tiles, and V tiles, in shared memory
 constexpr int AT_INFO = 32;      // key tiles whose page data are kept
 constexpr int AT_PTERMS = 3;     // e5m2 terms of a weight
 template <bool BF16>
-constexpr int AT_QTERMS = BF16 ? 2 : 3;  // e4m3 terms of a query
+constexpr int AT_QTERMS = BF16 ? 2 : 3;  // terms of a query: e4m3, then e5m2
 // Weights are kept as 2^(x - m + 11): up to 2^15 before the reference must move (below
 // e5m2's 57344). Their terms end at 2^-16, e5m2's smallest: a weight has its 11 bits down to
 // 2^-17 of the reference's, below that a resolution of 2^-27 of it. A larger shift would leave
@@ -80,8 +83,9 @@ constexpr int AT_QTERMS = BF16 ? 2 : 3;  // e4m3 terms of a query
 constexpr float AT_SHIFT = 11.f, AT_LIMIT = 15.f;
 
 // Instruction descriptors of kind::f8f6f4 (float32 accumulator, M = 128), without N.
-// Scores: A and B e4m3, K-major. Output: A e5m2 (tensor memory), B e4m3, MN-major.
-constexpr uint32_t AT_IDESC_S = (1u << 4) | (8u << 24);
+// Scores: A and B e4m3, K-major (A e5m2 for the later terms). Output: A e5m2 (tensor memory), B
+// e4m3, MN-major.
+constexpr uint32_t AT_IDESC_S = (1u << 4) | (8u << 24), AT_IDESC_E5M2_A = 1u << 7;
 constexpr uint32_t AT_IDESC_O = (1u << 4) | (1u << 7) | (1u << 16) | (8u << 24);
 
 // Descriptors are given as their low words (address and the unused leading offset) with the
@@ -427,7 +431,7 @@ __device__ __forceinline__ void at_drain(uint64_t* bar, bool abort) {
 
 // The queries of an item: half a warp takes a row, a lane eight components (sixteen above
 // dim 128). at_fetch copies them, as they are, to where the lane's own terms will be, so
-// that all rows are on their way at once; at_convert makes the terms: e4m3 in the layout of
+// that all rows are on their way at once; at_convert makes the terms: 8-bit in the layout of
 // a K-major operand, in each of the row's copies (W rows apart). The factor of a row's
 // scores is the power of two that its terms were divided by, times the call's scale; NaN
 // when a component is infinite, which the saturating terms would not show. (Rows past the
@@ -496,15 +500,16 @@ __device__ __noinline__ void at_convert(const AttendArgs& A, const AtItem* it,
 #pragma unroll
       for (int t = 0; t < AT_QTERMS<BF16>; ++t) {
         uint2 o;
-        o.x = e4m3x4(y[0], y[1], y[2], y[3]);
-        o.y = e4m3x4(y[4], y[5], y[6], y[7]);
+        o.x = t ? e5m2x4(y[0], y[1], y[2], y[3]) : e4m3x4(y[0], y[1], y[2], y[3]);
+        o.y = t ? e5m2x4(y[4], y[5], y[6], y[7]) : e4m3x4(y[4], y[5], y[6], y[7]);
 #pragma unroll
         for (int c = 0; c < 128 / W; ++c)
           *reinterpret_cast<uint2*>(dst + (size_t)t * NDB * AT_BLK + c * W * 128) = o;
         const uint32_t ow[2] = {o.x, o.y};
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float2 lo = e4m3_to_f2(ow[e] & 0xffffu), hi = e4m3_to_f2(ow[e] >> 16);
+          const float2 lo = t ? e5m2_to_f2(ow[e] & 0xffffu) : e4m3_to_f2(ow[e] & 0xffffu);
+          const float2 hi = t ? e5m2_to_f2(ow[e] >> 16) : e4m3_to_f2(ow[e] >> 16);
           y[4 * e] -= lo.x;
           y[4 * e + 1] -= lo.y;
           y[4 * e + 2] -= hi.x;
@@ -849,15 +854,16 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           uint32_t acc = 0;
           for (int t = 0; t < AT_QTERMS<BF16>; ++t)
             for (int db = 0; db < ndb; ++db) {
+              const uint32_t id = t ? ids | AT_IDESC_E5M2_A : ids;
               const uint32_t al = qd + (t * ndb + db) * (AT_BLK >> 4), bl = kd + db * (AT_BLK >> 4);
               const int kn = ksteps - 4 * db;
               if (kn >= 4) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                  umma_ss(d, al + 2 * k, bl + 2 * k, AT_HI, ids, k ? 1u : acc);
+                  umma_ss(d, al + 2 * k, bl + 2 * k, AT_HI, id, k ? 1u : acc);
               } else {
                 for (int k = 0; k < kn; ++k)
-                  umma_ss(d, al + 2 * k, bl + 2 * k, AT_HI, ids, k ? 1u : acc);
+                  umma_ss(d, al + 2 * k, bl + 2 * k, AT_HI, id, k ? 1u : acc);
               }
               acc = 1;
             }

@@ -26,6 +26,43 @@ def sv():
 W_REL, W_ABS, SUM = 2.0 ** -11, 2.0 ** -28, 2.0 ** -19
 
 
+# A query component: exact, or this much of the row's largest.
+Q_ABS = {torch.bfloat16: 2.0 ** -21, torch.float16: 2.0 ** -24}
+
+
+def per_key(q, k, v, L, n, scale, dtype, **mask):
+    """One row: the result in float64 (o [n, q_heads, dim], lse) and what a call's may be off by,
+    from an error of its own for each key's score:
+      d_j = scale (Q_ABS max|q| sum|k_j| + 2^-19 sum|q k_j|)     query terms, float32 sums
+            + 2^-20 + 2^-20 max|s|        the power; a score, the reference and its moves as
+                                          float32 numbers: 16 roundings of 2^-24
+    With weights w'_j = w_j e^(e_j), |e_j| <= d_j, the result moves by
+    sum w_j (e^(e_j) - 1)(v_j - o) / sum w'_j."""
+    T, Hq, D = q.shape
+    G = Hq // k.shape[1]
+    o, bo = np.zeros((n, Hq, D)), np.zeros((n, Hq, D))
+    lse, bl = np.zeros((n, Hq)), np.zeros((n, Hq))
+    for t in range(n):
+        see = kv_ref.visible(L, n, t, **mask)
+        for h in range(Hq):
+            kk, vv, x = k[see, h // G], v[see, h // G], q[t, h]
+            s = kk @ x * scale
+            m = s.max()
+            w = np.exp(s - m)
+            w /= w.sum()
+            d = abs(scale) * (Q_ABS[dtype] * np.abs(x).max() * np.abs(kk).sum(1)
+                              + 2.0 ** -19 * (np.abs(kk) @ np.abs(x)))
+            d += 2.0 ** -20 + 2.0 ** -20 * np.abs(s).max()
+            o[t, h] = w @ vv
+            lse[t, h] = np.log(np.exp(s - m).sum()) + m
+            move = (w * np.expm1(d)) @ np.abs(vv - o[t, h]) / (w @ np.exp(-d))
+            bo[t, h] = (torch.finfo(dtype).eps / 2 * (np.abs(o[t, h]) + move) + move
+                        + (W_REL + SUM) * (w @ np.abs(vv)) + W_ABS * np.abs(vv).sum(0)
+                        + torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps)
+            bl[t, h] = np.log(w @ np.exp(d)) + SUM + 2.0 ** -22 * abs(lse[t, h])
+    return o, lse, bo * 1.01, bl * 1.01
+
+
 def store(both, k, v):
     """One row's cache made of k, v [tokens, heads, dim] (numbers that e4m3 holds at the scales
     that append gives them)."""
@@ -67,3 +104,63 @@ def test_weights(sv, T, group, dtype):
     assert (np.abs(o) < av / 32).sum() > T * group  # (cancellations there are)
     assert (err <= bound).all(), float((err / bound).max())
     assert both.g.status() == 0
+
+
+@needs_cuda
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("dim,T,group", [(64, 1, 8), (128, 5, 7), (256, 3, 16), (128, 16, 8)])
+@pytest.mark.parametrize("ratio", [8, 10, 12, 15])
+def test_queries_with_one_large_channel(sv, ratio, dim, T, group, dtype):
+    """One channel of the queries 2^8 to 2^15 times the others, and keys that are zero there:
+    the scores come from the small ones alone, which keep their bits."""
+    L = 150
+    both = Both(sv, 1, 6, 64, 1, dim, 1, 6)
+    rng = np.random.default_rng(ratio + dim)
+    k = np.ldexp(rng.integers(8, 16, (L + T, 1, dim)), -3).astype(float)
+    k *= np.ldexp(rng.choice([-1.0, 1.0], (L + T, 1, dim)), rng.integers(0, 5, (L + T, 1, 1)))
+    k[..., 0] = 0.0
+    v = np.ldexp(rng.integers(-15, 16, (L + T, 1, dim)), -3).astype(float)
+    store(both, k, v)
+    both.commit([L - 1], L)
+    assert all(both.reserve([T]))
+    # Small channels of about 1 / 32, aligned with a few of the keys, so that these stand out.
+    q = 0.02 * rng.standard_normal((1, T, group, dim))
+    some = rng.integers(0, L, (T, group))
+    q[0] += 0.02 * np.sign(k[some, 0])
+    q[..., 0] = 2.0 ** (ratio - 5) * rng.uniform(1, 1.9, (1, T, group))
+    q = torch.from_numpy(q).to(dtype).cuda()
+    scale = 4 * dim ** -0.5
+    got = sv.sv_kv_attend(both.g, 0, q, n_new=i32([T]), scale=scale, want_lse=True)
+    o, lse, bo, bl = per_key(f64(q[0]), k, v, L, T, scale, dtype)
+    err, erl = np.abs(f64(got[0])[0] - o), np.abs(f64(got[1])[0] - lse)
+    assert (bo < np.abs(o)).mean() > 0.4  # a zero output would not pass
+    assert (err <= bo).all(), float((err / bo).max())
+    assert (erl <= bl).all(), float((erl / bl).max())
+    assert both.g.status() == 0
+
+
+@needs_cuda
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_queries_small_channels_together(sv, dim, dtype):
+    """Small channels that all have one value, at and below where a term of 8 bits ends, and
+    keys that add them up: what is lost of one is lost of all."""
+    L, T, group = 100, 8, 5
+    both = Both(sv, 1, 4, 64, 1, dim, 1, 4)
+    k, v = np.zeros((L + T, 1, dim)), np.zeros((L + T, 1, dim))
+    k[::2, 0, 1:] = 4.0
+    v[::2, 0], v[1::2, 0] = 1.0, -1.0
+    store(both, k, v)
+    both.commit([L - 1], L)
+    assert all(both.reserve([T]))
+    c = 0.998 * 2.0 ** -(np.arange(T * group) % 4) * np.linspace(1, 0.6, T * group)
+    q = np.zeros((1, T, group, dim))
+    q[0, ..., 1:] = (2.0 ** -4 * c).reshape(T, group, 1)
+    q[..., 0] = 448 * 2.0 ** 6
+    q = torch.from_numpy(q).to(dtype).cuda()
+    scale = 32 / dim
+    got = sv.sv_kv_attend(both.g, 0, q, n_new=i32([T]), scale=scale, want_lse=True)
+    o, lse, bo, bl = per_key(f64(q[0]), k, v, L, T, scale, dtype)
+    err, erl = np.abs(f64(got[0])[0] - o), np.abs(f64(got[1])[0] - lse)
+    assert (err <= bo).all(), float((err / bo).max())
+    assert (erl <= bl).all(), float((erl / bl).max())
