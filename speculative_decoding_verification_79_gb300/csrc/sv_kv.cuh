@@ -119,6 +119,37 @@ __device__ __forceinline__ float2 e5m2_to_f2(uint16_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// Is the positive scale s a power of two?
+__device__ __forceinline__ bool kv_pow2(float s) {
+  return (__float_as_uint(s) & 0x7fffffu) == 0;
+}
+
+// x * m / s so that rounding it to e4m3 rounds the exact value: x of 24 bits with m = 1, or an
+// e4m3 x with a scale m. The product is exact in double; the quotient's 53 bits tell values of
+// at most 28 by 24 bits from the points halfway between e4m3 numbers (5 bits), and so does its
+// cut to float with the rest marked in the lowest bit. (A quotient rounded to float may fall
+// on such a point.) For scales that another quantiser wrote: a power of two needs none of it.
+static __device__ __noinline__ float kv_quotient(float x, float m, float s) {
+  const double y = static_cast<double>(x) * m / s;
+  const float f = __double2float_rz(y);
+  return static_cast<double>(f) == y ? f : __uint_as_float(__float_as_uint(f) | 1u);
+}
+
+// Four e4m3 values at scale `from` (the bytes of w), at scale `to`.
+__device__ __forceinline__ uint32_t kv_rescale4(uint32_t w, float from, float to) {
+  const float2 lo = e4m3_to_f2(w & 0xffffu), hi = e4m3_to_f2(w >> 16);
+  float f[4] = {lo.x, lo.y, hi.x, hi.y};
+  if (kv_pow2(from) && kv_pow2(to)) {
+    const float r = from / to;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] *= r;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = kv_quotient(f[i], from, to);
+  }
+  return e4m3x4(f[0], f[1], f[2], f[3]);
+}
+
 // A load of data that an earlier kernel of the stream may have written. Not a read-only load:
 // those may be moved above the wait of kv_enter, and the data still changes while a kernel
 // that was brought up early is resident.

@@ -372,16 +372,12 @@ __global__ void __launch_bounds__(CM_THREADS)
     const int off = len & (C.page - 1);
     const float old = scale[kv_sidx(C, layer, s_dst[0], h)];
     if (off && s_ds[0] != old) {
-      const float f = old / s_ds[0];
       uint4* p = reinterpret_cast<uint4*>(pool + kv_block(C, layer, s_dst[0], h));
       for (int i = tid; i < off * vpt; i += CM_THREADS) {
         uint4 x = p[i];
         uint32_t* w = reinterpret_cast<uint32_t*>(&x);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 lo = e4m3_to_f2(w[j] & 0xffffu), hi = e4m3_to_f2(w[j] >> 16);
-          w[j] = e4m3x4(lo.x * f, lo.y * f, hi.x * f, hi.y * f);
-        }
+        for (int j = 0; j < 4; ++j) w[j] = kv_rescale4(w[j], old, s_ds[0]);
         p[i] = x;
       }
     }
@@ -389,13 +385,9 @@ __global__ void __launch_bounds__(CM_THREADS)
       const int t = i / vpt, c = i - t * vpt;
       uint4 x = buf[i];
       if (s_ss[t] != s_ds[t]) {
-        const float f = s_ss[t] / s_ds[t];
         uint32_t* w = reinterpret_cast<uint32_t*>(&x);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 lo = e4m3_to_f2(w[j] & 0xffffu), hi = e4m3_to_f2(w[j] >> 16);
-          w[j] = e4m3x4(lo.x * f, lo.y * f, hi.x * f, hi.y * f);
-        }
+        for (int j = 0; j < 4; ++j) w[j] = kv_rescale4(w[j], s_ss[t], s_ds[t]);
       }
       reinterpret_cast<uint4*>(pool + kv_block(C, layer, s_dst[t], h) +
                                (size_t)s_dslot[t] * C.dim)[c] = x;

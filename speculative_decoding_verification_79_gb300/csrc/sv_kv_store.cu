@@ -90,6 +90,23 @@ __device__ __forceinline__ uint4 quantise16(const float* f, float inv) {
   return o;
 }
 
+// The new values of a page (vectors of 16, vpt of them a token) at a scale that is no power of
+// two, which another quantiser gave the page.
+template <typename E>
+__device__ __noinline__ void append_any(const E* base, long long tok, int vpt, int nv, uint4* out,
+                                        float s) {
+  for (int i = threadIdx.x % AP_HALF; i < nv; i += AP_HALF) {
+    const int t = i / vpt;
+    Vec16<E> x;
+    x.load(base + t * tok + (i - t * vpt) * 16);
+    float f[16];
+    x.get(f);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) f[e] = kv_quotient(f[e], 1.f, s);
+    out[i] = quantise16(f, 1.f);
+  }
+}
+
 // grid (x: pages the new tokens can touch, y: heads, z: rows)
 template <typename E>
 __global__ void __launch_bounds__(AP_THREADS, sizeof(E) == 2 ? 4 : 2)
@@ -171,22 +188,32 @@ __global__ void __launch_bounds__(AP_THREADS, sizeof(E) == 2 ? 4 : 2)
   float s = kv_scale(a);
   if (off) {
     s = fmaxf(s, old);
-    if (s != old) {  // older tokens of the page, at its new scale
-      const float f = old / s;
+    if (s != old && kv_pow2(old) && kv_pow2(s)) {  // older tokens of the page, at its new scale
       for (int i = t0; i < off * vpt; i += AP_HALF) {
         uint4 x = reinterpret_cast<uint4*>(dst)[i];
         uint32_t* w = reinterpret_cast<uint32_t*>(&x);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float2 u = e4m3_to_f2(w[q] & 0xffffu), v = e4m3_to_f2(w[q] >> 16);
-          w[q] = e4m3x4(u.x * f, u.y * f, v.x * f, v.y * f);
-        }
+        for (int q = 0; q < 4; ++q) w[q] = kv_rescale4(w[q], old, s);
         reinterpret_cast<uint4*>(dst)[i] = x;
       }
     }
   }
-  const float inv = 1.f / s;
   uint4* out = reinterpret_cast<uint4*>(dst + (size_t)off * C.dim);
+  if (t0 == 0) *scale = s;
+  // (On a path of its own, which reads the values again: it leaves the registers to the rest.)
+  if (off && !(kv_pow2(old) && kv_pow2(s))) {
+    append_any<E>(base, src.tok, vpt, nv, out, s);
+    if (s != old)
+      for (int i = t0; i < off * vpt; i += AP_HALF) {
+        uint4 x = reinterpret_cast<uint4*>(dst)[i];
+        uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) w[q] = kv_rescale4(w[q], old, s);
+        reinterpret_cast<uint4*>(dst)[i] = x;
+      }
+    return;
+  }
+  const float inv = 1.f / s;
 #pragma unroll
   for (int r = 0; r < AP_CACHE; ++r) {
     const int i = t0 + r * AP_HALF;
@@ -203,7 +230,6 @@ __global__ void __launch_bounds__(AP_THREADS, sizeof(E) == 2 ? 4 : 2)
     x.get(f);
     out[i] = quantise16(f, inv);
   }
-  if (t0 == 0) *scale = s;
 }
 
 // One thread per 16 values; grid (x: vectors of one row and layer, y: rows, z: layers).

@@ -164,3 +164,104 @@ def test_queries_small_channels_together(sv, dim, dtype):
     err, erl = np.abs(f64(got[0])[0] - o), np.abs(f64(got[1])[0] - lse)
     assert (err <= bo).all(), float((err / bo).max())
     assert (erl <= bl).all(), float((erl / bl).max())
+
+
+def near(x):
+    """float32 x and its neighbours on both sides."""
+    x = np.float32(x)
+    return [np.nextafter(x, np.float32(0)), x, np.nextafter(x, np.float32(np.inf))]
+
+
+def halfway(rng, n, lo, hi):
+    """Numbers halfway between two e4m3 values: 17/16, 19/16 .. times a power of two."""
+    return (rng.integers(8, 16, n) * 2 + 1) * np.ldexp(1.0 / 16, rng.integers(lo, hi, n))
+
+
+def odd_pages(sv, heads, dim, layers=1):
+    """One row of 5 cached tokens of random codes, in a page of 16 whose scales are set after."""
+    both = Both(sv, layers, 4, 16, heads, dim, 1, 4)
+    rng = np.random.default_rng(heads)
+    codes = kv_ref.e4m3(np.ldexp(rng.uniform(-1, 1, (5, heads, dim)), rng.integers(-10, 9, dim)))
+    codes[0, :, 0] = 448.0
+    store(both, codes, codes)
+    both.commit([4], 5)
+    return both, rng, codes
+
+
+def codes_of(g, p):
+    return [f64(x.float()[0, p]) for x in (g.k, g.v)]  # [heads, page, dim]
+
+
+@needs_cuda
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_append_at_a_scale_that_stays(sv, dtype):
+    """New values on a page whose scale is no power of two and stays: each is the nearest e4m3
+    of the exact quotient, also next to the points halfway between two."""
+    H, D, T = 48, 96, 7
+    both, rng, codes = odd_pages(sv, H, D)
+    g = both.g
+    s = np.exp2(rng.uniform(-9, 9, H)).astype(np.float32)
+    g.k_scale[0, 0] = g.v_scale[0, 0] = torch.from_numpy(s).cuda()
+    x = np.zeros((1, T, H, D), dtype=np.float32)
+    for h in range(H):
+        at = halfway(rng, T * D // 3, -8, 7)
+        x[0, :, h] = np.array([near(m * float(s[h])) for m in at]).reshape(T, D) \
+            * rng.choice([-1, 1], (T, D))
+    k = torch.from_numpy(x).to(dtype)
+    assert all(both.reserve([T]))
+    sv.sv_kv_append(g, 0, k.cuda(), -k.cuda(), n_new=i32([T]))
+    want = kv_ref.e4m3(f64(k)[0] / s.astype(np.float64)[None, :, None])
+    for got, sign in zip(codes_of(g, 0), (1, -1)):
+        assert (got[:, :5].transpose(1, 0, 2) == codes).all()
+        assert (got[:, 5:5 + T].transpose(1, 0, 2) == sign * want).all()
+    assert (g.k_scale[0, 0].cpu().numpy() == s).all() and g.status() == 0
+
+
+@needs_cuda
+@pytest.mark.parametrize("call", ["append", "commit"])
+def test_rescale_from_a_scale_that_is_no_power_of_two(sv, call):
+    """Tokens of a page whose scale grows, from one that is no power of two, chosen so that an
+    old value lands next to a point halfway between two e4m3 values (append); and tokens that a
+    path moves between pages of such scales (commit)."""
+    H, D = 144, 96
+    both, rng, codes = odd_pages(sv, H, D)
+    g = both.g
+    u = np.abs(codes[1, np.arange(H), np.arange(H) % D])
+    u = np.where(u > 0, u, 448.0)
+    s = np.ldexp(1.0, rng.integers(-5, 6, H))
+    m = halfway(rng, H, -6, 0)
+    m *= np.ldexp(1.0, np.minimum(0, np.floor(np.log2(u / m)).astype(int)))  # (the scale grows)
+    old = np.array([near(s[h] * m[h] / u[h])[h % 3] for h in range(H)], dtype=np.float32)
+    if call == "append":
+        x = torch.zeros(1, 3, H, D)
+        x[0, 1, :, 0] = torch.from_numpy(448 * s)
+        g.k_scale[0, 0] = g.v_scale[0, 0] = torch.from_numpy(old).cuda()
+        assert all(both.reserve([3]))
+        sv.sv_kv_append(g, 0, x.cuda(), x.cuda(), n_new=i32([3]))
+        want = kv_ref.e4m3(codes * old.astype(float)[None, :, None] / s[None, :, None])
+        for got in codes_of(g, 0):
+            assert (got[:, :5].transpose(1, 0, 2) == want).all()
+            assert (got[:, 6, 0] == 448).all()
+        assert (f64(g.k_scale[0, 0]) == s).all() and g.status() == 0
+        return
+    # Path 0, 14: the second token comes from the next page, whose scale is larger and no power
+    # of two either; the page's older ones are rounded to it.
+    T = 15
+    big = (s * rng.uniform(1, 2, H)).astype(np.float32)
+    # (Its ratio to the first page's is what lands next to the halfway points.)
+    old = np.array([near(float(big[h]) * m[h] / u[h])[h % 3] for h in range(H)], dtype=np.float32)
+    assert all(both.reserve([T]))
+    new = kv_ref.e4m3(np.ldexp(rng.uniform(-1, 1, (1, T, H, D)), rng.integers(-10, 9, D)))
+    new[0, :, :, 0] = 448.0
+    sv.sv_kv_append(g, 0, torch.from_numpy(new).float().cuda(), torch.from_numpy(new).float().cuda(),
+                    n_new=i32([T]))
+    for sc in (g.k_scale, g.v_scale):
+        sc[0, 0], sc[0, 1] = torch.from_numpy(old).cuda(), torch.from_numpy(big).cuda()
+    path = [[14] + [-1] * (T - 1)]
+    sv.sv_kv_commit(g, i32([1]), T, path=i32(path))
+    stay = np.concatenate([codes, new[0, :1]])
+    want = kv_ref.e4m3(stay * old.astype(float)[None, :, None] / big.astype(float)[None, :, None])
+    for got in codes_of(g, 0):
+        assert (got[:, :6].transpose(1, 0, 2) == want).all()
+        assert (got[:, 6] == new[0, 14]).all()
+    assert (f64(g.k_scale[0, 0]) == big).all() and g.len.tolist() == [7] and g.status() == 0
