@@ -56,8 +56,8 @@
 #include <cudaTypedefs.h>
 
 #include <cmath>
-#include <mutex>
 
+#include "sv_device.cuh"
 #include "sv_kv.cuh"
 
 namespace sv {
@@ -1512,15 +1512,19 @@ cudaError_t launch_kv_attend(const AttendArgs& A, sv_dtype dt, cudaStream_t st) 
   static const Kernel kernels[2][2][3] = {{SV_ROW(false, 1), SV_ROW(false, 2)},
                                           {SV_ROW(true, 1), SV_ROW(true, 2)}};
 #undef SV_ROW
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [] {
+  int dev = 0, sms = 0;
+  cudaError_t e;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  static OncePerDevice sized;  // (the attribute belongs to the device that is current)
+  e = static_cast<cudaError_t>(sized.run(dev, [] {
+    cudaError_t attr = cudaSuccess;
     for (int i = 0; i < 12 && attr == cudaSuccess; ++i)
       attr = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernels[i / 6][i / 3 % 2][i % 3]),
                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   (int)(AT_SMEM - AT_STATIC));
-  });
-  if (attr != cudaSuccess) return attr;
+    return static_cast<int>(attr);
+  }));
+  if (e != cudaSuccess) return e;
   const KvCache& C = A.C;
   AttendPlan P;
   const bool bf16 = dt == SV_BF16;
@@ -1554,9 +1558,6 @@ cudaError_t launch_kv_attend(const AttendArgs& A, sv_dtype dt, cudaStream_t st) 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  int dev = 0, sms = 0;
-  cudaError_t e;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
     return e;
   const int grid = sms < KV_MAX_CTAS ? sms : KV_MAX_CTAS;
