@@ -417,8 +417,10 @@ class KVCache:
         self.buf = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=dev)
         off = (-self.buf.data_ptr()) % 256
         self.t = self.buf[off: off + self.nbytes]
-        _check("sv_workspace_init",
-               load().sv_workspace_init(_ptr(self.t), self.nbytes, _stream(stream)))
+        self.index = self.t.get_device()
+        with torch.cuda.device(self.index):
+            _check("sv_workspace_init",
+                   load().sv_workspace_init(_ptr(self.t), self.nbytes, _kv_stream(stream, self)))
         # Everything above must be complete before a call on any other stream uses it.
         torch.cuda.synchronize(self.t.device)
 
@@ -426,7 +428,9 @@ class KVCache:
         self.__dict__.update(sizes)  # layers, pages, page, heads, dim, batch, max_pages
         self.rows = (c.batch,)
 
-    status = Workspace.status
+    def status(self, stream=None, clear=False) -> int:
+        _kv_stream(stream, self)
+        return Workspace.status(self, stream, clear)
 
 
 # The cache's calls are made for every layer of every step, so their marshalling is kept
@@ -435,10 +439,29 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _kv_stream(stream, device):
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device.index or 0)
+# (torch's own shortcut to the current stream's handle, 2 us faster than the public way, which
+# serves where it is missing.)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _kv_stream(stream, cache):
+    """Handle of a call's stream. A call runs on the current device: that must be the cache's."""
+    if torch.cuda.current_device() != cache.index:
+        raise ValueError(f"the cache is on {cache.t.device}, which is not the current device")
+    if stream is None:
+        return _raw_stream(cache.index)
+    if stream.device.index != cache.index:
+        raise ValueError(f"the cache is on {cache.t.device}, the stream on {stream.device}")
+    return stream.cuda_stream
+
+
+def _kv_on(t, name, cache, dtype=None):
+    """_dev for a tensor that must be on the cache's device."""
+    _dev(t, name, dtype)
+    if t.get_device() != cache.index:
+        raise ValueError(f"{name} must be on {cache.t.device}")
+    return t
 
 
 def _kv_src(t, name, cache, heads):
@@ -446,6 +469,8 @@ def _kv_src(t, name, cache, heads):
     the element strides of rows and tokens."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != cache.index:
+        raise ValueError(f"{name} must be on {cache.t.device}")
     shape, stride = t.shape, t.stride()
     if len(shape) != 4 or shape[0] != cache.batch or shape[3] != cache.dim or \
             (heads is not None and shape[2] != heads):
@@ -461,7 +486,7 @@ def _kv_src(t, name, cache, heads):
 
 def _kv_counts(t, name, cache):
     if t is not None:
-        _dev(t, name, torch.int32)
+        _kv_on(t, name, cache, torch.int32)
         if t.shape != cache.rows:
             raise ValueError(f"{name} must be [{cache.batch}]")
     return t
@@ -483,7 +508,7 @@ def sv_kv_reserve(cache: KVCache, n_new, ok=None, stream=None):
     _kv_counts(n_new, "n_new", cache)
     _kv_counts(ok, "ok", cache)
     _check("sv_kv_reserve", load().sv_kv_reserve(cache.ref, _addr(n_new), _addr(ok),
-                                                 cache.ws, cache.nbytes, _kv_stream(stream, cache.t.device)))
+                                                 cache.ws, cache.nbytes, _kv_stream(stream, cache)))
     return ok
 
 
@@ -497,7 +522,7 @@ def sv_kv_append(cache: KVCache, layer, k, v, n_new=None, stream=None):
     _kv_counts(n_new, "n_new", cache)
     _check("sv_kv_append", load().sv_kv_append(
         cache.ref, int(layer), _addr(k), _addr(v), _kv_dtype(k, "k"), k_row, k_tok,
-        v_row, v_tok, shape[1], _addr(n_new), cache.ws, cache.nbytes, _kv_stream(stream, cache.t.device)))
+        v_row, v_tok, shape[1], _addr(n_new), cache.ws, cache.nbytes, _kv_stream(stream, cache)))
 
 
 def sv_kv_read(cache: KVCache, start, T, count=None, layer=0, n_layers=None,
@@ -515,12 +540,12 @@ def sv_kv_read(cache: KVCache, start, T, count=None, layer=0, n_layers=None,
     if v_out is None:
         v_out = start.new_empty(shape, dtype=dtype)
     for name, t in (("k_out", k_out), ("v_out", v_out)):
-        _dev(t, name, dtype)
+        _kv_on(t, name, cache, dtype)
         if tuple(t.shape) != shape:
             raise ValueError(f"{name} must be {list(shape)}")
     _check("sv_kv_read", load().sv_kv_read(
         cache.ref, int(layer), int(n_layers), _addr(start), _addr(count), int(T), _addr(k_out),
-        _addr(v_out), _kv_dtype(k_out, "k_out"), cache.ws, cache.nbytes, _kv_stream(stream, cache.t.device)))
+        _addr(v_out), _kv_dtype(k_out, "k_out"), cache.ws, cache.nbytes, _kv_stream(stream, cache)))
     return k_out, v_out
 
 
@@ -533,22 +558,22 @@ def sv_kv_attend(cache: KVCache, layer, q, n_new=None, parent=None, scale=None, 
     T, heads = shape[1], shape[2]
     _kv_counts(n_new, "n_new", cache)
     if parent is not None:
-        _dev(parent, "parent", torch.int32)
+        _kv_on(parent, "parent", cache, torch.int32)
         if parent.shape != shape[:2]:
             raise ValueError(f"parent must be [{cache.batch}, {T}]")
     if out is None:
         out = q.new_empty(shape)
-    elif _dev(out, "out", q.dtype).shape != shape:
+    elif _kv_on(out, "out", cache, q.dtype).shape != shape:
         raise ValueError("out must have q's shape")
     if lse is not None:
-        if _dev(lse, "lse", torch.float32).shape != shape[:3]:
+        if _kv_on(lse, "lse", cache, torch.float32).shape != shape[:3]:
             raise ValueError("lse must have q's first three dimensions")
     elif want_lse:
         lse = q.new_empty(shape[:3], dtype=torch.float32)
     _check("sv_kv_attend", load().sv_kv_attend(
         cache.ref, int(layer), _addr(q), _kv_dtype(q, "q"), row, tok, T, heads, _addr(n_new),
         _addr(parent), float(cache.dim ** -0.5 if scale is None else scale), int(window), int(sinks),
-        _addr(out), _addr(lse), cache.ws, cache.nbytes, _kv_stream(stream, cache.t.device)))
+        _addr(out), _addr(lse), cache.ws, cache.nbytes, _kv_stream(stream, cache)))
     return out if lse is None else (out, lse)
 
 
@@ -558,12 +583,12 @@ def sv_kv_commit(cache: KVCache, accepted, N, path=None, stream=None):
     sv_verify and sv_verify_tree return."""
     _kv_counts(accepted, "accepted", cache)
     if path is not None:
-        _dev(path, "path", torch.int32)
+        _kv_on(path, "path", cache, torch.int32)
         if path.shape != (cache.batch, int(N)):
             raise ValueError(f"path must be [{cache.batch}, {int(N)}]")
     _check("sv_kv_commit", load().sv_kv_commit(
         cache.ref, _addr(accepted), _addr(path), int(N), cache.ws, cache.nbytes,
-        _kv_stream(stream, cache.t.device)))
+        _kv_stream(stream, cache)))
 
 
 def sv_kv_fork(cache: KVCache, src, ok=None, stream=None):
@@ -573,5 +598,5 @@ def sv_kv_fork(cache: KVCache, src, ok=None, stream=None):
     _kv_counts(src, "src", cache)
     _kv_counts(ok, "ok", cache)
     _check("sv_kv_fork", load().sv_kv_fork(cache.ref, _addr(src), _addr(ok),
-                                           cache.ws, cache.nbytes, _kv_stream(stream, cache.t.device)))
+                                           cache.ws, cache.nbytes, _kv_stream(stream, cache)))
     return ok
