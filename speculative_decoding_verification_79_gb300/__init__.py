@@ -456,6 +456,15 @@ def _kv_stream(stream, cache):
     return stream.cuda_stream
 
 
+def _kv_made(stream, cache, *made):
+    """Results that the binding allocated, on the current stream, and a call on another one
+    writes: their memory is not handed out again before that stream is through with them."""
+    if stream is not None and stream.cuda_stream != _raw_stream(cache.index):
+        for t in made:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _kv_on(t, name, cache, dtype=None):
     """_dev for a tensor that must be on the cache's device."""
     _dev(t, name, dtype)
@@ -535,10 +544,11 @@ def sv_kv_read(cache: KVCache, start, T, count=None, layer=0, n_layers=None,
     if n_layers is None:
         n_layers = c.layers - int(layer)
     shape = (int(n_layers), c.batch, int(T), c.heads, c.dim)
+    k_made = v_made = None
     if k_out is None:
-        k_out = start.new_empty(shape, dtype=dtype)
+        k_out = k_made = start.new_empty(shape, dtype=dtype)
     if v_out is None:
-        v_out = start.new_empty(shape, dtype=dtype)
+        v_out = v_made = start.new_empty(shape, dtype=dtype)
     for name, t in (("k_out", k_out), ("v_out", v_out)):
         _kv_on(t, name, cache, dtype)
         if tuple(t.shape) != shape:
@@ -546,6 +556,7 @@ def sv_kv_read(cache: KVCache, start, T, count=None, layer=0, n_layers=None,
     _check("sv_kv_read", load().sv_kv_read(
         cache.ref, int(layer), int(n_layers), _addr(start), _addr(count), int(T), _addr(k_out),
         _addr(v_out), _kv_dtype(k_out, "k_out"), cache.ws, cache.nbytes, _kv_stream(stream, cache)))
+    _kv_made(stream, cache, k_made, v_made)
     return k_out, v_out
 
 
@@ -561,19 +572,21 @@ def sv_kv_attend(cache: KVCache, layer, q, n_new=None, parent=None, scale=None, 
         _kv_on(parent, "parent", cache, torch.int32)
         if parent.shape != shape[:2]:
             raise ValueError(f"parent must be [{cache.batch}, {T}]")
+    made = lse_made = None
     if out is None:
-        out = q.new_empty(shape)
+        out = made = q.new_empty(shape)
     elif _kv_on(out, "out", cache, q.dtype).shape != shape:
         raise ValueError("out must have q's shape")
     if lse is not None:
         if _kv_on(lse, "lse", cache, torch.float32).shape != shape[:3]:
             raise ValueError("lse must have q's first three dimensions")
     elif want_lse:
-        lse = q.new_empty(shape[:3], dtype=torch.float32)
+        lse = lse_made = q.new_empty(shape[:3], dtype=torch.float32)
     _check("sv_kv_attend", load().sv_kv_attend(
         cache.ref, int(layer), _addr(q), _kv_dtype(q, "q"), row, tok, T, heads, _addr(n_new),
         _addr(parent), float(cache.dim ** -0.5 if scale is None else scale), int(window), int(sinks),
         _addr(out), _addr(lse), cache.ws, cache.nbytes, _kv_stream(stream, cache)))
+    _kv_made(stream, cache, made, lse_made)
     return out if lse is None else (out, lse)
 
 

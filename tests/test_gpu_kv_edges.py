@@ -86,3 +86,31 @@ def test_attend_gives_up(sv, dim, T, group, lens):
         torch.cuda.synchronize()
         g.status(clear=True)
         assert all(torch.equal(a, b) for a, b in zip(got, want)), limit
+
+
+@needs_cuda
+@pytest.mark.parametrize("call", ["attend", "read"])
+def test_results_of_a_call_on_another_stream(sv, call):
+    """Results that the binding allocates for a call on a stream of its own, dropped before the
+    call has run: the current stream gets other memory meanwhile."""
+    both, q, n, _ = attend_case(sv, [40, 3], 2, 2, 4, 64, 16, torch.bfloat16, seed=1, n_new=[2, 2])
+    st, start = torch.cuda.Stream(), i32([0, 0])
+    n = i32(n)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        torch.cuda._sleep(100_000_000)  # some 50 ms
+    if call == "attend":
+        made = sv.sv_kv_attend(both.g, 0, q, n_new=n, want_lse=True, stream=st)
+    else:
+        made = sv.sv_kv_read(both.g, start, 40, stream=st)
+    kinds = [(t.shape, t.dtype, t.data_ptr()) for t in made]
+    del made
+    again = [torch.empty(s, dtype=d, device="cuda") for s, d, _ in kinds for _ in range(2)]
+    assert not st.query()  # (the call has not run yet)
+    assert not {t.data_ptr() for t in again} & {p for _, _, p in kinds}
+    torch.cuda.synchronize()
+    # On the current stream nothing is held back.
+    made = sv.sv_kv_read(both.g, start, 40, stream=torch.cuda.current_stream())
+    at = made[0].data_ptr()
+    del made
+    assert torch.empty(1, 2, 40, 2, 64, dtype=torch.bfloat16, device="cuda").data_ptr() == at
