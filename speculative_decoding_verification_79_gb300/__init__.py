@@ -397,7 +397,7 @@ class KVCache:
                      dim=int(dim), batch=int(batch), max_pages=int(max_pages))
         c = _CacheStruct(**sizes)
         self.nbytes = int(load().sv_kv_workspace_bytes(ctypes.byref(c)))
-        if self.nbytes == 0:
+        if self.nbytes == 0 or any(x != _int32(x) for x in sizes.values()):
             raise ValueError("unsupported cache sizes " + ", ".join(
                 f"{k}={v}" for k, v in sizes.items()))
         dev = torch.device(device or "cuda")
@@ -437,6 +437,13 @@ class KVCache:
 # short: plain integers for pointers, the current stream without a Python object for it.
 def _addr(t):
     return None if t is None else t.data_ptr()
+
+
+def _int32(x):
+    """An int argument of the C calls, where a larger one would wrap: the nearest that fits. (A
+    window or a number of sinks that large takes in every position; a layer, length or size
+    that large, and a negative one, is refused.)"""
+    return min(max(int(x), -2 ** 31), 2 ** 31 - 1)
 
 
 # (torch's own shortcut to the current stream's handle, 2 us faster than the public way, which
@@ -530,7 +537,7 @@ def sv_kv_append(cache: KVCache, layer, k, v, n_new=None, stream=None):
         raise ValueError("k and v must have one shape and dtype")
     _kv_counts(n_new, "n_new", cache)
     _check("sv_kv_append", load().sv_kv_append(
-        cache.ref, int(layer), _addr(k), _addr(v), _kv_dtype(k, "k"), k_row, k_tok,
+        cache.ref, _int32(layer), _addr(k), _addr(v), _kv_dtype(k, "k"), k_row, k_tok,
         v_row, v_tok, shape[1], _addr(n_new), cache.ws, cache.nbytes, _kv_stream(stream, cache)))
 
 
@@ -554,8 +561,8 @@ def sv_kv_read(cache: KVCache, start, T, count=None, layer=0, n_layers=None,
         if tuple(t.shape) != shape:
             raise ValueError(f"{name} must be {list(shape)}")
     _check("sv_kv_read", load().sv_kv_read(
-        cache.ref, int(layer), int(n_layers), _addr(start), _addr(count), int(T), _addr(k_out),
-        _addr(v_out), _kv_dtype(k_out, "k_out"), cache.ws, cache.nbytes, _kv_stream(stream, cache)))
+        cache.ref, _int32(layer), _int32(n_layers), _addr(start), _addr(count), _int32(T),
+        _addr(k_out), _addr(v_out), _kv_dtype(k_out, "k_out"), cache.ws, cache.nbytes, _kv_stream(stream, cache)))
     _kv_made(stream, cache, k_made, v_made)
     return k_out, v_out
 
@@ -583,8 +590,9 @@ def sv_kv_attend(cache: KVCache, layer, q, n_new=None, parent=None, scale=None, 
     elif want_lse:
         lse = lse_made = q.new_empty(shape[:3], dtype=torch.float32)
     _check("sv_kv_attend", load().sv_kv_attend(
-        cache.ref, int(layer), _addr(q), _kv_dtype(q, "q"), row, tok, T, heads, _addr(n_new),
-        _addr(parent), float(cache.dim ** -0.5 if scale is None else scale), int(window), int(sinks),
+        cache.ref, _int32(layer), _addr(q), _kv_dtype(q, "q"), row, tok, T, heads, _addr(n_new),
+        _addr(parent), float(cache.dim ** -0.5 if scale is None else scale), _int32(window),
+        _int32(sinks),
         _addr(out), _addr(lse), cache.ws, cache.nbytes, _kv_stream(stream, cache)))
     _kv_made(stream, cache, made, lse_made)
     return out if lse is None else (out, lse)
@@ -600,7 +608,7 @@ def sv_kv_commit(cache: KVCache, accepted, N, path=None, stream=None):
         if path.shape != (cache.batch, int(N)):
             raise ValueError(f"path must be [{cache.batch}, {int(N)}]")
     _check("sv_kv_commit", load().sv_kv_commit(
-        cache.ref, _addr(accepted), _addr(path), int(N), cache.ws, cache.nbytes,
+        cache.ref, _addr(accepted), _addr(path), _int32(N), cache.ws, cache.nbytes,
         _kv_stream(stream, cache)))
 
 

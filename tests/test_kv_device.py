@@ -159,3 +159,31 @@ def test_calls_run_on_the_caches_device(bind, monkeypatch):
         with pytest.raises(ValueError, match="not the current device"):
             call()
     assert len(lib.calls) == 12
+
+
+@pytest.mark.parametrize("x", [2 ** 31, 2 ** 32, 2 ** 40 + 5, -2 ** 31 - 1, -2 ** 32])
+def test_integers_past_32_bits(bind, x):
+    """Arguments of C ints never wrap into other values: the nearest end of the range, or a
+    refusal of sizes."""
+    sv, cache, lib = bind
+    end = 2 ** 31 - 1 if x > 0 else -2 ** 31
+    kv_calls(sv, cache, window=x, sinks=x, layer=x)["attend"]()
+    args = lib.calls[-1][1]
+    assert args[1] == end and args[11:13] == (end, end)
+    kv_calls(sv, cache, layer=x)["append"]()
+    assert lib.calls[-1][1][1] == end
+    kv_calls(sv, cache, layer=x)["read"]()
+    assert lib.calls[-1][1][1] == end
+    sv.sv_kv_commit(cache, Tensor((2,), torch.int32), x)
+    assert lib.calls[-1][1][3] == end
+
+
+@pytest.mark.parametrize("name", ["layers", "pages", "page", "heads", "dim", "batch", "max_pages"])
+def test_cache_sizes_past_32_bits(name):
+    """A size that C would wrap to a supported one."""
+    import speculative_decoding_verification_79_gb300 as sv
+
+    sizes = dict(layers=1, pages=4, page=16, heads=1, dim=16, batch=1, max_pages=4)
+    for wrap in (2 ** 32, -2 ** 32):
+        with pytest.raises(ValueError, match="unsupported cache sizes"):
+            sv.KVCache(**{**sizes, name: sizes[name] + wrap}, device="cpu")
