@@ -286,6 +286,25 @@ __device__ __forceinline__ int at_units(const AttendArgs& A, int b, int rt) {
   return rt < r.nrt ? KV_EXTRA + at_tile(A, r, rt).tiles() : 0;
 }
 
+// The first row after b that has queries (one exists), from a bit for each. A whole warp, a lane
+// a word: an idle batch has thousands of rows without any, and looking their counts up one
+// after the other took a call of 31 us to 950 (two rows of 20,000 tokens at the ends of 4,096).
+constexpr int AT_LIVE = (SV_MAX_B + 31) / 32;
+__device__ __forceinline__ int at_next_row(const uint32_t* rows, int batch, int b) {
+  const int lane = threadIdx.x & 31, words = (batch + 31) / 32;
+  for (int w0 = (b + 1) / 32; w0 < words; w0 += 32) {
+    const int w = w0 + lane;
+    uint32_t x = w < words ? rows[w] : 0;
+    if (w == (b + 1) / 32) x &= ~0u << ((b + 1) % 32);
+    const uint32_t found = __ballot_sync(0xffffffffu, x != 0);
+    if (found) {
+      const int first = __ffs(found) - 1;
+      return (w0 + first) * 32 + __ffs(__shfl_sync(0xffffffffu, x, first)) - 1;
+    }
+  }
+  return batch - 1;
+}
+
 // The units of this CTA, one query tile after the other: key tiles i0 .. i1 - 1 of the
 // current one. Every role walks the same sequence.
 struct AtWalk {
@@ -302,7 +321,8 @@ struct AtWalk {
     i1 = max(0, stop - base - KV_EXTRA);
     return i1 > i0;
   }
-  // From unit `rem` of query tile rt0 of row b0 (all heads).
+  // From unit `rem` of query tile rt0 of row b0 (all heads). One thread does this for all; the
+  // first query tile may have no key tile in the share (see first).
   __device__ __forceinline__ void start(const AttendArgs& A, int b0, int rt0, int rem, int from,
                                         int to) {
     at = from;
@@ -314,10 +334,15 @@ struct AtWalk {
     const int per = KV_EXTRA + tile.tiles();
     h = rem / per;
     base = from - (rem - h * per);
-    if (!settle()) next(A);
+    settle();
+  }
+  // For the warps that walk, before the first query tile.
+  __device__ __forceinline__ void first(const AttendArgs& A, const uint32_t* rows) {
+    if (live() && i1 <= i0) next(A, rows);
   }
   __device__ __forceinline__ bool live() const { return at < end; }
-  __device__ __noinline__ void next(const AttendArgs& A) {
+  // A whole warp; `rows` has a bit for each row that has queries.
+  __device__ __noinline__ void next(const AttendArgs& A, const uint32_t* rows) {
     do {
       base += KV_EXTRA + tile.tiles();
       at = base;
@@ -326,9 +351,8 @@ struct AtWalk {
         h = 0;
         if (++rt == row.nrt) {
           rt = 0;
-          do {  // (a row with queries exists: units are left)
-            row = at_row(A, ++b);
-          } while (row.rows == 0);
+          b = at_next_row(rows, A.C.batch, b);  // (it exists: units are left)
+          row = at_row(A, b);
         }
         tile = at_tile(A, row, rt);
       }
@@ -610,6 +634,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   __shared__ volatile int s_abort;
   __shared__ AtWalk s_walk;
   __shared__ int s_total, s_sum[AT_THREADS / 32];
+  __shared__ uint32_t s_rows[AT_LIVE];  // rows that have queries, a bit each
   // Per key tile and page of it: row of the pool (-1: none); key scale, log2 and inverse of
   // the value scale.
   __shared__ int s_y[AT_INFO][8];
@@ -686,11 +711,21 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   };
   int mine = 0, sum = 0;
 #pragma unroll 1
-  for (int p = tid; p < pairs; p += AT_THREADS) {
+  for (int p = tid; p - lane < pairs; p += AT_THREADS) {
     const int c = units_of(p);
     if (p == tid) mine = c;
     sum += c;
+    if (nrt == 1) {  // (p is the row)
+      const uint32_t has = __ballot_sync(0xffffffffu, c != 0);
+      if (lane == 0) s_rows[p / 32] = has;
+    }
   }
+  if (nrt > 1)
+#pragma unroll 1
+    for (int b = tid; b - lane < C.batch; b += AT_THREADS) {
+      const uint32_t has = __ballot_sync(0xffffffffu, b < C.batch && at_row(A, b).rows > 0);
+      if (lane == 0) s_rows[b / 32] = has;
+    }
   auto block_sum = [&](int x, int* before) {  // sum; *before: of lower threads
     int v = x;
 #pragma unroll
@@ -752,6 +787,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     // tiles later, and K is never more than its ring and three steps ahead of the rest.)
     fence_async_global();  // (what earlier kernels stored, before copies read it)
     AtWalk walk = s_walk;
+    walk.first(A, s_rows);
     const int ppt = AT_KEYS >> C.lgp;             // pages per tile
     const int tpc = min(32 / ppt, AT_INFO / 4);   // tiles per chunk
     const int mt = lane / ppt, sub = lane - mt * ppt;
@@ -769,7 +805,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       page = used ? kv_page(C, walk.b, key) : -1;
       i += n;
       if (i == walk.i1) {
-        walk.next(A);
+        walk.next(A, s_rows);
         i = walk.live() ? walk.i0 : 0;
       }
     };
@@ -888,6 +924,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     // description and rows.
     fence_async_global();
     AtWalk walk = s_walk;
+    walk.first(A, s_rows);
     const int ppt = AT_KEYS >> C.lgp;
     int k = 0, planned = 0;       // items planned, and their tiles
     bool more = true;
@@ -1011,7 +1048,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&dfull[kb]);
       if (live) planned += walk.i1 - walk.i0;
-      if (live) walk.next(A);
+      if (live) walk.next(A, s_rows);
       ++k;
       idle = 0;
     }

@@ -114,3 +114,47 @@ def test_results_of_a_call_on_another_stream(sv, call):
     at = made[0].data_ptr()
     del made
     assert torch.empty(1, 2, 40, 2, 64, dtype=torch.bfloat16, device="cuda").data_ptr() == at
+
+
+@needs_cuda
+@pytest.mark.parametrize("T,group", [(1, 4), (3, 8)])
+def test_attend_two_rows_of_a_large_batch(sv, T, group):
+    """Two rows with new tokens, next to each other and at the ends of 4,096, with a CTA that goes
+    from the one to the other: the same results, and rows without any cost next to nothing."""
+    B, H, D, lens = sv.SV_MAX_B, 8, 16, [19999, 19990]
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    kv = torch.randn(2, 1, 20000 + T, H, D, generator=gen, device="cuda").bfloat16()
+    kv = kv.expand(2, B, 20000 + T, H, D)  # (every row's source is the same: no stride)
+    live = torch.randn(2, T, H * group, D, generator=gen, device="cuda").bfloat16()
+    times, results = [], []
+    for at in ((0, 1), (0, B - 1), (7, B - 33)):
+        c = sv.KVCache(1, 640, 64, H, D, B, 320)
+        n0, n = [0] * B, [0] * B
+        for b, x in zip(at, lens):
+            n0[b], n[b] = x, T
+        sv.sv_kv_reserve(c, i32(n0))
+        sv.sv_kv_append(c, 0, kv[0, :, :20000], kv[1, :, :20000], n_new=i32(n0))
+        sv.sv_kv_commit(c, i32([x - 1 for x in n0]), 20000)
+        sv.sv_kv_reserve(c, i32(n))
+        sv.sv_kv_append(c, 0, kv[0, :, 20000:], kv[1, :, 20000:], n_new=i32(n))
+        q = torch.zeros(B, T, H * group, D, device="cuda", dtype=torch.bfloat16)
+        q[list(at)] = live
+        nn, out = i32(n), torch.empty_like(q)
+        best = []
+        for _ in range(30):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            for _ in range(4):
+                sv.sv_kv_attend(c, 0, q, n_new=nn, out=out)
+            b.record()
+            b.synchronize()
+            best.append(a.elapsed_time(b) * 1e3 / 4)
+        times.append(min(best))
+        results.append(out[list(at)].clone())
+        assert c.status() == 0
+        out[list(at)] = 0
+        assert (out == 0).all()
+    print(f"us a call: {times}")
+    assert results[0].abs().max() > 0
+    assert torch.equal(results[0], results[1]) and torch.equal(results[0], results[2])
+    assert max(times) < 1.5 * times[0] + 10, times
