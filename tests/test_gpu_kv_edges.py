@@ -3,7 +3,7 @@ and devices other than their own."""
 import pytest
 import torch
 
-from test_gpu_kv import Both, attend_case, i32, needs_cuda
+from test_gpu_kv import Both, attend_case, i32, needs_cuda, rand_kv
 
 pytestmark = pytest.mark.gpu
 
@@ -158,3 +158,68 @@ def test_attend_two_rows_of_a_large_batch(sv, T, group):
     assert results[0].abs().max() > 0
     assert torch.equal(results[0], results[1]) and torch.equal(results[0], results[2])
     assert max(times) < 1.5 * times[0] + 10, times
+
+
+@needs_cuda
+@pytest.mark.parametrize("what", ["", "page", "page_high", "shared", "count", "count_high", "len"])
+def test_append_long_rows_with_wrong_data(sv, what):
+    """Rows of several hundred pages, one of them wrong at its far end: left as it was, and the
+    others (rows without new tokens among them) served."""
+    T, page, B = 5000, 16, 4
+    both = Both(sv, 1, 960, page, 1, 16, B, 320)
+    g, r = both.g, both.r
+    n = [T, 4500, 0, 3]
+    assert all(both.reserve([3, 9, 5, 0]))
+    k, v = rand_kv(r, T, 3)
+    both.append(0, k, v, [3, 9, 5, 0])
+    both.commit([2, 8, 4, -1], T)
+    assert all(both.reserve(n))
+    bad = list(n)
+    last = (9 + 4500 - 1) // page
+    if what.startswith("page"):
+        g.table[1, last] = -1 if what == "page" else 960
+    elif what == "shared":
+        g.refs[int(g.table[1, last])] = 2
+    elif what.startswith("count"):
+        bad[1] = -1 if what == "count" else T + 1
+    elif what == "len":
+        g.len[1] = 320 * page - 4499
+    mine = r.rows[1]
+    before = [t.view(torch.uint8)[:, mine].clone() for t in (g.k, g.v)]
+    sv.sv_kv_append(g, 0, k, v, n_new=i32(bad))
+    torch.cuda.synchronize()
+    assert g.status(clear=True) == (sv.SV_ERR_DEVICE_INPUT if what else sv.SV_OK)
+    if what:
+        n[1] = 0
+        for t, u in zip((g.k, g.v), before):
+            assert torch.equal(t.view(torch.uint8)[:, mine], u)
+    r.append(0, k.double().cpu().numpy(), v.double().cpu().numpy(), n)
+    rows = [b for b in range(B) if b != 1 or not what]
+    total = [r.len[b] + n[b] for b in range(B)]
+    out = sv.sv_kv_read(g, i32([0] * B), max(total), count=i32(total), dtype=torch.float32)
+    for kv in range(2):
+        for b in rows:
+            assert (out[kv][0, b, : total[b]].double().cpu().numpy()
+                    == r.values(kv, 0, b, 0, total[b])).all()
+
+
+@needs_cuda
+def test_append_time_grows_with_the_tokens(sv):
+    """Four times the tokens on the smallest pages: about four times the time."""
+    times = []
+    for T in (16384, 65535):
+        c = sv.KVCache(1, T // 16 + 1, 16, 8, 128, 1, T // 16 + 1)
+        k = torch.randn(1, T, 8, 128, device="cuda").bfloat16()
+        sv.sv_kv_reserve(c, i32([T]))
+        best = []
+        for _ in range(20):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            for _ in range(3):
+                sv.sv_kv_append(c, 0, k, k)
+            b.record()
+            b.synchronize()
+            best.append(a.elapsed_time(b))
+        times.append(min(best))
+        assert c.status() == 0
+    assert times[1] < 5 * times[0], times
