@@ -415,8 +415,9 @@ size_t sv_kv_workspace_bytes(const sv_kv_cache *cache);
  * Row b needs max(0, ceil((len + n_new) / page) - n_pages) pages. Rows are served in
  * order with the free pages in ascending order. The first row whose need the free pages
  * no longer cover and every later one that needs pages get none (ok 0,
- * SV_ERR_NO_PAGES); so does a row whose table is too narrow or whose n_new is negative
- * (ok 0, SV_ERR_DEVICE_INPUT), which takes none away from the others.
+ * SV_ERR_NO_PAGES); so does a row whose table is too narrow, whose n_new or len is negative
+ * or whose n_pages is outside [0, max_pages] (ok 0, SV_ERR_DEVICE_INPUT), which takes none
+ * away from the others.
  */
 sv_status sv_kv_reserve(const sv_kv_cache *cache, const int32_t *n_new_d, int32_t *ok_d,
                         void *ws_d, size_t ws_bytes, void *stream);
@@ -500,8 +501,9 @@ sv_status sv_kv_attend(const sv_kv_cache *cache, int layer, const void *q_d, sv_
  * Token len + path[i-1] moves to len + i (i = 1 .. accepted; the path is increasing). The
  * scale of a page that receives tokens becomes the largest source scale among the tokens
  * it then holds, and each token whose scale changes is rounded to the new one. Then len
- * += n, and pages from ceil(len / page) on are released. A row with a bad count or path,
- * missing pages, or a page to write that another row holds is left as it was.
+ * += n, and pages from ceil(len / page) on are released. A row with a bad count or path, an
+ * n_pages outside [0, max_pages], a len past its pages, missing pages, or a page to write that
+ * another row holds is left as it was (SV_ERR_DEVICE_INPUT).
  */
 sv_status sv_kv_commit(const sv_kv_cache *cache, const int32_t *accepted_d, const int32_t *path_d,
                        int N, void *ws_d, size_t ws_bytes, void *stream);
@@ -515,7 +517,9 @@ sv_status sv_kv_commit(const sv_kv_cache *cache, const int32_t *accepted_d, cons
  * order.
  *  ok_d       [batch] int32 out or NULL: 1, or 0 for a taker the free pages do not cover:
  *             it holds the full pages only (its len is cut to them), SV_ERR_NO_PAGES. A
- *             src outside [-1, batch) keeps the row (ok 0, SV_ERR_DEVICE_INPUT).
+ *             src outside [-1, batch) keeps the row (ok 0, SV_ERR_DEVICE_INPUT). What others
+ *             take of a row whose n_pages is outside [0, max_pages] or whose len is past its
+ *             pages is cut to those (SV_ERR_DEVICE_INPUT).
  */
 sv_status sv_kv_fork(const sv_kv_cache *cache, const int32_t *src_d, int32_t *ok_d, void *ws_d,
                      size_t ws_bytes, void *stream);

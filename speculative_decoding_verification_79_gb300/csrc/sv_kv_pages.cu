@@ -276,14 +276,14 @@ __global__ void __launch_bounds__(128)
 // ---------------------------------------------------------------------------
 constexpr int CM_THREADS = 128;
 
-// Does row b's commit hold together (counts, path, pages)? One warp; every lane gets the
+// Does row b's commit hold together (counts, length, path, pages)? One warp; every lane gets the
 // answer. *moves: is there a token that changes place?
 __device__ bool commit_ok(const KvCache& C, int b, int acc, const int32_t* path, int N,
                           bool* moves) {
   const int lane = threadIdx.x & 31;
   bool good = acc >= -1 && acc < N;
-  const int len = C.len[b];
-  good = good && len >= 0 && (long long)len <= (long long)C.max_pages << C.lgp;
+  const int len = C.len[b], np = C.np[b];
+  good = good && np >= 0 && np <= C.max_pages && len >= 0 && len <= (long long)np << C.lgp;
   bool mv = false;
   if (good && path) {
     bool bad = false;
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(CM_THREADS)
   __shared__ int s_len, s_np;
   if (tid == 0) {
     s_len = C.len[b] + kv_ld(accepted + b) + 1;
-    s_np = min(max(C.np[b], 0), C.max_pages);
+    s_np = C.np[b];  // (in range when the flag is set)
   }
   __syncthreads();
   if (!S.flag[b]) return;

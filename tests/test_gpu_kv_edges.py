@@ -223,3 +223,34 @@ def test_append_time_grows_with_the_tokens(sv):
         times.append(min(best))
         assert c.status() == 0
     assert times[1] < 5 * times[0], times
+
+
+@needs_cuda
+@pytest.mark.parametrize("with_path", [False, True])
+@pytest.mark.parametrize("accepted", [-1, 0, 2])
+@pytest.mark.parametrize("what,value", [("n_pages", -5), ("n_pages", -2 ** 31), ("n_pages", 5),
+                                        ("n_pages", 2 ** 31 - 1), ("n_pages", 1), ("len", 33),
+                                        ("len", 2 ** 31 - 1), ("len", -1)])
+def test_commit_with_wrong_counts(sv, what, value, accepted, with_path):
+    """A row whose n_pages or len cannot be (33 tokens on two pages of 16): reported and left as
+    it was, whether tokens are kept or not; the others are served."""
+    both = Both(sv, 1, 20, 16, 1, 16, 3, 4)
+    both.fill([20, 20, 20], 5)
+    assert all(both.reserve([4, 4, 4]))
+    k, v = rand_kv(both.r, 4, 8)
+    both.append(0, k, v, [4, 4, 4])
+    g, r = both.g, both.r
+    getattr(g, what)[1] = value
+    state = [t.clone() for t in (g.table, g.n_pages, g.len)]
+    path = [[2, 3, -1, -1]] * 3 if with_path else None
+    sv.sv_kv_commit(g, i32([1, accepted, 0]), 4, path=None if path is None else i32(path))
+    torch.cuda.synchronize()
+    assert g.status(clear=True) == sv.SV_ERR_DEVICE_INPUT
+    for t, u in zip((g.table, g.n_pages, g.len), state):
+        assert torch.equal(t[1], u[1])
+    r.commit([1, -1, 0], path)
+    assert g.len.tolist()[::2] == r.len[::2]
+    assert (g.table.cpu().numpy()[::2] == r.table()[::2]).all()
+    # (the wrong row's pages are the ones it had)
+    refs = g.refs.cpu().numpy()
+    assert all(refs[p] == 1 for b in range(3) for p in r.rows[b])
