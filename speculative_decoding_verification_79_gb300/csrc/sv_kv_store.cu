@@ -336,9 +336,18 @@ cudaError_t launch_kv_read(const KvCache& C, const KvScratch&, int layer, int n_
                            const int32_t* start, const int32_t* count, int T, void* ko, void* vo,
                            sv_dtype dt, cudaStream_t st) {
   const long long vecs = (long long)T * C.heads * (C.dim / 16);
-  const dim3 grid(static_cast<unsigned>((vecs + 255) / 256), C.batch, n_layers);
   const auto kernel = dt == SV_BF16 ? kv_read_kernel<true> : kv_read_kernel<false>;
-  return kv_launch(kernel, grid, 256, 0, st, C, layer, start, count, T, ko, vo);
+  constexpr int MOST = 65535;  // layers of a launch (the grid's third dimension)
+  for (int l = 0; l < n_layers; l += MOST) {
+    const int n = n_layers - l < MOST ? n_layers - l : MOST;
+    const size_t at = (size_t)l * C.batch * vecs * 16 * (dt == SV_BF16 ? 2 : 4);
+    const dim3 grid(static_cast<unsigned>((vecs + 255) / 256), C.batch, n);
+    const cudaError_t e = kv_launch(kernel, grid, 256, 0, st, C, layer + l, start, count, T,
+                                    static_cast<void*>(static_cast<char*>(ko) + at),
+                                    static_cast<void*>(static_cast<char*>(vo) + at));
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace sv

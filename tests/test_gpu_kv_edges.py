@@ -254,3 +254,26 @@ def test_commit_with_wrong_counts(sv, what, value, accepted, with_path):
     # (the wrong row's pages are the ones it had)
     refs = g.refs.cpu().numpy()
     assert all(refs[p] == 1 for b in range(3) for p in r.rows[b])
+
+
+@needs_cuda
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_read_more_layers_than_a_grid_has(sv, dtype):
+    """A small cache of 70,000 layers, read at once and from a layer on."""
+    L, D = 70000, 16
+    c = sv.KVCache(L, 2, 16, 1, D, 1, 2)
+    c.table[0] = i32([1, 0])
+    c.n_pages.fill_(2)
+    c.len.fill_(20)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    for pool in (c.k, c.v):
+        pool.copy_(torch.randint(-8, 9, pool.shape, generator=gen, device="cuda").float())
+    c.k_scale.copy_(2.0 ** torch.randint(-3, 4, c.k_scale.shape, generator=gen, device="cuda"))
+    for first in (0, 3000):
+        k, v = sv.sv_kv_read(c, i32([14]), 4, layer=first, dtype=dtype)
+        pos = [(1, 14), (1, 15), (0, 0), (0, 1)]
+        for got, pool, scale in ((k, c.k, c.k_scale), (v, c.v, c.v_scale)):
+            for t, (p, i) in enumerate(pos):
+                want = pool[first:, p, 0, i].float() * scale[first:, p, 0][:, None]
+                assert torch.equal(got[:, 0, t, 0].float(), want)
+    assert c.status() == 0
