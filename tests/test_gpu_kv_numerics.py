@@ -1,13 +1,12 @@
 """What the cache attention's numbers may be off by, on inputs where each part of that shows:
 weights, queries, keys of very different size, and scales of another quantiser."""
-import math
 
 import numpy as np
 import pytest
 import torch
 
 import kv_ref
-from test_gpu_kv import Both, f64, i32, needs_cuda
+from test_gpu_kv import Both, f64, i32, needs_cuda, rand_kv, tree
 
 pytestmark = pytest.mark.gpu
 
@@ -30,14 +29,17 @@ W_REL, W_ABS, SUM = 2.0 ** -11, 2.0 ** -28, 2.0 ** -19
 Q_ABS = {torch.bfloat16: 2.0 ** -21, torch.float16: 2.0 ** -24}
 
 
-def per_key(q, k, v, L, n, scale, dtype, **mask):
+def per_key(q, k, v, L, n, scale, dtype, vs=None, **mask):
     """One row: the result in float64 (o [n, q_heads, dim], lse) and what a call's may be off by,
-    from an error of its own for each key's score:
+    vs [tokens, heads] being the scales of the values (None: all the same), from an error of its
+    own for each key's score:
       d_j = scale (Q_ABS max|q| sum|k_j| + 2^-19 sum|q k_j|)     query terms, float32 sums
             + 2^-20 + 2^-20 max|s|        the power; a score, the reference and its moves as
                                           float32 numbers: 16 roundings of 2^-24
     With weights w'_j = w_j e^(e_j), |e_j| <= d_j, the result moves by
-    sum w_j (e^(e_j) - 1)(v_j - o) / sum w'_j."""
+    sum w_j (e^(e_j) - 1)(v_j - o) / sum w'_j. A weight times its value's scale is off by W_ABS of
+    the largest such product, its value by that many times its code v_j / vs_j."""
+    vs = np.ones(k.shape[:2]) if vs is None else vs
     T, Hq, D = q.shape
     G = Hq // k.shape[1]
     o, bo = np.zeros((n, Hq, D)), np.zeros((n, Hq, D))
@@ -45,7 +47,7 @@ def per_key(q, k, v, L, n, scale, dtype, **mask):
     for t in range(n):
         see = kv_ref.visible(L, n, t, **mask)
         for h in range(Hq):
-            kk, vv, x = k[see, h // G], v[see, h // G], q[t, h]
+            kk, vv, u, x = k[see, h // G], v[see, h // G], vs[see, h // G], q[t, h]
             s = kk @ x * scale
             m = s.max()
             w = np.exp(s - m)
@@ -57,7 +59,8 @@ def per_key(q, k, v, L, n, scale, dtype, **mask):
             lse[t, h] = np.log(np.exp(s - m).sum()) + m
             move = (w * np.expm1(d)) @ np.abs(vv - o[t, h]) / (w @ np.exp(-d))
             bo[t, h] = (torch.finfo(dtype).eps / 2 * (np.abs(o[t, h]) + move) + move
-                        + (W_REL + SUM) * (w @ np.abs(vv)) + W_ABS * np.abs(vv).sum(0)
+                        + (W_REL + SUM) * (w @ np.abs(vv))
+                        + W_ABS * (w * u).max() * (np.abs(vv) / u[:, None]).sum(0)
                         + torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps)
             bl[t, h] = np.log(w @ np.exp(d)) + SUM + 2.0 ** -22 * abs(lse[t, h])
     return o, lse, bo * 1.01, bl * 1.01
@@ -265,3 +268,95 @@ def test_rescale_from_a_scale_that_is_no_power_of_two(sv, call):
         assert (got[:, :6].transpose(1, 0, 2) == want).all()
         assert (got[:, 6] == new[0, 14]).all()
     assert (f64(g.k_scale[0, 0]) == big).all() and g.len.tolist() == [7] and g.status() == 0
+
+
+def check_rows(both, q, n, got, scale, informative, **mask):
+    """Every row's results against per_key; `informative`: the share of the components that a
+    zero output would have to fail."""
+    r = both.r
+    told = []
+    for b in range(r.batch):
+        if not n[b]:
+            continue
+        L = r.len[b]
+        k, v = (r.values(kv, 0, b, 0, L + n[b]) for kv in (0, 1))
+        one = {m: (x[b] if m == "parent" and x is not None else x) for m, x in mask.items()}
+        vs = np.array([r.s[1, 0, r.rows[b][j // r.page]] for j in range(L + n[b])])
+        o, lse, bo, bl = per_key(f64(q[b]), k, v, L, n[b], scale, q.dtype, vs, **one)
+        out, top = f64(got[0])[b, :n[b]], torch.finfo(q.dtype).max
+        # Past the type's range a result is infinite.
+        past = np.isinf(out) & (np.sign(out) == np.sign(o)) & (np.abs(o) + bo > top)
+        err = np.where(past, 0.0, np.abs(out - o))
+        erl = np.abs(f64(got[1])[b, :n[b]] - lse)
+        assert (err <= bo).all(), (b, float((err / bo).max()), np.argwhere(err > bo)[:5])
+        assert (erl <= bl).all(), (b, float((erl / bl).max()))
+        told.append((bo < np.abs(o)).ravel())
+    assert np.concatenate(told).mean() > informative
+
+
+@needs_cuda
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("q_sigma,sigma", [(0.0, 3.0), (0.01, 0.0), (0.01, 3.0), (1.0, 0.0),
+                                           (1.0, 3.0), (5.0, 1.0), (30.0, 0.0), (30.0, 3.0)])
+@pytest.mark.parametrize("dim,T,heads,group,trees,window", [
+    (128, 3, 2, 4, False, 0), (64, 16, 1, 8, True, 0), (256, 9, 1, 4, False, 200),
+    (80, 33, 1, 3, False, 0)])
+def test_score_ranges(sv, q_sigma, sigma, dim, T, heads, group, trees, window, dtype):
+    """Flat scores, and scores so far apart that one key takes all, with tokens whose sizes
+    differ by powers of ten: each key has the error of its own score, so that what is certain
+    in the result has to be right."""
+    lens, n = [5, 400, 1100], [T, T, max(1, T - 2)]
+    per = -(-(max(lens) + T) // 16) + 1
+    both = Both(sv, 1, 3 * per, 16, heads, dim, 3, per)
+    seed = int(q_sigma) + dim
+    both.fill(lens, seed, sigma)
+    assert all(both.reserve(n))
+    k, v = rand_kv(both.r, T, seed + 77, sigma)
+    both.append(0, k, v, n)
+    rng = np.random.default_rng(seed)
+    par = [tree(rng, T) for _ in lens] if trees else None
+    gen = torch.Generator(device="cuda").manual_seed(seed + 5)
+    q = q_sigma * torch.randn(3, T, heads * group, dim, generator=gen, device="cuda")
+    q = q.to(dtype)
+    got = sv.sv_kv_attend(both.g, 0, q, n_new=i32(n), parent=None if par is None else i32(par),
+                          window=window, want_lse=True)
+    check_rows(both, q, n, got, dim ** -0.5, 0.75, parent=par, window=window)
+    assert both.g.status() == 0
+
+
+@needs_cuda
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("T,group", [(1, 8), (5, 7), (16, 8), (40, 4)])
+def test_one_key_takes_all(sv, T, group, dtype):
+    """A key in each row whose score is 40 above the others': the result is its value, the log
+    sum its score, wherever the key is."""
+    dim, L, page = 128, 700, 32
+    scale = dim ** -0.5
+    both = Both(sv, 1, 60, page, 1, dim, 2, 30)
+    r = both.r
+    rng = np.random.default_rng(T)
+    tot = L + T
+    k = kv_ref.e4m3(rng.standard_normal((2, tot, 1, dim)))
+    v = kv_ref.e4m3(4 * rng.standard_normal((2, tot, 1, dim)))
+    mean = kv_ref.e4m3(rng.standard_normal(dim))
+    top = (3, L - 1)
+    for b in range(2):  # (one key along the queries, all others without a part along them)
+        k[b, :, 0, :] -= (k[b, :, 0] @ mean)[:, None] * mean / (mean @ mean)
+        k[b, top[b], 0] = mean * 4
+    k = kv_ref.e4m3(np.clip(k, -100, 100))
+    assert all(both.reserve([tot, tot]))
+    x = [torch.from_numpy(y).cuda().float() for y in (k, v)]
+    both.append(0, x[0], x[1], [tot, tot])
+    both.commit([L - 1, L - 1], L)
+    assert all(both.reserve([T, T]))
+    a = 48 / (scale * 4 * (mean @ mean))
+    q = torch.from_numpy(a * mean * np.ones((2, T, group, 1))).to(dtype).cuda()
+    got = sv.sv_kv_attend(both.g, 0, q, n_new=i32([T, T]), want_lse=True)
+    check_rows(both, q, [T, T], got, scale, 0.99)
+    for b in range(2):
+        want = r.values(1, 0, b, top[b], top[b] + 1)[0, 0]
+        lse = scale * (f64(q)[b] @ r.values(0, 0, b, top[b], top[b] + 1)[0, 0])
+        # The other keys together: 740 e^-40, less than 2^-48 of the value's largest.
+        half = torch.finfo(dtype).eps / 2
+        assert (np.abs(f64(got[0])[b] - want) <= (half + SUM) * np.abs(want) + 2.0 ** -27 * 32).all()
+        assert (np.abs(f64(got[1])[b] - lse) <= 2.0 ** -17 * 48).all()
