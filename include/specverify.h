@@ -433,7 +433,10 @@ sv_status sv_kv_reserve(const sv_kv_cache *cache, const int32_t *n_new_d, int32_
  * For each page and head written, with a the largest |x| among its new tokens, the scale
  * becomes max(old scale if the page holds older tokens of the row, 2^e), e the smallest
  * exponent >= SV_KV_MIN_EXP with a <= 448 * 2^e. Older tokens of a page whose scale grows
- * are rounded to the new one. Values round to the nearest e4m3, ties to even. A value
+ * are rounded to the new one, and stay so: that costs values below 2^-14 of the new largest
+ * bits (e4m3's exponents end there), also when the token that needed the scale is rejected
+ * later, and the scale of a page that holds tokens is not lowered again. Values round to
+ * the nearest e4m3, ties to even. A value
  * that is not finite or above 448 * 2^64 does not count towards a; it is stored as NaN
  * or saturated, and sets SV_ERR_DEVICE_INPUT. A row with a bad count, missing pages or a
  * page to write that refs does not give to it alone is left as it was.

@@ -360,3 +360,52 @@ def test_one_key_takes_all(sv, T, group, dtype):
         half = torch.finfo(dtype).eps / 2
         assert (np.abs(f64(got[0])[b] - want) <= (half + SUM) * np.abs(want) + 2.0 ** -27 * 32).all()
         assert (np.abs(f64(got[1])[b] - lse) <= 2.0 ** -17 * 48).all()
+
+
+@needs_cuda
+@pytest.mark.parametrize("with_path", [False, True])
+@pytest.mark.parametrize("factor", [6, 15])
+def test_a_rejected_outlier_keeps_its_scale(sv, factor, with_path):
+    """A rejected token 2^6 or 2^15 times the others of its page: the page's older tokens stay
+    rounded to the scale it needed, exactly as the formula says, which costs them bits only in
+    the latter case; pages without older tokens start anew."""
+    D = 32
+    both = Both(sv, 2, 4, 16, 1, D, 1, 4)
+    rng = np.random.default_rng(1)
+    x = rng.uniform(1, 1.9, (13, 1, D))
+    x[0, 0, 0] = 448.0 / 256  # the first page's scale is 2^-8
+
+    def append(y):
+        z = torch.from_numpy(y[None]).float().cuda()
+        for layer in range(2):
+            sv.sv_kv_append(both.g, layer, z, -z)
+        both.r.append(0, f64(z), -f64(z), [len(y)])
+        both.r.append(1, f64(z), -f64(z), [len(y)])
+
+    assert all(both.reserve([13]))
+    append(x)
+    both.commit([12], 13)
+    before = both.r.values(0, 0, 0, 0, 13)
+    assert both.r.s[0, 0, 0, 0] == 2.0 ** -7  # (1.9 > 448 / 256)
+    y = rng.uniform(1, 1.7, (6, 1, D))
+    y[1] *= 2.0 ** factor  # position 14, on the first page
+    y[4] *= 2.0 ** factor  # position 17, on the next
+    assert all(both.reserve([6]))
+    append(y)
+    both.commit([0], 6, [[2, 3, -1, -1, -1, -1]] if with_path else None)
+    both.same()
+    both.same_values()
+    after = both.r.values(0, 0, 0, 0, 13)
+    s = both.r.s[0, 0, 0, 0]
+    assert s == 2.0 ** (factor - 8) and (after == kv_ref.e4m3(before / s) * s).all()
+    assert (after != before).any() == (factor > 14)
+    assert (np.abs(after - before) <= 2.0 ** -10 * s).all()  # half of e4m3's smallest step
+    # The next round overwrites the outlier; the first page keeps the scale, the next has its own.
+    assert all(both.reserve([6]))
+    append(rng.uniform(1, 1.7, (6, 1, D)))
+    both.commit([5], 6)
+    both.same()
+    both.same_values()
+    assert both.r.s[0, 0, 0, 0] == s and both.r.s[0, 0, 1, 0] == 2.0 ** -8
+    for got in (both.g.k_scale, both.g.v_scale):
+        assert got[:, :2, 0].tolist() == [[s, 2.0 ** -8]] * 2
