@@ -158,9 +158,6 @@ struct VerifyArgs {
 
 cudaError_t launch_verify(const VerifyArgs& A, bool bf16, bool greedy, int grid, cudaStream_t st);
 
-// The bound on waits that calls are given now, in clock cycles (sv_set_wait_limit).
-long long wait_limit();
-
 // Host side of a verify call (sv_api.cu): every argument check, then the kernel
 // arguments and grid (grid 0: nothing to launch); and the launch itself.
 sv_status verify_prepare(const void* target_d, const void* draft_d, sv_dtype dtype,

@@ -224,6 +224,9 @@ cudaError_t kv_launch(void (*kernel)(P...), dim3 grid, int block, size_t smem, c
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// The bound on waits that calls are given now, in clock cycles (sv_set_wait_limit; sv_api.cu).
+long long wait_limit();
+
 cudaError_t launch_kv_reserve(const KvCache& C, const KvScratch& S, const int32_t* n_new,
                               int32_t* ok, cudaStream_t st);
 cudaError_t launch_kv_fork(const KvCache& C, const KvScratch& S, const int32_t* src, int32_t* ok,
