@@ -443,18 +443,20 @@ def _int32(x):
     """An int argument of the C calls, where a larger one would wrap: the nearest that fits. (A
     window or a number of sinks that large takes in every position; a layer, length or size
     that large, and a negative one, is refused.)"""
-    return min(max(int(x), -2 ** 31), 2 ** 31 - 1)
+    x = int(x)
+    return x if -2147483648 <= x <= 2147483647 else (2147483647 if x > 0 else -2147483648)
 
 
-# (torch's own shortcut to the current stream's handle, 2 us faster than the public way, which
-# serves where it is missing.)
+# (torch's own shortcuts to the current stream's handle and device, 2 and 0.1 us faster than the
+# public ways, which serve where they are missing.)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _kv_stream(stream, cache):
     """Handle of a call's stream. A call runs on the current device: that must be the cache's."""
-    if torch.cuda.current_device() != cache.index:
+    if _current_device() != cache.index:
         raise ValueError(f"the cache is on {cache.t.device}, which is not the current device")
     if stream is None:
         return _raw_stream(cache.index)
@@ -466,25 +468,26 @@ def _kv_stream(stream, cache):
 def _kv_made(stream, cache, *made):
     """Results that the binding allocated, on the current stream, and a call on another one
     writes: their memory is not handed out again before that stream is through with them."""
-    if stream is not None and stream.cuda_stream != _raw_stream(cache.index):
+    if stream.cuda_stream != _raw_stream(cache.index):
         for t in made:
             if t is not None:
                 t.record_stream(stream)
 
 
-def _kv_on(t, name, cache, dtype=None):
-    """_dev for a tensor that must be on the cache's device."""
-    _dev(t, name, dtype)
+def _kv_on(t, name, cache, dtype):
+    """A dense tensor of the type on the cache's device."""
     if t.get_device() != cache.index:
         raise ValueError(f"{name} must be on {cache.t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     return t
 
 
 def _kv_src(t, name, cache, heads):
     """A [batch, T, heads, dim] tensor whose last two dimensions are dense: its shape, and
     the element strides of rows and tokens."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
     if t.get_device() != cache.index:
         raise ValueError(f"{name} must be on {cache.t.device}")
     shape, stride = t.shape, t.stride()
@@ -563,7 +566,8 @@ def sv_kv_read(cache: KVCache, start, T, count=None, layer=0, n_layers=None,
     _check("sv_kv_read", load().sv_kv_read(
         cache.ref, _int32(layer), _int32(n_layers), _addr(start), _addr(count), _int32(T),
         _addr(k_out), _addr(v_out), _kv_dtype(k_out, "k_out"), cache.ws, cache.nbytes, _kv_stream(stream, cache)))
-    _kv_made(stream, cache, k_made, v_made)
+    if stream is not None:
+        _kv_made(stream, cache, k_made, v_made)
     return k_out, v_out
 
 
@@ -594,7 +598,8 @@ def sv_kv_attend(cache: KVCache, layer, q, n_new=None, parent=None, scale=None, 
         _addr(parent), float(cache.dim ** -0.5 if scale is None else scale), _int32(window),
         _int32(sinks),
         _addr(out), _addr(lse), cache.ws, cache.nbytes, _kv_stream(stream, cache)))
-    _kv_made(stream, cache, made, lse_made)
+    if stream is not None:
+        _kv_made(stream, cache, made, lse_made)
     return out if lse is None else (out, lse)
 
 

@@ -93,7 +93,7 @@ def bind(monkeypatch):
     lib = Lib()
     monkeypatch.setattr(sv, "load", lambda: lib)
     monkeypatch.setattr(sv, "_raw_stream", lambda index: 55 + index)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(sv, "_current_device", lambda: 0)
     cache = types.SimpleNamespace(
         batch=2, dim=32, heads=2, rows=(2,), index=0, ref=None, ws=1 << 20, nbytes=1 << 20,
         t=types.SimpleNamespace(device=torch.device("cuda", 0)),
@@ -154,7 +154,7 @@ def test_calls_run_on_the_caches_device(bind, monkeypatch):
     for call in kv_calls(sv, cache, stream=Stream(1)).values():
         with pytest.raises(ValueError, match="the stream on cuda:1"):
             call()
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(sv, "_current_device", lambda: 1)
     for call in (*kv_calls(sv, cache).values(), lambda: sv.KVCache.status(cache)):
         with pytest.raises(ValueError, match="not the current device"):
             call()
