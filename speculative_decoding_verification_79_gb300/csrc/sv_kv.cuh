@@ -25,8 +25,8 @@ constexpr uint32_t ST_NO_PAGES = 4u;
 // list of fresh pages, a flag per row, and the attention's partial results.
 constexpr int KV_MAX_CTAS = 160;  // persistent CTAs of the attention kernel
 constexpr int KV_ROWS = 128;      // most query rows of its tile
-// Work of a query tile beside its key tiles, in key tiles: 3, 4, 5, 6 and 7 took 130, 122, 122,
-// 122 and 123 us for single tokens of 64 rows, and 156, 148, 145, 143 and 145 for trees of 16
+// Work of a query tile beside its key tiles, in key tiles: 3, 4, 5, 6 and 7 took 132, 121, 121,
+// 121 and 123 us for single tokens of 64 rows, and 161, 152, 150, 149 and 152 for trees of 16
 // nodes.
 constexpr int KV_EXTRA = 6;
 

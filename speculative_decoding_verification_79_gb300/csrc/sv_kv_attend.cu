@@ -8,12 +8,11 @@
 // operand is carried as a sum of 8-bit terms, multiplied one after the other into the same
 // float32 accumulator. A query row, scaled by a power of two to the e4m3 range, is the sum of
 // an e4m3 term (4 bits) and one (bf16) or two (fp16) e5m2 terms for the rest: after rounding to
-// 4 bits the rest of bf16's 8 has 3, which e5m2 holds, and its exponents reach 2^-10 further
-// down. (With e4m3 for all terms they end at 2^-10, 2^-18 of the largest component.) That is
-// exact down to 2^-15 of the largest component, and off by up to 2^-21 (bf16) or 2^-24 (fp16)
-// of that one below. A weight is rounded to fp16 and split into three e5m2 terms (e5m2 is
-// fp16's upper byte, so a split is integer arithmetic). Weights go from registers to tensor memory and are
-// multiplied from there.
+// 4 bits the rest of bf16's 8 has 3, which e5m2 holds, and e5m2's smallest number is 2^-16 where
+// e4m3's is 2^-9 (2^-18 of the largest component). That is exact down to 2^-13 of the largest
+// component, and off by up to 2^-21 (bf16) or 2^-24 (fp16) of that one below. A weight is rounded
+// to fp16 and split into three e5m2 terms (e5m2 is fp16's upper byte, so a split is integer
+// arithmetic). Weights go from registers to tensor memory and are multiplied from there.
 //
 // A thread owns a query row (a lane of the accumulator) and some of the tile's tokens, so
 // that the softmax needs no exchange but one vote between the four threads of a row. (With
@@ -42,12 +41,12 @@
 //
 // What bounds it. Up to dim 128 a key tile is 32 KB, 1,400 cycles of an SM's share of the
 // memory rate, and 20 products of 64 cycles; its softmax is a chain of waits, loads,
-// a vote, powers, splits and stores of about 1,600 cycles for 32 rows, 1,800 for 64 and 2,500
-// for 128, where the integer instructions of the split alone fill half of it. Measured on
-// 64 rows with 8 key/value heads of 128: single tokens of 8 queries a head, 4,100 tokens
-// cached in the mean, 120 us (4.5 TB/s, 66 % of a copy); blocks of 9 tokens of 4 queries,
-// 134 us; trees of up to 16 nodes of 8 queries, 143 us (585 TFLOP/s of the formula's, 2.5
-// times as many of 8-bit products). A query tile costs 3,000 to 8,000 cycles beside its key
+// a vote, powers, splits and stores of about 1,600 cycles for 32 rows, 1,800 for 64 and 2,600
+// for 128, where the integer instructions of the split alone fill half of it. Measured in CUDA
+// graphs (a call from Python takes 2 to 11 us more) on 64 rows with 8 key/value heads of 128:
+// single tokens of 8 queries a head, 4,100 tokens cached in the mean, 122 us (4.4 TB/s, 65 %
+// of a copy); blocks of 9 tokens of 4 queries, 137 us; trees of up to 16 nodes of 8 queries,
+// 149 us (560 TFLOP/s of the formula's, 2.5 times as many of 8-bit products). A query tile costs 3,000 to 8,000 cycles beside its key
 // tiles, and a launch 11,000 to 18,000 before the first (counting, page table, queries, each
 // a trip to memory), which is most of the 13 us of one row's single token.
 #include <cuda.h>
@@ -612,8 +611,9 @@ __device__ __noinline__ void at_land(uint64_t* full, int n, int g) {
 
 // (The three are template parameters because the loops' registers and instruction fetches
 // matter: with the vector's width a variable, single tokens took 127 us instead of 120 and
-// trees 173 instead of 166.) W: rows of a copy (32, 64 or 128 >= the query rows of a tile). BF16: type of the queries and
-// outputs (else fp16). NDB: 128-byte blocks of a token's vector.
+// trees 173 instead of 166, as they were then.) W: rows of a copy (32, 64 or 128 >= the query
+// rows of a tile). BF16: type of the queries and outputs (else fp16). NDB: 128-byte blocks of a
+// token's vector.
 template <int W, bool BF16, int NDB>
 __global__ void __launch_bounds__(AT_THREADS, 1)
     kv_attend_kernel(const __grid_constant__ AttendArgs A, const __grid_constant__ AttendPlan P,
@@ -1482,7 +1482,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
 // them in flight and a running reference. It reads what the CTAs left in L2: 2 to 3 us for
 // 30 MB. (A join by the last of the CTAs themselves held up its SM for up to 27 us: 128 rows
 // of 256 components are 128 KB a CTA.)
-// Blocks of a query tile: 2, 4, 8 and 16 took 154, 146, 143 and 143 us for the trees above.
+// Blocks of a query tile: 2, 4, 8 and 16 took 161, 153, 149 and 149 us for the trees above.
 constexpr int JOIN_THREADS = 256, JOIN_BLOCKS = 8;
 __global__ void __launch_bounds__(JOIN_THREADS)
     kv_attend_join_kernel(const __grid_constant__ AttendArgs A, int bf16) {
@@ -1567,8 +1567,8 @@ cudaError_t launch_kv_attend(const AttendArgs& A, sv_dtype dt, cudaStream_t st) 
   const bool bf16 = dt == SV_BF16;
   const int ndb = C.dim > 128 ? 2 : 1;
   const long long rows = (long long)A.T * A.group;
-  // The narrowest copy that holds the rows: 8 rows a head took 119 us with copies of 32, 123
-  // with 64 and 150 with 128 (64 rows of single tokens); 36 rows 134 with 64 and 158 with 128.
+  // The narrowest copy that holds the rows: 8 rows a head took 121 us with copies of 32, 127
+  // with 64 and 160 with 128 (64 rows of single tokens); 36 rows 137 with 64 and 169 with 128.
   const int width = rows <= 32 ? 32 : (rows <= 64 ? 64 : 128);
   const size_t tile = (size_t)ndb * AT_BLK;
   // At least 32 components of 128 row copies, or 16 of them, which leaves room for one more

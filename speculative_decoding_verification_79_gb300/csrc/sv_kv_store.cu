@@ -4,7 +4,7 @@
 // values. Two steps: the largest |x| of the page's new tokens gives the scale, then each
 // value is rounded to e4m3 at that scale, sixteen to a 16-byte store. The values stay in
 // registers between the steps, so that they are read once. Bound by memory: 8 prompts of
-// 4,093 tokens (8 heads of 128, bf16) are 201 MB; 42 us, 4.8 TB/s. With four CTAs an SM
+// 4,093 tokens (8 heads of 128, bf16, pages of 64) are 201 MB; 39 to 42 us, 4.8 to 5.1 TB/s. With four CTAs an SM
 // (64 registers; three took 45 us). A block of 9 tokens of 64 rows is a chain of memory
 // trips (length, page table, values), 6 us; page, old scale and values are fetched together.
 //
