@@ -46,9 +46,10 @@
 // graphs (a call from Python takes 2 to 11 us more) on 64 rows with 8 key/value heads of 128:
 // single tokens of 8 queries a head, 4,100 tokens cached in the mean, 122 us (4.4 TB/s, 65 %
 // of a copy); blocks of 9 tokens of 4 queries, 137 us; trees of up to 16 nodes of 8 queries,
-// 149 us (560 TFLOP/s of the formula's, 2.5 times as many of 8-bit products). A query tile costs 3,000 to 8,000 cycles beside its key
-// tiles, and a launch 11,000 to 18,000 before the first (counting, page table, queries, each
-// a trip to memory), which is most of the 13 us of one row's single token.
+// 149 us (560 TFLOP/s of the formula's, 2.5 times as many of 8-bit products). A query tile
+// costs 3,000 to 8,000 cycles beside its key tiles, and a launch 11,000 to 18,000 before the
+// first (counting, page table, queries, each a trip to memory), which is most of the 13 us of
+// one row's single token.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
