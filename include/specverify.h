@@ -528,6 +528,89 @@ sv_status sv_kv_fork(const sv_kv_cache *cache, const int32_t *src_d, int32_t *ok
                      size_t ws_bytes, void *stream);
 
 /*
+ * ---------------------------------------------------------------------------------
+ * Rotary positions. Pair i of a head, (a, b), at position P becomes
+ *     gain * (a cos(P f_i) - b sin(P f_i), b cos(P f_i) + a sin(P f_i)),
+ * i < rot / 2. Pairs are components (i, i + rot/2), or (2i, 2i + 1) when interleaved;
+ * components from rot on stay as they are. Frequencies are kept as turns per position in units
+ * of 2^-64 (modulo 2^64, as a position is whole), so that the angle of a far position is as
+ * exact as that of a near one.
+ */
+#define SV_ROPE_MAX_DIM 512
+typedef enum sv_rope_scaling {
+    SV_ROPE_PLAIN = 0,  /* f_i = base^(-2i / rot) */
+    SV_ROPE_LINEAR = 1, /* f_i / stretch */
+    SV_ROPE_TURNS = 2,  /* f_i (w + (1 - w) / stretch), w = (n - low) / (high - low) in [0, 1],
+                           n = original f_i / 2 pi: the pair's turns over the original context */
+    SV_ROPE_INDEX = 3   /* the same with w = 1 - (i - i0) / (i1 - i0) in [0, 1], i0 and i1 the
+                           indices of pairs of `high` and `low` turns, rounded down and up and
+                           kept in [0, rot - 1] */
+} sv_rope_scaling;
+
+/*
+ * sv_rope_fixed: n angles per position (radians, finite) as the frequencies of sv_rope_spec.
+ * sv_rope_freqs: the rot / 2 frequencies of a scaling. stretch > 0; original > 0 and
+ * 0 < low < high for SV_ROPE_TURNS and SV_ROPE_INDEX, else not used; base > 1.
+ * Both on host memory, without a GPU.
+ */
+sv_status sv_rope_fixed(const double *angle, int n, int64_t *freq_out);
+sv_status sv_rope_freqs(int rot, double base, sv_rope_scaling scaling, double stretch,
+                        double original, double low, double high, int64_t *freq_out);
+
+typedef struct sv_rope_spec {
+    const int64_t *freq_d; /* [rot / 2], device */
+    int rot;               /* rotated components of a head, even */
+    int interleaved;       /* which components are pairs */
+    float gain;            /* finite */
+} sv_rope_spec;
+
+/*
+ * sv_rope: rotate T tokens per row.
+ *  x_d, out_d [batch, T, heads, dim] SV_BF16, SV_F16 or SV_F32; heads and dim dense, rows and
+ *             tokens *_row / *_tok elements apart (multiples of 16 bytes), so a slice of a
+ *             fused projection can be passed. out_d is x_d itself, with the same strides, or
+ *             does not overlap it; its tokens do not overlap each other.
+ *  pos_d      [batch, T] int32: positions (any value), or NULL: token t of row b is at
+ *             start_d[b] + t, or start_d[b] + its depth in the tree of parent_d.
+ *  start_d    [batch] int32, or NULL for 0. Not with pos_d.
+ *  parent_d   [batch, T] int32 or NULL: draft trees as in sv_verify_tree; T <= SV_MAX_TREE.
+ *             Not with pos_d.
+ *  n_new_d    [batch] int32 in [0, T], or NULL for T everywhere. Tokens t >= n_new become 0;
+ *             in place they stay as they are.
+ *  inverse    rotate by -P f_i: the gradient of x from that of out (the gain stays).
+ *  ws_d       any workspace of at least 256 bytes (only its status word is used).
+ * Angles and arithmetic are float32 behind the exact product (a component is off by up to
+ * 2^-21 of its pair's length), rounded once to the type. A row with a bad count or tree becomes
+ * NaN and sets SV_ERR_DEVICE_INPUT.
+ *  Limits: 0 <= batch <= SV_MAX_B; 0 <= T <= SV_KV_MAX_T; heads 1..SV_KV_MAX_HEADS; dim a
+ *  multiple of 16 up to SV_ROPE_MAX_DIM; 2 <= rot <= dim.
+ */
+sv_status sv_rope(const sv_rope_spec *rope, const void *x_d, sv_dtype dtype, int64_t x_row,
+                  int64_t x_tok, int batch, int T, int heads, int dim, const int32_t *pos_d,
+                  const int32_t *start_d, const int32_t *parent_d, const int32_t *n_new_d,
+                  int inverse, void *out_d, int64_t out_row, int64_t out_tok, void *ws_d,
+                  size_t ws_bytes, void *stream);
+
+/*
+ * sv_kv_append_rope: sv_kv_append of keys that are rotated on the way (the cache holds them
+ * rotated; the values as they come), and rotation of the queries.
+ *  parent_d   [batch, T] int32 or NULL: token t of row b is at position len + t, or
+ *             len + its depth in the tree, which is where sv_kv_commit puts an accepted one.
+ *  q_d        [batch, T, q_heads, dim] of the same type, or NULL (q_heads 0). q_out_d as out_d
+ *             of sv_rope, also in what it gets for tokens t >= n_new and bad rows.
+ * Keys are rotated in float32 and rounded once, to e4m3; the page's scale is found from the
+ * rotated keys. A row that sv_kv_append would leave as it was, or with a bad tree, is left as it
+ * was. rope->rot is at most dim.
+ */
+sv_status sv_kv_append_rope(const sv_kv_cache *cache, int layer, const void *k_src_d,
+                            const void *v_src_d, sv_dtype dtype, int64_t k_row, int64_t k_tok,
+                            int64_t v_row, int64_t v_tok, int T, const int32_t *n_new_d,
+                            const int32_t *parent_d, const sv_rope_spec *rope, const void *q_d,
+                            int64_t q_row, int64_t q_tok, int q_heads, void *q_out_d,
+                            int64_t q_out_row, int64_t q_out_tok, void *ws_d, size_t ws_bytes,
+                            void *stream);
+
+/*
  * sv_get_status: wait for `stream`, then read the sticky status word of the
  * workspace into *status_out (SV_OK, SV_ERR_NO_PAGES, SV_ERR_DEVICE_INPUT or
  * SV_ERR_TIMEOUT; the most severe, in this order, seen since the last clear).

@@ -32,6 +32,13 @@ class _CacheStruct(ctypes.Structure):
                                             "max_pages")]
 
 
+class _RopeStruct(ctypes.Structure):
+    """sv_rope_spec of specverify.h."""
+
+    _fields_ = [("freq", ctypes.c_void_p), ("rot", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("gain", ctypes.c_float)]
+
+
 class SpecVerifyError(RuntimeError):
     def __init__(self, fn, code):
         self.code = code
@@ -101,6 +108,17 @@ def load(build_if_missing: bool = True):
     lib.sv_kv_commit.restype = i32
     lib.sv_kv_fork.argtypes = [cp, vp, vp, vp, sz, vp]
     lib.sv_kv_fork.restype = i32
+    f64, rp = ctypes.c_double, ctypes.POINTER(_RopeStruct)
+    lib.sv_rope_fixed.argtypes = [vp, i32, vp]
+    lib.sv_rope_fixed.restype = i32
+    lib.sv_rope_freqs.argtypes = [i32, f64, i32, f64, f64, f64, f64, vp]
+    lib.sv_rope_freqs.restype = i32
+    lib.sv_rope.argtypes = [rp, vp, i32, i64, i64, i32, i32, i32, i32, vp, vp, vp, vp, i32, vp, i64,
+                            i64, vp, sz, vp]
+    lib.sv_rope.restype = i32
+    lib.sv_kv_append_rope.argtypes = [cp, i32, vp, vp, i32, i64, i64, i64, i64, i32, vp, vp, rp, vp,
+                                      i64, i64, i32, vp, i64, i64, vp, sz, vp]
+    lib.sv_kv_append_rope.restype = i32
     lib.sv_get_status.argtypes = [vp, vp, i32, ctypes.POINTER(ctypes.c_int32)]
     lib.sv_get_status.restype = i32
     lib.sv_status_string.argtypes = [i32]
@@ -455,13 +473,14 @@ _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.curre
 
 
 def _kv_stream(stream, cache):
-    """Handle of a call's stream. A call runs on the current device: that must be the cache's."""
+    """Handle of a call's stream. A call runs on the current device: that must be the cache's (or
+    the rotary table's)."""
     if _current_device() != cache.index:
-        raise ValueError(f"the cache is on {cache.t.device}, which is not the current device")
+        raise ValueError(f"the {getattr(cache, 'what', 'cache')} is on {cache.t.device}, which is not the current device")
     if stream is None:
         return _raw_stream(cache.index)
     if stream.device.index != cache.index:
-        raise ValueError(f"the cache is on {cache.t.device}, the stream on {stream.device}")
+        raise ValueError(f"the {getattr(cache, 'what', 'cache')} is on {cache.t.device}, the stream on {stream.device}")
     return stream.cuda_stream
 
 
@@ -626,3 +645,149 @@ def sv_kv_fork(cache: KVCache, src, ok=None, stream=None):
     _check("sv_kv_fork", load().sv_kv_fork(cache.ref, _addr(src), _addr(ok),
                                            cache.ws, cache.nbytes, _kv_stream(stream, cache)))
     return ok
+
+
+# ---------------------------------------------------------------------------------------
+# Rotary positions.
+_SCALINGS = {"none": 0, "linear": 1, "turns": 2, "index": 3}
+
+
+class Rope:
+    """Rotary frequencies on a device (see specverify.h): rot / 2 of them from base and scaling
+    ("none", "linear", "turns" or "index", with stretch and, for the last two, original, low and
+    high), or from `angles` (radians per position); interleaved pairs or halves; the gain of
+    cosine and sine. Holds the status word of sv_rope's calls."""
+
+    what = "rotary table"
+
+    def __init__(self, rot, base=10000.0, interleaved=False, scaling="none", stretch=1.0,
+                 original=0.0, low=1.0, high=32.0, gain=1.0, angles=None, device=None):
+        rot = int(rot)
+        if scaling not in _SCALINGS:
+            raise ValueError(f"scaling must be one of {', '.join(_SCALINGS)}, got {scaling!r}")
+        if rot < 2 or rot % 2 or rot > 512:
+            raise ValueError(f"rot must be even, from 2 to 512, got {rot}")
+        if not abs(float(gain)) <= 3.4028234663852886e38:
+            raise ValueError(f"gain must be finite, got {gain}")
+        freq = (ctypes.c_int64 * (rot // 2))()
+        if angles is not None:
+            if len(angles) != rot // 2:
+                raise ValueError(f"angles must be {rot // 2} numbers")
+            _check("sv_rope_fixed", load().sv_rope_fixed(
+                (ctypes.c_double * len(freq))(*(float(x) for x in angles)), len(freq), freq))
+        else:
+            _check("sv_rope_freqs", load().sv_rope_freqs(
+                rot, float(base), _SCALINGS[scaling], float(stretch), float(original), float(low),
+                float(high), freq))
+        dev = torch.device(device or "cuda")
+        self.freq = torch.tensor(list(freq), dtype=torch.int64).to(dev)
+        self.buf = torch.zeros(512, dtype=torch.uint8, device=dev)
+        off = (-self.buf.data_ptr()) % 256
+        self.t = self.buf[off: off + 256]
+        self.rot, self.index, self.nbytes = rot, self.t.get_device(), 256
+        self.c = _RopeStruct(self.freq.data_ptr(), rot, int(bool(interleaved)), float(gain))
+        self.ref, self.ws = ctypes.byref(self.c), self.t.data_ptr()
+        # Everything above must be complete before a call on any other stream uses it.
+        torch.cuda.synchronize(self.t.device)
+
+    def status(self, stream=None, clear=False) -> int:
+        _kv_stream(stream, self)
+        return Workspace.status(self, stream, clear)
+
+
+def _rope_src(t, name, index, like=None):
+    """Shape of a [batch, T, heads, dim] tensor whose last two dimensions are dense, and the
+    element strides of its rows and tokens."""
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}")
+    shape = t.shape
+    if len(shape) != 4 or (like is not None and (shape != like.shape or t.dtype != like.dtype)):
+        raise ValueError(f"{name} must be [batch, T, heads, dim]" if like is None else
+                         f"{name} must be {list(like.shape)} of {like.dtype}")
+    row, tok, head, one = t.stride()
+    B, T, heads, dim = shape
+    if one != 1 or (heads > 1 and head != dim):
+        raise ValueError(f"{name}: heads and dim must be contiguous")
+    # Strides of dimensions of one element are free in torch: use the dense ones.
+    if T <= 1:
+        tok = heads * dim
+    return shape, (row if B > 1 else T * tok), tok
+
+
+def _rope_ints(t, name, index, shape):
+    """The address of a dense int32 tensor of the shape."""
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}")
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous torch.int32 {list(shape)}")
+    return t.data_ptr()
+
+
+def sv_rope(rope: Rope, x, pos=None, start=None, parent=None, n_new=None, inverse=False, out=None,
+            stream=None):
+    """Rotate x [batch, T, heads, dim] (bf16, fp16 or fp32; slices of a fused projection are
+    fine) by positions pos [batch, T], or start [batch] (0 when not given) plus a token's
+    number or depth in parent [batch, T] (all int32; see specverify.h). out may be x; inverse
+    is the gradient's rotation. Returns out."""
+    index = rope.index
+    shape, row, tok = _rope_src(x, "x", index)
+    B, T, heads, dim = shape
+    made = None
+    if out is None:
+        out = made = x.new_empty(shape)
+        out_tok = heads * dim
+        out_row = T * out_tok
+    else:
+        _, out_row, out_tok = _rope_src(out, "out", index, x)
+    code = load().sv_rope(
+        rope.ref, x.data_ptr(), _kv_dtype(x, "x"), row, tok, B, _int32(T), _int32(heads), _int32(dim),
+        None if pos is None else _rope_ints(pos, "pos", index, shape[:2]),
+        None if start is None else _rope_ints(start, "start", index, shape[:1]),
+        None if parent is None else _rope_ints(parent, "parent", index, shape[:2]),
+        None if n_new is None else _rope_ints(n_new, "n_new", index, shape[:1]),
+        1 if inverse else 0, out.data_ptr(), out_row, out_tok, rope.ws, 256, _kv_stream(stream, rope))
+    if code != SV_OK:
+        raise SpecVerifyError("sv_rope", code)
+    if stream is not None:
+        _kv_made(stream, rope, made)
+    return out
+
+
+def sv_kv_append_rope(cache: KVCache, layer, k, v, rope: Rope, q=None, q_out=None, n_new=None,
+                      parent=None, stream=None):
+    """sv_kv_append with the keys rotated on the way by their positions in the row (a token's
+    depth when parent [batch, T] gives a tree), and the queries q [batch, T, q_heads, dim], if
+    given, rotated to q_out (which may be q; see specverify.h). Returns q_out."""
+    shape, k_row, k_tok = _kv_src(k, "k", cache, cache.heads)
+    v_shape, v_row, v_tok = _kv_src(v, "v", cache, cache.heads)
+    if shape != v_shape or k.dtype != v.dtype:
+        raise ValueError("k and v must have one shape and dtype")
+    if rope.index != cache.index:
+        raise ValueError(f"the rotary table must be on {cache.t.device}")
+    _kv_counts(n_new, "n_new", cache)
+    if parent is not None:
+        _kv_on(parent, "parent", cache, torch.int32)
+        if parent.shape != shape[:2]:
+            raise ValueError(f"parent must be [{cache.batch}, {shape[1]}]")
+    q_row = q_tok = out_row = out_tok = heads = 0
+    made = None
+    if q is not None:
+        q_shape, q_row, q_tok = _kv_src(q, "q", cache, None)
+        if q_shape[1] != shape[1] or q.dtype != k.dtype:
+            raise ValueError("q must have k's tokens and dtype")
+        heads = q_shape[2]
+        if q_out is None:
+            q_out = made = q.new_empty(q_shape)
+            out_tok = heads * cache.dim
+            out_row = shape[1] * out_tok
+        else:
+            _, out_row, out_tok = _rope_src(q_out, "q_out", cache.index, q)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _check("sv_kv_append_rope", load().sv_kv_append_rope(
+        cache.ref, _int32(layer), _addr(k), _addr(v), _kv_dtype(k, "k"), k_row, k_tok, v_row, v_tok,
+        shape[1], _addr(n_new), _addr(parent), rope.ref, _addr(q), q_row, q_tok, heads, _addr(q_out),
+        out_row, out_tok, cache.ws, cache.nbytes, _kv_stream(stream, cache)))
+    if stream is not None:
+        _kv_made(stream, cache, made)
+    return q_out

@@ -35,7 +35,14 @@ bool kv_sizes(const sv_kv_cache* c, KvCache* C) {
   return true;
 }
 
-// Every check that a cache and its workspace need, and their kernel form.
+sv_status done(cudaError_t e) { return e == cudaSuccess ? SV_OK : SV_ERR_CUDA; }
+
+size_t elem_bytes(sv_dtype dt) { return dt == SV_F32 ? 4 : 2; }
+
+}  // namespace
+
+namespace sv {
+
 sv_status kv_open(const sv_kv_cache* c, void* ws_d, size_t ws_bytes, KvCache* C, KvScratch* S) {
   if (!c) return SV_ERR_ARG;
   if (!kv_sizes(c, C)) return SV_ERR_SHAPE;
@@ -71,18 +78,12 @@ sv_status kv_open(const sv_kv_cache* c, void* ws_d, size_t ws_bytes, KvCache* C,
   return SV_OK;
 }
 
-sv_status done(cudaError_t e) { return e == cudaSuccess ? SV_OK : SV_ERR_CUDA; }
-
-size_t elem_bytes(sv_dtype dt) { return dt == SV_F32 ? 4 : 2; }
-
-// A strided [batch, T, heads, dim] source: 16-byte aligned base and strides, tokens that do
-// not overlap.
-bool src_ok(const void* p, int64_t row, int64_t tok, size_t eb, int64_t width) {
+bool kv_src_ok(const void* p, int64_t row, int64_t tok, size_t eb, int64_t width) {
   return p && aligned(p, 16) && row >= 0 && tok >= width && (row * (int64_t)eb) % 16 == 0 &&
          (tok * (int64_t)eb) % 16 == 0;
 }
 
-}  // namespace
+}  // namespace sv
 
 extern "C" {
 
@@ -115,7 +116,7 @@ sv_status sv_kv_append(const sv_kv_cache* cache, int layer, const void* k_src_d,
   if (T == 0) return SV_OK;
   const int64_t width = (int64_t)C.heads * C.dim;
   const size_t eb = elem_bytes(dtype);
-  if (!src_ok(k_src_d, k_row, k_tok, eb, width) || !src_ok(v_src_d, v_row, v_tok, eb, width) ||
+  if (!kv_src_ok(k_src_d, k_row, k_tok, eb, width) || !kv_src_ok(v_src_d, v_row, v_tok, eb, width) ||
       (n_new_d && !aligned(n_new_d, 4)))
     return SV_ERR_ARG;
   return done(launch_kv_append(C, S, layer, KvSrc{k_src_d, k_row, k_tok},
@@ -163,7 +164,7 @@ sv_status sv_kv_attend(const sv_kv_cache* cache, int layer, const void* q_d, sv_
   if (layer < 0 || layer >= C.layers || !std::isfinite(scale2) || window < 0 || sinks < 0)
     return SV_ERR_ARG;
   if (T == 0) return SV_OK;
-  if (!src_ok(q_d, q_row, q_tok, 2, (int64_t)q_heads * C.dim) || !out_d || !aligned(out_d, 16) ||
+  if (!kv_src_ok(q_d, q_row, q_tok, 2, (int64_t)q_heads * C.dim) || !out_d || !aligned(out_d, 16) ||
       (lse_d && !aligned(lse_d, 4)) || (n_new_d && !aligned(n_new_d, 4)) ||
       (parent_d && !aligned(parent_d, 4)))
     return SV_ERR_ARG;

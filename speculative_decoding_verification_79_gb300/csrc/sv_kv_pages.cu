@@ -9,35 +9,6 @@
 
 namespace sv {
 
-constexpr int PG_THREADS = 1024;
-
-// Exclusive prefix sum of x over the block's PG_THREADS threads; *total gets the sum.
-// Two barriers; `sh` holds 64 values.
-template <typename I>
-__device__ I block_scan(I x, I* sh, I* total) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  I v = x;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const I t = __shfl_up_sync(0xffffffffu, v, d);
-    if (lane >= d) v += t;
-  }
-  if (lane == 31) sh[w] = v;
-  __syncthreads();
-  if (w == 0) {
-    I s = sh[lane];
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const I t = __shfl_up_sync(0xffffffffu, s, d);
-      if (lane >= d) s += t;
-    }
-    sh[32 + lane] = s;  // inclusive
-  }
-  __syncthreads();
-  *total = sh[63];
-  return v - x + (w ? sh[32 + w - 1] : 0);
-}
-
 // The first `want` free pages (refs 0) in ascending order, to list[0 ..]; returns how many
 // there are (at most `want`). Whole block.
 __device__ int find_free(const KvCache& C, int want, int32_t* list, int* sh) {

@@ -19,10 +19,6 @@ namespace sv {
 
 constexpr int AP_THREADS = 256;
 constexpr int AP_HALF = AP_THREADS / 2;
-// With more pages to a row than this, its pages are checked by a launch before. On pages of 16,
-// 8 heads of 128: 2,056 tokens (130 pages) take 11.6 us with it and 9.6 without, 4,093 of eight
-// rows (257) 75 and 77, 16,384 of one row 41 and 52, 65,535 155 and 331.
-constexpr int AP_CHECK = 256;
 constexpr int AP_CACHE = 4;  // vectors of 16 values that a thread keeps between the steps
 
 template <typename E>
@@ -94,29 +90,14 @@ __device__ __forceinline__ uint4 quantise16(const float* f, float inv) {
   return o;
 }
 
-// May row b's n new tokens be written: is their number right, and does the row hold the pages
-// that they touch, alone? This thread's part of the answer (all threads' must be true).
-__device__ __forceinline__ bool append_fits(const KvCache& C, int len, int n, int T) {
-  return n > 0 && n <= T && len >= 0 && ((long long)len + n - 1) >> C.lgp < C.max_pages;
-}
-__device__ __forceinline__ bool append_holds(const KvCache& C, int b, int len, int n) {
-  bool fine = true;
-  const int j0 = len >> C.lgp, j1 = (len + n - 1) >> C.lgp;
-  for (int j = j0 + static_cast<int>(threadIdx.x); j <= j1; j += AP_THREADS) {
-    const int p = kv_page(C, b, j << C.lgp);
-    fine = fine && p >= 0 && kv_ld(C.refs + p) == 1;
-  }
-  return fine;
-}
-
-// The same for every row, a CTA each, to flag: a launch before those of long appends, whose CTAs
+// kv_append_fits and kv_append_holds for every row, a CTA each, to flag: a launch before those of long appends, whose CTAs
 // would each look at all of a row's pages.
 __global__ void __launch_bounds__(AP_THREADS)
     kv_append_check_kernel(const KvCache C, const KvScratch S, int T, const int32_t* n_new) {
   kv_enter();
   const int b = blockIdx.x;
   const int n = n_new ? kv_ld(n_new + b) : T, len = kv_ld(C.len + b);
-  const bool fine = n == 0 || (append_fits(C, len, n, T) && append_holds(C, b, len, n));
+  const bool fine = n == 0 || (kv_append_fits(C, len, n, T) && kv_append_holds(C, b, len, n));
   const int all = __syncthreads_and(fine ? 1 : 0);
   if (threadIdx.x == 0) {
     S.flag[b] = all;
@@ -152,7 +133,7 @@ __global__ void __launch_bounds__(AP_THREADS, sizeof(E) == 2 ? 4 : 2)
   const int n = n_new ? kv_ld(n_new + b) : T;
   if (n == 0) return;
   const int len = kv_ld(C.len + b);
-  const bool sane = append_fits(C, len, n, T);
+  const bool sane = kv_append_fits(C, len, n, T);
   const int half = tid / AP_HALF, t0 = tid - half * AP_HALF;
   const KvSrc src = half ? vsrc : ksrc;
   const int j0 = sane ? len >> C.lgp : 0, j = j0 + blockIdx.x;
@@ -177,7 +158,7 @@ __global__ void __launch_bounds__(AP_THREADS, sizeof(E) == 2 ? 4 : 2)
   float* scale = (half ? C.vs : C.ks) + kv_sidx(C, layer, max(p, 0), h);
   const float old = off && p >= 0 ? kv_ld(scale) : 0.f;
   // Every page that the row writes is its own.
-  const bool fine = checked ? kv_ld(S.flag + b) != 0 : sane && append_holds(C, b, len, n);
+  const bool fine = checked ? kv_ld(S.flag + b) != 0 : sane && kv_append_holds(C, b, len, n);
   if (!__syncthreads_and(fine ? 1 : 0)) {
     if (tid == 0 && h == 0 && blockIdx.x == 0 && !checked) kv_report(S.hdr, ST_DEVICE_INPUT);
     return;
@@ -316,6 +297,11 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+cudaError_t launch_kv_append_check(const KvCache& C, const KvScratch& S, int T,
+                                   const int32_t* n_new, cudaStream_t st) {
+  return kv_launch(kv_append_check_kernel, dim3(C.batch), AP_THREADS, 0, st, C, S, T, n_new);
+}
+
 cudaError_t launch_kv_append(const KvCache& C, const KvScratch& S, int layer, KvSrc k, KvSrc v,
                              sv_dtype dt, int T, const int32_t* n_new, cudaStream_t st) {
   // A row's tokens start anywhere in a page, so T of them touch at most this many.
@@ -323,10 +309,9 @@ cudaError_t launch_kv_append(const KvCache& C, const KvScratch& S, int layer, Kv
   const auto kernel = dt == SV_F32    ? kv_append_kernel<float>
                       : dt == SV_BF16 ? kv_append_kernel<__nv_bfloat16>
                                       : kv_append_kernel<__half>;
-  const int checked = static_cast<int>(grid.x) > AP_CHECK;
+  const int checked = static_cast<int>(grid.x) > KV_APPEND_CHECK;
   if (checked) {
-    const cudaError_t e =
-        kv_launch(kv_append_check_kernel, dim3(C.batch), AP_THREADS, 0, st, C, S, T, n_new);
+    const cudaError_t e = launch_kv_append_check(C, S, T, n_new, st);
     if (e != cudaSuccess) return e;
   }
   return kv_launch(kernel, grid, AP_THREADS, 0, st, C, S, layer, k, v, T, n_new, checked);
