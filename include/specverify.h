@@ -494,6 +494,36 @@ sv_status sv_kv_attend(const sv_kv_cache *cache, int layer, const void *q_d, sv_
                        void *stream);
 
 /*
+ * sv_kv_share, sv_kv_attend_shared: sv_kv_attend of rows that hold the same pages for their
+ * first tokens (what sv_kv_fork makes: samples, beams, chats behind one system prompt), which
+ * reads those once for a group of rows instead of once a row.
+ *  share_d    device buffer of sv_kv_share_bytes(cache, T, q_heads) bytes, 256-byte aligned,
+ *             zeroed once (sv_workspace_init; zeros say that no rows share): the groups, and the
+ *             parts of results that a call leaves for its end. It serves calls of up to the T and
+ *             q_heads that it was made for, one at a time.
+ *  group_d    [batch] int32: rows with the same number in [0, batch) are a group (the src of
+ *             sv_kv_fork says so), -1: a row is alone. NULL: rows whose first page is the same.
+ *             Another number sets SV_ERR_DEVICE_INPUT and leaves the row alone.
+ * sv_kv_share finds what the rows of each group have in common: the leading pages that are the same
+ * in all of them and full of each one's cached tokens, cut to a multiple of 128 tokens. It holds
+ * for every layer, and until rows are forked, freed or shortened: reserving, appending
+ * and committing more tokens does not change it. Groups of rows that have little in common are
+ * attended to row by row where that is faster.
+ * sv_kv_attend_shared takes what sv_kv_attend takes and gives the same up to the order of its
+ * float32 sums. It compares the pages of every group's rows again: a row that no longer
+ * holds its group's common tokens gets NaN in out and lse, in this call and all others until the
+ * next sv_kv_share, and sets SV_ERR_DEVICE_INPUT.
+ */
+size_t sv_kv_share_bytes(const sv_kv_cache *cache, int T, int q_heads);
+sv_status sv_kv_share(const sv_kv_cache *cache, const int32_t *group_d, void *share_d,
+                      size_t share_bytes, void *ws_d, size_t ws_bytes, void *stream);
+sv_status sv_kv_attend_shared(const sv_kv_cache *cache, int layer, const void *q_d, sv_dtype dtype,
+                              int64_t q_row, int64_t q_tok, int T, int q_heads,
+                              const int32_t *n_new_d, const int32_t *parent_d, float scale,
+                              int window, int sinks, void *out_d, float *lse_d, void *share_d,
+                              size_t share_bytes, void *ws_d, size_t ws_bytes, void *stream);
+
+/*
  * sv_kv_commit: keep the accepted part of the last block in every layer, and release the
  * pages past it.
  *  accepted_d [batch] int32 in [-1, N-1]: out_accepted of sv_verify (block position 0 is

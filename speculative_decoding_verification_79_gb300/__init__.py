@@ -104,6 +104,13 @@ def load(build_if_missing: bool = True):
     lib.sv_kv_attend.argtypes = [cp, i32, vp, i32, i64, i64, i32, i32, vp, vp, f32, i32, i32, vp,
                                  vp, vp, sz, vp]
     lib.sv_kv_attend.restype = i32
+    lib.sv_kv_share_bytes.argtypes = [cp, i32, i32]
+    lib.sv_kv_share_bytes.restype = sz
+    lib.sv_kv_share.argtypes = [cp, vp, vp, sz, vp, sz, vp]
+    lib.sv_kv_share.restype = i32
+    lib.sv_kv_attend_shared.argtypes = [cp, i32, vp, i32, i64, i64, i32, i32, vp, vp, f32, i32, i32,
+                                        vp, vp, vp, sz, vp, sz, vp]
+    lib.sv_kv_attend_shared.restype = i32
     lib.sv_kv_commit.argtypes = [cp, vp, vp, i32, vp, sz, vp]
     lib.sv_kv_commit.restype = i32
     lib.sv_kv_fork.argtypes = [cp, vp, vp, vp, sz, vp]
@@ -590,11 +597,8 @@ def sv_kv_read(cache: KVCache, start, T, count=None, layer=0, n_layers=None,
     return k_out, v_out
 
 
-def sv_kv_attend(cache: KVCache, layer, q, n_new=None, parent=None, scale=None, window=0,
-                 sinks=0, out=None, lse=None, want_lse=False, stream=None):
-    """Attention of the new tokens' queries [batch, T, q_heads, dim] (bf16 or fp16) over one
-    layer of the cache (see specverify.h); scale defaults to dim ** -0.5. Returns out, or
-    (out, lse) when lse is given or wanted."""
+def _kv_attend(name, cache, layer, q, n_new, parent, scale, window, sinks, out, lse, want_lse,
+               stream, *share):
     shape, row, tok = _kv_src(q, "q", cache, None)
     T, heads = shape[1], shape[2]
     _kv_counts(n_new, "n_new", cache)
@@ -612,14 +616,68 @@ def sv_kv_attend(cache: KVCache, layer, q, n_new=None, parent=None, scale=None, 
             raise ValueError("lse must have q's first three dimensions")
     elif want_lse:
         lse = lse_made = q.new_empty(shape[:3], dtype=torch.float32)
-    _check("sv_kv_attend", load().sv_kv_attend(
+    _check(name, getattr(load(), name)(
         cache.ref, _int32(layer), _addr(q), _kv_dtype(q, "q"), row, tok, T, heads, _addr(n_new),
         _addr(parent), float(cache.dim ** -0.5 if scale is None else scale), _int32(window),
         _int32(sinks),
-        _addr(out), _addr(lse), cache.ws, cache.nbytes, _kv_stream(stream, cache)))
+        _addr(out), _addr(lse), *share, cache.ws, cache.nbytes, _kv_stream(stream, cache)))
     if stream is not None:
         _kv_made(stream, cache, made, lse_made)
     return out if lse is None else (out, lse)
+
+
+def sv_kv_attend(cache: KVCache, layer, q, n_new=None, parent=None, scale=None, window=0,
+                 sinks=0, out=None, lse=None, want_lse=False, stream=None):
+    """Attention of the new tokens' queries [batch, T, q_heads, dim] (bf16 or fp16) over one
+    layer of the cache (see specverify.h); scale defaults to dim ** -0.5. Returns out, or
+    (out, lse) when lse is given or wanted."""
+    return _kv_attend("sv_kv_attend", cache, layer, q, n_new, parent, scale, window, sinks, out,
+                      lse, want_lse, stream)
+
+
+class KVShare:
+    """Which rows of a cache hold the same pages (none at first), and room for the parts of
+    results of sv_kv_attend_shared with up to T tokens of q_heads query heads (see
+    specverify.h)."""
+
+    def __init__(self, cache: KVCache, T, q_heads, stream=None):
+        self.nbytes = int(load().sv_kv_share_bytes(cache.ref, _int32(T), _int32(q_heads)))
+        if self.nbytes == 0:
+            raise ValueError(f"unsupported sizes T={T}, q_heads={q_heads}")
+        self.buf = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=cache.t.device)
+        off = (-self.buf.data_ptr()) % 256
+        self.t = self.buf[off: off + self.nbytes]
+        self.ptr, self.index, self.cache = self.t.data_ptr(), cache.index, cache
+        with torch.cuda.device(self.index):
+            _check("sv_workspace_init",
+                   load().sv_workspace_init(_ptr(self.t), self.nbytes, _kv_stream(stream, cache)))
+        # The zeroing must be complete before a call on any other stream uses it.
+        torch.cuda.synchronize(self.t.device)
+
+
+def _kv_share_of(share, cache):
+    if share.cache is not cache:
+        raise ValueError("share belongs to another cache")
+    return share.ptr, share.nbytes
+
+
+def sv_kv_share(cache: KVCache, share: KVShare, group=None, stream=None):
+    """Find the tokens that rows have in common: rows with the same number in group [batch] int32
+    (-1: alone), or whose first page is the same (see specverify.h). Until rows are forked, freed
+    or shortened, for every layer."""
+    _kv_counts(group, "group", cache)
+    _check("sv_kv_share", load().sv_kv_share(
+        cache.ref, _addr(group), *_kv_share_of(share, cache), cache.ws, cache.nbytes,
+        _kv_stream(stream, cache)))
+
+
+def sv_kv_attend_shared(cache: KVCache, layer, q, share: KVShare, n_new=None, parent=None,
+                        scale=None, window=0, sinks=0, out=None, lse=None, want_lse=False,
+                        stream=None):
+    """sv_kv_attend that reads the tokens which rows have in common (sv_kv_share) once for all of
+    them."""
+    return _kv_attend("sv_kv_attend_shared", cache, layer, q, n_new, parent, scale, window, sinks,
+                      out, lse, want_lse, stream, *_kv_share_of(share, cache))
 
 
 def sv_kv_commit(cache: KVCache, accepted, N, path=None, stream=None):

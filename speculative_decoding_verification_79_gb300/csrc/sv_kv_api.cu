@@ -2,7 +2,7 @@
 // layout, launches. Declarations and contracts are in include/specverify.h.
 #include <cmath>
 
-#include "sv_kv.cuh"
+#include "sv_kv_share.cuh"
 
 using namespace sv;
 
@@ -85,6 +85,68 @@ bool kv_src_ok(const void* p, int64_t row, int64_t tok, size_t eb, int64_t width
 
 }  // namespace sv
 
+namespace {
+
+// The checks of an attention call, and its arguments (not set when T is 0).
+sv_status attend_args(const sv_kv_cache* cache, int layer, const void* q_d, sv_dtype dtype,
+                      int64_t q_row, int64_t q_tok, int T, int q_heads, const int32_t* n_new_d,
+                      const int32_t* parent_d, float scale, int window, int sinks, void* out_d,
+                      float* lse_d, void* ws_d, size_t ws_bytes, AttendArgs* args) {
+  if (dtype != SV_BF16 && dtype != SV_F16) return SV_ERR_DTYPE;
+  KvCache C;
+  KvScratch S;
+  const sv_status st = kv_open(cache, ws_d, ws_bytes, &C, &S);
+  if (st != SV_OK) return st;
+  if (T < 0 || T > SV_KV_MAX_T || (parent_d && T > SV_MAX_TREE)) return SV_ERR_SHAPE;
+  if (q_heads < C.heads || q_heads % C.heads != 0 || q_heads / C.heads > KV_ROWS)
+    return SV_ERR_SHAPE;
+  // Key tiles of 128 tokens, and what a query tile of 128 rows costs beside them, in 31 bits.
+  const long long qtiles = ((long long)T * (q_heads / C.heads) + KV_ROWS - 1) / KV_ROWS;
+  const long long ktiles = ((long long)C.max_pages * C.page + 127) / 128 + KV_EXTRA;
+  if (qtiles * C.batch * C.heads >= (1LL << 31) / ktiles) return SV_ERR_SHAPE;
+  if ((long long)C.max_pages * C.page > (1LL << 31) - 256) return SV_ERR_SHAPE;
+  const float scale2 = static_cast<float>((double)scale * 1.4426950408889634);
+  if (layer < 0 || layer >= C.layers || !std::isfinite(scale2) || window < 0 || sinks < 0)
+    return SV_ERR_ARG;
+  if (T == 0) return SV_OK;
+  if (!kv_src_ok(q_d, q_row, q_tok, 2, (int64_t)q_heads * C.dim) || !out_d || !aligned(out_d, 16) ||
+      (lse_d && !aligned(lse_d, 4)) || (n_new_d && !aligned(n_new_d, 4)) ||
+      (parent_d && !aligned(parent_d, 4)))
+    return SV_ERR_ARG;
+  AttendArgs& A = *args;
+  A.C = C;
+  A.S = S;
+  A.layer = layer;
+  A.q = q_d;
+  A.q_row = q_row;
+  A.q_tok = q_tok;
+  A.T = T;
+  A.q_heads = q_heads;
+  A.group = q_heads / C.heads;
+  A.n_new = n_new_d;
+  A.parent = parent_d;
+  A.scale = scale2;
+  A.window = window;
+  A.sinks = sinks;
+  A.wait_limit = wait_limit();
+  A.out = out_d;
+  A.lse = lse_d;
+  return SV_OK;
+}
+
+// A cache's sizes with T tokens of q_heads query heads, whose query tiles and their parts can be
+// numbered in 31 bits.
+bool share_sizes(const sv_kv_cache* cache, int T, int q_heads, KvCache* C) {
+  if (!kv_sizes(cache, C) || T < 1 || T > SV_KV_MAX_T || q_heads < C->heads || q_heads % C->heads != 0 ||
+      q_heads / C->heads > KV_ROWS)
+    return false;
+  const long long rows = (long long)T * (q_heads / C->heads), lim = (1LL << 31) / C->heads;
+  return C->batch * ((rows + KV_ROWS - 1) / KV_ROWS) < lim - KV_MAX_CTAS &&
+         C->batch * rows < (1LL << 31) - KV_ROWS && C->batch * rows / KV_ROWS + C->batch < lim - KV_MAX_CTAS;
+}
+
+}  // namespace
+
 extern "C" {
 
 size_t sv_kv_workspace_bytes(const sv_kv_cache* cache) {
@@ -147,46 +209,47 @@ sv_status sv_kv_attend(const sv_kv_cache* cache, int layer, const void* q_d, sv_
                        const int32_t* n_new_d, const int32_t* parent_d, float scale, int window,
                        int sinks, void* out_d, float* lse_d, void* ws_d, size_t ws_bytes,
                        void* stream) {
-  if (dtype != SV_BF16 && dtype != SV_F16) return SV_ERR_DTYPE;
-  KvCache C;
-  KvScratch S;
-  const sv_status st = kv_open(cache, ws_d, ws_bytes, &C, &S);
-  if (st != SV_OK) return st;
-  if (T < 0 || T > SV_KV_MAX_T || (parent_d && T > SV_MAX_TREE)) return SV_ERR_SHAPE;
-  if (q_heads < C.heads || q_heads % C.heads != 0 || q_heads / C.heads > KV_ROWS)
-    return SV_ERR_SHAPE;
-  // Key tiles of 128 tokens, and what a query tile of 128 rows costs beside them, in 31 bits.
-  const long long qtiles = ((long long)T * (q_heads / C.heads) + KV_ROWS - 1) / KV_ROWS;
-  const long long ktiles = ((long long)C.max_pages * C.page + 127) / 128 + KV_EXTRA;
-  if (qtiles * C.batch * C.heads >= (1LL << 31) / ktiles) return SV_ERR_SHAPE;
-  if ((long long)C.max_pages * C.page > (1LL << 31) - 256) return SV_ERR_SHAPE;
-  const float scale2 = static_cast<float>((double)scale * 1.4426950408889634);
-  if (layer < 0 || layer >= C.layers || !std::isfinite(scale2) || window < 0 || sinks < 0)
-    return SV_ERR_ARG;
-  if (T == 0) return SV_OK;
-  if (!kv_src_ok(q_d, q_row, q_tok, 2, (int64_t)q_heads * C.dim) || !out_d || !aligned(out_d, 16) ||
-      (lse_d && !aligned(lse_d, 4)) || (n_new_d && !aligned(n_new_d, 4)) ||
-      (parent_d && !aligned(parent_d, 4)))
-    return SV_ERR_ARG;
   AttendArgs A;
-  A.C = C;
-  A.S = S;
-  A.layer = layer;
-  A.q = q_d;
-  A.q_row = q_row;
-  A.q_tok = q_tok;
-  A.T = T;
-  A.q_heads = q_heads;
-  A.group = q_heads / C.heads;
-  A.n_new = n_new_d;
-  A.parent = parent_d;
-  A.scale = scale2;
-  A.window = window;
-  A.sinks = sinks;
-  A.wait_limit = wait_limit();
-  A.out = out_d;
-  A.lse = lse_d;
+  const sv_status st = attend_args(cache, layer, q_d, dtype, q_row, q_tok, T, q_heads, n_new_d, parent_d,
+                                   scale, window, sinks, out_d, lse_d, ws_d, ws_bytes, &A);
+  if (st != SV_OK || T == 0) return st;
   return done(launch_kv_attend(A, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+size_t sv_kv_share_bytes(const sv_kv_cache* cache, int T, int q_heads) {
+  SharedArgs A;
+  return share_sizes(cache, T, q_heads, &A.C) ? kv_share_layout(A.C, T, q_heads / A.C.heads, nullptr, &A) : 0;
+}
+
+sv_status sv_kv_share(const sv_kv_cache* cache, const int32_t* group_d, void* share_d,
+                      size_t share_bytes, void* ws_d, size_t ws_bytes, void* stream) {
+  SharedArgs A;
+  const sv_status st = kv_open(cache, ws_d, ws_bytes, &A.C, &A.S);
+  if (st != SV_OK) return st;
+  // (The groups are at the start of the buffer, whatever T and heads it was made for.)
+  if (!share_d || !aligned(share_d, 256) || share_bytes < kv_share_layout(A.C, 1, 1, nullptr, &A))
+    return SV_ERR_WORKSPACE;
+  if (group_d && !aligned(group_d, 4)) return SV_ERR_ARG;
+  kv_share_layout(A.C, 1, 1, static_cast<unsigned char*>(share_d), &A);
+  return done(launch_kv_share(A.C, A.S, A.H, group_d, static_cast<cudaStream_t>(stream)));
+}
+
+sv_status sv_kv_attend_shared(const sv_kv_cache* cache, int layer, const void* q_d, sv_dtype dtype,
+                              int64_t q_row, int64_t q_tok, int T, int q_heads,
+                              const int32_t* n_new_d, const int32_t* parent_d, float scale,
+                              int window, int sinks, void* out_d, float* lse_d, void* share_d,
+                              size_t share_bytes, void* ws_d, size_t ws_bytes, void* stream) {
+  SharedArgs A;
+  const sv_status st = attend_args(cache, layer, q_d, dtype, q_row, q_tok, T, q_heads, n_new_d, parent_d,
+                                   scale, window, sinks, out_d, lse_d, ws_d, ws_bytes, &A);
+  if (st != SV_OK) return st;
+  if (T == 0) return SV_OK;
+  KvCache C;
+  if (!share_sizes(cache, T, q_heads, &C)) return SV_ERR_SHAPE;
+  if (!share_d || !aligned(share_d, 256) ||
+      share_bytes < kv_share_layout(A.C, T, A.group, static_cast<unsigned char*>(share_d), &A))
+    return SV_ERR_WORKSPACE;
+  return done(launch_kv_attend_shared(A, dtype, static_cast<cudaStream_t>(stream)));
 }
 
 sv_status sv_kv_commit(const sv_kv_cache* cache, const int32_t* accepted_d, const int32_t* path_d,

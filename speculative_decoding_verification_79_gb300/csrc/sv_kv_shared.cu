@@ -1,0 +1,297 @@
+// sv_kv_shared.cu -- attention of rows that share pages (sm_103a): which rows share how much, the
+// launch, and the join of the parts. The kernel is in sv_kv_shared.cuh.
+#include "sv_kv_shared.cuh"
+
+namespace sv {
+
+namespace {
+
+constexpr int SH_THREADS = 1024;
+constexpr int SH_MOST = 4096;  // rows, at most (SV_MAX_B)
+static_assert(SV_MAX_B <= SH_MOST, "a CTA sorts all rows");
+
+// Rows by group. One CTA sorts (group's key, row), lowest rows first, and numbers the runs of two
+// or more: rows of those go to `order`, all others are alone. The key is group[b] or, without it,
+// the page of the row's first token.
+__global__ void __launch_bounds__(SH_THREADS)
+    kv_share_group_kernel(const KvCache C, const KvScratch S, const KvShare H, const int32_t* group) {
+  kv_enter();
+  __shared__ unsigned long long s_key[SH_MOST];
+  __shared__ int s_scan[64], s_first[SH_MOST / 2 + 1], s_most;
+  constexpr unsigned long long ALONE = 1ull << 48, NONE = ~0ull;
+  const int tid = threadIdx.x;
+  int n = 2;
+  while (n < C.batch) n *= 2;
+  if (tid == 0) s_most = 0;
+  for (int b = tid; b < n; b += SH_THREADS) {
+    unsigned long long key = NONE;
+    if (b < C.batch) {
+      key = ALONE | b;
+      if (group) {
+        const int g = kv_ld(group + b);
+        if (g < -1 || g >= C.batch)
+          kv_report(S.hdr, ST_DEVICE_INPUT);
+        else if (g >= 0)
+          key = (unsigned long long)g << 12 | b;
+      } else {
+        const int p = kv_page(C, b, 0);
+        if (p >= 0) key = (unsigned long long)p << 12 | b;
+      }
+      H.bad[b] = 0;
+    }
+    s_key[b] = key;
+  }
+  for (int size = 2; size <= n; size *= 2)
+    for (int d = size / 2; d; d /= 2) {
+      __syncthreads();
+      for (int i = tid; i < n / 2; i += SH_THREADS) {
+        const int lo = i / d * 2 * d + i % d, hi = lo + d;
+        const bool up = (lo & size) == 0;
+        const unsigned long long x = s_key[lo], y = s_key[hi];
+        if ((x > y) == up) {
+          s_key[lo] = y;
+          s_key[hi] = x;
+        }
+      }
+    }
+  __syncthreads();
+  // Four neighbours a thread: rows in groups before each (low half) and groups before (high).
+  auto same = [&](int i) {  // are entries i - 1 and i of one group?
+    return i > 0 && i < C.batch && s_key[i] < ALONE && s_key[i] >> 12 == s_key[i - 1] >> 12;
+  };
+  int in[4], c = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int i = 4 * tid + k;
+    const bool with = same(i), head = !with && same(i + 1);
+    in[k] = head ? 2 : (with ? 1 : 0);
+    c += (in[k] ? 1 : 0) + (in[k] == 2 ? 1 << 16 : 0);
+  }
+  int all;
+  int at = block_scan(c, s_scan, &all);
+  const int groups = all >> 16, rows = all & 0xffff, at0 = at;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (in[k] == 2) s_first[at >> 16] = at & 0xffff;
+    at += (in[k] ? 1 : 0) + (in[k] == 2 ? 1 << 16 : 0);
+  }
+  if (tid == 0) s_first[groups] = rows;
+  __syncthreads();
+  at = at0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int i = 4 * tid + k;
+    if (i >= C.batch) break;
+    const int b = static_cast<int>(s_key[i] & 0xfff);
+    if (!in[k]) {
+      H.row[b] = make_int4(-1, 1, 0, 0);
+      continue;
+    }
+    const int g = (at >> 16) - (in[k] == 2 ? 0 : 1), first = s_first[g], size = s_first[g + 1] - first;
+    H.row[b] = make_int4(g, size, 0, (at & 0xffff) - first);
+    H.order[at & 0xffff] = b;
+    if (in[k] == 2) {
+      H.group[g] = make_int4(first, size, 0x7fffffff, b);
+      atomicMax(&s_most, size);
+    }
+    at += 1 + (in[k] == 2 ? 1 << 16 : 0);
+  }
+  __syncthreads();
+  if (tid == 0) {
+    H.head[0] = groups;
+    H.head[1] = s_most;
+    H.head[2] = rows;
+  }
+}
+
+// How many tokens every row of a group has in common: whole tiles of 128 on pages that are the same
+// in all of them, and no more than any row holds. A warp a row compares it with the group's first.
+__global__ void __launch_bounds__(256) kv_share_pages_kernel(const KvCache C, const KvShare H) {
+  kv_enter();
+  const int i = blockIdx.x * 8 + threadIdx.x / 32, lane = threadIdx.x & 31;
+  if (i >= kv_ld(H.head + 2)) return;
+  const int b = kv_ld(H.order + i), g = kv_ld(H.row + b).x, lead = kv_ld(H.group + g).w;
+  const int len = max(0, kv_ld(C.len + b));
+  const int pages = min(min(kv_ld(C.np + b), C.max_pages), len >> C.lgp);
+  const int32_t *mine = C.table + (size_t)b * C.max_pages, *its = C.table + (size_t)lead * C.max_pages;
+  int common = max(pages, 0);
+  for (int j0 = 0; j0 < common; j0 += 128) {
+    unsigned differ[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int j = j0 + 32 * k + lane;
+      bool d = j >= common;
+      if (!d) {
+        const int p = kv_ld(mine + j);
+        d = p < 0 || p >= C.pages || p != kv_ld(its + j);
+      }
+      differ[k] = __ballot_sync(0xffffffffu, d);
+    }
+#pragma unroll
+    for (int k = 3; k >= 0; --k)
+      if (differ[k]) common = min(common, j0 + 32 * k + __ffs(differ[k]) - 1);
+  }
+  if (lane == 0)
+    atomicMin(&H.group[g].z, static_cast<int>(((long long)common << C.lgp) & ~127LL));
+}
+
+__global__ void __launch_bounds__(256) kv_share_rows_kernel(const KvCache C, const KvShare H) {
+  kv_enter();
+  const int b = blockIdx.x * 256 + threadIdx.x;
+  if (b >= C.batch) return;
+  const int g = kv_ld(H.row + b).x;
+  if (g >= 0) H.row[b].z = kv_ld(&H.group[g].z);
+}
+
+// Joins the parts of every query tile of a row: its own keys' and, where it is in a group, those
+// of the common ones, in the order of the CTAs that made them. A thread takes four components of a
+// query. (A query tile with one part has its result already.)
+constexpr int SJ_THREADS = 256;
+// (When a wait gave up, a query tile may have no span of this call: what is there is kept in range.)
+__device__ __forceinline__ KvSpan join_span(const KvSpan* p) {
+  const KvSpan s = kv_ld(p);
+  return KvSpan{min(max(s.first, 0), KV_MAX_CTAS - 1), min(s.last, KV_MAX_CTAS - 1)};
+}
+__global__ void __launch_bounds__(SJ_THREADS)
+    kv_shared_join_kernel(const __grid_constant__ SharedArgs A, int bf16) {
+  kv_enter();
+  const int heads = A.C.heads, vec = A.C.dim / 4;
+  const long long items = (long long)A.C.batch * A.tiles * heads;
+  for (long long item = blockIdx.x; item < items; item += gridDim.x) {
+    const int h = static_cast<int>(item % heads), bt = static_cast<int>(item / heads);
+    const int b = bt / A.tiles, rt = bt - b * A.tiles;
+    const AtRow row = at_row<AT_OWN>(A, b);
+    if (rt >= row.nrt) continue;
+    const int no = at_tile_no(A, AT_OWN, b, rt, h);
+    const KvSpan own = join_span(A.own_span + no);
+    if (!row.skip && own.first == own.last) continue;
+    const int r0 = rt * row.rr, R = min(r0 + row.rr, row.rows) - r0;
+    const bool bad = kv_ld(A.H.bad + b) != 0;
+    const int4 mine = kv_ld(A.H.row + b);
+    const AtRow group = row.skip ? at_row<AT_GROUPS>(A, mine.x) : row;
+    const int n = (R + 7) / 8 * 8 * vec;
+    for (int e = threadIdx.x; e < n; e += SJ_THREADS) {
+      const int r = e / (8 * vec) * 8 + e % 8, dv = e / 8 % vec;
+      if (r >= R) continue;
+      const int t = (r0 + r) / A.group, gh = r0 + r - t * A.group;
+      float ref = -INFINITY, sum = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      auto add = [&](const float2* stats, const float* part, int no, KvSpan span, int r, int rows) {
+        constexpr int K = 4;  // loads in flight
+        for (int c0 = span.first; c0 <= span.last; c0 += K) {
+          float2 s2[K];
+          float4 y[K];
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            const int id = no + min(c0 + k, span.last);
+            s2[k] = __ldcg(stats + (size_t)id * rows + r);
+            y[k] = __ldcg(reinterpret_cast<const float4*>(part) + at_part(id, r, 4 * dv, A.C.dim, rows));
+          }
+          float top = ref;
+#pragma unroll
+          for (int k = 0; k < K; ++k)
+            if (s2[k].y != 0.f) top = fmaxf(top, s2[k].x);
+          const float f0 = sum == 0.f ? 0.f : exp2f(ref - top);
+          ref = top;
+          sum *= f0;
+          o.x *= f0;
+          o.y *= f0;
+          o.z *= f0;
+          o.w *= f0;
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            if (s2[k].y == 0.f || c0 + k > span.last) continue;
+            const float f = exp2f(s2[k].x - top);
+            sum = fmaf(s2[k].y, f, sum);
+            o.x = fmaf(y[k].x, f, o.x);
+            o.y = fmaf(y[k].y, f, o.y);
+            o.z = fmaf(y[k].z, f, o.z);
+            o.w = fmaf(y[k].w, f, o.w);
+          }
+        }
+      };
+      if (row.skip) {
+        const int i = (mine.w * A.T + t) * A.group + gh, grt = i / group.rr;
+        if (!A.window || at_tile<AT_GROUPS>(A, group, mine.x, grt).tiles() > 0) {
+          const int gno = at_tile_no(A, AT_GROUPS, mine.x, grt, h);
+          add(A.stat, A.part, gno, join_span(A.span + gno), i - grt * group.rr, KV_ROWS);
+        }
+      }
+      add(A.own_stat, A.own_part, no, own, r, A.own_rows);
+      float inv = sum == 0.f ? 0.f : 1.f / sum;
+      if (bad) inv = sum = NAN;
+      const long long out = ((long long)b * A.T + t) * A.q_heads + h * A.group + gh;
+      at_store4(A.out, out * A.C.dim + dv * 4,
+                make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv), bf16);
+      if (dv == 0 && A.lse)
+        A.lse[out] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+    }
+  }
+}
+
+}  // namespace
+
+size_t kv_share_layout(const KvCache& C, int T, int group, unsigned char* base, SharedArgs* A) {
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    unsigned char* const at = base + off;
+    off = align_up(off + bytes, 256);
+    return at;
+  };
+  const size_t B = (size_t)C.batch;
+  A->H.head = reinterpret_cast<int32_t*>(take(4 * KV_SHARE_HEAD));
+  A->H.row = reinterpret_cast<int4*>(take(16 * B));
+  A->H.group = reinterpret_cast<int4*>(take(16 * (B / 2 + 1)));
+  A->H.order = reinterpret_cast<int32_t*>(take(4 * B));
+  A->H.bad = reinterpret_cast<int32_t*>(take(4 * B));
+  const size_t rows = (size_t)T * group;
+  A->tiles = static_cast<int>((rows + KV_ROWS - 1) / KV_ROWS);
+  A->own_rows = rows < KV_ROWS ? static_cast<int>((rows + 7) / 8 * 8) : KV_ROWS;
+  // Slots: a query tile has one more than CTAs' shares end in it.
+  const size_t own_tiles = B * A->tiles * C.heads, tiles = (B * rows / KV_ROWS + B / 2 + 1) * C.heads;
+  A->own_span = reinterpret_cast<KvSpan*>(take(sizeof(KvSpan) * own_tiles));
+  A->span = reinterpret_cast<KvSpan*>(take(sizeof(KvSpan) * tiles));
+  A->own_stat = reinterpret_cast<float2*>(take(8 * (own_tiles + KV_MAX_CTAS) * A->own_rows));
+  A->stat = reinterpret_cast<float2*>(take(8 * (tiles + KV_MAX_CTAS) * KV_ROWS));
+  A->own_part = reinterpret_cast<float*>(take(4 * (own_tiles + KV_MAX_CTAS) * A->own_rows * C.dim));
+  A->part = reinterpret_cast<float*>(take(4 * (tiles + KV_MAX_CTAS) * KV_ROWS * C.dim));
+  return off;
+}
+
+cudaError_t launch_kv_share(const KvCache& C, const KvScratch& S, const KvShare& H,
+                            const int32_t* group, cudaStream_t st) {
+  cudaError_t e = kv_launch(kv_share_group_kernel, dim3(1), SH_THREADS, 0, st, C, S, H, group);
+  if (e == cudaSuccess)
+    e = kv_launch(kv_share_pages_kernel, dim3((C.batch + 7) / 8), 256, 0, st, C, H);
+  if (e == cudaSuccess)
+    e = kv_launch(kv_share_rows_kernel, dim3((C.batch + 255) / 256), 256, 0, st, C, H);
+  return e;
+}
+
+cudaError_t launch_kv_attend_shared(const SharedArgs& A, sv_dtype dt, cudaStream_t st) {
+  static const SharedKernel* const kernels[2][2] = {{shared_kernels_f16_1, shared_kernels_f16_2},
+                                                    {shared_kernels_bf16_1, shared_kernels_bf16_2}};
+  int dev = 0;
+  cudaError_t e;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  static OncePerDevice sized;  // (the attribute belongs to the device that is current)
+  e = static_cast<cudaError_t>(sized.run(dev, [] {
+    cudaError_t attr = cudaSuccess;
+    for (int i = 0; i < 12 && attr == cudaSuccess; ++i)
+      attr = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernels[i / 6][i / 3 % 2][i % 3]),
+                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  (int)(AT_SMEM - AT_STATIC));
+    return static_cast<int>(attr);
+  }));
+  if (e != cudaSuccess) return e;
+  AttendLaunch L;
+  if ((e = at_launch(A, dt, at_width((long long)A.T * A.group), dev, &L)) != cudaSuccess) return e;
+  const SharedKernel kernel = kernels[dt == SV_BF16][L.ndb - 1][L.width == 32 ? 0 : (L.width == 64 ? 1 : 2)];
+  if ((e = kv_launch(kernel, dim3(L.grid), AT_THREADS, L.smem, st, A, L.P, L.tm[0], L.tm[1])) != cudaSuccess)
+    return e;
+  const long long items = (long long)A.C.batch * A.tiles * A.C.heads, most = 8LL * L.grid;
+  return kv_launch(kv_shared_join_kernel, dim3(static_cast<unsigned>(items < most ? items : most)), SJ_THREADS,
+                   0, st, A, dt == SV_BF16 ? 1 : 0);
+}
+
+}  // namespace sv
