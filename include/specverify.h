@@ -507,13 +507,17 @@ sv_status sv_kv_attend(const sv_kv_cache *cache, int layer, const void *q_d, sv_
  * sv_kv_share finds what the rows of each group have in common: the leading pages that are the same
  * in all of them and full of each one's cached tokens, cut to a multiple of 128 tokens. It holds
  * for every layer, and until rows are forked, freed or shortened: reserving, appending
- * and committing more tokens does not change it. Groups of rows that have little in common are
- * attended to row by row where that is faster.
+ * and committing more tokens does not change it.
  * sv_kv_attend_shared takes what sv_kv_attend takes and gives the same up to the order of its
- * float32 sums. It compares the pages of every group's rows again: a row that no longer
- * holds its group's common tokens gets NaN in out and lse, in this call and all others until the
- * next sv_kv_share, and sets SV_ERR_DEVICE_INPUT.
+ * float32 sums. Rows of a group that has little in common, or that gains nothing from it (128
+ * queries and more a row fill their products by themselves), are attended to one by one. Where a
+ * group's common tokens are read once, its rows' pages are compared again: a row that no longer
+ * holds them gets NaN in out and lse, in this call and all others until the next sv_kv_share, and
+ * sets SV_ERR_DEVICE_INPUT.
+ * sv_set_share_always(1) has every group's common tokens read once, whether that is faster or not;
+ * returns what was set before (a testing aid, for the whole process).
  */
+int sv_set_share_always(int on);
 size_t sv_kv_share_bytes(const sv_kv_cache *cache, int T, int q_heads);
 sv_status sv_kv_share(const sv_kv_cache *cache, const int32_t *group_d, void *share_d,
                       size_t share_bytes, void *ws_d, size_t ws_bytes, void *stream);

@@ -104,6 +104,8 @@ def load(build_if_missing: bool = True):
     lib.sv_kv_attend.argtypes = [cp, i32, vp, i32, i64, i64, i32, i32, vp, vp, f32, i32, i32, vp,
                                  vp, vp, sz, vp]
     lib.sv_kv_attend.restype = i32
+    lib.sv_set_share_always.argtypes = [i32]
+    lib.sv_set_share_always.restype = i32
     lib.sv_kv_share_bytes.argtypes = [cp, i32, i32]
     lib.sv_kv_share_bytes.restype = sz
     lib.sv_kv_share.argtypes = [cp, vp, vp, sz, vp, sz, vp]
@@ -376,6 +378,12 @@ def set_wait_limit(cycles: int) -> int:
     """Bound (GPU clock cycles) on a verify or cache attention call's waits for other warps;
     cycles <= 0 restores the default. Returns the previous bound (a testing aid)."""
     return int(load().sv_set_wait_limit(int(cycles)))
+
+
+def set_share_always(on: bool) -> bool:
+    """Have sv_kv_attend_shared read every group's common tokens once, whether that is faster or
+    not (a testing aid). Returns what was set before."""
+    return bool(load().sv_set_share_always(int(bool(on))))
 
 
 def sv_verify_tree(target, draft, parent, draft_tok, n_nodes, uniforms, temperature,

@@ -18,7 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libspecverify.so")
 SOURCES = ["sv_api.cu", "sv_verify.cu", "sv_schedule.cu", "sv_static.cu", "sv_calib.cu", "sv_markov.cu",
            "sv_tree.cu", "sv_kv_api.cu", "sv_kv_pages.cu", "sv_kv_store.cu", "sv_kv_attend.cu",
-           "sv_rope_api.cu", "sv_rope.cu", "sv_kv_rope.cu", "sv_kv_shared.cu",
+           "sv_rope_api.cu", "sv_rope.cu", "sv_kv_rope.cu", "sv_kv_shared.cu", "sv_kv_group.cu",
            "sv_kv_shared_f16_1.cu", "sv_kv_shared_f16_2.cu", "sv_kv_shared_bf16_1.cu",
            "sv_kv_shared_bf16_2.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

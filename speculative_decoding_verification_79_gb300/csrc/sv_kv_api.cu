@@ -1,5 +1,6 @@
 // sv_kv_api.cu -- the C-ABI boundary of the key/value cache: argument checks, workspace
 // layout, launches. Declarations and contracts are in include/specverify.h.
+#include <atomic>
 #include <cmath>
 
 #include "sv_kv_share.cuh"
@@ -7,6 +8,8 @@
 using namespace sv;
 
 namespace {
+
+std::atomic<int> share_always{0};
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -142,7 +145,8 @@ bool share_sizes(const sv_kv_cache* cache, int T, int q_heads, KvCache* C) {
     return false;
   const long long rows = (long long)T * (q_heads / C->heads), lim = (1LL << 31) / C->heads;
   return C->batch * ((rows + KV_ROWS - 1) / KV_ROWS) < lim - KV_MAX_CTAS &&
-         C->batch * rows < (1LL << 31) - KV_ROWS && C->batch * rows / KV_ROWS + C->batch < lim - KV_MAX_CTAS;
+         C->batch * rows < (1LL << 31) - KV_ROWS && C->batch * rows / KV_ROWS + C->batch + 2 < lim - 2 * KV_MAX_CTAS &&
+         (rows + KV_ROWS - 1) / KV_ROWS < 65536;
 }
 
 }  // namespace
@@ -216,6 +220,8 @@ sv_status sv_kv_attend(const sv_kv_cache* cache, int layer, const void* q_d, sv_
   return done(launch_kv_attend(A, dtype, static_cast<cudaStream_t>(stream)));
 }
 
+int sv_set_share_always(int on) { return share_always.exchange(on != 0); }
+
 size_t sv_kv_share_bytes(const sv_kv_cache* cache, int T, int q_heads) {
   SharedArgs A;
   return share_sizes(cache, T, q_heads, &A.C) ? kv_share_layout(A.C, T, q_heads / A.C.heads, nullptr, &A) : 0;
@@ -249,6 +255,9 @@ sv_status sv_kv_attend_shared(const sv_kv_cache* cache, int layer, const void* q
   if (!share_d || !aligned(share_d, 256) ||
       share_bytes < kv_share_layout(A.C, T, A.group, static_cast<unsigned char*>(share_d), &A))
     return SV_ERR_WORKSPACE;
+  A.always = share_always.load(std::memory_order_relaxed);
+  // Values of up to 128 components, and keys that all of a group's queries see.
+  A.large = A.C.dim <= 128 && window == 0;
   return done(launch_kv_attend_shared(A, dtype, static_cast<cudaStream_t>(stream)));
 }
 

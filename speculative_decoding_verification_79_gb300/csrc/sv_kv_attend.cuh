@@ -31,6 +31,8 @@ constexpr int AT_BLK = AT_KEYS * 128;  // 128 tokens x 128 bytes
 constexpr int AT_MAX_RING = 8;   // most K tiles, and V tiles, in shared memory
 constexpr int AT_INFO = 32;      // key tiles whose page data are kept
 constexpr int AT_PTERMS = 3;     // e5m2 terms of a weight
+// Warps of sv_kv_group.cu's CTA that form weights, and that convert values.
+constexpr int GR_WEIGHTS = 16, GR_CONVERT = 4;
 template <bool BF16>
 constexpr int AT_QTERMS = BF16 ? 2 : 3;  // terms of a query: e4m3, then e5m2
 // Weights are kept as 2^(x - m + 11): up to 2^15 before the reference must move (below
@@ -199,14 +201,24 @@ __host__ __device__ constexpr int at_width(long long rows) {
   return rows <= 32 ? 32 : (rows <= 64 ? 64 : 128);
 }
 
-// Key tiles that a group of n rows has in common, or 0 when its rows are better off alone: when
-// reading them once does not save more than the group's own query tiles cost.
+// Large groups are attended to by a kernel of their own, sv_kv_group.cu, in 1,850 cycles a key tile.
+constexpr int AT_LARGE_COST = 1850;
+__device__ __forceinline__ bool at_large(const SharedArgs& A, long long rows) {
+  return A.large && at_width(rows) == 128;
+}
+// Key tiles that a group of n rows has in common, or 0 when its rows are better off alone. Sharing
+// takes the group's query tiles, and for each row's own query tile results in parts, which are
+// written, read and joined: some 8,000 cycles and 200 a query (for 8 queries 17 us of 512 query
+// tiles, for 128 queries 66 us of 544). Four rows of 128 queries each gain nothing from it: trees of
+// 16 nodes of 8 queries on 3,000 common tokens took 226 us shared and 151 alone.
 __device__ __forceinline__ int at_common(const SharedArgs& A, int n, int tokens) {
   const int keys = tokens / AT_KEYS;
+  if (A.always) return keys;
   const long long rows = (long long)A.T * A.group, all = n * rows;
-  const long long alone = n * ((rows + KV_ROWS - 1) / KV_ROWS) * at_cost(at_width(rows)) * keys;
-  const long long once =
-      (all + KV_ROWS - 1) / KV_ROWS * at_cost(at_width(all)) * (long long)(keys + KV_EXTRA);
+  const long long tiles = n * ((rows + KV_ROWS - 1) / KV_ROWS);
+  const long long alone = tiles * at_cost(at_width(rows)) * keys;
+  const int cost = at_large(A, all) ? AT_LARGE_COST : at_cost(at_width(all));
+  const long long once = (all + KV_ROWS - 1) / KV_ROWS * cost * (long long)(keys + KV_EXTRA) + tiles * 8000 + 200 * all;
   return alone > once ? keys : 0;
 }
 __device__ __forceinline__ int at_skip(const AttendArgs&, int) { return 0; }
@@ -324,8 +336,8 @@ __device__ __forceinline__ AtQuery at_query(const Args& A, int b, int i) {
 // each has at most one that is not full.)
 __device__ __forceinline__ int at_tile_no(const AttendArgs&, AtMode, int, int, int) { return 0; }
 __device__ __forceinline__ int at_tile_no(const SharedArgs& A, AtMode m, int b, int rt, int h) {
-  const int base = m == AT_OWN ? b * A.tiles
-                               : static_cast<int>((long long)kv_ld(A.H.group + b).x * A.T * A.group / KV_ROWS) + b;
+  const long long first = m == AT_OWN ? 0 : (long long)kv_ld(A.H.group + b).x * A.T * A.group;
+  const int base = m == AT_OWN ? b * A.tiles : static_cast<int>(first / KV_ROWS) + b;
   return (base + rt) * A.C.heads + h;
 }
 
@@ -688,23 +700,27 @@ static __device__ __noinline__ void at_land(uint64_t* full, int n, int g) {
 }
 
 // The state of a CTA in shared memory.
-template <AtMode M, int W>
-struct AtShared {
+template <AtMode M>
+struct AtCommon {
   uint64_t kfull[AT_MAX_RING], kempty[AT_MAX_RING];
   uint64_t vfull[AT_MAX_RING], vempty[AT_MAX_RING], tinfo[AT_INFO];
   uint64_t sfull[3], pfull[3], pvdone[3], vchk[AT_MAX_RING], qfull, dfull[2], dempty[2], drain[2];
+  uint64_t wfull[2], wempty[2], hfull[3];  // of sv_kv_group.cu: values in 16 bits, weights
   uint32_t tmem;
   int abort;
   AtWalk<M> walk;
-  int total, sum[AT_THREADS / 32];
+  int total, sum[32];  // (of up to 32 warps)
   uint32_t rows[AT_LIVE];  // rows that have queries, a bit each
   // Per key tile and page of it: row of the pool (-1: none); key scale, log2 and inverse of
   // the value scale.
   int y[AT_INFO][8];
   float4 sc[AT_INFO][8];
-  // Item k's description and rows, at k & 1: factor of the score, position of the query,
-  // block nodes it sees (trees), its row of the output.
-  AtItem item[2];
+  AtItem item[2];  // item k's description, at k & 1
+};
+template <AtMode M, int W>
+struct AtShared : AtCommon<M> {
+  // Item k's rows, at k & 1: factor of the score, position of the query, block nodes it sees
+  // (trees), its row of the output.
   float c[2][W];
   int pos[2][W];
   unsigned long long see[2][W];
@@ -719,7 +735,7 @@ struct AtShared {
 };
 
 // Barriers and tensor memory, before anything of the call is read.
-template <typename Shared>
+template <int WARPS = AT_SM_WARPS, typename Shared>
 __device__ __forceinline__ void at_setup(Shared& sh) {
   const int tid = threadIdx.x;
   if (tid < AT_INFO) {
@@ -735,14 +751,17 @@ __device__ __forceinline__ void at_setup(Shared& sh) {
       mbar_init(&sh.sfull[tid], 2);
       mbar_init(&sh.pfull[tid], AT_SM_WARPS);
       mbar_init(&sh.pvdone[tid], 1);
+      mbar_init(&sh.hfull[tid], GR_WEIGHTS);
     }
     if (tid < 2) {
       mbar_init(&sh.dfull[tid], 1);
-      mbar_init(&sh.dempty[tid], AT_SM_WARPS);
+      mbar_init(&sh.dempty[tid], WARPS);
       mbar_init(&sh.drain[tid], 1);
+      mbar_init(&sh.wfull[tid], GR_CONVERT);
+      mbar_init(&sh.wempty[tid], 1);
     }
     if (tid == 0) {
-      mbar_init(&sh.qfull, AT_SM_WARPS);
+      mbar_init(&sh.qfull, WARPS);
       *const_cast<volatile int*>(&sh.abort) = 0;
     }
     fence_mbar_init();
@@ -757,6 +776,7 @@ __device__ __forceinline__ void at_setup(Shared& sh) {
 }
 
 // Sum of x over the CTA's threads; *before: of lower threads.
+template <int THREADS = AT_THREADS>
 __device__ __forceinline__ int at_block_sum(int x, int* sums, int* before) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   int v = x;
@@ -765,10 +785,11 @@ __device__ __forceinline__ int at_block_sum(int x, int* sums, int* before) {
     const int t = __shfl_up_sync(0xffffffffu, v, d);
     if (lane >= d) v += t;
   }
+  static_assert(THREADS <= 1024, "an entry a warp");
   if (lane == 31) sums[w] = v;
   __syncthreads();
   int all = 0, pre = 0;
-  for (int i = 0; i < AT_THREADS / 32; ++i) {
+  for (int i = 0; i < THREADS / 32; ++i) {
     if (i < w) pre += sums[i];
     all += sums[i];
   }
@@ -787,13 +808,13 @@ __device__ __forceinline__ int at_units_of(const Args& A, int p, int nrt, int pa
   const int b = nrt == 1 ? p : p / nrt;
   return at_units<M>(A, b, p - b * nrt) * A.C.heads;
 }
-template <AtMode M, typename Args>
+template <AtMode M, int THREADS = AT_THREADS, typename Args>
 __device__ __forceinline__ AtCount at_count(const Args& A, uint32_t* rows) {
   const int tid = threadIdx.x, lane = tid & 31, nrt = at_most_tiles<M>(A), n = at_rows<M>(A);
   const int pairs = n * nrt;
   AtCount a = {0, 0};
 #pragma unroll 1
-  for (int p = tid; p - lane < pairs; p += AT_THREADS) {
+  for (int p = tid; p - lane < pairs; p += THREADS) {
     const int c = at_units_of<M>(A, p, nrt, pairs);
     if (p == tid) a.mine = c;
     a.sum += c;
@@ -804,7 +825,7 @@ __device__ __forceinline__ AtCount at_count(const Args& A, uint32_t* rows) {
   }
   if (nrt > 1)
 #pragma unroll 1
-    for (int b = tid; b - lane < n; b += AT_THREADS) {
+    for (int b = tid; b - lane < n; b += THREADS) {
       const uint32_t has = __ballot_sync(0xffffffffu, b < n && at_row<M>(A, b).rows > 0);
       if (lane == 0) rows[b / 32] = has;
     }
@@ -834,6 +855,160 @@ static __device__ __noinline__ void at_check_groups(const SharedArgs& A, int war
       kv_report(A.S.hdr, ST_DEVICE_INPUT);
     }
   }
+}
+
+// This CTA's share: the units of all rows' query tiles, cut into equal parts. The second pass over
+// them finds the one where the share begins. The CTA's warps go on together.
+template <AtMode M, int THREADS = AT_THREADS, typename Args, typename Shared>
+__device__ __forceinline__ void at_begin(const Args& A, Shared& sh, AtCount count, int total, int before,
+                                         int cta, int most_ctas) {
+  const int tid = threadIdx.x;
+  const int nrt = at_most_tiles<M>(A), pairs = at_rows<M>(A) * nrt;
+  const int ctas = min(most_ctas, total);
+  const int from = cta < ctas ? at_share(cta, total, ctas) : 0;
+  const int to = cta < ctas ? at_share(cta + 1, total, ctas) : 0;
+  if (tid == 0) {
+    sh.total = total;
+    if (from >= to) sh.walk.at = sh.walk.end = 0;
+  }
+  if (from < to) {
+    int base = 0;
+#pragma unroll 1
+    for (int p0 = 0;; p0 += THREADS) {
+      const int c = p0 == 0 ? count.mine : at_units_of<M>(A, p0 + tid, nrt, pairs);
+      int all = total;
+      if (pairs > THREADS) {  // (otherwise `before` is right already)
+        __syncthreads();
+        all = at_block_sum<THREADS>(c, sh.sum, &before);
+      }
+      if (from >= base + before && from < base + before + c) {
+        // (One thread for all: its row's data and this code are at hand, which saves the
+        // copies 3,000 cycles before their first page.)
+        const int b = (p0 + tid) / nrt;
+        AtWalk<M> walk;
+        walk.start(A, b, p0 + tid - b * nrt, from - base - before, from, to);
+        sh.walk = walk;
+      }
+      base += all;
+      if (base > from) break;
+    }
+  }
+  tm_fence_before();
+  __syncthreads();
+  tm_fence_after();
+}
+
+__device__ __forceinline__ void at_prefetch(const CUtensorMap* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y)
+               : "memory");
+}
+
+// The warp that copies K tiles into their ring (of nk); returns how many it has issued. With tmV the
+// pages of the chunk ahead, of K and V, are brought to L2 meanwhile.
+template <AtMode M, int NDB, typename Args, typename Shared>
+__device__ __forceinline__ int at_copy_keys(const Args& A, int nk, const CUtensorMap& tmK, Shared& sh,
+                                            const uint32_t* s_rows, unsigned char* Ks,
+                                            const CUtensorMap* tmV = nullptr) {
+  constexpr int ndb = NDB, slot = ndb * AT_BLK;
+  const KvCache& C = A.C;
+  const int lane = threadIdx.x & 31;
+  auto &kfull = sh.kfull, &kempty = sh.kempty;
+  auto& tinfo = sh.tinfo;
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return mbar_try(bar, parity) || at_wait_on(bar, parity, const_cast<volatile int*>(&sh.abort), A);
+  };
+  // Pages are looked up for several tiles at a time, a page per lane and a
+  // chunk ahead of their use; their data go to the other warps through a ring of entries,
+  // one per tile, written before the tile's barrier is armed. (An entry is used again 32
+  // tiles later, and K is never more than its ring and three steps ahead of the rest.)
+  fence_async_global();  // (what earlier kernels stored, before copies read it)
+  AtWalk<M> walk = sh.walk;
+  walk.first(A, s_rows);
+  const int ppt = AT_KEYS >> C.lgp;             // pages per tile
+  const int tpc = min(32 / ppt, AT_INFO / 4);   // tiles per chunk
+  const int mt = lane / ppt, sub = lane - mt * ppt;
+  const size_t layer0 = (size_t)A.layer * C.pages;
+  int n = 0, h = 0, page = -1;  // the chunk ahead: tiles, head, this lane's page
+  bool used = false;
+  int i = walk.live() ? walk.i0 : 0;
+  auto look = [&]() {
+    n = 0;
+    if (!walk.live()) return;
+    h = walk.h;
+    n = min(tpc, walk.i1 - i);
+    const int key = (mt < n ? walk.tile.key_tile(i + mt) : 0) * AT_KEYS + (sub << C.lgp);
+    used = mt < n && key < walk.tile.end;
+    page = used ? kv_page(C, walk.row.lead, key) : -1;
+    if (tmV && page >= 0)
+      for (int db = 0; db < ndb; ++db) {
+        at_prefetch(&tmK, db * 128, (page * C.heads + h) << C.lgp);
+        at_prefetch(tmV, db * 128, (page * C.heads + h) << C.lgp);
+      }
+    i += n;
+    if (i == walk.i1) {
+      walk.next(A, s_rows);
+      i = walk.live() ? walk.i0 : 0;
+    }
+  };
+  int g = 0, q = 0, ph = 0;
+  bool ok = true;
+  look();
+  while (ok && n) {
+    const int count = n, head = h;
+    const bool use = used;
+    const int pg = page, y = pg >= 0 ? (pg * C.heads + head) << C.lgp : -1;
+    const uint32_t held = __ballot_sync(0xffffffffu, y >= 0);
+    for (int t = 0; t < count; ++t) {
+      if (ph > 0 && !__all_sync(0xffffffffu, wait(&kempty[q], (ph - 1) & 1))) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) {
+        const uint32_t pages = __popc((held >> (t * ppt)) & ((1u << ppt) - 1u));
+        mbar_arrive_expect_tx(&kfull[q], (pages << C.lgp) * 128u * ndb);
+      }
+      __syncwarp();
+      if (mt == t && y >= 0) {
+        unsigned char* dst = Ks + (size_t)q * slot + ((size_t)sub << C.lgp) * 128;
+        for (int db = 0; db < ndb; ++db) at_tma(dst + db * AT_BLK, &tmK, db * 128, y, &kfull[q]);
+      }
+      if (t == 0) {  // the chunk's data, while its first tile is on its way
+        float ks = 1.f, vs = 1.f;
+        if (use) {
+          if (pg >= 0) {
+            ks = kv_ld(C.ks + (layer0 + pg) * C.heads + head);
+            vs = kv_ld(C.vs + (layer0 + pg) * C.heads + head);
+          }
+          // A page out of range, or scales outside theirs: the scores become NaN.
+          constexpr float LO = 5.421010862427522e-20f, HI = 18446744073709551616.f;  // 2^-64, 2^64
+          if (pg < 0 || !(ks >= LO && ks <= HI && vs >= LO && vs <= HI)) {
+            ks = NAN;
+            vs = 1.f;
+            kv_report(A.S.hdr, ST_DEVICE_INPUT);
+          }
+        }
+        if (mt < count) {
+          const int e = (g + mt) & (AT_INFO - 1);
+          sh.y[e][sub] = y;
+          sh.sc[e][sub] = make_float4(ks, log2f(vs), 1.f / vs, 0.f);
+        }
+        __syncwarp();
+      }
+      if (lane == 0) {  // (the second of kfull's arrivals: the tile's data are there)
+        mbar_arrive(&kfull[q]);
+        mbar_arrive(&tinfo[g & (AT_INFO - 1)]);
+      }
+      ++g;
+      if (++q == nk) {
+        q = 0;
+        ++ph;
+      }
+      if (t == 0) look();
+    }
+  }
+  return g;
 }
 
 // Where a mode's partial results are, and the rows of a slot.
@@ -914,130 +1089,12 @@ __device__ __forceinline__ void at_body(const Args& A, const AttendPlan& P, cons
     return mbar_try(bar, parity) || at_wait_on(bar, parity, &s_abort, A);
   };
 
-  // This CTA's share: the units of all rows' query tiles, cut into equal parts. The second pass
-  // over them finds the one where the share begins.
-  const int nrt = at_most_tiles<M>(A), pairs = at_rows<M>(A) * nrt;
-  const int ctas = min(most_ctas, total);
-  const int from = cta < ctas ? at_share(cta, total, ctas) : 0;
-  const int to = cta < ctas ? at_share(cta + 1, total, ctas) : 0;
-  if (tid == 0) {
-    sh.total = total;
-    if (from >= to) s_walk.at = s_walk.end = 0;
-  }
-  if (from < to) {
-    int base = 0;
-#pragma unroll 1
-    for (int p0 = 0;; p0 += AT_THREADS) {
-      const int c = p0 == 0 ? count.mine : at_units_of<M>(A, p0 + tid, nrt, pairs);
-      int all = total;
-      if (pairs > AT_THREADS) {  // (otherwise `before` is right already)
-        __syncthreads();
-        all = at_block_sum(c, sh.sum, &before);
-      }
-      if (from >= base + before && from < base + before + c) {
-        // (One thread for all: its row's data and this code are at hand, which saves the
-        // copies 3,000 cycles before their first page.)
-        const int b = (p0 + tid) / nrt;
-        AtWalk<M> walk;
-        walk.start(A, b, p0 + tid - b * nrt, from - base - before, from, to);
-        s_walk = walk;
-      }
-      base += all;
-      if (base > from) break;
-    }
-  }
-  tm_fence_before();
-  __syncthreads();
-  tm_fence_after();
+  at_begin<M>(A, sh, count, total, before, cta, most_ctas);
   const uint32_t tmem = sh.tmem;
 
   int copied = 0;  // tiles whose copies this warp has issued
   if (w == 0) {
-    // ---- K copies. Pages are looked up for several tiles at a time, a page per lane and a
-    // chunk ahead of their use; their data go to the other warps through a ring of entries,
-    // one per tile, written before the tile's barrier is armed. (An entry is used again 32
-    // tiles later, and K is never more than its ring and three steps ahead of the rest.)
-    fence_async_global();  // (what earlier kernels stored, before copies read it)
-    AtWalk<M> walk = s_walk;
-    walk.first(A, s_rows);
-    const int ppt = AT_KEYS >> C.lgp;             // pages per tile
-    const int tpc = min(32 / ppt, AT_INFO / 4);   // tiles per chunk
-    const int mt = lane / ppt, sub = lane - mt * ppt;
-    const size_t layer0 = (size_t)A.layer * C.pages;
-    int n = 0, h = 0, page = -1;  // the chunk ahead: tiles, head, this lane's page
-    bool used = false;
-    int i = walk.live() ? walk.i0 : 0;
-    auto look = [&]() {
-      n = 0;
-      if (!walk.live()) return;
-      h = walk.h;
-      n = min(tpc, walk.i1 - i);
-      const int key = (mt < n ? walk.tile.key_tile(i + mt) : 0) * AT_KEYS + (sub << C.lgp);
-      used = mt < n && key < walk.tile.end;
-      page = used ? kv_page(C, walk.row.lead, key) : -1;
-      i += n;
-      if (i == walk.i1) {
-        walk.next(A, s_rows);
-        i = walk.live() ? walk.i0 : 0;
-      }
-    };
-    int g = 0, q = 0, ph = 0;
-    bool ok = true;
-    look();
-    while (ok && n) {
-      const int count = n, head = h;
-      const bool use = used;
-      const int pg = page, y = pg >= 0 ? (pg * C.heads + head) << C.lgp : -1;
-      const uint32_t held = __ballot_sync(0xffffffffu, y >= 0);
-      for (int t = 0; t < count; ++t) {
-        if (ph > 0 && !__all_sync(0xffffffffu, wait(&kempty[q], (ph - 1) & 1))) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) {
-          const uint32_t pages = __popc((held >> (t * ppt)) & ((1u << ppt) - 1u));
-          mbar_arrive_expect_tx(&kfull[q], (pages << C.lgp) * 128u * ndb);
-        }
-        __syncwarp();
-        if (mt == t && y >= 0) {
-          unsigned char* dst = Ks + (size_t)q * slot + ((size_t)sub << C.lgp) * 128;
-          for (int db = 0; db < ndb; ++db) at_tma(dst + db * AT_BLK, &tmK, db * 128, y, &kfull[q]);
-        }
-        if (t == 0) {  // the chunk's data, while its first tile is on its way
-          float ks = 1.f, vs = 1.f;
-          if (use) {
-            if (pg >= 0) {
-              ks = kv_ld(C.ks + (layer0 + pg) * C.heads + head);
-              vs = kv_ld(C.vs + (layer0 + pg) * C.heads + head);
-            }
-            // A page out of range, or scales outside theirs: the scores become NaN.
-            constexpr float LO = 5.421010862427522e-20f, HI = 18446744073709551616.f;  // 2^-64, 2^64
-            if (pg < 0 || !(ks >= LO && ks <= HI && vs >= LO && vs <= HI)) {
-              ks = NAN;
-              vs = 1.f;
-              kv_report(A.S.hdr, ST_DEVICE_INPUT);
-            }
-          }
-          if (mt < count) {
-            const int e = (g + mt) & (AT_INFO - 1);
-            s_y[e][sub] = y;
-            s_sc[e][sub] = make_float4(ks, log2f(vs), 1.f / vs, 0.f);
-          }
-          __syncwarp();
-        }
-        if (lane == 0) {  // (the second of kfull's arrivals: the tile's data are there)
-          mbar_arrive(&kfull[q]);
-          mbar_arrive(&tinfo[g & (AT_INFO - 1)]);
-        }
-        ++g;
-        if (++q == P.nk) {
-          q = 0;
-          ++ph;
-        }
-        if (t == 0) look();
-      }
-    }
-    copied = g;
+    copied = at_copy_keys<M, NDB>(A, P.nk, tmK, sh, s_rows, Ks);
   } else if (w == 1) {
     // ---- Scores of a tile.
     if (at_elect()) {
@@ -1686,6 +1743,8 @@ struct AttendLaunch {
   int ndb, width, grid;
   size_t smem;
 };
+cudaError_t launch_kv_attend_group(const SharedArgs& A, const AttendLaunch& L, sv_dtype dt, int dev,
+                                  cudaStream_t st);
 cudaError_t at_launch(const AttendArgs& A, sv_dtype dt, int width, int dev, AttendLaunch* L);
 
 }  // namespace sv

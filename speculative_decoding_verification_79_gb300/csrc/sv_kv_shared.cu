@@ -152,80 +152,96 @@ __device__ __forceinline__ KvSpan join_span(const KvSpan* p) {
   const KvSpan s = kv_ld(p);
   return KvSpan{min(max(s.first, 0), KV_MAX_CTAS - 1), min(s.last, KV_MAX_CTAS - 1)};
 }
+
+// A warp: eight query rows of a query tile and head, their parts' sums first, then four lanes a row
+// take its vectors in turn, eight of them in flight. (Rows next to each other: whole sectors.)
 __global__ void __launch_bounds__(SJ_THREADS)
     kv_shared_join_kernel(const __grid_constant__ SharedArgs A, int bf16) {
   kv_enter();
-  const int heads = A.C.heads, vec = A.C.dim / 4;
-  const long long items = (long long)A.C.batch * A.tiles * heads;
-  for (long long item = blockIdx.x; item < items; item += gridDim.x) {
-    const int h = static_cast<int>(item % heads), bt = static_cast<int>(item / heads);
-    const int b = bt / A.tiles, rt = bt - b * A.tiles;
-    const AtRow row = at_row<AT_OWN>(A, b);
-    if (rt >= row.nrt) continue;
-    const int no = at_tile_no(A, AT_OWN, b, rt, h);
-    const KvSpan own = join_span(A.own_span + no);
-    if (!row.skip && own.first == own.last) continue;
-    const int r0 = rt * row.rr, R = min(r0 + row.rr, row.rows) - r0;
-    const bool bad = kv_ld(A.H.bad + b) != 0;
+  const int vec = A.C.dim / 4, eights = A.own_rows / 8, heads = A.C.heads, lane = threadIdx.x & 31;
+  const long long item = (long long)blockIdx.x * (SJ_THREADS / 32) + threadIdx.x / 32;
+  const int chunk = static_cast<int>(item % eights);
+  const long long tile = item / eights;
+  const int h = static_cast<int>(tile % heads), bt = static_cast<int>(tile / heads);
+  const int b = bt / A.tiles, rt = bt - b * A.tiles;
+  if (b >= A.C.batch) return;
+  const AtRow row = at_row<AT_OWN>(A, b);
+  const int r0 = rt * row.rr, r = 8 * chunk + (lane & 7), R = min(r0 + row.rr, row.rows) - r0;
+  if (rt >= row.nrt || 8 * chunk >= R) return;
+  const int no = at_tile_no(A, AT_OWN, b, rt, h);
+  const KvSpan own = join_span(A.own_span + no);
+  if (!row.skip && own.first == own.last) return;
+  if (r >= R) return;
+  // The group's part of the query: row gr of `count` slots from id on.
+  int id = 0, gr = 0, count = 0;
+  if (row.skip) {
     const int4 mine = kv_ld(A.H.row + b);
-    const AtRow group = row.skip ? at_row<AT_GROUPS>(A, mine.x) : row;
-    const int n = (R + 7) / 8 * 8 * vec;
-    for (int e = threadIdx.x; e < n; e += SJ_THREADS) {
-      const int r = e / (8 * vec) * 8 + e % 8, dv = e / 8 % vec;
-      if (r >= R) continue;
-      const int t = (r0 + r) / A.group, gh = r0 + r - t * A.group;
-      float ref = -INFINITY, sum = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      auto add = [&](const float2* stats, const float* part, int no, KvSpan span, int r, int rows) {
-        constexpr int K = 4;  // loads in flight
-        for (int c0 = span.first; c0 <= span.last; c0 += K) {
-          float2 s2[K];
-          float4 y[K];
-#pragma unroll
-          for (int k = 0; k < K; ++k) {
-            const int id = no + min(c0 + k, span.last);
-            s2[k] = __ldcg(stats + (size_t)id * rows + r);
-            y[k] = __ldcg(reinterpret_cast<const float4*>(part) + at_part(id, r, 4 * dv, A.C.dim, rows));
-          }
-          float top = ref;
-#pragma unroll
-          for (int k = 0; k < K; ++k)
-            if (s2[k].y != 0.f) top = fmaxf(top, s2[k].x);
-          const float f0 = sum == 0.f ? 0.f : exp2f(ref - top);
-          ref = top;
-          sum *= f0;
-          o.x *= f0;
-          o.y *= f0;
-          o.z *= f0;
-          o.w *= f0;
-#pragma unroll
-          for (int k = 0; k < K; ++k) {
-            if (s2[k].y == 0.f || c0 + k > span.last) continue;
-            const float f = exp2f(s2[k].x - top);
-            sum = fmaf(s2[k].y, f, sum);
-            o.x = fmaf(y[k].x, f, o.x);
-            o.y = fmaf(y[k].y, f, o.y);
-            o.z = fmaf(y[k].z, f, o.z);
-            o.w = fmaf(y[k].w, f, o.w);
-          }
-        }
-      };
-      if (row.skip) {
-        const int i = (mine.w * A.T + t) * A.group + gh, grt = i / group.rr;
-        if (!A.window || at_tile<AT_GROUPS>(A, group, mine.x, grt).tiles() > 0) {
-          const int gno = at_tile_no(A, AT_GROUPS, mine.x, grt, h);
-          add(A.stat, A.part, gno, join_span(A.span + gno), i - grt * group.rr, KV_ROWS);
-        }
-      }
-      add(A.own_stat, A.own_part, no, own, r, A.own_rows);
-      float inv = sum == 0.f ? 0.f : 1.f / sum;
-      if (bad) inv = sum = NAN;
-      const long long out = ((long long)b * A.T + t) * A.q_heads + h * A.group + gh;
-      at_store4(A.out, out * A.C.dim + dv * 4,
-                make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv), bf16);
-      if (dv == 0 && A.lse)
-        A.lse[out] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+    const AtRow group = at_row<AT_GROUPS>(A, mine.x);
+    const int i = mine.w * A.T * A.group + r0 + r, grt = i / group.rr;
+    gr = i - grt * group.rr;
+    if (!A.window || at_tile<AT_GROUPS>(A, group, mine.x, grt).tiles() > 0) {
+      id = at_tile_no(A, AT_GROUPS, mine.x, grt, h);
+      const KvSpan span = join_span(A.span + id);
+      count = span.last - span.first + 1;
+      id += span.first;
     }
+  }
+  const int slots = count + own.last - own.first + 1;
+  auto slot = [&](int k, const float2** stat, const float4** part, int* rows) {
+    const bool mine = k >= count;
+    const int at = mine ? no + own.first + k - count : id + k, rr = mine ? r : gr;
+    *rows = mine ? A.own_rows : KV_ROWS;
+    *stat = (mine ? A.own_stat : A.stat) + (size_t)at * *rows + rr;
+    *part = reinterpret_cast<const float4*>(mine ? A.own_part : A.part) + at_part(at, rr, 0, A.C.dim, *rows);
+  };
+  float ref = -INFINITY, sum = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < slots; ++k) {
+    const float2* stat;
+    const float4* part;
+    int rows;
+    slot(k, &stat, &part, &rows);
+    const float2 x = __ldcg(stat);
+    if (x.y == 0.f) continue;
+    const float top = fmaxf(ref, x.x);
+    sum = fmaf(x.y, exp2f(x.x - top), sum == 0.f ? 0.f : sum * exp2f(ref - top));
+    ref = top;
+  }
+  float inv = sum == 0.f ? 0.f : 1.f / sum;
+  if (kv_ld(A.H.bad + b)) inv = sum = NAN;
+  const int i = r0 + r, t = i / A.group, gh = i - t * A.group;
+  const long long out = ((long long)b * A.T + t) * A.q_heads + h * A.group + gh;
+  if (lane < 8 && A.lse) A.lse[out] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+  constexpr int U = 8;
+  for (int v0 = lane >> 3; v0 < vec; v0 += 4 * U) {
+    float4 o[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int k = 0; k < slots; ++k) {
+      const float2* stat;
+      const float4* part;
+      int rows;
+      slot(k, &stat, &part, &rows);
+      const float2 x = __ldcg(stat);
+      float4 y[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) y[u] = __ldcg(part + (size_t)min(v0 + 4 * u, vec - 1) * rows);
+      const float f = exp2f(x.x - ref);
+      if (x.y == 0.f) continue;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        o[u].x = fmaf(y[u].x, f, o[u].x);
+        o[u].y = fmaf(y[u].y, f, o[u].y);
+        o[u].z = fmaf(y[u].z, f, o[u].z);
+        o[u].w = fmaf(y[u].w, f, o[u].w);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (v0 + 4 * u < vec)
+        at_store4(A.out, out * A.C.dim + (v0 + 4 * u) * 4,
+                  make_float4(o[u].x * inv, o[u].y * inv, o[u].z * inv, o[u].w * inv), bf16);
   }
 }
 
@@ -286,12 +302,17 @@ cudaError_t launch_kv_attend_shared(const SharedArgs& A, sv_dtype dt, cudaStream
   if (e != cudaSuccess) return e;
   AttendLaunch L;
   if ((e = at_launch(A, dt, at_width((long long)A.T * A.group), dev, &L)) != cudaSuccess) return e;
+  // (No group has more rows than the batch.)
+  if (A.large && at_width((long long)A.C.batch * A.T * A.group) == 128 &&
+      (e = launch_kv_attend_group(A, L, dt, dev, st)) != cudaSuccess)
+    return e;
   const SharedKernel kernel = kernels[dt == SV_BF16][L.ndb - 1][L.width == 32 ? 0 : (L.width == 64 ? 1 : 2)];
   if ((e = kv_launch(kernel, dim3(L.grid), AT_THREADS, L.smem, st, A, L.P, L.tm[0], L.tm[1])) != cudaSuccess)
     return e;
-  const long long items = (long long)A.C.batch * A.tiles * A.C.heads, most = 8LL * L.grid;
-  return kv_launch(kv_shared_join_kernel, dim3(static_cast<unsigned>(items < most ? items : most)), SJ_THREADS,
-                   0, st, A, dt == SV_BF16 ? 1 : 0);
+  const long long eights = (long long)A.C.batch * A.tiles * A.C.heads * (A.own_rows / 8);
+  const long long blocks = (eights + SJ_THREADS / 32 - 1) / (SJ_THREADS / 32);
+  return kv_launch(kv_shared_join_kernel, dim3(static_cast<unsigned>(blocks)), SJ_THREADS, 0, st, A,
+                   dt == SV_BF16 ? 1 : 0);
 }
 
 }  // namespace sv

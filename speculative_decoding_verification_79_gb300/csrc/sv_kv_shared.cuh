@@ -9,13 +9,12 @@
 // tile was cut between CTAs.
 //
 // Both parts are in one launch: the CTAs are divided between them by their work, counted in key
-// tiles of their width. A CTA runs one of the two.
+// tiles of their width. A CTA runs one of the two. Large groups are attended to by a launch before
+// (sv_kv_group.cu).
 #pragma once
 #include "sv_kv_attend.cuh"
 
 namespace sv {
-
-constexpr size_t at_larger(size_t a, size_t b) { return a > b ? a : b; }
 
 template <int W, bool BF16, int NDB>
 __global__ void __launch_bounds__(AT_THREADS, 1)
@@ -23,34 +22,37 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
                             const __grid_constant__ CUtensorMap tmK,
                             const __grid_constant__ CUtensorMap tmV) {
   extern __shared__ unsigned char dsm_raw[];
+  // (Barriers and the like are at the same place for both parts.)
   __shared__ alignas(16) unsigned char raw[sizeof(AtShared<AT_OWN, 128>)];
   __shared__ uint32_t s_groups[AT_LIVE];
   __shared__ int s_sum[AT_THREADS / 32];
   auto& sh = reinterpret_cast<AtShared<AT_OWN, W>&>(raw);
   at_setup(sh);
   kv_enter();
-  const AtCount own = at_count<AT_OWN>(A, sh.rows), common = at_count<AT_GROUPS>(A, s_groups);
+  const long long most = (long long)kv_ld(A.H.head + 1) * A.T * A.group;  // queries of the largest group
+  const int rows = at_width(most), grid = gridDim.x;
+  const AtCount own = at_count<AT_OWN>(A, sh.rows);
+  AtCount common = {0, 0};
+  if (!at_large(A, most)) common = at_count<AT_GROUPS>(A, s_groups);
   int own_before, before;
   const int own_total = at_block_sum(own.sum, sh.sum, &own_before);
   const int total = at_block_sum(common.sum, s_sum, &before);
-  const int rows = at_width((long long)kv_ld(A.H.head + 1) * A.T * A.group), grid = gridDim.x;
   const float a = static_cast<float>(total) * at_cost(rows), b = static_cast<float>(own_total) * at_cost(W);
   const int ctas = total ? max(1, min(grid - 1, __float2int_rn(grid * (a / (a + b))))) : 0;
   const int cta = blockIdx.x;
   __syncthreads();  // (the sums are read; their place is used again)
-  if (cta >= ctas) {
+  if (cta >= ctas)
     at_body<AT_OWN, W, BF16, NDB>(A, P, tmK, tmV, sh, sh.rows, dsm_raw, own, own_total, own_before,
                                   cta - ctas, grid - ctas);
-  } else if (W == 32 && rows == 32) {
+  else if (W == 32 && rows == 32)
     at_body<AT_GROUPS, 32, BF16, NDB>(A, P, tmK, tmV, reinterpret_cast<AtShared<AT_GROUPS, 32>&>(raw),
                                       s_groups, dsm_raw, common, total, before, cta, ctas);
-  } else if (W == 32 && rows == 64) {
+  else if (W == 32 && rows == 64)
     at_body<AT_GROUPS, 64, BF16, NDB>(A, P, tmK, tmV, reinterpret_cast<AtShared<AT_GROUPS, 64>&>(raw),
                                       s_groups, dsm_raw, common, total, before, cta, ctas);
-  } else {
+  else
     at_body<AT_GROUPS, 128, BF16, NDB>(A, P, tmK, tmV, reinterpret_cast<AtShared<AT_GROUPS, 128>&>(raw),
                                        s_groups, dsm_raw, common, total, before, cta, ctas);
-  }
 }
 
 typedef void (*SharedKernel)(const SharedArgs, const AttendPlan, const CUtensorMap, const CUtensorMap);

@@ -23,6 +23,16 @@ def sv():
     return m
 
 
+@pytest.fixture(autouse=True, params=[True, False], ids=["always", "rule"])
+def always(request, sv):
+    """Every group's common tokens read once, and only where the library finds that faster."""
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    prev = sv.set_share_always(request.param)
+    yield request.param
+    sv.set_share_always(prev)
+
+
 def rows_of(groups, alone):
     """Rows of groups and lone rows, dealt out so that a group's rows are not neighbours: leader
     of each row."""
@@ -219,9 +229,11 @@ def test_smaller_calls_on_a_buffer(sv):
 @needs_cuda
 @pytest.mark.parametrize("what", ["table", "len", "n_pages", "count", "count_high", "tree", "own_page",
                                   "scale"])
-def test_rows_with_wrong_data(sv, what):
+def test_rows_with_wrong_data(sv, what, always):
     """A row that no longer holds what its group shares, or has other wrong data, is NaN; the
     others are right, and so is the row when the groups are found again."""
+    if not always:
+        pytest.skip("rows may be attended to by themselves")
     T = 6
     both, q, n, par, share, kw, want = case(sv, [(6, 2000), (3, 400)], [90], [20, 60], T, 2, 4, 64, 16,
                                             trees=True, seed=8, n=[6] * 10)
