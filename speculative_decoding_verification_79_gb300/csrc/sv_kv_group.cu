@@ -263,10 +263,11 @@ __global__ void __launch_bounds__(GR_THREADS, 1)
   kv_enter();
   // (Before anything is set up: there may be no group that is large enough.)
   if (!at_large(A, (long long)kv_ld(A.H.head + 1) * A.T * A.group)) return;
-  at_setup<GR_WARPS>(sh);
   const AtCount count = at_count<AT_GROUPS, GR_THREADS>(A, sh.rows);
   int before;
   const int total = at_block_sum<GR_THREADS>(count.sum, sh.sum, &before);
+  if (total == 0) return;
+  at_setup<GR_WARPS>(sh);
   const int cta = blockIdx.x, most_ctas = gridDim.x;
   const uint32_t* const s_rows = sh.rows;
   at_begin<AT_GROUPS, GR_THREADS>(A, sh, count, total, before, cta, most_ctas);

@@ -3,16 +3,29 @@
 //
 // A block takes the keys (or the values) of one page of one row, head after head: loads a head's
 // new tokens, rotates them in float32, reduces the largest |x| over the block for the page's scale
-// and rounds once, to e4m3. A thread has the same pairs of the same tokens in every head, so that
+// and rounds once, to e4m3. A thread has the same pairs of the same token in every head, so that
 // their cosines and sines stay in its registers, and the next head's loads are under way while a
 // head's largest value is found. Blocks behind those of keys and values rotate the queries
-// (rope_row). Bound by memory.
+// (rope_row). Bound by memory: 8 prompts of 4,093 tokens with 8 heads and 32 query heads of 128
+// take 140 us, 0.95 GB at 6.8 TB/s (sv_kv_append and sv_rope one after the other: 123 us, without
+// the rotation of the keys). A few tokens of many rows take the trips to memory one after the other
+// (lengths, table, counts of holders, old scale, beside the tokens themselves): 64 rows 5.5 us for
+// a token, 10.8 us for trees of 16.
+//
+// What decides is that the loop over heads has no call in it and fits 64 registers, so that an SM
+// holds 1,024 threads: with calls for the rare cases inside it (another quantiser's scale, the
+// rescaling of older tokens, divisions) it spilt on every head, and those prompts took 232 us. So
+// the loop leaves a page's rare cases to append_rest, behind it.
 #include "sv_rope.cuh"
 
 namespace sv {
 
-constexpr int AR_THREADS = 256;
-constexpr int AR_VALUES = 32;  // of a page and head that a thread keeps in registers
+// Threads of a block: one for 16 values of the new tokens of a page, in whole warps, as far as that
+// goes. (The queries in a launch of their own: those prompts 149 us, trees 15.2. Twice or four
+// times as many blocks, of fewer heads each: 153 and 167 us, the cosines being computed again.)
+constexpr int AR_LEAST = 128, AR_MOST = 1024;
+constexpr int AR_VALUES = 16;  // of a page and head that a thread keeps in registers
+constexpr int AR_PER = 32;     // heads of a block
 
 template <int P>
 __device__ __forceinline__ void put_e4m3(uint8_t* p, const float* f, float inv) {
@@ -61,19 +74,89 @@ __device__ __forceinline__ int load_unit(const AppendRopeArgs& A, const KvSrc& s
   return t;
 }
 
-// The new values of a head at a scale that is no power of two, which another quantiser gave the
-// page. (On a path of its own, which reads the values again: it leaves the registers to the rest.)
+// The largest |x| that the scales' range holds; `odd` when another one is there.
+template <int P>
+__device__ __forceinline__ float append_seen(const float* x, bool* odd) {
+  float a = 0.f;
+#pragma unroll
+  for (int e = 0; e < 2 * P; ++e) {
+    const float y = fabsf(x[e]);
+    if (y <= KV_XMAX)
+      a = fmaxf(a, y);
+    else
+      *odd = true;
+  }
+  return a;
+}
+
+// The scale of a page and head from the largest |x| of each thread's values (whole block). `mx`:
+// shared memory that no thread reads any more.
+__device__ __forceinline__ float append_scale(float a, float old, float* scale, float* mx) {
+  const int tid = threadIdx.x;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
+  if ((tid & 31) == 0) mx[tid >> 5] = a;
+  __syncthreads();  // (and every thread has read the old scale)
+#pragma unroll 8
+  for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) a = fmaxf(a, mx[w]);
+  const float s = fmaxf(kv_scale(a), old);
+  if (tid == 0) *scale = s;
+  return s;
+}
+
+// Is s a power of two whose reciprocal is a normal number too? (Any other scale is of another
+// quantiser.)
+__device__ __forceinline__ bool append_plain(float s) {
+  const uint32_t u = __float_as_uint(s);
+  return (u & 0x807fffffu) == 0 && u >= 0x00800000u && u <= 0x7e800000u;
+}
+
+// One head of a page, all that the registers' path leaves: the page's older tokens, brought from
+// scale `old` to s; the new tokens when s is no plain power of two; and, in a page whose new tokens
+// exceed the block's registers (`large`), its scale and tokens in two passes over the values.
 template <typename E, int P, bool INTER, bool ROT>
-__device__ __noinline__ void append_any(const AppendRopeArgs& A, const KvSrc& src, const PagePart& g,
-                                        int h, RowPos pos, uint8_t* out, float s) {
-  for (int i = threadIdx.x; i < g.count * g.units; i += AR_THREADS) {
+__device__ __noinline__ void append_rest(const AppendRopeArgs& A, const KvSrc& src, const PagePart& g,
+                                         int h, RowPos pos, int off, uint8_t* dst, float* scale,
+                                         float old, bool large, float* mx) {
+  const int nu = g.count * g.units, step = static_cast<int>(blockDim.x);
+  float s;
+  if (large) {
+    old = off ? kv_ld(scale) : 0.f;
+    float a = 0.f;
+    bool odd = false;
+    for (int i = threadIdx.x; i < nu; i += step) {
+      float x[2 * P];
+      RopeUnit<P, INTER> unit(0, 0);
+      load_unit<E, P, INTER, ROT>(A, src, g, i, h, pos, x, &unit);
+      a = fmaxf(a, append_seen<P>(x, &odd));
+    }
+    if (odd) kv_report(A.S.hdr, ST_DEVICE_INPUT);
+    s = append_scale(a, old, scale, mx);
+  } else {
+    s = kv_ld(scale);
+  }
+  if (off && s != old)
+    for (int i = threadIdx.x; i < off * A.C.dim / 16; i += step) {
+      uint4 x = reinterpret_cast<uint4*>(dst)[i];
+      uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) w[q] = kv_rescale4(w[q], old, s);
+      reinterpret_cast<uint4*>(dst)[i] = x;
+    }
+  if (!large && append_plain(s)) return;
+  dst += (size_t)off * A.C.dim;
+  const bool pow2 = kv_pow2(s);
+  const float inv = pow2 ? 1.f / s : 1.f;
+  for (int i = threadIdx.x; i < nu; i += step) {
     float x[2 * P];
     RopeUnit<P, INTER> unit(0, 0);
     const int t = load_unit<E, P, INTER, ROT>(A, src, g, i, h, pos, x, &unit);
+    if (!pow2) {
 #pragma unroll
-    for (int e = 0; e < 2 * P; ++e) x[e] = kv_quotient(x[e], 1.f, s);
-    put_e4m3<P>(out + (size_t)t * A.C.dim + unit.lo, x, 1.f);
-    put_e4m3<P>(out + (size_t)t * A.C.dim + unit.hi, x + P, 1.f);
+      for (int e = 0; e < 2 * P; ++e) x[e] = kv_quotient(x[e], 1.f, s);
+    }
+    put_e4m3<P>(dst + (size_t)t * A.C.dim + unit.lo, x, inv);
+    put_e4m3<P>(dst + (size_t)t * A.C.dim + unit.hi, x + P, inv);
   }
 }
 
@@ -81,115 +164,112 @@ __device__ __noinline__ void append_any(const AppendRopeArgs& A, const KvSrc& sr
 template <typename E, int P, bool INTER, bool ROT>
 __device__ __forceinline__ void append_page(const AppendRopeArgs& A, const KvSrc& src, uint8_t* pool,
                                             float* scales, int b, int j, int h0, int h1, int len,
-                                            int n, int page, RowPos pos) {
-  __shared__ float s_max[2][AR_THREADS / 32];
+                                            int n, RowPos pos) {
+  __shared__ float s_max[2][32], s_old[AR_PER];
   const KvCache& C = A.C;
   const int tid = threadIdx.x, lo = max(len, j << C.lgp), hi = min(len + n, (j + 1) << C.lgp);
   const PagePart g{lo - len, hi - lo, C.dim / (2 * P), b * src.row};
   const int nu = g.count * g.units, off = lo - (j << C.lgp), rot = ROT ? A.R.rot : 0;
   constexpr int K = AR_VALUES / (2 * P);
   const E* const base = static_cast<const E*>(src.p) + g.row + (long long)g.t0 * src.tok;
+  // Of this thread's units: the token, where its two vectors begin, and whether it is rotated.
+  const E* from[K];
+  int to[K], gap[K];
+  bool turns[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int i = tid + k * static_cast<int>(blockDim.x), t = i / g.units;
+    const RopeUnit<P, INTER> unit(i - t * g.units, rot);
+    from[k] = base + (long long)t * src.tok + unit.lo;
+    to[k] = i < nu ? t * C.dim + unit.lo : -1;
+    gap[k] = unit.hi - unit.lo;
+    turns[k] = ROT && unit.turns;
+  }
   float2 cs[ROT ? K : 1][P];
   RopeVec<E, P> raw[K][2];
   auto fetch = [&](int h) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int i = tid + k * AR_THREADS;
-      if (i >= nu) break;
-      const int t = i / g.units;
-      const RopeUnit<P, INTER> unit(i - t * g.units, rot);
-      const E* x = base + (long long)t * src.tok + (size_t)h * C.dim;
-      raw[k][0].load(x + unit.lo);
-      raw[k][1].load(x + unit.hi);
+      if (to[k] < 0) break;
+      const E* x = from[k] + (size_t)h * C.dim;
+      raw[k][0].load(x);
+      raw[k][1].load(x + gap[k]);
     }
   };
-  fetch(h0);
+  const bool large = nu > K * static_cast<int>(blockDim.x);
+  if (!large) fetch(h0);
+  // (The tokens are on their way while the row's pages are looked up: is every one that it writes its
+  // own?)
+  const int page = kv_page(C, b, j << C.lgp);
+  const bool fine = A.checked ? kv_ld(A.S.flag + b) != 0 : kv_append_holds(C, b, len, n);
+  if (!__syncthreads_and(fine ? 1 : 0)) {
+    if (tid == 0 && blockIdx.x == 0 && !A.checked) kv_report(A.S.hdr, ST_DEVICE_INPUT);
+    return;
+  }
+  if (nu <= 0) return;
+  auto rest = [&](int h, float old) {
+    append_rest<E, P, INTER, ROT>(A, src, g, h, pos, off, pool + kv_block(C, A.layer, page, h),
+                                  scales + kv_sidx(C, A.layer, page, h), old, large, s_max[h & 1]);
+  };
+  if (large) {
+    for (int h = h0; h < h1; ++h) rest(h, 0.f);
+    return;
+  }
   if constexpr (ROT) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int i = tid + k * AR_THREADS, t = i / g.units, u = i - t * g.units;
-      if (i < nu && 2 * P * u < rot) rope_turns<P>(A.R, pos(g.t0 + t), u, cs[k]);
+      const int i = tid + k * static_cast<int>(blockDim.x), t = i / g.units;
+      if (i < nu && turns[k]) rope_turns<P>(A.R, pos(g.t0 + t), i - t * g.units, cs[k]);
     }
   }
+  bool more = false;  // a scale has changed, or is no plain power of two
   for (int h = h0; h < h1; ++h) {
     float* const scale = scales + kv_sidx(C, A.layer, page, h);
     const float old = off ? kv_ld(scale) : 0.f;
     float f[K][2 * P], a = 0.f;
+    uint32_t most = 0;  // of |x|, whose order as numbers is that of their bits, NaN above all
     bool odd = false;  // a value outside the scales' range
-    auto see = [&](const float* x) {
-#pragma unroll
-      for (int e = 0; e < 2 * P; ++e) {
-        const float y = fabsf(x[e]);
-        if (y <= KV_XMAX)
-          a = fmaxf(a, y);
-        else
-          odd = true;
-      }
-    };
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int i = tid + k * AR_THREADS;
-      if (i >= nu) break;
+      if (to[k] < 0) break;
       raw[k][0].get(f[k]);
       raw[k][1].get(f[k] + P);
-      if (ROT && 2 * P * (i % g.units) < rot) rope_apply<P, INTER>(f[k], cs[ROT ? k : 0]);
-      see(f[k]);
+      if (turns[k]) rope_apply<P, INTER>(f[k], cs[ROT ? k : 0]);
+#pragma unroll
+      for (int e = 0; e < 2 * P; e += 2)
+        most = __vimax3_u32(most, __float_as_uint(fabsf(f[k][e])), __float_as_uint(fabsf(f[k][e + 1])));
     }
     if (h + 1 < h1) fetch(h + 1);
-    // (Values past the registers' share are loaded, and rotated, again for the second step.)
-    for (int i = tid + K * AR_THREADS; i < nu; i += AR_THREADS) {
-      float x[2 * P];
-      RopeUnit<P, INTER> unit(0, 0);
-      load_unit<E, P, INTER, ROT>(A, src, g, i, h, pos, x, &unit);
-      see(x);
+    if (most <= __float_as_uint(KV_XMAX)) {
+      a = __uint_as_float(most);
+    } else {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (to[k] >= 0) a = fmaxf(a, append_seen<P>(f[k], &odd));
     }
     if (odd) kv_report(A.S.hdr, ST_DEVICE_INPUT);
-#pragma unroll
-    for (int d = 16; d; d >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
-    float* const mx = s_max[(h - h0) & 1];
-    if ((tid & 31) == 0) mx[tid >> 5] = a;
-    __syncthreads();  // (every thread has read the old scale; the other half of s_max is free)
-#pragma unroll
-    for (int w = 0; w < AR_THREADS / 32; ++w) a = fmaxf(a, mx[w]);
-    const float s = fmaxf(kv_scale(a), old);
-    uint8_t* const dst = pool + kv_block(C, A.layer, page, h);
-    if (off && s != old)  // older tokens of the page, at its new scale
-      for (int i = tid; i < off * C.dim / 16; i += AR_THREADS) {
-        uint4 x = reinterpret_cast<uint4*>(dst)[i];
-        uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) w[q] = kv_rescale4(w[q], old, s);
-        reinterpret_cast<uint4*>(dst)[i] = x;
-      }
-    if (tid == 0) *scale = s;
-    uint8_t* const out = dst + (size_t)off * C.dim;
-    if (!kv_pow2(s)) {
-      append_any<E, P, INTER, ROT>(A, src, g, h, pos, out, s);
-      continue;
-    }
-    const float inv = 1.f / s;
+    if (tid == 0) s_old[h - h0] = old;
+    const float s = append_scale(a, old, scale, s_max[h & 1]);
+    more = more || (off && s != old) || !append_plain(s);
+    if (!append_plain(s)) continue;
+    uint8_t* const out = pool + kv_block(C, A.layer, page, h) + (size_t)off * C.dim;
+    const float inv = __uint_as_float(0x7f000000u - __float_as_uint(s));  // 1 / s
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int i = tid + k * AR_THREADS;
-      if (i >= nu) break;
-      const int t = i / g.units;
-      const RopeUnit<P, INTER> unit(i - t * g.units, rot);
-      put_e4m3<P>(out + (size_t)t * C.dim + unit.lo, f[k], inv);
-      put_e4m3<P>(out + (size_t)t * C.dim + unit.hi, f[k] + P, inv);
+      if (to[k] < 0) break;
+      put_e4m3<P>(out + to[k], f[k], inv);
+      put_e4m3<P>(out + to[k] + gap[k], f[k] + P, inv);
     }
-    for (int i = tid + K * AR_THREADS; i < nu; i += AR_THREADS) {
-      float x[2 * P];
-      RopeUnit<P, INTER> unit(0, 0);
-      const int t = load_unit<E, P, INTER, ROT>(A, src, g, i, h, pos, x, &unit);
-      put_e4m3<P>(out + (size_t)t * C.dim + unit.lo, x, inv);
-      put_e4m3<P>(out + (size_t)t * C.dim + unit.hi, x + P, inv);
-    }
+  }
+  if (more) {  // (the same in every thread)
+    __syncthreads();
+    for (int h = h0; h < h1; ++h) rest(h, s_old[h - h0]);
   }
 }
 
 // grid (x: blocks of keys, of values, of queries; y: rows)
 template <typename E, int P, bool INTER>
-__global__ void __launch_bounds__(AR_THREADS, sizeof(E) == 2 ? 2 : 1)
+__global__ void __launch_bounds__(AR_MOST)
     kv_append_rope_kernel(const __grid_constant__ AppendRopeArgs A) {
   kv_enter();
   __shared__ int s_par[SV_MAX_TREE], s_depth[SV_MAX_TREE];
@@ -209,52 +289,53 @@ __global__ void __launch_bounds__(AR_THREADS, sizeof(E) == 2 ? 2 : 1)
     w.out = static_cast<E*>(A.q.out) + b * A.q_out_row;
     w.n = n;
     w.bad = bad;
-    rope_row<E, P, INTER>(A.R, w, (blockIdx.x - 2 * kv_blocks) * AR_THREADS + tid,
-                          A.q_blocks * AR_THREADS, pos);
+    rope_row<E, P, INTER, 2>(A.R, w, (blockIdx.x - 2 * kv_blocks) * blockDim.x + tid,
+                             A.q_blocks * blockDim.x, pos);
     return;
   }
   if (bad || n == 0) return;
   const int i = blockIdx.x - (values ? kv_blocks : 0);
   const int chunk = i / A.pages, j = (len >> C.lgp) + i - chunk * A.pages;
-  // Every page that the row writes is its own.
-  const bool sane = kv_append_fits(C, len, n, T);
-  const bool fine = A.checked ? kv_ld(A.S.flag + b) != 0 : sane && kv_append_holds(C, b, len, n);
-  if (!__syncthreads_and(fine ? 1 : 0)) {
+  if (!kv_append_fits(C, len, n, T)) {
     if (tid == 0 && blockIdx.x == 0 && !A.checked) kv_report(A.S.hdr, ST_DEVICE_INPUT);
     return;
   }
-  if ((long long)j << C.lgp >= (long long)len + n) return;
-  const int page = kv_page(C, b, j << C.lgp), h0 = chunk * A.per, h1 = min(h0 + A.per, C.heads);
+  const int h0 = chunk * A.per, h1 = min(h0 + A.per, C.heads);
   if (values)
-    append_page<E, 8, false, false>(A, A.v, C.v, C.vs, b, j, h0, h1, len, n, page, pos);
+    append_page<E, 8, false, false>(A, A.v, C.v, C.vs, b, j, h0, h1, len, n, pos);
   else
-    append_page<E, P, INTER, true>(A, A.k, C.k, C.ks, b, j, h0, h1, len, n, page, pos);
+    append_page<E, P, INTER, true>(A, A.k, C.k, C.ks, b, j, h0, h1, len, n, pos);
 }
 
 template <typename E>
-static cudaError_t launch_type(const AppendRopeArgs& A, bool inter, dim3 grid, cudaStream_t st) {
+static cudaError_t launch_type(const AppendRopeArgs& A, bool inter, dim3 grid, int threads,
+                               cudaStream_t st) {
   const int P = rope_pairs(A.R.rot);
   auto* kernel = P == 8   ? (inter ? kv_append_rope_kernel<E, 8, true> : kv_append_rope_kernel<E, 8, false>)
                  : P == 4 ? (inter ? kv_append_rope_kernel<E, 4, true> : kv_append_rope_kernel<E, 4, false>)
                           : (inter ? kv_append_rope_kernel<E, 1, true> : kv_append_rope_kernel<E, 1, false>);
-  return kv_launch(kernel, grid, AR_THREADS, 0, st, A);
+  return kv_launch(kernel, grid, threads, 0, st, A);
 }
 
 cudaError_t launch_kv_append_rope(AppendRopeArgs& A, bool inter, sv_dtype dt, cudaStream_t st) {
   const KvCache& C = A.C;
   // A row's tokens start anywhere in a page, so T of them touch at most this many.
   A.pages = (A.T + C.page - 2) / C.page + 1;
-  // Heads of a block: all of them, which computes cosines once, or fewer while the blocks are
-  // not four to an SM.
+  const int tokens = A.T < C.page ? A.T : C.page;
+  int threads = (tokens * C.dim / AR_VALUES + 31) / 32 * 32;
+  threads = threads < AR_LEAST ? AR_LEAST : (threads > AR_MOST ? AR_MOST : threads);
+  // Heads of a block: all of them, which computes cosines once, or fewer while the blocks do not
+  // fill the SMs.
   const long long blocks = 2LL * A.pages * C.batch;
-  const long long want = (4 * 152 + blocks - 1) / blocks;
-  const int cut = static_cast<int>(want < C.heads ? want : C.heads);
+  const long long want = (152LL * AR_MOST / threads + blocks - 1) / blocks;
+  const long long least = (C.heads + AR_PER - 1) / AR_PER;
+  const int cut = static_cast<int>(want < least ? least : (want < C.heads ? want : C.heads));
   A.per = (C.heads + cut - 1) / cut;
   A.chunks = (C.heads + A.per - 1) / A.per;
   A.q_blocks = 0;
   if (A.q.heads) {
     const int units = (A.q.same ? A.R.rot : A.q.dim) / (2 * rope_pairs(A.R.rot));
-    rope_cut(C.batch, A.T, A.q.heads, units, AR_THREADS, &A.q.shares, &A.q_blocks);
+    rope_cut(C.batch, A.T, A.q.heads, units, threads, AR_MOST, &A.q.shares, &A.q_blocks);
   }
   A.checked = A.pages > KV_APPEND_CHECK;
   if (A.checked) {
@@ -262,9 +343,9 @@ cudaError_t launch_kv_append_rope(AppendRopeArgs& A, bool inter, sv_dtype dt, cu
     if (e != cudaSuccess) return e;
   }
   const dim3 grid(2 * A.pages * A.chunks + A.q_blocks, C.batch);
-  return dt == SV_F32    ? launch_type<float>(A, inter, grid, st)
-         : dt == SV_BF16 ? launch_type<__nv_bfloat16>(A, inter, grid, st)
-                         : launch_type<__half>(A, inter, grid, st);
+  return dt == SV_F32    ? launch_type<float>(A, inter, grid, threads, st)
+         : dt == SV_BF16 ? launch_type<__nv_bfloat16>(A, inter, grid, threads, st)
+                         : launch_type<__half>(A, inter, grid, threads, st);
 }
 
 }  // namespace sv

@@ -24,7 +24,7 @@ __global__ void __launch_bounds__(ROPE_THREADS)
     w.bad = !rope_depths(A.parent + (size_t)b * T, w.n, s_par, s_depth);
   if (w.bad && blockIdx.x == 0 && threadIdx.x == 0) kv_report(A.hdr, ST_DEVICE_INPUT);
   const long long start = A.start ? kv_ld(A.start + b) : 0;
-  rope_row<E, P, INTER>(A.R, w, blockIdx.x * ROPE_THREADS + threadIdx.x, gridDim.x * ROPE_THREADS,
+  rope_row<E, P, INTER, 4>(A.R, w, blockIdx.x * ROPE_THREADS + threadIdx.x, gridDim.x * ROPE_THREADS,
                         [&](int t) -> long long {
                           if (A.pos) return kv_ld(A.pos + (size_t)b * T + t);
                           return start + (A.parent ? s_depth[t] : t);
@@ -44,7 +44,7 @@ cudaError_t launch_rope(const RopeArgs& A0, bool inter, sv_dtype dt, int rows, c
   RopeArgs A = A0;
   int blocks;
   const int units = (A.row.same ? A.R.rot : A.row.dim) / (2 * rope_pairs(A.R.rot));
-  rope_cut(rows, A.row.T, A.row.heads, units, ROPE_THREADS, &A.row.shares, &blocks);
+  rope_cut(rows, A.row.T, A.row.heads, units, ROPE_THREADS, 2048, &A.row.shares, &blocks);
   const dim3 grid(blocks, rows);
   return dt == SV_F32    ? launch_type<float>(A, inter, grid, st)
          : dt == SV_BF16 ? launch_type<__nv_bfloat16>(A, inter, grid, st)

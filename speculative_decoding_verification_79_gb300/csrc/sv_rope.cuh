@@ -192,7 +192,7 @@ struct RopeRow {
   int T, n, heads, dim, shares;
   bool same, bad;
 };
-template <typename E, int P, bool INTER, typename Pos>
+template <typename E, int P, bool INTER, int K, typename Pos>
 __device__ __forceinline__ void rope_row(const Rope& R, const RopeRow& w, int first, int step, Pos pos) {
   const int units = (w.same && !w.bad ? R.rot : w.dim) / (2 * P);
   const int live = w.bad ? w.T : (w.same ? w.n : w.T);
@@ -214,7 +214,7 @@ __device__ __forceinline__ void rope_row(const Rope& R, const RopeRow& w, int fi
     }
     float2 cs[P];
     if (unit.turns) rope_turns<P>(R, pos(t), u, cs);
-    constexpr int K = 4;  // heads whose loads are in flight
+    // (K heads' loads are in flight.)
     for (int h0 = share; h0 < w.heads; h0 += K * w.shares) {
       RopeVec<E, P> a[K], b[K];
 #pragma unroll
@@ -246,10 +246,11 @@ __device__ __forceinline__ void rope_row(const Rope& R, const RopeRow& w, int fi
 
 // How a call's rows are cut: shares of the heads, and blocks of a row. A thread takes up to 8
 // heads, so that their loads hide each other and cosines are computed once for them; fewer while
-// the threads of all rows do not fill the GPU's 152 x 2,048.
-inline void rope_cut(int rows, int T, int heads, int units, int threads, int* shares, int* blocks) {
+// the threads of all rows do not fill the GPU's 152 SMs (with `resident` threads each).
+inline void rope_cut(int rows, int T, int heads, int units, int threads, int resident, int* shares,
+                     int* blocks) {
   const long long all = (long long)rows * T * units * heads;
-  long long per = all / (152 * 2048);
+  long long per = (all + 152LL * resident - 1) / (152LL * resident);
   per = per < 1 ? 1 : (per > 8 ? 8 : per);
   *shares = static_cast<int>((heads + per - 1) / per);
   const long long items = (long long)T * units * *shares;
