@@ -284,7 +284,7 @@ cudaError_t launch_kv_share(const KvCache& C, const KvScratch& S, const KvShare&
   return e;
 }
 
-cudaError_t launch_kv_attend_shared(const SharedArgs& A, sv_dtype dt, cudaStream_t st) {
+cudaError_t launch_kv_attend_shared(const SharedArgs& A0, sv_dtype dt, cudaStream_t st) {
   static const SharedKernel* const kernels[2][2] = {{shared_kernels_f16_1, shared_kernels_f16_2},
                                                     {shared_kernels_bf16_1, shared_kernels_bf16_2}};
   int dev = 0;
@@ -300,12 +300,12 @@ cudaError_t launch_kv_attend_shared(const SharedArgs& A, sv_dtype dt, cudaStream
     return static_cast<int>(attr);
   }));
   if (e != cudaSuccess) return e;
+  SharedArgs A = A0;
   AttendLaunch L;
   if ((e = at_launch(A, dt, at_width((long long)A.T * A.group), dev, &L)) != cudaSuccess) return e;
   // (No group has more rows than the batch.)
-  if (A.large && at_width((long long)A.C.batch * A.T * A.group) == 128 &&
-      (e = launch_kv_attend_group(A, L, dt, dev, st)) != cudaSuccess)
-    return e;
+  A.behind = A.large && at_width((long long)A.C.batch * A.T * A.group) == 128;
+  if (A.behind && (e = launch_kv_attend_group(A, L, dt, dev, st)) != cudaSuccess) return e;
   const SharedKernel kernel = kernels[dt == SV_BF16][L.ndb - 1][L.width == 32 ? 0 : (L.width == 64 ? 1 : 2)];
   if ((e = kv_launch(kernel, dim3(L.grid), AT_THREADS, L.smem, st, A, L.P, L.tm[0], L.tm[1])) != cudaSuccess)
     return e;
