@@ -34,6 +34,7 @@ constexpr int KV_EXTRA = 6;
 // rows r0 .. r0 + R - 1 of (row b, head h). R = 0: the CTA has none.
 struct KvOpen {
   int b, h, r0, R, last;
+  int slot;  // (rows that share pages: of the first of its parts, and last counts from there)
 };
 
 struct KvWs {

@@ -1702,17 +1702,22 @@ __device__ __forceinline__ void at_body(const Args& A, const AttendPlan& P, cons
           opened = true;
           if (st == 0) {
             const int all = sh.total, n = min(most_ctas, all);
-            A.S.open[cta] = KvOpen{it.b, it.h, it.r0, it.R, at_owner(it.u0 + it.tiles - 1, all, n)};
+            A.S.open[cta] = KvOpen{it.b, it.h, it.r0, it.R, at_owner(it.u0 + it.tiles - 1, all, n), 0};
           }
         }
-      } else if (it.i0 == 0 && st == 0) {
-        const int all = sh.total, n = min(most_ctas, all);
-        at_spans<M>(A)[it.no] = KvSpan{cta, at_owner(it.u0 + it.tiles - 1, all, n)};
+      } else if (!whole && it.i0 == 0) {
+        const int all = sh.total, n = min(most_ctas, all), last = at_owner(it.u0 + it.tiles - 1, all, n);
+        if (M == AT_GROUPS || it.part) {
+          if (st == 0) at_spans<M>(A)[it.no] = KvSpan{cta, last};
+        } else {
+          opened = true;
+          if (st == 0) A.S.open[blockIdx.x] = KvOpen{it.b, it.h, it.r0, it.R, last - cta, it.no + cta};
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&dempty[kb]);
     }
-    if (M == AT_ROWS && !opened && st == 0) A.S.open[cta].R = 0;
+    if (!opened && st == 0) A.S.open[blockIdx.x].R = 0;
   }
 
   tm_fence_before();

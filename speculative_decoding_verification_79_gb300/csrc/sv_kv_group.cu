@@ -260,13 +260,24 @@ __global__ void __launch_bounds__(GR_THREADS, 1)
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return gr_try(bar, parity) || gr_wait_on(bar, parity, &s_abort, A);
   };
-  kv_enter();
-  // (Before anything is set up: there may be no group that is large enough.)
-  if (!at_large(A, (long long)kv_ld(A.H.head + 1) * A.T * A.group)) return;
-  const AtCount count = at_count<AT_GROUPS, GR_THREADS>(A, sh.rows);
-  int before;
-  const int total = at_block_sum<GR_THREADS>(count.sum, sh.sum, &before);
-  if (total == 0) return;
+  // A CTA starts as an SM's CTA of the launch for rows ends: it needs nothing of that one but that it
+  // is over before this one is. All earlier work that one has waited for before it let this one
+  // start, and the fence puts this SM's reads behind it. (Waiting for all of it first: 64 chats
+  // behind one prompt 97.5 us instead of 93.8. This launch first, the rows'
+  // behind it: 90 us instead of 84, and 75 instead of 67 for 64 rows of 64 queries without a group,
+  // since the rows' CTAs then find no room to be set up early.)
+  __threadfence();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  AtCount count = {0, 0};
+  int before = 0, total = 0;
+  if (at_large(A, (long long)kv_ld(A.H.head + 1) * A.T * A.group)) {
+    count = at_count<AT_GROUPS, GR_THREADS>(A, sh.rows);
+    total = at_block_sum<GR_THREADS>(count.sum, sh.sum, &before);
+  }
+  if (total == 0) {  // (before anything is set up)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   at_setup<GR_WARPS>(sh);
   const int cta = blockIdx.x, most_ctas = gridDim.x;
   const uint32_t* const s_rows = sh.rows;
@@ -563,6 +574,7 @@ __global__ void __launch_bounds__(GR_THREADS, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
                  : "memory");
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Its shared memory beside static arrays.

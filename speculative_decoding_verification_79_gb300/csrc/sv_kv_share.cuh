@@ -24,7 +24,6 @@ struct SharedArgs : AttendArgs {
   KvShare H;
   int tiles;        // query tiles of a row at most
   int large;        // may large groups go to their own kernel?
-  int behind;       // was that kernel launched before?
   int always;       // is every group's common part shared (sv_set_share_always)?
   int own_rows;     // rows of a slot of partial results of rows
   KvSpan *own_span, *span;  // by query tile: of rows, of groups

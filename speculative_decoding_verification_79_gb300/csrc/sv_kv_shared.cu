@@ -153,31 +153,54 @@ __device__ __forceinline__ KvSpan join_span(const KvSpan* p) {
   return KvSpan{min(max(s.first, 0), KV_MAX_CTAS - 1), min(s.last, KV_MAX_CTAS - 1)};
 }
 
-// A warp: eight query rows of a query tile and head, their parts' sums first, then four lanes a row
-// take its vectors in turn, eight of them in flight. (Rows next to each other: whole sectors.)
-__global__ void __launch_bounds__(SJ_THREADS)
-    kv_shared_join_kernel(const __grid_constant__ SharedArgs A, int bf16) {
+// A warp: 64 components of eight query rows of a query tile and head, four lanes a row, four parts'
+// loads in flight and a running reference. (Rows next to each other: whole sectors.) Query tiles of
+// rows alone are in parts only where two CTAs' shares meet: the first warps take those from the
+// CTAs' records, the others those of rows in groups. (Looking at every query tile and head
+// instead took a call for 64 rows of 64 queries on 740 tokens 81 us instead of 75, as it was then;
+// all sums first, then the parts two at a time, 8 samples of a document of 120,001 tokens, whose
+// query tiles have some fourteen parts, 140 us instead of 126.)
+__global__ void __launch_bounds__(SJ_THREADS, 2)
+    kv_shared_join_kernel(const __grid_constant__ SharedArgs A, int ctas, int bf16) {
   kv_enter();
-  const int vec = A.C.dim / 4, eights = A.own_rows / 8, heads = A.C.heads, lane = threadIdx.x & 31;
-  const long long item = (long long)blockIdx.x * (SJ_THREADS / 32) + threadIdx.x / 32;
-  const int chunk = static_cast<int>(item % eights);
-  const long long tile = item / eights;
-  const int h = static_cast<int>(tile % heads), bt = static_cast<int>(tile / heads);
-  const int b = bt / A.tiles, rt = bt - b * A.tiles;
-  if (b >= A.C.batch) return;
-  const AtRow row = at_row<AT_OWN>(A, b);
-  const int r0 = rt * row.rr, r = 8 * chunk + (lane & 7), R = min(r0 + row.rr, row.rows) - r0;
-  if (rt >= row.nrt || 8 * chunk >= R) return;
-  const int no = at_tile_no(A, AT_OWN, b, rt, h);
-  const KvSpan own = join_span(A.own_span + no);
-  if (!row.skip && own.first == own.last) return;
-  if (r >= R) return;
-  // The group's part of the query: row gr of `count` slots from id on.
-  int id = 0, gr = 0, count = 0;
-  if (row.skip) {
+  constexpr int U = 4, K = 4;
+  const int vec = A.C.dim / 4, pieces = (vec + 4 * U - 1) / (4 * U), heads = A.C.heads;
+  const int eights = A.own_rows / 8, lane = threadIdx.x & 31;
+  const long long met = (long long)ctas * eights;  // items of CTAs' shares that meet
+  const long long at = (long long)blockIdx.x * (SJ_THREADS / 32) + threadIdx.x / 32;
+  const long long item = at / pieces;
+  const int piece = static_cast<int>(at - item * pieces), chunk = static_cast<int>(item % eights);
+  int b, h, r0, R, no, owns;      // (no: the first of `owns` slots of the row's own)
+  int id = 0, gr = 0, count = 0;  // of the group's: row gr of `count` slots from id on
+  const int r = 8 * chunk + (lane & 7);
+  bool bad = false;
+  if (item < met) {
+    const KvOpen it = A.S.open[item / eights];
+    if (8 * chunk >= it.R) return;
+    b = it.b;
+    h = it.h;
+    r0 = it.r0;
+    R = it.R;
+    no = it.slot;
+    owns = it.last + 1;
+  } else {
+    if (kv_ld(A.H.head) == 0) return;
+    const long long tile = (item - met) / eights, bt = tile / heads;
+    h = static_cast<int>(tile - bt * heads);
+    b = static_cast<int>(bt / A.tiles);
+    if (b >= A.C.batch) return;
+    const int rt = static_cast<int>(bt - (long long)b * A.tiles);
+    const AtRow row = at_row<AT_OWN>(A, b);
+    r0 = rt * row.rr;
+    R = min(r0 + row.rr, row.rows) - r0;
+    if (!row.skip || rt >= row.nrt || 8 * chunk >= R) return;
+    no = at_tile_no(A, AT_OWN, b, rt, h);
+    const KvSpan own = join_span(A.own_span + no);
+    no += own.first;
+    owns = own.last - own.first + 1;
     const int4 mine = kv_ld(A.H.row + b);
     const AtRow group = at_row<AT_GROUPS>(A, mine.x);
-    const int i = mine.w * A.T * A.group + r0 + r, grt = i / group.rr;
+    const int i = mine.w * A.T * A.group + r0 + min(r, R - 1), grt = i / group.rr;
     gr = i - grt * group.rr;
     if (!A.window || at_tile<AT_GROUPS>(A, group, mine.x, grt).tiles() > 0) {
       id = at_tile_no(A, AT_GROUPS, mine.x, grt, h);
@@ -185,64 +208,72 @@ __global__ void __launch_bounds__(SJ_THREADS)
       count = span.last - span.first + 1;
       id += span.first;
     }
+    bad = kv_ld(A.H.bad + b) != 0;
   }
-  const int slots = count + own.last - own.first + 1;
+  if (r >= R) return;
+  const int slots = count + owns;
   auto slot = [&](int k, const float2** stat, const float4** part, int* rows) {
     const bool mine = k >= count;
-    const int at = mine ? no + own.first + k - count : id + k, rr = mine ? r : gr;
+    const int at = mine ? no + k - count : id + k, rr = mine ? r : gr;
     *rows = mine ? A.own_rows : KV_ROWS;
     *stat = (mine ? A.own_stat : A.stat) + (size_t)at * *rows + rr;
-    *part = reinterpret_cast<const float4*>(mine ? A.own_part : A.part) + at_part(at, rr, 0, A.C.dim, *rows);
+    *part = reinterpret_cast<const float4*>(mine ? A.own_part : A.part) +
+            at_part(at, rr, 0, A.C.dim, *rows);
   };
+  const int v0 = 4 * U * piece + (lane >> 3);
   float ref = -INFINITY, sum = 0.f;
-#pragma unroll 4
-  for (int k = 0; k < slots; ++k) {
-    const float2* stat;
-    const float4* part;
-    int rows;
-    slot(k, &stat, &part, &rows);
-    const float2 x = __ldcg(stat);
-    if (x.y == 0.f) continue;
-    const float top = fmaxf(ref, x.x);
-    sum = fmaf(x.y, exp2f(x.x - top), sum == 0.f ? 0.f : sum * exp2f(ref - top));
-    ref = top;
-  }
-  float inv = sum == 0.f ? 0.f : 1.f / sum;
-  if (kv_ld(A.H.bad + b)) inv = sum = NAN;
-  const int i = r0 + r, t = i / A.group, gh = i - t * A.group;
-  const long long out = ((long long)b * A.T + t) * A.q_heads + h * A.group + gh;
-  if (lane < 8 && A.lse) A.lse[out] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
-  constexpr int U = 8;
-  for (int v0 = lane >> 3; v0 < vec; v0 += 4 * U) {
-    float4 o[U];
+  float4 o[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-    for (int k = 0; k < slots; ++k) {
+  for (int u = 0; u < U; ++u) o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = 0; k0 < slots; k0 += K) {
+    float2 x[K];
+    float4 y[K][U];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      x[k] = make_float2(0.f, 0.f);
+      if (k0 + k >= slots) continue;
       const float2* stat;
       const float4* part;
       int rows;
-      slot(k, &stat, &part, &rows);
-      const float2 x = __ldcg(stat);
-      float4 y[U];
+      slot(k0 + k, &stat, &part, &rows);
+      x[k] = __ldcg(stat);
 #pragma unroll
-      for (int u = 0; u < U; ++u) y[u] = __ldcg(part + (size_t)min(v0 + 4 * u, vec - 1) * rows);
-      const float f = exp2f(x.x - ref);
-      if (x.y == 0.f) continue;
+      for (int u = 0; u < U; ++u) y[k][u] = __ldcg(part + (size_t)min(v0 + 4 * u, vec - 1) * rows);
+    }
+    float top = ref;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (x[k].y != 0.f) top = fmaxf(top, x[k].x);
+    const float f0 = sum == 0.f ? 0.f : exp2f(ref - top);
+    ref = top;
+    sum *= f0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) o[u] = make_float4(o[u].x * f0, o[u].y * f0, o[u].z * f0, o[u].w * f0);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (x[k].y == 0.f) continue;
+      const float f = exp2f(x[k].x - top);
+      sum = fmaf(x[k].y, f, sum);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        o[u].x = fmaf(y[u].x, f, o[u].x);
-        o[u].y = fmaf(y[u].y, f, o[u].y);
-        o[u].z = fmaf(y[u].z, f, o[u].z);
-        o[u].w = fmaf(y[u].w, f, o[u].w);
+        o[u].x = fmaf(y[k][u].x, f, o[u].x);
+        o[u].y = fmaf(y[k][u].y, f, o[u].y);
+        o[u].z = fmaf(y[k][u].z, f, o[u].z);
+        o[u].w = fmaf(y[k][u].w, f, o[u].w);
       }
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (v0 + 4 * u < vec)
-        at_store4(A.out, out * A.C.dim + (v0 + 4 * u) * 4,
-                  make_float4(o[u].x * inv, o[u].y * inv, o[u].z * inv, o[u].w * inv), bf16);
   }
+  float inv = sum == 0.f ? 0.f : 1.f / sum;
+  if (bad) inv = sum = NAN;
+  const int i = r0 + r, t = i / A.group, gh = i - t * A.group;
+  const long long out = ((long long)b * A.T + t) * A.q_heads + h * A.group + gh;
+  if (piece == 0 && lane < 8 && A.lse)
+    A.lse[out] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (v0 + 4 * u < vec)
+      at_store4(A.out, out * A.C.dim + (v0 + 4 * u) * 4,
+                make_float4(o[u].x * inv, o[u].y * inv, o[u].z * inv, o[u].w * inv), bf16);
 }
 
 }  // namespace
@@ -284,7 +315,7 @@ cudaError_t launch_kv_share(const KvCache& C, const KvScratch& S, const KvShare&
   return e;
 }
 
-cudaError_t launch_kv_attend_shared(const SharedArgs& A0, sv_dtype dt, cudaStream_t st) {
+cudaError_t launch_kv_attend_shared(const SharedArgs& A, sv_dtype dt, cudaStream_t st) {
   static const SharedKernel* const kernels[2][2] = {{shared_kernels_f16_1, shared_kernels_f16_2},
                                                     {shared_kernels_bf16_1, shared_kernels_bf16_2}};
   int dev = 0;
@@ -300,19 +331,20 @@ cudaError_t launch_kv_attend_shared(const SharedArgs& A0, sv_dtype dt, cudaStrea
     return static_cast<int>(attr);
   }));
   if (e != cudaSuccess) return e;
-  SharedArgs A = A0;
   AttendLaunch L;
   if ((e = at_launch(A, dt, at_width((long long)A.T * A.group), dev, &L)) != cudaSuccess) return e;
-  // (No group has more rows than the batch.)
-  A.behind = A.large && at_width((long long)A.C.batch * A.T * A.group) == 128;
-  if (A.behind && (e = launch_kv_attend_group(A, L, dt, dev, st)) != cudaSuccess) return e;
   const SharedKernel kernel = kernels[dt == SV_BF16][L.ndb - 1][L.width == 32 ? 0 : (L.width == 64 ? 1 : 2)];
   if ((e = kv_launch(kernel, dim3(L.grid), AT_THREADS, L.smem, st, A, L.P, L.tm[0], L.tm[1])) != cudaSuccess)
     return e;
-  const long long eights = (long long)A.C.batch * A.tiles * A.C.heads * (A.own_rows / 8);
-  const long long blocks = (eights + SJ_THREADS / 32 - 1) / (SJ_THREADS / 32);
+  // (No group has more rows than the batch.)
+  if (A.large && at_width((long long)A.C.batch * A.T * A.group) == 128 &&
+      (e = launch_kv_attend_group(A, L, dt, dev, st)) != cudaSuccess)
+    return e;
+  const long long eights = ((long long)A.C.batch * A.tiles * A.C.heads + L.grid) * (A.own_rows / 8);
+  const long long warps = eights * ((A.C.dim / 4 + 15) / 16);
+  const long long blocks = (warps + SJ_THREADS / 32 - 1) / (SJ_THREADS / 32);
   return kv_launch(kv_shared_join_kernel, dim3(static_cast<unsigned>(blocks)), SJ_THREADS, 0, st, A,
-                   dt == SV_BF16 ? 1 : 0);
+                   static_cast<int>(L.grid), dt == SV_BF16 ? 1 : 0);
 }
 
 }  // namespace sv

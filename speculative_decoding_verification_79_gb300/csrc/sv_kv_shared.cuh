@@ -28,14 +28,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   __shared__ int s_sum[AT_THREADS / 32];
   auto& sh = reinterpret_cast<AtShared<AT_OWN, W>&>(raw);
   at_setup(sh);
-  // Behind the launch for large groups, a CTA starts as an SM's CTA of that one ends: it needs
-  // nothing of it but that it is over before this one is. All earlier work that one has waited for
-  // before it let this one start, and the fence puts this SM's reads behind it.
-  if (A.behind)
-    __threadfence();
-  else
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  kv_enter();
   const long long most = (long long)kv_ld(A.H.head + 1) * A.T * A.group;  // queries of the largest group
   const int rows = at_width(most), grid = gridDim.x;
   const AtCount own = at_count<AT_OWN>(A, sh.rows);
@@ -60,7 +53,6 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   else
     at_body<AT_GROUPS, 128, BF16, NDB>(A, P, tmK, tmV, reinterpret_cast<AtShared<AT_GROUPS, 128>&>(raw),
                                        s_groups, dsm_raw, common, total, before, cta, ctas);
-  if (A.behind) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 typedef void (*SharedKernel)(const SharedArgs, const AttendPlan, const CUtensorMap, const CUtensorMap);
