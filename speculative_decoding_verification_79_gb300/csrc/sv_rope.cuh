@@ -25,8 +25,8 @@ struct Rope {
   float gain, sgain;
 };
 
-// Pairs of a thread, by the rotated size: as many as make 16-byte vectors of halves of a head
-// (P * P' pairs: rot / 2 a multiple of 8), fewer when the halves are not aligned to that.
+// Pairs of a thread, by the rotated size: 8, whose halves are 16-byte vectors of 16-bit values when
+// the second half begins at a multiple of 8 components; else 4 or 1, as its alignment allows.
 inline int rope_pairs(int rot) { return rot % 16 == 0 ? 8 : (rot % 8 == 0 ? 4 : 1); }
 
 __device__ __forceinline__ float2 rope_turn(const Rope& R, long long pos, int64_t freq) {

@@ -407,3 +407,125 @@ def test_rounds_together(sv):
                 assert all(c.fork(src))
             sv.sv_kv_share(a.g, share, i32(src))
     assert a.g.status() == sv.SV_OK
+
+
+@needs_cuda
+def test_strides_and_another_stream(sv):
+    """Queries inside a fused projection, tokens of all rows side by side, and results that the
+    binding allocates for another stream: the bits of the dense call."""
+    both, q, n, par, share, kw, want = case(sv, [(5, 700), (20, 400)], [90], [9, 60], 9, 2, 8, 64, 16,
+                                            trees=True, seed=8)
+    B, T, heads, dim = q.shape
+    wide = torch.empty(B, T, heads + 6, dim, dtype=BF, device="cuda")
+    wide[:, :, 2:heads + 2] = q
+    across = q.transpose(0, 1).contiguous().transpose(0, 1)
+    for x in (wide[:, :, 2:heads + 2], across):
+        got = sv.sv_kv_attend_shared(both.g, 0, x, share, **kw)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    got = sv.sv_kv_attend_shared(both.g, 0, q, share, stream=st, **kw)
+    st.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@needs_cuda
+def test_two_graphs_and_plain_calls(sv):
+    """Two captured graphs of other sizes on one cache and one buffer, plain attention between
+    them: each gives what it gives alone."""
+    both, lead = grouped(sv, [(20, 700), (3, 400)], [90], [9, 60], 2, 64, 16, 9)
+    g, B = both.g, both.r.batch
+    block(both, 9, 0, [9] * B)
+    share = sv.KVShare(g, 9, 16)
+    sv.sv_kv_share(g, share, i32(lead))
+    runs, nn = [], i32([1] * B)
+    for T, n_new in ((9, None), (1, nn)):
+        q = queries(both, T, 8, BF, T)
+        out, lse = torch.empty_like(q), torch.empty(q.shape[:3], device="cuda")
+        kw = dict(n_new=n_new if n_new is not None else i32([T] * B))
+        check_attend(both, 0, q, [T] * B, got=sv.sv_kv_attend_shared(g, 0, q, share, want_lse=True, **kw))
+        first = sv.sv_kv_attend_shared(g, 0, q, share, want_lse=True, **kw)
+        plain = sv.sv_kv_attend(g, 0, q, want_lse=True, **kw)
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            sv.sv_kv_attend_shared(g, 0, q, share, out=out, lse=lse, **kw)
+        runs.append((graph, q, kw, out, lse, first, plain))
+    for k in (0, 1, 1, 0, 0, 1):
+        graph, q, kw, out, lse, first, plain = runs[k]
+        out.fill_(math.nan)
+        graph.replay()
+        again = sv.sv_kv_attend(g, 0, q, want_lse=True, **kw)
+        torch.cuda.synchronize()
+        for x, y in zip((out, lse) + tuple(again), tuple(first) + tuple(plain)):
+            assert torch.equal(x, y)
+    assert g.status() == sv.SV_OK
+
+
+@needs_cuda
+@pytest.mark.parametrize("rows,heads,group", [(4096, 1, 1), (1024, 2, 16)])
+def test_largest_batches(sv, rows, heads, group):
+    """All rows of the largest batch in one group, and half of them in groups of two: against
+    the plain call, both within the bounds that check_attend takes (twice the smaller's)."""
+    page, dim, common = 16, 32, 256
+    shared, per = common // page, common // page + 1
+    g = sv.KVCache(1, shared * (rows // 2 + 1) + rows, page, heads, dim, rows, per)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    k = 0.5 * torch.randn(g.k.shape, generator=gen, device="cuda")
+    g.k.copy_(k.to(torch.float8_e4m3fn))
+    g.v.copy_(torch.randn(g.v.shape, generator=gen, device="cuda").to(torch.float8_e4m3fn))
+    own = torch.arange(rows, dtype=torch.int32, device="cuda")
+    q = torch.randn(rows, 1, heads * group, dim, generator=gen, device="cuda").to(BF)
+    share = sv.KVShare(g, 1, heads * group)
+    for pairs in (False, True):
+        # (Rows b and b ^ 1 are a group in the first half; all are, without pairs.)
+        lead = torch.where(own < rows // 2, own // 2, own) if pairs else own * 0
+        start = torch.unique(lead, return_inverse=True)[1].int()
+        keep = (start < rows // 2) if pairs else (own >= 0)
+        pool = start.clamp(max=rows // 2)[:, None] * shared + torch.arange(shared, device="cuda")
+        g.table[:, :shared] = pool.int()
+        g.table[:, shared] = shared * (rows // 2 + 1) + own
+        g.n_pages.fill_(per)
+        g.len.fill_(common + 5)
+        g.refs.fill_(1)
+        group_no = torch.where(keep, lead, -1).int() if pairs else lead
+        sv.sv_kv_share(g, share, group_no)
+        got = sv.sv_kv_attend_shared(g, 0, q, share, want_lse=True)
+        want = sv.sv_kv_attend(g, 0, q, want_lse=True)
+        # bf16 results of one sum in two orders: a step of bf16 (2^-7 of the value) and the weights'
+        # bound on what the values, up to 4.5, add up to: 2^-9 each way.
+        err = (got[0].float() - want[0].float()).abs()
+        assert (err <= 2 ** -7 * want[0].float().abs() + 4.5 * 2 ** -8).all()
+        assert ((got[1] - want[1]).abs() <= 2 ** -9).all()
+    assert g.status() == sv.SV_OK
+
+
+@needs_cuda
+def test_binding_refusals(sv, always):
+    both, lead = grouped(sv, [(3, 140)], [9], [9], 2, 64, 16, 2)
+    g, B = both.g, both.r.batch
+    share, q = sv.KVShare(g, 2, 8), queries(both, 2, 4, BF, 0)
+    other = sv.KVCache(1, 8, 16, 2, 64, B, 4)
+    for f in (lambda: sv.sv_kv_share(other, share), lambda: sv.sv_kv_share(g, share, i32([0])),
+              lambda: sv.sv_kv_share(g, share, torch.zeros(B, device="cuda")),
+              lambda: sv.sv_kv_share(g, share, torch.zeros(B, dtype=torch.int32)),
+              lambda: sv.sv_kv_attend_shared(other, 0, q, share),
+              lambda: sv.sv_kv_attend_shared(g, 0, q[:, :, :, :32], share),
+              lambda: sv.sv_kv_attend_shared(g, 0, q[1:], share),
+              lambda: sv.sv_kv_attend_shared(g, 0, q.cpu(), share),
+              lambda: sv.sv_kv_attend_shared(g, 0, q, share, out=q.float()),
+              lambda: sv.sv_kv_attend_shared(g, 0, q, share, lse=torch.empty(B, 2, 7, device="cuda")),
+              lambda: sv.sv_kv_attend_shared(g, 0, q, share, n_new=i32([1])),
+              lambda: sv.sv_kv_attend_shared(g, 0, q, share, parent=i32([[0]])),
+              lambda: sv.KVShare(g, 2, 7), lambda: sv.KVShare(g, -1, 8)):
+        with pytest.raises(ValueError):
+            f()
+    wide = queries(both, 2, 8, BF, 0)
+    for f in (lambda: sv.sv_kv_attend_shared(g, 1, q, share),
+              lambda: sv.sv_kv_attend_shared(g, 0, q.float(), share),
+              lambda: sv.sv_kv_attend_shared(g, 0, wide, share),
+              lambda: sv.sv_kv_attend_shared(g, 0, q, share, window=-1)):
+        with pytest.raises(sv.SpecVerifyError):
+            f()
+    assert sv.sv_kv_attend_shared(g, 0, q[:, :0], share).shape == (B, 0, 8, 64)
+    assert g.status() == sv.SV_OK

@@ -461,3 +461,52 @@ def test_binding_refusals(sv):
             f()
     assert sv.sv_rope(rope, k[:, :0]).shape == (3, 0, 2, 64)
     assert sv.sv_rope(rope, k[:0]).shape == (0, 7, 2, 64)
+
+
+@pytest.mark.parametrize("T", [1, 17, 1300])
+def test_append_rope_many_heads(sv, T):
+    """More heads than a block takes, with few blocks and with many; older tokens whose scale
+    grows, or stays, head by head."""
+    B, H = 8, 70
+    a, b = (sv.KVCache(1, B * 85, 16, H, 16, B, 85) for _ in range(2))
+    for c in (a, b):  # (bytes that no call writes are compared too)
+        c.k.view(torch.uint8).fill_(0)
+        c.v.view(torch.uint8).fill_(0)
+    rope = sv.Rope(16)
+    size = torch.exp2(torch.arange(H, device="cuda") % 7 - 3.0)[None, None, :, None]
+    for r, n in enumerate((5, T, 3)):
+        for c in (a, b):
+            sv.sv_kv_reserve(c, i32([n] * B))
+        k, v = rand((B, n, H, 16), r, F32) * size, rand((B, n, H, 16), r + 9, F32) / size
+        sv.sv_kv_append_rope(a, 0, k, v, rope)
+        sv.sv_kv_append(b, 0, sv.sv_rope(rope, k, start=b.len), v)
+        same_bytes(a, b)
+        for c in (a, b):
+            sv.sv_kv_commit(c, i32([n - 1] * B), n)
+        size = size.flip(2)
+    assert a.status() == sv.SV_OK
+
+
+@pytest.mark.parametrize("old", [0.3, 2.0 ** -20, 2.0 ** 60, 2.0 ** 126, 2.0 ** 127])
+@pytest.mark.parametrize("page,dim", [(16, 16), (64, 128), (128, 256)])
+def test_append_rope_other_scales(sv, old, page, dim):
+    """Pages whose older tokens have another quantiser's scale, in some heads, with new tokens that
+    fit a block's registers, and that do not."""
+    a, b = caches(sv, 2, page=page, heads=3, dim=dim, pages=12, max_pages=4)
+    rope = sv.Rope(dim, interleaved=True)
+    for c in (a, b):
+        c.k.view(torch.uint8).fill_(0x31)
+        c.v.view(torch.uint8).fill_(0x31)
+        sv.sv_kv_reserve(c, i32([5, 0, 1]))
+        c.k_scale[:, :, 1] = old
+        c.v_scale[:, :, 0] = old
+        c.v_scale[:, :, 2] = old
+        sv.sv_kv_commit(c, i32([4, -1, 0]), 5)
+    n = page + 7
+    for c in (a, b):
+        sv.sv_kv_reserve(c, i32([n] * 3))
+    k, v = rand((3, n, 3, dim), 1, BF), rand((3, n, 3, dim), 2, BF) * 900.0
+    sv.sv_kv_append_rope(a, 0, k, v, rope)
+    sv.sv_kv_append(b, 0, sv.sv_rope(rope, k.float(), start=b.len), v.float())
+    same_bytes(a, b)
+    assert a.status() == b.status()
