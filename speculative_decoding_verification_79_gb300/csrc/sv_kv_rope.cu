@@ -7,22 +7,24 @@
 // their cosines and sines stay in its registers, and the next head's loads are under way while a
 // head's largest value is found. Blocks behind those of keys and values rotate the queries
 // (rope_row). Bound by memory: 8 prompts of 4,093 tokens with 8 heads and 32 query heads of 128
-// take 140 us, 0.95 GB at 6.8 TB/s (sv_kv_append and sv_rope one after the other: 123 us, without
-// the rotation of the keys). A few tokens of many rows take the trips to memory one after the other
-// (lengths, table, counts of holders, old scale, beside the tokens themselves): 64 rows 5.5 us for
-// a token, 10.8 us for trees of 16.
+// take 127 us, 738 MB at 5.8 TB/s (the queries alone 80). A few tokens of many rows take the trips
+// to memory one after the other (lengths, table, counts of holders, old scale, beside the tokens
+// themselves): 64 rows 5.1 us for a token, 9.5 us for trees of 16.
 //
 // What decides is that the loop over heads has no call in it and fits 64 registers, so that an SM
 // holds 1,024 threads: with calls for the rare cases inside it (another quantiser's scale, the
 // rescaling of older tokens, divisions) it spilt on every head, and those prompts took 232 us. So
-// the loop leaves a page's rare cases to append_rest, behind it.
+// the loop leaves a page's rare cases to append_rest, behind it. (Which was given what it needs by
+// the loop's block, kept in registers meanwhile: 135 us; with the block's maximum found by shuffles
+// and a loop: 141.)
 #include "sv_rope.cuh"
 
 namespace sv {
 
 // Threads of a block: one for 16 values of the new tokens of a page, in whole warps, as far as that
-// goes. (The queries in a launch of their own: those prompts 149 us, trees 15.2. Twice or four
-// times as many blocks, of fewer heads each: 153 and 167 us, the cosines being computed again.)
+// goes. (The queries in a launch of their own: those prompts 149 us instead of 140, as it was then,
+// trees 15.2 instead of 10.8. Twice or four times as many blocks, of fewer heads each: 153 and 167
+// us, the cosines being computed again.)
 constexpr int AR_LEAST = 128, AR_MOST = 1024;
 constexpr int AR_VALUES = 16;  // of a page and head that a thread keeps in registers
 constexpr int AR_PER = 32;     // heads of a block
@@ -91,14 +93,14 @@ __device__ __forceinline__ float append_seen(const float* x, bool* odd) {
 
 // The scale of a page and head from the largest |x| of each thread's values (whole block). `mx`:
 // shared memory that no thread reads any more.
-__device__ __forceinline__ float append_scale(float a, float old, float* scale, float* mx) {
-  const int tid = threadIdx.x;
-#pragma unroll
-  for (int d = 16; d; d >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
-  if ((tid & 31) == 0) mx[tid >> 5] = a;
+__device__ __forceinline__ float append_scale(float a, float old, float* scale, uint32_t* mx) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  // (Numbers from 0 on are in the order of their bits.)
+  const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(a));
+  if (lane == 0) mx[tid >> 5] = most;
   __syncthreads();  // (and every thread has read the old scale)
-#pragma unroll 8
-  for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) a = fmaxf(a, mx[w]);
+  const uint32_t x = lane < static_cast<int>(blockDim.x) / 32 ? mx[lane] : 0;
+  a = __uint_as_float(__reduce_max_sync(0xffffffffu, x));
   const float s = fmaxf(kv_scale(a), old);
   if (tid == 0) *scale = s;
   return s;
@@ -111,65 +113,101 @@ __device__ __forceinline__ bool append_plain(float s) {
   return (u & 0x807fffffu) == 0 && u >= 0x00800000u && u <= 0x7e800000u;
 }
 
-// One head of a page, all that the registers' path leaves: the page's older tokens, brought from
-// scale `old` to s; the new tokens when s is no plain power of two; and, in a page whose new tokens
-// exceed the block's registers (`large`), its scale and tokens in two passes over the values.
+// A block's part of a row: keys (ROT) or values of heads h0 .. h1 - 1 in one page, the row's j-th,
+// of which the first `off` tokens are older.
+template <int P, bool ROT>
+struct AppendPart {
+  KvSrc src;
+  uint8_t* pool;
+  float* scales;
+  int b, j, h0, h1, len, n, off;
+  PagePart g;
+  __device__ __forceinline__ explicit AppendPart(const AppendRopeArgs& A) {
+    const KvCache& C = A.C;
+    b = blockIdx.y;
+    n = A.n_new ? kv_ld(A.n_new + b) : A.T;
+    len = kv_ld(C.len + b);
+    const int i = blockIdx.x - (ROT ? 0 : A.pages * A.chunks), chunk = i / A.pages;
+    j = (len >> C.lgp) + i - chunk * A.pages;
+    h0 = chunk * A.per;
+    h1 = min(h0 + A.per, C.heads);
+    src = ROT ? A.k : A.v;
+    pool = ROT ? C.k : C.v;
+    scales = ROT ? C.ks : C.vs;
+    const int lo = max(len, j << C.lgp), hi = min(len + n, (j + 1) << C.lgp);
+    g = PagePart{lo - len, hi - lo, C.dim / (2 * P), b * src.row};
+    off = lo - (j << C.lgp);
+  }
+};
+
+// What the registers' path leaves, head by head: a page's older tokens, brought from scale `old` to
+// the page's new one; the new tokens when that is no plain power of two; and, in a page whose new
+// tokens exceed the block's registers (`large`), its scale and tokens in two passes over the values.
+// (It finds out by itself what part the block has, so that nothing for it is kept in registers.)
 template <typename E, int P, bool INTER, bool ROT>
-__device__ __noinline__ void append_rest(const AppendRopeArgs& A, const KvSrc& src, const PagePart& g,
-                                         int h, RowPos pos, int off, uint8_t* dst, float* scale,
-                                         float old, bool large, float* mx) {
-  const int nu = g.count * g.units, step = static_cast<int>(blockDim.x);
-  float s;
-  if (large) {
-    old = off ? kv_ld(scale) : 0.f;
-    float a = 0.f;
-    bool odd = false;
+__device__ __noinline__ void append_rest(const AppendRopeArgs& A, const int* depth, const float* s_old,
+                                         uint32_t* s_max, bool large) {
+  const AppendPart<P, ROT> W(A);
+  const RowPos pos{W.len, depth};
+  const int nu = W.g.count * W.g.units, step = static_cast<int>(blockDim.x);
+  const int page = kv_page(A.C, W.b, W.j << A.C.lgp);
+  for (int h = W.h0; h < W.h1; ++h) {
+    uint8_t* dst = W.pool + kv_block(A.C, A.layer, page, h);
+    float* const scale = W.scales + kv_sidx(A.C, A.layer, page, h);
+    float old = s_old[h - W.h0];
+    float s;
+    if (large) {
+      old = W.off ? kv_ld(scale) : 0.f;
+      float a = 0.f;
+      bool odd = false;
+      for (int i = threadIdx.x; i < nu; i += step) {
+        float x[2 * P];
+        RopeUnit<P, INTER> unit(0, 0);
+        load_unit<E, P, INTER, ROT>(A, W.src, W.g, i, h, pos, x, &unit);
+        a = fmaxf(a, append_seen<P>(x, &odd));
+      }
+      if (odd) kv_report(A.S.hdr, ST_DEVICE_INPUT);
+      s = append_scale(a, old, scale, s_max + (h & 1) * 32);
+    } else {
+      s = kv_ld(scale);
+    }
+    if (W.off && s != old)
+      for (int i = threadIdx.x; i < W.off * A.C.dim / 16; i += step) {
+        uint4 x = reinterpret_cast<uint4*>(dst)[i];
+        uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) w[q] = kv_rescale4(w[q], old, s);
+        reinterpret_cast<uint4*>(dst)[i] = x;
+      }
+    if (!large && append_plain(s)) continue;
+    dst += (size_t)W.off * A.C.dim;
+    const bool pow2 = kv_pow2(s);
+    const float inv = pow2 ? 1.f / s : 1.f;
     for (int i = threadIdx.x; i < nu; i += step) {
       float x[2 * P];
       RopeUnit<P, INTER> unit(0, 0);
-      load_unit<E, P, INTER, ROT>(A, src, g, i, h, pos, x, &unit);
-      a = fmaxf(a, append_seen<P>(x, &odd));
-    }
-    if (odd) kv_report(A.S.hdr, ST_DEVICE_INPUT);
-    s = append_scale(a, old, scale, mx);
-  } else {
-    s = kv_ld(scale);
-  }
-  if (off && s != old)
-    for (int i = threadIdx.x; i < off * A.C.dim / 16; i += step) {
-      uint4 x = reinterpret_cast<uint4*>(dst)[i];
-      uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+      const int t = load_unit<E, P, INTER, ROT>(A, W.src, W.g, i, h, pos, x, &unit);
+      if (!pow2) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) w[q] = kv_rescale4(w[q], old, s);
-      reinterpret_cast<uint4*>(dst)[i] = x;
+        for (int e = 0; e < 2 * P; ++e) x[e] = kv_quotient(x[e], 1.f, s);
+      }
+      put_e4m3<P>(dst + (size_t)t * A.C.dim + unit.lo, x, inv);
+      put_e4m3<P>(dst + (size_t)t * A.C.dim + unit.hi, x + P, inv);
     }
-  if (!large && append_plain(s)) return;
-  dst += (size_t)off * A.C.dim;
-  const bool pow2 = kv_pow2(s);
-  const float inv = pow2 ? 1.f / s : 1.f;
-  for (int i = threadIdx.x; i < nu; i += step) {
-    float x[2 * P];
-    RopeUnit<P, INTER> unit(0, 0);
-    const int t = load_unit<E, P, INTER, ROT>(A, src, g, i, h, pos, x, &unit);
-    if (!pow2) {
-#pragma unroll
-      for (int e = 0; e < 2 * P; ++e) x[e] = kv_quotient(x[e], 1.f, s);
-    }
-    put_e4m3<P>(dst + (size_t)t * A.C.dim + unit.lo, x, inv);
-    put_e4m3<P>(dst + (size_t)t * A.C.dim + unit.hi, x + P, inv);
   }
 }
 
-// Keys or values of heads h0 .. h1 - 1 in one page, the row's j-th. ROT: they are rotated.
+// Keys (ROT) or values.
 template <typename E, int P, bool INTER, bool ROT>
-__device__ __forceinline__ void append_page(const AppendRopeArgs& A, const KvSrc& src, uint8_t* pool,
-                                            float* scales, int b, int j, int h0, int h1, int len,
-                                            int n, RowPos pos) {
-  __shared__ float s_max[2][32], s_old[AR_PER];
+__device__ __forceinline__ void append_page(const AppendRopeArgs& A, const int* depth) {
+  __shared__ uint32_t s_max[2][32];
+  __shared__ float s_old[AR_PER];
   const KvCache& C = A.C;
-  const int tid = threadIdx.x, lo = max(len, j << C.lgp), hi = min(len + n, (j + 1) << C.lgp);
-  const PagePart g{lo - len, hi - lo, C.dim / (2 * P), b * src.row};
-  const int nu = g.count * g.units, off = lo - (j << C.lgp), rot = ROT ? A.R.rot : 0;
+  const AppendPart<P, ROT> W(A);
+  const PagePart& g = W.g;
+  const KvSrc& src = W.src;
+  const int tid = threadIdx.x, nu = g.count * g.units, off = W.off, h0 = W.h0, h1 = W.h1;
+  const int rot = ROT ? A.R.rot : 0;
   constexpr int K = AR_VALUES / (2 * P);
   const E* const base = static_cast<const E*>(src.p) + g.row + (long long)g.t0 * src.tok;
   // Of this thread's units: the token, where its two vectors begin, and whether it is rotated.
@@ -180,51 +218,50 @@ __device__ __forceinline__ void append_page(const AppendRopeArgs& A, const KvSrc
   for (int k = 0; k < K; ++k) {
     const int i = tid + k * static_cast<int>(blockDim.x), t = i / g.units;
     const RopeUnit<P, INTER> unit(i - t * g.units, rot);
-    from[k] = base + (long long)t * src.tok + unit.lo;
+    from[k] = base + (long long)t * src.tok + (size_t)h0 * C.dim + unit.lo;
     to[k] = i < nu ? t * C.dim + unit.lo : -1;
     gap[k] = unit.hi - unit.lo;
     turns[k] = ROT && unit.turns;
   }
   float2 cs[ROT ? K : 1][P];
   RopeVec<E, P> raw[K][2];
-  auto fetch = [&](int h) {
+  auto fetch = [&]() {  // the next head's
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if (to[k] < 0) break;
-      const E* x = from[k] + (size_t)h * C.dim;
-      raw[k][0].load(x);
-      raw[k][1].load(x + gap[k]);
+      raw[k][0].load(from[k]);
+      raw[k][1].load(from[k] + gap[k]);
+      from[k] += C.dim;
     }
   };
   const bool large = nu > K * static_cast<int>(blockDim.x);
-  if (!large) fetch(h0);
+  if (!large) fetch();
   // (The tokens are on their way while the row's pages are looked up: is every one that it writes its
   // own?)
-  const int page = kv_page(C, b, j << C.lgp);
-  const bool fine = A.checked ? kv_ld(A.S.flag + b) != 0 : kv_append_holds(C, b, len, n);
+  const int page = kv_page(C, W.b, W.j << C.lgp);
+  const bool fine =
+      A.checked ? kv_ld(A.S.flag + W.b) != 0 : kv_append_holds(C, W.b, W.len, W.n);
   if (!__syncthreads_and(fine ? 1 : 0)) {
     if (tid == 0 && blockIdx.x == 0 && !A.checked) kv_report(A.S.hdr, ST_DEVICE_INPUT);
     return;
   }
   if (nu <= 0) return;
-  auto rest = [&](int h, float old) {
-    append_rest<E, P, INTER, ROT>(A, src, g, h, pos, off, pool + kv_block(C, A.layer, page, h),
-                                  scales + kv_sidx(C, A.layer, page, h), old, large, s_max[h & 1]);
-  };
   if (large) {
-    for (int h = h0; h < h1; ++h) rest(h, 0.f);
+    append_rest<E, P, INTER, ROT>(A, depth, s_old, s_max[0], true);
     return;
   }
   if constexpr (ROT) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int i = tid + k * static_cast<int>(blockDim.x), t = i / g.units;
-      if (i < nu && turns[k]) rope_turns<P>(A.R, pos(g.t0 + t), i - t * g.units, cs[k]);
+      if (i < nu && turns[k]) rope_turns<P>(A.R, RowPos{W.len, depth}(g.t0 + t), i - t * g.units, cs[k]);
     }
   }
   bool more = false;  // a scale has changed, or is no plain power of two
-  for (int h = h0; h < h1; ++h) {
-    float* const scale = scales + kv_sidx(C, A.layer, page, h);
+  float* scale = W.scales + kv_sidx(C, A.layer, page, h0);
+  uint8_t* out = W.pool + kv_block(C, A.layer, page, h0) + (size_t)off * C.dim;
+  const int block = C.page * C.dim;
+  for (int h = h0; h < h1; ++h, ++scale, out += block) {
     const float old = off ? kv_ld(scale) : 0.f;
     float f[K][2 * P], a = 0.f;
     uint32_t most = 0;  // of |x|, whose order as numbers is that of their bits, NaN above all
@@ -239,7 +276,7 @@ __device__ __forceinline__ void append_page(const AppendRopeArgs& A, const KvSrc
       for (int e = 0; e < 2 * P; e += 2)
         most = __vimax3_u32(most, __float_as_uint(fabsf(f[k][e])), __float_as_uint(fabsf(f[k][e + 1])));
     }
-    if (h + 1 < h1) fetch(h + 1);
+    if (h + 1 < h1) fetch();
     if (most <= __float_as_uint(KV_XMAX)) {
       a = __uint_as_float(most);
     } else {
@@ -252,7 +289,6 @@ __device__ __forceinline__ void append_page(const AppendRopeArgs& A, const KvSrc
     const float s = append_scale(a, old, scale, s_max[h & 1]);
     more = more || (off && s != old) || !append_plain(s);
     if (!append_plain(s)) continue;
-    uint8_t* const out = pool + kv_block(C, A.layer, page, h) + (size_t)off * C.dim;
     const float inv = __uint_as_float(0x7f000000u - __float_as_uint(s));  // 1 / s
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -263,7 +299,7 @@ __device__ __forceinline__ void append_page(const AppendRopeArgs& A, const KvSrc
   }
   if (more) {  // (the same in every thread)
     __syncthreads();
-    for (int h = h0; h < h1; ++h) rest(h, s_old[h - h0]);
+    append_rest<E, P, INTER, ROT>(A, depth, s_old, s_max[0], false);
   }
 }
 
@@ -294,17 +330,15 @@ __global__ void __launch_bounds__(AR_MOST)
     return;
   }
   if (bad || n == 0) return;
-  const int i = blockIdx.x - (values ? kv_blocks : 0);
-  const int chunk = i / A.pages, j = (len >> C.lgp) + i - chunk * A.pages;
   if (!kv_append_fits(C, len, n, T)) {
     if (tid == 0 && blockIdx.x == 0 && !A.checked) kv_report(A.S.hdr, ST_DEVICE_INPUT);
     return;
   }
-  const int h0 = chunk * A.per, h1 = min(h0 + A.per, C.heads);
+  const int* const depth = A.parent ? s_depth : nullptr;
   if (values)
-    append_page<E, 8, false, false>(A, A.v, C.v, C.vs, b, j, h0, h1, len, n, pos);
+    append_page<E, 8, false, false>(A, depth);
   else
-    append_page<E, P, INTER, true>(A, A.k, C.k, C.ks, b, j, h0, h1, len, n, pos);
+    append_page<E, P, INTER, true>(A, depth);
 }
 
 template <typename E>
