@@ -144,8 +144,8 @@ __global__ void __launch_bounds__(256) kv_share_rows_kernel(const KvCache C, con
 }
 
 // Joins the parts of every query tile of a row: its own keys' and, where it is in a group, those
-// of the common ones, in the order of the CTAs that made them. A thread takes four components of a
-// query. (A query tile with one part has its result already.)
+// of the common ones, in the order of the CTAs that made them. (A query tile with one part has its
+// result already.)
 constexpr int SJ_THREADS = 256;
 // (When a wait gave up, a query tile may have no span of this call: what is there is kept in range.)
 __device__ __forceinline__ KvSpan join_span(const KvSpan* p) {
