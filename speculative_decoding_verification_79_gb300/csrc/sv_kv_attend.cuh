@@ -201,25 +201,35 @@ __host__ __device__ constexpr int at_width(long long rows) {
   return rows <= 32 ? 32 : (rows <= 64 ? 64 : 128);
 }
 
-// Large groups are attended to by a kernel of their own, sv_kv_group.cu, in 1,850 cycles a key tile.
-constexpr int AT_LARGE_COST = 1850;
+// Large groups are attended to by a kernel of their own, sv_kv_group.cu, in 2,400 cycles a key tile.
+constexpr int AT_LARGE_COST = 2400;
 __device__ __forceinline__ bool at_large(const SharedArgs& A, long long rows) {
   return A.large && at_width(rows) == 128;
 }
 // Key tiles that a group of n rows has in common, or 0 when its rows are better off alone. Sharing
 // takes the group's query tiles, and for each row's own query tile results in parts, which are
-// written, read and joined: some 8,000 cycles and 200 a query (for 8 queries 17 us of 512 query
-// tiles, for 128 queries 66 us of 544). Four rows of 128 queries each gain nothing from it: trees of
-// 16 nodes of 8 queries on 3,000 common tokens took 226 us shared and 151 alone.
+// written, read and joined: some 3,000 cycles and 80 a query (10 us of 512 query tiles of 36
+// queries). Beside that the call is longer by 5 us with a second kind of work in its launch and by
+// 14 with another launch: what is gained in all (taking the groups to be alike) has to exceed that
+// on 152 SMs. Shared and alone, us, with 8 heads: four rows of 128 queries on 3,000 common tokens
+// 226 and 151 (such rows fill their products by themselves); 64 rows of 72 queries on 8,192, by
+// twos 327 and 311, by fours 261 and 310; of 36 by 32 on 2,048 79 and 89, on 768 70 and 60; of 8
+// by twos on 2,048 76 and 81, on 768 56 and 49; 8 rows of 36 by twos on 8,192 50 and 47.
 __device__ __forceinline__ int at_common(const SharedArgs& A, int n, int tokens) {
   const int keys = tokens / AT_KEYS;
   if (A.always) return keys;
+  // (A window leaves out what is between the row's start and it.)
+  const long long span = ((long long)A.window + AT_KEYS - 1) / AT_KEYS + ((long long)A.sinks + AT_KEYS - 1) / AT_KEYS + 1;
+  const int seen = A.window && span < keys ? static_cast<int>(span) : keys;
   const long long rows = (long long)A.T * A.group, all = n * rows;
   const long long tiles = n * ((rows + KV_ROWS - 1) / KV_ROWS);
-  const long long alone = tiles * at_cost(at_width(rows)) * keys;
-  const int cost = at_large(A, all) ? AT_LARGE_COST : at_cost(at_width(all));
-  const long long once = (all + KV_ROWS - 1) / KV_ROWS * cost * (long long)(keys + KV_EXTRA) + tiles * 8000 + 200 * all;
-  return alone > once ? keys : 0;
+  const long long alone = tiles * at_cost(at_width(rows)) * seen;
+  const bool large = at_large(A, all);
+  const int cost = large ? AT_LARGE_COST : at_cost(at_width(all));
+  const long long once =
+      (all + KV_ROWS - 1) / KV_ROWS * cost * (long long)(seen + KV_EXTRA) + tiles * 3000 + 80 * all;
+  const long long gain = (alone - once) * A.C.heads * kv_ld(A.H.head);
+  return gain > (large ? 152 * 27000LL : 152 * 10000LL) ? keys : 0;
 }
 __device__ __forceinline__ int at_skip(const AttendArgs&, int) { return 0; }
 __device__ __forceinline__ int at_skip(const SharedArgs& A, int b) {
