@@ -13,10 +13,13 @@
 // 128 with two accumulators each, which convert a V tile for both, took 4,400 to 5,800 cycles for a
 // key tile of the two, however its warps were divided: a chain is 3,500.)
 //
-// Bound by the weights: 16 warps' exponentials, largest values, conversions and tensor memory moves are
-// 775 to 880 cycles of a step when the warps are spread over it, and 1,250 to 1,500 as they run, all
-// at the same place, after the same barrier. 64 rows of 8 queries a head behind 8,100 common tokens
-// (8 heads): 30 us. 8 rows of 35 queries a head behind 120,001 (4 heads): 94 us, 0.73 PFLOP/s.
+// Bound by that chain: once it runs, a step takes 1,580 cycles (bf16) or 1,730 (fp16, three terms).
+// Products keep the tensor cores for 1,030 and 1,290 of them; the weights take 1,200 from scores seen
+// to weights stored (their instructions 830 if all warps' were spread evenly), and then wait some
+// 400 for the next scores, whose products waited for the outputs of three steps before. Tensor memory
+// has no room for a fourth accumulator. 64 rows of 8 queries a head behind 8,100 common tokens (8
+// heads, 14 steps a CTA): 30 us. 8 rows of 35 queries a head behind 120,001 (4 heads, 74 steps): 94
+// us, 0.73 PFLOP/s. With its start, queries and results that is 2,400 cycles a step.
 //
 // All of a group's queries see all of its common tokens (no window), so no key is masked, and a NaN
 // in the cache reaches all of them by itself: 0 times NaN is NaN.
