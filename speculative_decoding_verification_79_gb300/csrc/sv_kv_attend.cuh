@@ -215,21 +215,31 @@ __device__ __forceinline__ bool at_large(const SharedArgs& A, long long rows) {
 // 226 and 151 (such rows fill their products by themselves); 64 rows of 72 queries on 8,192, by
 // twos 327 and 311, by fours 261 and 310; of 36 by 32 on 2,048 79 and 89, on 768 70 and 60; of 8
 // by twos on 2,048 76 and 81, on 768 56 and 49; 8 rows of 36 by twos on 8,192 50 and 47.
+// (The warps that plan ask this for every query tile, in every kernel of the call with the same answer:
+// few instructions, each with its rounding said.)
+constexpr float AT_KIND = 152 * 10000.f, AT_LAUNCH = 152 * 27000.f;
 __device__ __forceinline__ int at_common(const SharedArgs& A, int n, int tokens) {
   const int keys = tokens / AT_KEYS;
   if (A.always) return keys;
-  // (A window leaves out what is between the row's start and it.)
-  const long long span = ((long long)A.window + AT_KEYS - 1) / AT_KEYS + ((long long)A.sinks + AT_KEYS - 1) / AT_KEYS + 1;
-  const int seen = A.window && span < keys ? static_cast<int>(span) : keys;
-  const long long rows = (long long)A.T * A.group, all = n * rows;
-  const long long tiles = n * ((rows + KV_ROWS - 1) / KV_ROWS);
-  const long long alone = tiles * at_cost(at_width(rows)) * seen;
+  const int seen = min(keys, A.reach), all = n * A.T * A.group;
   const bool large = at_large(A, all);
-  const int cost = large ? AT_LARGE_COST : at_cost(at_width(all));
-  const long long once =
-      (all + KV_ROWS - 1) / KV_ROWS * cost * (long long)(seen + KV_EXTRA) + tiles * 3000 + 80 * all;
-  const long long gain = (alone - once) * A.C.heads * kv_ld(A.H.head);
-  return gain > (large ? 152 * 27000LL : 152 * 10000LL) ? keys : 0;
+  const float cost = large ? AT_LARGE_COST : at_cost(at_width(all));
+  const float row = __fsub_rn(__fmul_rn(__int2float_rn(seen), A.row_cost), A.row_parts);
+  const float alone = __fmul_rn(__int2float_rn(n), row);
+  const float once = __fmul_rn(__fmul_rn(__int2float_rn((all + KV_ROWS - 1) / KV_ROWS), cost),
+                               __int2float_rn(seen + KV_EXTRA));
+  const float gain = __fmul_rn(__fsub_rn(alone, once), __int2float_rn(A.C.heads * kv_ld(A.H.head)));
+  return gain > (large ? AT_LAUNCH : AT_KIND) ? keys : 0;
+}
+// What the rule takes from a call: a row's cost a key tile and for its parts, key tiles that a query
+// sees at most (a window leaves out what is between the row's start and it).
+inline void at_rule(SharedArgs* A) {
+  const int rows = A->T * A->group;
+  A->row_cost = static_cast<float>(A->tiles) * static_cast<float>(at_cost(at_width(rows)));
+  A->row_parts = 3000.f * static_cast<float>(A->tiles) + 80.f * static_cast<float>(rows);
+  const long long span = ((long long)A->window + AT_KEYS - 1) / AT_KEYS +
+                         ((long long)A->sinks + AT_KEYS - 1) / AT_KEYS + 1;
+  A->reach = A->window && span < 0x7fffffff ? static_cast<int>(span) : 0x7fffffff;
 }
 __device__ __forceinline__ int at_skip(const AttendArgs&, int) { return 0; }
 __device__ __forceinline__ int at_skip(const SharedArgs& A, int b) {

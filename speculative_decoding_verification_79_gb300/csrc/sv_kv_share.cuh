@@ -25,6 +25,8 @@ struct SharedArgs : AttendArgs {
   int tiles;        // query tiles of a row at most
   int large;        // may large groups go to their own kernel?
   int always;       // is every group's common part shared (sv_set_share_always)?
+  float row_cost, row_parts;  // (see at_rule)
+  int reach;
   int own_rows;     // rows of a slot of partial results of rows
   KvSpan *own_span, *span;  // by query tile: of rows, of groups
   float *own_part, *part;
@@ -36,6 +38,6 @@ struct SharedArgs : AttendArgs {
 size_t kv_share_layout(const KvCache& C, int T, int group, unsigned char* base, SharedArgs* A);
 cudaError_t launch_kv_share(const KvCache& C, const KvScratch& S, const KvShare& H,
                             const int32_t* group, cudaStream_t st);
-cudaError_t launch_kv_attend_shared(const SharedArgs& A, sv_dtype dt, cudaStream_t st);
+cudaError_t launch_kv_attend_shared(SharedArgs& A, sv_dtype dt, cudaStream_t st);
 
 }  // namespace sv

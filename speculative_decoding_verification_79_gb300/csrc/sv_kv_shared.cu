@@ -315,7 +315,8 @@ cudaError_t launch_kv_share(const KvCache& C, const KvScratch& S, const KvShare&
   return e;
 }
 
-cudaError_t launch_kv_attend_shared(const SharedArgs& A, sv_dtype dt, cudaStream_t st) {
+cudaError_t launch_kv_attend_shared(SharedArgs& A, sv_dtype dt, cudaStream_t st) {
+  at_rule(&A);
   static const SharedKernel* const kernels[2][2] = {{shared_kernels_f16_1, shared_kernels_f16_2},
                                                     {shared_kernels_bf16_1, shared_kernels_bf16_2}};
   int dev = 0;
