@@ -529,3 +529,29 @@ def test_binding_refusals(sv, always):
             f()
     assert sv.sv_kv_attend_shared(g, 0, q[:, :0], share).shape == (B, 0, 8, 64)
     assert g.status() == sv.SV_OK
+
+
+@needs_cuda
+@pytest.mark.parametrize("T,heads,group,dim,page,window", [
+    (150, 1, 8, 64, 16, 0), (150, 2, 3, 128, 64, 0), (131, 1, 2, 192, 32, 300), (300, 1, 1, 80, 128, 0)])
+def test_prompts_behind_common_tokens(sv, T, heads, group, dim, page, window):
+    """Questions of many tokens on one document: several query tiles a row, the last ones short."""
+    case(sv, [(2, 700), (3, 260)], [90], [40, 3], T, heads, group, dim, page, window=window, seed=T,
+         n=[T, 1, T - 1, 129, T, 7])
+
+
+@needs_cuda
+def test_one_row(sv):
+    """The smallest batch, alone and named a group of its own."""
+    for by_page in (False, True):
+        case(sv, [], [300], [9], 3, 2, 4, 64, 16, seed=1, by_page=by_page, n=[3])
+    case(sv, [(1, 300)], [], [9], 1, 1, 1, 16, 16, seed=2, n=[1])
+
+
+@needs_cuda
+@pytest.mark.parametrize("dim,window", [(32, 0), (160, 0), (64, 15000)])
+def test_some_groups_gain(sv, dim, window):
+    """One call in which sharing pays for one group and not for the others, in the kernel for large
+    groups, beside the rows, and under a window."""
+    case(sv, [(16, 20000), (2, 300), (3, 140)], [77], [3, 130, 60], 1, 8, 8, dim, 128, seed=dim,
+         window=window, n=[1] * 22, rows=[0, 1, 2, 3, 7, 20, 21])
