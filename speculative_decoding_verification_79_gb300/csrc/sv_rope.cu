@@ -2,14 +2,15 @@
 //
 // A block takes tokens of one row; a thread P pairs of one token in up to 8 heads. Bound by
 // memory: every value is read and written once; the 8 cosines and sines of a thread are some 300
-// instructions, spread over its heads. 8 x 4,093 tokens of 32 heads of 128 in bf16: 80.5 us, 537 MB
-// at 6.7 TB/s. 4 x 2,047 tokens of 12 heads of 80 in float32, interleaved: 13.7 us, 63 MB at 4.6;
-// one token: 2.8 us, a launch.
+// instructions, spread over its heads. 8 x 4,093 tokens of 32 heads of 128 in bf16: 80.4 us, 537 MB
+// at 6.7 TB/s. 4 x 2,047 tokens of 12 heads of 80 in float32, interleaved: 13.1 us, 63 MB at 4.8;
+// one token: 2.5 us, a launch. (Blocks of 256 threads: 80.7, 13.7 and 2.9 us. Two heads' loads in
+// flight instead of four: 85 for the first; 64 registers: 87.)
 #include "sv_rope.cuh"
 
 namespace sv {
 
-constexpr int ROPE_THREADS = 256;
+constexpr int ROPE_THREADS = 128;
 
 template <typename E, int P, bool INTER>
 __global__ void __launch_bounds__(ROPE_THREADS)
