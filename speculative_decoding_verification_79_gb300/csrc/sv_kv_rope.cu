@@ -24,8 +24,9 @@ namespace sv {
 // Threads of a block: one for 16 values of the new tokens of a page, in whole warps, as far as that
 // goes. (The queries in a launch of their own: those prompts 149 us instead of 140, as it was then,
 // trees 15.2 instead of 10.8. Twice or four times as many blocks, of fewer heads each: 153 and 167
-// us, the cosines being computed again.)
-constexpr int AR_LEAST = 128, AR_MOST = 1024;
+// us, the cosines being computed again. At least 32, 64, 128 and 256 threads: 7.1, 6.7, 7.8 and 8.7
+// us for a token of 64 rows with 64 query heads, appended and read.)
+constexpr int AR_LEAST = 64, AR_MOST = 1024;
 constexpr int AR_VALUES = 16;  // of a page and head that a thread keeps in registers
 constexpr int AR_PER = 32;     // heads of a block
 
