@@ -306,6 +306,7 @@ size_t kv_share_layout(const KvCache& C, int T, int group, unsigned char* base, 
   A->H.group = reinterpret_cast<int4*>(take(16 * (B / 2 + 1)));
   A->H.order = reinterpret_cast<int32_t*>(take(4 * B));
   A->H.bad = reinterpret_cast<int32_t*>(take(4 * B));
+  A->H.ready = reinterpret_cast<uint32_t*>(take(4 * KV_MAX_CTAS));
   const size_t rows = (size_t)T * group;
   A->tiles = static_cast<int>((rows + KV_ROWS - 1) / KV_ROWS);
   A->own_rows = rows < KV_ROWS ? static_cast<int>((rows + 7) / 8 * 8) : KV_ROWS;
@@ -351,12 +352,12 @@ cudaError_t launch_kv_attend_shared(SharedArgs& A, sv_dtype dt, cudaStream_t st)
   AttendLaunch L;
   if ((e = at_launch(A, dt, at_width((long long)A.T * A.group), dev, &L)) != cudaSuccess) return e;
   const SharedKernel kernel = kernels[dt == SV_BF16][L.ndb - 1][L.width == 32 ? 0 : (L.width == 64 ? 1 : 2)];
+  // (No group has more rows than the batch.)
+  const bool groups = A.large && at_width((long long)A.C.batch * A.T * A.group) == 128;
+  A.ready = groups ? A.H.ready : nullptr;
   if ((e = kv_launch(kernel, dim3(L.grid), AT_THREADS, L.smem, st, A, L.P, L.tm[0], L.tm[1])) != cudaSuccess)
     return e;
-  // (No group has more rows than the batch.)
-  if (A.large && at_width((long long)A.C.batch * A.T * A.group) == 128 &&
-      (e = launch_kv_attend_group(A, L, dt, dev, st)) != cudaSuccess)
-    return e;
+  if (groups && (e = launch_kv_attend_group(A, L, dt, dev, st)) != cudaSuccess) return e;
   const long long eights = ((long long)A.C.batch * A.tiles * A.C.heads + L.grid) * (A.own_rows / 8);
   const long long warps = eights * ((A.C.dim / 4 + 15) / 16);
   const long long blocks = (warps + SJ_THREADS / 32 - 1) / (SJ_THREADS / 32);

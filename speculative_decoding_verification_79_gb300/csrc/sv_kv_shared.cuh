@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   __shared__ int s_sum[AT_THREADS / 32];
   auto& sh = reinterpret_cast<AtShared<AT_OWN, W>&>(raw);
   at_setup(sh);
-  kv_enter();
+  kv_enter_ready(A.ready);
   const long long most = (long long)kv_ld(A.H.head + 1) * A.T * A.group;  // queries of the largest group
   const int rows = at_width(most), grid = gridDim.x;
   const AtCount own = at_count<AT_OWN>(A, sh.rows);
