@@ -60,3 +60,77 @@ def test_flags_between_launches(sv, always):  # noqa: F811
     torch.cuda.synchronize()
     assert not flags(s, B).any()
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1]) and g.status() == sv.SV_OK
+
+
+@needs_cuda
+def test_groups_of_very_different_sizes(sv, always):  # noqa: F811
+    """One group of 2,048 rows beside 1,024 of two, with as many queries as the call takes: groups
+    times the largest one's query tiles pass 2^31. Rows of each kind against float64."""
+    if torch.cuda.get_device_properties(0).total_memory < 160 << 30:
+        pytest.skip("needs 95 GB of device memory")
+    rows, T, heads, dim, page = 4096, 1024, 128, 16, 128
+    g = sv.KVCache(1, 1025 + 8, page, 1, dim, rows, 2)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    for pool in (g.k, g.v):
+        pool.copy_(torch.randn(pool.shape, generator=gen, device="cuda").to(torch.float8_e4m3fn))
+    own = torch.arange(rows, dtype=torch.int32, device="cuda")
+    number = torch.where(own < 2048, 0, own // 2 - 1023).int()  # 0, then 1 .. 1024
+    live = {0: 3, 2047: 1, 2048: 2, 3071: T, 4094: 5, 4095: 4}
+    n_new = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    g.table[:, 0], g.table[:, 1] = number, -1
+    g.n_pages.fill_(1)
+    g.len.fill_(page)
+    g.refs.fill_(1)
+    for i, (b, n) in enumerate(live.items()):  # (a row of T tokens has room for 128)
+        n_new[b] = live[b] = min(n, 128)
+        g.table[b, 1], g.n_pages[b] = 1025 + i, 2
+    q = torch.randn(1, T, heads, dim, generator=gen, device="cuda").to(BF).expand(rows, -1, -1, -1)
+    share = sv.KVShare(g, T, heads)
+    sv.sv_kv_share(g, share, number)
+    got = sv.sv_kv_attend_shared(g, 0, q, share, n_new=n_new)
+    assert g.status() == sv.SV_OK
+    for b, n in live.items():
+        k, v = (torch.cat([x[0, p, 0] for p in g.table[b].tolist()]).double() for x in (g.k, g.v))
+        for t in range(n):
+            seen = page + t + 1
+            w = torch.softmax(q[b, t].double() @ k[:seen].T * dim ** -0.5, -1)
+            want, size = w @ v[:seen], w @ v[:seen].abs()
+            # Half a step of bf16, weights off by 2^-11 of themselves or 2^-28 of the largest, and a
+            # margin of as much for the scores' and sums' float32.
+            err = (got[b, t].double() - want).abs()
+            assert (err <= 2.0 ** -8 * want.abs() + 2.0 ** -10 * size + 2.0 ** -27 * seen).all()
+    del got, share
+    torch.cuda.empty_cache()
+
+
+@needs_cuda
+@pytest.mark.parametrize("dim,window", [(32, 0), (160, 0), (32, 300)])
+def test_one_large_group_beside_many_small(sv, always, dim, window):  # noqa: F811
+    """Groups whose query tiles are found by number, in each kernel that takes groups, against the
+    plain call: bf16 results of one sum in two orders, a step of bf16 (2^-7 of the value) and the
+    weights' bound on what the values, up to 4.5, add up to, 2^-9 each way."""
+    rows, T, group, page, common = 600 + 2 * 150, 3, 8, 16, 256
+    shared, per = common // page, common // page + 1
+    g = sv.KVCache(1, shared * 151 + rows, page, 1, dim, rows, per)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    g.k.copy_((0.5 * torch.randn(g.k.shape, generator=gen, device="cuda")).to(torch.float8_e4m3fn))
+    g.v.copy_(torch.randn(g.v.shape, generator=gen, device="cuda").to(torch.float8_e4m3fn))
+    own = torch.arange(rows, dtype=torch.int32, device="cuda")
+    number = torch.where(own % 3 == 0, own // 6 + 1, 0).int()  # pairs between the others
+    g.table[:, :shared] = (number[:, None] * shared + torch.arange(shared, device="cuda")).int()
+    g.table[:, shared] = shared * 151 + own
+    g.n_pages.fill_(per)
+    g.len.copy_(common + own % 10)
+    g.refs.fill_(1)
+    q = torch.randn(rows, T, group, dim, generator=gen, device="cuda").to(BF)
+    n_new = (1 + own % 3).int()
+    kw = dict(n_new=n_new, window=window, sinks=5, want_lse=True)
+    share = sv.KVShare(g, T, group)
+    sv.sv_kv_share(g, share, number)
+    got = sv.sv_kv_attend_shared(g, 0, q, share, **kw)
+    want = sv.sv_kv_attend(g, 0, q, **kw)
+    err = (got[0].float() - want[0].float()).abs()
+    assert (err <= 2 ** -7 * want[0].float().abs() + 4.5 * 2 ** -8).all()
+    new = torch.arange(T, device="cuda") < n_new[:, None]
+    assert ((got[1] - want[1])[new].abs() <= 2 ** -9).all() and (got[1][~new] == want[1][~new]).all()
+    assert g.status() == sv.SV_OK
