@@ -505,14 +505,14 @@ sv_status sv_kv_attend(const sv_kv_cache *cache, int layer, const void *q_d, sv_
  *             sv_kv_fork says so), -1: a row is alone. NULL: rows whose first page is the same.
  *             Another number sets SV_ERR_DEVICE_INPUT and leaves the row alone.
  * sv_kv_share finds what the rows of each group have in common: the leading pages that are the same
- * in all of them and full of each one's cached tokens, cut to a multiple of 128 tokens. It holds
- * for every layer, and until rows are forked, freed or shortened: reserving, appending
- * and committing more tokens does not change it.
+ * in all of them and full of each one's cached tokens, cut to a multiple of 128 tokens, and keeps
+ * their numbers. It holds for every layer, and until rows are forked, freed or shortened: reserving,
+ * appending and committing more tokens does not change it.
  * sv_kv_attend_shared takes what sv_kv_attend takes and gives the same up to the order of its
  * float32 sums. Rows of a group that has little in common, or that gains nothing from it (128
  * queries and more a row fill their products by themselves), are attended to one by one. Where a
- * group's common tokens are read once, its rows' pages are compared again: a row that no longer
- * holds them gets NaN in out and lse, in this call and all others until the next sv_kv_share, and
+ * group's common tokens are read once, its rows' pages are compared with those found: a row that no
+ * longer holds them (any of the group's, the others are not touched by it) gets NaN in out and lse, in this call and all others until the next sv_kv_share, and
  * sets SV_ERR_DEVICE_INPUT.
  * sv_set_share_always(1) has every group's common tokens read once, whether that is faster or not;
  * returns what was set before (a testing aid, for the whole process).

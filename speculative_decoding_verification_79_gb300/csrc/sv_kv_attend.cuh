@@ -190,7 +190,6 @@ struct AtRow {
   int len, n;    // cached and new tokens; n = 0 when the row's data is wrong
   int rows;      // query rows of a head
   int nrt, rr;   // query tiles, rows of each (the last may have fewer)
-  int lead;      // row whose pages are read
   int skip;      // first key tiles that are left to the group
   bool bad;
 };
@@ -258,12 +257,10 @@ __device__ __forceinline__ AtRow at_row(const Args& A, int b) {
     r.rows = keys ? x.y * A.T * A.group : 0;
     r.nrt = (r.rows + KV_ROWS - 1) / KV_ROWS;
     r.rr = r.nrt ? (r.rows + r.nrt - 1) / r.nrt : 0;
-    r.lead = x.w;
     r.skip = 0;
     r.bad = false;
     return r;
   }
-  r.lead = b;
   r.skip = M == AT_OWN ? at_skip(A, b) : 0;
   r.len = kv_ld(A.C.len + b);
   r.n = A.n_new ? kv_ld(A.n_new + b) : A.T;
@@ -276,6 +273,16 @@ __device__ __forceinline__ AtRow at_row(const Args& A, int b) {
   r.nrt = (r.rows + KV_ROWS - 1) / KV_ROWS;
   r.rr = r.nrt ? (r.rows + r.nrt - 1) / r.nrt : 0;
   return r;
+}
+
+// The page of a row's token at `key` (of a group: one of those that it shares), -1 when out of range.
+template <AtMode M, typename Args>
+__device__ __forceinline__ int at_page(const Args& A, int b, int key) {
+  if constexpr (M == AT_GROUPS) {
+    const int p = kv_ld(A.H.pages + (size_t)b * A.C.max_pages + (key >> A.C.lgp));
+    return p >= 0 && p < A.C.pages ? p : -1;
+  }
+  return kv_page(A.C, b, key);
 }
 
 // Query tile rt of a row: rows r0 .. r1 - 1, and the key tiles that any of them sees:
@@ -905,8 +912,7 @@ static __device__ __noinline__ void at_check_groups(const SharedArgs& A, int war
     const int4 x = kv_ld(A.H.row + b);
     const int pages = x.x < 0 ? 0 : at_common(A, x.y, x.z) << (7 - C.lgp);
     if (from >= pages) continue;
-    const int lead = kv_ld(A.H.group + x.x).w;
-    const int32_t *mine = C.table + (size_t)b * C.max_pages, *its = C.table + (size_t)lead * C.max_pages;
+    const int32_t *mine = C.table + (size_t)b * C.max_pages, *its = A.H.pages + (size_t)x.x * C.max_pages;
     bool bad = pages > kv_ld(C.np + b) || pages > C.max_pages || pages << C.lgp > kv_ld(C.len + b);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -1003,7 +1009,7 @@ __device__ __forceinline__ int at_copy_keys(const Args& A, int nk, const CUtenso
     n = min(tpc, walk.i1 - i);
     const int key = (mt < n ? walk.tile.key_tile(i + mt) : 0) * AT_KEYS + (sub << C.lgp);
     used = mt < n && key < walk.tile.end;
-    page = used ? kv_page(C, walk.row.lead, key) : -1;
+    page = used ? at_page<M>(A, walk.b, key) : -1;
     if (tmV && page >= 0)
       for (int db = 0; db < ndb; ++db) {
         at_prefetch(&tmK, db * 128, (page * C.heads + h) << C.lgp);

@@ -14,10 +14,11 @@ struct KvSpan {
 struct KvShare {
   int32_t* head;   // number of groups, rows of the largest
   int4* row;       // [batch] group (-1: alone), its rows, its tokens, the row's place in it
-  int4* group;     // [batch / 2] first row in `order`, rows, tokens, the row whose pages are read
+  int4* group;     // [batch / 2] first row in `order`, rows, tokens, its lowest row
   int32_t* order;  // [batch] rows by group
   int32_t* bad;    // [batch] set when a row's pages are no longer those of its group
   uint32_t* ready; // [KV_MAX_CTAS] see kv_enter_ready; 0 between calls
+  int32_t* pages;  // [batch / 2, max_pages] the pages that a group's tokens are in
 };
 constexpr int KV_SHARE_HEAD = 64;
 

@@ -12,13 +12,15 @@ static_assert(SV_MAX_B <= SH_MOST, "a CTA sorts all rows");
 
 // How many tokens every row of a group has in common: whole tiles of 128 on pages that are the same
 // in all of them, and no more than any row holds. A warp compares a row, the i-th in `order`, with
-// its group's first.
+// its group's lowest, and writes that one's pages down: they are the group's from then on, whatever
+// becomes of the row.
 __device__ __forceinline__ void share_pages(const KvCache& C, const KvShare& H, int i) {
   const int lane = threadIdx.x & 31;
   const int b = kv_ld(H.order + i), g = kv_ld(H.row + b).x, lead = kv_ld(H.group + g).w;
   const int len = max(0, kv_ld(C.len + b));
   const int pages = min(min(kv_ld(C.np + b), C.max_pages), len >> C.lgp);
   const int32_t *mine = C.table + (size_t)b * C.max_pages, *its = C.table + (size_t)lead * C.max_pages;
+  int32_t* const kept = H.pages + (size_t)g * C.max_pages;
   int common = max(pages, 0);
   for (int j0 = 0; j0 < common; j0 += 128) {
     unsigned differ[4];
@@ -29,6 +31,7 @@ __device__ __forceinline__ void share_pages(const KvCache& C, const KvShare& H, 
       if (!d) {
         const int p = kv_ld(mine + j);
         d = p < 0 || p >= C.pages || p != kv_ld(its + j);
+        if (b == lead) kept[j] = p;
       }
       differ[k] = __ballot_sync(0xffffffffu, d);
     }
@@ -307,6 +310,7 @@ size_t kv_share_layout(const KvCache& C, int T, int group, unsigned char* base, 
   A->H.order = reinterpret_cast<int32_t*>(take(4 * B));
   A->H.bad = reinterpret_cast<int32_t*>(take(4 * B));
   A->H.ready = reinterpret_cast<uint32_t*>(take(4 * KV_MAX_CTAS));
+  A->H.pages = reinterpret_cast<int32_t*>(take(4 * (B / 2) * C.max_pages));
   const size_t rows = (size_t)T * group;
   A->tiles = static_cast<int>((rows + KV_ROWS - 1) / KV_ROWS);
   A->own_rows = rows < KV_ROWS ? static_cast<int>((rows + 7) / 8 * 8) : KV_ROWS;

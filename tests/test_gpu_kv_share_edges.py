@@ -134,3 +134,39 @@ def test_one_large_group_beside_many_small(sv, always, dim, window):  # noqa: F8
     new = torch.arange(T, device="cuda") < n_new[:, None]
     assert ((got[1] - want[1])[new].abs() <= 2 ** -9).all() and (got[1][~new] == want[1][~new]).all()
     assert g.status() == sv.SV_OK
+
+
+@needs_cuda
+@pytest.mark.parametrize("which", ["first", "last"])
+@pytest.mark.parametrize("what", ["table", "len", "n_pages", "freed", "longer prompt", "shorter prompt"])
+def test_rows_that_change(sv, always, what, which):  # noqa: F811
+    """Any row of a group may change, its lowest too: that row is NaN, and the others, which still
+    hold the group's pages, are right."""
+    T, groups, tails = 6, [(5, 2000), (3, 400), (2, 2600)], [20, 60]
+    both, lead = grouped(sv, groups, [90], tails, 2, 64, 16, T)
+    g, B = both.g, both.r.batch
+    share = sv.KVShare(g, T, 8)
+    sv.sv_kv_share(g, share, i32(lead))
+    size = {x: lead.count(x) for x in lead}
+    mine = next(x for x in lead if size[x] == 5)
+    bad = mine if which == "first" else max(b for b in range(B) if lead[b] == mine)
+    other = next(x for x in lead if size[x] == (2 if what == "longer prompt" else 3))
+    if what in ("freed", "longer prompt", "shorter prompt"):
+        src = list(range(B))
+        src[bad] = -1 if what == "freed" else other
+        assert all(both.fork(src))
+    n = [T] * B
+    n[bad] = 0 if what == "freed" else T
+    block(both, T, 3, n)
+    if what == "table":
+        g.table[bad, 3] = int(g.table[bad, 126])
+    if what == "len":
+        g.len[bad] = 30
+    if what == "n_pages":
+        g.n_pages[bad] = 2
+    q = queries(both, T, 4, BF, 8)
+    for _ in range(2):
+        out, lse = sv.sv_kv_attend_shared(g, 0, q, share, n_new=i32(n), want_lse=True)
+        assert g.status(clear=True) == sv.SV_ERR_DEVICE_INPUT
+        assert torch.isnan(out[bad].float()).all() and torch.isnan(lse[bad]).all()
+        check_attend(both, 0, q, n, got=(out, lse), rows=[b for b in range(B) if b != bad])
