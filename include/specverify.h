@@ -512,8 +512,9 @@ sv_status sv_kv_attend(const sv_kv_cache *cache, int layer, const void *q_d, sv_
  * float32 sums. Rows of a group that has little in common, or that gains nothing from it (128
  * queries and more a row fill their products by themselves), are attended to one by one. Where a
  * group's common tokens are read once, its rows' pages are compared with those found: a row that no
- * longer holds them (any of the group's, the others are not touched by it) gets NaN in out and lse, in this call and all others until the next sv_kv_share, and
- * sets SV_ERR_DEVICE_INPUT.
+ * longer holds them (any of the group's; the others are not touched by it) sets SV_ERR_DEVICE_INPUT
+ * and gets NaN in all of its out and lse, in this call and in every other that reads the group's
+ * tokens once, until the next sv_kv_share.
  * sv_set_share_always(1) has every group's common tokens read once, whether that is faster or not;
  * returns what was set before (a testing aid, for the whole process).
  */

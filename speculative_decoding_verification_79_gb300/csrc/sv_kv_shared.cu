@@ -209,24 +209,29 @@ __global__ void __launch_bounds__(SJ_THREADS, 2)
     if (b >= A.C.batch) return;
     const int rt = static_cast<int>(bt - (long long)b * A.tiles);
     const AtRow row = at_row<AT_OWN>(A, b);
-    r0 = rt * row.rr;
-    R = min(r0 + row.rr, row.rows) - r0;
-    if (!row.skip || rt >= row.nrt || 8 * chunk >= R) return;
-    no = at_tile_no(A, AT_OWN, b, rt, h);
-    const KvSpan own = join_span(A.own_span + no);
-    no += own.first;
-    owns = own.last - own.first + 1;
-    const int4 mine = kv_ld(A.H.row + b);
-    const AtRow group = at_row<AT_GROUPS>(A, mine.x);
-    const int i = mine.w * A.T * A.group + r0 + min(r, R - 1), grt = i / group.rr;
-    gr = i - grt * group.rr;
-    if (!A.window || at_tile<AT_GROUPS>(A, group, mine.x, grt).tiles() > 0) {
-      id = at_tile_no(A, AT_GROUPS, mine.x, grt, h);
-      const KvSpan span = join_span(A.span + id);
-      count = span.last - span.first + 1;
-      id += span.first;
-    }
+    if (!row.skip) return;
     bad = kv_ld(A.H.bad + b) != 0;
+    // (Of a row that is NaN all queries, new tokens or not: 128 to a query tile.)
+    r0 = rt * (bad ? KV_ROWS : row.rr);
+    R = min(r0 + (bad ? KV_ROWS : row.rr), bad ? A.T * A.group : row.rows) - r0;
+    if ((rt >= row.nrt && !bad) || 8 * chunk >= R) return;
+    no = owns = 0;
+    if (!bad) {
+      no = at_tile_no(A, AT_OWN, b, rt, h);
+      const KvSpan own = join_span(A.own_span + no);
+      no += own.first;
+      owns = own.last - own.first + 1;
+      const int4 mine = kv_ld(A.H.row + b);
+      const AtRow group = at_row<AT_GROUPS>(A, mine.x);
+      const int i = mine.w * A.T * A.group + r0 + min(r, R - 1), grt = i / group.rr;
+      gr = i - grt * group.rr;
+      if (!A.window || at_tile<AT_GROUPS>(A, group, mine.x, grt).tiles() > 0) {
+        id = at_tile_no(A, AT_GROUPS, mine.x, grt, h);
+        const KvSpan span = join_span(A.span + id);
+        count = span.last - span.first + 1;
+        id += span.first;
+      }
+    }
   }
   if (r >= R) return;
   const int slots = count + owns;

@@ -170,3 +170,36 @@ def test_rows_that_change(sv, always, what, which):  # noqa: F811
         assert g.status(clear=True) == sv.SV_ERR_DEVICE_INPUT
         assert torch.isnan(out[bad].float()).all() and torch.isnan(lse[bad]).all()
         check_attend(both, 0, q, n, got=(out, lse), rows=[b for b in range(B) if b != bad])
+
+
+@needs_cuda
+@pytest.mark.parametrize("T,group,live", [(6, 4, 2), (6, 4, 0), (40, 8, 30), (40, 8, 0), (3, 2, 3)])
+def test_changed_rows_are_nan_throughout(sv, always, T, group, live):  # noqa: F811
+    """A row that changed is NaN in all tokens, new or not, like rows with other wrong data; in calls
+    that attend to its group one by one it has its own results."""
+    both, lead = grouped(sv, [(5, 2000), (3, 400)], [90], [20, 60], 2, 64, 16, T)
+    g, B = both.g, both.r.batch
+    share = sv.KVShare(g, T, 2 * group)
+    sv.sv_kv_share(g, share, i32(lead))
+    bad = max(b for b in range(B) if lead.count(lead[b]) == 5)
+    n = [max(1, T - b) for b in range(B)]
+    n[bad] = live
+    block(both, T, 3, n)
+    other = int(g.table[bad, 126])
+    old = int(g.table[bad, 3])
+    q = queries(both, T, group, BF, 8)
+    kw = dict(n_new=i32(n), want_lse=True)
+    g.table[bad, 3] = other
+    out, lse = sv.sv_kv_attend_shared(g, 0, q, share, **kw)
+    assert g.status(clear=True) == sv.SV_ERR_DEVICE_INPUT
+    assert torch.isnan(out[bad].float()).all() and torch.isnan(lse[bad]).all()
+    check_attend(both, 0, q, n, got=(out, lse), rows=[b for b in range(B) if b != bad])
+    g.table[bad, 3] = old
+    out, lse = sv.sv_kv_attend_shared(g, 0, q, share, **kw)
+    assert torch.isnan(out[bad].float()).all() and torch.isnan(lse[bad]).all()
+    # (Numbers of their own: the call reads nobody's tokens once.)
+    fresh = sv.KVShare(g, T, 2 * group)
+    check_attend(both, 0, q, n, got=sv.sv_kv_attend_shared(g, 0, q, fresh, **kw))
+    sv.sv_kv_share(g, share, i32(lead))
+    check_attend(both, 0, q, n, got=sv.sv_kv_attend_shared(g, 0, q, share, **kw))
+    assert g.status() == sv.SV_OK
