@@ -586,7 +586,8 @@ typedef enum sv_rope_scaling {
  * sv_rope_fixed: n angles per position (radians, finite) as the frequencies of sv_rope_spec.
  * sv_rope_freqs: the rot / 2 frequencies of a scaling. stretch > 0; original > 0 and
  * 0 < low < high for SV_ROPE_TURNS and SV_ROPE_INDEX, else not used; base > 1.
- * Both on host memory, without a GPU.
+ * Both round once, to the nearest 2^-64 of a turn (angles of up to 10^6 turns, bases up to 10^250):
+ * at position P an angle is off by P 2^-65 of a turn. On host memory, without a GPU.
  */
 sv_status sv_rope_fixed(const double *angle, int n, int64_t *freq_out);
 sv_status sv_rope_freqs(int rot, double base, sv_rope_scaling scaling, double stretch,

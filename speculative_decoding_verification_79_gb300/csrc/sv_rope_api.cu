@@ -12,11 +12,54 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 
 constexpr double TWO_PI = 6.283185307179586476925;
 
-// Turns per position as a fraction of 2^64. (The whole turns of a frequency make none.)
-int64_t fixed(double angle) {
-  const double turns = angle / TWO_PI, part = turns - std::floor(turns);
-  if (!(part < 1.0)) return 0;  // (a tiny negative angle, rounded up)
-  return static_cast<int64_t>(static_cast<uint64_t>(std::ldexp(part, 64)));
+// Frequencies are rounded once, to 2^-64 of a turn, from sums of two doubles (some 100 bits): a
+// double's own 2^-56 of a turn would be 2^-25 of one at position 2^31. (Not long double, which has
+// other sizes on other machines.)
+struct Two {
+  double hi, lo;
+};
+Two two_sum(double a, double b) {
+  const double s = a + b, t = s - a;
+  return Two{s, (a - (s - t)) + (b - t)};
+}
+Two operator+(Two a, Two b) {
+  const Two s = two_sum(a.hi, b.hi);
+  return two_sum(s.hi, s.lo + (a.lo + b.lo));
+}
+Two operator*(Two a, Two b) {
+  const double p = a.hi * b.hi;
+  return two_sum(p, std::fma(a.hi, b.hi, -p) + (a.hi * b.lo + a.lo * b.hi));
+}
+Two operator/(Two a, Two b) {
+  const double q = a.hi / b.hi;
+  const Two r = a + Two{-q, 0.0} * b;
+  return two_sum(q, r.hi / b.hi);
+}
+Two one(double x) { return Two{x, 0.0}; }
+// e^x for |x| <= 710, x / 2^20 by its series (ten terms: 10^-35) and the square of that 20 times.
+Two exp_two(Two x) {
+  const Two r{std::ldexp(x.hi, -20), std::ldexp(x.lo, -20)};
+  Two y = one(1.0);
+  for (int k = 10; k; --k) y = one(1.0) + r * y / one(k);
+  for (int k = 0; k < 20; ++k) y = y * y;
+  return y;
+}
+// ln x of 1 < x: a step of Newton's method on e^y = x from the double.
+Two log_two(double x) {
+  const double y = std::log(x);
+  return one(y) + (one(x) * exp_two(one(-y)) + one(-1.0));
+}
+
+// Turns per position of an angle (radians) as a fraction of 2^64. (Whole turns make none.)
+int64_t fixed(Two angle) {
+  const Two turns = angle * Two{0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57};  // 1 / 2 pi
+  const double whole = turns.hi - std::nearbyint(turns.hi), rest = turns.lo - std::nearbyint(turns.lo);
+  // Both in units of 2^-64, rounded together; what passes 2^32 is carried.
+  const double up = std::floor(std::ldexp(whole, 32));
+  const double low = std::nearbyint(std::ldexp(std::ldexp(whole, 32) - up, 32) + std::ldexp(rest, 64));
+  const double carry = std::floor(std::ldexp(low, -32));
+  return static_cast<int64_t>((static_cast<uint64_t>(static_cast<int64_t>(up + carry)) << 32) +
+                              static_cast<uint64_t>(low - std::ldexp(carry, 32)));
 }
 
 bool spec_ok(const sv_rope_spec* r, int dim) {
@@ -51,7 +94,7 @@ sv_status sv_rope_fixed(const double* angle, int n, int64_t* freq_out) {
   if (n && (!angle || !freq_out)) return SV_ERR_ARG;
   for (int i = 0; i < n; ++i)
     if (!std::isfinite(angle[i])) return SV_ERR_ARG;
-  for (int i = 0; i < n; ++i) freq_out[i] = fixed(angle[i]);
+  for (int i = 0; i < n; ++i) freq_out[i] = fixed(one(angle[i]));
   return SV_OK;
 }
 
@@ -74,13 +117,17 @@ sv_status sv_rope_freqs(int rot, double base, sv_rope_scaling scaling, double st
     i0 = std::fmax(std::floor(index(high)), 0.0);
     i1 = std::fmin(std::ceil(index(low)), rot - 1.0);
   }
+  const Two ln = log_two(base);
   for (int i = 0; i < rot / 2; ++i) {
-    const double f = std::pow(base, -2.0 * i / rot);
-    double w = scaling == SV_ROPE_PLAIN ? 1.0 : 0.0;
-    if (scaling == SV_ROPE_TURNS) w = (original * f / TWO_PI - low) / (high - low);
-    if (scaling == SV_ROPE_INDEX) w = 1.0 - (i - i0) / std::fmax(i1 - i0, 1e-3);
-    w = std::fmin(std::fmax(w, 0.0), 1.0);
-    freq_out[i] = fixed(f * (w + (1.0 - w) / stretch));
+    const Two f = exp_two(one(-2.0 * i) / one(rot) * ln);
+    Two w = one(scaling == SV_ROPE_PLAIN ? 1.0 : 0.0);
+    if (scaling == SV_ROPE_TURNS)
+      w = (one(original) * f * Two{0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57} + one(-low)) /
+          two_sum(high, -low);
+    if (scaling == SV_ROPE_INDEX) w = one(1.0) + one(i0 - i) / one(std::fmax(i1 - i0, 1e-3));
+    if (!(w.hi > 0.0)) w = one(0.0);
+    if (w.hi > 1.0 || (w.hi == 1.0 && w.lo > 0.0)) w = one(1.0);
+    freq_out[i] = fixed(f * (w + (one(1.0) + Two{-w.hi, -w.lo}) / one(stretch)));
   }
   return SV_OK;
 }

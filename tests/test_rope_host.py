@@ -1,5 +1,6 @@
 """CPU checks of the rotary calls: frequencies, and host-side refusals."""
 import ctypes
+import decimal
 import math
 
 import pytest
@@ -150,3 +151,61 @@ def test_table_refusals(sv):
         sv.Rope(64, base=0.5, device="cpu")
     with pytest.raises(sv.SpecVerifyError):
         sv.Rope(4, angles=[0.1, math.inf], device="cpu")
+
+
+TAU = decimal.Decimal("6.28318530717958647692528676655900576839433879875021164194988918461563281257242")
+
+
+def units(turns):
+    """A fraction of a turn in units of 2^-64, not rounded."""
+    return (turns % 1) * 2 ** 64
+
+
+def off(got, want):
+    """How far, in units of 2^-64, whole turns left out."""
+    d = (got - want) % 2 ** 64
+    return float(min(d, 2 ** 64 - d))
+
+
+@pytest.mark.parametrize("rot,base", [(2, 10000.0), (20, 500000.0), (128, 10000.0), (128, 500000.0),
+                                      (512, 1e6), (64, 1.0000001), (256, 1e200), (96, 10000.3)])
+def test_frequencies_to_the_last_unit(sv, rot, base):
+    """Every frequency is its formula's, rounded once to 2^-64 of a turn (half a unit, and 2^-9 of one
+    for sums of two doubles), so that at position 2^31 an angle is off by 2^-34 of a turn."""
+    with decimal.localcontext() as c:
+        c.prec = 70
+        D = decimal.Decimal
+        f = [(-(D(2 * i) / rot) * D(base).ln()).exp() for i in range(rot // 2)]
+
+        def exactly(scaling, want, **kw):
+            out = (ctypes.c_int64 * (rot // 2))()
+            args = dict(dict(stretch=1.0, original=0.0, low=0.0, high=0.0), **kw)
+            rc = sv.load().sv_rope_freqs(rot, base, scaling, *args.values(), out)
+            assert rc == sv.SV_OK
+            assert max(off(D(x % 2 ** 64), units(y / TAU)) for x, y in zip(out, want)) <= 0.5 + 2 ** -9
+
+        exactly(0, f)
+        exactly(1, [x / D(7.3) for x in f], stretch=7.3)
+        w = [min(D(1), max(D(0), (8192 * x / TAU - 1) / 3)) for x in f]
+        exactly(2, [x * (k + (1 - k) / 8) for x, k in zip(f, w)], stretch=8.0, original=8192.0, low=1.0,
+                high=4.0)
+        at = lambda n: rot * math.log(4096 / (2 * math.pi * n)) / (2 * math.log(base))  # noqa: E731
+        a, b = max(math.floor(at(32)), 0), min(math.ceil(at(1)), rot - 1)
+        w = [1 - min(D(1), max(D(0), D(i - a) / D(max(b - a, 1e-3)))) for i in range(rot // 2)]
+        exactly(3, [x * (k + (1 - k) / 16) for x, k in zip(f, w)], stretch=16.0, original=4096.0,
+                low=1.0, high=32.0)
+
+
+def test_given_angles_to_the_last_unit(sv):
+    """Angles as the doubles they are, up to a million turns and signs; larger ones wrap somehow."""
+    a = [1.0, -1.0, 0.1, -0.1, 1e-3, 3.0, -3.0, 6.0, 6.283185307179586, -6.283185307179586, 1e-17,
+         -1e-17, 1e-300, -1e-300, 0.0, 12345.678, -98765.4321, 5e6, -5e6, 2.0 ** -40, -(2.0 ** -40)]
+    rc, got = fixed(sv, a)
+    assert rc == sv.SV_OK
+    with decimal.localcontext() as c:
+        c.prec = 70
+        want = [units(decimal.Decimal(x) / TAU) for x in a]
+        for x, g, w in zip(a, got, want):
+            assert off(decimal.Decimal(g), w) <= 0.5 + 2 ** -9, x
+    big = [s * 10.0 ** e for e in (10, 17, 20, 40, 300) for s in (1, -1)]
+    assert fixed(sv, big)[0] == sv.SV_OK
