@@ -794,7 +794,12 @@ def sv_rope(rope: Rope, x, pos=None, start=None, parent=None, n_new=None, invers
     """Rotate x [batch, T, heads, dim] (bf16, fp16 or fp32; slices of a fused projection are
     fine) by positions pos [batch, T], or start [batch] (0 when not given) plus a token's
     number or depth in parent [batch, T] (all int32; see specverify.h). out may be x; inverse
-    is the gradient's rotation. Returns out."""
+    is the gradient's rotation. Returns out, with its graph where x requires grad (then not
+    with out): the backward pass rotates back by pos, start, parent and n_new as they are then."""
+    if x.requires_grad and torch.is_grad_enabled():
+        if out is not None:
+            raise ValueError("out: x requires grad, which a result written to out does not pass on")
+        return _RopeGrad.apply(x, rope, pos, start, parent, n_new, inverse, stream)
     index = rope.index
     shape, row, tok = _rope_src(x, "x", index)
     B, T, heads, dim = shape
@@ -819,11 +824,31 @@ def sv_rope(rope: Rope, x, pos=None, start=None, parent=None, n_new=None, invers
     return out
 
 
+class _RopeGrad(torch.autograd.Function):
+    """sv_rope in a graph: a rotation is orthogonal up to its gain, so its gradient is the inverse one
+    (which is linear too: gradients of gradients are the same calls)."""
+
+    @staticmethod
+    def forward(ctx, x, rope, pos, start, parent, n_new, inverse, stream):
+        ctx.rope, ctx.inverse = rope, inverse
+        ctx.save_for_backward(pos, start, parent, n_new)
+        return sv_rope(rope, x, pos, start, parent, n_new, inverse, stream=stream)
+
+    @staticmethod
+    def backward(ctx, g):
+        pos, start, parent, n_new = ctx.saved_tensors
+        g = g.contiguous()
+        if g.data_ptr() % 16:
+            g = g.clone()
+        return (sv_rope(ctx.rope, g, pos, start, parent, n_new, not ctx.inverse),) + (None,) * 7
+
+
 def sv_kv_append_rope(cache: KVCache, layer, k, v, rope: Rope, q=None, q_out=None, n_new=None,
                       parent=None, stream=None):
     """sv_kv_append with the keys rotated on the way by their positions in the row (a token's
     depth when parent [batch, T] gives a tree), and the queries q [batch, T, q_heads, dim], if
-    given, rotated to q_out (which may be q; see specverify.h). Returns q_out."""
+    given, rotated to q_out (which may be q; see specverify.h). Returns q_out. (No graph is made, as
+    by all calls of the cache.)"""
     shape, k_row, k_tok = _kv_src(k, "k", cache, cache.heads)
     v_shape, v_row, v_tok = _kv_src(v, "v", cache, cache.heads)
     if shape != v_shape or k.dtype != v.dtype:

@@ -4,6 +4,7 @@ import decimal
 import math
 
 import pytest
+import torch
 
 FAKE = 1 << 20  # never dereferenced: every call below fails its checks first
 
@@ -209,3 +210,11 @@ def test_given_angles_to_the_last_unit(sv):
             assert off(decimal.Decimal(g), w) <= 0.5 + 2 ** -9, x
     big = [s * 10.0 ** e for e in (10, 17, 20, 40, 300) for s in (1, -1)]
     assert fixed(sv, big)[0] == sv.SV_OK
+
+
+def test_out_of_a_tensor_that_requires_grad(sv):
+    """A result written to out would lose x's graph without a word: refused, as torch does."""
+    x, out = (torch.zeros(1, 1, 1, 16, requires_grad=g) for g in (True, False))
+    for o in (out, x):
+        with pytest.raises(ValueError, match="requires grad"):
+            sv.sv_rope(object(), x, out=o)
