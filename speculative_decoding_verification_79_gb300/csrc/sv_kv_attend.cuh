@@ -214,6 +214,11 @@ __device__ __forceinline__ bool at_large(const SharedArgs& A, long long rows) {
 // 226 and 151 (such rows fill their products by themselves); 64 rows of 72 queries on 8,192, by
 // twos 327 and 311, by fours 261 and 310; of 36 by 32 on 2,048 79 and 89, on 768 70 and 60; of 8
 // by twos on 2,048 76 and 81, on 768 56 and 49; 8 rows of 36 by twos on 8,192 50 and 47.
+// A group is priced by its own queries, although all of a call's run as the largest does: by what they
+// then take, small ones beside a large one were left alone, one of 16 rows and 24 of two on 2,048 90
+// us instead of 81, one and 8 on 8,192 98 instead of 83 (sv_kv_attend 72 and 105). Taking groups to be
+// alike shares a large one among many small ones where it alone would not pay: one and 24 on 768
+// tokens 56 us, all shared 59, sv_kv_attend 44.
 // (The warps that plan ask this for every query tile, in every kernel of the call with the same answer:
 // few instructions, each with its rounding said.)
 constexpr float AT_KIND = 152 * 10000.f, AT_LAUNCH = 152 * 27000.f;

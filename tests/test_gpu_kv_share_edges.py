@@ -203,3 +203,37 @@ def test_changed_rows_are_nan_throughout(sv, always, T, group, live):  # noqa: F
     sv.sv_kv_share(g, share, i32(lead))
     check_attend(both, 0, q, n, got=sv.sv_kv_attend_shared(g, 0, q, share, **kw))
     assert g.status() == sv.SV_OK
+
+
+@needs_cuda
+@pytest.mark.parametrize("groups,T,heads,group,dim,window,once", [
+    ([(16, 20000), (2, 300), (3, 140)], 1, 8, 8, 128, 0, [True, False, False]),  # large groups' kernel
+    ([(16, 20000), (2, 300)], 1, 8, 8, 160, 0, [True, False]),                   # beside the rows
+    ([(4, 20000)], 1, 8, 1, 128, 0, [True]),                                     # a narrow one
+    ([(4, 2000)], 1, 1, 1, 128, 0, [False]),           # gains less than a second kind of work costs
+    ([(2, 2000), (3, 1500)], 16, 2, 8, 128, 0, [False, False]),  # rows that fill their products
+    ([(16, 20000)], 1, 8, 8, 64, 15000, [True]),       # a window that reaches most
+    ([(16, 20000)], 1, 8, 8, 64, 200, [False])])       # and one that reaches three tiles
+def test_which_groups_are_read_once(sv, groups, T, heads, group, dim, window, once):  # noqa: F811
+    """What the rule decides, by groups that clearly gain or lose. Another page in a row's common
+    tokens shows it: the row is NaN where they are read once, and has results of its own else."""
+    both, lead = grouped(sv, groups, [77], [30, 130], heads, dim, 128, T)
+    g, B = both.g, both.r.batch
+    block(both, T, 1, [T] * B)
+    share, q = sv.KVShare(g, T, heads * group), queries(both, T, group, BF, 1)
+    sv.sv_kv_share(g, share, i32(lead))
+    kw = dict(window=window, sinks=3 if window else 0)
+    before = sv.sv_kv_attend_shared(g, 0, q, share, **kw)
+    assert g.status() == sv.SV_OK and torch.isfinite(before.float()).all()
+    sizes = [m for m, _ in groups]  # (no two alike)
+    changed = [max(b for b in range(B) if lead.count(lead[b]) == m and lead[b] != b) for m in sizes]
+    full = int(g.table[changed[0], 1])  # (of the longest group: pages are NaN past what was written)
+    for b in changed:
+        g.table[b, 0] = full
+    out = sv.sv_kv_attend_shared(g, 0, q, share, **kw)
+    assert g.status() == (sv.SV_ERR_DEVICE_INPUT if any(once) else sv.SV_OK)
+    nan = torch.isnan(out.float()).flatten(1)
+    assert [bool(nan[b].all()) for b in changed] == once
+    assert not nan[[b for b, x in zip(changed, once) if not x]].any()
+    rest = [b for b in range(B) if b not in changed]
+    assert torch.equal(out[rest], before[rest])
