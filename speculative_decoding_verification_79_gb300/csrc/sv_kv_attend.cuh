@@ -851,7 +851,7 @@ template <AtMode M, typename Args>
 __device__ __forceinline__ int at_pairs(const Args& A, int nrt) {
   const int n = at_rows<M>(A);
   if constexpr (M == AT_GROUPS)
-    if (n > AT_LISTED / max(nrt, 1)) {  // (no less than any number; see at_group_base)
+    if ((long long)n * nrt > AT_LISTED) {  // (no less than any number; see at_group_base)
       const long long rows = (long long)kv_ld(A.H.head + 2) * A.T * A.group;
       return max(static_cast<int>(rows / KV_ROWS) + n, AT_LISTED + 1);
     }
