@@ -683,7 +683,7 @@ def sv_kv_attend_shared(cache: KVCache, layer, q, share: KVShare, n_new=None, pa
                         scale=None, window=0, sinks=0, out=None, lse=None, want_lse=False,
                         stream=None):
     """sv_kv_attend that reads the tokens which rows have in common (sv_kv_share) once for all of
-    them."""
+    them, where that is faster than one by one (where it never is, sv_kv_attend is, by 2 to 11 us)."""
     return _kv_attend("sv_kv_attend_shared", cache, layer, q, n_new, parent, scale, window, sinks,
                       out, lse, want_lse, stream, *_kv_share_of(share, cache))
 

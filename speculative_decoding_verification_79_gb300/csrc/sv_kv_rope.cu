@@ -7,7 +7,7 @@
 // their cosines and sines stay in its registers, and the next head's loads are under way while a
 // head's largest value is found. Blocks behind those of keys and values rotate the queries
 // (rope_row). Bound by memory: 8 prompts of 4,093 tokens with 8 heads and 32 query heads of 128
-// take 127 us, 738 MB at 5.8 TB/s (the queries alone 80). A few tokens of many rows take the trips
+// take 128 us, 738 MB at 5.8 TB/s (the queries alone 80). A few tokens of many rows take the trips
 // to memory one after the other (lengths, table, counts of holders, old scale, beside the tokens
 // themselves): 64 rows 5.1 us for a token, 9.5 us for trees of 16.
 //
@@ -17,6 +17,18 @@
 // the loop leaves a page's rare cases to append_rest, behind it. (Which was given what it needs by
 // the loop's block, kept in registers meanwhile: 135 us; with the block's maximum found by shuffles
 // and a loop: 141.)
+//
+// It fits for 16-bit values with rot a multiple of 16. Others spill, and a page of more than 16,384
+// values (128 tokens of 192 or 256 components) goes to append_rest whole, which reads it twice and
+// computes cosines for each head again. Those prompts with keys and queries, and keys and values alone
+// (beside sv_kv_append, which does not rotate), us:
+//   dim 128, rot 128, pages of 64 / 128, bf16      128, 58 (43) / 141, 69 (45)
+//   the same, pages of 64, float32                 231, 73 (61); 160 to 184 bytes of spill loads
+//   dim 80, rot 40, bf16                           103, 43 (33); 40 to 64 (4 pairs a thread)
+//   dim 80, rot 20, bf16                           272, 129 (33); 270 to 370 (single pairs)
+//   dim 192, pages of 64 / 128, bf16               240, 109 (62) / 367, 258 (68)
+//   dim 256, pages of 64 / 128, bf16               279, 125 (80) / 445, 308 (93)
+//   dim 256, pages of 128, float32                 659, 363 (167)
 #include "sv_rope.cuh"
 
 namespace sv {

@@ -14,7 +14,7 @@
 //
 // Bound as sv_kv_attend is: a query tile's chain of scores, weights and outputs, some 10,000 cycles
 // whatever its keys, then 1,600 to 2,600 cycles a key tile. 64 rows of 64 queries on 740 tokens
-// without a group take 67 us, sv_kv_attend 60: the counts of what is shared, a launch for large
+// without a group take 69 us, sv_kv_attend 61: the counts of what is shared, a launch for large
 // groups that ends at once, and the join. 64 chats of one token (8 heads of 8 queries, 60 to 1,500
 // tokens of their own behind 8,100 common ones): 52 us for the rows' own tokens, 30 for the common
 // ones, 10 for the join, 84 together, since each starts as CTAs of the one before end.

@@ -26,7 +26,10 @@ struct Rope {
 };
 
 // Pairs of a thread, by the rotated size: 8, whose halves are 16-byte vectors of 16-bit values when
-// the second half begins at a multiple of 8 components; else 4 or 1, as its alignment allows.
+// the second half begins at a multiple of 8 components; else 4 or 1, as its alignment allows. (The
+// components that stay as they are go the same way. 8 x 4,093 tokens of 32 heads of 80 in bf16: 52 us,
+// 6.4 TB/s, with rot 40; 99 us, 3.4 TB/s, with rot 20, in float32 111 us at 6.1. 8 heads of 512: 80 us
+// with rot 32, 136 with rot 30.)
 inline int rope_pairs(int rot) { return rot % 16 == 0 ? 8 : (rot % 8 == 0 ? 4 : 1); }
 
 __device__ __forceinline__ float2 rope_turn(const Rope& R, long long pos, int64_t freq) {
