@@ -66,7 +66,8 @@ def test_flags_between_launches(sv, always):  # noqa: F811
 def test_groups_of_very_different_sizes(sv, always):  # noqa: F811
     """One group of 2,048 rows beside 1,024 of two, with as many queries as the call takes: groups
     times the largest one's query tiles pass 2^31. Rows of each kind against float64."""
-    if torch.cuda.get_device_properties(0).total_memory < 160 << 30:
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 120 << 30:
         pytest.skip("needs 95 GB of device memory")
     rows, T, heads, dim, page = 4096, 1024, 128, 16, 128
     g = sv.KVCache(1, 1025 + 8, page, 1, dim, rows, 2)
